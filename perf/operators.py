@@ -180,8 +180,8 @@ def _call(s):
     f = gdn.recur_forward(rec, x, a, b, z, s["cu_seqlens"], initial_state=s["state"], want_saved=op == "train")
     out = {"y": f["out"], "state": f["final_state"]}
     if op == "train":
-        out.update(gdn.recur_backward(rec, x, a, b, z, s["dy"], f["saved"], s["cu_seqlens"], initial_state=s["state"],
-                                      d_final_state=s["d_final"]))
+        out.update(gdn.recur_backward(rec, x, a, b, z, s["dy"], f["saved"], s["cu_seqlens"],
+                                      d_final_state=s["d_final"], want_d_initial=s["state"] is not None))
     return out
 
 
