@@ -42,7 +42,9 @@ EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_snapshot_restore", "gdn_gemm_bf16", "gdn_layer_prefill_workspace_bytes",
            "gdn_layer_prefill", "gdn_layer_decode_workspace_bytes", "gdn_layer_decode",
            "gdn_status_string", "gdn_last_error", "gdn_selftest_mfma", "gdn_prefill_noalloc",
-           "gdn_prefill_window_slots", "gdn_decode_workspace_bytes", "gdn_gemm_bf16_path")
+           "gdn_prefill_window_slots", "gdn_decode_workspace_bytes", "gdn_gemm_bf16_path",
+           "gdn_recur_saved_bytes", "gdn_recur_workspace_bytes", "gdn_recur_forward",
+           "gdn_recur_backward_workspace_bytes", "gdn_recur_backward", "gdn_recur_decode")
 NOALLOC_SCRATCH_BYTES = 128 << 20       # GDN_NOALLOC_SCRATCH_BYTES
 SNAPSHOT_MAGIC = 0x50534E47
 SNAPSHOT_VERSION = 1
@@ -126,6 +128,32 @@ class CDecodeIO(ctypes.Structure):
                  ("state_slots", ctypes.c_void_p), ("num_slots", ctypes.c_int32),
                  ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                  ("status", ctypes.c_void_p)])
+
+
+class CRecur(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class CRecurIO(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("T_total", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
+                ("x", ctypes.c_void_p), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("z", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("a_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("y_stride", ctypes.c_int64), ("initial_state", ctypes.c_void_p),
+                ("final_state", ctypes.c_void_p), ("state_slots", ctypes.c_void_p),
+                ("num_slots", ctypes.c_int32), ("saved", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class CRecurGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("dy_stride", ctypes.c_int64),
+                ("d_final_state", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("da", ctypes.c_void_p), ("db", ctypes.c_void_p), ("dz", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64), ("da_stride", ctypes.c_int64),
+                ("db_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64),
+                ("dA_log", ctypes.c_void_p), ("ddt_bias", ctypes.c_void_p),
+                ("d_initial_state", ctypes.c_void_p)]
 
 
 _lib = None
@@ -214,6 +242,21 @@ def lib():
         L.gdn_snapshot_restore.argtypes = [ctypes.POINTER(CLayer), ctypes.c_void_p, ctypes.c_size_t,
                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                            ctypes.c_int32, ctypes.c_void_p]
+        for name in ("gdn_recur_saved_bytes", "gdn_recur_workspace_bytes",
+                     "gdn_recur_backward_workspace_bytes"):
+            f = getattr(L, name)
+            f.restype = ctypes.c_size_t
+            f.argtypes = [ctypes.POINTER(CRecur), ctypes.c_int32, ctypes.c_int64]
+        L.gdn_recur_forward.restype = ctypes.c_int
+        L.gdn_recur_forward.argtypes = [ctypes.POINTER(CRecur), ctypes.POINTER(CRecurIO),
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        L.gdn_recur_backward.restype = ctypes.c_int
+        L.gdn_recur_backward.argtypes = [ctypes.POINTER(CRecur), ctypes.POINTER(CRecurIO),
+                                         ctypes.POINTER(CRecurGrad), ctypes.c_void_p,
+                                         ctypes.c_size_t, ctypes.c_void_p]
+        L.gdn_recur_decode.restype = ctypes.c_int
+        L.gdn_recur_decode.argtypes = [ctypes.POINTER(CRecur), ctypes.POINTER(CRecurIO),
+                                       ctypes.c_void_p]
         _lib = L
     return _lib
 
@@ -737,6 +780,281 @@ def layer_decode_raw(layer: Layer, proj: Proj, *, B, x, y, state_in, state_out, 
         workspace.numel() * workspace.element_size() if workspace is not None else 0)
     _check(lib().gdn_layer_decode(ctypes.byref(cl), ctypes.byref(cp), ctypes.byref(io),
                                   _ptr(workspace), nb, _stream(stream)))
+
+
+# ---- the diagonal gated recurrence -------------------------------------------
+
+def _on_device(t, name):
+    """Raise ValueError unless t is on the current device: the library
+    launches there, on the given stream."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a device tensor is required")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _matrix(t, name, rows, cols, dtype):
+    """Raise ValueError unless t is a [>= rows, cols] tensor of `dtype` on
+    the current device whose rows are dense; returns its pointer and row
+    stride in elements."""
+    _on_device(t, name)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] != cols:
+        raise ValueError(f"{name}: [{rows}, {cols}] needed, shape is {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} needed, not {t.dtype}")
+    if rows == 0:
+        return None, cols
+    rs, cs = t.stride()
+    if cs != 1 and cols != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if rows > 1 and rs < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), max(rs, cols)
+
+
+def _dense(t, name, rows, cols):
+    """Pointer of an optional dense fp32 [>= rows, cols] tensor (cols None:
+    [>= rows])."""
+    import torch
+    if t is None:
+        return None
+    _on_device(t, name)
+    shape = t.shape
+    ok = len(shape) == 1 if cols is None else (len(shape) == 2 and shape[1] == cols)
+    if not ok or shape[0] < rows or t.dtype != torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous float32 [{rows}{'' if cols is None else f', {cols}'}] "
+                         f"needed, not {t.dtype} {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _index(t, name, n):
+    """Pointer of an optional contiguous device int32 tensor of >= n entries."""
+    import torch
+    if t is None:
+        return None
+    _on_device(t, name)
+    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous device int32 tensor of {n} entries is required")
+    return t.data_ptr()
+
+
+def _bytes(t, name):
+    """Pointer and size of an optional workspace."""
+    if t is None:
+        return None, 0
+    _on_device(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _on(stream):
+    """A context in which torch allocates for `stream` (None: the current
+    one), so that memory a call on it uses is not reused under it."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+@dataclass
+class Recur:
+    """A diagonal gated recurrence over D channels: A_log, dt_bias [D] fp32
+    device tensors, act_dtype of x, a, b, z, y and their gradients.  With
+    alpha_t = exp(-exp(A_log) softplus(a_t + dt_bias)):
+    h_t = alpha_t h_{t-1} + sqrt(1 - alpha_t^2) sigmoid(b_t) x_t and
+    y_t = h_t SiLU(z_t) (y_t = h_t without z)."""
+    D: int
+    A_log: object
+    dt_bias: object
+    act_dtype: int = GDN_DTYPE_BF16
+
+    @property
+    def dtype(self):
+        import torch
+        return torch.bfloat16 if self.act_dtype == GDN_DTYPE_BF16 else torch.float32
+
+    def c(self) -> CRecur:
+        key = (self.D, self.act_dtype, self.A_log.data_ptr(), self.A_log.numel(),
+               self.dt_bias.data_ptr(), self.dt_bias.numel())
+        if getattr(self, "_key", None) != key:
+            self._c = CRecur(self.D, self.act_dtype, _dense(self.A_log, "A_log", self.D, None),
+                             _dense(self.dt_bias, "dt_bias", self.D, None))
+            self._key = key
+        return self._c
+
+
+def _recur_size(name, rec, N, T):
+    n = getattr(lib(), name)(ctypes.byref(rec.c()), int(N), int(T))
+    if n == 0 and lib().gdn_last_error():
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, lib().gdn_last_error().decode())
+    return int(n)
+
+
+def recur_saved_bytes(rec: Recur, N: int, T_total: int) -> int:
+    """Bytes of the states gdn_recur_forward saves for the backward pass."""
+    return _recur_size("gdn_recur_saved_bytes", rec, N, T_total)
+
+
+def recur_workspace_bytes(rec: Recur, N: int, T_total: int) -> int:
+    """Bytes of workspace of ``gdn_recur_forward`` (0: it needs none)."""
+    return _recur_size("gdn_recur_workspace_bytes", rec, N, T_total)
+
+
+def recur_backward_workspace_bytes(rec: Recur, N: int, T_total: int) -> int:
+    """Bytes of workspace of ``gdn_recur_backward``."""
+    return _recur_size("gdn_recur_backward_workspace_bytes", rec, N, T_total)
+
+
+def _recur_io(rec, N, T, rows, cu_seqlens, x, a, b, z, y, initial_state, final_state, state_slots,
+              num_slots, saved, status):
+    D, dt = rec.D, rec.dtype
+    px, sx = _matrix(x, "x", rows, D, dt)
+    pa, sa = _matrix(a, "a", rows, D, dt)
+    pb, sb = _matrix(b, "b", rows, D, dt)
+    pz, sz = (None, 0) if z is None else _matrix(z, "z", rows, D, dt)
+    py, sy = (None, 0) if y is None else _matrix(y, "y", rows, D, dt)
+    entries = N if state_slots is None else num_slots
+    return CRecurIO(N, T, _index(cu_seqlens, "cu_seqlens", N + 1), px, pa, pb, pz, sx, sa, sb, sz,
+                    py, sy, _dense(initial_state, "initial_state", entries, D),
+                    _dense(final_state, "final_state", entries, D),
+                    _index(state_slots, "state_slots", N), num_slots,
+                    None if saved is None else _bytes(saved, "saved")[0],
+                    _index(status, "status", 1))
+
+
+def _recur_saved(rec, saved, N, T):
+    if saved is not None and _bytes(saved, "saved")[1] < recur_saved_bytes(rec, N, T):
+        raise ValueError(f"saved: {recur_saved_bytes(rec, N, T)} bytes needed")
+
+
+def recur_forward_raw(rec: Recur, *, N, T_total, cu_seqlens, x, a, b, y, z=None, initial_state=None,
+                      final_state=None, saved=None, workspace=None, stream=None, state_slots=None,
+                      num_slots=0, status=None):
+    """Call ``gdn_recur_forward`` on caller-provided buffers (no allocation).
+    status as for prefill_raw (GDN_STATUS_BAD_INDEX only)."""
+    N, T = int(N), int(T_total)
+    io = _recur_io(rec, N, T, T, cu_seqlens, x, a, b, z, y, initial_state, final_state, state_slots,
+                   int(num_slots), saved, status)
+    _recur_saved(rec, saved, N, T)
+    ws, nb = _bytes(workspace, "workspace")
+    _check(lib().gdn_recur_forward(ctypes.byref(rec.c()), ctypes.byref(io), ws, nb, _stream(stream)))
+
+
+def recur_forward(rec: Recur, x, a, b, z, cu_seqlens, initial_state=None, want_saved=False,
+                  in_place=False, out=None, state_slots=None, workspace=None, stream=None,
+                  status=None):
+    """Forward over packed sequences: x, a, b, z (or None) [T, D] in the act
+    dtype (rows may be strided), cu_seqlens int32 [N+1] on the device.
+    Allocates what is not given and returns a dict with out [T, D],
+    final_state [N, D] fp32 and (if asked) saved, which recur_backward
+    takes.  With state_slots (int32 [N]) initial_state is a pool, which is
+    updated in place."""
+    import torch
+    T, N, D = int(x.shape[0]), int(cu_seqlens.numel()) - 1, rec.D
+    if state_slots is not None and initial_state is None:
+        raise ValueError("state_slots needs the pool as initial_state")
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, D), dtype=rec.dtype, device=x.device)
+        if initial_state is not None and (in_place or state_slots is not None):
+            fs = initial_state
+        else:
+            fs = torch.empty((N, D), dtype=torch.float32, device=x.device)
+        saved = None
+        if want_saved:
+            saved = torch.empty(recur_saved_bytes(rec, N, T), dtype=torch.uint8, device=x.device)
+        if workspace is None:
+            nb = recur_workspace_bytes(rec, N, T)
+            if nb:
+                workspace = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        recur_forward_raw(rec, N=N, T_total=T, cu_seqlens=cu_seqlens, x=x, a=a, b=b, z=z, y=out,
+                          initial_state=initial_state, final_state=fs, saved=saved,
+                          workspace=workspace, stream=stream, state_slots=state_slots,
+                          num_slots=0 if state_slots is None else int(initial_state.shape[0]),
+                          status=status)
+    res = {"out": out, "final_state": fs}
+    if want_saved:
+        res["saved"] = saved
+    return res
+
+
+def recur_backward_raw(rec: Recur, *, N, T_total, cu_seqlens, x, a, b, dy, saved, dx, da, db,
+                       z=None, dz=None, d_final_state=None, d_initial_state=None, dA_log=None,
+                       ddt_bias=None, workspace=None, stream=None, status=None):
+    """Call ``gdn_recur_backward`` on caller-provided buffers (no
+    allocation)."""
+    N, T, D, dt = int(N), int(T_total), rec.D, rec.dtype
+    io = _recur_io(rec, N, T, T, cu_seqlens, x, a, b, z, None, None, None, None, 0, saved, status)
+    _recur_saved(rec, saved, N, T)
+    if (z is None) != (dz is None):
+        raise ValueError("dz: needed with z, and only with it")
+    (py, sy), (px, sx), (pa, sa), (pb, sb) = (_matrix(t, n, T, D, dt) for t, n in (
+        (dy, "dy"), (dx, "dx"), (da, "da"), (db, "db")))
+    pz, sz = (None, 0) if dz is None else _matrix(dz, "dz", T, D, dt)
+    gr = CRecurGrad(py, sy, _dense(d_final_state, "d_final_state", N, D), px, pa, pb, pz, sx, sa, sb, sz,
+                    _dense(dA_log, "dA_log", D, None), _dense(ddt_bias, "ddt_bias", D, None),
+                    _dense(d_initial_state, "d_initial_state", N, D))
+    ws, nb = _bytes(workspace, "workspace")
+    _check(lib().gdn_recur_backward(ctypes.byref(rec.c()), ctypes.byref(io), ctypes.byref(gr), ws, nb,
+                                    _stream(stream)))
+
+
+def recur_backward(rec: Recur, x, a, b, z, dy, saved, cu_seqlens, d_final_state=None,
+                   want_d_initial=False, workspace=None, stream=None, status=None):
+    """Gradients of a recur_forward call from dy [T, D] and (optionally)
+    d_final_state [N, D]: a dict with dx, da, db, dz (with z), all [T, D] in
+    the act dtype, dA_log, ddt_bias [D] fp32 and (if asked) d_initial_state
+    [N, D] fp32.  saved: what recur_forward saved of the same inputs."""
+    import torch
+    T, N, D = int(x.shape[0]), int(cu_seqlens.numel()) - 1, rec.D
+    dev = x.device
+    with _on(stream):
+        res = {n: torch.empty((T, D), dtype=rec.dtype, device=dev) for n in ("dx", "da", "db")}
+        if z is not None:
+            res["dz"] = torch.empty((T, D), dtype=rec.dtype, device=dev)
+        res["dA_log"] = torch.empty(D, dtype=torch.float32, device=dev)
+        res["ddt_bias"] = torch.empty(D, dtype=torch.float32, device=dev)
+        if want_d_initial:
+            res["d_initial_state"] = torch.empty((N, D), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(recur_backward_workspace_bytes(rec, N, T), dtype=torch.uint8,
+                                    device=dev)
+        recur_backward_raw(rec, N=N, T_total=T, cu_seqlens=cu_seqlens, x=x, a=a, b=b, z=z, dy=dy,
+                           saved=saved, d_final_state=d_final_state, workspace=workspace,
+                           stream=stream, status=status, **res)
+    return res
+
+
+def recur_decode_raw(rec: Recur, *, N, x, a, b, y, initial_state, final_state, z=None,
+                     state_slots=None, num_slots=0, stream=None, status=None):
+    """Call ``gdn_recur_decode`` on caller-provided buffers (no allocation).
+    status as for decode_raw."""
+    N = int(N)
+    io = _recur_io(rec, N, 0, N, None, x, a, b, z, y, initial_state, final_state, state_slots,
+                   int(num_slots), None, status)
+    _check(lib().gdn_recur_decode(ctypes.byref(rec.c()), ctypes.byref(io), _stream(stream)))
+
+
+def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True, out=None,
+                 stream=None, status=None):
+    """One token per sequence: x, a, b, z (or None) [B, D], state [B, D] fp32
+    (or a pool [slots, D] with state_slots int32 [B]), updated in place by
+    default.  Returns a dict with out [B, D] and final_state (in_place=False:
+    a new tensor, of which only these sequences' entries are written)."""
+    import torch
+    B = int(x.shape[0])
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, rec.D), dtype=rec.dtype, device=x.device)
+        fs = state if in_place else torch.empty_like(state)
+        recur_decode_raw(rec, N=B, x=x, a=a, b=b, z=z, y=out, initial_state=state, final_state=fs,
+                         state_slots=state_slots,
+                         num_slots=0 if state_slots is None else int(state.shape[0]),
+                         stream=stream, status=status)
+    return {"out": out, "final_state": fs}
 
 
 def snapshot_bytes(layer: Layer) -> int:

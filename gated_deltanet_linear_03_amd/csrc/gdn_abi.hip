@@ -894,6 +894,315 @@ gdn_status gdn_snapshot_restore(const gdn_layer* L, const void* host, size_t hos
     return GDN_OK;
 }
 
+// ---- the diagonal gated recurrence -------------------------------------------
+
+namespace {
+
+static_assert(2 * GDN_RECUR_SAVED_ROWS == gdn::kRecurUnit, "saved states every half unit");
+
+gdn_status check_recur(const gdn_recur* R) {
+    if (!R) return fail(GDN_ERR_INVALID_ARGUMENT, "recur is NULL");
+    if (R->D <= 0 || R->D > (1 << 24)) return fail(GDN_ERR_INVALID_ARGUMENT, "D (%d) must be in [1, 2^24]", R->D);
+    if (R->act_dtype != GDN_DTYPE_FP32 && R->act_dtype != GDN_DTYPE_BF16)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "act_dtype %d unknown", R->act_dtype);
+    return GDN_OK;
+}
+
+gdn_status check_recur_sizes(const gdn_recur* R, int32_t N, int64_t T) {
+    gdn_status st = check_recur(R);
+    if (st != GDN_OK) return st;
+    if (N < 0 || T < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "N (%d) and T_total (%lld) must be >= 0", N,
+                                    static_cast<long long>(T));
+    if (T > 0 && N == 0) return fail(GDN_ERR_INVALID_ARGUMENT, "T_total > 0 with N == 0");
+    if (T >= (int64_t(1) << 31)) return fail(GDN_ERR_INVALID_ARGUMENT, "T_total must be < 2^31");
+    // (twice: a backward pass has two tiles per unit)
+    const int64_t groups = (R->D + gdn::kRecurChannels - 1) / gdn::kRecurChannels;
+    if (2 * gdn::recur_units(N, T) * groups >= (int64_t(1) << 31))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "too many tiles (N=%d, T_total=%lld, D=%d)", N, static_cast<long long>(T), R->D);
+    return GDN_OK;
+}
+
+bool recur_walks(int32_t N, int64_t T) {
+    return T <= gdn::kRecurWalkUnits * gdn::kRecurUnit && N <= gdn::kRecurWalkSeqs;
+}
+
+struct RecurWs {
+    int64_t off_seq = 0, off_tickets = 0, off_words = 0, off_partial = 0, total = 0;
+};
+
+// unit table, sequence of each unit, tickets, words (, backward: the sums)
+RecurWs recur_ws(const gdn_recur* R, int32_t N, int64_t T, bool backward) {
+    const int64_t units = gdn::recur_units(N, T), tiles = backward ? 2 * units : units;
+    const int64_t groups = (R->D + gdn::kRecurChannels - 1) / gdn::kRecurChannels;
+    RecurWs w;
+    w.off_seq = round_up(4 * (static_cast<int64_t>(N) + 1), 256);
+    w.off_tickets = round_up(w.off_seq + 4 * units, 256);
+    w.off_words = round_up(w.off_tickets + 4 * groups, 256);
+    w.off_partial = round_up(w.off_words + 8 * tiles * groups * gdn::kRecurChannels, 256);
+    w.total = w.off_partial + (backward ? 8 * tiles * groups * gdn::kRecurChannels : 0);
+    return w;
+}
+
+// rows [rows][D] with a row stride: bytes from the first element to the last
+size_t row_bytes(int64_t rows, int64_t stride, int64_t D, size_t es) {
+    return rows > 0 ? static_cast<size_t>((rows - 1) * stride + D) * es : 0;
+}
+
+// Two sets of rows share bytes.  Rows of one stride that interleave (slices
+// of one packed buffer) do not.
+bool rows_clash(const void* p, int64_t ps, const void* q, int64_t qs, int64_t rows, int64_t D, size_t es) {
+    if (!overlaps(p, row_bytes(rows, ps, D, es), q, row_bytes(rows, qs, D, es))) return false;
+    if (ps != qs) return true;
+    const int64_t d = (reinterpret_cast<intptr_t>(p) - reinterpret_cast<intptr_t>(q)) / static_cast<int64_t>(es);
+    const int64_t m = ((d % ps) + ps) % ps;
+    return m < D || m > ps - D;
+}
+
+gdn_status check_rows(const char* name, const void* p, int64_t stride, int64_t D, size_t es) {
+    if (!p) return fail(GDN_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+    if (!aligned(p, es)) return fail(GDN_ERR_INVALID_ARGUMENT, "%s is not element aligned", name);
+    if (stride < D) return fail(GDN_ERR_INVALID_ARGUMENT, "%s_stride (%lld) is below D", name, static_cast<long long>(stride));
+    return GDN_OK;
+}
+
+// The parts of io that the three calls share, into p; rows: token rows given.
+gdn_status recur_params(const gdn_recur* R, const gdn_recur_io* io, int64_t rows, gdn::RecurParams* p) {
+    const size_t es = act_size(R->act_dtype);
+    const int64_t D = R->D;
+    p->N = io->N;
+    p->D = R->D;
+    p->groups = static_cast<int>((D + gdn::kRecurChannels - 1) / gdn::kRecurChannels);
+    p->T = io->T_total;
+    p->A_log = R->A_log;
+    p->dt_bias = R->dt_bias;
+    p->x = io->x; p->a = io->a; p->b = io->b; p->z = io->z;
+    p->xs = stride_or(io->x_stride, D);
+    p->as = stride_or(io->a_stride, D);
+    p->bs = stride_or(io->b_stride, D);
+    p->zs = stride_or(io->z_stride, D);
+    p->status = io->status;
+    if (!R->A_log || !R->dt_bias || !aligned(R->A_log, 4) || !aligned(R->dt_bias, 4))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "A_log and dt_bias are required, 4-byte aligned");
+    if (!aligned(io->status, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "status must be 4-byte aligned");
+    if (rows > 0) {
+        gdn_status st;
+        if ((st = check_rows("x", io->x, p->xs, D, es)) != GDN_OK) return st;
+        if ((st = check_rows("a", io->a, p->as, D, es)) != GDN_OK) return st;
+        if ((st = check_rows("b", io->b, p->bs, D, es)) != GDN_OK) return st;
+        if (io->z && (st = check_rows("z", io->z, p->zs, D, es)) != GDN_OK) return st;
+    }
+    return GDN_OK;
+}
+
+// The states and y of a forward or one-token call
+gdn_status recur_outputs(const gdn_recur* R, const gdn_recur_io* io, int64_t rows, gdn::RecurParams* p) {
+    const size_t es = act_size(R->act_dtype);
+    const int64_t D = R->D;
+    p->y = io->y;
+    p->ys = stride_or(io->y_stride, D);
+    p->h0 = io->initial_state;
+    p->hT = io->final_state;
+    p->slots = io->state_slots;
+    p->num_slots = io->num_slots;
+    if (io->state_slots && (io->num_slots <= 0 || !aligned(io->state_slots, 4)))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "num_slots (%d) must be positive and state_slots 4-byte aligned", io->num_slots);
+    if (!aligned(io->initial_state, 4) || !aligned(io->final_state, 4))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "states must be 4-byte aligned");
+    const size_t ns = static_cast<size_t>(io->state_slots ? io->num_slots : io->N) * D * 4;
+    if (bad_alias(io->initial_state, ns, io->final_state, ns))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "final_state partially overlaps initial_state");
+    size_t ny = 0;
+    if (rows > 0) {
+        gdn_status st = check_rows("y", io->y, p->ys, D, es);
+        if (st != GDN_OK) return st;
+        ny = row_bytes(rows, p->ys, D, es);
+        if (overlaps(io->y, ny, io->initial_state, ns) || overlaps(io->y, ny, io->final_state, ns))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "y overlaps a state");
+        const void* in[4] = {io->x, io->a, io->b, io->z};
+        const int64_t stride[4] = {p->xs, p->as, p->bs, p->zs};
+        for (int i = 0; i < 4; ++i) {
+            if (!in[i]) continue;
+            if (overlaps(io->final_state, ns, in[i], row_bytes(rows, stride[i], D, es)))
+                return fail(GDN_ERR_INVALID_ARGUMENT, "final_state overlaps an input");
+            if (!(in[i] == io->y && stride[i] == p->ys) && rows_clash(io->y, p->ys, in[i], stride[i], rows, D, es))
+                return fail(GDN_ERR_INVALID_ARGUMENT, "y overlaps an input's rows");
+        }
+    }
+    if (io->status && (overlaps(io->status, 4, io->y, ny) || overlaps(io->status, 4, io->initial_state, ns) ||
+                       overlaps(io->status, 4, io->final_state, ns)))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "status overlaps an output or a state");
+    return GDN_OK;
+}
+
+gdn_status recur_workspace(const RecurWs& w, void* ws, size_t ws_bytes, gdn::RecurParams* p, int64_t tiles) {
+    if (!ws) return fail(GDN_ERR_WORKSPACE, "workspace is NULL (need %lld bytes)", static_cast<long long>(w.total));
+    if (!aligned(ws, 256)) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < static_cast<size_t>(w.total))
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, need %lld", ws_bytes, static_cast<long long>(w.total));
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    p->tiles = static_cast<int>(tiles);
+    p->unit_off = reinterpret_cast<int32_t*>(base);
+    p->unit_seq = reinterpret_cast<int32_t*>(base + w.off_seq);
+    p->tickets = reinterpret_cast<uint32_t*>(base + w.off_tickets);
+    p->words = reinterpret_cast<uint64_t*>(base + w.off_words);
+    p->partial = reinterpret_cast<float2*>(base + w.off_partial);
+    return GDN_OK;
+}
+
+}  // namespace
+
+size_t gdn_recur_saved_bytes(const gdn_recur* R, int32_t N, int64_t T) {
+    g_err[0] = 0;
+    if (check_recur_sizes(R, N, T) != GDN_OK) return 0;
+    const int64_t n = 2 * gdn::recur_units(N, T) * R->D * 4;
+    return static_cast<size_t>(n > 0 ? n : 4);
+}
+
+size_t gdn_recur_workspace_bytes(const gdn_recur* R, int32_t N, int64_t T) {
+    g_err[0] = 0;
+    if (check_recur_sizes(R, N, T) != GDN_OK || recur_walks(N, T)) return 0;
+    return static_cast<size_t>(recur_ws(R, N, T, false).total);
+}
+
+size_t gdn_recur_backward_workspace_bytes(const gdn_recur* R, int32_t N, int64_t T) {
+    g_err[0] = 0;
+    if (check_recur_sizes(R, N, T) != GDN_OK) return 0;
+    return static_cast<size_t>(recur_ws(R, N, T, true).total);
+}
+
+gdn_status gdn_recur_forward(const gdn_recur* R, const gdn_recur_io* io, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = 0;
+    if (!io) return fail(GDN_ERR_INVALID_ARGUMENT, "io is NULL");
+    gdn_status st = check_recur_sizes(R, io->N, io->T_total);
+    if (st != GDN_OK) return st;
+    if (io->N > 0 && (!io->cu_seqlens || !aligned(io->cu_seqlens, 4)))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL or misaligned");
+    gdn::RecurParams p{};
+    if ((st = recur_params(R, io, io->T_total, &p)) != GDN_OK) return st;
+    if ((st = recur_outputs(R, io, io->T_total, &p)) != GDN_OK) return st;
+    if (!aligned(io->saved, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "saved must be 4-byte aligned");
+    p.cu = io->cu_seqlens;
+    p.saved = io->saved;
+    p.walk = recur_walks(io->N, io->T_total);
+    const int64_t units = gdn::recur_units(io->N, io->T_total);
+    const size_t nsv = static_cast<size_t>(2 * units * R->D) * 4;
+    const size_t ns = static_cast<size_t>(io->state_slots ? io->num_slots : io->N) * R->D * 4;
+    const size_t ny = row_bytes(io->T_total, p.ys, R->D, act_size(R->act_dtype));
+    if (overlaps(io->saved, nsv, io->y, ny) || overlaps(io->saved, nsv, io->initial_state, ns) ||
+        overlaps(io->saved, nsv, io->final_state, ns) || overlaps(io->saved, nsv, io->status, 4))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "saved overlaps y, a state or status");
+    if (!p.walk) {
+        const RecurWs w = recur_ws(R, io->N, io->T_total, false);
+        if ((st = recur_workspace(w, ws, ws_bytes, &p, units)) != GDN_OK) return st;
+        const size_t nw = static_cast<size_t>(w.total);
+        if (overlaps(ws, nw, io->y, ny) || overlaps(ws, nw, io->initial_state, ns) || overlaps(ws, nw, io->final_state, ns) ||
+            overlaps(ws, nw, io->saved, nsv) || overlaps(ws, nw, io->status, 4))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "workspace overlaps an output or a state");
+    }
+    p.partial = nullptr;
+    if (io->N == 0) return GDN_OK;
+    hipError_t e = gdn::launch_recur_forward(p, R->act_dtype == GDN_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "recurrence launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
+gdn_status gdn_recur_backward(const gdn_recur* R, const gdn_recur_io* io, const gdn_recur_grad* gr, void* ws,
+                              size_t ws_bytes, void* stream) {
+    g_err[0] = 0;
+    if (!io || !gr) return fail(GDN_ERR_INVALID_ARGUMENT, "io or grad is NULL");
+    gdn_status st = check_recur_sizes(R, io->N, io->T_total);
+    if (st != GDN_OK) return st;
+    const int64_t T = io->T_total, D = R->D;
+    const size_t es = act_size(R->act_dtype);
+    if (io->N > 0 && (!io->cu_seqlens || !aligned(io->cu_seqlens, 4)))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL or misaligned");
+    if (io->N > 0 && (!io->saved || !aligned(io->saved, 4)))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "saved (the states gdn_recur_forward saved) is required, 4-byte aligned");
+    gdn::RecurParams p{};
+    if ((st = recur_params(R, io, T, &p)) != GDN_OK) return st;
+    p.cu = io->cu_seqlens;
+    p.saved = io->saved;
+    p.dy = gr->dy;
+    p.dx = gr->dx; p.da = gr->da; p.db = gr->db; p.dz = gr->dz;
+    p.dys = stride_or(gr->dy_stride, D);
+    p.dxs = stride_or(gr->dx_stride, D);
+    p.das = stride_or(gr->da_stride, D);
+    p.dbs = stride_or(gr->db_stride, D);
+    p.dzs = stride_or(gr->dz_stride, D);
+    p.dhT = gr->d_final_state;
+    p.dh0 = gr->d_initial_state;
+    p.dA_log = gr->dA_log;
+    p.ddt_bias = gr->ddt_bias;
+    if (!aligned(gr->d_final_state, 4) || !aligned(gr->d_initial_state, 4) || !aligned(gr->dA_log, 4) ||
+        !aligned(gr->ddt_bias, 4))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "state and parameter gradients must be 4-byte aligned");
+    const size_t ns = static_cast<size_t>(io->N) * D * 4;
+    if (bad_alias(gr->d_final_state, ns, gr->d_initial_state, ns))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "d_initial_state partially overlaps d_final_state");
+    const int64_t units = gdn::recur_units(io->N, T);
+    const size_t nsv = static_cast<size_t>(2 * units * D) * 4;
+    const RecurWs w = recur_ws(R, io->N, T, true);
+    const size_t nw = static_cast<size_t>(w.total);
+    if (T > 0) {
+        if ((st = check_rows("dy", gr->dy, p.dys, D, es)) != GDN_OK) return st;
+        if ((st = check_rows("dx", gr->dx, p.dxs, D, es)) != GDN_OK) return st;
+        if ((st = check_rows("da", gr->da, p.das, D, es)) != GDN_OK) return st;
+        if ((st = check_rows("db", gr->db, p.dbs, D, es)) != GDN_OK) return st;
+        if (io->z && (st = check_rows("dz", gr->dz, p.dzs, D, es)) != GDN_OK) return st;
+        const void* out[4] = {gr->dx, gr->da, gr->db, io->z ? gr->dz : nullptr};
+        const int64_t os[4] = {p.dxs, p.das, p.dbs, p.dzs};
+        const void* in[5] = {io->x, io->a, io->b, io->z, gr->dy};
+        const int64_t is[5] = {p.xs, p.as, p.bs, p.zs, p.dys};
+        for (int i = 0; i < 4; ++i) {
+            if (!out[i]) continue;
+            const size_t no = row_bytes(T, os[i], D, es);
+            for (int k = 0; k < 5; ++k)
+                if (in[k] && overlaps(out[i], no, in[k], row_bytes(T, is[k], D, es)))
+                    return fail(GDN_ERR_INVALID_ARGUMENT, "a gradient's rows overlap an input");
+            for (int k = 0; k < i; ++k)
+                if (out[k] && rows_clash(out[i], os[i], out[k], os[k], T, D, es))
+                    return fail(GDN_ERR_INVALID_ARGUMENT, "two gradients' rows overlap");
+            if (overlaps(out[i], no, io->saved, nsv) || overlaps(out[i], no, gr->d_final_state, ns) ||
+                overlaps(out[i], no, gr->d_initial_state, ns) || overlaps(out[i], no, ws, nw) ||
+                overlaps(out[i], no, gr->dA_log, 4 * D) || overlaps(out[i], no, gr->ddt_bias, 4 * D))
+                return fail(GDN_ERR_INVALID_ARGUMENT, "a gradient's rows overlap another buffer");
+        }
+    }
+    if (overlaps(gr->d_initial_state, ns, io->saved, nsv) || overlaps(gr->d_initial_state, ns, ws, nw) ||
+        overlaps(ws, nw, io->saved, nsv) || overlaps(ws, nw, gr->d_final_state, ns))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "workspace, saved and state gradients must not overlap");
+    if (io->N > 0 && (st = recur_workspace(w, ws, ws_bytes, &p, 2 * units)) != GDN_OK) return st;
+    if (!gr->dA_log && !gr->ddt_bias) p.partial = nullptr;
+    if (io->N == 0) {
+        // no tokens: the parameters' gradients are zero
+        hipStream_t s = static_cast<hipStream_t>(stream);
+        hipError_t e = gdn::launch_fill_zero(gr->dA_log, D, s);
+        if (e == hipSuccess) e = gdn::launch_fill_zero(gr->ddt_bias, D, s);
+        if (e != hipSuccess) return fail(GDN_ERR_HIP, "fill launch failed: %s", hipGetErrorString(e));
+        return GDN_OK;
+    }
+    hipError_t e = gdn::launch_recur_backward(p, R->act_dtype == GDN_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "recurrence launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
+gdn_status gdn_recur_decode(const gdn_recur* R, const gdn_recur_io* io, void* stream) {
+    g_err[0] = 0;
+    if (!io) return fail(GDN_ERR_INVALID_ARGUMENT, "io is NULL");
+    gdn_status st = check_recur(R);
+    if (st != GDN_OK) return st;
+    if (io->N < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "N (%d) must be >= 0", io->N);
+    if (static_cast<int64_t>(io->N) * R->D >= (int64_t(1) << 38)) return fail(GDN_ERR_INVALID_ARGUMENT, "N * D too large");
+    if (io->N == 0) return GDN_OK;
+    if (!io->final_state) return fail(GDN_ERR_INVALID_ARGUMENT, "final_state is NULL");
+    gdn::RecurParams p{};
+    if ((st = recur_params(R, io, io->N, &p)) != GDN_OK) return st;
+    if ((st = recur_outputs(R, io, io->N, &p)) != GDN_OK) return st;
+    hipError_t e = gdn::launch_recur_decode(p, R->act_dtype == GDN_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "recurrence launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
 gdn_status gdn_selftest_mfma(const float* A, const float* B, float* C, void* stream) {
     g_err[0] = 0;
     if (!A || !B || !C) return fail(GDN_ERR_INVALID_ARGUMENT, "NULL pointer");

@@ -172,4 +172,52 @@ hipError_t launch_gemm_bf16_nt(const void* A, int64_t lda, const void* B, int64_
                                int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
                                hipStream_t s, GemmPath path = kGemmAuto);
 
+// ---- the diagonal gated recurrence (gdn_recur.hip) -----------------------
+constexpr int kRecurUnit = 256;          // rows (tokens) of one forward tile; a backward tile is half of one
+constexpr int kRecurChannels = 64;       // channels of a tile
+constexpr int kRecurWalkUnits = 2;       // calls of up to this many units of tokens: one work-group per sequence
+constexpr int kRecurWalkSeqs = 512;      // and up to this many sequences
+
+struct RecurParams {
+    int N, D, groups;                    // groups: ceil(D / kRecurChannels)
+    int64_t T;
+    const int32_t* cu;
+    const int32_t* slots;                // [N] pool entry of each sequence's state, or NULL (entry n)
+    int num_slots;
+    int32_t* status;
+    const float* A_log;
+    const float* dt_bias;
+    const void *x, *a, *b, *z;           // z NULL: no output gate
+    void* y;
+    int64_t xs, as, bs, zs, ys;          // row strides, elements
+    const float* h0;
+    float* hT;
+    float* saved;                        // [2 * units][D] state before every half unit (forward: written, may be NULL)
+    int walk;                            // forward without workspace: one work-group walks a sequence
+    // backward
+    const void* dy;
+    void *dx, *da, *db, *dz;
+    int64_t dys, dxs, das, dbs, dzs;
+    const float* dhT;
+    float* dh0;
+    float *dA_log, *ddt_bias;
+    // workspace views
+    int tiles;                           // bound on the number of tiles (units; backward: half units)
+    int32_t* unit_off;                   // [N+1] first unit of each sequence; [N] < 0: the indices were rejected
+    int32_t* unit_seq;                   // [units] sequence of each unit
+    uint32_t* tickets;                   // [groups] next tile of a channel group
+    uint64_t* words;                     // [tiles][groups * kRecurChannels]
+    float2* partial;                     // [tiles][groups * kRecurChannels] sums for dA_log, ddt_bias, or NULL
+};
+
+// Units of N sequences of T rows in all, at most: sum of max(1, ceil(L_n / unit))
+inline int64_t recur_units(int64_t N, int64_t T) { return T / kRecurUnit + N; }
+
+// n floats set to zero (p NULL: nothing)
+hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s);
+
+hipError_t launch_recur_forward(const RecurParams& p, bool bf16, hipStream_t s);
+hipError_t launch_recur_backward(const RecurParams& p, bool bf16, hipStream_t s);
+hipError_t launch_recur_decode(const RecurParams& p, bool bf16, hipStream_t s);
+
 }  // namespace gdn

@@ -500,6 +500,108 @@ gdn_status gdn_snapshot_restore(const gdn_layer* layer, const void* host_buf,
                                 void* conv_state, int32_t slot,
                                 int32_t num_slots, void* stream);
 
+/* ---- the diagonal gated recurrence --------------------------------------
+ * The channel-wise sibling of the delta rule: a state of one value per
+ * channel instead of a matrix per head, with the layer's decay gate.  Per
+ * sequence and channel, token by token (fp32 inside):
+ *
+ *   g_t = -exp(A_log) * softplus(a_t + dt_bias),  alpha_t = exp(g_t)
+ *   h_t = alpha_t h_{t-1} + sqrt(1 - alpha_t^2) * sigmoid(b_t) * x_t
+ *   y_t = h_t * SiLU(z_t)                  (y_t = h_t without z)
+ *
+ * Forward over packed sequences, its backward pass, and one token for each
+ * of a batch of sequences.  A sequence's results are bit-identical whether
+ * it runs alone or in a batch, and from call to call.  Rows are [tokens][D]
+ * with a row stride in elements (0 means dense), so slices of a packed
+ * projection's rows can be given; D, the strides and the addresses need no
+ * more than element alignment. */
+typedef struct {
+    int32_t D;                     /* channels, >= 1 */
+    int32_t act_dtype;             /* gdn_dtype of x, a, b, z, y and their gradients */
+    const float* A_log;            /* [D] */
+    const float* dt_bias;          /* [D] */
+} gdn_recur;
+
+/* Sequence n owns rows [cu_seqlens[n], cu_seqlens[n+1]); lengths may be 0
+ * (the state passes through).  initial_state NULL means zeros; final_state
+ * may equal initial_state (in-place update) but must not partially overlap
+ * it; NULL = not written.  Rows of y past T_total are not touched.  y may be
+ * x, a, b or z itself (same address and stride), and must otherwise share no
+ * bytes with what is read. */
+typedef struct {
+    int32_t N;
+    int64_t T_total;               /* == cu_seqlens[N], < 2^31 */
+    const int32_t* cu_seqlens;     /* device int32 [N+1], non-decreasing, [0] = 0
+                                    * (checked on the device: see status) */
+    const void *x, *a, *b, *z;     /* z optional */
+    int64_t x_stride, a_stride, b_stride, z_stride;
+    void* y;
+    int64_t y_stride;
+    const float* initial_state;    /* [N][D], or [num_slots][D] with state_slots */
+    float* final_state;
+    const int32_t* state_slots;    /* optional pool entries, as in gdn_prefill_io */
+    int32_t num_slots;
+    /* optional, for gdn_recur_backward: gdn_recur_saved_bytes bytes that
+     * receive the state before every GDN_RECUR_SAVED_ROWS-th token of each
+     * sequence: fp32 [.][D], a sequence of L tokens taking 2 * max(1,
+     * ceil(L / (2 * GDN_RECUR_SAVED_ROWS))) entries after those of the
+     * sequences before it (entries past its last token are unspecified). */
+    float* saved;
+    /* optional device int32: 0 after the call, or GDN_STATUS_BAD_INDEX when
+     * cu_seqlens or state_slots break their contract; nothing but the status
+     * word is then written.  (Duplicate entries are not detected.) */
+    int32_t* status;
+} gdn_recur_io;
+
+#define GDN_RECUR_SAVED_ROWS 128
+
+/* Bytes of the saved states of N sequences of T_total tokens in all (an
+ * upper bound over every length split); 0 on error. */
+size_t gdn_recur_saved_bytes(const gdn_recur* recur, int32_t N, int64_t T_total);
+
+/* Bytes of device workspace gdn_recur_forward needs; 0 on error
+ * (gdn_last_error() tells) and where it needs none: calls of up to 512
+ * tokens in all in up to 512 sequences run without one. */
+size_t gdn_recur_workspace_bytes(const gdn_recur* recur, int32_t N, int64_t T_total);
+
+/* Enqueue the forward pass.  workspace: device memory, 256-byte aligned, not
+ * shared with a concurrently running call (its contents need not start at
+ * zero). */
+gdn_status gdn_recur_forward(const gdn_recur* recur, const gdn_recur_io* io,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient's buffers.  dx, da, db (and dz where io has z) are written in
+ * the act dtype, row strides as above; they may be slices of one packed
+ * buffer and must share no bytes with what is read.  d_final_state NULL
+ * means zeros.  dA_log, ddt_bias and d_initial_state are optional. */
+typedef struct {
+    const void* dy;
+    int64_t dy_stride;
+    const float* d_final_state;    /* [N][D] */
+    void *dx, *da, *db, *dz;
+    int64_t dx_stride, da_stride, db_stride, dz_stride;
+    float *dA_log, *ddt_bias;      /* [D], over all tokens */
+    float* d_initial_state;        /* [N][D] */
+} gdn_recur_grad;
+
+/* Bytes of device workspace gdn_recur_backward needs; 0 on error. */
+size_t gdn_recur_backward_workspace_bytes(const gdn_recur* recur, int32_t N, int64_t T_total);
+
+/* Enqueue the backward pass of a gdn_recur_forward call: io as in that call
+ * (x, a, b, z, cu_seqlens and the saved states it wrote are read; y, the
+ * states and the pool entries are not used). */
+gdn_status gdn_recur_backward(const gdn_recur* recur, const gdn_recur_io* io,
+                              const gdn_recur_grad* grad, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* One token for each of io->N sequences: row n is sequence n's token, its
+ * state entry n (or state_slots[n] of the pool) of initial_state, updated
+ * into final_state (required; may equal initial_state).  T_total,
+ * cu_seqlens and saved are not used.  status is never cleared:
+ * GDN_STATUS_BAD_INDEX is ORed in when a state_slots entry is out of range,
+ * and that sequence is skipped. */
+gdn_status gdn_recur_decode(const gdn_recur* recur, const gdn_recur_io* io, void* stream);
+
 /* Static text for a status code. */
 const char* gdn_status_string(gdn_status status);
 

@@ -1,0 +1,404 @@
+"""The diagonal gated recurrence on the device against its fp64 definition:
+forward, backward and one token, over ragged and empty sequences, odd widths,
+packed rows, state pools, both types; the same bits alone and in a batch, from
+call to call and from a replayed graph; nothing written outside the buffers;
+bad indices write nothing."""
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_linear_03_amd as gdn
+import recur_helpers as rh
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}        # half a step of the type, relative
+
+
+class Case:
+    def __init__(self, lens, D, dtype="bf16", gate=True, states=True, seed=0, packed=True, tweak=None):
+        rng = np.random.default_rng(seed)
+        self.lens, self.D, self.dtype = lens, D, dtype
+        T, N = sum(lens), len(lens)
+        self.T, self.N = T, N
+        self.A_log, self.dt_bias = rh.parameters(rng, D)
+        names = ["x", "a", "b"] + (["z"] if gate else [])
+        host = {k: rh.rows(rng, T, D) for k in names + ["dy"]}
+        if tweak:
+            tweak(host)
+        k = len(names)
+        if packed:      # slices of one projection's rows, as many columns again behind them
+            buf = torch.empty((T, k * D + 3), dtype=DT[dtype], device="cuda")
+            self.t = {n: buf[:, i * D:(i + 1) * D] for i, n in enumerate(names)}
+            for n in names:
+                self.t[n].copy_(torch.from_numpy(host[n]))
+        else:
+            self.t = {n: torch.from_numpy(host[n]).to("cuda", DT[dtype]) for n in names}
+        self.t["dy"] = torch.from_numpy(host["dy"]).to("cuda", DT[dtype])
+        self.t.setdefault("z", None)
+        self.f64 = {n: None if v is None else v.double().cpu().numpy() for n, v in self.t.items()}
+        self.h0 = rh.rows(rng, N, D).astype(np.float32) if states else None
+        self.dhT = rh.rows(rng, N, D).astype(np.float32) if states else None
+        self.cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        self.rec = gdn.Recur(D=D, A_log=torch.from_numpy(self.A_log).cuda(), dt_bias=torch.from_numpy(self.dt_bias).cuda(),
+                             act_dtype=gdn.GDN_DTYPE_BF16 if dtype == "bf16" else gdn.GDN_DTYPE_FP32)
+        self.dh0 = None if self.h0 is None else torch.from_numpy(self.h0).cuda()
+        self.ddhT = None if self.dhT is None else torch.from_numpy(self.dhT).cuda()
+
+    def forward(self, **kw):
+        t = self.t
+        return gdn.recur_forward(self.rec, t["x"], t["a"], t["b"], t["z"], self.cu, initial_state=self.dh0, **kw)
+
+    def backward(self, saved, **kw):
+        t = self.t
+        return gdn.recur_backward(self.rec, t["x"], t["a"], t["b"], t["z"], t["dy"], saved, self.cu,
+                                  d_final_state=self.ddhT, want_d_initial=True, **kw)
+
+    def reference(self, grad=True):
+        f = self.f64
+        up = lambda v: None if v is None else v.astype(np.float64)  # noqa: E731
+        return rh.reference(self.lens, f["x"], f["a"], f["b"], f["z"], up(self.A_log), up(self.dt_bias), up(self.h0),
+                            f["dy"] if grad else None, up(self.dhT))
+
+
+def check(name, got, want, bound, half):
+    got = got.double().cpu().numpy()
+    assert got.shape == want.shape, name
+    assert np.isfinite(got).all(), name
+    lim = bound + (np.abs(want) + bound) * half + 1e-37
+    bad = np.abs(got - want) > lim
+    assert not bad.any(), (f"{name}: {int(bad.sum())} values off, worst {np.max(np.abs(got - want) / lim):.2f} of the bound "
+                           f"at {np.argwhere(bad)[:3].tolist()}")
+
+
+SHAPES = [
+    ([1], 1), ([0], 4), ([2, 0, 1], 3), ([7], 64), ([255, 256, 257], 65), ([128, 129, 127], 63), ([512], 192),
+    ([513], 130), ([1024], 64), ([700, 0, 1, 613, 0, 0, 256], 100), ([1, 2, 3, 4] * 40, 70), ([3000, 1], 129),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("gate", [True, False], ids=["gate", "plain"])
+@pytest.mark.parametrize("i", range(len(SHAPES)), ids=[f"{len(n)}x{sum(n)}x{d}" for n, d in SHAPES])
+def test_forward_and_backward(i, gate, dtype):
+    lens, D = SHAPES[i]
+    c = Case(lens, D, dtype, gate, states=i % 2 == 0 or i == 7, seed=i, packed=i % 3 != 1)
+    f = c.forward(want_saved=True)
+    g = c.backward(f["saved"])
+    val, err = c.reference()
+    check("y", f["out"], val["y"], err["y"], HALF[dtype])
+    check("final_state", f["final_state"], val["final"], err["final"], HALF["fp32"])
+    for n in ("dx", "da", "db") + (("dz",) if gate else ()):
+        check(n, g[n], val[n], err[n], HALF[dtype])
+    check("d_initial_state", g["d_initial_state"], val["d_initial"], err["d_initial"], HALF["fp32"])
+    for n in ("dA_log", "ddt_bias"):
+        check(n, g[n], val[n], err[n], HALF["fp32"])
+    assert ("dz" in g) == gate
+
+
+def test_many_tiles_in_one_channel_group():
+    """One chain of 160 tiles forward and 320 backward, all in flight at once:
+    the search for the state before a tile goes over several windows."""
+    c = Case([160 * 256 - 3], 40, "bf16", seed=5)
+    f = c.forward(want_saved=True)
+    g = c.backward(f["saved"])
+    val, err = c.reference()
+    check("y", f["out"], val["y"], err["y"], HALF["bf16"])
+    check("final", f["final_state"], val["final"], err["final"], HALF["fp32"])
+    for n in ("dx", "da", "db", "dz"):
+        check(n, g[n], val[n], err[n], HALF["bf16"])
+    check("d_initial_state", g["d_initial_state"], val["d_initial"], err["d_initial"], HALF["fp32"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_closed_gates(dtype):
+    """Logits far out: decays of exactly 1 and 0, input gates of 0 and 1,
+    output gates far on both sides; the gradients stay finite."""
+    def tweak(h):
+        for k, pat in (("a", (-300.0, 300.0, -90.0, 0.0, 2e4)), ("b", (200.0, -200.0, 0.0)), ("z", (60.0, -60.0, 0.0))):
+            for i, v in enumerate(pat):
+                h[k][:, i::len(pat)] = v
+    c = Case([300, 40], 60, dtype, seed=3, tweak=tweak)
+    f = c.forward(want_saved=True)
+    g = c.backward(f["saved"])
+    val, err = c.reference()
+    check("y", f["out"], val["y"], err["y"], HALF[dtype])
+    check("final", f["final_state"], val["final"], err["final"], HALF["fp32"])
+    for n in ("dx", "da", "db", "dz"):
+        check(n, g[n], val[n], err[n], HALF[dtype])
+
+
+def test_nan_and_inf_stay_in_their_sequence_and_channel():
+    c = Case([300, 280, 290], 130, "fp32", seed=4)
+    clean = c.forward()
+    c.t["x"][400, 7] = float("nan")           # second sequence, channel 7
+    c.t["a"][350, 9] = float("nan")
+    c.t["x"][301, 11] = float("inf")
+    f = c.forward(want_saved=True)
+    torch.cuda.synchronize()
+    touched = torch.zeros_like(f["out"], dtype=torch.bool)
+    touched[400:580, 7] = True
+    touched[350:580, 9] = True
+    touched[301:580, 11] = True
+    assert torch.equal(f["out"][~touched], clean["out"][~touched])
+    assert f["out"][400:580, 7].isnan().all() and f["out"][350:580, 9].isnan().all()
+    assert not f["out"][301:304, 11].isfinite().any()
+    assert f["final_state"][1, 7].isnan() and f["final_state"][[0, 2]].isfinite().all()
+    g = c.backward(f["saved"])                 # h enters da and dz only from row 400 on; ends, finite elsewhere
+    assert g["dx"][:300].isfinite().all() and g["dx"][580:].isfinite().all()
+
+
+def test_same_bits_alone_in_a_batch_and_again():
+    """300 and 512 tokens alone run without a workspace, in the batch with
+    one; bits agree, and so do repeated calls'."""
+    lens, D = [300, 512, 1, 0, 2000, 256], 200
+    c = Case(lens, D, "bf16", seed=8)
+    f = c.forward(want_saved=True)
+    g = c.backward(f["saved"])
+    for _ in range(4):
+        f2 = c.forward(want_saved=True)
+        g2 = c.backward(f2["saved"])
+        assert torch.equal(f2["out"], f["out"]) and torch.equal(f2["final_state"], f["final_state"])
+        for n in g:
+            assert torch.equal(g2[n], g[n]), n
+    at = 0
+    for n, L in enumerate(lens):
+        sl = slice(at, at + L)
+        at += L
+        cu = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+        t = {k: None if v is None else v[sl] for k, v in c.t.items()}
+        one = gdn.recur_forward(c.rec, t["x"], t["a"], t["b"], t["z"], cu, initial_state=c.dh0[n:n + 1], want_saved=True)
+        assert torch.equal(one["out"], f["out"][sl]) and torch.equal(one["final_state"], f["final_state"][n:n + 1])
+        og = gdn.recur_backward(c.rec, t["x"], t["a"], t["b"], t["z"], t["dy"], one["saved"], cu,
+                                d_final_state=c.ddhT[n:n + 1], want_d_initial=True)
+        for k in ("dx", "da", "db", "dz"):
+            assert torch.equal(og[k], g[k][sl]), (n, k)
+        assert torch.equal(og["d_initial_state"], g["d_initial_state"][n:n + 1])
+
+
+def test_resume_and_decode_continue_a_sequence():
+    """A sequence cut in two calls carries on from the state; then token by
+    token, to the bounds of the recurrence (the tiles' order of operations
+    differs, so not to the bit)."""
+    c = Case([900], 96, "fp32", seed=9)
+    val, err = c.reference(grad=False)
+    st = c.dh0.clone()
+    outs = []
+    for lo, hi in ((0, 513), (513, 890)):
+        cu = torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda")
+        r = gdn.recur_forward(c.rec, *(c.t[k][lo:hi] for k in "xabz"), cu, initial_state=st, in_place=True)
+        assert r["final_state"] is st
+        outs.append(r["out"])
+    for t in range(890, 900):
+        r = gdn.recur_decode(c.rec, *(c.t[k][t:t + 1] for k in "xabz"), st)
+        outs.append(r["out"])
+    check("y", torch.cat(outs), val["y"], err["y"], HALF["fp32"])
+    check("final", st, val["final"], err["final"], HALF["fp32"])
+
+
+@pytest.mark.parametrize("B, D, dtype, gate, pool", [(1, 1, "bf16", True, False), (1, 2048, "bf16", True, True),
+                                                     (64, 100, "fp32", False, True), (7, 67, "bf16", False, False),
+                                                     (300, 64, "fp32", True, True)])
+def test_decode(B, D, dtype, gate, pool):
+    c = Case([1] * B, D, dtype, gate, seed=B)
+    val, err = c.reference(grad=False)
+    rng = np.random.default_rng(B)
+    if pool:
+        slots = torch.from_numpy(rng.permutation(2 * B + 1)[:B].astype(np.int32)).cuda()
+        st = torch.full((2 * B + 1, D), 7.5, device="cuda")
+        st[slots.long()] = c.dh0
+        r = gdn.recur_decode(c.rec, c.t["x"], c.t["a"], c.t["b"], c.t["z"], st, state_slots=slots)
+        got = st[slots.long()]
+        rest = torch.ones(2 * B + 1, dtype=torch.bool, device="cuda")
+        rest[slots.long()] = False
+        assert (st[rest] == 7.5).all()
+    else:
+        st = c.dh0.clone()
+        r = gdn.recur_decode(c.rec, c.t["x"], c.t["a"], c.t["b"], c.t["z"], st, in_place=False)
+        assert torch.equal(st, c.dh0)
+        got = r["final_state"]
+    check("y", r["out"], val["y"], err["y"], HALF[dtype])
+    check("state", got, val["final"], err["final"], HALF["fp32"])
+
+
+def test_decode_skips_a_bad_slot():
+    c = Case([1] * 4, 32, "fp32", seed=2)
+    st = c.dh0.clone()
+    slots = torch.tensor([3, -1, 0, 4], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((4, 32), 5.0, device="cuda")
+    gdn.recur_decode(c.rec, c.t["x"], c.t["a"], c.t["b"], c.t["z"], st, state_slots=slots, out=out, status=status)
+    assert int(status) == gdn.GDN_STATUS_BAD_INDEX
+    assert (out[[1, 3]] == 5.0).all() and torch.equal(st[[1, 2]], c.dh0[[1, 2]])
+    assert not torch.equal(st[0], c.dh0[0]) and not torch.equal(st[3], c.dh0[3])
+
+
+def test_state_pool_forward():
+    lens = [300, 0, 400, 5]
+    c = Case(lens, 72, "bf16", seed=11)
+    plain = c.forward()
+    slots = torch.tensor([6, 1, 0, 4], dtype=torch.int32, device="cuda")
+    pool = torch.full((8, 72), -3.0, device="cuda")
+    pool[slots.long()] = c.dh0
+    r = gdn.recur_forward(c.rec, *(c.t[k] for k in "xabz"), c.cu, initial_state=pool, state_slots=slots)
+    assert torch.equal(r["out"], plain["out"]) and torch.equal(pool[slots.long()], plain["final_state"])
+    assert (pool[[2, 3, 5, 7]] == -3.0).all()
+
+
+@pytest.mark.parametrize("lens", [[200, 100], [900, 300]], ids=["short", "long"])
+@pytest.mark.parametrize("what", ["start", "falling", "end", "slot"])
+def test_bad_indices_write_nothing(lens, what):
+    c = Case(lens, 64, "fp32", seed=1)
+    good = c.forward(want_saved=True)
+    cu = c.cu.clone()
+    slots = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    if what == "start":
+        cu[0] = 1
+    elif what == "falling":
+        cu[1] = c.T + 5
+    elif what == "end":
+        cu[2] = c.T - 1
+    else:
+        slots[1] = 2
+    y = torch.full((c.T, 64), 9.0, device="cuda")
+    pool = c.dh0.clone()
+    status = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+    gdn.recur_forward(c.rec, *(c.t[k] for k in "xabz"), cu, initial_state=pool, out=y, state_slots=slots, status=status)
+    assert int(status) == gdn.GDN_STATUS_BAD_INDEX
+    assert (y == 9.0).all() and torch.equal(pool, c.dh0)
+    if what != "slot":
+        g = {n: torch.full((c.T, 64), 9.0, device="cuda") for n in ("dx", "da", "db", "dz")}
+        s = {n: torch.full((64,), 9.0, device="cuda") for n in ("dA_log", "ddt_bias")}
+        ws = torch.empty(gdn.recur_backward_workspace_bytes(c.rec, c.N, c.T), dtype=torch.uint8, device="cuda")
+        gdn.recur_backward_raw(c.rec, N=c.N, T_total=c.T, cu_seqlens=cu, x=c.t["x"], a=c.t["a"], b=c.t["b"], z=c.t["z"],
+                               dy=c.t["dy"], saved=good["saved"], workspace=ws, status=status, **g, **s)
+        assert int(status) == gdn.GDN_STATUS_BAD_INDEX
+        assert all((v == 9.0).all() for v in list(g.values()) + list(s.values()))
+    status.fill_(77)
+    c.forward(status=status)
+    assert int(status) == 0
+
+
+def _margins(shape, dtype, stride=None):
+    """A [rows, cols] view with rows of `stride` elements inside a buffer of
+    sentinel bytes, and a check that only the view's elements changed."""
+    r, k = shape
+    stride = stride or k
+    raw = torch.full((4096 + r * stride * dtype.itemsize + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    body = raw[4096:4096 + r * stride * dtype.itemsize].view(dtype).view(r, stride)
+    view = body[:, :k]
+
+    def intact():
+        return bool((raw[:4096] == 0xA5).all() and (raw[-4096:] == 0xA5).all()
+                    and (body[:, k:].contiguous().view(torch.uint8) == 0xA5).all())
+    return view, intact
+
+
+@pytest.mark.parametrize("lens, D, dtype", [([300, 0, 211], 65, "bf16"), ([700, 1, 90], 66, "fp32"), ([129], 3, "bf16")])
+def test_writes_stay_inside(lens, D, dtype):
+    """Rows of y and the gradients with columns between them; the buffers'
+    rows behind the last sequence are left alone."""
+    c = Case(lens, D, dtype, seed=6)
+    ref = c.forward(want_saved=True)
+    gref = c.backward(ref["saved"])
+    T, N, dt = c.T, c.N, DT[dtype]
+    bufs = {n: _margins((T + 2, D), dt, D + 5) for n in ("y", "dx", "da", "db", "dz")}
+    for v, _ in bufs.values():
+        v[T:] = 3.0
+    st = {n: _margins((N, D), torch.float32) for n in ("final_state", "d_initial_state")}
+    par = {n: _margins((1, D), torch.float32) for n in ("dA_log", "ddt_bias")}
+    wsf = _margins((1, max(1, gdn.recur_workspace_bytes(c.rec, N, T))), torch.uint8)
+    wsb = _margins((1, gdn.recur_backward_workspace_bytes(c.rec, N, T)), torch.uint8)
+    sv = _margins((1, gdn.recur_saved_bytes(c.rec, N, T)), torch.uint8)
+    common = dict(N=N, T_total=T, cu_seqlens=c.cu, **{k: c.t[k] for k in "xabz"})
+    gdn.recur_forward_raw(c.rec, y=bufs["y"][0], initial_state=c.dh0, final_state=st["final_state"][0], saved=sv[0][0],
+                          workspace=wsf[0][0], **common)
+    gdn.recur_backward_raw(c.rec, dy=c.t["dy"], saved=sv[0][0], workspace=wsb[0][0], d_final_state=c.ddhT,
+                           d_initial_state=st["d_initial_state"][0], **{n: bufs[n][0] for n in ("dx", "da", "db", "dz")},
+                           **{n: v[0][0] for n, v in par.items()}, **common)
+    torch.cuda.synchronize()
+    for group in (bufs, st, par):
+        for n, (_, intact) in group.items():
+            assert intact(), n
+    assert wsf[1]() and wsb[1]() and sv[1]()
+    assert torch.equal(bufs["y"][0][:T], ref["out"]) and torch.equal(st["final_state"][0], ref["final_state"])
+    for n in ("dx", "da", "db", "dz"):
+        assert torch.equal(bufs[n][0][:T], gref[n]) and (bufs[n][0][T:] == 3.0).all(), n
+
+
+def test_output_in_an_inputs_place_and_packed_gradients():
+    c = Case([600, 77], 64, "bf16", seed=12)
+    ref = c.forward(want_saved=True)
+    gref = c.backward(ref["saved"])
+    d = torch.empty((c.T, 4 * 64), dtype=torch.bfloat16, device="cuda")
+    views = {n: d[:, i * 64:(i + 1) * 64] for i, n in enumerate(("dx", "da", "db", "dz"))}
+    ws = torch.empty(gdn.recur_backward_workspace_bytes(c.rec, c.N, c.T), dtype=torch.uint8, device="cuda")
+    gdn.recur_backward_raw(c.rec, N=c.N, T_total=c.T, cu_seqlens=c.cu, dy=c.t["dy"], saved=ref["saved"], workspace=ws,
+                           d_final_state=c.ddhT, **{k: c.t[k] for k in "xabz"}, **views)
+    for n, v in views.items():
+        assert torch.equal(v, gref[n]), n
+    r = c.forward(out=c.t["x"])
+    assert torch.equal(r["out"], ref["out"]) and r["out"].data_ptr() == c.t["x"].data_ptr()
+
+
+def test_graph_replays_and_other_stream():
+    """Forward, backward and a decode step captured on a side stream; replays
+    with other inputs match eager calls made in between."""
+    c = Case([900, 130], 96, "bf16", seed=13)
+    d = Case([1] * 5, 96, "bf16", seed=14)
+    st = d.dh0.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        f = c.forward(want_saved=True)
+        g = c.backward(f["saved"])
+        r = gdn.recur_decode(d.rec, *(d.t[k] for k in "xabz"), st, in_place=False)
+        return [f["out"], f["final_state"], *g.values(), r["out"], r["final_state"]]
+
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for k in range(4):
+        c.t["x"].copy_(torch.randn(c.T, 96, generator=gen, device="cuda"))
+        c.t["a"].copy_(torch.randn(c.T, 96, generator=gen, device="cuda"))
+        st.copy_(torch.randn(5, 96, generator=gen, device="cuda"))
+        graph.replay()
+        got = [v.clone() for v in captured]
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), k
+    # the binding on another stream: allocated and launched there
+    torch.cuda.synchronize()
+    want = c.forward()["out"]
+    torch.cuda.synchronize()
+    got = c.forward(stream=side)["out"]
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_binding_refusals():
+    c = Case([20], 16, "bf16", seed=1)
+    t = c.t
+    with pytest.raises(ValueError, match="torch.bfloat16 needed"):
+        gdn.recur_forward(c.rec, t["x"].float(), t["a"], t["b"], t["z"], c.cu)
+    with pytest.raises(ValueError, match="needed"):
+        gdn.recur_forward(c.rec, t["x"][:, :8], t["a"], t["b"], t["z"], c.cu)
+    with pytest.raises(ValueError, match="int32"):
+        gdn.recur_forward(c.rec, t["x"], t["a"], t["b"], t["z"], c.cu.long())
+    with pytest.raises(ValueError, match="a: "):
+        gdn.recur_forward(c.rec, t["x"], t["a"][:10], t["b"], t["z"], c.cu)
+    with pytest.raises(ValueError, match="initial_state"):
+        gdn.recur_forward(c.rec, t["x"], t["a"], t["b"], t["z"], c.cu, initial_state=torch.zeros(1, 8, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        gdn.recur_forward(c.rec, t["x"].t().contiguous().t(), t["a"], t["b"], t["z"], c.cu)
+    with pytest.raises(ValueError, match="saved"):
+        gdn.recur_backward(c.rec, t["x"], t["a"], t["b"], t["z"], t["dy"], torch.empty(8, dtype=torch.uint8, device="cuda"), c.cu)
+    with pytest.raises(ValueError, match="pool"):
+        gdn.recur_forward(c.rec, t["x"], t["a"], t["b"], t["z"], c.cu, state_slots=torch.zeros(1, dtype=torch.int32, device="cuda"))
