@@ -35,6 +35,11 @@ GDN_GEMM_TILED = 1
 GDN_GEMM_FEW_ROWS = 2
 GDN_GEMM_LIBRARY = 3
 GDN_GEMM_LIBRARY_FEW_ROWS = 4
+GDN_ACT_NONE = 0
+GDN_ACT_RELU = 1
+GDN_ACT_GELU = 2
+GDN_ACT_GELU_TANH = 3
+GDN_ACT_SILU = 4
 
 EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_prefill_timed", "gdn_prefill_launches", "gdn_decode", "gdn_decode_multi",
@@ -44,7 +49,8 @@ EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_status_string", "gdn_last_error", "gdn_selftest_mfma", "gdn_prefill_noalloc",
            "gdn_prefill_window_slots", "gdn_decode_workspace_bytes", "gdn_gemm_bf16_path",
            "gdn_recur_saved_bytes", "gdn_recur_workspace_bytes", "gdn_recur_forward",
-           "gdn_recur_backward_workspace_bytes", "gdn_recur_backward", "gdn_recur_decode")
+           "gdn_recur_backward_workspace_bytes", "gdn_recur_backward", "gdn_recur_decode",
+           "gdn_linear", "gdn_linear_backward_workspace_bytes", "gdn_linear_backward")
 NOALLOC_SCRATCH_BYTES = 128 << 20       # GDN_NOALLOC_SCRATCH_BYTES
 SNAPSHOT_MAGIC = 0x50534E47
 SNAPSHOT_VERSION = 1
@@ -156,6 +162,25 @@ class CRecurGrad(ctypes.Structure):
                 ("d_initial_state", ctypes.c_void_p)]
 
 
+class CLinearIO(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("w_stride", ctypes.c_int64), ("bias", ctypes.c_void_p), ("act", ctypes.c_int32),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int32), ("y_stride", ctypes.c_int64),
+                ("preact", ctypes.c_void_p), ("preact_stride", ctypes.c_int64)]
+
+
+class CLinearGrad(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("dy", ctypes.c_void_p), ("dy_dtype", ctypes.c_int32), ("dy_stride", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("w_stride", ctypes.c_int64), ("preact", ctypes.c_void_p),
+                ("preact_stride", ctypes.c_int64), ("act", ctypes.c_int32), ("dx", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64), ("dw", ctypes.c_void_p), ("dw_stride", ctypes.c_int64),
+                ("dbias", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -257,6 +282,13 @@ def lib():
         L.gdn_recur_decode.restype = ctypes.c_int
         L.gdn_recur_decode.argtypes = [ctypes.POINTER(CRecur), ctypes.POINTER(CRecurIO),
                                        ctypes.c_void_p]
+        L.gdn_linear.restype = ctypes.c_int
+        L.gdn_linear.argtypes = [ctypes.POINTER(CLinearIO), ctypes.c_void_p]
+        L.gdn_linear_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_linear_backward_workspace_bytes.argtypes = [ctypes.c_int64] * 3
+        L.gdn_linear_backward.restype = ctypes.c_int
+        L.gdn_linear_backward.argtypes = [ctypes.POINTER(CLinearGrad), ctypes.c_void_p, ctypes.c_size_t,
+                                          ctypes.c_void_p]
         _lib = L
     return _lib
 
@@ -1055,6 +1087,99 @@ def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True,
                          num_slots=0 if state_slots is None else int(state.shape[0]),
                          stream=stream, status=status)
     return {"out": out, "final_state": fs}
+
+
+# ---- the linear layer with its epilogue ---------------------------------------
+
+def _float_code(dtype, name):
+    import torch
+    if dtype == torch.bfloat16:
+        return GDN_DTYPE_BF16
+    if dtype == torch.float32:
+        return GDN_DTYPE_FP32
+    raise ValueError(f"{name}: bfloat16 or float32 needed, not {dtype}")
+
+
+def linear(x, w, bias=None, act=GDN_ACT_NONE, residual=None, out=None, out_dtype=None, preact=None,
+           stream=None):
+    """y = act(x w^T + bias) + residual: x [M, K], w [N, K] bf16 (rows may be
+    strided, in multiples of 8 elements), bias [N] fp32, residual [M, N] of
+    the output's type; act one of GDN_ACT_*.  out: the tensor to write (may
+    be residual), else one of out_dtype (default: residual's type, else
+    bf16).  preact: a bf16 [M, N] tensor that receives x w^T + bias for
+    linear_backward.  Returns the output."""
+    import torch
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"x and w: matrices needed, shapes are {tuple(x.shape)} and {tuple(w.shape)}")
+    M, K = x.shape
+    N = w.shape[0]
+    bf16 = torch.bfloat16
+    px, sx = _matrix(x, "x", M, K, bf16)
+    pw, sw = _matrix(w, "w", N, K, bf16)
+    if out is None:
+        dt = out_dtype if out_dtype is not None else (bf16 if residual is None else residual.dtype)
+        code = _float_code(dt, "out_dtype")
+        with _on(stream):
+            out = torch.empty((M, N), dtype=dt, device=x.device)
+        py, sy = out.data_ptr(), N
+    else:
+        dt = out.dtype
+        if out_dtype is not None and out_dtype != dt:
+            raise ValueError(f"out: {out_dtype} needed, not {dt}")
+        code = _float_code(dt, "out")
+        py, sy = _matrix(out, "out", M, N, dt)
+    pr, sr = (None, 0) if residual is None else _matrix(residual, "residual", M, N, dt)
+    pp, sp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, bf16)
+    io = CLinearIO(M, N, K, px, sx, pw, sw, _dense(bias, "bias", N, None), int(act), pr, sr, py, code, sy,
+                   pp, sp)
+    _check(lib().gdn_linear(ctypes.byref(io), _stream(stream)))
+    return out
+
+
+def linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    n = lib().gdn_linear_backward_workspace_bytes(int(M), int(N), int(K))
+    if n == 0:
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, lib().gdn_last_error().decode())
+    return int(n)
+
+
+def linear_backward(dy, x, w, preact=None, act=GDN_ACT_NONE, want_dx=True, want_dw=True,
+                    want_dbias=False, dx=None, dw=None, dbias=None, workspace=None, stream=None):
+    """Gradients of linear() from dy [M, N] (bf16 or fp32): a dict with dx
+    [M, K] and dw [N, K] (bf16) and, if asked, dbias [N] (fp32).  preact: what
+    linear() wrote there (not needed with GDN_ACT_NONE).  The residual's
+    gradient is dy itself.  dx, dw, dbias: tensors to write instead of new
+    ones."""
+    import torch
+    if dy.dim() != 2 or x.dim() != 2 or w.dim() != 2:
+        raise ValueError("dy, x and w: matrices needed")
+    M, K = x.shape
+    N = w.shape[0]
+    bf16 = torch.bfloat16
+    pdy, sdy = _matrix(dy, "dy", M, N, dy.dtype)
+    code = _float_code(dy.dtype, "dy")
+    px, sx = _matrix(x, "x", M, K, bf16)
+    pw, sw = _matrix(w, "w", N, K, bf16)
+    if preact is None and act != GDN_ACT_NONE:
+        raise ValueError("preact: needed with an activation")
+    pp, sp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, bf16)
+    res = {}
+    with _on(stream):
+        if want_dx or dx is not None:
+            res["dx"] = dx if dx is not None else torch.empty((M, K), dtype=bf16, device=x.device)
+        if want_dw or dw is not None:
+            res["dw"] = dw if dw is not None else torch.empty((N, K), dtype=bf16, device=x.device)
+        if want_dbias or dbias is not None:
+            res["dbias"] = dbias if dbias is not None else torch.empty(N, dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(linear_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=x.device)
+    pdx, sdx = _matrix(res["dx"], "dx", M, K, bf16) if "dx" in res else (None, 0)
+    pdw, sdw = _matrix(res["dw"], "dw", N, K, bf16) if "dw" in res else (None, 0)
+    gr = CLinearGrad(M, N, K, pdy, code, sdy, px, sx, pw, sw, pp, sp, int(act), pdx, sdx, pdw, sdw,
+                     _dense(res.get("dbias"), "dbias", N, None))
+    ws, nb = _bytes(workspace, "workspace")
+    _check(lib().gdn_linear_backward(ctypes.byref(gr), ws, nb, _stream(stream)))
+    return res
 
 
 def snapshot_bytes(layer: Layer) -> int:

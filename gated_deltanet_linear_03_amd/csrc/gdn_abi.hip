@@ -1203,6 +1203,192 @@ gdn_status gdn_recur_decode(const gdn_recur* R, const gdn_recur_io* io, void* st
     return GDN_OK;
 }
 
+// ---- the linear layer with its epilogue ------------------------------------------
+
+static_assert(gdn::kActNone == GDN_ACT_NONE && gdn::kActRelu == GDN_ACT_RELU && gdn::kActGelu == GDN_ACT_GELU &&
+                  gdn::kActGeluTanh == GDN_ACT_GELU_TANH && gdn::kActSilu == GDN_ACT_SILU,
+              "activations of the kernels and the header");
+
+namespace {
+
+gdn_status check_dims(int64_t M, int64_t N, int64_t K) {
+    const int64_t lim = int64_t(1) << 31;
+    if (M < 0 || N < 0 || K < 0 || M >= lim || N >= lim || K >= lim)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "M, N, K must be in [0, 2^31) (%lld, %lld, %lld)", static_cast<long long>(M),
+                    static_cast<long long>(N), static_cast<long long>(K));
+    if (K % 8) return fail(GDN_ERR_INVALID_ARGUMENT, "K (%lld) must be a multiple of 8", static_cast<long long>(K));
+    // one work-group per 64 x 64 tile of an output at the least
+    const int64_t tiles = lim / 2;
+    auto count = [](int64_t r, int64_t c) { return ((r + 63) / 64) * ((c + 63) / 64); };
+    if (count(M, N) >= tiles || count(M, K) + count(N, K) >= tiles || (M / 64 + 1) * (N / 256 + 1) >= tiles)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "output too large");
+    return GDN_OK;
+}
+
+// a bf16 operand that is read in 16-byte runs
+gdn_status check_operand(const char* name, const void* p, int64_t stride, int64_t cols) {
+    if (!p) return fail(GDN_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+    if (!aligned(p, 16) || stride % 8)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned with a stride that is a multiple of 8", name);
+    if (stride < cols) return fail(GDN_ERR_INVALID_ARGUMENT, "%s_stride (%lld) is below its row length", name, static_cast<long long>(stride));
+    return GDN_OK;
+}
+
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+bool any_overlap(const Span& a, const Span* b, int n) {
+    for (int i = 0; i < n; ++i)
+        if (overlaps(a.p, a.n, b[i].p, b[i].n)) return true;
+    return false;
+}
+
+}  // namespace
+
+gdn_status gdn_linear(const gdn_linear_io* io, void* stream) {
+    g_err[0] = 0;
+    if (!io) return fail(GDN_ERR_INVALID_ARGUMENT, "io is NULL");
+    const int64_t M = io->M, N = io->N, K = io->K;
+    gdn_status st = check_dims(M, N, K);
+    if (st != GDN_OK) return st;
+    if (io->act < GDN_ACT_NONE || io->act > GDN_ACT_SILU) return fail(GDN_ERR_INVALID_ARGUMENT, "act %d unknown", io->act);
+    if (io->y_dtype != GDN_DTYPE_BF16 && io->y_dtype != GDN_DTYPE_FP32)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "y_dtype %d unknown", io->y_dtype);
+    if (M == 0 || N == 0) return GDN_OK;
+    const size_t es = act_size(io->y_dtype);
+    gdn::GemmProduct p{};
+    p.M = M; p.N = N; p.K = K;
+    p.A = io->x; p.B = io->w;
+    p.lda = stride_or(io->x_stride, K);
+    p.ldb = stride_or(io->w_stride, K);
+    if (K > 0 && (st = check_operand("x", io->x, p.lda, K)) != GDN_OK) return st;
+    if (K > 0 && (st = check_operand("w", io->w, p.ldb, K)) != GDN_OK) return st;
+    p.ep.bias = io->bias;
+    p.ep.act = io->act;
+    p.ep.bf16 = io->y_dtype == GDN_DTYPE_BF16;
+    p.ep.y = io->y;
+    p.ep.ldy = stride_or(io->y_stride, N);
+    p.ep.residual = io->residual;
+    p.ep.ldr = stride_or(io->residual_stride, N);
+    p.ep.preact = static_cast<uint16_t*>(io->preact);
+    p.ep.ldp = stride_or(io->preact_stride, N);
+    if (!aligned(io->bias, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "bias must be 4-byte aligned");
+    if ((st = check_rows("y", io->y, p.ep.ldy, N, es)) != GDN_OK) return st;
+    if (io->residual && (st = check_rows("residual", io->residual, p.ep.ldr, N, es)) != GDN_OK) return st;
+    if (io->preact && (st = check_rows("preact", io->preact, p.ep.ldp, N, 2)) != GDN_OK) return st;
+    const Span y{io->y, row_bytes(M, p.ep.ldy, N, es)}, pre{io->preact, row_bytes(M, p.ep.ldp, N, 2)};
+    const Span res{io->residual, row_bytes(M, p.ep.ldr, N, es)};
+    const Span in[3] = {{io->x, K > 0 ? row_bytes(M, p.lda, K, 2) : 0}, {io->w, K > 0 ? row_bytes(N, p.ldb, K, 2) : 0},
+                        {io->bias, static_cast<size_t>(4 * N)}};
+    const bool in_place = io->residual == io->y && p.ep.ldr == p.ep.ldy;
+    if (any_overlap(y, in, 3) || any_overlap(pre, in, 3) || any_overlap(pre, &res, 1) || any_overlap(pre, &y, 1) ||
+        (!in_place && any_overlap(y, &res, 1)))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "y or preact overlaps an input or each other");
+    hipError_t e = gdn::launch_linear(p, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "linear launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
+namespace {
+
+struct LinearWs {
+    int64_t ldd = 0, off_part = 0, total = 0;
+};
+
+// dp [M][N rounded up to 8] bf16, then the column sums of its row blocks
+LinearWs linear_ws(int64_t M, int64_t N) {
+    LinearWs w;
+    w.ldd = round_up(N, 8);
+    w.off_part = round_up(2 * M * w.ldd, 256);
+    w.total = w.off_part + round_up(4 * gdn::linear_dp_blocks(M) * N, 256);
+    if (w.total < 256) w.total = 256;
+    return w;
+}
+
+}  // namespace
+
+size_t gdn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    g_err[0] = 0;
+    if (check_dims(M, N, K) != GDN_OK) return 0;
+    return static_cast<size_t>(linear_ws(M, N).total);
+}
+
+gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = 0;
+    if (!gr) return fail(GDN_ERR_INVALID_ARGUMENT, "grad is NULL");
+    const int64_t M = gr->M, N = gr->N, K = gr->K;
+    gdn_status st = check_dims(M, N, K);
+    if (st != GDN_OK) return st;
+    if (gr->act < GDN_ACT_NONE || gr->act > GDN_ACT_SILU) return fail(GDN_ERR_INVALID_ARGUMENT, "act %d unknown", gr->act);
+    if (gr->dy_dtype != GDN_DTYPE_BF16 && gr->dy_dtype != GDN_DTYPE_FP32)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "dy_dtype %d unknown", gr->dy_dtype);
+    // what has elements to write
+    void* dx = M > 0 && K > 0 ? gr->dx : nullptr;
+    void* dw = N > 0 && K > 0 ? gr->dw : nullptr;
+    float* dbias = N > 0 ? gr->dbias : nullptr;
+    if (!dx && !dw && !dbias) return GDN_OK;
+    const size_t ds = act_size(gr->dy_dtype);
+    gdn::LinearDp dp{};
+    gdn::GemmProduct px{}, pw{};
+    dp.M = M; dp.N = N;
+    dp.dy = gr->dy;
+    dp.dy_bf16 = gr->dy_dtype == GDN_DTYPE_BF16;
+    dp.ldy = stride_or(gr->dy_stride, N);
+    dp.act = gr->act;
+    dp.ldp = stride_or(gr->preact_stride, N);
+    const int64_t ldx = stride_or(gr->x_stride, K), ldw = stride_or(gr->w_stride, K);
+    const int64_t lddx = stride_or(gr->dx_stride, K), lddw = stride_or(gr->dw_stride, K);
+    if (M > 0 && N > 0) {
+        if ((st = check_rows("dy", gr->dy, dp.ldy, N, ds)) != GDN_OK) return st;
+        if (gr->act != GDN_ACT_NONE) {
+            if ((st = check_rows("preact", gr->preact, dp.ldp, N, 2)) != GDN_OK) return st;
+            dp.preact = static_cast<const uint16_t*>(gr->preact);
+        }
+    }
+    if (dx && N > 0 && (st = check_operand("w", gr->w, ldw, K)) != GDN_OK) return st;
+    if (dw && M > 0 && (st = check_operand("x", gr->x, ldx, K)) != GDN_OK) return st;
+    if (dx && (st = check_rows("dx", dx, lddx, K, 2)) != GDN_OK) return st;
+    if (dw && (st = check_rows("dw", dw, lddw, K, 2)) != GDN_OK) return st;
+    if (!aligned(gr->dbias, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "dbias must be 4-byte aligned");
+    const LinearWs w = linear_ws(M, N);
+    if (!ws) return fail(GDN_ERR_WORKSPACE, "workspace is NULL (need %lld bytes)", static_cast<long long>(w.total));
+    if (!aligned(ws, 256)) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < static_cast<size_t>(w.total))
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, need %lld", ws_bytes, static_cast<long long>(w.total));
+    const Span in[4] = {{gr->dy, row_bytes(M, dp.ldy, N, ds)},
+                        {dp.preact, dp.preact ? row_bytes(M, dp.ldp, N, 2) : 0},
+                        {gr->x, dw ? row_bytes(M, ldx, K, 2) : 0}, {gr->w, dx ? row_bytes(N, ldw, K, 2) : 0}};
+    const Span out[4] = {{dx, dx ? row_bytes(M, lddx, K, 2) : 0}, {dw, dw ? row_bytes(N, lddw, K, 2) : 0},
+                         {dbias, static_cast<size_t>(4 * N)}, {ws, static_cast<size_t>(w.total)}};
+    for (int i = 0; i < 4; ++i)
+        if (any_overlap(out[i], in, 4) || any_overlap(out[i], out, i))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input or another output");
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    // without an activation a bf16 dy with rows of whole 16-byte runs is dp
+    const bool direct = gr->act == GDN_ACT_NONE && dp.dy_bf16 && aligned(gr->dy, 16) && dp.ldy % 8 == 0 && N % 8 == 0;
+    const void* operand = direct ? gr->dy : base;
+    const int64_t ldd = direct ? dp.ldy : w.ldd;
+    if (!direct && (dx || dw) && M > 0 && N > 0) {
+        dp.dp = reinterpret_cast<uint16_t*>(base);
+        dp.ldd = w.ldd;
+    }
+    if (dbias && M > 0) dp.part = reinterpret_cast<float*>(base + w.off_part);
+    px.A = operand; px.lda = ldd; px.B = gr->w; px.ldb = ldw;
+    px.M = M; px.N = K; px.K = N;
+    pw.A = operand; pw.lda = ldd; pw.B = gr->x; pw.ldb = ldx;
+    pw.M = N; pw.N = K; pw.K = M;
+    px.ep.bf16 = pw.ep.bf16 = 1;
+    px.ep.y = dx; px.ep.ldy = lddx;
+    pw.ep.y = dw; pw.ep.ldy = lddw;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = gdn::launch_linear_backward(dp, px, pw, M > 0 ? dbias : nullptr, s);
+    if (e == hipSuccess && M == 0) e = gdn::launch_fill_zero(dbias, N, s);
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "linear backward launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
 gdn_status gdn_selftest_mfma(const float* A, const float* B, float* C, void* stream) {
     g_err[0] = 0;
     if (!A || !B || !C) return fail(GDN_ERR_INVALID_ARGUMENT, "NULL pointer");

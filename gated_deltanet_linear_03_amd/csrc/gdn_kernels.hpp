@@ -220,4 +220,51 @@ hipError_t launch_recur_forward(const RecurParams& p, bool bf16, hipStream_t s);
 hipError_t launch_recur_backward(const RecurParams& p, bool bf16, hipStream_t s);
 hipError_t launch_recur_decode(const RecurParams& p, bool bf16, hipStream_t s);
 
+// ---- the linear layer with its epilogue (gdn_linear.hip) -------------------
+// The values are those of GDN_ACT_* in gdn.h.
+enum LinearAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+// y = act(sum + bias) + residual; preact receives sum + bias (bf16)
+struct GemmEpilogue {
+    const float* bias;                   // [N] or NULL
+    int act;
+    int bf16;                            // type of y and residual
+    const void* residual;
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+    uint16_t* preact;
+    int64_t ldp;
+};
+
+// C[M][N] = sum over K of A and B, bf16 with fp32 accumulation
+struct GemmProduct {
+    const void *A, *B;
+    int64_t lda, ldb;
+    int64_t M, N, K;
+    GemmEpilogue ep;
+};
+
+// dp[M][ldd] = dy act'(preact) in bf16 (columns past N zero), and its column
+// sums per block of rows; either may be NULL
+struct LinearDp {
+    int64_t M, N;
+    const void* dy;
+    int dy_bf16;
+    int64_t ldy;
+    const uint16_t* preact;
+    int64_t ldp;
+    int act;
+    uint16_t* dp;
+    int64_t ldd;
+    float* part;                         // [linear_dp_blocks(M)][N]
+    int cols;                            // blocks of columns (set by the launcher)
+};
+
+int64_t linear_dp_blocks(int64_t M);
+hipError_t launch_linear(const GemmProduct& p, hipStream_t s);
+// dx or dw with ep.y NULL is left out
+hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias,
+                                  hipStream_t s);
+
 }  // namespace gdn

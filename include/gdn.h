@@ -602,6 +602,79 @@ gdn_status gdn_recur_backward(const gdn_recur* recur, const gdn_recur_io* io,
  * and that sequence is skipped. */
 gdn_status gdn_recur_decode(const gdn_recur* recur, const gdn_recur_io* io, void* stream);
 
+/* ---- the linear layer with its epilogue --------------------------------
+ * y = act(x w^T + bias) + residual in one kernel, and its backward pass: the
+ * projections around a recurrent layer, with the gates' bias and activation
+ * or the residual stream folded into the product.  bf16 operands, fp32
+ * accumulation, epilogue in fp32, one rounding at the end.  This library's
+ * own kernels at every size (gdn_gemm_bf16 is the plain product through the
+ * vendor's library). */
+#define GDN_ACT_NONE 0
+#define GDN_ACT_RELU 1
+#define GDN_ACT_GELU 2             /* p Phi(p), Phi the normal distribution */
+#define GDN_ACT_GELU_TANH 3        /* p (1 + tanh(sqrt(2/pi) (p + 0.044715 p^3))) / 2 */
+#define GDN_ACT_SILU 4             /* p sigmoid(p) */
+
+/* Row strides in elements, 0 means dense.  x, w: 16-byte aligned, K and
+ * their strides multiples of 8; the others element aligned, M and N free.
+ * residual may be y itself (same address and stride); otherwise the bytes
+ * from the first to the last element of y and of preact must not overlap
+ * those of another buffer. */
+typedef struct {
+    int64_t M, N, K;               /* M, N, K >= 0, each < 2^31 */
+    const void* x;                 /* [M][K] bf16 */
+    int64_t x_stride;
+    const void* w;                 /* [N][K] bf16 */
+    int64_t w_stride;
+    const float* bias;             /* optional [N] */
+    int32_t act;                   /* GDN_ACT_* */
+    const void* residual;          /* optional [M][N] in y_dtype */
+    int64_t residual_stride;
+    void* y;                       /* [M][N] */
+    int32_t y_dtype;               /* GDN_DTYPE_BF16 or GDN_DTYPE_FP32 */
+    int64_t y_stride;
+    void* preact;                  /* optional [M][N] bf16: x w^T + bias, for the backward pass */
+    int64_t preact_stride;
+} gdn_linear_io;
+
+/* Enqueue the layer.  Up to 64 rows run on a weight-streaming kernel, more on
+ * a tiled one; both sum in an order that does not depend on the other rows,
+ * but the orders differ, so a row's bits may change when M crosses 64. */
+gdn_status gdn_linear(const gdn_linear_io* io, void* stream);
+
+/* Gradients: dp = dy act'(preact), dbias = column sums of dp, dx = dp w,
+ * dw = dp^T x (the residual's gradient is dy).  dp is an operand of the two
+ * products and rounded to bf16 for them; dbias sums it in fp32.  preact may
+ * be NULL with GDN_ACT_NONE.  Each of dx, dw, dbias may be NULL.  relu has
+ * slope 0 at 0.  The bytes from the first to the last element of an output
+ * must not overlap those of another buffer. */
+typedef struct {
+    int64_t M, N, K;
+    const void* dy;                /* [M][N], element aligned */
+    int32_t dy_dtype;
+    int64_t dy_stride;
+    const void* x;                 /* [M][K] bf16 (needed for dw) */
+    int64_t x_stride;
+    const void* w;                 /* [N][K] bf16 (needed for dx) */
+    int64_t w_stride;
+    const void* preact;            /* [M][N] bf16 */
+    int64_t preact_stride;
+    int32_t act;
+    void* dx;                      /* [M][K] bf16 */
+    int64_t dx_stride;
+    void* dw;                      /* [N][K] bf16 */
+    int64_t dw_stride;
+    float* dbias;                  /* [N] */
+} gdn_linear_grad;
+
+/* Bytes of device workspace gdn_linear_backward needs; 0 on error. */
+size_t gdn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Enqueue the backward pass.  workspace: device memory, 256-byte aligned, not
+ * shared with a concurrently running call. */
+gdn_status gdn_linear_backward(const gdn_linear_grad* grad, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* gdn_status_string(gdn_status status);
 

@@ -1,0 +1,364 @@
+"""The linear layer with its epilogue, forward and backward, on the device
+against its definition in 64 bits: tiles that end inside, single rows,
+reductions of every residue, strided operands, each activation; the same bits
+from call to call and next to other rows; nothing written outside.
+
+Bounds: a 32-bit sum of K products of bf16 values (exact in 32 bits each)
+rounds at most K times in any order, so it is off by at most K 2^-24 sum|x w|;
+the epilogue adds a relative 2^-20 of each activation's terms and half a step
+of the output's type.  In the backward pass dp is rounded to bf16 (by up to
+2^-8 of itself) before the products."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_linear_03_amd as gdn
+
+pytestmark = pytest.mark.gpu
+
+ACTS = {"none": gdn.GDN_ACT_NONE, "relu": gdn.GDN_ACT_RELU, "gelu": gdn.GDN_ACT_GELU,
+        "gelu_tanh": gdn.GDN_ACT_GELU_TANH, "silu": gdn.GDN_ACT_SILU}
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def act64(p, act):
+    """act(p), act'(p) and a bound on |act''| times 1 (all five are below 1.2
+    in second derivative), in float64 on the CPU."""
+    if act == "relu":
+        return p.clamp(min=0), (p > 0).double()
+    if act == "gelu":
+        cdf = 0.5 * torch.erfc(-p / math.sqrt(2))
+        return p * cdf, cdf + p * torch.exp(-p * p / 2) / math.sqrt(2 * math.pi)
+    if act == "gelu_tanh":
+        c = math.sqrt(2 / math.pi)
+        q = torch.sigmoid(2 * c * (p + 0.044715 * p ** 3))
+        return p * q, q + p * q * (1 - q) * 2 * c * (1 + 3 * 0.044715 * p * p)
+    if act == "silu":
+        q = torch.sigmoid(p)
+        return p * q, q * (1 + p * (1 - q))
+    return p, torch.ones_like(p)
+
+
+def close(name, got, want, lim):
+    got = got.double().cpu()
+    assert got.shape == want.shape, name
+    bad = ~((got - want).abs() <= lim)
+    assert not bad.any(), (f"{name}: {int(bad.sum())} off, worst {float(((got - want).abs() / lim).max()):.2f} of the bound at "
+                           f"{bad.nonzero()[:3].tolist()}")
+
+
+def data(M, N, K, seed, pad=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((M, K + pad), generator=g, device="cuda").to(torch.bfloat16)[:, :K]
+    w = (torch.randn((N, K + pad), generator=g, device="cuda") / math.sqrt(max(K, 1))).to(torch.bfloat16)[:, :K]
+    return g, x, w
+
+
+def reference(x, w, bias, act, res):
+    x, w = x.double().cpu(), w.double().cpu()
+    p = x @ w.t()
+    lim = (x.abs() @ w.abs().t()) * (x.shape[1] * 2.0 ** -24)
+    if bias is not None:
+        p = p + bias.double().cpu()
+        lim = lim + p.abs() * 2.0 ** -24
+    y, slope = act64(p, act)
+    # |act(p + d) - act(p)| <= |d| (|slope| + 1.2 |d|)
+    ylim = lim * (slope.abs() + 1.2 * lim) + y.abs() * 2.0 ** -20 + 2.0 ** -22 * (act not in ("none", "relu")) * p.abs()
+    if act == "relu":
+        ylim = lim
+    if res is not None:
+        y = y + res.double().cpu()
+        ylim = ylim + y.abs() * 2.0 ** -24
+    return p, lim, y, ylim
+
+
+SHAPES = [(1, 1, 8), (1, 65, 2048), (2, 200, 72), (16, 16, 128), (17, 33, 136), (33, 100, 640), (64, 130, 256),
+          (65, 7, 8), (65, 64, 64), (100, 129, 72), (129, 255, 200), (300, 300, 1000), (64, 50, 0), (70, 50, 0)]
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("i", range(len(SHAPES)), ids=[f"{m}x{n}x{k}" for m, n, k in SHAPES])
+def test_forward(i, act):
+    M, N, K = SHAPES[i]
+    k = i + list(ACTS).index(act)
+    dt = (torch.bfloat16, torch.float32)[k % 2]
+    g, x, w = data(M, N, K, 100 + i, pad=8 * (k % 3))
+    bias = torch.randn(N, generator=g, device="cuda") if k % 4 != 1 else None
+    res = torch.randn((M, N + k % 3), generator=g, device="cuda").to(dt)[:, :N] if k % 5 > 1 else None
+    pre = torch.empty((M, N + 1), dtype=torch.bfloat16, device="cuda")[:, :N] if k % 2 else None
+    y = gdn.linear(x, w, bias=bias, act=ACTS[act], residual=res, out_dtype=dt, preact=pre)
+    assert y.dtype == dt
+    p, plim, want, lim = reference(x, w, bias, act, res)
+    close("y", y, want, lim + (want.abs() + lim) * HALF[dt] + 1e-37)
+    if pre is not None:
+        close("preact", pre, p, plim + (p.abs() + plim) * HALF[torch.bfloat16] + 1e-37)
+
+
+@pytest.mark.parametrize("M, N, K", [(257, 8200, 264), (4100, 300, 128), (1030, 2050, 520)])
+def test_forward_in_large_tiles(M, N, K):
+    """Enough tiles for each tile size, rows and columns that end inside one."""
+    g, x, w = data(M, N, K, 7)
+    bias = torch.randn(N, generator=g, device="cuda")
+    res = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+    y = gdn.linear(x, w, bias=bias, act=gdn.GDN_ACT_SILU, residual=res)
+    p, _, want, lim = reference(x, w, bias, "silu", res)
+    close("y", y, want, lim + (want.abs() + lim) * HALF[torch.bfloat16])
+
+
+GRADS = [(1, 1, 8), (3, 5, 16), (64, 64, 64), (65, 130, 72), (130, 67, 200), (200, 96, 128), (257, 300, 136), (1000, 33, 264),
+         (0, 16, 8), (5, 0, 8)]
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("i", range(len(GRADS)), ids=[f"{m}x{n}x{k}" for m, n, k in GRADS])
+def test_backward(i, act):
+    M, N, K = GRADS[i]
+    k = i + list(ACTS).index(act)
+    g, x, w = data(M, N, K, 200 + i, pad=8 * (k % 2))
+    dt = (torch.bfloat16, torch.float32)[k % 3 == 1]
+    pad = k % 4
+    dy = torch.randn((M, N + pad), generator=g, device="cuda").to(dt)[:, :N]
+    pre = (2 * torch.randn((M, N + pad), generator=g, device="cuda")).to(torch.bfloat16)[:, :N]
+    r = gdn.linear_backward(dy, x, w, preact=None if act == "none" else pre, act=ACTS[act], want_dbias=True)
+    _gradients(r, dy, x, w, pre, act)
+
+
+def _gradients(r, dy, x, w, pre, act):
+    x, w = x.double().cpu(), w.double().cpu()
+    d = dy.double().cpu()
+    s = act64(pre.double().cpu(), act)[1]
+    dp = d * s
+    # the slope's terms are at most 1 + |p| each, to 2^-20; dp to bf16
+    e = d.abs() * (0 if act in ("none", "relu") else 1) * (1 + pre.double().cpu().abs()) * 2.0 ** -20
+    M, N = dp.shape
+    rnd = 0.0 if act == "none" and dy.dtype == torch.bfloat16 else 2.0 ** -8
+    eb = e + dp.abs() * rnd
+    half = HALF[torch.bfloat16]
+    for name, want, lim in (
+            ("dx", dp @ w, eb @ w.abs() + (dp.abs() @ w.abs()) * (N * 2.0 ** -24)),
+            ("dw", dp.t() @ x, eb.t() @ x.abs() + (dp.abs().t() @ x.abs()) * (M * 2.0 ** -24))):
+        close(name, r[name], want, lim + (want.abs() + lim) * half + 1e-37)
+    close("dbias", r["dbias"], dp.sum(0), e.sum(0) + dp.abs().sum(0) * ((M + 2) * 2.0 ** -24) + 1e-37)
+
+
+@pytest.mark.parametrize("M, N, K", [(4096, 1032, 1024), (520, 4100, 2056), (1100, 1200, 1304)])
+def test_backward_in_large_tiles(M, N, K):
+    g, x, w = data(M, N, K, 8)
+    dy = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+    pre = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+    r = gdn.linear_backward(dy, x, w, preact=pre, act=gdn.GDN_ACT_GELU, want_dbias=True)
+    _gradients(r, dy, x, w, pre, "gelu")
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_slope_against_differences(act):
+    """dbias of a one-row product is act'(preact): against differences of the
+    forward's own values in fp32 (step 2^-6, so off by at most 2^-13 |act'''|
+    / 6 plus the roundings of two values over the step)."""
+    p = torch.linspace(-6, 6, 769, device="cuda").to(torch.bfloat16).float()
+    N = p.numel()
+    x = torch.zeros((1, 8), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((N, 8), dtype=torch.bfloat16, device="cuda")
+    h = 2.0 ** -6
+    f = [gdn.linear(x, w, bias=p + d, act=ACTS[act], out_dtype=torch.float32) for d in (h, -h)]
+    diff = ((f[0] - f[1]) / (2 * h)).double().cpu()
+    r = gdn.linear_backward(torch.ones((1, N), device="cuda"), x, w, preact=p.to(torch.bfloat16)[None], act=ACTS[act],
+                            want_dbias=True)
+    assert (r["dbias"].double().cpu() - diff[0]).abs().max() < 2.0 ** -13 + 16 * 2.0 ** -22 / h
+
+
+def test_special_values():
+    """relu, gelu and silu of infinities and NaN; NaN and Inf in rows behind
+    the reduction's and the output's ends never enter."""
+    M, N, K = 70, 70, 72
+    buf = torch.full((M + 60, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    g, x, w = data(M, N, K, 3)
+    xs, ws = buf[:M, :K], torch.full((N + 60, 128), float("inf"), dtype=torch.bfloat16, device="cuda")[:N, :K]
+    xs.copy_(x)
+    ws.copy_(w)
+    assert torch.equal(gdn.linear(xs, ws), gdn.linear(x, w))
+    few = gdn.linear(xs[:9], ws)
+    assert torch.equal(few, gdn.linear(x[:9], w))
+    dy = torch.full((M, N + 9), float("nan"), dtype=torch.bfloat16, device="cuda")[:, :N]
+    dy.copy_(torch.randn((M, N), generator=g, device="cuda"))
+    a, b = gdn.linear_backward(dy, xs, ws, want_dbias=True), gdn.linear_backward(dy.contiguous(), x, w, want_dbias=True)
+    for n in a:
+        assert torch.equal(a[n], b[n]) and a[n].isfinite().all(), n
+    z = torch.zeros((1, 8), dtype=torch.bfloat16, device="cuda")
+    bias = torch.tensor([float("inf"), float("nan"), -1e30, 1e30, 0.0, -0.0], device="cuda")
+    wz = torch.zeros((6, 8), dtype=torch.bfloat16, device="cuda")
+    for act in ("relu", "gelu", "gelu_tanh", "silu"):
+        y = gdn.linear(z, wz, bias=bias, act=ACTS[act], out_dtype=torch.float32)[0]
+        assert y[0] == float("inf") and y[1].isnan() and y[2] == 0 and y[3] == torch.tensor(1e30) and (y[4:] == 0).all(), act
+        pre = torch.tensor([[float("inf"), float("nan"), -1e30, 1e30, -200.0, 200.0]], device="cuda").to(torch.bfloat16)
+        r = gdn.linear_backward(torch.ones((1, 6), device="cuda"), z, wz, preact=pre, act=ACTS[act], want_dbias=True)
+        d = r["dbias"].tolist()
+        assert d[0] == 1 and math.isnan(d[1]) and d[2:] == [0, 1, 0, 1], act
+
+
+@pytest.mark.parametrize("M, N, K", [(5, 70, 264), (200, 130, 72)])
+def test_writes_stay_inside_and_in_place_residual(M, N, K):
+    g, x, w = data(M, N, K, 5)
+    dy = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+    pre = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+
+    def margins(r, c, dt):
+        raw = torch.full((r + 4, c + 5), 77.0, dtype=dt, device="cuda")
+        return raw[2:2 + r, :c], raw
+
+    for dt in (torch.bfloat16, torch.float32):
+        y, raw = margins(M, N, dt)
+        q, qraw = margins(M, N, torch.bfloat16)
+        gdn.linear(x, w, act=gdn.GDN_ACT_RELU, out=y, preact=q)
+        want = gdn.linear(x, w, act=gdn.GDN_ACT_RELU, out_dtype=dt)
+        assert torch.equal(y, want)
+        for t, v in ((raw, y), (qraw, q)):
+            keep = t.clone()
+            v.fill_(77.0)
+            assert (t == 77.0).all()
+            t.copy_(keep)
+        res = torch.randn((M, N), generator=g, device="cuda").to(dt)
+        want = gdn.linear(x, w, residual=res)
+        assert gdn.linear(x, w, residual=res, out=res) is res and torch.equal(res, want)
+    dx, rx = margins(M, K, torch.bfloat16)
+    dw, rw = margins(N, K, torch.bfloat16)
+    db = torch.full((N + 8,), 77.0, device="cuda")
+    nb = gdn.linear_backward_workspace_bytes(M, N, K)
+    ws = torch.full((nb + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    r = gdn.linear_backward(dy, x, w, preact=pre, act=gdn.GDN_ACT_SILU, dx=dx, dw=dw, dbias=db[:N], workspace=ws[256:256 + nb])
+    ref = gdn.linear_backward(dy, x, w, preact=pre, act=gdn.GDN_ACT_SILU, want_dbias=True)
+    for n in ref:
+        assert torch.equal(r[n], ref[n]), n
+    for t, v in ((rx, dx), (rw, dw), (db, db[:N])):
+        v.fill_(77.0)
+        assert (t == 77.0).all()
+    assert (ws[:256] == 0xA5).all() and (ws[256 + nb:] == 0xA5).all()
+
+
+def test_same_bits_next_to_other_rows_and_again():
+    g, x, w = data(700, 600, 520, 9)
+    y = gdn.linear(x, w)
+    for _ in range(3):
+        assert torch.equal(gdn.linear(x, w), y)
+    assert torch.equal(gdn.linear(x[100:300], w), y[100:300])
+    few = gdn.linear(x[:64], w)
+    assert torch.equal(gdn.linear(x[5:6], w), few[5:6]) and torch.equal(gdn.linear(x[30:50], w), few[30:50])
+    dy = torch.randn((700, 600), generator=g, device="cuda").to(torch.bfloat16)
+    a = gdn.linear_backward(dy, x, w, want_dbias=True)
+    for _ in range(3):
+        b = gdn.linear_backward(dy, x, w, want_dbias=True)
+        assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_graph_replays_and_other_stream():
+    g, x, w = data(300, 200, 264, 10)
+    pre = torch.empty((300, 200), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        y = gdn.linear(x, w, act=gdn.GDN_ACT_GELU, preact=pre)
+        one = gdn.linear(x[:1], w, act=gdn.GDN_ACT_SILU)
+        r = gdn.linear_backward(y, x, w, preact=pre, act=gdn.GDN_ACT_GELU, want_dbias=True)
+        return [y, one, *r.values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for k in range(4):
+        x.copy_(torch.randn((300, 264), generator=g, device="cuda"))
+        graph.replay()
+        got = [v.clone() for v in captured]
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), k
+    torch.cuda.synchronize()
+    want = gdn.linear(x, w)
+    torch.cuda.synchronize()
+    got = gdn.linear(x, w, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_binding_refusals():
+    g, x, w = data(80, 40, 64, 11)
+    with pytest.raises(ValueError, match="bfloat16 needed"):
+        gdn.linear(x.float(), w)
+    with pytest.raises(ValueError, match="needed"):
+        gdn.linear(x, w[:, :56])
+    with pytest.raises(ValueError, match="bias"):
+        gdn.linear(x, w, bias=torch.zeros(39, device="cuda"))
+    with pytest.raises(ValueError, match="residual"):
+        gdn.linear(x, w, residual=torch.zeros((80, 40), device="cuda"), out_dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="bfloat16 or float32"):
+        gdn.linear(x, w, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="preact"):
+        gdn.linear_backward(x @ w.t(), x, w, act=gdn.GDN_ACT_SILU)
+    with pytest.raises(ValueError, match="device tensor"):
+        gdn.linear(x.cpu(), w)
+    with pytest.raises(gdn.GdnError):
+        gdn.linear(x[:, :60], w[:, :60])
+    with pytest.raises(gdn.GdnError):
+        gdn.linear(x, w, act=17)
+
+
+def test_block_of_linear_and_recurrence():
+    """A recurrent block as it is used, forward and backward: one packed
+    projection with bias, the recurrence on its slices, the output projection
+    onto the residual stream; gradients back to the input and every weight,
+    against the same block in 64 bits by automatic differentiation.  Rounding
+    to bf16 between the steps is what separates the two: each of the tensors
+    handed over is rounded once (2^-9 relative, root mean square below
+    2^-9), and no gradient passes through more than six of them."""
+    lens, H, D = [130, 0, 300, 7], 64, 96
+    T = sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x = rn(T, H).to(torch.bfloat16)
+    w_in, w_out = (rn(4 * D, H) / 8).to(torch.bfloat16), (rn(H, D) / 10).to(torch.bfloat16)
+    bias, A_log, dt_bias = rn(4 * D) * 0.1, rn(D) * 0.5, rn(D) - 2
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    rec = gdn.Recur(D=D, A_log=A_log, dt_bias=dt_bias)
+    dout = rn(T, H).to(torch.bfloat16)
+
+    p = gdn.linear(x, w_in, bias=bias)
+    xs, a, b, z = (p[:, i * D:(i + 1) * D] for i in range(4))
+    f = gdn.recur_forward(rec, xs, a, b, z, cu, want_saved=True)
+    out = gdn.linear(f["out"], w_out, residual=x)
+    go = gdn.linear_backward(dout, f["out"], w_out)
+    dp = torch.empty((T, 4 * D), dtype=torch.bfloat16, device="cuda")
+    dA, dd = torch.empty_like(A_log), torch.empty_like(dt_bias)
+    ws = torch.empty(gdn.recur_backward_workspace_bytes(rec, len(lens), T), dtype=torch.uint8, device="cuda")
+    gdn.recur_backward_raw(rec, N=len(lens), T_total=T, cu_seqlens=cu, x=xs, a=a, b=b, z=z, dy=go["dx"], saved=f["saved"],
+                           dA_log=dA, ddt_bias=dd, workspace=ws,
+                           **{n: dp[:, i * D:(i + 1) * D] for i, n in enumerate(("dx", "da", "db", "dz"))})
+    gi = gdn.linear_backward(dp, x, w_in, want_dbias=True)
+    got = {"x": gi["dx"].double() + dout.double(), "w_in": gi["dw"], "bias": gi["dbias"], "w_out": go["dw"], "A_log": dA,
+           "dt_bias": dd}
+
+    leaf = {n: t.double().cpu().requires_grad_() for n, t in (("x", x), ("w_in", w_in), ("bias", bias), ("A_log", A_log),
+                                                               ("dt_bias", dt_bias), ("w_out", w_out))}
+    P = leaf["x"] @ leaf["w_in"].t() + leaf["bias"]
+    X, Av, Bv, Z = (P[:, i * D:(i + 1) * D] for i in range(4))
+    gl = -torch.exp(leaf["A_log"]) * torch.nn.functional.softplus(Av + leaf["dt_bias"])
+    al, u = torch.exp(gl), torch.sqrt(-torch.expm1(2 * gl)) * torch.sigmoid(Bv) * X
+    rows, at = [], 0
+    for L in lens:
+        h = torch.zeros(D, dtype=torch.float64)
+        for t in range(at, at + L):
+            h = al[t] * h + u[t]
+            rows.append(h)
+        at += L
+    Y = torch.stack(rows) * Z * torch.sigmoid(Z)
+    O = Y @ leaf["w_out"].t() + leaf["x"]
+    O.backward(dout.double().cpu())
+    bound = 6 * 2.0 ** -9
+    rel = lambda p, q: float((p.double().cpu() - q).norm() / q.norm())  # noqa: E731
+    assert rel(out, O.detach()) < bound
+    for n, v in got.items():
+        assert rel(v, leaf[n].grad) < bound, n

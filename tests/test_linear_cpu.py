@@ -1,0 +1,98 @@
+"""The linear layer with its epilogue on the host: struct layouts, workspace
+sizes and calls that are refused before anything is enqueued."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import gated_deltanet_linear_03_amd as gdn
+
+FAKE = 0x10000            # never dereferenced
+FAR = 1 << 36
+WS, NWS = FAKE + 20 * FAR, 1 << 34
+
+
+def _io(**kw):
+    io = gdn.CLinearIO()
+    io.M, io.N, io.K = 100, 72, 64
+    io.x, io.w, io.bias, io.residual, io.y, io.preact = (FAKE + i * FAR for i in range(1, 7))
+    io.act, io.y_dtype = gdn.GDN_ACT_SILU, gdn.GDN_DTYPE_BF16
+    for k, v in kw.items():
+        setattr(io, k, v)
+    return io
+
+
+@pytest.mark.parametrize("change, word", [
+    (dict(K=63), "multiple of 8"), (dict(M=-1), "M, N, K"), (dict(N=1 << 31), "M, N, K"), (dict(act=5), "act"),
+    (dict(act=-1), "act"), (dict(y_dtype=2), "y_dtype"), (dict(x=None), "x is NULL"), (dict(w=None), "w is NULL"),
+    (dict(y=None), "y is NULL"), (dict(x=FAKE + FAR + 8), "16-byte"), (dict(x_stride=68), "multiple of 8"),
+    (dict(w_stride=56), "w_stride"), (dict(y_stride=71), "y_stride"), (dict(residual_stride=8), "residual_stride"),
+    (dict(preact_stride=8), "preact_stride"), (dict(bias=FAKE + 2), "bias"), (dict(y=FAKE + 5 * FAR + 1), "element aligned"),
+    (dict(y=FAKE + FAR), "overlaps"), (dict(preact=FAKE + 5 * FAR), "overlaps"), (dict(residual=FAKE + 5 * FAR + 2), "overlaps"),
+    (dict(residual=FAKE + 5 * FAR, residual_stride=80), "overlaps"), (dict(M=1 << 30, N=1 << 30), "too large"),
+])
+def test_linear_refuses(change, word):
+    assert gdn.lib().gdn_linear(ctypes.byref(_io(**change)), None) == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert word in gdn.lib().gdn_last_error().decode()
+
+
+def test_empty_outputs_are_no_calls():
+    for kw in (dict(M=0), dict(N=0)):
+        assert gdn.lib().gdn_linear(ctypes.byref(_io(**kw)), None) == gdn.GDN_OK
+    assert gdn.lib().gdn_linear(None, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+
+
+def _grad(**kw):
+    gr = gdn.CLinearGrad()
+    gr.M, gr.N, gr.K = 100, 72, 64
+    gr.dy, gr.x, gr.w, gr.preact, gr.dx, gr.dw, gr.dbias = (FAKE + i * FAR for i in range(1, 8))
+    gr.dy_dtype, gr.act = gdn.GDN_DTYPE_BF16, gdn.GDN_ACT_GELU
+    for k, v in kw.items():
+        setattr(gr, k, v)
+    return gr
+
+
+@pytest.mark.parametrize("change, word", [
+    (dict(K=60), "multiple of 8"), (dict(act=9), "act"), (dict(dy_dtype=3), "dy_dtype"), (dict(dy=None), "dy is NULL"),
+    (dict(preact=None), "preact is NULL"), (dict(x=None), "x is NULL"), (dict(w=None), "w is NULL"),
+    (dict(x=FAKE + 2 * FAR + 2), "16-byte"), (dict(w_stride=66), "multiple of 8"), (dict(dx_stride=63), "dx_stride"),
+    (dict(dw_stride=8), "dw_stride"), (dict(dbias=FAKE + 1), "dbias"), (dict(dx=FAKE + FAR), "overlaps"),
+    (dict(dw=FAKE + 5 * FAR + 64), "overlaps"), (dict(dbias=WS), "overlaps"),
+])
+def test_backward_refuses(change, word):
+    st = gdn.lib().gdn_linear_backward(ctypes.byref(_grad(**change)), WS, NWS, None)
+    assert st == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert word in gdn.lib().gdn_last_error().decode()
+
+
+def test_backward_workspace():
+    L = gdn.lib()
+    need = L.gdn_linear_backward_workspace_bytes(100, 72, 64)
+    assert need >= 2 * 100 * 72
+    for ws, n in ((None, NWS), (WS + 8, NWS), (WS, need - 1)):
+        assert L.gdn_linear_backward(ctypes.byref(_grad()), ws, n, None) == gdn.GDN_ERR_WORKSPACE
+    assert L.gdn_linear_backward_workspace_bytes(1, 2, 3) == 0 and L.gdn_last_error()
+    assert L.gdn_linear_backward(ctypes.byref(_grad(dx=None, dw=None, dbias=None)), None, 0, None) == gdn.GDN_OK
+
+
+def test_struct_layouts(tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    checks = {"gdn_linear_io": gdn.CLinearIO, "gdn_linear_grad": gdn.CLinearGrad}
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "gdn.h"', "int main(void) {"]
+    for name, cls in checks.items():
+        lines.append(f'  printf("{name} %zu\\n", sizeof({name}));')
+        lines += [f'  printf("{name}.{f} %zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("\n".join(lines + ["  return 0;\n}"]))
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run([cc, "-std=c11", "-I", inc, str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = dict(line.split() for line in subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True,
+                                                       check=True).stdout.splitlines())
+    for name, cls in checks.items():
+        assert int(got[name]) == ctypes.sizeof(cls), name
+        for f, _ in cls._fields_:
+            assert int(got[f"{name}.{f}"]) == getattr(cls, f).offset, (name, f)
