@@ -898,11 +898,15 @@ gdn_status gdn_snapshot_restore(const gdn_layer* L, const void* host, size_t hos
 
 namespace {
 
-static_assert(2 * GDN_RECUR_SAVED_ROWS == gdn::kRecurUnit, "saved states every half unit");
+static_assert(GDN_RECUR_SAVED_ROWS == gdn::kRecurSaved, "rows between saved states");
+constexpr int kHalves = gdn::kRecurUnit / gdn::kRecurSaved;
+
+// the kernels address a tile's rows with 32-bit byte offsets
+constexpr int kMaxStride = 1 << 22;
 
 gdn_status check_recur(const gdn_recur* R) {
     if (!R) return fail(GDN_ERR_INVALID_ARGUMENT, "recur is NULL");
-    if (R->D <= 0 || R->D > (1 << 24)) return fail(GDN_ERR_INVALID_ARGUMENT, "D (%d) must be in [1, 2^24]", R->D);
+    if (R->D <= 0 || R->D > kMaxStride) return fail(GDN_ERR_INVALID_ARGUMENT, "D (%d) must be in [1, 2^22]", R->D);
     if (R->act_dtype != GDN_DTYPE_FP32 && R->act_dtype != GDN_DTYPE_BF16)
         return fail(GDN_ERR_INVALID_ARGUMENT, "act_dtype %d unknown", R->act_dtype);
     return GDN_OK;
@@ -932,7 +936,7 @@ struct RecurWs {
 
 // unit table, sequence of each unit, tickets, words (, backward: the sums)
 RecurWs recur_ws(const gdn_recur* R, int32_t N, int64_t T, bool backward) {
-    const int64_t units = gdn::recur_units(N, T), tiles = backward ? 2 * units : units;
+    const int64_t units = gdn::recur_units(N, T), tiles = backward ? kHalves * units : units;
     const int64_t groups = (R->D + gdn::kRecurChannels - 1) / gdn::kRecurChannels;
     RecurWs w;
     w.off_seq = round_up(4 * (static_cast<int64_t>(N) + 1), 256);
@@ -956,6 +960,11 @@ bool rows_clash(const void* p, int64_t ps, const void* q, int64_t qs, int64_t ro
     const int64_t d = (reinterpret_cast<intptr_t>(p) - reinterpret_cast<intptr_t>(q)) / static_cast<int64_t>(es);
     const int64_t m = ((d % ps) + ps) % ps;
     return m < D || m > ps - D;
+}
+
+gdn_status check_stride(const char* name, int64_t stride) {
+    if (stride > kMaxStride) return fail(GDN_ERR_INVALID_ARGUMENT, "%s_stride (%lld) is above 2^22", name, static_cast<long long>(stride));
+    return GDN_OK;
 }
 
 gdn_status check_rows(const char* name, const void* p, int64_t stride, int64_t D, size_t es) {
@@ -986,10 +995,11 @@ gdn_status recur_params(const gdn_recur* R, const gdn_recur_io* io, int64_t rows
     if (!aligned(io->status, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "status must be 4-byte aligned");
     if (rows > 0) {
         gdn_status st;
-        if ((st = check_rows("x", io->x, p->xs, D, es)) != GDN_OK) return st;
-        if ((st = check_rows("a", io->a, p->as, D, es)) != GDN_OK) return st;
-        if ((st = check_rows("b", io->b, p->bs, D, es)) != GDN_OK) return st;
-        if (io->z && (st = check_rows("z", io->z, p->zs, D, es)) != GDN_OK) return st;
+        if ((st = check_rows("x", io->x, p->xs, D, es)) != GDN_OK || (st = check_stride("x", p->xs)) != GDN_OK) return st;
+        if ((st = check_rows("a", io->a, p->as, D, es)) != GDN_OK || (st = check_stride("a", p->as)) != GDN_OK) return st;
+        if ((st = check_rows("b", io->b, p->bs, D, es)) != GDN_OK || (st = check_stride("b", p->bs)) != GDN_OK) return st;
+        if (io->z && ((st = check_rows("z", io->z, p->zs, D, es)) != GDN_OK || (st = check_stride("z", p->zs)) != GDN_OK))
+            return st;
     }
     return GDN_OK;
 }
@@ -1014,7 +1024,7 @@ gdn_status recur_outputs(const gdn_recur* R, const gdn_recur_io* io, int64_t row
     size_t ny = 0;
     if (rows > 0) {
         gdn_status st = check_rows("y", io->y, p->ys, D, es);
-        if (st != GDN_OK) return st;
+        if (st != GDN_OK || (st = check_stride("y", p->ys)) != GDN_OK) return st;
         ny = row_bytes(rows, p->ys, D, es);
         if (overlaps(io->y, ny, io->initial_state, ns) || overlaps(io->y, ny, io->final_state, ns))
             return fail(GDN_ERR_INVALID_ARGUMENT, "y overlaps a state");
@@ -1054,7 +1064,7 @@ gdn_status recur_workspace(const RecurWs& w, void* ws, size_t ws_bytes, gdn::Rec
 size_t gdn_recur_saved_bytes(const gdn_recur* R, int32_t N, int64_t T) {
     g_err[0] = 0;
     if (check_recur_sizes(R, N, T) != GDN_OK) return 0;
-    const int64_t n = 2 * gdn::recur_units(N, T) * R->D * 4;
+    const int64_t n = kHalves * gdn::recur_units(N, T) * R->D * 4;
     return static_cast<size_t>(n > 0 ? n : 4);
 }
 
@@ -1085,7 +1095,7 @@ gdn_status gdn_recur_forward(const gdn_recur* R, const gdn_recur_io* io, void* w
     p.saved = io->saved;
     p.walk = recur_walks(io->N, io->T_total);
     const int64_t units = gdn::recur_units(io->N, io->T_total);
-    const size_t nsv = static_cast<size_t>(2 * units * R->D) * 4;
+    const size_t nsv = static_cast<size_t>(kHalves * units * R->D) * 4;
     const size_t ns = static_cast<size_t>(io->state_slots ? io->num_slots : io->N) * R->D * 4;
     const size_t ny = row_bytes(io->T_total, p.ys, R->D, act_size(R->act_dtype));
     if (overlaps(io->saved, nsv, io->y, ny) || overlaps(io->saved, nsv, io->initial_state, ns) ||
@@ -1140,15 +1150,17 @@ gdn_status gdn_recur_backward(const gdn_recur* R, const gdn_recur_io* io, const 
     if (bad_alias(gr->d_final_state, ns, gr->d_initial_state, ns))
         return fail(GDN_ERR_INVALID_ARGUMENT, "d_initial_state partially overlaps d_final_state");
     const int64_t units = gdn::recur_units(io->N, T);
-    const size_t nsv = static_cast<size_t>(2 * units * D) * 4;
+    const size_t nsv = static_cast<size_t>(kHalves * units * D) * 4;
     const RecurWs w = recur_ws(R, io->N, T, true);
     const size_t nw = static_cast<size_t>(w.total);
     if (T > 0) {
-        if ((st = check_rows("dy", gr->dy, p.dys, D, es)) != GDN_OK) return st;
-        if ((st = check_rows("dx", gr->dx, p.dxs, D, es)) != GDN_OK) return st;
-        if ((st = check_rows("da", gr->da, p.das, D, es)) != GDN_OK) return st;
-        if ((st = check_rows("db", gr->db, p.dbs, D, es)) != GDN_OK) return st;
-        if (io->z && (st = check_rows("dz", gr->dz, p.dzs, D, es)) != GDN_OK) return st;
+        const char* names[5] = {"dy", "dx", "da", "db", "dz"};
+        const void* rows[5] = {gr->dy, gr->dx, gr->da, gr->db, gr->dz};
+        const int64_t strides[5] = {p.dys, p.dxs, p.das, p.dbs, p.dzs};
+        for (int i = 0; i < (io->z ? 5 : 4); ++i)
+            if ((st = check_rows(names[i], rows[i], strides[i], D, es)) != GDN_OK ||
+                (st = check_stride(names[i], strides[i])) != GDN_OK)
+                return st;
         const void* out[4] = {gr->dx, gr->da, gr->db, io->z ? gr->dz : nullptr};
         const int64_t os[4] = {p.dxs, p.das, p.dbs, p.dzs};
         const void* in[5] = {io->x, io->a, io->b, io->z, gr->dy};
@@ -1171,7 +1183,7 @@ gdn_status gdn_recur_backward(const gdn_recur* R, const gdn_recur_io* io, const 
     if (overlaps(gr->d_initial_state, ns, io->saved, nsv) || overlaps(gr->d_initial_state, ns, ws, nw) ||
         overlaps(ws, nw, io->saved, nsv) || overlaps(ws, nw, gr->d_final_state, ns))
         return fail(GDN_ERR_INVALID_ARGUMENT, "workspace, saved and state gradients must not overlap");
-    if (io->N > 0 && (st = recur_workspace(w, ws, ws_bytes, &p, 2 * units)) != GDN_OK) return st;
+    if (io->N > 0 && (st = recur_workspace(w, ws, ws_bytes, &p, kHalves * units)) != GDN_OK) return st;
     if (!gr->dA_log && !gr->ddt_bias) p.partial = nullptr;
     if (io->N == 0) {
         // no tokens: the parameters' gradients are zero

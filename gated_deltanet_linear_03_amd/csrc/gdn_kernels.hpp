@@ -173,9 +173,10 @@ hipError_t launch_gemm_bf16_nt(const void* A, int64_t lda, const void* B, int64_
                                hipStream_t s, GemmPath path = kGemmAuto);
 
 // ---- the diagonal gated recurrence (gdn_recur.hip) -----------------------
-constexpr int kRecurUnit = 256;          // rows (tokens) of one forward tile; a backward tile is half of one
+constexpr int kRecurUnit = 128;          // rows (tokens) of one forward tile
+constexpr int kRecurSaved = 64;          // rows of a backward tile: a state is saved before each
 constexpr int kRecurChannels = 64;       // channels of a tile
-constexpr int kRecurWalkUnits = 2;       // calls of up to this many units of tokens: one work-group per sequence
+constexpr int kRecurWalkUnits = 4;       // calls of up to this many units of tokens: one work-group per sequence
 constexpr int kRecurWalkSeqs = 512;      // and up to this many sequences
 
 struct RecurParams {
@@ -192,7 +193,7 @@ struct RecurParams {
     int64_t xs, as, bs, zs, ys;          // row strides, elements
     const float* h0;
     float* hT;
-    float* saved;                        // [2 * units][D] state before every half unit (forward: written, may be NULL)
+    float* saved;                        // [units * (kRecurUnit / kRecurSaved)][D] state before every kRecurSaved rows (forward: written, may be NULL)
     int walk;                            // forward without workspace: one work-group walks a sequence
     // backward
     const void* dy;

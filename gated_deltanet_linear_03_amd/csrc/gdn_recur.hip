@@ -37,15 +37,16 @@ namespace gdn {
 
 namespace {
 
-constexpr int kRT = 512;                          // threads of a tile work-group
-constexpr int kRWaves = kRT / kWave;
+constexpr int kThreads = 256;                     // of a tile work-group: four waves
+constexpr int kWaves = kThreads / kWave;
 constexpr int kCh = kRecurChannels;               // channels of a tile
 constexpr int kVC = 4;                            // adjacent channels per lane
 constexpr int kChLanes = kCh / kVC;               // 16 lanes side by side
-constexpr int kGroups = kRT / kChLanes;           // 32 groups of consecutive rows
 constexpr int kGroupsPerWave = kWave / kChLanes;  // 4
+constexpr int kGroups = kThreads / kChLanes;      // 16 groups of consecutive rows
 constexpr int kFwdRows = kRecurUnit / kGroups;    // rows per lane, forward (8)
-constexpr int kBwdTile = kRecurUnit / 2;          // rows of a backward tile
+constexpr int kBwdTile = kRecurSaved;             // rows of a backward tile
+constexpr int kHalves = kRecurUnit / kBwdTile;
 constexpr int kBwdRows = kBwdTile / kGroups;      // rows per lane, backward (4)
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -75,7 +76,7 @@ __device__ __forceinline__ float apply_word(uint64_t w, float s) {
     return hi == kState ? lo : fmaf(__uint_as_float(hi), s, lo);
 }
 
-constexpr int kWindow = 16;                       // words looked at in one go
+constexpr int kWindow = 4;                        // words looked at in one go (4, 8: the same; 16: 1% slower)
 
 // The state after the predecessor tile.  Predecessor k (1 = the nearest,
 // `depth` = the first tile of the sequence) has its word at w + k * step.
@@ -118,7 +119,21 @@ __device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int 
     return s;
 }
 
-// ---- four adjacent channels of one row -------------------------------------
+// A row pointer is a wave-uniform address plus a lane's 32-bit byte offset:
+// the loads and stores of whole tiles then cost no vector address arithmetic.
+template <typename T>
+__device__ __forceinline__ const T* lane_ptr(const T* base, uint32_t off) {
+    return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + off);
+}
+template <typename T>
+__device__ __forceinline__ T* lane_ptr(T* base, uint32_t off) {
+    return reinterpret_cast<T*>(reinterpret_cast<char*>(base) + off);
+}
+
+// ---- four adjacent channels of one row (ONCE: nothing reads them again soon;
+// stores of whole quads are non-temporal too: 131072 x 2048, forward without
+// its arithmetic, 587 us with plain accesses, 559 with such stores, 544 with
+// both) -------------------------------------
 template <bool BF16>
 struct Quad;
 template <>
@@ -126,16 +141,22 @@ struct Quad<true> {
     using T = uint16_t;
     uint32_t lo, hi;
     // rows and tensors are element aligned only (packed projections of any width)
-    struct __attribute__((packed, aligned(2))) Mem { uint32_t lo, hi; };
+    typedef uint32_t Mem __attribute__((ext_vector_type(2), aligned(2)));
+    template <bool ONCE = false>
     __device__ __forceinline__ static Quad load(const T* p) {
-        const Mem m = *reinterpret_cast<const Mem*>(p);
-        return Quad{m.lo, m.hi};
+        const Mem* q = reinterpret_cast<const Mem*>(p);
+        const Mem m = ONCE ? __builtin_nontemporal_load(q) : *q;
+        return Quad{m.x, m.y};
     }
     __device__ __forceinline__ static Quad load(const T* p, int nv) {
         uint32_t e[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[j] = j < nv ? p[j] : 0u;
         return Quad{e[0] | (e[1] << 16), e[2] | (e[3] << 16)};
+    }
+    __device__ __forceinline__ Quad dropped(int n) const {
+        const uint64_t v = n < 4 ? ((static_cast<uint64_t>(hi) << 32) | lo) >> (16 * n) : 0ull;
+        return Quad{static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32)};
     }
     __device__ __forceinline__ float get(int j) const {
         const uint32_t v = j < 2 ? lo : hi;
@@ -144,10 +165,9 @@ struct Quad<true> {
     __device__ __forceinline__ static void store(T* p, const float* f, int nv) {
         if (nv == 4) {
             const f32x2 a = {f[0], f[1]}, b = {f[2], f[3]};
-            Mem m;
-            m.lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2));
-            m.hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2));
-            *reinterpret_cast<Mem*>(p) = m;
+            const Mem m = {__builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2))};
+            __builtin_nontemporal_store(m, reinterpret_cast<Mem*>(p));
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -159,10 +179,12 @@ template <>
 struct Quad<false> {
     using T = float;
     float e[4];
-    struct __attribute__((packed, aligned(4))) Mem { float e[4]; };
+    typedef float Mem __attribute__((ext_vector_type(4), aligned(4)));
+    template <bool ONCE = false>
     __device__ __forceinline__ static Quad load(const T* p) {
-        const Mem m = *reinterpret_cast<const Mem*>(p);
-        return Quad{{m.e[0], m.e[1], m.e[2], m.e[3]}};
+        const Mem* q = reinterpret_cast<const Mem*>(p);
+        const Mem m = ONCE ? __builtin_nontemporal_load(q) : *q;
+        return Quad{{m.x, m.y, m.z, m.w}};
     }
     __device__ __forceinline__ static Quad load(const T* p, int nv) {
         Quad q;
@@ -170,13 +192,15 @@ struct Quad<false> {
         for (int j = 0; j < 4; ++j) q.e[j] = j < nv ? p[j] : 0.f;
         return q;
     }
+    __device__ __forceinline__ Quad dropped(int n) const {
+        return n == 0 ? *this : n == 1 ? Quad{{e[1], e[2], e[3], 0.f}} : n == 2 ? Quad{{e[2], e[3], 0.f, 0.f}}
+                      : n == 3 ? Quad{{e[3], 0.f, 0.f, 0.f}} : Quad{{0.f, 0.f, 0.f, 0.f}};
+    }
     __device__ __forceinline__ float get(int j) const { return e[j]; }
     __device__ __forceinline__ static void store(T* p, const float* f, int nv) {
         if (nv == 4) {
-            Mem m;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m.e[j] = f[j];
-            *reinterpret_cast<Mem*>(p) = m;
+            const Mem m = {f[0], f[1], f[2], f[3]};
+            __builtin_nontemporal_store(m, reinterpret_cast<Mem*>(p));
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -186,46 +210,43 @@ struct Quad<false> {
 };
 
 // ---- the gates -------------------------------------------------------------
-// log(1 + e) / e on [0, 1], degree 9 (interpolated at the Chebyshev points;
-// relative error below 1.3e-8): a polynomial costs less than the hardware
-// log and the division that keeps its small values exact.
-__device__ __forceinline__ float log1p_unit(float e) {
-    float p = -3.176057013e-03f;
-    p = fmaf(p, e, 1.954252832e-02f);
-    p = fmaf(p, e, -5.637361482e-02f);
-    p = fmaf(p, e, 1.054362357e-01f);
-    p = fmaf(p, e, -1.526966691e-01f);
-    p = fmaf(p, e, 1.966327429e-01f);
-    p = fmaf(p, e, -2.495161593e-01f);
-    p = fmaf(p, e, 3.332971036e-01f);
-    p = fmaf(p, e, -4.999989271e-01f);
-    p = fmaf(p, e, 1.0f);
-    return p * e;
+// log(1 + e) on [0, 1] as e times a polynomial of degree 8 (log(1 + e) / e
+// interpolated at the Chebyshev points; relative error below 1e-7): it costs
+// less than the hardware log with the correction that keeps small values
+// exact.
+__device__ __forceinline__ float log1p_unit_over(float e) {
+    float p = 5.126101896e-03f;
+    p = fmaf(p, e, -2.907406539e-02f);
+    p = fmaf(p, e, 7.751608640e-02f);
+    p = fmaf(p, e, -1.360224783e-01f);
+    p = fmaf(p, e, 1.907688081e-01f);
+    p = fmaf(p, e, -2.483539879e-01f);
+    p = fmaf(p, e, 3.331812024e-01f);
+    p = fmaf(p, e, -4.999944568e-01f);
+    return fmaf(p, e, 9.999999404e-01f);
 }
 
 __device__ __forceinline__ float sigmoid_fast(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
 
-// rate2 = exp(A_log) log2(e).  g2 = g log2(e) = -rate2 softplus(v); alpha =
-// 2^g2; q = 1 - alpha^2 = -expm1(2 g), by its series near 0 (seven terms at
-// |2 g| < 0.35: relative error below 2e-8) so that slow channels keep it.
+// nrate2 = -exp(A_log) log2(e).  g2 = g log2(e) = nrate2 softplus(v); alpha =
+// 2^g2; q = 1 - alpha^2 = -expm1(2 g), near 0 from expm1(t) / t (degree 4,
+// relative error below 3e-8 on [-0.35, 0]) so that slow channels keep it.
 struct Gate {
+    float e;                                      // e^-|v|
     float g2, alpha, q;
 };
-__device__ __forceinline__ Gate gate(float v, float rate2) {
-    const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));
-    const float s = fmaxf(v, 0.f) + log1p_unit(e);
+__device__ __forceinline__ Gate gate(float v, float nrate2) {
     Gate r;
-    r.g2 = -rate2 * s;
+    r.e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));
+    r.g2 = nrate2 * fmaf(log1p_unit_over(r.e), r.e, fmaxf(v, 0.f));
     r.alpha = __builtin_amdgcn_exp2f(r.g2);
     const float t = r.g2 * (2.f * kLn2);          // 2 g
-    float p = 1.f / 5040.f;
-    p = fmaf(p, t, 1.f / 720.f);
-    p = fmaf(p, t, 1.f / 120.f);
-    p = fmaf(p, t, 1.f / 24.f);
-    p = fmaf(p, t, 1.f / 6.f);
-    p = fmaf(p, t, 0.5f);
+    float p = 7.211245596e-03f;
+    p = fmaf(p, t, 4.133187234e-02f);
+    p = fmaf(p, t, 1.666253060e-01f);
+    p = fmaf(p, t, 4.999982119e-01f);
     p = fmaf(p, t, 1.f);
     r.q = t > -0.35f ? -t * p : fmaf(-r.alpha, r.alpha, 1.f);
     return r;
@@ -256,6 +277,7 @@ __device__ __forceinline__ Place place_of(int lo, int len, int seq, int unit) {
 struct Lane {
     int wave, lane, cl, rg, nv;                   // cl: lane along the channels; rg: row group of the tile
     int c;                                        // first channel
+    int lc, drop;                                 // quads of a row that ends inside: read at lc, drop the first elements
 };
 __device__ __forceinline__ Lane lane_of(int c0, int D) {
     Lane l;
@@ -266,6 +288,8 @@ __device__ __forceinline__ Lane lane_of(int c0, int D) {
     l.c = c0 + l.cl * kVC;
     const int left = D - l.c;
     l.nv = left < 0 ? 0 : (left < kVC ? left : kVC);
+    l.lc = left < kVC ? D - kVC : l.c;            // (D < kVC: read element by element)
+    l.drop = kVC - l.nv;
     return l;
 }
 
@@ -301,14 +325,25 @@ __device__ __forceinline__ void wave_start(const Lane& l, const float* A, const 
     }
 }
 
+// Four channels of a row in a tile that may end inside them: one load for
+// any width from kVC up.
+template <typename Q>
+__device__ __forceinline__ Q load_edge(const typename Q::T* row, const Lane& l, int D) {
+    if (D >= kVC) return Q::load(row + l.lc).dropped(l.drop);
+    const Q q = Q::load(row + l.c, l.nv);
+    __builtin_amdgcn_sched_barrier(0);            // row by row: the elements' registers are not kept for all rows
+    return q;
+}
+
 // ---- forward ---------------------------------------------------------------
 struct FwdShared {
-    float2 step[kRWaves][kCh];                    // (A, H) of a wave's rows
+    float2 step[kWaves][kCh];                  // (A, H) of a wave's rows
     float start[kCh];                             // state before the tile
     int tile;
 };
 
-template <bool BF16, bool GATE>
+// KEEP: the inputs are read again by a backward pass
+template <bool BF16, bool GATE, bool KEEP>
 struct FwdTile {
     using Q = Quad<BF16>;
     using T = typename Q::T;
@@ -316,44 +351,44 @@ struct FwdTile {
     Q z[kFwdRows];
     float A[kVC], H[kVC];                         // inclusive over the wave's groups
 
-    // Reads the tile's rows, and composes them up to this lane.  Rows past
-    // the unit's end read its last row and act as (A, H) = (1, 0).
-    __device__ __forceinline__ void load(const RecurParams& p, const Place& pl, const Lane& l, const float* rate2,
-                                         const float* bias, bool whole) {
+    // Reads the tile's rows and composes them up to this lane.  WHOLE: every
+    // row and channel of the tile exists.  Otherwise rows past the unit's end
+    // read its last row and act as (A, H) = (1, 0).
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const RecurParams& p, const Place& pl, const Lane& l, const float* nrate2,
+                                         const float* bias) {
         const int r0 = l.rg * kFwdRows;
         Q x[kFwdRows], a[kFwdRows], b[kFwdRows];
-        auto fetch = [&](auto take) {
+        auto fetch = [&](Q* to, const void* from, int64_t stride) {
+            if constexpr (WHOLE) {
+                const T* base = static_cast<const T*>(from) + pl.row0 * stride + (l.c - l.cl * kVC);
+                const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + l.cl * kVC) * sizeof(T);
 #pragma unroll
-            for (int i = 0; i < kFwdRows; ++i) {
-                const int r = r0 + i < pl.rows ? r0 + i : pl.rows - 1;
-                const int64_t row = pl.row0 + r;
-                a[i] = take(static_cast<const T*>(p.a) + row * p.as + l.c);
-                b[i] = take(static_cast<const T*>(p.b) + row * p.bs + l.c);
-                x[i] = take(static_cast<const T*>(p.x) + row * p.xs + l.c);
-            }
-            if constexpr (GATE) {
+                for (int i = 0; i < kFwdRows; ++i) to[i] = Q::template load<!KEEP>(lane_ptr(base + i * stride, off));
+            } else {
 #pragma unroll
                 for (int i = 0; i < kFwdRows; ++i) {
                     const int r = r0 + i < pl.rows ? r0 + i : pl.rows - 1;
-                    z[i] = take(static_cast<const T*>(p.z) + (pl.row0 + r) * p.zs + l.c);
+                    to[i] = load_edge<Q>(static_cast<const T*>(from) + (pl.row0 + r) * stride, l, p.D);
                 }
             }
         };
-        if (whole) fetch([](const T* q) { return Q::load(q); });
-        else fetch([&](const T* q) { return Q::load(q, l.nv); });
-#pragma unroll
-        for (int j = 0; j < kVC; ++j) { A[j] = 1.f; H[j] = 0.f; }
+        fetch(a, p.a, p.as);
+        fetch(b, p.b, p.bs);
+        fetch(x, p.x, p.xs);
+        if constexpr (GATE) fetch(z, p.z, p.zs);
 #pragma unroll
         for (int i = 0; i < kFwdRows; ++i) {
-            const bool on = r0 + i < pl.rows;
 #pragma unroll
             for (int j = 0; j < kVC; ++j) {
-                const Gate g = gate(a[i].get(j) + bias[j], rate2[j]);
-                const float v = __builtin_amdgcn_sqrtf(g.q) * sigmoid_fast(b[i].get(j)) * x[i].get(j);
-                al[i][j] = on ? g.alpha : 1.f;
-                u[i][j] = on ? v : 0.f;
-                H[j] = fmaf(al[i][j], H[j], u[i][j]);
-                A[j] *= al[i][j];
+                const Gate g = gate(a[i].get(j) + bias[j], nrate2[j]);
+                al[i][j] = g.alpha;
+                u[i][j] = __builtin_amdgcn_sqrtf(g.q) * sigmoid_fast(b[i].get(j)) * x[i].get(j);
+                if constexpr (!WHOLE) {
+                    if (r0 + i >= pl.rows) { al[i][j] = 1.f; u[i][j] = 0.f; }
+                }
+                H[j] = i == 0 ? u[i][j] : fmaf(al[i][j], H[j], u[i][j]);
+                A[j] = i == 0 ? al[i][j] : A[j] * al[i][j];
             }
         }
         wave_compose<false>(l, A, H);
@@ -367,6 +402,7 @@ struct FwdTile {
     }
 
     // The rows from the state before the tile (sh.start) to the outputs.
+    template <bool WHOLE>
     __device__ __forceinline__ void finish(const RecurParams& p, const FwdShared& sh, const Place& pl, const Lane& l,
                                            int64_t unit_index) {
         float s[kVC];
@@ -380,11 +416,12 @@ struct FwdTile {
             }
         }
         wave_start<false>(l, A, H, s);
-        if (p.saved && l.rg % (kGroups / 2) == 0) {
-            float* to = p.saved + (2 * unit_index + l.rg / (kGroups / 2)) * p.D + l.c;
-            Quad<false>::store(to, s, l.nv);
-        }
+        constexpr int kPer = kGroups / kHalves;   // row groups between saved states
+        if (p.saved && l.rg % kPer == 0)
+            Quad<false>::store(p.saved + (kHalves * unit_index + l.rg / kPer) * p.D + l.c, s, l.nv);
         const int r0 = l.rg * kFwdRows;
+        T* base = static_cast<T*>(p.y) + pl.row0 * p.ys + (l.c - l.cl * kVC);
+        const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(p.ys) + l.cl * kVC) * sizeof(T);
 #pragma unroll
         for (int i = 0; i < kFwdRows; ++i) {
             float o[kVC];
@@ -397,16 +434,16 @@ struct FwdTile {
                     o[j] *= zj * sigmoid_fast(zj);
                 }
             }
-            if (r0 + i < pl.rows && l.nv > 0)
-                Q::store(static_cast<T*>(p.y) + (pl.row0 + r0 + i) * p.ys + l.c, o, l.nv);
+            if constexpr (WHOLE) Q::store(lane_ptr(base + i * p.ys, off), o, kVC);
+            else if (r0 + i < pl.rows && l.nv > 0) Q::store(lane_ptr(base + i * p.ys, off), o, l.nv);
         }
     }
 };
 
-__device__ __forceinline__ void load_params(const RecurParams& p, const Lane& l, float* rate2, float* bias) {
+__device__ __forceinline__ void load_params(const RecurParams& p, const Lane& l, float* nrate2, float* bias) {
 #pragma unroll
     for (int j = 0; j < kVC; ++j) {
-        rate2[j] = j < l.nv ? expf(p.A_log[l.c + j]) * kLog2e : 0.f;
+        nrate2[j] = j < l.nv ? -kLog2e * expf(p.A_log[l.c + j]) : 0.f;
         bias[j] = j < l.nv ? p.dt_bias[l.c + j] : 0.f;
     }
 }
@@ -415,38 +452,47 @@ __device__ __forceinline__ void load_params(const RecurParams& p, const Lane& l,
 __device__ __forceinline__ float2 tile_step(const float2 (*step)[kCh], int lane, bool rev) {
     float A = 1.f, H = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRWaves; ++w) {
-        const float2 e = step[rev ? kRWaves - 1 - w : w][lane];
+    for (int w = 0; w < kWaves; ++w) {
+        const float2 e = step[rev ? kWaves - 1 - w : w][lane];
         H = fmaf(e.x, H, e.y);
         A *= e.x;
     }
     return make_float2(A, H);
 }
 
-// grid: channel groups x the bound on units
-template <bool BF16, bool GATE>
-__global__ __launch_bounds__(kRT, 2) void recur_forward_kernel(RecurParams p) {
+// Where tile `tile` of the units' table lies (tile < total)
+__device__ __forceinline__ Place unit_place(const RecurParams& p, int unit) {
+    const int seq = p.unit_seq[unit];
+    const int lo = p.cu[seq];
+    return place_of(lo, p.cu[seq + 1] - lo, seq, unit - p.unit_off[seq]);
+}
+
+__device__ __forceinline__ int draw_ticket(const RecurParams& p, int cg) {
+    return static_cast<int>(__hip_atomic_fetch_add(p.tickets + cg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// grid: channel groups x the bound on units.  (Work-groups that stay and draw
+// tile after tile, with the next ticket drawn early, were slower: they need
+// more registers, so fewer run at once.)
+template <bool BF16, bool GATE, bool KEEP>
+__global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams p) {
     __shared__ FwdShared sh;
-    const int total = p.unit_off[p.N];
+    const int total = p.unit_off[p.N];            // < 0: the call's indices were rejected
     const int cg = blockIdx.x % p.groups;
-    if (threadIdx.x == 0)
-        sh.tile = static_cast<int>(__hip_atomic_fetch_add(p.tickets + cg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    if (threadIdx.x == 0) sh.tile = draw_ticket(p, cg);
     const int c0 = cg * kCh;
     const Lane l = lane_of(c0, p.D);
-    float rate2[kVC], bias[kVC];
-    load_params(p, l, rate2, bias);
+    float nrate2[kVC], bias[kVC];
+    load_params(p, l, nrate2, bias);
     __syncthreads();
     const int tile = __builtin_amdgcn_readfirstlane(sh.tile);
-    if (tile >= total) return;                    // total < 0: the call's indices were rejected
-    const int seq = p.unit_seq[tile];
-    const int lo = p.cu[seq];
-    const Place pl = place_of(lo, p.cu[seq + 1] - lo, seq, tile - p.unit_off[seq]);
-
-    FwdTile<BF16, GATE> t;
-    if (pl.rows > 0) {
-        t.load(p, pl, l, rate2, bias, c0 + kCh <= p.D);
-        t.publish(sh, l);
-    }
+    if (tile >= total) return;
+    const Place pl = unit_place(p, tile);
+    FwdTile<BF16, GATE, KEEP> t;
+    const bool whole = pl.rows == kRecurUnit && c0 + kCh <= p.D;
+    if (whole) t.template load<true>(p, pl, l, nrate2, bias);
+    else if (pl.rows > 0) t.template load<false>(p, pl, l, nrate2, bias);
+    if (pl.rows > 0) t.publish(sh, l);
     __syncthreads();
     if (l.wave == 0) {
         const int c = c0 + l.lane;
@@ -455,25 +501,27 @@ __global__ __launch_bounds__(kRT, 2) void recur_forward_kernel(RecurParams p) {
         const bool last = pl.unit + 1 == pl.units;
         float s = 0.f;
         if (pl.unit == 0) {
-            if (p.h0 && c < p.D) s = p.h0[static_cast<int64_t>(state_slot(p.slots, seq)) * p.D + c];
+            if (p.h0 && c < p.D) s = p.h0[static_cast<int64_t>(state_slot(p.slots, pl.seq)) * p.D + c];
         } else {
             if (!last) put_word(w, step_word(e.x, e.y));
             s = look_back(w, -static_cast<int64_t>(p.groups) * kCh, pl.unit);
         }
         const float after = fmaf(e.x, s, e.y);
         if (!last) put_word(w, pack_word(kState, after));
-        else if (p.hT && c < p.D) p.hT[static_cast<int64_t>(state_slot(p.slots, seq)) * p.D + c] = pl.rows > 0 ? after : s;
+        else if (p.hT && c < p.D)
+            p.hT[static_cast<int64_t>(state_slot(p.slots, pl.seq)) * p.D + c] = pl.rows > 0 ? after : s;
         sh.start[l.lane] = s;
     }
     __syncthreads();
-    if (pl.rows > 0) t.finish(p, sh, pl, l, tile);
+    if (whole) t.template finish<true>(p, sh, pl, l, tile);
+    else if (pl.rows > 0) t.template finish<false>(p, sh, pl, l, tile);
 }
 
 // One work-group per (channel group, sequence) walks the sequence's tiles in
 // order: no words, no workspace, one launch.  Same bits: the state after a
 // tile is the same fma.
-template <bool BF16, bool GATE>
-__global__ __launch_bounds__(kRT, 2) void recur_walk_kernel(RecurParams p) {
+template <bool BF16, bool GATE, bool KEEP>
+__global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) {
     __shared__ FwdShared sh;
     __shared__ int bad, first_unit;
     if (threadIdx.x == 0) { bad = 0; first_unit = 0; }
@@ -481,7 +529,7 @@ __global__ __launch_bounds__(kRT, 2) void recur_walk_kernel(RecurParams p) {
     // every work-group checks the indices, so nothing is written on a bad one
     const int seq = blockIdx.x / p.groups;
     int mine = 0, before = 0;
-    for (int n = threadIdx.x; n < p.N; n += kRT) {
+    for (int n = threadIdx.x; n < p.N; n += kThreads) {
         const int lo = p.cu[n], hi = p.cu[n + 1];
         if (hi < lo || (n == 0 && lo != 0) || (n + 1 == p.N && hi != p.T)) mine = 1;
         if (p.slots && (p.slots[n] < 0 || p.slots[n] >= p.num_slots)) mine = 1;
@@ -495,20 +543,23 @@ __global__ __launch_bounds__(kRT, 2) void recur_walk_kernel(RecurParams p) {
     const int cg = blockIdx.x % p.groups;
     const int c0 = cg * kCh;
     const Lane l = lane_of(c0, p.D);
-    float rate2[kVC], bias[kVC];
-    load_params(p, l, rate2, bias);
+    float nrate2[kVC], bias[kVC];
+    load_params(p, l, nrate2, bias);
     const int lo = p.cu[seq], len = p.cu[seq + 1] - lo;
     const int c = c0 + l.lane;
     const int64_t at = static_cast<int64_t>(state_slot(p.slots, seq)) * p.D + c;
     if (l.wave == 0) sh.start[l.lane] = p.h0 && c < p.D ? p.h0[at] : 0.f;
-    FwdTile<BF16, GATE> t;
+    FwdTile<BF16, GATE, KEEP> t;
     const int units = units_of(len);
     for (int k = 0; k < units && len > 0; ++k) {
         const Place pl = place_of(lo, len, seq, k);
-        t.load(p, pl, l, rate2, bias, c0 + kCh <= p.D);
+        const bool whole = pl.rows == kRecurUnit && c0 + kCh <= p.D;
+        if (whole) t.template load<true>(p, pl, l, nrate2, bias);
+        else t.template load<false>(p, pl, l, nrate2, bias);
         t.publish(sh, l);
         __syncthreads();
-        t.finish(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
+        if (whole) t.template finish<true>(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
+        else t.template finish<false>(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
         float after = 0.f;
         if (l.wave == 0) {
             const float2 e = tile_step(sh.step, l.lane, false);
@@ -573,201 +624,234 @@ __global__ __launch_bounds__(kPlanThreads) void recur_plan_kernel(RecurParams p)
 
 // ---- backward --------------------------------------------------------------
 struct BwdShared {
-    float2 fwd[kRWaves][kCh], rev[kRWaves][kCh];
-    float2 sums[kRWaves][kCh];
+    float2 fwd[kWaves][kCh], rev[kWaves][kCh];
+    float2 sums[kWaves][kCh];
     float start[kCh];                             // c past the tile's last row
     int tile;
 };
 
-// grid: channel groups x 2 x the bound on units; a tile is half a unit, and
-// the tiles of a sequence are taken from its end.  The rows' h are run again
-// from the state the forward pass saved at the tile's first row.
+// A lane's rows of a backward tile: what the second half (after the tile's
+// start is known) needs of each element, computed once.
 template <bool BF16, bool GATE>
-__global__ __launch_bounds__(kRT, 2) void recur_backward_kernel(RecurParams p) {
+struct BwdTile {
     using Q = Quad<BF16>;
     using T = typename Q::T;
-    constexpr int L = kBwdRows;
-    __shared__ BwdShared sh;
-    const int total = 2 * p.unit_off[p.N];
-    const int cg = blockIdx.x % p.groups;
-    if (threadIdx.x == 0)
-        sh.tile = static_cast<int>(__hip_atomic_fetch_add(p.tickets + cg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    const int c0 = cg * kCh;
-    const Lane l = lane_of(c0, p.D);
-    float rate2[kVC], bias[kVC];
-    load_params(p, l, rate2, bias);
-    __syncthreads();
-    const int ticket = __builtin_amdgcn_readfirstlane(sh.tile);
-    if (ticket >= total) return;
-    const int tile = total - 1 - ticket;
-    const int seq = p.unit_seq[tile / 2];
-    const int lo = p.cu[seq], len = p.cu[seq + 1] - lo;
-    const Place pl = place_of(lo, len, seq, tile / 2 - p.unit_off[seq]);
-    const int t0 = (tile % 2) * kBwdTile;         // first row within the unit
-    const int left = pl.rows - t0;
-    const int rows = left < 0 ? 0 : (left < kBwdTile ? left : kBwdTile);
-    const int64_t row0 = pl.row0 + t0;
-    const int behind = 2 * pl.units - 1 - (2 * pl.unit + tile % 2);   // tiles of the sequence after this one
+    static constexpr int L = kBwdRows;
+    Q x[L];
+    float al[L][kVC], u[L][kVC];                  // alpha; u, later h before the row
+    float e[L][kVC], dz[L][kVC];                  // dy silu(z), dy silu'(z)
+    float wb[L][kVC], nb[L][kVC];                 // w beta, 1 - beta
+    float k[L][kVC];                              // alpha^2 / w^2 (0 where w is)
+    float sg[L][kVC], g2[L][kVC];                 // sigmoid(v), g log2(e)
+    float A[kVC], H[kVC], Ar[kVC], Hr[kVC];       // inclusive over the wave's groups, both ways
 
-    const int r0 = l.rg * L;
-    Q x[L], a[L], b[L], z[L], dy[L];
-    float al[L][kVC], hp[L][kVC], c[L][kVC];      // alpha, h before the row, alpha dy silu(z)
-    float Af[kVC], Hf[kVC], Ar[kVC], Hr[kVC];
-    if (rows > 0) {
-        auto fetch = [&](auto take) {
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const RecurParams& p, const Lane& l, int64_t row0, int rows, const float* nrate2,
+                                         const float* bias) {
+        const int r0 = l.rg * L;
+        Q a[L], b[L], z[L], dy[L];
+        auto fetch = [&](Q* to, const void* from, int64_t stride) {
+            if constexpr (WHOLE) {
+                const T* base = static_cast<const T*>(from) + row0 * stride + (l.c - l.cl * kVC);
+                const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + l.cl * kVC) * sizeof(T);
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const int64_t row = row0 + (r0 + i < rows ? r0 + i : rows - 1);
-                a[i] = take(static_cast<const T*>(p.a) + row * p.as + l.c);
-                b[i] = take(static_cast<const T*>(p.b) + row * p.bs + l.c);
-                x[i] = take(static_cast<const T*>(p.x) + row * p.xs + l.c);
-                dy[i] = take(static_cast<const T*>(p.dy) + row * p.dys + l.c);
-                if constexpr (GATE) z[i] = take(static_cast<const T*>(p.z) + row * p.zs + l.c);
+                for (int i = 0; i < L; ++i) to[i] = Q::template load<true>(lane_ptr(base + i * stride, off));
+            } else {
+#pragma unroll
+                for (int i = 0; i < L; ++i)
+                    to[i] = load_edge<Q>(static_cast<const T*>(from) + (row0 + (r0 + i < rows ? r0 + i : rows - 1)) * stride, l,
+                                         p.D);
             }
         };
-        if (c0 + kCh <= p.D) fetch([](const T* q) { return Q::load(q); });
-        else fetch([&](const T* q) { return Q::load(q, l.nv); });
-#pragma unroll
-        for (int j = 0; j < kVC; ++j) { Af[j] = Ar[j] = 1.f; Hf[j] = Hr[j] = 0.f; }
+        fetch(a, p.a, p.as);
+        fetch(b, p.b, p.bs);
+        fetch(x, p.x, p.xs);
+        fetch(dy, p.dy, p.dys);
+        if constexpr (GATE) fetch(z, p.z, p.zs);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            const bool on = r0 + i < rows;
 #pragma unroll
             for (int j = 0; j < kVC; ++j) {
-                const Gate g = gate(a[i].get(j) + bias[j], rate2[j]);
-                const float u = __builtin_amdgcn_sqrtf(g.q) * sigmoid_fast(b[i].get(j)) * x[i].get(j);
-                float e = dy[i].get(j);
+                const float v = a[i].get(j) + bias[j];
+                const Gate g = gate(v, nrate2[j]);
+                const float r = __builtin_amdgcn_rcpf(1.f + g.e);
+                sg[i][j] = v < 0.f ? g.e * r : r;
+                g2[i][j] = g.g2;
+                // g -> 0: dx x alpha^2 / w^2 vanishes against sigmoid(v), which multiplies it
+                k[i][j] = g.q > 0.f ? g.alpha * g.alpha * __builtin_amdgcn_rcpf(g.q) : 0.f;
+                const float beta = sigmoid_fast(b[i].get(j));
+                nb[i][j] = 1.f - beta;
+                wb[i][j] = __builtin_amdgcn_sqrtf(g.q) * beta;
+                al[i][j] = g.alpha;
+                u[i][j] = wb[i][j] * x[i].get(j);
+                e[i][j] = dy[i].get(j);
                 if constexpr (GATE) {
-                    const float zj = z[i].get(j);
-                    e *= zj * sigmoid_fast(zj);
+                    const float zj = z[i].get(j), q = sigmoid_fast(zj);
+                    dz[i][j] = e[i][j] * (q * fmaf(zj, 1.f - q, 1.f));
+                    e[i][j] *= zj * q;
                 }
-                al[i][j] = on ? g.alpha : 1.f;
-                hp[i][j] = on ? u : 0.f;          // u for now
-                c[i][j] = on ? g.alpha * e : 0.f;
-                Hf[j] = fmaf(al[i][j], Hf[j], hp[i][j]);
-                Af[j] *= al[i][j];
+                if constexpr (!WHOLE) {
+                    if (r0 + i >= rows) { al[i][j] = 1.f; u[i][j] = 0.f; e[i][j] = 0.f; }
+                }
+                H[j] = i == 0 ? u[i][j] : fmaf(al[i][j], H[j], u[i][j]);
+                A[j] = i == 0 ? al[i][j] : A[j] * al[i][j];
             }
         }
+        // c_t = alpha_t (c_{t+1} + e_t)
 #pragma unroll
-        for (int i = L - 1; i >= 0; --i)
+        for (int j = 0; j < kVC; ++j) {
+            Ar[j] = A[j];
+            Hr[j] = al[L - 1][j] * e[L - 1][j];
 #pragma unroll
-            for (int j = 0; j < kVC; ++j) {
-                Hr[j] = fmaf(al[i][j], Hr[j], c[i][j]);
-                Ar[j] *= al[i][j];
-            }
-        wave_compose<false>(l, Af, Hf);
+            for (int i = L - 2; i >= 0; --i) Hr[j] = al[i][j] * (Hr[j] + e[i][j]);
+        }
+        wave_compose<false>(l, A, H);
         wave_compose<true>(l, Ar, Hr);
+    }
+
+    __device__ __forceinline__ void publish(BwdShared& sh, const Lane& l) {
         if (l.lane / kChLanes == kGroupsPerWave - 1) {
 #pragma unroll
-            for (int j = 0; j < kVC; ++j) sh.fwd[l.wave][l.cl * kVC + j] = make_float2(Af[j], Hf[j]);
+            for (int j = 0; j < kVC; ++j) sh.fwd[l.wave][l.cl * kVC + j] = make_float2(A[j], H[j]);
         }
         if (l.lane / kChLanes == 0) {
 #pragma unroll
             for (int j = 0; j < kVC; ++j) sh.rev[l.wave][l.cl * kVC + j] = make_float2(Ar[j], Hr[j]);
         }
     }
+
+    // sa, sb: sums of dg g2 and of dg sigmoid(v) over the lane's rows
+    template <bool WHOLE>
+    __device__ __forceinline__ void finish(const RecurParams& p, const BwdShared& sh, const Lane& l, int64_t row0, int rows,
+                                           int64_t tile, const float* nrate2, float* sa, float* sb) {
+        float s[kVC], r[kVC], nrate[kVC];
+        const Quad<false> h = Quad<false>::load(p.saved + tile * p.D + l.c, l.nv);
+#pragma unroll
+        for (int j = 0; j < kVC; ++j) {
+            s[j] = h.get(j);
+            r[j] = sh.start[l.cl * kVC + j];
+            nrate[j] = nrate2[j] * kLn2;
+        }
+        for (int w = 0; w < l.wave; ++w)
+#pragma unroll
+            for (int j = 0; j < kVC; ++j) {
+                const float2 t = sh.fwd[w][l.cl * kVC + j];
+                s[j] = fmaf(t.x, s[j], t.y);
+            }
+        for (int w = kWaves - 1; w > l.wave; --w)
+#pragma unroll
+            for (int j = 0; j < kVC; ++j) {
+                const float2 t = sh.rev[w][l.cl * kVC + j];
+                r[j] = fmaf(t.x, r[j], t.y);
+            }
+        wave_start<false>(l, A, H, s);
+        wave_start<true>(l, Ar, Hr, r);
+        const int r0 = l.rg * L;
+        // a row's four gradients at (row0 + r0 + i); strides are of 22 bits, so offsets are of 32
+        auto put = [&](void* to, int64_t stride, int i, const float* f) {
+            T* base = static_cast<T*>(to) + row0 * stride + (l.c - l.cl * kVC);
+            const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + l.cl * kVC) * sizeof(T);
+            if constexpr (WHOLE) Q::store(lane_ptr(base + i * stride, off), f, kVC);
+            else if (r0 + i < rows && l.nv > 0) Q::store(lane_ptr(base + i * stride, off), f, l.nv);
+        };
+#pragma unroll
+        for (int i = 0; i < L; ++i) {             // u: from u to the state before the row; dz
+            float o[kVC];
+#pragma unroll
+            for (int j = 0; j < kVC; ++j) {
+                const float next = fmaf(al[i][j], s[j], u[i][j]);
+                u[i][j] = s[j];
+                s[j] = next;
+                if constexpr (GATE) o[j] = next * dz[i][j];
+            }
+            if constexpr (GATE) put(p.dz, p.dzs, i, o);
+        }
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i) {
+            float dx[kVC], da[kVC], db[kVC];
+#pragma unroll
+            for (int j = 0; j < kVC; ++j) {
+                const float G = e[i][j] + r[j];
+                const float aG = al[i][j] * G;
+                r[j] = aG;
+                dx[j] = G * wb[i][j];
+                const float t = dx[j] * x[i].get(j);
+                db[j] = t * nb[i][j];
+                const float dg = fmaf(aG, u[i][j], -t * k[i][j]);
+                const float ds = dg * sg[i][j];
+                da[j] = ds * nrate[j];
+                if (WHOLE || r0 + i < rows) {
+                    sa[j] = fmaf(dg, g2[i][j], sa[j]);
+                    sb[j] += ds;
+                }
+            }
+            put(p.dx, p.dxs, i, dx);
+            put(p.da, p.das, i, da);
+            put(p.db, p.dbs, i, db);
+        }
+    }
+};
+
+// grid: channel groups x kHalves x the bound on units; the tiles of a sequence
+// are taken from its end.  The rows' h are run again from the state the
+// forward pass saved at the tile's first row.
+template <bool BF16, bool GATE>
+__global__ __launch_bounds__(kThreads, 2) void recur_backward_kernel(RecurParams p) {
+    __shared__ BwdShared sh;
+    const int total = kHalves * p.unit_off[p.N];
+    const int cg = blockIdx.x % p.groups;
+    if (threadIdx.x == 0) sh.tile = draw_ticket(p, cg);
+    const int c0 = cg * kCh;
+    const Lane l = lane_of(c0, p.D);
+    float nrate2[kVC], bias[kVC];
+    load_params(p, l, nrate2, bias);
+    __syncthreads();
+    const int tile = total - 1 - __builtin_amdgcn_readfirstlane(sh.tile);
+    if (tile < 0) return;
+    const Place pl = unit_place(p, tile / kHalves);
+    const int t0 = (tile % kHalves) * kBwdTile;   // first row within the unit
+    const int left = pl.rows - t0;
+    const int rows = left < 0 ? 0 : (left < kBwdTile ? left : kBwdTile);
+    const int64_t row0 = pl.row0 + t0;
+    const bool whole = rows == kBwdTile && c0 + kCh <= p.D;
+    BwdTile<BF16, GATE> t;
+    if (whole) t.template load<true>(p, l, row0, rows, nrate2, bias);
+    else if (rows > 0) t.template load<false>(p, l, row0, rows, nrate2, bias);
+    if (rows > 0) t.publish(sh, l);
     __syncthreads();
     if (l.wave == 0) {
         const int ch = c0 + l.lane;
         const float2 e = rows > 0 ? tile_step(sh.rev, l.lane, true) : make_float2(1.f, 0.f);
         uint64_t* w = p.words + static_cast<int64_t>(tile) * p.groups * kCh + ch;
-        const bool first = 2 * pl.unit + tile % 2 == 0;
+        const bool first = pl.unit == 0 && tile % kHalves == 0;
+        const int behind = kHalves * (pl.units - pl.unit) - 1 - tile % kHalves;   // tiles of the sequence after this one
         float s = 0.f;
         if (behind == 0) {
-            if (p.dhT && ch < p.D) s = p.dhT[static_cast<int64_t>(seq) * p.D + ch];
+            if (p.dhT && ch < p.D) s = p.dhT[static_cast<int64_t>(pl.seq) * p.D + ch];
         } else {
             if (!first) put_word(w, step_word(e.x, e.y));
             s = look_back(w, static_cast<int64_t>(p.groups) * kCh, behind);
         }
         const float after = fmaf(e.x, s, e.y);
         if (!first) put_word(w, pack_word(kState, after));
-        else if (p.dh0 && ch < p.D) p.dh0[static_cast<int64_t>(seq) * p.D + ch] = rows > 0 ? after : s;
+        else if (p.dh0 && ch < p.D) p.dh0[static_cast<int64_t>(pl.seq) * p.D + ch] = rows > 0 ? after : s;
         sh.start[l.lane] = s;
     }
     __syncthreads();
-    float sa[kVC], sb[kVC];                       // sums of dg g2 and of dg sigmoid(v)
+    float sa[kVC], sb[kVC];
 #pragma unroll
     for (int j = 0; j < kVC; ++j) sa[j] = sb[j] = 0.f;
-    if (rows > 0) {
-        float s[kVC], r[kVC];
-        const Quad<false> h = Quad<false>::load(p.saved + static_cast<int64_t>(tile) * p.D + l.c, l.nv);
-#pragma unroll
-        for (int j = 0; j < kVC; ++j) {
-            s[j] = h.get(j);
-            r[j] = sh.start[l.cl * kVC + j];
-        }
-        for (int w = 0; w < l.wave; ++w)
-#pragma unroll
-            for (int j = 0; j < kVC; ++j) {
-                const float2 e = sh.fwd[w][l.cl * kVC + j];
-                s[j] = fmaf(e.x, s[j], e.y);
-            }
-        for (int w = kRWaves - 1; w > l.wave; --w)
-#pragma unroll
-            for (int j = 0; j < kVC; ++j) {
-                const float2 e = sh.rev[w][l.cl * kVC + j];
-                r[j] = fmaf(e.x, r[j], e.y);
-            }
-        wave_start<false>(l, Af, Hf, s);
-        wave_start<true>(l, Ar, Hr, r);
-#pragma unroll
-        for (int i = 0; i < L; ++i)               // hp: from u to the state before the row
-#pragma unroll
-            for (int j = 0; j < kVC; ++j) {
-                const float next = fmaf(al[i][j], s[j], hp[i][j]);
-                hp[i][j] = s[j];
-                s[j] = next;
-            }
-#pragma unroll
-        for (int i = L - 1; i >= 0; --i) {
-            const bool on = r0 + i < rows;
-            float dx[kVC], da[kVC], db[kVC], dz[kVC];
-#pragma unroll
-            for (int j = 0; j < kVC; ++j) {
-                const float v = a[i].get(j) + bias[j];
-                const Gate g = gate(v, rate2[j]);
-                const float w = __builtin_amdgcn_sqrtf(g.q);
-                // g -> 0: alpha / w grows as sigmoid(v) falls, their product goes to 0
-                const float over = g.q > 0.f ? __builtin_amdgcn_rcpf(w) : 0.f;
-                const float beta = sigmoid_fast(b[i].get(j));
-                const float xj = x[i].get(j);
-                float e = dy[i].get(j);
-                if constexpr (GATE) {
-                    const float zj = z[i].get(j), q = sigmoid_fast(zj);
-                    const float hrow = fmaf(al[i][j], hp[i][j], w * beta * xj);
-                    dz[j] = e * hrow * (q * fmaf(zj, 1.f - q, 1.f));
-                    e *= zj * q;
-                }
-                const float G = e + r[j];
-                r[j] = fmaf(al[i][j], r[j], c[i][j]);
-                const float bx = beta * xj;
-                dx[j] = G * w * beta;
-                db[j] = G * w * bx * (1.f - beta);
-                const float dg = g.alpha * G * (hp[i][j] - bx * g.alpha * over);
-                const float ds = dg * sigmoid_fast(v);
-                da[j] = -ds * (rate2[j] * kLn2);
-                if (on) {
-                    sa[j] = fmaf(dg, g.g2, sa[j]);
-                    sb[j] += ds;
-                }
-            }
-            if (on && l.nv > 0) {
-                const int64_t row = row0 + r0 + i;
-                Q::store(static_cast<T*>(p.dx) + row * p.dxs + l.c, dx, l.nv);
-                Q::store(static_cast<T*>(p.da) + row * p.das + l.c, da, l.nv);
-                Q::store(static_cast<T*>(p.db) + row * p.dbs + l.c, db, l.nv);
-                if constexpr (GATE) Q::store(static_cast<T*>(p.dz) + row * p.dzs + l.c, dz, l.nv);
-            }
-        }
-    }
+    if (whole) t.template finish<true>(p, sh, l, row0, rows, tile, nrate2, sa, sb);
+    else if (rows > 0) t.template finish<false>(p, sh, l, row0, rows, tile, nrate2, sa, sb);
     if (!p.partial) return;
     // the tile's sums over its rows, in a fixed order
 #pragma unroll
     for (int j = 0; j < kVC; ++j) {
-        sa[j] += __shfl_xor(sa[j], 16, kWave);
-        sb[j] += __shfl_xor(sb[j], 16, kWave);
-        sa[j] += __shfl_xor(sa[j], 32, kWave);
-        sb[j] += __shfl_xor(sb[j], 32, kWave);
+#pragma unroll
+        for (int d = kChLanes; d < kWave; d *= 2) {
+            sa[j] += __shfl_xor(sa[j], d, kWave);
+            sb[j] += __shfl_xor(sb[j], d, kWave);
+        }
     }
     if (l.lane < kChLanes) {
 #pragma unroll
@@ -775,14 +859,14 @@ __global__ __launch_bounds__(kRT, 2) void recur_backward_kernel(RecurParams p) {
     }
     __syncthreads();
     if (l.wave == 0) {
-        float2 t = sh.sums[0][l.lane];
+        float2 v = sh.sums[0][l.lane];
 #pragma unroll
-        for (int w = 1; w < kRWaves; ++w) {
+        for (int w = 1; w < kWaves; ++w) {
             const float2 e = sh.sums[w][l.lane];
-            t.x += e.x;
-            t.y += e.y;
+            v.x += e.x;
+            v.y += e.y;
         }
-        p.partial[static_cast<int64_t>(tile) * p.groups * kCh + c0 + l.lane] = t;
+        p.partial[static_cast<int64_t>(tile) * p.groups * kCh + c0 + l.lane] = v;
     }
 }
 
@@ -791,7 +875,7 @@ __global__ __launch_bounds__(kRT, 2) void recur_backward_kernel(RecurParams p) {
 constexpr int kSumThreads = 1024, kSumSlices = kSumThreads / kCh;
 
 __global__ __launch_bounds__(kSumThreads) void recur_sum_kernel(RecurParams p) {
-    const int total = 2 * p.unit_off[p.N];
+    const int total = kHalves * p.unit_off[p.N];
     if (total < 0) return;
     __shared__ float2 part[kSumSlices][kCh];
     const int ch = threadIdx.x % kCh, sl = threadIdx.x / kCh;
@@ -846,8 +930,8 @@ __global__ __launch_bounds__(kDecodeThreads) void recur_decode_kernel(RecurParam
     float s[kVC], o[kVC];
 #pragma unroll
     for (int j = 0; j < kVC; ++j) {
-        const float rate2 = j < nv ? expf(p.A_log[c + j]) * kLog2e : 0.f, bias = j < nv ? p.dt_bias[c + j] : 0.f;
-        const Gate g = gate(a.get(j) + bias, rate2);
+        const float nrate2 = j < nv ? -kLog2e * expf(p.A_log[c + j]) : 0.f, bias = j < nv ? p.dt_bias[c + j] : 0.f;
+        const Gate g = gate(a.get(j) + bias, nrate2);
         const float u = __builtin_amdgcn_sqrtf(g.q) * sigmoid_fast(b.get(j)) * x.get(j);
         s[j] = fmaf(g.alpha, h.get(j), u);
         o[j] = s[j];
@@ -873,18 +957,19 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s) {
     return hipGetLastError();
 }
 
-#define GDN_RECUR_CALL(KERNEL, GRID, BLOCK)                                                  \
-    do {                                                                                     \
-        const dim3 g_(static_cast<unsigned>(GRID)), b_(BLOCK);                               \
-        if (bf16 && p.z) hipLaunchKernelGGL((KERNEL<true, true>), g_, b_, 0, s, p);          \
-        else if (bf16) hipLaunchKernelGGL((KERNEL<true, false>), g_, b_, 0, s, p);           \
-        else if (p.z) hipLaunchKernelGGL((KERNEL<false, true>), g_, b_, 0, s, p);            \
-        else hipLaunchKernelGGL((KERNEL<false, false>), g_, b_, 0, s, p);                    \
+// KERNEL<bf16, gate, ...>
+#define GDN_RECUR_CALL(KERNEL, GRID, BLOCK, ...)                                                    \
+    do {                                                                                            \
+        const dim3 g_(static_cast<unsigned>(GRID)), b_(BLOCK);                                      \
+        if (bf16 && p.z) hipLaunchKernelGGL((KERNEL<true, true __VA_ARGS__>), g_, b_, 0, s, p);     \
+        else if (bf16) hipLaunchKernelGGL((KERNEL<true, false __VA_ARGS__>), g_, b_, 0, s, p);      \
+        else if (p.z) hipLaunchKernelGGL((KERNEL<false, true __VA_ARGS__>), g_, b_, 0, s, p);       \
+        else hipLaunchKernelGGL((KERNEL<false, false __VA_ARGS__>), g_, b_, 0, s, p);               \
     } while (0)
 
 static hipError_t launch_plan(const RecurParams& p, hipStream_t s) {
     const int64_t nwords = static_cast<int64_t>(p.tiles) * p.groups * kCh;
-    int64_t blocks = 1 + nwords / (kPlanThreads * 8);
+    int64_t blocks = 1 + nwords / (kPlanThreads * 4);
     if (blocks > 1024) blocks = 1024;
     hipLaunchKernelGGL(recur_plan_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kPlanThreads), 0, s, p);
     return hipGetLastError();
@@ -892,19 +977,21 @@ static hipError_t launch_plan(const RecurParams& p, hipStream_t s) {
 
 hipError_t launch_recur_forward(const RecurParams& p, bool bf16, hipStream_t s) {
     if (p.walk) {
-        GDN_RECUR_CALL(recur_walk_kernel, static_cast<int64_t>(p.groups) * p.N, kRT);
+        GDN_RECUR_CALL(recur_walk_kernel, static_cast<int64_t>(p.groups) * p.N, kThreads, , true);
         return hipGetLastError();
     }
     hipError_t e = launch_plan(p, s);
     if (e != hipSuccess) return e;
-    GDN_RECUR_CALL(recur_forward_kernel, static_cast<int64_t>(p.groups) * p.tiles, kRT);
+    const int64_t grid = static_cast<int64_t>(p.groups) * p.tiles;
+    if (p.saved) GDN_RECUR_CALL(recur_forward_kernel, grid, kThreads, , true);
+    else GDN_RECUR_CALL(recur_forward_kernel, grid, kThreads, , false);
     return hipGetLastError();
 }
 
 hipError_t launch_recur_backward(const RecurParams& p, bool bf16, hipStream_t s) {
     hipError_t e = launch_plan(p, s);
     if (e != hipSuccess) return e;
-    GDN_RECUR_CALL(recur_backward_kernel, static_cast<int64_t>(p.groups) * p.tiles, kRT);
+    GDN_RECUR_CALL(recur_backward_kernel, static_cast<int64_t>(p.groups) * p.tiles, kThreads);
     e = hipGetLastError();
     if (e != hipSuccess || !p.partial) return e;
     hipLaunchKernelGGL(recur_sum_kernel, dim3(static_cast<unsigned>(p.groups)), dim3(kSumThreads), 0, s, p);

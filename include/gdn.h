@@ -513,8 +513,8 @@ gdn_status gdn_snapshot_restore(const gdn_layer* layer, const void* host_buf,
  * of a batch of sequences.  A sequence's results are bit-identical whether
  * it runs alone or in a batch, and from call to call.  Rows are [tokens][D]
  * with a row stride in elements (0 means dense), so slices of a packed
- * projection's rows can be given; D, the strides and the addresses need no
- * more than element alignment. */
+ * projection's rows can be given; D and the strides are at most 2^22, and
+ * they and the addresses need no more than element alignment. */
 typedef struct {
     int32_t D;                     /* channels, >= 1 */
     int32_t act_dtype;             /* gdn_dtype of x, a, b, z, y and their gradients */
@@ -553,7 +553,7 @@ typedef struct {
     int32_t* status;
 } gdn_recur_io;
 
-#define GDN_RECUR_SAVED_ROWS 128
+#define GDN_RECUR_SAVED_ROWS 64
 
 /* Bytes of the saved states of N sequences of T_total tokens in all (an
  * upper bound over every length split); 0 on error. */

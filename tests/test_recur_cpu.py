@@ -51,9 +51,9 @@ def _recur(D=128, act=gdn.GDN_DTYPE_BF16, A_log=FAKE, dt_bias=FAKE):
 def test_sizes():
     L = gdn.lib()
     r = _recur(D=100)
-    # units of 256 rows, one at least per sequence: T / 256 + N bounds their number; two states each
+    # units of 128 rows, one at least per sequence: T / 128 + N bounds their number; two states each
     for N, T in ((1, 1), (1, 4096), (8, 5000), (600, 10)):
-        assert L.gdn_recur_saved_bytes(ctypes.byref(r), N, T) == 2 * (T // 256 + N) * 100 * 4
+        assert L.gdn_recur_saved_bytes(ctypes.byref(r), N, T) == 2 * (T // 128 + N) * 100 * 4
     # short calls run without a workspace, and say so without an error
     assert L.gdn_recur_workspace_bytes(ctypes.byref(r), 3, 512) == 0 and L.gdn_last_error() == b""
     assert L.gdn_recur_workspace_bytes(ctypes.byref(r), 3, 513) > 0
@@ -81,7 +81,7 @@ WS, NWS = FAKE + 20 * FAR, 1 << 30
 @pytest.mark.parametrize("change, word", [
     (dict(x=None), "x is NULL"), (dict(b=None), "b is NULL"), (dict(y=None), "y is NULL"),
     (dict(x=FAKE + FAR + 1), "element aligned"), (dict(x_stride=100), "x_stride"),
-    (dict(y_stride=127), "y_stride"), (dict(N=-1), "N"), (dict(T_total=-3), "T_total"),
+    (dict(y_stride=127), "y_stride"), (dict(a_stride=(1 << 22) + 1), "2^22"), (dict(N=-1), "N"), (dict(T_total=-3), "T_total"),
     (dict(N=0), "N == 0"), (dict(T_total=1 << 31), "2^31"), (dict(cu_seqlens=None), "cu_seqlens"),
     (dict(cu_seqlens=FAKE + 2), "cu_seqlens"), (dict(status=FAKE + 1), "status"),
     (dict(state_slots=FAKE, num_slots=0), "num_slots"),
