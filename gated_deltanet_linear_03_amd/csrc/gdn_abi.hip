@@ -1228,7 +1228,8 @@ gdn_status check_dims(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M >= lim || N >= lim || K >= lim)
         return fail(GDN_ERR_INVALID_ARGUMENT, "M, N, K must be in [0, 2^31) (%lld, %lld, %lld)", static_cast<long long>(M),
                     static_cast<long long>(N), static_cast<long long>(K));
-    if (K % 8) return fail(GDN_ERR_INVALID_ARGUMENT, "K (%lld) must be a multiple of 8", static_cast<long long>(K));
+    if (K % 8 || K > kMaxStride)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "K (%lld) must be a multiple of 8 up to 2^22", static_cast<long long>(K));
     // one work-group per 64 x 64 tile of an output at the least
     const int64_t tiles = lim / 2;
     auto count = [](int64_t r, int64_t c) { return ((r + 63) / 64) * ((c + 63) / 64); };
@@ -1243,7 +1244,7 @@ gdn_status check_operand(const char* name, const void* p, int64_t stride, int64_
     if (!aligned(p, 16) || stride % 8)
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned with a stride that is a multiple of 8", name);
     if (stride < cols) return fail(GDN_ERR_INVALID_ARGUMENT, "%s_stride (%lld) is below its row length", name, static_cast<long long>(stride));
-    return GDN_OK;
+    return check_stride(name, stride);
 }
 
 struct Span {
@@ -1319,11 +1320,17 @@ LinearWs linear_ws(int64_t M, int64_t N) {
     return w;
 }
 
+// dp's rows are an operand too
+gdn_status check_backward(int64_t N) {
+    if (N > kMaxStride) return fail(GDN_ERR_INVALID_ARGUMENT, "N (%lld) must be at most 2^22", static_cast<long long>(N));
+    return GDN_OK;
+}
+
 }  // namespace
 
 size_t gdn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     g_err[0] = 0;
-    if (check_dims(M, N, K) != GDN_OK) return 0;
+    if (check_dims(M, N, K) != GDN_OK || check_backward(N) != GDN_OK) return 0;
     return static_cast<size_t>(linear_ws(M, N).total);
 }
 
@@ -1332,7 +1339,7 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_by
     if (!gr) return fail(GDN_ERR_INVALID_ARGUMENT, "grad is NULL");
     const int64_t M = gr->M, N = gr->N, K = gr->K;
     gdn_status st = check_dims(M, N, K);
-    if (st != GDN_OK) return st;
+    if (st != GDN_OK || (st = check_backward(N)) != GDN_OK) return st;
     if (gr->act < GDN_ACT_NONE || gr->act > GDN_ACT_SILU) return fail(GDN_ERR_INVALID_ARGUMENT, "act %d unknown", gr->act);
     if (gr->dy_dtype != GDN_DTYPE_BF16 && gr->dy_dtype != GDN_DTYPE_FP32)
         return fail(GDN_ERR_INVALID_ARGUMENT, "dy_dtype %d unknown", gr->dy_dtype);
@@ -1379,7 +1386,8 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_by
             return fail(GDN_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input or another output");
     uint8_t* base = static_cast<uint8_t*>(ws);
     // without an activation a bf16 dy with rows of whole 16-byte runs is dp
-    const bool direct = gr->act == GDN_ACT_NONE && dp.dy_bf16 && aligned(gr->dy, 16) && dp.ldy % 8 == 0 && N % 8 == 0;
+    const bool direct = gr->act == GDN_ACT_NONE && dp.dy_bf16 && aligned(gr->dy, 16) && dp.ldy % 8 == 0 && N % 8 == 0 &&
+                        dp.ldy <= kMaxStride;
     const void* operand = direct ? gr->dy : base;
     const int64_t ldd = direct ? dp.ldy : w.ldd;
     if (!direct && (dx || dw) && M > 0 && N > 0) {

@@ -104,151 +104,189 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// up to four adjacent elements, element aligned only
-__device__ __forceinline__ void load4(const void* p, bool bf16, int64_t at, int nv, float* f) {
+// up to W adjacent elements, element aligned only
+template <int W>
+__device__ __forceinline__ void load_n(const void* p, bool bf16, int64_t at, int nv, float* f) {
     if (bf16) {
         const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-        if (nv == 4) {
-            const Half4 h = *reinterpret_cast<const Half4*>(q);
-            f[0] = __uint_as_float(h.lo << 16);
-            f[1] = __uint_as_float(h.lo & 0xFFFF0000u);
-            f[2] = __uint_as_float(h.hi << 16);
-            f[3] = __uint_as_float(h.hi & 0xFFFF0000u);
+        if (nv == W) {
+#pragma unroll
+            for (int g = 0; g < W / 4; ++g) {
+                const Half4 h = *reinterpret_cast<const Half4*>(q + 4 * g);
+                f[4 * g] = __uint_as_float(h.lo << 16);
+                f[4 * g + 1] = __uint_as_float(h.lo & 0xFFFF0000u);
+                f[4 * g + 2] = __uint_as_float(h.hi << 16);
+                f[4 * g + 3] = __uint_as_float(h.hi & 0xFFFF0000u);
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = e < nv ? bf16_bits_to_f32(q[e]) : 0.f;
+            for (int e = 0; e < W; ++e) f[e] = e < nv ? bf16_bits_to_f32(q[e]) : 0.f;
         }
     } else {
         const float* q = static_cast<const float*>(p) + at;
-        if (nv == 4) {
-            const Float4 h = *reinterpret_cast<const Float4*>(q);
+        if (nv == W) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = h.e[e];
+            for (int g = 0; g < W / 4; ++g) {
+                const Float4 h = *reinterpret_cast<const Float4*>(q + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[4 * g + e] = h.e[e];
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = e < nv ? q[e] : 0.f;
+            for (int e = 0; e < W; ++e) f[e] = e < nv ? q[e] : 0.f;
         }
     }
 }
 
-__device__ __forceinline__ void store4(void* p, bool bf16, int64_t at, int nv, const float* f) {
+template <int W>
+__device__ __forceinline__ void store_n(void* p, bool bf16, int64_t at, int nv, const float* f) {
     if (bf16) {
         uint16_t* q = static_cast<uint16_t*>(p) + at;
-        if (nv == 4) {
-            Half4 h;
-            h.lo = pack_bf16(f[0], f[1]);
-            h.hi = pack_bf16(f[2], f[3]);
-            *reinterpret_cast<Half4*>(q) = h;
+        if (nv == W) {
+            if constexpr (W == 8) {
+                struct __attribute__((packed, aligned(2))) Half8 { uint32_t e[4]; } h;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) h.e[g] = pack_bf16(f[2 * g], f[2 * g + 1]);
+                *reinterpret_cast<Half8*>(q) = h;
+            } else {
+                *reinterpret_cast<Half4*>(q) = Half4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < W; ++e)
                 if (e < nv) q[e] = f32_to_bf16_bits(f[e]);
         }
     } else {
         float* q = static_cast<float*>(p) + at;
-        if (nv == 4) {
-            Float4 h;
+        if (nv == W) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h.e[e] = f[e];
-            *reinterpret_cast<Float4*>(q) = h;
+            for (int g = 0; g < W / 4; ++g)
+                *reinterpret_cast<Float4*>(q + 4 * g) = Float4{{f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]}};
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < W; ++e)
                 if (e < nv) q[e] = f[e];
         }
     }
 }
 
-// y = act(sum + bias) + residual for up to four adjacent columns of one row;
+// y = act(sum + bias) + residual for up to W adjacent columns of one row;
 // preact receives sum + bias
-__device__ __forceinline__ void finish4(const GemmEpilogue& ep, int64_t m, int64_t n, int nv, float* f) {
+template <int W>
+__device__ __forceinline__ void finish_n(const GemmEpilogue& ep, int64_t m, int64_t n, int nv, float* f) {
     if (ep.bias) {
+        float c[W];
+        load_n<W>(ep.bias, false, n, nv, c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < nv) f[e] += ep.bias[n + e];
+        for (int e = 0; e < W; ++e) f[e] += c[e];
     }
-    if (ep.preact) store4(ep.preact, true, m * ep.ldp + n, nv, f);
-    if (ep.act != kActNone) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = activate(f[e], ep.act);
+    if (ep.preact) store_n<W>(ep.preact, true, m * ep.ldp + n, nv, f);
+    switch (ep.act) {                              // (uniform: one branch for all the values)
+#define GDN_ACT_CASE(ACT)                                        \
+    case ACT:                                                    \
+        _Pragma("unroll") for (int e = 0; e < W; ++e) f[e] = activate(f[e], ACT); \
+        break;
+        GDN_ACT_CASE(kActRelu)
+        GDN_ACT_CASE(kActGelu)
+        GDN_ACT_CASE(kActGeluTanh)
+        GDN_ACT_CASE(kActSilu)
+#undef GDN_ACT_CASE
+        default: break;
     }
     if (ep.residual) {
-        float r[4];
-        load4(ep.residual, ep.bf16, m * ep.ldr + n, nv, r);
+        float r[W];
+        load_n<W>(ep.residual, ep.bf16, m * ep.ldr + n, nv, r);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] += r[e];
+        for (int e = 0; e < W; ++e) f[e] += r[e];
     }
-    store4(ep.y, ep.bf16, m * ep.ldy + n, nv, f);
+    store_n<W>(ep.y, ep.bf16, m * ep.ldy + n, nv, f);
 }
 
-// ---- the tiled kernel ------------------------------------------------------------
-constexpr int kThreads = 512, kWaves = kThreads / kWave;
-constexpr int kTK = 64;                       // reduction per LDS stage
-constexpr int kWGM = 2, kWGN = 4;             // waves over the tile
+// ---- the tiled kernels -----------------------------------------------------------
+constexpr int kTK = 32;                       // reduction per LDS stage
+constexpr int kStages = 4;
 
 using LdsPtr = __attribute__((address_space(3))) void*;
 
-// One operand's tile of R output rows x 64 of the reduction, in an LDS stage
-// of R * 64 bf16 that is filled by global_load_lds (a wave's 64 lanes x 16
+// One operand's tile of R output rows x 32 of the reduction, in an LDS stage
+// of R * 32 bf16 that is filled by global_load_lds (a wave's 64 lanes x 16
 // bytes land in a row of 1 KiB; which 16 bytes a lane fetches is free, and
 // that is where the bank swizzle is done).
-//   KC (reduction contiguous): rows of 64 = eight 16-byte chunks, chunk c of
-//     row r at c ^ (r % 8); a fragment is one ds_read_b128.
-//   else (output rows contiguous): 64 rows of R, each as 32-byte pairs, pair
-//     q of reduction row k at q ^ f(k), f = k % 4 + 4 ((k / 8) % 4) (as many
-//     bits as there are pairs); a fragment is two ds_read_b64_tr_b16, whose
-//     16 lanes read four rows x 32 bytes and get a column each.
-template <bool KC, int R>
+//   KC (reduction contiguous): rows of 32 = four 16-byte chunks, chunk c of
+//     row r at c ^ f(r), f = bit 2 of r + 2 (bit 1 ^ bit 3): the chunks that
+//     8 or 16 adjacent lanes read lie in different banks.  A fragment is one
+//     ds_read_b128.
+//   else (output rows contiguous): 32 rows of R, each as 32-byte pairs, pair
+//     q of reduction row k at q ^ f(k), f = k % 4 + 4 (k / 8) (as many bits as
+//     there are pairs).  A fragment is two ds_read_b64_tr_b16, whose 16 lanes
+//     read four rows x 32 bytes and get a column each.
+// NW: waves of the work-group; WR: rows of a wave.
+template <bool KC, int R, int NW, int WR>
 struct Operand {
-    static constexpr int kLoads = R / 64;     // per wave and stage
+    static constexpr int kLoads = R * kTK * 2 / 1024 / NW;       // per wave and stage
     static constexpr int kPairs = R / 16;
-    const uint16_t* src[kLoads];
-    int k[kLoads];                            // this lane's first reduction index within a stage
-    int64_t step;
+    static_assert(kLoads >= 1, "a stage is at least one load of each wave");
+    // A lane's addresses: a wave-uniform one that moves along the reduction,
+    // plus 32-bit byte offsets (strides are of 22 bits).
+    const uint8_t* base;
+    int64_t step;                             // bytes per slice
+    uint32_t off[kLoads];
+    int k[kLoads];                            // first reduction index within a slice
+    // fragment addresses within a stage, elements
+    int at[KC ? 1 : WR / 16];
 
-    __device__ __forceinline__ static int pair_swizzle(int kr) { return ((kr & 3) | (((kr >> 3) & 3) << 2)) & (kPairs - 1); }
+    __device__ __forceinline__ static int chunk_swizzle(int r) { return ((r >> 2) & 1) | ((((r >> 1) ^ (r >> 3)) & 1) << 1); }
+    __device__ __forceinline__ static int pair_swizzle(int kr) { return ((kr & 3) | ((kr >> 3) << 2)) & (kPairs - 1); }
 
-    // rows: of the output; row0: the tile's first
-    __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int wave, int lane) {
-        step = KC ? kTK : kTK * ld;
+    // rows: of the output; row0: the tile's first; w: which of the tile's WR rows are this wave's
+    __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int wave, int lane, int w) {
+        const int l16 = lane % 16, lq = lane / 16;
+        step = 2 * (KC ? kTK : kTK * ld);
+        base = reinterpret_cast<const uint8_t*>(KC ? p + row0 * ld : p + row0);
+        const int left = rows - row0 < R ? static_cast<int>(rows - row0) : R;   // rows past the end: never stored
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-            const int j = wave + u * kWaves;
+            const int j = wave + u * NW;
             if constexpr (KC) {
-                const int r = 8 * j + lane / 8;
-                k[u] = 8 * ((lane & 7) ^ (lane / 8));
-                const int64_t g = row0 + r < rows ? row0 + r : rows - 1;   // rows past the end: never stored
-                src[u] = p + g * ld + k[u];
+                const int r = 16 * j + lane / 4;
+                k[u] = 8 * ((lane & 3) ^ chunk_swizzle(r));
+                off[u] = 2 * (static_cast<uint32_t>(r < left ? r : left - 1) * static_cast<uint32_t>(ld) + k[u]);
             } else {
                 constexpr int kChunks = R / 8;
                 k[u] = j * (kWave / kChunks) + lane / kChunks;
-                const int c = (lane % kChunks) ^ (pair_swizzle(k[u]) << 1);
-                const int64_t g = row0 + 8 * c < rows ? row0 + 8 * c : 0;   // (ld covers whole chunks)
-                src[u] = p + k[u] * ld + g;
+                const int c = 8 * ((lane % kChunks) ^ (pair_swizzle(k[u]) << 1));
+                off[u] = 2 * (static_cast<uint32_t>(k[u]) * static_cast<uint32_t>(ld) + (c < left ? c : 0));   // (ld covers whole chunks)
             }
+        }
+        if constexpr (KC) {
+            at[0] = (w * WR + l16) * kTK + 8 * (lq ^ chunk_swizzle(l16));
+        } else {
+            const int kr = 8 * lq + l16 / 4;
+#pragma unroll
+            for (int i = 0; i < WR / 16; ++i) at[i] = kr * R + 16 * ((w * (WR / 16) + i) ^ pair_swizzle(kr)) + 4 * (l16 % 4);
         }
     }
 
+    // the next slice into a stage; left: how much of the reduction there still
+    // is (FULL: a whole slice at least)
+    template <bool FULL>
     __device__ __forceinline__ void issue(uint16_t* lds, int wave, int64_t left) {
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-            const int j = wave + u * kWaves;
-            const uint16_t* s = left >= kTK || k[u] < left ? src[u] : zero_chunk;
-            __builtin_amdgcn_global_load_lds(s, (LdsPtr)(lds + j * 512), 16, 0, 0);
-            src[u] += step;
+            const void* s = FULL || k[u] < left ? static_cast<const void*>(base + off[u]) : zero_chunk;
+            __builtin_amdgcn_global_load_lds(s, (LdsPtr)(lds + (wave + u * NW) * 512), 16, 0, 0);
         }
+        base += step;
     }
 
-    // fragment of output rows r0 .. r0 + 15 (r0 a multiple of 16), reduction 32 ks ..
-    __device__ __forceinline__ static u32x4 frag(const uint16_t* lds, int r0, int ks, int l16, int lq) {
+    // fragment of the wave's output rows 16 i .. 16 i + 15
+    __device__ __forceinline__ u32x4 frag(const uint16_t* lds, int i) const {
         if constexpr (KC) {
-            return *reinterpret_cast<const u32x4*>(lds + (r0 + l16) * kTK + 8 * ((4 * ks + lq) ^ (l16 & 7)));
+            return *reinterpret_cast<const u32x4*>(lds + at[0] + 16 * i * kTK);
         } else {
-            const int kr = 32 * ks + 8 * lq + l16 / 4;
-            const uint16_t* at = lds + kr * R + 16 * ((r0 / 16) ^ pair_swizzle(kr)) + 4 * (l16 % 4);
             union { s16x4 h[2]; u32x4 v; } f;
-            f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
-            f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 4 * R));
+            f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at[i]));
+            f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at[i] + 4 * R));
             return f.v;
         }
     }
@@ -269,98 +307,262 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int* tm, int* tn)
     *tn = in / rows;
 }
 
-template <bool AK, bool BK, int BM, int BN>
-__device__ __forceinline__ void gemm_tile(const GemmProduct& p, int tile, uint16_t* As0, uint16_t* As1, uint16_t* Bs0,
-                                          uint16_t* Bs1) {
-    constexpr int WM = BM / kWGM, WN = BN / kWGN, TM = WM / 16, TN = WN / 16;
-    const int tid = threadIdx.x;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+// s_waitcnt vmcnt(N) lgkmcnt(0) (gfx9 encoding)
+template <int N>
+__device__ __forceinline__ void wait_vm_lds() {
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+}
+// s_waitcnt vmcnt(N)
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+template <bool V>
+struct Bool { static constexpr bool value = V; };
+
+__device__ __forceinline__ void wave_barrier() {   // (nothing is scheduled across it, matrix instructions included)
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A tile of BM x BN for NWM x NWN waves, each with WM x WN of it.
+template <int BM_, int BN_, int NWM_, int NWN_>
+struct Shape {
+    static constexpr int BM = BM_, BN = BN_, NWM = NWM_, NWN = NWN_;
+    static constexpr int kWaves = NWM * NWN, kThreads = kWaves * kWave;
+    static constexpr int WM = BM / NWM, WN = BN / NWN, TM = WM / 16, TN = WN / 16;
+    static constexpr int kA = BM * kTK, kB = BN * kTK;            // elements of a stage
+    // the epilogue's strips: a quarter of each wave's rows (16 at least), in 32 bits, four columns of padding
+    static constexpr int kStripTiles = TM / 4 > 0 ? TM / 4 : 1;
+    static constexpr int kStripLd = WN + 4, kStrip = 16 * kStripTiles * kStripLd;
+    static constexpr int kStageBytes = kStages * (kA + kB) * 2, kStripBytes = kWaves * kStrip * 4;
+    static constexpr int kBytes = kStageBytes > kStripBytes ? kStageBytes : kStripBytes;
+};
+
+// From the accumulators to the outputs.  The weights' fragment is the first
+// operand of a matrix instruction, so a lane holds row l16 and the four
+// adjacent columns 4 lq .. of each 16 x 16 tile; through LDS (each wave its
+// own strip), so that a row of the wave's columns is finished and stored as
+// one run, eight columns a lane.
+template <typename S>
+__device__ __forceinline__ void store_tile(const GemmProduct& p, f32x4 (&acc)[S::TM][S::TN], int64_t m0, int64_t n0, uint8_t* shared,
+                                           int wave, int lane, int wm, int wn) {
     const int l16 = lane % 16, lq = lane / 16;
-    const int wm = wave / kWGN, wn = wave % kWGN;
+    float* const strip = reinterpret_cast<float*>(shared) + wave * S::kStrip;
+    constexpr int kRun = S::WN / 8;           // lanes of a row
+    constexpr int kRowsAtOnce = kWave / kRun;
+    const int64_t n = n0 + wn * S::WN + 8 * (lane % kRun);
+    const int nv = p.N - n < 8 ? static_cast<int>(p.N - n) : 8;
+#pragma unroll
+    for (int part = 0; part < S::TM; part += S::kStripTiles) {
+#pragma unroll
+        for (int i = 0; i < S::kStripTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+                *reinterpret_cast<f32x4*>(strip + (16 * i + l16) * S::kStripLd + 16 * j + 4 * lq) = acc[part + i][j];
+        asm volatile("" ::: "memory");        // one wave: its LDS accesses stay in order
+#pragma unroll 1
+        for (int r = lane / kRun; r < 16 * S::kStripTiles; r += kRowsAtOnce) {
+            const int64_t m = m0 + wm * S::WM + 16 * part + r;
+            if (m < p.M && nv > 0) {
+                float f[8];
+                const f32x4* q = reinterpret_cast<const f32x4*>(strip + r * S::kStripLd + 8 * (lane % kRun));
+                const f32x4 q0 = q[0], q1 = q[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { f[e] = q0[e]; f[4 + e] = q1[e]; }
+                finish_n<8>(p.ep, m, n, nv, f);
+            }
+        }
+        asm volatile("" ::: "memory");
+    }
+}
+
+// Large tiles, 256 x 256 for 2 x 4 waves of 128 x 64: one work-group fills a
+// compute unit, with two waves on each SIMD.  A slice of 32 of the reduction
+// is two phases of 16 matrix instructions a wave (its upper and its lower 64
+// rows); before a phase the wave reads the fragments it needs, between two
+// barriers.  The lower four waves run half a phase behind the upper four, so
+// while one wave of a SIMD feeds the matrix core the other one reads and
+// requests.  Slice kt + 3 is requested in the second phase of slice kt, into
+// the stage of slice kt - 1, whose last fragments every wave had in registers
+// before the barrier that this phase began with.
+template <bool AK, bool BK, typename S>
+__device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8_t* shared) {
+    using OA = Operand<AK, S::BM, S::kWaves, S::WM>;
+    using OB = Operand<BK, S::BN, S::kWaves, S::WN>;
+    constexpr int TM = S::TM, TN = S::TN, H = TM / 2;
+    constexpr int kPer = OA::kLoads + OB::kLoads;
+    uint16_t* const as = reinterpret_cast<uint16_t*>(shared);
+    uint16_t* const bs = as + kStages * S::kA;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const int wm = wave / S::NWN, wn = wave % S::NWN;
     int tm, tn;
-    tile_of(tile, static_cast<int>((p.M + BM - 1) / BM), static_cast<int>((p.N + BN - 1) / BN), &tm, &tn);
-    const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
-
-    Operand<AK, BM> a;
-    Operand<BK, BN> b;
-    a.init(static_cast<const uint16_t*>(p.A), p.lda, m0, p.M, wave, lane);
-    b.init(static_cast<const uint16_t*>(p.B), p.ldb, n0, p.N, wave, lane);
-
+    tile_of(tile, static_cast<int>((p.M + S::BM - 1) / S::BM), static_cast<int>((p.N + S::BN - 1) / S::BN), &tm, &tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * S::BM, n0 = static_cast<int64_t>(tn) * S::BN;
+    OA a;
+    OB b;
+    a.init(static_cast<const uint16_t*>(p.A), p.lda, m0, p.M, wave, lane, wm);
+    b.init(static_cast<const uint16_t*>(p.B), p.ldb, n0, p.N, wave, lane, wn);
     f32x4 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // slice kt from one stage while slice kt + 1 arrives in the other
-    auto step = [&](int64_t k0, const uint16_t* as, const uint16_t* bs, uint16_t* an, uint16_t* bn) {
-        wait_vm_all();                        // this wave's loads of the slice
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();         // and everyone's; the other stage is free
-        asm volatile("" ::: "memory");
-        if (k0 + kTK < p.K) {
-            a.issue(an, wave, p.K - k0 - kTK);
-            b.issue(bn, wave, p.K - k0 - kTK);
-        }
+    // slices in whole rounds of the stages: those past the reduction's end read zeros
+    const int nk = static_cast<int>((p.K + kTK - 1) / kTK + kStages - 1) / kStages * kStages;
+    const int full = static_cast<int>(p.K / kTK);
+    auto round = [&](auto whole, int kt) {    // slices kt .. kt + 3 (kt a multiple of 4)
+        constexpr bool FULL = decltype(whole)::value;
 #pragma unroll
-        for (int ks = 0; ks < kTK / 32; ++ks) {
-            u32x4 fb[TN];
+        for (int st = 0; st < kStages; ++st) {
+            u32x4 fa[H], fb[TN];
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = Operand<BK, BN>::frag(bs, wn * WN + 16 * j, ks, l16, lq);
+            for (int j = 0; j < TN; ++j) fb[j] = b.frag(bs + st * S::kB, j);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const u32x4 fa = Operand<AK, BM>::frag(as, wm * WM + 16 * i, ks, l16, lq);
+            for (int i = 0; i < H; ++i) fa[i] = a.frag(as + st * S::kA, i);
+            wave_barrier();
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma(fb[j], fa, acc[i][j]);
-            }
+            for (int i = 0; i < H; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma(fb[j], fa[i], acc[i][j]);
+            __builtin_amdgcn_s_setprio(0);
+            wave_barrier();
+            constexpr int kAhead = kStages - 1;
+            const int64_t left = p.K - static_cast<int64_t>(kt + st + kAhead) * kTK;
+#pragma unroll
+            for (int i = 0; i < H; ++i) fa[i] = a.frag(as + st * S::kA, H + i);
+            a.template issue<FULL>(as + (st + kAhead) % kStages * S::kA, wave, left);
+            b.template issue<FULL>(bs + (st + kAhead) % kStages * S::kB, wave, left);
+            wait_vm<2 * kPer>();              // slice kt + 1 has landed
+            wave_barrier();
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[H + i][j] = mfma(fb[j], fa[i], acc[H + i][j]);
+            __builtin_amdgcn_s_setprio(0);
+            wave_barrier();
         }
     };
-    if (p.K > 0) {
-        a.issue(As0, wave, p.K);
-        b.issue(Bs0, wave, p.K);
-    }
-    for (int64_t k0 = 0; k0 < p.K; k0 += 2 * kTK) {
-        step(k0, As0, Bs0, As1, Bs1);
-        if (k0 + kTK < p.K) step(k0 + kTK, As1, Bs1, As0, Bs0);
-    }
-
-    // the weights' fragment is the first operand, so a lane holds row l16 and
-    // the four adjacent columns 4 lq .. of each 16 x 16 tile
+    if (nk > 0) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + wm * WM + 16 * i + l16;
-        if (m >= p.M) continue;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t n = n0 + wn * WN + 16 * j + 4 * lq;
-            if (n >= p.N) continue;
-            const int nv = p.N - n < 4 ? static_cast<int>(p.N - n) : 4;
-            float f[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            finish4(p.ep, m, n, nv, f);
+        for (int st = 0; st < kStages - 1; ++st) {
+            const int64_t left = p.K - st * kTK;
+            a.template issue<false>(as + st * S::kA, wave, left);
+            b.template issue<false>(bs + st * S::kB, wave, left);
         }
+        wait_vm<2 * kPer>();                  // slice 0
+        wave_barrier();
+        if (wm) wave_barrier();               // half a phase behind
+        int kt = 0;
+        for (; kt + 2 * kStages - 1 <= full; kt += kStages) round(Bool<true>{}, kt);
+        for (; kt < nk; kt += kStages) round(Bool<false>{}, kt);
+        if (!wm) wave_barrier();
+        wait_vm<0>();                         // the requests past the end
     }
+    wave_barrier();                           // the stages become the epilogue's strips
+    store_tile<S>(p, acc, m0, n0, shared, wave, lane, wm, wn);
 }
 
-template <int BM, int BN>
-struct Stages {
-    static constexpr int kA = BM * kTK, kB = BN * kTK;
-};
+// Small tiles, for 2 x 2 waves: several work-groups share a compute unit and
+// hide each other's latencies.  In iteration kt a wave multiplies slice kt
+// from registers, reads slice kt + 1's fragments from LDS into the other set
+// and requests slice kt + 4 into the stage that slice kt's fragments were
+// read from an iteration ago; one barrier an iteration.
+template <bool AK, bool BK, typename S>
+__device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8_t* shared) {
+    using OA = Operand<AK, S::BM, S::kWaves, S::WM>;
+    using OB = Operand<BK, S::BN, S::kWaves, S::WN>;
+    constexpr int TM = S::TM, TN = S::TN;
+    constexpr int kPer = OA::kLoads + OB::kLoads;
+    uint16_t* const as = reinterpret_cast<uint16_t*>(shared);
+    uint16_t* const bs = as + kStages * S::kA;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const int wm = wave / S::NWN, wn = wave % S::NWN;
+    int tm, tn;
+    tile_of(tile, static_cast<int>((p.M + S::BM - 1) / S::BM), static_cast<int>((p.N + S::BN - 1) / S::BN), &tm, &tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * S::BM, n0 = static_cast<int64_t>(tn) * S::BN;
+    OA a;
+    OB b;
+    a.init(static_cast<const uint16_t*>(p.A), p.lda, m0, p.M, wave, lane, wm);
+    b.init(static_cast<const uint16_t*>(p.B), p.ldb, n0, p.N, wave, lane, wn);
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int nk = static_cast<int>((p.K + kTK - 1) / kTK + kStages - 1) / kStages * kStages;
+    const int full = static_cast<int>(p.K / kTK);
+    u32x4 fa[2][TM], fb[2][TN];
+    auto fragments = [&](int stage, int set) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[set][j] = b.frag(bs + stage * S::kB, j);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[set][i] = a.frag(as + stage * S::kA, i);
+    };
+    auto round = [&](auto whole, int kt) {
+        constexpr bool FULL = decltype(whole)::value;
+#pragma unroll
+        for (int st = 0; st < kStages; ++st) {
+            const int64_t left = p.K - static_cast<int64_t>(kt + st + kStages) * kTK;
+            wait_vm_lds<2 * kPer>();          // slice kt + 1 has landed, slice kt's fragments are in registers
+            wave_barrier();
+            a.template issue<FULL>(as + st * S::kA, wave, left);
+            b.template issue<FULL>(bs + st * S::kB, wave, left);
+            fragments((st + 1) % kStages, (st + 1) % 2);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma(fb[st % 2][j], fa[st % 2][i], acc[i][j]);
+        }
+    };
+    if (nk > 0) {
+#pragma unroll
+        for (int st = 0; st < kStages; ++st) {
+            const int64_t left = p.K - st * kTK;
+            a.template issue<false>(as + st * S::kA, wave, left);
+            b.template issue<false>(bs + st * S::kB, wave, left);
+        }
+        wait_vm_lds<3 * kPer>();              // slice 0
+        wave_barrier();
+        fragments(0, 0);
+        int kt = 0;
+        for (; kt + 2 * kStages <= full; kt += kStages) round(Bool<true>{}, kt);
+        for (; kt < nk; kt += kStages) round(Bool<false>{}, kt);
+        wait_vm_lds<0>();                     // the requests past the end
+    }
+    wave_barrier();                           // the stages become the epilogue's strips
+    store_tile<S>(p, acc, m0, n0, shared, wave, lane, wm, wn);
+}
 
-template <int BM, int BN>
-__global__ __launch_bounds__(kThreads, 2) void linear_forward_kernel(GemmProduct p) {
-    __shared__ __align__(1024) uint16_t As0[BM * kTK], As1[BM * kTK];
-    __shared__ __align__(1024) uint16_t Bs0[BN * kTK], Bs1[BN * kTK];
-    gemm_tile<true, true, BM, BN>(p, blockIdx.x, As0, As1, Bs0, Bs1);
+using Large = Shape<256, 256, 2, 4>;
+using Medium = Shape<128, 128, 2, 2>;
+using Small = Shape<64, 64, 2, 2>;
+
+template <bool AK, bool BK, typename S>
+__device__ __forceinline__ void gemm_tile(const GemmProduct& p, int tile, uint8_t* shared) {
+    if constexpr (S::BM == 256) gemm_large<AK, BK, S>(p, tile, shared);
+    else gemm_small<AK, BK, S>(p, tile, shared);
+}
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, S::BM == 256 ? 2 : 1) void linear_forward_kernel(GemmProduct p) {
+    __shared__ __align__(1024) uint8_t shared[S::kBytes];
+    gemm_tile<true, true, S>(p, blockIdx.x, shared);
 }
 
 // dx (first `first` work-groups) and dw (the rest) in one launch: each alone
 // often has fewer tiles than the card has compute units.
-template <int BM, int BN>
-__global__ __launch_bounds__(kThreads, 2) void linear_backward_kernel(GemmProduct dx, GemmProduct dw, int first) {
-    __shared__ __align__(1024) uint16_t As0[BM * kTK], As1[BM * kTK];
-    __shared__ __align__(1024) uint16_t Bs0[BN * kTK], Bs1[BN * kTK];
-    if (static_cast<int>(blockIdx.x) < first) gemm_tile<true, false, BM, BN>(dx, blockIdx.x, As0, As1, Bs0, Bs1);
-    else gemm_tile<false, false, BM, BN>(dw, blockIdx.x - first, As0, As1, Bs0, Bs1);
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, S::BM == 256 ? 2 : 1) void linear_backward_kernel(GemmProduct dx, GemmProduct dw, int first) {
+    __shared__ __align__(1024) uint8_t shared[S::kBytes];
+    if (static_cast<int>(blockIdx.x) < first) gemm_tile<true, false, S>(dx, blockIdx.x, shared);
+    else gemm_tile<false, false, S>(dw, blockIdx.x - first, shared);
 }
 
 // ---- few rows --------------------------------------------------------------------
@@ -417,7 +619,7 @@ __global__ __launch_bounds__(NWV * kWave) void linear_few_kernel(GemmProduct p) 
         if (m >= p.M || n >= p.N) continue;
         const int nv = p.N - n < 4 ? static_cast<int>(p.N - n) : 4;
         float f[4] = {s[0], s[1], s[2], s[3]};
-        finish4(p.ep, m, n, nv, f);
+        finish_n<4>(p.ep, m, n, nv, f);
     }
 }
 
@@ -439,15 +641,15 @@ __global__ __launch_bounds__(256) void linear_dp_kernel(LinearDp p) {
         const int64_t m = m0 + i;
         if (m >= p.M) break;
         float d[4], q[4];
-        load4(p.dy, p.dy_bf16, m * p.ldy + n, nv, d);
+        load_n<4>(p.dy, p.dy_bf16, m * p.ldy + n, nv, d);
         if (p.act != kActNone) {
-            load4(p.preact, true, m * p.ldp + n, nv, q);
+            load_n<4>(p.preact, true, m * p.ldp + n, nv, q);
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[e] = e < nv ? d[e] * slope(q[e], p.act) : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] += d[e];
-        if (p.dp && n < p.ldd) store4(p.dp, true, m * p.ldd + n, 4, d);   // (columns past N: zeros)
+        if (p.dp && n < p.ldd) store_n<4>(p.dp, true, m * p.ldd + n, 4, d);   // (columns past N: zeros)
     }
     if (!p.part) return;
 #pragma unroll
@@ -478,19 +680,19 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void linear_sum_kernel(const
     }
 }
 
-template <int BM, int BN>
-int64_t tiles(const GemmProduct& p) { return ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN); }
+template <typename S>
+int64_t tiles(const GemmProduct& p) { return ((p.M + S::BM - 1) / S::BM) * ((p.N + S::BN - 1) / S::BN); }
 
-template <int BM, int BN>
+template <typename S>
 hipError_t forward_t(const GemmProduct& p, hipStream_t s) {
-    hipLaunchKernelGGL((linear_forward_kernel<BM, BN>), dim3(static_cast<unsigned>(tiles<BM, BN>(p))), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((linear_forward_kernel<S>), dim3(static_cast<unsigned>(tiles<S>(p))), dim3(S::kThreads), 0, s, p);
     return hipGetLastError();
 }
 
-template <int BM, int BN>
+template <typename S>
 hipError_t backward_t(const GemmProduct& dx, const GemmProduct& dw, hipStream_t s) {
-    const int64_t t1 = dx.ep.y ? tiles<BM, BN>(dx) : 0, t2 = dw.ep.y ? tiles<BM, BN>(dw) : 0;
-    hipLaunchKernelGGL((linear_backward_kernel<BM, BN>), dim3(static_cast<unsigned>(t1 + t2)), dim3(kThreads), 0, s, dx, dw,
+    const int64_t t1 = dx.ep.y ? tiles<S>(dx) : 0, t2 = dw.ep.y ? tiles<S>(dw) : 0;
+    hipLaunchKernelGGL((linear_backward_kernel<S>), dim3(static_cast<unsigned>(t1 + t2)), dim3(S::kThreads), 0, s, dx, dw,
                        static_cast<int>(t1));
     return hipGetLastError();
 }
@@ -510,9 +712,9 @@ hipError_t launch_linear(const GemmProduct& p, hipStream_t s) {
         }
         return hipGetLastError();
     }
-    if (tiles<256, 256>(p) >= cus) return forward_t<256, 256>(p, s);
-    if (tiles<128, 128>(p) >= cus) return forward_t<128, 128>(p, s);
-    return forward_t<64, 64>(p, s);
+    if (tiles<Large>(p) >= cus) return forward_t<Large>(p, s);
+    if (tiles<Medium>(p) >= cus) return forward_t<Medium>(p, s);
+    return forward_t<Small>(p, s);
 }
 
 int64_t linear_dp_blocks(int64_t M) { return (M + kDpRows - 1) / kDpRows; }
@@ -535,11 +737,11 @@ hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, con
     }
     if (!dx.ep.y && !dw.ep.y) return hipSuccess;
     const int cus = compute_units();
-    const int64_t big = (dx.ep.y ? tiles<256, 256>(dx) : 0) + (dw.ep.y ? tiles<256, 256>(dw) : 0);
-    const int64_t mid = (dx.ep.y ? tiles<128, 128>(dx) : 0) + (dw.ep.y ? tiles<128, 128>(dw) : 0);
-    if (big >= cus) return backward_t<256, 256>(dx, dw, s);
-    if (mid >= cus) return backward_t<128, 128>(dx, dw, s);
-    return backward_t<64, 64>(dx, dw, s);
+    const int64_t large = (dx.ep.y ? tiles<Large>(dx) : 0) + (dw.ep.y ? tiles<Large>(dw) : 0);
+    const int64_t medium = (dx.ep.y ? tiles<Medium>(dx) : 0) + (dw.ep.y ? tiles<Medium>(dw) : 0);
+    if (large >= cus) return backward_t<Large>(dx, dw, s);
+    if (medium >= cus) return backward_t<Medium>(dx, dw, s);
+    return backward_t<Small>(dx, dw, s);
 }
 
 }  // namespace gdn

@@ -616,7 +616,8 @@ gdn_status gdn_recur_decode(const gdn_recur* recur, const gdn_recur_io* io, void
 #define GDN_ACT_SILU 4             /* p sigmoid(p) */
 
 /* Row strides in elements, 0 means dense.  x, w: 16-byte aligned, K and
- * their strides multiples of 8; the others element aligned, M and N free.
+ * their strides multiples of 8 up to 2^22; the others element aligned, M and
+ * N free (N up to 2^22 in the backward pass).
  * residual may be y itself (same address and stride); otherwise the bytes
  * from the first to the last element of y and of preact must not overlap
  * those of another buffer. */
