@@ -57,8 +57,34 @@ __device__ __forceinline__ float half_erfc(float p, float* e) {
     return 0.5f * erfcx_poly(fabsf(p) * kSqrtHalf) * *e;
 }
 
+// The same, log2 of it as a polynomial of degree 7 in |p| (weighted least
+// squares on [0, 14]; relative error of the result below 5e-6 for |p| < 4,
+// 5e-4 where it is below 1e-5, and past the fit the leading term takes it to
+// 0): 15 vector operations a value instead of 24.  For outputs in bf16, whose
+// rounding is 2^-9; at 4096 x 12288 x 2048 gelu's share of the kernel's time
+// falls from 25 to 13 us of 190.
+__device__ __forceinline__ float half_erfc_bf16(float p) {
+    const float x = fabsf(p);
+    float q = -1.40202519e-06f;
+    q = fmaf(q, x, 5.41653571e-05f);
+    q = fmaf(q, x, -8.82210385e-04f);
+    q = fmaf(q, x, 8.35662335e-03f);
+    q = fmaf(q, x, -5.37223667e-02f);
+    q = fmaf(q, x, -4.58640128e-01f);
+    q = fmaf(q, x, -1.15120113e+00f);
+    q = fmaf(q, x, -9.99998331e-01f);
+    return __builtin_amdgcn_exp2f(q);
+}
+
+// gelu for an output in bf16 (chosen by the launchers; not part of the ABI)
+constexpr int kActGeluBf16 = 5;
+
 __device__ __forceinline__ float activate(float p, int act) {
     switch (act) {
+        case kActGeluBf16: {
+            const float c = half_erfc_bf16(p);
+            return p * (p > 0.f ? 1.f - c : c);
+        }
         case kActRelu: return p < 0.f ? 0.f : p;      // NaN stays NaN
         case kActGelu: {
             float e;
@@ -98,6 +124,7 @@ __device__ __forceinline__ float slope(float p, int act) {
 // ---- output elements -----------------------------------------------------------
 struct __attribute__((packed, aligned(2))) Half4 { uint32_t lo, hi; };
 struct __attribute__((packed, aligned(4))) Float4 { float e[4]; };
+typedef uint32_t Run8 __attribute__((ext_vector_type(4), aligned(2)));   // eight bf16, element aligned
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const f32x2 v = {a, b};
@@ -144,10 +171,9 @@ __device__ __forceinline__ void store_n(void* p, bool bf16, int64_t at, int nv, 
         uint16_t* q = static_cast<uint16_t*>(p) + at;
         if (nv == W) {
             if constexpr (W == 8) {
-                struct __attribute__((packed, aligned(2))) Half8 { uint32_t e[4]; } h;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) h.e[g] = pack_bf16(f[2 * g], f[2 * g + 1]);
-                *reinterpret_cast<Half8*>(q) = h;
+                // (non-temporal: the tiles' outputs and residuals pass the L2 by, which holds operands)
+                const Run8 h = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+                __builtin_nontemporal_store(h, reinterpret_cast<Run8*>(q));
             } else {
                 *reinterpret_cast<Half4*>(q) = Half4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
             }
@@ -170,6 +196,23 @@ __device__ __forceinline__ void store_n(void* p, bool bf16, int64_t at, int nv, 
     }
 }
 
+template <int W>
+__device__ __forceinline__ void activate_n(float* f, int act) {
+    switch (act) {                                // (uniform: one branch for all the values)
+#define GDN_ACT_CASE(ACT)                                                         \
+    case ACT:                                                                     \
+        _Pragma("unroll") for (int e = 0; e < W; ++e) f[e] = activate(f[e], ACT); \
+        break;
+        GDN_ACT_CASE(kActRelu)
+        GDN_ACT_CASE(kActGelu)
+        GDN_ACT_CASE(kActGeluBf16)
+        GDN_ACT_CASE(kActGeluTanh)
+        GDN_ACT_CASE(kActSilu)
+#undef GDN_ACT_CASE
+        default: break;
+    }
+}
+
 // y = act(sum + bias) + residual for up to W adjacent columns of one row;
 // preact receives sum + bias
 template <int W>
@@ -181,18 +224,7 @@ __device__ __forceinline__ void finish_n(const GemmEpilogue& ep, int64_t m, int6
         for (int e = 0; e < W; ++e) f[e] += c[e];
     }
     if (ep.preact) store_n<W>(ep.preact, true, m * ep.ldp + n, nv, f);
-    switch (ep.act) {                              // (uniform: one branch for all the values)
-#define GDN_ACT_CASE(ACT)                                        \
-    case ACT:                                                    \
-        _Pragma("unroll") for (int e = 0; e < W; ++e) f[e] = activate(f[e], ACT); \
-        break;
-        GDN_ACT_CASE(kActRelu)
-        GDN_ACT_CASE(kActGelu)
-        GDN_ACT_CASE(kActGeluTanh)
-        GDN_ACT_CASE(kActSilu)
-#undef GDN_ACT_CASE
-        default: break;
-    }
+    activate_n<W>(f, ep.act);
     if (ep.residual) {
         float r[W];
         load_n<W>(ep.residual, ep.bf16, m * ep.ldr + n, nv, r);
@@ -204,7 +236,6 @@ __device__ __forceinline__ void finish_n(const GemmEpilogue& ep, int64_t m, int6
 
 // ---- the tiled kernels -----------------------------------------------------------
 constexpr int kTK = 32;                       // reduction per LDS stage
-constexpr int kStages = 4;
 
 using LdsPtr = __attribute__((address_space(3))) void*;
 
@@ -330,14 +361,15 @@ __device__ __forceinline__ void wave_barrier() {   // (nothing is scheduled acro
 }
 
 // A tile of BM x BN for NWM x NWN waves, each with WM x WN of it.
-template <int BM_, int BN_, int NWM_, int NWN_>
+// PER_SIMD: waves that share a SIMD when the compute unit is full.
+template <int BM_, int BN_, int NWM_, int NWN_, int STAGES, int PER_SIMD>
 struct Shape {
-    static constexpr int BM = BM_, BN = BN_, NWM = NWM_, NWN = NWN_;
+    static constexpr int BM = BM_, BN = BN_, NWM = NWM_, NWN = NWN_, kStages = STAGES, kPerSimd = PER_SIMD;
     static constexpr int kWaves = NWM * NWN, kThreads = kWaves * kWave;
     static constexpr int WM = BM / NWM, WN = BN / NWN, TM = WM / 16, TN = WN / 16;
     static constexpr int kA = BM * kTK, kB = BN * kTK;            // elements of a stage
-    // the epilogue's strips: a quarter of each wave's rows (16 at least), in 32 bits, four columns of padding
-    static constexpr int kStripTiles = TM / 4 > 0 ? TM / 4 : 1;
+    // the epilogue's strips: half of each wave's rows, in 32 bits, four columns of padding
+    static constexpr int kStripTiles = TM / 2;
     static constexpr int kStripLd = WN + 4, kStrip = 16 * kStripTiles * kStripLd;
     static constexpr int kStageBytes = kStages * (kA + kB) * 2, kStripBytes = kWaves * kStrip * 4;
     static constexpr int kBytes = kStageBytes > kStripBytes ? kStageBytes : kStripBytes;
@@ -346,40 +378,108 @@ struct Shape {
 // From the accumulators to the outputs.  The weights' fragment is the first
 // operand of a matrix instruction, so a lane holds row l16 and the four
 // adjacent columns 4 lq .. of each 16 x 16 tile; through LDS (each wave its
-// own strip), so that a row of the wave's columns is finished and stored as
-// one run, eight columns a lane.
-template <typename S>
-__device__ __forceinline__ void store_tile(const GemmProduct& p, f32x4 (&acc)[S::TM][S::TN], int64_t m0, int64_t n0, uint8_t* shared,
-                                           int wave, int lane, int wm, int wn) {
-    const int l16 = lane % 16, lq = lane / 16;
-    float* const strip = reinterpret_cast<float*>(shared) + wave * S::kStrip;
-    constexpr int kRun = S::WN / 8;           // lanes of a row
-    constexpr int kRowsAtOnce = kWave / kRun;
-    const int64_t n = n0 + wn * S::WN + 8 * (lane % kRun);
-    const int nv = p.N - n < 8 ? static_cast<int>(p.N - n) : 8;
-#pragma unroll
-    for (int part = 0; part < S::TM; part += S::kStripTiles) {
-#pragma unroll
-        for (int i = 0; i < S::kStripTiles; ++i)
-#pragma unroll
-            for (int j = 0; j < S::TN; ++j)
-                *reinterpret_cast<f32x4*>(strip + (16 * i + l16) * S::kStripLd + 16 * j + 4 * lq) = acc[part + i][j];
-        asm volatile("" ::: "memory");        // one wave: its LDS accesses stay in order
-#pragma unroll 1
-        for (int r = lane / kRun; r < 16 * S::kStripTiles; r += kRowsAtOnce) {
-            const int64_t m = m0 + wm * S::WM + 16 * part + r;
-            if (m < p.M && nv > 0) {
-                float f[8];
-                const f32x4* q = reinterpret_cast<const f32x4*>(strip + r * S::kStripLd + 8 * (lane % kRun));
-                const f32x4 q0 = q[0], q1 = q[1];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) { f[e] = q0[e]; f[4 + e] = q1[e]; }
-                finish_n<8>(p.ep, m, n, nv, f);
-            }
-        }
-        asm volatile("" ::: "memory");
+// own strip, half of its rows at a time), so that a row of the wave's columns
+// is finished and stored as one run, eight columns a lane.  The residual's
+// rows of the first half are requested before the last slices are multiplied,
+// those of the second half before the first one is finished.
+// PLAIN: nothing but y.
+template <typename S, bool PLAIN>
+struct Store {
+    static constexpr int kRun = S::WN / 8;    // lanes of a row
+    static constexpr int kRowsAtOnce = kWave / kRun;
+    static constexpr int kRows = 16 * S::kStripTiles, kMine = kRows / kRowsAtOnce;   // rows of a half; of a lane
+    static constexpr int kBatch = kMine < 4 ? kMine : 4;
+    int64_t m0, n;                            // the wave's first row, the lane's first column
+    int first, nv;                            // the lane's first row of a half; its columns
+    bool early;                               // the residual can be fetched as bf16 runs
+    Run8 res[kMine];
+
+    __device__ __forceinline__ void init(const GemmProduct& p, int64_t m, int64_t n0, int lane) {
+        m0 = m;
+        first = lane / kRun;
+        n = n0 + 8 * (lane % kRun);
+        nv = p.N - n < 8 ? (p.N > n ? static_cast<int>(p.N - n) : 0) : 8;
+        early = !PLAIN && p.ep.residual && p.ep.bf16 && nv == 8;
     }
-}
+
+    __device__ __forceinline__ void fetch(const GemmProduct& p, int half) {
+        if (PLAIN || !early) return;
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const int64_t m = m0 + half * kRows + first + u * kRowsAtOnce;
+            if (m < p.M) 
+                res[u] = __builtin_nontemporal_load(
+                    reinterpret_cast<const Run8*>(static_cast<const uint16_t*>(p.ep.residual) + m * p.ep.ldr + n));
+        }
+    }
+
+    __device__ __forceinline__ void run(const GemmProduct& p, f32x4 (&acc)[S::TM][S::TN], float* strip, int lane) {
+        const int l16 = lane % 16, lq = lane / 16;
+        float bias[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bias[e] = 0.f;
+        if (!PLAIN && p.ep.bias && nv > 0) load_n<8>(p.ep.bias, false, n, nv, bias);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < S::kStripTiles; ++i)
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+                    *reinterpret_cast<f32x4*>(strip + (16 * i + l16) * S::kStripLd + 16 * j + 4 * lq) =
+                        acc[half * S::kStripTiles + i][j];
+            asm volatile("" ::: "memory");    // one wave: its LDS accesses stay in order
+#pragma unroll
+            for (int u0 = 0; u0 < kMine; u0 += kBatch) {
+                float f[kBatch][8];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const f32x4* q = reinterpret_cast<const f32x4*>(strip + (first + (u0 + u) * kRowsAtOnce) * S::kStripLd +
+                                                                    8 * (lane % kRun));
+                    const f32x4 q0 = q[0], q1 = q[1];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { f[u][e] = q0[e] + bias[e]; f[u][4 + e] = q1[e] + bias[4 + e]; }
+                }
+                const int64_t mb = m0 + half * kRows + first + u0 * kRowsAtOnce;
+                if (!PLAIN && p.ep.preact) {
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int64_t m = mb + u * kRowsAtOnce;
+                        if (m < p.M && nv > 0) store_n<8>(p.ep.preact, true, m * p.ep.ldp + n, nv, f[u]);
+                    }
+                }
+                if (!PLAIN) activate_n<8 * kBatch>(&f[0][0], p.ep.act);
+                if (PLAIN) {
+                } else if (early) {
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f[u][2 * e] += __uint_as_float(res[u0 + u][e] << 16);
+                            f[u][2 * e + 1] += __uint_as_float(res[u0 + u][e] & 0xFFFF0000u);
+                        }
+                } else if (p.ep.residual) {
+                    float r[kBatch][8];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int64_t m = mb + u * kRowsAtOnce;
+                        if (m < p.M && nv > 0) load_n<8>(p.ep.residual, p.ep.bf16, m * p.ep.ldr + n, nv, r[u]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[u][e] += r[u][e];
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int64_t m = mb + u * kRowsAtOnce;
+                    if (m < p.M && nv > 0) store_n<8>(p.ep.y, p.ep.bf16, m * p.ep.ldy + n, nv, f[u]);
+                }
+            }
+            if (half == 0) fetch(p, 1);
+            asm volatile("" ::: "memory");
+        }
+    }
+};
 
 // Large tiles, 256 x 256 for 2 x 4 waves of 128 x 64: one work-group fills a
 // compute unit, with two waves on each SIMD.  A slice of 32 of the reduction
@@ -390,12 +490,12 @@ __device__ __forceinline__ void store_tile(const GemmProduct& p, f32x4 (&acc)[S:
 // requests.  Slice kt + 3 is requested in the second phase of slice kt, into
 // the stage of slice kt - 1, whose last fragments every wave had in registers
 // before the barrier that this phase began with.
-template <bool AK, bool BK, typename S>
+template <bool AK, bool BK, bool PLAIN, typename S>
 __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8_t* shared) {
     using OA = Operand<AK, S::BM, S::kWaves, S::WM>;
     using OB = Operand<BK, S::BN, S::kWaves, S::WN>;
     constexpr int TM = S::TM, TN = S::TN, H = TM / 2;
-    constexpr int kPer = OA::kLoads + OB::kLoads;
+    constexpr int kPer = OA::kLoads + OB::kLoads, kStages = S::kStages;
     uint16_t* const as = reinterpret_cast<uint16_t*>(shared);
     uint16_t* const bs = as + kStages * S::kA;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -415,6 +515,8 @@ __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8
     // slices in whole rounds of the stages: those past the reduction's end read zeros
     const int nk = static_cast<int>((p.K + kTK - 1) / kTK + kStages - 1) / kStages * kStages;
     const int full = static_cast<int>(p.K / kTK);
+    Store<S, PLAIN> out;
+    out.init(p, m0 + wm * S::WM, n0 + wn * S::WN, lane);
     auto round = [&](auto whole, int kt) {    // slices kt .. kt + 3 (kt a multiple of 4)
         constexpr bool FULL = decltype(whole)::value;
 #pragma unroll
@@ -438,7 +540,7 @@ __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8
             for (int i = 0; i < H; ++i) fa[i] = a.frag(as + st * S::kA, H + i);
             a.template issue<FULL>(as + (st + kAhead) % kStages * S::kA, wave, left);
             b.template issue<FULL>(bs + (st + kAhead) % kStages * S::kB, wave, left);
-            wait_vm<2 * kPer>();              // slice kt + 1 has landed
+            wait_vm<(kStages - 2) * kPer>();  // slice kt + 1 has landed
             wave_barrier();
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -456,17 +558,19 @@ __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8
             a.template issue<false>(as + st * S::kA, wave, left);
             b.template issue<false>(bs + st * S::kB, wave, left);
         }
-        wait_vm<2 * kPer>();                  // slice 0
+        wait_vm<(kStages - 2) * kPer>();      // slice 0
         wave_barrier();
-        if (wm) wave_barrier();               // half a phase behind
+        if (wave >= S::kWaves / 2) wave_barrier();   // half a phase behind
         int kt = 0;
         for (; kt + 2 * kStages - 1 <= full; kt += kStages) round(Bool<true>{}, kt);
+        out.fetch(p, 0);
         for (; kt < nk; kt += kStages) round(Bool<false>{}, kt);
-        if (!wm) wave_barrier();
+        if (wave < S::kWaves / 2) wave_barrier();
         wait_vm<0>();                         // the requests past the end
     }
     wave_barrier();                           // the stages become the epilogue's strips
-    store_tile<S>(p, acc, m0, n0, shared, wave, lane, wm, wn);
+    if (nk == 0) out.fetch(p, 0);
+    out.run(p, acc, reinterpret_cast<float*>(shared) + wave * S::kStrip, lane);
 }
 
 // Small tiles, for 2 x 2 waves: several work-groups share a compute unit and
@@ -474,12 +578,12 @@ __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8
 // from registers, reads slice kt + 1's fragments from LDS into the other set
 // and requests slice kt + 4 into the stage that slice kt's fragments were
 // read from an iteration ago; one barrier an iteration.
-template <bool AK, bool BK, typename S>
+template <bool AK, bool BK, bool PLAIN, typename S>
 __device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8_t* shared) {
     using OA = Operand<AK, S::BM, S::kWaves, S::WM>;
     using OB = Operand<BK, S::BN, S::kWaves, S::WN>;
     constexpr int TM = S::TM, TN = S::TN;
-    constexpr int kPer = OA::kLoads + OB::kLoads;
+    constexpr int kPer = OA::kLoads + OB::kLoads, kStages = S::kStages;
     uint16_t* const as = reinterpret_cast<uint16_t*>(shared);
     uint16_t* const bs = as + kStages * S::kA;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -498,6 +602,8 @@ __device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int nk = static_cast<int>((p.K + kTK - 1) / kTK + kStages - 1) / kStages * kStages;
     const int full = static_cast<int>(p.K / kTK);
+    Store<S, PLAIN> out;
+    out.init(p, m0 + wm * S::WM, n0 + wn * S::WN, lane);
     u32x4 fa[2][TM], fb[2][TN];
     auto fragments = [&](int stage, int set) {
 #pragma unroll
@@ -533,36 +639,39 @@ __device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8
         fragments(0, 0);
         int kt = 0;
         for (; kt + 2 * kStages <= full; kt += kStages) round(Bool<true>{}, kt);
+        out.fetch(p, 0);
         for (; kt < nk; kt += kStages) round(Bool<false>{}, kt);
         wait_vm_lds<0>();                     // the requests past the end
     }
     wave_barrier();                           // the stages become the epilogue's strips
-    store_tile<S>(p, acc, m0, n0, shared, wave, lane, wm, wn);
+    if (nk == 0) out.fetch(p, 0);
+    out.run(p, acc, reinterpret_cast<float*>(shared) + wave * S::kStrip, lane);
 }
 
-using Large = Shape<256, 256, 2, 4>;
-using Medium = Shape<128, 128, 2, 2>;
-using Small = Shape<64, 64, 2, 2>;
+using Large = Shape<256, 256, 2, 4, 4, 2>;
+using Wide = Shape<256, 128, 4, 2, 4, 2>;
+using Medium = Shape<128, 128, 2, 2, 4, 2>;
+using Small = Shape<64, 64, 2, 2, 4, 2>;
 
-template <bool AK, bool BK, typename S>
+template <bool AK, bool BK, bool PLAIN, typename S>
 __device__ __forceinline__ void gemm_tile(const GemmProduct& p, int tile, uint8_t* shared) {
-    if constexpr (S::BM == 256) gemm_large<AK, BK, S>(p, tile, shared);
-    else gemm_small<AK, BK, S>(p, tile, shared);
+    if constexpr (S::BM == 256) gemm_large<AK, BK, PLAIN, S>(p, tile, shared);
+    else gemm_small<AK, BK, PLAIN, S>(p, tile, shared);
 }
 
 template <typename S>
-__global__ __launch_bounds__(S::kThreads, S::BM == 256 ? 2 : 1) void linear_forward_kernel(GemmProduct p) {
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void linear_forward_kernel(GemmProduct p) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
-    gemm_tile<true, true, S>(p, blockIdx.x, shared);
+    gemm_tile<true, true, false, S>(p, blockIdx.x, shared);
 }
 
 // dx (first `first` work-groups) and dw (the rest) in one launch: each alone
 // often has fewer tiles than the card has compute units.
 template <typename S>
-__global__ __launch_bounds__(S::kThreads, S::BM == 256 ? 2 : 1) void linear_backward_kernel(GemmProduct dx, GemmProduct dw, int first) {
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void linear_backward_kernel(GemmProduct dx, GemmProduct dw, int first) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
-    if (static_cast<int>(blockIdx.x) < first) gemm_tile<true, false, S>(dx, blockIdx.x, shared);
-    else gemm_tile<false, false, S>(dw, blockIdx.x - first, shared);
+    if (static_cast<int>(blockIdx.x) < first) gemm_tile<true, false, true, S>(dx, blockIdx.x, shared);
+    else gemm_tile<false, false, true, S>(dw, blockIdx.x - first, shared);
 }
 
 // ---- few rows --------------------------------------------------------------------
@@ -624,41 +733,69 @@ __global__ __launch_bounds__(NWV * kWave) void linear_few_kernel(GemmProduct p) 
 }
 
 // ---- dp = dy act'(p) and its column sums -------------------------------------------
-// A work-group covers 64 rows x 256 columns: lane l of 64 takes four columns
-// of every fourth row; dp is rounded to bf16 (the products' operand type), the
+// Bound: HBM (dy and p in, dp out).  A work-group covers 64 rows x 256
+// columns: 32 lanes of eight columns, every eighth row, four rows' loads in
+// flight together; dp is rounded to bf16 (the products' operand type), the
 // sums are of the values before that.
-constexpr int kDpRows = 64, kDpCols = 256;
+constexpr int kDpRows = 64, kDpCols = 256, kDpBatch = 4;
 
 __global__ __launch_bounds__(256) void linear_dp_kernel(LinearDp p) {
-    __shared__ float sums[4][kDpCols];
-    const int lane = threadIdx.x % 64, g = threadIdx.x / 64;
+    __shared__ float sums[8][kDpCols];
+    const int lane = threadIdx.x % 32, g = threadIdx.x / 32;
     const int64_t block = blockIdx.x / p.cols, col0 = static_cast<int64_t>(blockIdx.x % p.cols) * kDpCols;
-    const int64_t m0 = block * kDpRows, n = col0 + 4 * lane;
+    const int64_t m0 = block * kDpRows, n = col0 + 8 * lane;
     const int64_t left = p.N - n;
-    const int nv = left < 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = g; i < kDpRows; i += 4) {
-        const int64_t m = m0 + i;
-        if (m >= p.M) break;
-        float d[4], q[4];
-        load_n<4>(p.dy, p.dy_bf16, m * p.ldy + n, nv, d);
-        if (p.act != kActNone) {
-            load_n<4>(p.preact, true, m * p.ldp + n, nv, q);
+    const int nv = left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
+    float s[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = e < nv ? d[e] * slope(q[e], p.act) : 0.f;
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+#pragma unroll
+    for (int i0 = 0; i0 < kDpRows / 8; i0 += kDpBatch) {
+        float d[kDpBatch][8], q[kDpBatch][8];
+#pragma unroll
+        for (int u = 0; u < kDpBatch; ++u) {
+            const int64_t m = m0 + g + 8 * (i0 + u);
+            load_n<8>(p.dy, p.dy_bf16, m * p.ldy + n, m < p.M ? nv : 0, d[u]);
+        }
+        if (p.act != kActNone) {
+#pragma unroll
+            for (int u = 0; u < kDpBatch; ++u) {
+                const int64_t m = m0 + g + 8 * (i0 + u);
+                load_n<8>(p.preact, true, m * p.ldp + n, m < p.M ? nv : 0, q[u]);
+            }
+            switch (p.act) {
+#define GDN_SLOPE_CASE(ACT)                                                               \
+    case ACT:                                                                             \
+        _Pragma("unroll") for (int u = 0; u < kDpBatch; ++u)                              \
+            _Pragma("unroll") for (int e = 0; e < 8; ++e) d[u][e] *= slope(q[u][e], ACT); \
+        break;
+                GDN_SLOPE_CASE(kActRelu)
+                GDN_SLOPE_CASE(kActGelu)
+                GDN_SLOPE_CASE(kActGeluTanh)
+                GDN_SLOPE_CASE(kActSilu)
+#undef GDN_SLOPE_CASE
+                default: break;
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += d[e];
-        if (p.dp && n < p.ldd) store_n<4>(p.dp, true, m * p.ldd + n, 4, d);   // (columns past N: zeros)
+        for (int u = 0; u < kDpBatch; ++u) {
+            const int64_t m = m0 + g + 8 * (i0 + u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += d[u][e];              // (rows and columns past the end: zeros)
+            if (p.dp && m < p.M && n < p.ldd) store_n<8>(p.dp, true, m * p.ldd + n, 8, d[u]);
+        }
     }
     if (!p.part) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sums[g][4 * lane + e] = s[e];
+    for (int e = 0; e < 8; ++e) sums[g][8 * lane + e] = s[e];
     __syncthreads();
     const int64_t c = col0 + threadIdx.x;
-    if (c < p.N)
-        p.part[block * p.N + c] =
-            (sums[0][threadIdx.x] + sums[1][threadIdx.x]) + (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
+    if (c < p.N) {
+        float t = sums[0][threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) t += sums[k][threadIdx.x];
+        p.part[block * p.N + c] = t;
+    }
 }
 
 constexpr int kSumCols = 64, kSumSlices = 16;
@@ -699,9 +836,58 @@ hipError_t backward_t(const GemmProduct& dx, const GemmProduct& dw, hipStream_t 
 
 }  // namespace
 
-hipError_t launch_linear(const GemmProduct& p, hipStream_t s) {
-    if (p.M <= 0 || p.N <= 0) return hipSuccess;
-    const int cus = compute_units();
+// Which tiles: the time of one tile on a compute unit at K = 2048, in us
+// (measured at 4096 x 4096 for 256 x 256, 4096 x 2048 for 256 x 128, 2048 x
+// 2048 for 128 x 128 and 64 x 64), times the rounds of tiles over the compute
+// units.  At 4096 x 2048 x 4096: 81 us in tiles of 256 x 256, 68 in 256 x
+// 128, 80 in 128 x 128, 126 in 64 x 64; at 2048 x 2048 x 2048: 44, 31, 25, 33;
+// at 1024 x 2048 x 2048: 42, 29, 23, 17; at 1024 x 12352 x 2048: 54, 68, 75, 96.
+enum Tiles { kLarge, kWide, kMedium, kSmall };
+
+struct Choice {
+    Tiles tiles;
+    double us;
+};
+
+static Choice choose(const GemmProduct* a, const GemmProduct* b, int cus) {
+    auto us = [&](int64_t n, double each) { return static_cast<double>((n + cus - 1) / cus) * each; };
+    auto count = [&](auto f) { return (a ? f(*a) : 0) + (b ? f(*b) : 0); };
+    const Choice all[4] = {{kLarge, us(count([](const GemmProduct& p) { return tiles<Large>(p); }), 47.0)},
+                           {kWide, us(count([](const GemmProduct& p) { return tiles<Wide>(p); }), 30.0)},
+                           {kMedium, us(count([](const GemmProduct& p) { return tiles<Medium>(p); }), 21.0)},
+                           {kSmall, us(count([](const GemmProduct& p) { return tiles<Small>(p); }), 8.5)}};
+    Choice best = all[0];
+    for (int i = 1; i < 4; ++i)
+        if (all[i].us < best.us) best = all[i];
+    return best;
+}
+
+static hipError_t forward(const GemmProduct& p, Tiles t, hipStream_t s) {
+    switch (t) {
+        case kLarge: return forward_t<Large>(p, s);
+        case kWide: return forward_t<Wide>(p, s);
+        case kMedium: return forward_t<Medium>(p, s);
+        default: return forward_t<Small>(p, s);
+    }
+}
+
+// Columns n0 .. n0 + n - 1 of a product
+static GemmProduct columns(const GemmProduct& p, int64_t n0, int64_t n) {
+    GemmProduct c = p;
+    const size_t es = p.ep.bf16 ? 2 : 4;
+    c.N = n;
+    c.B = static_cast<const uint16_t*>(p.B) + n0 * p.ldb;
+    if (c.ep.bias) c.ep.bias += n0;
+    if (c.ep.preact) c.ep.preact += n0;
+    if (c.ep.residual) c.ep.residual = static_cast<const uint8_t*>(p.ep.residual) + n0 * es;
+    c.ep.y = static_cast<uint8_t*>(p.ep.y) + n0 * es;
+    return c;
+}
+
+hipError_t launch_linear(const GemmProduct& given, hipStream_t s) {
+    if (given.M <= 0 || given.N <= 0) return hipSuccess;
+    GemmProduct p = given;
+    if (p.ep.act == kActGelu && p.ep.bf16) p.ep.act = kActGeluBf16;
     if (p.M <= kFewRows) {
         const dim3 grid(static_cast<unsigned>((p.N + 15) / 16));
         switch ((p.M + 15) / 16) {
@@ -712,9 +898,22 @@ hipError_t launch_linear(const GemmProduct& p, hipStream_t s) {
         }
         return hipGetLastError();
     }
-    if (tiles<Large>(p) >= cus) return forward_t<Large>(p, s);
-    if (tiles<Medium>(p) >= cus) return forward_t<Medium>(p, s);
-    return forward_t<Small>(p, s);
+    // A last column of tiles that is nearly empty can cost a whole round of
+    // them (12352 = 48 x 256 + 64 columns at 4096 rows: 784 tiles, four rounds
+    // instead of three): then the rest goes by itself in smaller tiles.  A
+    // column's sum runs in the same order either way.
+    const int cus = compute_units();
+    const Choice whole = choose(&p, nullptr, cus);
+    const int64_t rest = p.N % 256, main = p.N - rest;
+    if (rest > 0 && main > 0) {
+        const GemmProduct m = columns(p, 0, main), r = columns(p, main, rest);
+        const Choice cm = choose(&m, nullptr, cus), cr = choose(&r, nullptr, cus);
+        if (cm.us + cr.us + 3.0 < whole.us) {     // 3: the second launch
+            const hipError_t e = forward(m, cm.tiles, s);
+            return e != hipSuccess ? e : forward(r, cr.tiles, s);
+        }
+    }
+    return forward(p, whole.tiles, s);
 }
 
 int64_t linear_dp_blocks(int64_t M) { return (M + kDpRows - 1) / kDpRows; }
@@ -736,12 +935,12 @@ hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, con
         if (e != hipSuccess) return e;
     }
     if (!dx.ep.y && !dw.ep.y) return hipSuccess;
-    const int cus = compute_units();
-    const int64_t large = (dx.ep.y ? tiles<Large>(dx) : 0) + (dw.ep.y ? tiles<Large>(dw) : 0);
-    const int64_t medium = (dx.ep.y ? tiles<Medium>(dx) : 0) + (dw.ep.y ? tiles<Medium>(dw) : 0);
-    if (large >= cus) return backward_t<Large>(dx, dw, s);
-    if (medium >= cus) return backward_t<Medium>(dx, dw, s);
-    return backward_t<Small>(dx, dw, s);
+    switch (choose(dx.ep.y ? &dx : nullptr, dw.ep.y ? &dw : nullptr, compute_units()).tiles) {
+        case kLarge: return backward_t<Large>(dx, dw, s);
+        case kWide: return backward_t<Wide>(dx, dw, s);
+        case kMedium: return backward_t<Medium>(dx, dw, s);
+        default: return backward_t<Small>(dx, dw, s);
+    }
 }
 
 }  // namespace gdn
