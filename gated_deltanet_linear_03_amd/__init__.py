@@ -50,7 +50,7 @@ EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_prefill_window_slots", "gdn_decode_workspace_bytes", "gdn_gemm_bf16_path",
            "gdn_recur_saved_bytes", "gdn_recur_workspace_bytes", "gdn_recur_forward",
            "gdn_recur_backward_workspace_bytes", "gdn_recur_backward", "gdn_recur_decode",
-           "gdn_linear", "gdn_linear_backward_workspace_bytes", "gdn_linear_backward")
+           "gdn_linear", "gdn_linear_workspace_bytes", "gdn_linear_backward_workspace_bytes", "gdn_linear_backward")
 NOALLOC_SCRATCH_BYTES = 128 << 20       # GDN_NOALLOC_SCRATCH_BYTES
 SNAPSHOT_MAGIC = 0x50534E47
 SNAPSHOT_VERSION = 1
@@ -283,7 +283,9 @@ def lib():
         L.gdn_recur_decode.argtypes = [ctypes.POINTER(CRecur), ctypes.POINTER(CRecurIO),
                                        ctypes.c_void_p]
         L.gdn_linear.restype = ctypes.c_int
-        L.gdn_linear.argtypes = [ctypes.POINTER(CLinearIO), ctypes.c_void_p]
+        L.gdn_linear.argtypes = [ctypes.POINTER(CLinearIO), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        L.gdn_linear_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_linear_workspace_bytes.argtypes = [ctypes.c_int64] * 3
         L.gdn_linear_backward_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_linear_backward_workspace_bytes.argtypes = [ctypes.c_int64] * 3
         L.gdn_linear_backward.restype = ctypes.c_int
@@ -1100,8 +1102,16 @@ def _float_code(dtype, name):
     raise ValueError(f"{name}: bfloat16 or float32 needed, not {dtype}")
 
 
+def linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of workspace of ``gdn_linear`` (0: it needs none)."""
+    n = lib().gdn_linear_workspace_bytes(int(M), int(N), int(K))
+    if n == 0 and lib().gdn_last_error():
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, lib().gdn_last_error().decode())
+    return int(n)
+
+
 def linear(x, w, bias=None, act=GDN_ACT_NONE, residual=None, out=None, out_dtype=None, preact=None,
-           stream=None):
+           workspace=None, stream=None):
     """y = act(x w^T + bias) + residual: x [M, K], w [N, K] bf16 (rows may be
     strided, in multiples of 8 elements), bias [N] fp32, residual [M, N] of
     the output's type; act one of GDN_ACT_*.  out: the tensor to write (may
@@ -1132,7 +1142,13 @@ def linear(x, w, bias=None, act=GDN_ACT_NONE, residual=None, out=None, out_dtype
     pp, sp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, bf16)
     io = CLinearIO(M, N, K, px, sx, pw, sw, _dense(bias, "bias", N, None), int(act), pr, sr, py, code, sy,
                    pp, sp)
-    _check(lib().gdn_linear(ctypes.byref(io), _stream(stream)))
+    if workspace is None and 16 < M <= 64:
+        nb = linear_workspace_bytes(M, N, K)
+        if nb:
+            with _on(stream):
+                workspace = torch.empty(nb, dtype=torch.uint8, device=x.device)
+    ws, nb = _bytes(workspace, "workspace")
+    _check(lib().gdn_linear(ctypes.byref(io), ws, nb, _stream(stream)))
     return out
 
 

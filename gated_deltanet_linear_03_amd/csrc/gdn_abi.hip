@@ -1260,7 +1260,14 @@ bool any_overlap(const Span& a, const Span* b, int n) {
 
 }  // namespace
 
-gdn_status gdn_linear(const gdn_linear_io* io, void* stream) {
+size_t gdn_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    g_err[0] = 0;
+    if (check_dims(M, N, K) != GDN_OK) return 0;
+    const int parts = gdn::linear_parts(M, N, K);
+    return parts > 1 ? static_cast<size_t>(round_up(4 * parts * M * N, 256)) : 0;
+}
+
+gdn_status gdn_linear(const gdn_linear_io* io, void* ws, size_t ws_bytes, void* stream) {
     g_err[0] = 0;
     if (!io) return fail(GDN_ERR_INVALID_ARGUMENT, "io is NULL");
     const int64_t M = io->M, N = io->N, K = io->K;
@@ -1299,7 +1306,16 @@ gdn_status gdn_linear(const gdn_linear_io* io, void* stream) {
     if (any_overlap(y, in, 3) || any_overlap(pre, in, 3) || any_overlap(pre, &res, 1) || any_overlap(pre, &y, 1) ||
         (!in_place && any_overlap(y, &res, 1)))
         return fail(GDN_ERR_INVALID_ARGUMENT, "y or preact overlaps an input or each other");
-    hipError_t e = gdn::launch_linear(p, static_cast<hipStream_t>(stream));
+    const size_t need = gdn_linear_workspace_bytes(M, N, K);
+    if (need > 0) {
+        if (!ws) return fail(GDN_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+        if (!aligned(ws, 256)) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        if (ws_bytes < need) return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, need %zu", ws_bytes, need);
+        const Span w{ws, need};
+        if (any_overlap(w, in, 3) || any_overlap(w, &res, 1) || any_overlap(w, &y, 1) || any_overlap(w, &pre, 1))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "workspace overlaps another buffer");
+    }
+    hipError_t e = gdn::launch_linear(p, static_cast<float*>(ws), static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(GDN_ERR_HIP, "linear launch failed: %s", hipGetErrorString(e));
     return GDN_OK;
 }
@@ -1307,15 +1323,21 @@ gdn_status gdn_linear(const gdn_linear_io* io, void* stream) {
 namespace {
 
 struct LinearWs {
-    int64_t ldd = 0, off_part = 0, total = 0;
+    int64_t ldd = 0, off_part = 0, off_dx = 0, off_dw = 0, total = 0;
 };
 
-// dp [M][N rounded up to 8] bf16, then the column sums of its row blocks
-LinearWs linear_ws(int64_t M, int64_t N) {
+// dp [M][N rounded up to 8] bf16, the column sums of its row blocks, and dx
+// and dw in parts where their reductions are split
+LinearWs linear_ws(int64_t M, int64_t N, int64_t K) {
     LinearWs w;
+    int px = 1, pw = 1;
+    gdn::linear_backward_parts(M, N, K, &px, &pw);
+    const bool split = px > 1 || pw > 1;
     w.ldd = round_up(N, 8);
     w.off_part = round_up(2 * M * w.ldd, 256);
-    w.total = w.off_part + round_up(4 * gdn::linear_dp_blocks(M) * N, 256);
+    w.off_dx = w.off_part + round_up(4 * gdn::linear_dp_blocks(M) * N, 256);
+    w.off_dw = w.off_dx + (split ? round_up(4 * px * M * K, 256) : 0);
+    w.total = w.off_dw + (split ? round_up(4 * pw * N * K, 256) : 0);
     if (w.total < 256) w.total = 256;
     return w;
 }
@@ -1331,7 +1353,7 @@ gdn_status check_backward(int64_t N) {
 size_t gdn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     g_err[0] = 0;
     if (check_dims(M, N, K) != GDN_OK || check_backward(N) != GDN_OK) return 0;
-    return static_cast<size_t>(linear_ws(M, N).total);
+    return static_cast<size_t>(linear_ws(M, N, K).total);
 }
 
 gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_bytes, void* stream) {
@@ -1371,7 +1393,7 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_by
     if (dx && (st = check_rows("dx", dx, lddx, K, 2)) != GDN_OK) return st;
     if (dw && (st = check_rows("dw", dw, lddw, K, 2)) != GDN_OK) return st;
     if (!aligned(gr->dbias, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "dbias must be 4-byte aligned");
-    const LinearWs w = linear_ws(M, N);
+    const LinearWs w = linear_ws(M, N, K);
     if (!ws) return fail(GDN_ERR_WORKSPACE, "workspace is NULL (need %lld bytes)", static_cast<long long>(w.total));
     if (!aligned(ws, 256)) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (ws_bytes < static_cast<size_t>(w.total))
@@ -1403,7 +1425,8 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_by
     px.ep.y = dx; px.ep.ldy = lddx;
     pw.ep.y = dw; pw.ep.ldy = lddw;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = gdn::launch_linear_backward(dp, px, pw, M > 0 ? dbias : nullptr, s);
+    hipError_t e = gdn::launch_linear_backward(dp, px, pw, M > 0 ? dbias : nullptr, reinterpret_cast<float*>(base + w.off_dx),
+                                               reinterpret_cast<float*>(base + w.off_dw), s);
     if (e == hipSuccess && M == 0) e = gdn::launch_fill_zero(dbias, N, s);
     if (e != hipSuccess) return fail(GDN_ERR_HIP, "linear backward launch failed: %s", hipGetErrorString(e));
     return GDN_OK;

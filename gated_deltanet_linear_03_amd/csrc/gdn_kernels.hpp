@@ -262,10 +262,17 @@ struct LinearDp {
     int cols;                            // blocks of columns (set by the launcher)
 };
 
+constexpr int kLinearStreamRows = 16;    // up to this many rows: the weight-streaming kernel
+constexpr int kLinearFewRows = 64;       // up to this many: the reduction in parts, as N and K make it
+
+// Parts of the reduction: 1 or how many [M][N] fp32 sums the call keeps
+int linear_parts(int64_t M, int64_t N, int64_t K);
+// the same for dx ([M][K]) and dw ([N][K])
+void linear_backward_parts(int64_t M, int64_t N, int64_t K, int* dx, int* dw);
 int64_t linear_dp_blocks(int64_t M);
-hipError_t launch_linear(const GemmProduct& p, hipStream_t s);
+hipError_t launch_linear(const GemmProduct& p, float* sums, hipStream_t s);
 // dx or dw with ep.y NULL is left out
-hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias,
-                                  hipStream_t s);
+hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias, float* sums_dx,
+                                  float* sums_dw, hipStream_t s);
 
 }  // namespace gdn

@@ -11,9 +11,9 @@
 // transposed on the way from LDS to the matrix cores (ds_read_b64_tr_b16),
 // so nothing is ever transposed in memory.
 //
-// Few rows (M <= 64): the product is a stream over w, and bound by HBM; the
-// few-row kernel reads each weight once in 256-byte runs with K split over
-// the waves of a work-group.
+// Few rows: the product is a stream over w, and bound by HBM.  Up to 16 rows
+// each work-group takes 16 columns with K split over its waves; up to 64 rows
+// K is split over work-groups of 64 columns, whose sums a second kernel adds.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -674,94 +674,162 @@ __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void linear_backward_kern
     else gemm_tile<false, false, true, S>(dw, blockIdx.x - first, shared);
 }
 
-// ---- few rows --------------------------------------------------------------------
-// A work-group owns 16 rows of w (16 columns of y) and splits K over its NWV
-// waves; per 128-wide step of K, lane (l16, lq) reads 64 contiguous bytes of
-// its weight row and of its row of each 16-row tile of x.  The waves' partial
-// tiles are summed in LDS in wave order.
-constexpr int kFewRows = 64, kFewStep = 128;
+// ---- the reduction in parts ------------------------------------------------------
+// Products with fewer tiles than compute units, and enough of a reduction:
+// part s of `parts` takes an equal share of it (in rounds of 128) and leaves
+// its sums in 32 bits; a second kernel adds the parts in order and finishes.
+__host__ __device__ inline int64_t part_share(int64_t K, int parts) {
+    return ((K + 127) / 128 + parts - 1) / parts * 128;
+}
 
-template <int MT, int NWV>
-__global__ __launch_bounds__(NWV * kWave) void linear_few_kernel(GemmProduct p) {
-    __shared__ f32x4 part[NWV][MT][kWave];
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+template <bool AK, bool BK>
+__device__ __forceinline__ void gemm_part(const GemmProduct& whole, int block, float* sums, int parts, uint8_t* shared) {
+    const int tiles = static_cast<int>(((whole.M + 63) / 64) * ((whole.N + 63) / 64));
+    const int part = block / tiles;
+    const int64_t share = part_share(whole.K, parts), k0 = share * part;
+    GemmProduct p = whole;
+    p.K = whole.K - k0 < share ? (whole.K > k0 ? whole.K - k0 : 0) : share;
+    if (p.K > 0) {
+        p.A = static_cast<const uint16_t*>(whole.A) + (AK ? k0 : k0 * whole.lda);
+        p.B = static_cast<const uint16_t*>(whole.B) + (BK ? k0 : k0 * whole.ldb);
+    }
+    p.ep.y = sums + part * whole.M * whole.N;
+    p.ep.ldy = whole.N;
+    p.ep.bf16 = 0;
+    gemm_tile<AK, BK, true, Small>(p, block % tiles, shared);
+}
+
+__global__ __launch_bounds__(Small::kThreads, Small::kPerSimd) void linear_part_kernel(GemmProduct p, float* sums, int parts) {
+    __shared__ __align__(1024) uint8_t shared[Small::kBytes];
+    gemm_part<true, true>(p, blockIdx.x, sums, parts, shared);
+}
+
+// dx (the first `first` work-groups) and dw in parts
+__global__ __launch_bounds__(Small::kThreads, Small::kPerSimd) void linear_backward_part_kernel(
+        GemmProduct dx, GemmProduct dw, float* sx, float* sw, int px, int pw, int first) {
+    __shared__ __align__(1024) uint8_t shared[Small::kBytes];
+    if (static_cast<int>(blockIdx.x) < first) gemm_part<true, false>(dx, blockIdx.x, sx, px, shared);
+    else gemm_part<false, false>(dw, blockIdx.x - first, sw, pw, shared);
+}
+
+// four columns a thread
+__device__ __forceinline__ void join(const GemmProduct& p, const float* sums, int parts, int64_t i) {
+    const int64_t per = (p.N + 3) / 4, m = i / per, n = (i % per) * 4;
+    if (m >= p.M) return;
+    const int nv = p.N - n < 4 ? static_cast<int>(p.N - n) : 4;
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    const int64_t step = p.M * p.N, at = m * p.N + n;
+    int s = 0;
+    for (; s + 4 <= parts; s += 4) {
+        float t[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load_n<4>(sums, false, (s + u) * step + at, nv, t[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] += t[u][e];
+    }
+    for (; s < parts; ++s) {
+        float t[4];
+        load_n<4>(sums, false, s * step + at, nv, t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] += t[e];
+    }
+    finish_n<4>(p.ep, m, n, nv, f);
+}
+
+constexpr int kJoinThreads = 256;
+
+__global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(GemmProduct p, const float* sums, int parts) {
+    join(p, sums, parts, static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x);
+}
+
+__global__ __launch_bounds__(kJoinThreads) void linear_backward_join_kernel(GemmProduct dx, GemmProduct dw, const float* sx,
+                                                                           const float* sw, int px, int pw, int first) {
+    const int b = blockIdx.x;
+    if (b < first) join(dx, sx, px, static_cast<int64_t>(b) * kJoinThreads + threadIdx.x);
+    else join(dw, sw, pw, static_cast<int64_t>(b - first) * kJoinThreads + threadIdx.x);
+}
+
+// ---- few rows --------------------------------------------------------------------
+// Up to 16 rows.  (More would read all of x through each compute unit's L1
+// for every 16 columns: 64 x 2048 x 4096 took 23 us so.)  A work-group owns 16 rows of w (16 columns of y) and splits K over its waves;
+// per 64-wide step of K the lanes of a row read two runs of 64 bytes of their
+// weight row and of their row of x, DEPTH steps ahead.  Steps past a
+// wave's share and k past K read zeros.  The waves' partial tiles are summed
+// in LDS in wave order.
+constexpr int kFewStep = 64, kFewWaves = 8;
+
+template <int DEPTH>
+__global__ __launch_bounds__(kFewWaves * kWave, 2) void linear_few_kernel(GemmProduct p) {
+    __shared__ f32x4 part[kFewWaves][kWave];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int l16 = lane % 16, lq = lane / 16;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-    const int64_t steps = (p.K + kFewStep - 1) / kFewStep;
-    const int64_t s0 = steps * wave / NWV, s1 = steps * (wave + 1) / NWV;
-    const bool nok = n0 + l16 < p.N;
-    const uint16_t* brow = static_cast<const uint16_t*>(p.B) + (nok ? n0 + l16 : 0) * p.ldb;
-    const uint16_t* arow[MT];
-    bool mok[MT];
-    f32x4 acc[MT];
+    const int steps = static_cast<int>((p.K + kFewStep - 1) / kFewStep);
+    const int s0 = static_cast<int>(static_cast<int64_t>(steps) * wave / kFewWaves);
+    const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (wave + 1) / kFewWaves);
+    const int64_t end = static_cast<int64_t>(s1) * kFewStep < p.K ? static_cast<int64_t>(s1) * kFewStep : p.K;
+    // rows past the end: never stored
+    const uint16_t* brow = static_cast<const uint16_t*>(p.B) + (n0 + l16 < p.N ? n0 + l16 : p.N - 1) * p.ldb;
+    const uint16_t* arow = static_cast<const uint16_t*>(p.A) + (l16 < p.M ? l16 : p.M - 1) * p.lda;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    u32x4 bf[DEPTH][2], af[DEPTH][2];
+    auto load = [&](int st, int slot) {
+        const int64_t k0 = static_cast<int64_t>(st) * kFewStep + lq * 8;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        mok[t] = 16 * t + l16 < p.M;
-        arow[t] = static_cast<const uint16_t*>(p.A) + (mok[t] ? 16 * t + l16 : 0) * p.lda;
-        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll 2
-    for (int64_t st = s0; st < s1; ++st) {
-        const int64_t kb = st * kFewStep + lq * 32;
-        u32x4 bf[4];
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = k0 + 32 * h;
+            bf[slot][h] = *reinterpret_cast<const u32x4*>(k < end ? brow + k : zero_chunk);
+            af[slot][h] = *reinterpret_cast<const u32x4*>(k < end ? arow + k : zero_chunk);
+        }
+    };
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            bf[j] = nok && kb + 8 * j < p.K ? *reinterpret_cast<const u32x4*>(brow + kb + 8 * j) : zero;
+    for (int d = 0; d < DEPTH; ++d) load(s0 + d, d);
+    for (int st = s0; st < s1; st += DEPTH) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            u32x4 af[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                af[j] = mok[t] && kb + 8 * j < p.K ? *reinterpret_cast<const u32x4*>(arow[t] + kb + 8 * j) : zero;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[t] = mfma(bf[j], af[j], acc[t]);
+        for (int d = 0; d < DEPTH; ++d) {
+            acc = mfma(bf[d][0], af[d][0], acc);
+            acc = mfma(bf[d][1], af[d][1], acc);
+            if (st + DEPTH < s1) load(st + DEPTH + d, d);
         }
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+    part[wave][lane] = acc;
     __syncthreads();
-    for (int t = wave; t < MT; t += NWV) {
-        f32x4 s = part[0][t][lane];
-        for (int w = 1; w < NWV; ++w) s += part[w][t][lane];
-        const int64_t m = 16 * t + l16, n = n0 + 4 * lq;
-        if (m >= p.M || n >= p.N) continue;
-        const int nv = p.N - n < 4 ? static_cast<int>(p.N - n) : 4;
-        float f[4] = {s[0], s[1], s[2], s[3]};
-        finish_n<4>(p.ep, m, n, nv, f);
-    }
+    if (wave != 0) return;
+    f32x4 s = part[0][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += part[w][lane];
+    const int64_t m = l16, n = n0 + 4 * lq;
+    if (m >= p.M || n >= p.N) return;
+    const int nv = p.N - n < 4 ? static_cast<int>(p.N - n) : 4;
+    float f[4] = {s[0], s[1], s[2], s[3]};
+    finish_n<4>(p.ep, m, n, nv, f);
 }
 
 // ---- dp = dy act'(p) and its column sums -------------------------------------------
-// Bound: HBM (dy and p in, dp out).  A work-group covers 64 rows x 256
-// columns: 32 lanes of eight columns, every eighth row, four rows' loads in
-// flight together; dp is rounded to bf16 (the products' operand type), the
+// Bound: HBM (dy and p in, dp out).  A work-group covers 32 rows x 256
+// columns: 32 lanes of eight columns, every eighth row, the four rows' loads
+// in flight together; dp is rounded to bf16 (the products' operand type), the
 // sums are of the values before that.
-constexpr int kDpRows = 64, kDpCols = 256, kDpBatch = 4;
+constexpr int kDpRows = 32, kDpCols = 256, kDpBatch = 4;
 
-__global__ __launch_bounds__(256) void linear_dp_kernel(LinearDp p) {
-    __shared__ float sums[8][kDpCols];
-    const int lane = threadIdx.x % 32, g = threadIdx.x / 32;
-    const int64_t block = blockIdx.x / p.cols, col0 = static_cast<int64_t>(blockIdx.x % p.cols) * kDpCols;
-    const int64_t m0 = block * kDpRows, n = col0 + 8 * lane;
-    const int64_t left = p.N - n;
-    const int nv = left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
-    float s[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+// WHOLE: all rows and columns of the block exist
+template <bool WHOLE>
+__device__ __forceinline__ void dp_rows(const LinearDp& p, int64_t m0, int64_t n, int nv, int g, float* s) {
 #pragma unroll
     for (int i0 = 0; i0 < kDpRows / 8; i0 += kDpBatch) {
         float d[kDpBatch][8], q[kDpBatch][8];
 #pragma unroll
         for (int u = 0; u < kDpBatch; ++u) {
             const int64_t m = m0 + g + 8 * (i0 + u);
-            load_n<8>(p.dy, p.dy_bf16, m * p.ldy + n, m < p.M ? nv : 0, d[u]);
+            load_n<8>(p.dy, p.dy_bf16, m * p.ldy + n, WHOLE ? 8 : (m < p.M ? nv : 0), d[u]);
         }
         if (p.act != kActNone) {
 #pragma unroll
             for (int u = 0; u < kDpBatch; ++u) {
                 const int64_t m = m0 + g + 8 * (i0 + u);
-                load_n<8>(p.preact, true, m * p.ldp + n, m < p.M ? nv : 0, q[u]);
+                load_n<8>(p.preact, true, m * p.ldp + n, WHOLE ? 8 : (m < p.M ? nv : 0), q[u]);
             }
             switch (p.act) {
 #define GDN_SLOPE_CASE(ACT)                                                               \
@@ -782,9 +850,27 @@ __global__ __launch_bounds__(256) void linear_dp_kernel(LinearDp p) {
             const int64_t m = m0 + g + 8 * (i0 + u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] += d[u][e];              // (rows and columns past the end: zeros)
-            if (p.dp && m < p.M && n < p.ldd) store_n<8>(p.dp, true, m * p.ldd + n, 8, d[u]);
+            if (p.dp && (WHOLE || (m < p.M && n < p.ldd))) {
+                const u32x4 h = {pack_bf16(d[u][0], d[u][1]), pack_bf16(d[u][2], d[u][3]), pack_bf16(d[u][4], d[u][5]),
+                                 pack_bf16(d[u][6], d[u][7])};
+                *reinterpret_cast<u32x4*>(p.dp + m * p.ldd + n) = h;   // (the workspace's rows: whole 16-byte runs)
+            }
         }
     }
+}
+
+__global__ __launch_bounds__(256) void linear_dp_kernel(LinearDp p) {
+    __shared__ float sums[8][kDpCols];
+    const int lane = threadIdx.x % 32, g = threadIdx.x / 32;
+    const int64_t block = blockIdx.x / p.cols, col0 = static_cast<int64_t>(blockIdx.x % p.cols) * kDpCols;
+    const int64_t m0 = block * kDpRows, n = col0 + 8 * lane;
+    const int64_t left = p.N - n;
+    const int nv = left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    if (m0 + kDpRows <= p.M && col0 + kDpCols <= p.N) dp_rows<true>(p, m0, n, nv, g, s);
+    else dp_rows<false>(p, m0, n, nv, g, s);
     if (!p.part) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[g][8 * lane + e] = s[e];
@@ -884,20 +970,38 @@ static GemmProduct columns(const GemmProduct& p, int64_t n0, int64_t n) {
     return c;
 }
 
-hipError_t launch_linear(const GemmProduct& given, hipStream_t s) {
+// Parts of a reduction of K for `tiles` tiles of 64 x 64: as many as fill
+// the compute units twice, of 256 at least.
+static int parts_for(int64_t tiles, int64_t K, int cus) {
+    const int64_t want = (2 * cus + tiles - 1) / tiles, most = K / 256;
+    const int64_t n = want < most ? want : most;
+    return n < 1 ? 1 : static_cast<int>(n > 64 ? 64 : n);
+}
+
+int linear_parts(int64_t M, int64_t N, int64_t K) {
+    return M > kLinearStreamRows && M <= kLinearFewRows ? parts_for((N + 63) / 64, K, compute_units()) : 1;
+}
+
+static int64_t join_blocks(const GemmProduct& p) { return (p.M * ((p.N + 3) / 4) + kJoinThreads - 1) / kJoinThreads; }
+
+hipError_t launch_linear(const GemmProduct& given, float* sums, hipStream_t s) {
     if (given.M <= 0 || given.N <= 0) return hipSuccess;
     GemmProduct p = given;
     if (p.ep.act == kActGelu && p.ep.bf16) p.ep.act = kActGeluBf16;
-    if (p.M <= kFewRows) {
-        const dim3 grid(static_cast<unsigned>((p.N + 15) / 16));
-        switch ((p.M + 15) / 16) {
-            case 1: hipLaunchKernelGGL((linear_few_kernel<1, 8>), grid, dim3(8 * kWave), 0, s, p); break;
-            case 2: hipLaunchKernelGGL((linear_few_kernel<2, 8>), grid, dim3(8 * kWave), 0, s, p); break;
-            case 3: hipLaunchKernelGGL((linear_few_kernel<3, 8>), grid, dim3(8 * kWave), 0, s, p); break;
-            default: hipLaunchKernelGGL((linear_few_kernel<4, 8>), grid, dim3(8 * kWave), 0, s, p); break;
-        }
+    if (p.M <= kLinearStreamRows) {
+        hipLaunchKernelGGL((linear_few_kernel<4>), dim3(static_cast<unsigned>((p.N + 15) / 16)), dim3(kFewWaves * kWave), 0, s, p);
         return hipGetLastError();
     }
+    const int parts = linear_parts(p.M, p.N, p.K);
+    if (parts > 1) {
+        hipLaunchKernelGGL(linear_part_kernel, dim3(static_cast<unsigned>(tiles<Small>(p) * parts)), dim3(Small::kThreads), 0, s, p,
+                           sums, parts);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(linear_join_kernel, dim3(static_cast<unsigned>(join_blocks(p))), dim3(kJoinThreads), 0, s, p, sums, parts);
+        return hipGetLastError();
+    }
+    if (p.M <= kLinearFewRows) return forward_t<Small>(p, s);
     // A last column of tiles that is nearly empty can cost a whole round of
     // them (12352 = 48 x 256 + 64 columns at 4096 rows: 784 tiles, four rounds
     // instead of three): then the rest goes by itself in smaller tiles.  A
@@ -918,8 +1022,20 @@ hipError_t launch_linear(const GemmProduct& given, hipStream_t s) {
 
 int64_t linear_dp_blocks(int64_t M) { return (M + kDpRows - 1) / kDpRows; }
 
-hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias,
-                                  hipStream_t s) {
+// Parts of dx's and dw's reductions
+void linear_backward_parts(int64_t M, int64_t N, int64_t K, int* dx, int* dw) {
+    const int cus = compute_units();
+    const int64_t tx = ((M + 63) / 64) * ((K + 63) / 64), tw = ((N + 63) / 64) * ((K + 63) / 64);
+    *dx = *dw = 1;
+    // (from as many small tiles as compute units on, larger tiles take over)
+    if (tx > 0 && tw > 0 && tx + tw < cus) {
+        *dx = parts_for(tx + tw, N, cus);
+        *dw = parts_for(tx + tw, M, cus);
+    }
+}
+
+hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias, float* sums_dx,
+                                  float* sums_dw, hipStream_t s) {
     if (dp.dp || dp.part) {
         LinearDp d = dp;
         d.cols = static_cast<int>(((dp.dp ? dp.ldd : dp.N) + kDpCols - 1) / kDpCols);
@@ -935,6 +1051,19 @@ hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, con
         if (e != hipSuccess) return e;
     }
     if (!dx.ep.y && !dw.ep.y) return hipSuccess;
+    int px = 1, pw = 1;
+    linear_backward_parts(dp.M, dp.N, dx.N, &px, &pw);
+    if (px > 1 || pw > 1) {
+        const int64_t t1 = dx.ep.y ? tiles<Small>(dx) * px : 0, t2 = dw.ep.y ? tiles<Small>(dw) * pw : 0;
+        hipLaunchKernelGGL(linear_backward_part_kernel, dim3(static_cast<unsigned>(t1 + t2)), dim3(Small::kThreads), 0, s, dx, dw,
+                           sums_dx, sums_dw, px, pw, static_cast<int>(t1));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const int64_t b1 = dx.ep.y ? join_blocks(dx) : 0, b2 = dw.ep.y ? join_blocks(dw) : 0;
+        hipLaunchKernelGGL(linear_backward_join_kernel, dim3(static_cast<unsigned>(b1 + b2)), dim3(kJoinThreads), 0, s, dx, dw,
+                           sums_dx, sums_dw, px, pw, static_cast<int>(b1));
+        return hipGetLastError();
+    }
     switch (choose(dx.ep.y ? &dx : nullptr, dw.ep.y ? &dw : nullptr, compute_units()).tiles) {
         case kLarge: return backward_t<Large>(dx, dw, s);
         case kWide: return backward_t<Wide>(dx, dw, s);

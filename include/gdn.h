@@ -638,10 +638,19 @@ typedef struct {
     int64_t preact_stride;
 } gdn_linear_io;
 
-/* Enqueue the layer.  Up to 64 rows run on a weight-streaming kernel, more on
- * a tiled one; both sum in an order that does not depend on the other rows,
- * but the orders differ, so a row's bits may change when M crosses 64. */
-gdn_status gdn_linear(const gdn_linear_io* io, void* stream);
+/* Bytes of device workspace gdn_linear needs; 0 where it needs none (up to 16
+ * and from 65 rows on, and with a short K) and on error (gdn_last_error()
+ * tells). */
+size_t gdn_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Enqueue the layer.  Up to 16 rows run on a weight-streaming kernel, up to
+ * 64 with K in parts (one more kernel adds them), more on tiles.  Each sums
+ * in an order that does not depend on the other rows, but the orders differ,
+ * so a row's bits may change when M crosses 16 or 64.  workspace: device
+ * memory, 256-byte aligned, not shared with a concurrently running call (its
+ * contents need not start at zero). */
+gdn_status gdn_linear(const gdn_linear_io* io, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Gradients: dp = dy act'(preact), dbias = column sums of dp, dx = dp w,
  * dw = dp^T x (the residual's gradient is dy).  dp is an operand of the two

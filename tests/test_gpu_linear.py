@@ -81,7 +81,7 @@ def reference(x, w, bias, act, res):
 
 
 SHAPES = [(1, 1, 8), (1, 65, 2048), (2, 200, 72), (16, 16, 128), (17, 33, 136), (33, 100, 640), (64, 130, 256),
-          (65, 7, 8), (65, 64, 64), (100, 129, 72), (129, 255, 200), (300, 300, 1000), (64, 50, 0), (70, 50, 0)]
+          (20, 70, 1000), (33, 200, 2064), (64, 40, 4096), (65, 7, 8), (65, 64, 64), (100, 129, 72), (129, 255, 200), (300, 300, 1000), (64, 50, 0), (70, 50, 0)]
 
 
 @pytest.mark.parametrize("act", list(ACTS))
@@ -114,7 +114,7 @@ def test_forward_in_large_tiles(M, N, K):
     close("y", y, want, lim + (want.abs() + lim) * HALF[torch.bfloat16])
 
 
-GRADS = [(1, 1, 8), (3, 5, 16), (64, 64, 64), (65, 130, 72), (130, 67, 200), (200, 96, 128), (257, 300, 136), (1000, 33, 264),
+GRADS = [(1, 1, 8), (3, 5, 16), (64, 64, 64), (65, 130, 72), (130, 67, 200), (200, 96, 128), (257, 300, 136), (1000, 33, 264), (1030, 70, 72), (90, 1100, 200), (700, 520, 40),
          (0, 16, 8), (5, 0, 8)]
 
 
@@ -242,6 +242,12 @@ def test_writes_stay_inside_and_in_place_residual(M, N, K):
         v.fill_(77.0)
         assert (t == 77.0).all()
     assert (ws[:256] == 0xA5).all() and (ws[256 + nb:] == 0xA5).all()
+    # the sums of 17 .. 64 rows stay in their workspace too
+    g, x, w = data(33, 70, 1032, 6)
+    nb = gdn.linear_workspace_bytes(33, 70, 1032)
+    ws = torch.full((nb + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert torch.equal(gdn.linear(x, w, workspace=ws[256:256 + nb]), gdn.linear(x, w))
+    assert (ws[:256] == 0xA5).all() and (ws[256 + nb:] == 0xA5).all()
 
 
 def test_same_bits_next_to_other_rows_and_again():
@@ -250,8 +256,8 @@ def test_same_bits_next_to_other_rows_and_again():
     for _ in range(3):
         assert torch.equal(gdn.linear(x, w), y)
     assert torch.equal(gdn.linear(x[100:300], w), y[100:300])
-    few = gdn.linear(x[:64], w)
-    assert torch.equal(gdn.linear(x[5:6], w), few[5:6]) and torch.equal(gdn.linear(x[30:50], w), few[30:50])
+    few, stream = gdn.linear(x[:64], w), gdn.linear(x[:16], w)
+    assert torch.equal(gdn.linear(x[5:6], w), stream[5:6]) and torch.equal(gdn.linear(x[30:50], w), few[30:50])
     dy = torch.randn((700, 600), generator=g, device="cuda").to(torch.bfloat16)
     a = gdn.linear_backward(dy, x, w, want_dbias=True)
     for _ in range(3):

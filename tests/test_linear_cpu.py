@@ -34,14 +34,28 @@ def _io(**kw):
     (dict(residual=FAKE + 5 * FAR, residual_stride=80), "overlaps"), (dict(M=1 << 30, N=1 << 30), "too large"),
 ])
 def test_linear_refuses(change, word):
-    assert gdn.lib().gdn_linear(ctypes.byref(_io(**change)), None) == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert gdn.lib().gdn_linear(ctypes.byref(_io(**change)), WS, NWS, None) == gdn.GDN_ERR_INVALID_ARGUMENT
     assert word in gdn.lib().gdn_last_error().decode()
 
 
 def test_empty_outputs_are_no_calls():
     for kw in (dict(M=0), dict(N=0)):
-        assert gdn.lib().gdn_linear(ctypes.byref(_io(**kw)), None) == gdn.GDN_OK
-    assert gdn.lib().gdn_linear(None, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+        assert gdn.lib().gdn_linear(ctypes.byref(_io(**kw)), None, 0, None) == gdn.GDN_OK
+    assert gdn.lib().gdn_linear(None, None, 0, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+
+
+def test_forward_workspace():
+    """Rows 17 .. 64 keep [parts][M][N] fp32 sums when K is at least 512."""
+    L = gdn.lib()
+    for M, N, K in ((16, 2048, 4096), (65, 2048, 4096), (32, 2048, 504), (0, 64, 4096)):
+        assert L.gdn_linear_workspace_bytes(M, N, K) == 0 and L.gdn_last_error() == b""
+    need = L.gdn_linear_workspace_bytes(40, 72, 1024)
+    assert need > 0 and need % 256 == 0 and need % (4 * 40 * 72) < 256
+    assert L.gdn_linear_workspace_bytes(1, 1, 3) == 0 and L.gdn_last_error()
+    for ws, n in ((None, NWS), (WS + 8, NWS), (WS, need - 1)):
+        assert L.gdn_linear(ctypes.byref(_io(M=40, K=1024)), ws, n, None) == gdn.GDN_ERR_WORKSPACE
+    assert L.gdn_linear(ctypes.byref(_io(M=40, K=1024)), FAKE + 5 * FAR, NWS, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert b"workspace overlaps" in L.gdn_last_error()
 
 
 def _grad(**kw):
