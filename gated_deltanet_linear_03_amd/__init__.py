@@ -818,22 +818,38 @@ def layer_decode_raw(layer: Layer, proj: Proj, *, B, x, y, state_in, state_out, 
 
 # ---- the diagonal gated recurrence -------------------------------------------
 
-def _on_device(t, name):
-    """Raise ValueError unless t is on the current device: the library
-    launches there, on the given stream."""
+# (One token's call costs more on the host than on the device, so these checks
+# try what is usual first and name what is wrong only when it is not.)
+
+def _device():
+    """Index of the current device: the library launches there."""
     import torch
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, dev):
+    """Handle of a stream (None: torch's current one on device `dev`)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _on_device(t, name, dev):
+    """Raise ValueError unless t is on the current device."""
     if not t.is_cuda:
         raise ValueError(f"{name}: a device tensor is required")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: on cuda:{t.get_device()}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, the current device is cuda:{dev}")
 
 
-def _matrix(t, name, rows, cols, dtype):
-    """Raise ValueError unless t is a [>= rows, cols] tensor of `dtype` on
-    the current device whose rows are dense; returns its pointer and row
-    stride in elements."""
-    _on_device(t, name)
+def _matrix(t, name, rows, cols, dtype, dev):
+    """Pointer and row stride in elements of a [>= rows, cols] tensor of
+    `dtype` on the current device whose rows are dense; ValueError for
+    anything else."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols):
+        rs, cs = t.stride()
+        if cs == 1 and rs >= cols and rows:
+            return t.data_ptr(), rs
+    _on_device(t, name, dev)
     shape = t.shape
     if len(shape) != 2 or shape[0] < rows or shape[1] != cols:
         raise ValueError(f"{name}: [{rows}, {cols}] needed, shape is {tuple(shape)}")
@@ -849,48 +865,51 @@ def _matrix(t, name, rows, cols, dtype):
     return t.data_ptr(), max(rs, cols)
 
 
-def _dense(t, name, rows, cols):
+def _dense(t, name, rows, cols, dev):
     """Pointer of an optional dense fp32 [>= rows, cols] tensor (cols None:
     [>= rows])."""
-    import torch
     if t is None:
         return None
-    _on_device(t, name)
+    import torch
     shape = t.shape
     ok = len(shape) == 1 if cols is None else (len(shape) == 2 and shape[1] == cols)
-    if not ok or shape[0] < rows or t.dtype != torch.float32 or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous float32 [{rows}{'' if cols is None else f', {cols}'}] "
-                         f"needed, not {t.dtype} {tuple(shape)}")
-    return t.data_ptr()
+    if (ok and t.get_device() == dev and shape[0] >= rows and t.dtype is torch.float32
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _on_device(t, name, dev)
+    raise ValueError(f"{name}: contiguous float32 [{rows}{'' if cols is None else f', {cols}'}] "
+                     f"needed, not {t.dtype} {tuple(shape)}")
 
 
-def _index(t, name, n):
+def _index(t, name, n, dev):
     """Pointer of an optional contiguous device int32 tensor of >= n entries."""
-    import torch
     if t is None:
         return None
-    _on_device(t, name)
-    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous device int32 tensor of {n} entries is required")
-    return t.data_ptr()
+    import torch
+    if t.dtype is torch.int32 and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    _on_device(t, name, dev)
+    raise ValueError(f"{name}: a contiguous device int32 tensor of {n} entries is required")
 
 
-def _bytes(t, name):
+def _bytes(t, name, dev):
     """Pointer and size of an optional workspace."""
     if t is None:
         return None, 0
-    _on_device(t, name)
+    _on_device(t, name, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _on(stream):
-    """A context in which torch allocates for `stream` (None: the current
-    one), so that memory a call on it uses is not reused under it."""
-    import contextlib
+def _new(like, shape, dtype, stream):
+    """A new tensor beside `like`, allocated for `stream` (None: the current
+    one): memory that a call on it uses is not reused under it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 @dataclass
@@ -911,12 +930,19 @@ class Recur:
         return torch.bfloat16 if self.act_dtype == GDN_DTYPE_BF16 else torch.float32
 
     def c(self) -> CRecur:
-        key = (self.D, self.act_dtype, self.A_log.data_ptr(), self.A_log.numel(),
-               self.dt_bias.data_ptr(), self.dt_bias.numel())
-        if getattr(self, "_key", None) != key:
-            self._c = CRecur(self.D, self.act_dtype, _dense(self.A_log, "A_log", self.D, None),
-                             _dense(self.dt_bias, "dt_bias", self.D, None))
+        # the parameters are measured once per set of tensors, device and shape
+        A, d = self.A_log, self.dt_bias
+        key = (A.data_ptr(), d.data_ptr(), A.shape, d.shape, self.D, self.act_dtype)
+        if self.__dict__.get("_key") != key:
+            for t, name in ((A, "A_log"), (d, "dt_bias")):
+                if not t.is_cuda:
+                    raise ValueError(f"{name}: a device tensor is required")
+            self._dev = _device()
+            self._c = CRecur(self.D, self.act_dtype, _dense(A, "A_log", self.D, None, self._dev),
+                             _dense(d, "dt_bias", self.D, None, self._dev))
             self._key = key
+        elif self._dev != _device():
+            _on_device(A, "A_log", _device())
         return self._c
 
 
@@ -942,25 +968,25 @@ def recur_backward_workspace_bytes(rec: Recur, N: int, T_total: int) -> int:
     return _recur_size("gdn_recur_backward_workspace_bytes", rec, N, T_total)
 
 
-def _recur_io(rec, N, T, rows, cu_seqlens, x, a, b, z, y, initial_state, final_state, state_slots,
-              num_slots, saved, status):
+def _recur_io(rec, dev, N, T, rows, cu_seqlens, x, a, b, z, y, initial_state, final_state,
+              state_slots, num_slots, saved, status):
     D, dt = rec.D, rec.dtype
-    px, sx = _matrix(x, "x", rows, D, dt)
-    pa, sa = _matrix(a, "a", rows, D, dt)
-    pb, sb = _matrix(b, "b", rows, D, dt)
-    pz, sz = (None, 0) if z is None else _matrix(z, "z", rows, D, dt)
-    py, sy = (None, 0) if y is None else _matrix(y, "y", rows, D, dt)
+    px, sx = _matrix(x, "x", rows, D, dt, dev)
+    pa, sa = _matrix(a, "a", rows, D, dt, dev)
+    pb, sb = _matrix(b, "b", rows, D, dt, dev)
+    pz, sz = (None, 0) if z is None else _matrix(z, "z", rows, D, dt, dev)
+    py, sy = (None, 0) if y is None else _matrix(y, "y", rows, D, dt, dev)
     entries = N if state_slots is None else num_slots
-    return CRecurIO(N, T, _index(cu_seqlens, "cu_seqlens", N + 1), px, pa, pb, pz, sx, sa, sb, sz,
-                    py, sy, _dense(initial_state, "initial_state", entries, D),
-                    _dense(final_state, "final_state", entries, D),
-                    _index(state_slots, "state_slots", N), num_slots,
-                    None if saved is None else _bytes(saved, "saved")[0],
-                    _index(status, "status", 1))
+    ps = _dense(initial_state, "initial_state", entries, D, dev)
+    pf = ps if final_state is initial_state else _dense(final_state, "final_state", entries, D, dev)
+    return CRecurIO(N, T, _index(cu_seqlens, "cu_seqlens", N + 1, dev), px, pa, pb, pz, sx, sa, sb,
+                    sz, py, sy, ps, pf, _index(state_slots, "state_slots", N, dev), num_slots,
+                    None if saved is None else _bytes(saved, "saved", dev)[0],
+                    _index(status, "status", 1, dev))
 
 
-def _recur_saved(rec, saved, N, T):
-    if saved is not None and _bytes(saved, "saved")[1] < recur_saved_bytes(rec, N, T):
+def _recur_saved(rec, saved, N, T, dev):
+    if saved is not None and _bytes(saved, "saved", dev)[1] < recur_saved_bytes(rec, N, T):
         raise ValueError(f"saved: {recur_saved_bytes(rec, N, T)} bytes needed")
 
 
@@ -969,12 +995,13 @@ def recur_forward_raw(rec: Recur, *, N, T_total, cu_seqlens, x, a, b, y, z=None,
                       num_slots=0, status=None):
     """Call ``gdn_recur_forward`` on caller-provided buffers (no allocation).
     status as for prefill_raw (GDN_STATUS_BAD_INDEX only)."""
-    N, T = int(N), int(T_total)
-    io = _recur_io(rec, N, T, T, cu_seqlens, x, a, b, z, y, initial_state, final_state, state_slots,
-                   int(num_slots), saved, status)
-    _recur_saved(rec, saved, N, T)
-    ws, nb = _bytes(workspace, "workspace")
-    _check(lib().gdn_recur_forward(ctypes.byref(rec.c()), ctypes.byref(io), ws, nb, _stream(stream)))
+    N, T, dev = int(N), int(T_total), _device()
+    io = _recur_io(rec, dev, N, T, T, cu_seqlens, x, a, b, z, y, initial_state, final_state,
+                   state_slots, int(num_slots), saved, status)
+    _recur_saved(rec, saved, N, T, dev)
+    ws, nb = _bytes(workspace, "workspace", dev)
+    _check(lib().gdn_recur_forward(ctypes.byref(rec.c()), ctypes.byref(io), ws, nb,
+                                   _raw_stream(stream, dev)))
 
 
 def recur_forward(rec: Recur, x, a, b, z, cu_seqlens, initial_state=None, want_saved=False,
@@ -990,25 +1017,22 @@ def recur_forward(rec: Recur, x, a, b, z, cu_seqlens, initial_state=None, want_s
     T, N, D = int(x.shape[0]), int(cu_seqlens.numel()) - 1, rec.D
     if state_slots is not None and initial_state is None:
         raise ValueError("state_slots needs the pool as initial_state")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, D), dtype=rec.dtype, device=x.device)
-        if initial_state is not None and (in_place or state_slots is not None):
-            fs = initial_state
-        else:
-            fs = torch.empty((N, D), dtype=torch.float32, device=x.device)
-        saved = None
-        if want_saved:
-            saved = torch.empty(recur_saved_bytes(rec, N, T), dtype=torch.uint8, device=x.device)
-        if workspace is None:
-            nb = recur_workspace_bytes(rec, N, T)
-            if nb:
-                workspace = torch.empty(nb, dtype=torch.uint8, device=x.device)
-        recur_forward_raw(rec, N=N, T_total=T, cu_seqlens=cu_seqlens, x=x, a=a, b=b, z=z, y=out,
-                          initial_state=initial_state, final_state=fs, saved=saved,
-                          workspace=workspace, stream=stream, state_slots=state_slots,
-                          num_slots=0 if state_slots is None else int(initial_state.shape[0]),
-                          status=status)
+    if out is None:
+        out = _new(x, (T, D), rec.dtype, stream)
+    if initial_state is not None and (in_place or state_slots is not None):
+        fs = initial_state
+    else:
+        fs = _new(x, (N, D), torch.float32, stream)
+    saved = _new(x, (recur_saved_bytes(rec, N, T),), torch.uint8, stream) if want_saved else None
+    if workspace is None:
+        nb = recur_workspace_bytes(rec, N, T)
+        if nb:
+            workspace = _new(x, (nb,), torch.uint8, stream)
+    recur_forward_raw(rec, N=N, T_total=T, cu_seqlens=cu_seqlens, x=x, a=a, b=b, z=z, y=out,
+                      initial_state=initial_state, final_state=fs, saved=saved,
+                      workspace=workspace, stream=stream, state_slots=state_slots,
+                      num_slots=0 if state_slots is None else int(initial_state.shape[0]),
+                      status=status)
     res = {"out": out, "final_state": fs}
     if want_saved:
         res["saved"] = saved
@@ -1020,20 +1044,22 @@ def recur_backward_raw(rec: Recur, *, N, T_total, cu_seqlens, x, a, b, dy, saved
                        ddt_bias=None, workspace=None, stream=None, status=None):
     """Call ``gdn_recur_backward`` on caller-provided buffers (no
     allocation)."""
-    N, T, D, dt = int(N), int(T_total), rec.D, rec.dtype
-    io = _recur_io(rec, N, T, T, cu_seqlens, x, a, b, z, None, None, None, None, 0, saved, status)
-    _recur_saved(rec, saved, N, T)
+    N, T, D, dt, dev = int(N), int(T_total), rec.D, rec.dtype, _device()
+    io = _recur_io(rec, dev, N, T, T, cu_seqlens, x, a, b, z, None, None, None, None, 0, saved,
+                   status)
+    _recur_saved(rec, saved, N, T, dev)
     if (z is None) != (dz is None):
         raise ValueError("dz: needed with z, and only with it")
-    (py, sy), (px, sx), (pa, sa), (pb, sb) = (_matrix(t, n, T, D, dt) for t, n in (
+    (py, sy), (px, sx), (pa, sa), (pb, sb) = (_matrix(t, n, T, D, dt, dev) for t, n in (
         (dy, "dy"), (dx, "dx"), (da, "da"), (db, "db")))
-    pz, sz = (None, 0) if dz is None else _matrix(dz, "dz", T, D, dt)
-    gr = CRecurGrad(py, sy, _dense(d_final_state, "d_final_state", N, D), px, pa, pb, pz, sx, sa, sb, sz,
-                    _dense(dA_log, "dA_log", D, None), _dense(ddt_bias, "ddt_bias", D, None),
-                    _dense(d_initial_state, "d_initial_state", N, D))
-    ws, nb = _bytes(workspace, "workspace")
+    pz, sz = (None, 0) if dz is None else _matrix(dz, "dz", T, D, dt, dev)
+    gr = CRecurGrad(py, sy, _dense(d_final_state, "d_final_state", N, D, dev), px, pa, pb, pz, sx, sa,
+                    sb, sz, _dense(dA_log, "dA_log", D, None, dev),
+                    _dense(ddt_bias, "ddt_bias", D, None, dev),
+                    _dense(d_initial_state, "d_initial_state", N, D, dev))
+    ws, nb = _bytes(workspace, "workspace", dev)
     _check(lib().gdn_recur_backward(ctypes.byref(rec.c()), ctypes.byref(io), ctypes.byref(gr), ws, nb,
-                                    _stream(stream)))
+                                    _raw_stream(stream, dev)))
 
 
 def recur_backward(rec: Recur, x, a, b, z, dy, saved, cu_seqlens, d_final_state=None,
@@ -1044,21 +1070,17 @@ def recur_backward(rec: Recur, x, a, b, z, dy, saved, cu_seqlens, d_final_state=
     [N, D] fp32.  saved: what recur_forward saved of the same inputs."""
     import torch
     T, N, D = int(x.shape[0]), int(cu_seqlens.numel()) - 1, rec.D
-    dev = x.device
-    with _on(stream):
-        res = {n: torch.empty((T, D), dtype=rec.dtype, device=dev) for n in ("dx", "da", "db")}
-        if z is not None:
-            res["dz"] = torch.empty((T, D), dtype=rec.dtype, device=dev)
-        res["dA_log"] = torch.empty(D, dtype=torch.float32, device=dev)
-        res["ddt_bias"] = torch.empty(D, dtype=torch.float32, device=dev)
-        if want_d_initial:
-            res["d_initial_state"] = torch.empty((N, D), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(recur_backward_workspace_bytes(rec, N, T), dtype=torch.uint8,
-                                    device=dev)
-        recur_backward_raw(rec, N=N, T_total=T, cu_seqlens=cu_seqlens, x=x, a=a, b=b, z=z, dy=dy,
-                           saved=saved, d_final_state=d_final_state, workspace=workspace,
-                           stream=stream, status=status, **res)
+    names = ("dx", "da", "db") if z is None else ("dx", "da", "db", "dz")
+    res = {n: _new(x, (T, D), rec.dtype, stream) for n in names}
+    res["dA_log"] = _new(x, (D,), torch.float32, stream)
+    res["ddt_bias"] = _new(x, (D,), torch.float32, stream)
+    if want_d_initial:
+        res["d_initial_state"] = _new(x, (N, D), torch.float32, stream)
+    if workspace is None:
+        workspace = _new(x, (recur_backward_workspace_bytes(rec, N, T),), torch.uint8, stream)
+    recur_backward_raw(rec, N=N, T_total=T, cu_seqlens=cu_seqlens, x=x, a=a, b=b, z=z, dy=dy,
+                       saved=saved, d_final_state=d_final_state, workspace=workspace, stream=stream,
+                       status=status, **res)
     return res
 
 
@@ -1066,10 +1088,10 @@ def recur_decode_raw(rec: Recur, *, N, x, a, b, y, initial_state, final_state, z
                      state_slots=None, num_slots=0, stream=None, status=None):
     """Call ``gdn_recur_decode`` on caller-provided buffers (no allocation).
     status as for decode_raw."""
-    N = int(N)
-    io = _recur_io(rec, N, 0, N, None, x, a, b, z, y, initial_state, final_state, state_slots,
+    N, dev = int(N), _device()
+    io = _recur_io(rec, dev, N, 0, N, None, x, a, b, z, y, initial_state, final_state, state_slots,
                    int(num_slots), None, status)
-    _check(lib().gdn_recur_decode(ctypes.byref(rec.c()), ctypes.byref(io), _stream(stream)))
+    _check(lib().gdn_recur_decode(ctypes.byref(rec.c()), ctypes.byref(io), _raw_stream(stream, dev)))
 
 
 def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True, out=None,
@@ -1078,16 +1100,13 @@ def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True,
     (or a pool [slots, D] with state_slots int32 [B]), updated in place by
     default.  Returns a dict with out [B, D] and final_state (in_place=False:
     a new tensor, of which only these sequences' entries are written)."""
-    import torch
-    B = int(x.shape[0])
-    with _on(stream):
-        if out is None:
-            out = torch.empty((B, rec.D), dtype=rec.dtype, device=x.device)
-        fs = state if in_place else torch.empty_like(state)
-        recur_decode_raw(rec, N=B, x=x, a=a, b=b, z=z, y=out, initial_state=state, final_state=fs,
-                         state_slots=state_slots,
-                         num_slots=0 if state_slots is None else int(state.shape[0]),
-                         stream=stream, status=status)
+    B, D, dev = x.shape[0], rec.D, _device()
+    if out is None:
+        out = _new(x, (B, D), rec.dtype, stream)
+    fs = state if in_place else _new(state, state.shape, state.dtype, stream)
+    io = _recur_io(rec, dev, B, 0, B, None, x, a, b, z, out, state, fs, state_slots,
+                   0 if state_slots is None else state.shape[0], None, status)
+    _check(lib().gdn_recur_decode(ctypes.byref(rec.c()), ctypes.byref(io), _raw_stream(stream, dev)))
     return {"out": out, "final_state": fs}
 
 
@@ -1121,34 +1140,36 @@ def linear(x, w, bias=None, act=GDN_ACT_NONE, residual=None, out=None, out_dtype
     import torch
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError(f"x and w: matrices needed, shapes are {tuple(x.shape)} and {tuple(w.shape)}")
+    dev = _device()
     M, K = x.shape
     N = w.shape[0]
     bf16 = torch.bfloat16
-    px, sx = _matrix(x, "x", M, K, bf16)
-    pw, sw = _matrix(w, "w", N, K, bf16)
+    px, sx = _matrix(x, "x", M, K, bf16, dev)
+    pw, sw = _matrix(w, "w", N, K, bf16, dev)
     if out is None:
         dt = out_dtype if out_dtype is not None else (bf16 if residual is None else residual.dtype)
         code = _float_code(dt, "out_dtype")
-        with _on(stream):
-            out = torch.empty((M, N), dtype=dt, device=x.device)
+        out = _new(x, (M, N), dt, stream)
         py, sy = out.data_ptr(), N
     else:
         dt = out.dtype
         if out_dtype is not None and out_dtype != dt:
             raise ValueError(f"out: {out_dtype} needed, not {dt}")
         code = _float_code(dt, "out")
-        py, sy = _matrix(out, "out", M, N, dt)
-    pr, sr = (None, 0) if residual is None else _matrix(residual, "residual", M, N, dt)
-    pp, sp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, bf16)
-    io = CLinearIO(M, N, K, px, sx, pw, sw, _dense(bias, "bias", N, None), int(act), pr, sr, py, code, sy,
-                   pp, sp)
-    if workspace is None and 16 < M <= 64:
+        py, sy = _matrix(out, "out", M, N, dt, dev)
+    pr, sr = (None, 0) if residual is None else _matrix(residual, "residual", M, N, dt, dev)
+    pp, sp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, bf16, dev)
+    io = CLinearIO(M, N, K, px, sx, pw, sw, _dense(bias, "bias", N, None, dev), act, pr, sr, py, code,
+                   sy, pp, sp)
+    ws, nb = None, 0
+    if workspace is not None:
+        ws, nb = _bytes(workspace, "workspace", dev)
+    elif 16 < M <= 64:
         nb = linear_workspace_bytes(M, N, K)
         if nb:
-            with _on(stream):
-                workspace = torch.empty(nb, dtype=torch.uint8, device=x.device)
-    ws, nb = _bytes(workspace, "workspace")
-    _check(lib().gdn_linear(ctypes.byref(io), ws, nb, _stream(stream)))
+            workspace = _new(x, (nb,), torch.uint8, stream)
+            ws = workspace.data_ptr()
+    _check(lib().gdn_linear(ctypes.byref(io), ws, nb, _raw_stream(stream, dev)))
     return out
 
 
@@ -1169,32 +1190,32 @@ def linear_backward(dy, x, w, preact=None, act=GDN_ACT_NONE, want_dx=True, want_
     import torch
     if dy.dim() != 2 or x.dim() != 2 or w.dim() != 2:
         raise ValueError("dy, x and w: matrices needed")
+    dev = _device()
     M, K = x.shape
     N = w.shape[0]
     bf16 = torch.bfloat16
-    pdy, sdy = _matrix(dy, "dy", M, N, dy.dtype)
+    pdy, sdy = _matrix(dy, "dy", M, N, dy.dtype, dev)
     code = _float_code(dy.dtype, "dy")
-    px, sx = _matrix(x, "x", M, K, bf16)
-    pw, sw = _matrix(w, "w", N, K, bf16)
+    px, sx = _matrix(x, "x", M, K, bf16, dev)
+    pw, sw = _matrix(w, "w", N, K, bf16, dev)
     if preact is None and act != GDN_ACT_NONE:
         raise ValueError("preact: needed with an activation")
-    pp, sp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, bf16)
+    pp, sp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, bf16, dev)
     res = {}
-    with _on(stream):
-        if want_dx or dx is not None:
-            res["dx"] = dx if dx is not None else torch.empty((M, K), dtype=bf16, device=x.device)
-        if want_dw or dw is not None:
-            res["dw"] = dw if dw is not None else torch.empty((N, K), dtype=bf16, device=x.device)
-        if want_dbias or dbias is not None:
-            res["dbias"] = dbias if dbias is not None else torch.empty(N, dtype=torch.float32, device=x.device)
-        if workspace is None:
-            workspace = torch.empty(linear_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=x.device)
-    pdx, sdx = _matrix(res["dx"], "dx", M, K, bf16) if "dx" in res else (None, 0)
-    pdw, sdw = _matrix(res["dw"], "dw", N, K, bf16) if "dw" in res else (None, 0)
-    gr = CLinearGrad(M, N, K, pdy, code, sdy, px, sx, pw, sw, pp, sp, int(act), pdx, sdx, pdw, sdw,
-                     _dense(res.get("dbias"), "dbias", N, None))
-    ws, nb = _bytes(workspace, "workspace")
-    _check(lib().gdn_linear_backward(ctypes.byref(gr), ws, nb, _stream(stream)))
+    if want_dx or dx is not None:
+        res["dx"] = dx if dx is not None else _new(x, (M, K), bf16, stream)
+    if want_dw or dw is not None:
+        res["dw"] = dw if dw is not None else _new(x, (N, K), bf16, stream)
+    if want_dbias or dbias is not None:
+        res["dbias"] = dbias if dbias is not None else _new(x, (N,), torch.float32, stream)
+    if workspace is None:
+        workspace = _new(x, (linear_backward_workspace_bytes(M, N, K),), torch.uint8, stream)
+    pdx, sdx = _matrix(res["dx"], "dx", M, K, bf16, dev) if "dx" in res else (None, 0)
+    pdw, sdw = _matrix(res["dw"], "dw", N, K, bf16, dev) if "dw" in res else (None, 0)
+    gr = CLinearGrad(M, N, K, pdy, code, sdy, px, sx, pw, sw, pp, sp, act, pdx, sdx, pdw, sdw,
+                     _dense(res.get("dbias"), "dbias", N, None, dev))
+    ws, nb = _bytes(workspace, "workspace", dev)
+    _check(lib().gdn_linear_backward(ctypes.byref(gr), ws, nb, _raw_stream(stream, dev)))
     return res
 
 
