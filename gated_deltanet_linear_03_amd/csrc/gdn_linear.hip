@@ -242,8 +242,8 @@ using LdsPtr = __attribute__((address_space(3))) void*;
 // 16 bytes from each lane's address into LDS at `lds` + 16 * lane, without the
 // compiler knowing that it writes LDS.  It takes every ds_read_b64_tr_b16 to
 // depend on all such loads in flight and waits for them, which undoes the
-// stages (a 2048 x 2048 x 2048 product in tiles of 128 x 128: 41 us instead of
-// 24); here the waits are this code's own.  A load has no register to write,
+// stages (dx of 2048 x 2048 x 2048 in tiles of 128 x 128: 41 us instead of
+// 23); here the waits are this code's own.  A load has no register to write,
 // reads its addresses when it is issued, and the memory clobber keeps LDS
 // accesses on their side of it; the s_nop covers an address register that a
 // vector instruction has just written.
@@ -255,7 +255,7 @@ __device__ __forceinline__ void load_to_lds(const void* p, uint32_t lds) {
 }
 
 // One operand's tile of R output rows x 32 of the reduction, in an LDS stage
-// of R * 32 bf16 that is filled by global_load_lds (a wave's 64 lanes x 16
+// of R * 32 bf16 that is filled by load_to_lds (a wave's 64 lanes x 16
 // bytes land in a row of 1 KiB; which 16 bytes a lane fetches is free, and
 // that is where the bank swizzle is done).
 //   KC (reduction contiguous): rows of 32 = four 16-byte chunks, chunk c of
@@ -315,19 +315,13 @@ struct Operand {
 
     // the next slice into a stage; left: how much of the reduction there still
     // is (FULL: a whole slice at least)
-    template <bool FULL, bool OWN>            // OWN: by load_to_lds
+    template <bool FULL>
     __device__ __forceinline__ void issue(uint16_t* lds, int wave, int64_t left) {
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-            uint16_t* const to = lds + (wave + u * NW) * 512;
-            if constexpr (OWN) {
-                const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LdsPtr)to));
-                if constexpr (FULL) load_to_lds(base, off[u], at);
-                else load_to_lds(k[u] < left ? static_cast<const void*>(base + off[u]) : zero_chunk, at);
-            } else {
-                const void* s = FULL || k[u] < left ? static_cast<const void*>(base + off[u]) : zero_chunk;
-                __builtin_amdgcn_global_load_lds(s, (LdsPtr)to, 16, 0, 0);
-            }
+            const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LdsPtr)(lds + (wave + u * NW) * 512)));
+            if constexpr (FULL) load_to_lds(base, off[u], to);
+            else load_to_lds(k[u] < left ? static_cast<const void*>(base + off[u]) : zero_chunk, to);
         }
         base += step;
     }
@@ -560,8 +554,8 @@ __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8
             const int64_t left = p.K - static_cast<int64_t>(kt + st + kAhead) * kTK;
 #pragma unroll
             for (int i = 0; i < H; ++i) fa[i] = a.frag(as + st * S::kA, H + i);
-            a.template issue<FULL, !(AK && BK)>(as + (st + kAhead) % kStages * S::kA, wave, left);
-            b.template issue<FULL, !(AK && BK)>(bs + (st + kAhead) % kStages * S::kB, wave, left);
+            a.template issue<FULL>(as + (st + kAhead) % kStages * S::kA, wave, left);
+            b.template issue<FULL>(bs + (st + kAhead) % kStages * S::kB, wave, left);
             wait_vm<(kStages - 2) * kPer>();  // slice kt + 1 has landed
             wave_barrier();
             __builtin_amdgcn_s_setprio(1);
@@ -577,8 +571,8 @@ __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8
 #pragma unroll
         for (int st = 0; st < kStages - 1; ++st) {
             const int64_t left = p.K - st * kTK;
-            a.template issue<false, !(AK && BK)>(as + st * S::kA, wave, left);
-            b.template issue<false, !(AK && BK)>(bs + st * S::kB, wave, left);
+            a.template issue<false>(as + st * S::kA, wave, left);
+            b.template issue<false>(bs + st * S::kB, wave, left);
         }
         wait_vm<(kStages - 2) * kPer>();      // slice 0
         wave_barrier();
@@ -640,8 +634,8 @@ __device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8
             const int64_t left = p.K - static_cast<int64_t>(kt + st + kStages) * kTK;
             wait_vm_lds<2 * kPer>();          // slice kt + 1 has landed, slice kt's fragments are in registers
             wave_barrier();
-            a.template issue<FULL, !(AK && BK)>(as + st * S::kA, wave, left);
-            b.template issue<FULL, !(AK && BK)>(bs + st * S::kB, wave, left);
+            a.template issue<FULL>(as + st * S::kA, wave, left);
+            b.template issue<FULL>(bs + st * S::kB, wave, left);
             fragments((st + 1) % kStages, (st + 1) % 2);
 #pragma unroll
             for (int i = 0; i < TM; ++i)
@@ -653,8 +647,8 @@ __device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8
 #pragma unroll
         for (int st = 0; st < kStages; ++st) {
             const int64_t left = p.K - st * kTK;
-            a.template issue<false, !(AK && BK)>(as + st * S::kA, wave, left);
-            b.template issue<false, !(AK && BK)>(bs + st * S::kB, wave, left);
+            a.template issue<false>(as + st * S::kA, wave, left);
+            b.template issue<false>(bs + st * S::kB, wave, left);
         }
         wait_vm_lds<3 * kPer>();              // slice 0
         wave_barrier();
