@@ -941,7 +941,7 @@ RecurWs recur_ws(const gdn_recur* R, int32_t N, int64_t T, bool backward) {
     RecurWs w;
     w.off_seq = round_up(4 * (static_cast<int64_t>(N) + 1), 256);
     w.off_tickets = round_up(w.off_seq + 4 * units, 256);
-    w.off_words = round_up(w.off_tickets + 4 * groups, 256);
+    w.off_words = round_up(w.off_tickets + 4 * groups * gdn::kRecurTicketPitch, 256);
     w.off_partial = round_up(w.off_words + 8 * tiles * groups * gdn::kRecurChannels, 256);
     w.total = w.off_partial + (backward ? 8 * tiles * groups * gdn::kRecurChannels : 0);
     return w;

@@ -175,6 +175,10 @@ hipError_t launch_gemm_bf16_nt(const void* A, int64_t lda, const void* B, int64_
 // ---- the diagonal gated recurrence (gdn_recur.hip) -----------------------
 constexpr int kRecurUnit = 128;          // rows (tokens) of one forward tile
 constexpr int kRecurSaved = 64;          // rows of a backward tile: a state is saved before each
+// A counter has a cache line of its own: next to each other, the counters of
+// 32 channel groups made a work-group of a 4096 x 2048 call wait 6.6 us for its
+// ticket, apart 2.
+constexpr int kRecurTicketPitch = 64;
 constexpr int kRecurChannels = 64;       // channels of a tile
 constexpr int kRecurWalkUnits = 4;       // calls of up to this many units of tokens: one work-group per sequence
 constexpr int kRecurWalkSeqs = 512;      // and up to this many sequences
@@ -206,7 +210,7 @@ struct RecurParams {
     int tiles;                           // bound on the number of tiles (units; backward: half units)
     int32_t* unit_off;                   // [N+1] first unit of each sequence; [N] < 0: the indices were rejected
     int32_t* unit_seq;                   // [units] sequence of each unit
-    uint32_t* tickets;                   // [groups] next tile of a channel group
+    uint32_t* tickets;                   // [groups][kRecurTicketPitch] next tile of a channel group
     uint64_t* words;                     // [tiles][groups * kRecurChannels]
     float2* partial;                     // [tiles][groups * kRecurChannels] sums for dA_log, ddt_bias, or NULL
 };

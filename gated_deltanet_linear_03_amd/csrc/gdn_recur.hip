@@ -154,6 +154,8 @@ struct Quad<true> {
         for (int j = 0; j < 4; ++j) e[j] = j < nv ? p[j] : 0u;
         return Quad{e[0] | (e[1] << 16), e[2] | (e[3] << 16)};
     }
+    // the value is what it was, but nothing computed from it before is kept for later
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(lo), "+v"(hi)); }
     __device__ __forceinline__ Quad dropped(int n) const {
         const uint64_t v = n < 4 ? ((static_cast<uint64_t>(hi) << 32) | lo) >> (16 * n) : 0ull;
         return Quad{static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32)};
@@ -192,6 +194,7 @@ struct Quad<false> {
         for (int j = 0; j < 4; ++j) q.e[j] = j < nv ? p[j] : 0.f;
         return q;
     }
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(e[0]), "+v"(e[1]), "+v"(e[2]), "+v"(e[3])); }
     __device__ __forceinline__ Quad dropped(int n) const {
         return n == 0 ? *this : n == 1 ? Quad{{e[1], e[2], e[3], 0.f}} : n == 2 ? Quad{{e[2], e[3], 0.f, 0.f}}
                       : n == 3 ? Quad{{e[3], 0.f, 0.f, 0.f}} : Quad{{0.f, 0.f, 0.f, 0.f}};
@@ -468,7 +471,7 @@ __device__ __forceinline__ Place unit_place(const RecurParams& p, int unit) {
 }
 
 __device__ __forceinline__ int draw_ticket(const RecurParams& p, int cg) {
-    return static_cast<int>(__hip_atomic_fetch_add(p.tickets + cg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    return static_cast<int>(__hip_atomic_fetch_add(p.tickets + cg * kRecurTicketPitch, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
 // grid: channel groups x the bound on units.  (Work-groups that stay and draw
@@ -571,24 +574,23 @@ __global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) 
     if (l.wave == 0 && p.hT && c < p.D) p.hT[at] = sh.start[l.lane];
 }
 
-// Block 0 checks the indices and lays out the units (unit_off, unit_seq);
-// the others, and block 0 after that, set the words to kEmpty and the
-// tickets to 0.
-constexpr int kPlanThreads = 1024;
+// Block 0 checks the indices, lays out the units (unit_off, unit_seq) and sets
+// the tickets to 0; the others set the words to kEmpty.
+constexpr int kPlanThreads = 256;
 
 __global__ __launch_bounds__(kPlanThreads) void recur_plan_kernel(RecurParams p) {
     const int tid = threadIdx.x;
     const int64_t nwords = static_cast<int64_t>(p.tiles) * p.groups * kCh;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kPlanThreads;
-    uint2* words = reinterpret_cast<uint2*>(p.words);
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; i < nwords; i += stride)
-        words[i] = make_uint2(kEmpty, kEmpty);
-    if (blockIdx.x != 0) return;
-    for (int i = tid; i < p.groups; i += kPlanThreads) p.tickets[i] = 0;
-    __shared__ int part[kPlanThreads];
-    __shared__ int bad;
-    if (tid == 0) bad = 0;
-    __syncthreads();
+    if (blockIdx.x != 0) {
+        const int64_t stride = static_cast<int64_t>(gridDim.x - 1) * kPlanThreads;
+        u32x4* pairs = reinterpret_cast<u32x4*>(p.words);              // (nwords is even)
+        for (int64_t i = static_cast<int64_t>(blockIdx.x - 1) * kPlanThreads + tid; i < nwords / 2; i += stride)
+            pairs[i] = u32x4{kEmpty, kEmpty, kEmpty, kEmpty};
+        return;
+    }
+    for (int i = tid; i < p.groups; i += kPlanThreads) p.tickets[i * kRecurTicketPitch] = 0;
+    __shared__ int part[kPlanThreads / kWave];
+    // each thread a run of sequences
     const int per = (p.N + kPlanThreads - 1) / kPlanThreads;
     const int n0 = tid * per < p.N ? tid * per : p.N, n1 = n0 + per < p.N ? n0 + per : p.N;
     int sum = 0, mine = 0;
@@ -598,58 +600,85 @@ __global__ __launch_bounds__(kPlanThreads) void recur_plan_kernel(RecurParams p)
         else sum += units_of(hi - lo);
         if (p.slots && (p.slots[n] < 0 || p.slots[n] >= p.num_slots)) mine = 1;
     }
-    if (mine) atomicOr(&bad, 1);
-    part[tid] = sum;
-    __syncthreads();
-    for (int d = 1; d < kPlanThreads; d *= 2) {   // inclusive sums
-        const int v = tid >= d ? part[tid - d] : 0;
-        __syncthreads();
-        part[tid] += v;
-        __syncthreads();
+    int upto = sum;                               // inclusive over the wave, then over the waves
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int v = __shfl_up(upto, d, kWave);
+        if (tid % kWave >= d) upto += v;
     }
+    if (tid % kWave == kWave - 1) part[tid / kWave] = upto;
+    const bool bad = __syncthreads_or(mine);
+    if (tid == 0 && p.status) *p.status = bad ? kStatusBadIndex : 0;
     if (bad) {
         if (tid == 0) p.unit_off[p.N] = -1;
-    } else {
-        int at = part[tid] - sum;
-        for (int n = n0; n < n1; ++n) {
-            p.unit_off[n] = at;
-            const int k = units_of(p.cu[n + 1] - p.cu[n]);
-            for (int i = 0; i < k; ++i) p.unit_seq[at + i] = n;
-            at += k;
-        }
-        if (tid == 0) p.unit_off[p.N] = part[kPlanThreads - 1];
+        return;
     }
-    if (tid == 0 && p.status) *p.status = bad ? kStatusBadIndex : 0;
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / kWave; ++w) {
+        if (w < tid / kWave) upto += part[w];
+        total += part[w];
+    }
+    int at = upto - sum;
+    for (int n = n0; n < n1; ++n) {
+        p.unit_off[n] = at;
+        const int k = units_of(p.cu[n + 1] - p.cu[n]);
+        if (p.N > kPlanThreads)                   // (few sequences: all threads together, below)
+            for (int i = 0; i < k; ++i) p.unit_seq[at + i] = n;
+        at += k;
+    }
+    if (tid == 0) p.unit_off[p.N] = total;
+    if (p.N > kPlanThreads) return;
+    __shared__ int first[kPlanThreads];
+    first[tid] = upto - sum;                      // (one sequence a thread)
+    __syncthreads();
+    for (int i = tid; i < total; i += kPlanThreads) {
+        int lo = 0, hi = p.N;                     // the last sequence that begins at or before unit i
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (first[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        p.unit_seq[i] = lo;
+    }
 }
 
 // ---- backward --------------------------------------------------------------
 struct BwdShared {
     float2 fwd[kWaves][kCh], rev[kWaves][kCh];
     float2 sums[kWaves][kCh];
+    float2 par[kCh];                              // nrate2, bias (kept here, not in registers, while the tile waits)
     float start[kCh];                             // c past the tile's last row
     int tile;
 };
 
 // A lane's rows of a backward tile: what the second half (after the tile's
-// start is known) needs of each element, computed once.
+// start is known) needs of each element.  Registers decide how many
+// work-groups share a compute unit, so what comes from z and dy, and what a's
+// gate gives beside alpha, is computed again from their packed rows.
 template <bool BF16, bool GATE>
 struct BwdTile {
     using Q = Quad<BF16>;
     using T = typename Q::T;
     static constexpr int L = kBwdRows;
-    Q x[L];
+    Q a[L], dy[L], z[L];
     float al[L][kVC], u[L][kVC];                  // alpha; u, later h before the row
-    float e[L][kVC], dz[L][kVC];                  // dy silu(z), dy silu'(z)
-    float wb[L][kVC], nb[L][kVC];                 // w beta, 1 - beta
-    float k[L][kVC];                              // alpha^2 / w^2 (0 where w is)
-    float sg[L][kVC], g2[L][kVC];                 // sigmoid(v), g log2(e)
+    float wb[L][kVC];                             // w beta
+    float xn[L][kVC], xk[L][kVC];                 // x (1 - beta), x alpha^2 / w^2 (0 where w is)
     float A[kVC], H[kVC], Ar[kVC], Hr[kVC];       // inclusive over the wave's groups, both ways
+
+    // dy silu(z)
+    __device__ __forceinline__ float into_h(int i, int j) const {
+        if constexpr (!GATE) return dy[i].get(j);
+        const float zj = z[i].get(j);
+        return dy[i].get(j) * (zj * sigmoid_fast(zj));
+    }
 
     template <bool WHOLE>
     __device__ __forceinline__ void load(const RecurParams& p, const Lane& l, int64_t row0, int rows, const float* nrate2,
                                          const float* bias) {
         const int r0 = l.rg * L;
-        Q a[L], b[L], z[L], dy[L];
+        Q x[L], b[L];
         auto fetch = [&](Q* to, const void* from, int64_t stride) {
             if constexpr (WHOLE) {
                 const T* base = static_cast<const T*>(from) + row0 * stride + (l.c - l.cl * kVC);
@@ -672,38 +701,30 @@ struct BwdTile {
         for (int i = 0; i < L; ++i) {
 #pragma unroll
             for (int j = 0; j < kVC; ++j) {
-                const float v = a[i].get(j) + bias[j];
+                const float v = a[i].get(j) + bias[j], xj = x[i].get(j);
                 const Gate g = gate(v, nrate2[j]);
-                const float r = __builtin_amdgcn_rcpf(1.f + g.e);
-                sg[i][j] = v < 0.f ? g.e * r : r;
-                g2[i][j] = g.g2;
-                // g -> 0: dx x alpha^2 / w^2 vanishes against sigmoid(v), which multiplies it
-                k[i][j] = g.q > 0.f ? g.alpha * g.alpha * __builtin_amdgcn_rcpf(g.q) : 0.f;
+                // g -> 0: alpha^2 / w^2 grows as sigmoid(v), which multiplies it, falls
+                xk[i][j] = g.q > 0.f ? xj * (g.alpha * g.alpha * __builtin_amdgcn_rcpf(g.q)) : 0.f;
                 const float beta = sigmoid_fast(b[i].get(j));
-                nb[i][j] = 1.f - beta;
+                xn[i][j] = xj * (1.f - beta);
                 wb[i][j] = __builtin_amdgcn_sqrtf(g.q) * beta;
                 al[i][j] = g.alpha;
-                u[i][j] = wb[i][j] * x[i].get(j);
-                e[i][j] = dy[i].get(j);
-                if constexpr (GATE) {
-                    const float zj = z[i].get(j), q = sigmoid_fast(zj);
-                    dz[i][j] = e[i][j] * (q * fmaf(zj, 1.f - q, 1.f));
-                    e[i][j] *= zj * q;
-                }
+                u[i][j] = wb[i][j] * xj;
                 if constexpr (!WHOLE) {
-                    if (r0 + i >= rows) { al[i][j] = 1.f; u[i][j] = 0.f; e[i][j] = 0.f; }
+                    if (r0 + i >= rows) { al[i][j] = 1.f; u[i][j] = 0.f; }
                 }
                 H[j] = i == 0 ? u[i][j] : fmaf(al[i][j], H[j], u[i][j]);
                 A[j] = i == 0 ? al[i][j] : A[j] * al[i][j];
             }
         }
-        // c_t = alpha_t (c_{t+1} + e_t)
+        // c_t = alpha_t (c_{t+1} + e_t); a row past the end hands c on
 #pragma unroll
         for (int j = 0; j < kVC; ++j) {
             Ar[j] = A[j];
-            Hr[j] = al[L - 1][j] * e[L - 1][j];
+            Hr[j] = 0.f;
 #pragma unroll
-            for (int i = L - 2; i >= 0; --i) Hr[j] = al[i][j] * (Hr[j] + e[i][j]);
+            for (int i = L - 1; i >= 0; --i)
+                if (WHOLE || r0 + i < rows) Hr[j] = al[i][j] * (Hr[j] + into_h(i, j));
         }
         wave_compose<false>(l, A, H);
         wave_compose<true>(l, Ar, Hr);
@@ -720,17 +741,24 @@ struct BwdTile {
         }
     }
 
-    // sa, sb: sums of dg g2 and of dg sigmoid(v) over the lane's rows
+    // sa, sb: sums of dg g2 and of da over the lane's rows
     template <bool WHOLE>
     __device__ __forceinline__ void finish(const RecurParams& p, const BwdShared& sh, const Lane& l, int64_t row0, int rows,
-                                           int64_t tile, const float* nrate2, float* sa, float* sb) {
-        float s[kVC], r[kVC], nrate[kVC];
+                                           int64_t tile, float* sa, float* sb) {
+        if constexpr (GATE) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) z[i].forget();
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) a[i].forget();
+        float s[kVC], r[kVC], nrate2[kVC], bias[kVC];
         const Quad<false> h = Quad<false>::load(p.saved + tile * p.D + l.c, l.nv);
 #pragma unroll
         for (int j = 0; j < kVC; ++j) {
+            nrate2[j] = sh.par[l.cl * kVC + j].x;
+            bias[j] = sh.par[l.cl * kVC + j].y;
             s[j] = h.get(j);
             r[j] = sh.start[l.cl * kVC + j];
-            nrate[j] = nrate2[j] * kLn2;
         }
         for (int w = 0; w < l.wave; ++w)
 #pragma unroll
@@ -762,7 +790,10 @@ struct BwdTile {
                 const float next = fmaf(al[i][j], s[j], u[i][j]);
                 u[i][j] = s[j];
                 s[j] = next;
-                if constexpr (GATE) o[j] = next * dz[i][j];
+                if constexpr (GATE) {
+                    const float zj = z[i].get(j), q = sigmoid_fast(zj);
+                    o[j] = next * (dy[i].get(j) * (q * fmaf(zj, 1.f - q, 1.f)));
+                }
             }
             if constexpr (GATE) put(p.dz, p.dzs, i, o);
         }
@@ -771,18 +802,20 @@ struct BwdTile {
             float dx[kVC], da[kVC], db[kVC];
 #pragma unroll
             for (int j = 0; j < kVC; ++j) {
-                const float G = e[i][j] + r[j];
+                const bool on = WHOLE || r0 + i < rows;
+                const float G = (on ? into_h(i, j) : 0.f) + r[j];
                 const float aG = al[i][j] * G;
                 r[j] = aG;
                 dx[j] = G * wb[i][j];
-                const float t = dx[j] * x[i].get(j);
-                db[j] = t * nb[i][j];
-                const float dg = fmaf(aG, u[i][j], -t * k[i][j]);
-                const float ds = dg * sg[i][j];
-                da[j] = ds * nrate[j];
-                if (WHOLE || r0 + i < rows) {
-                    sa[j] = fmaf(dg, g2[i][j], sa[j]);
-                    sb[j] += ds;
+                db[j] = dx[j] * xn[i][j];
+                const float dg = fmaf(aG, u[i][j], -dx[j] * xk[i][j]);
+                const float v = a[i].get(j) + bias[j];
+                const float ev = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v)), rv = __builtin_amdgcn_rcpf(1.f + ev);
+                const float g2 = nrate2[j] * fmaf(log1p_unit_over(ev), ev, fmaxf(v, 0.f));
+                da[j] = dg * ((v < 0.f ? ev * rv : rv) * (nrate2[j] * kLn2));
+                if (on) {
+                    sa[j] = fmaf(dg, g2, sa[j]);
+                    sb[j] += da[j];
                 }
             }
             put(p.dx, p.dxs, i, dx);
@@ -795,8 +828,11 @@ struct BwdTile {
 // grid: channel groups x kHalves x the bound on units; the tiles of a sequence
 // are taken from its end.  The rows' h are run again from the state the
 // forward pass saved at the tile's first row.
+// Three waves a SIMD where the registers allow it: with the gates' values kept
+// (228 registers, two waves) the 32768 x 4096 training step takes 1.12 ms,
+// with a's gate computed again 1.07; fp32 rows with a gate would spill.
 template <bool BF16, bool GATE>
-__global__ __launch_bounds__(kThreads, 2) void recur_backward_kernel(RecurParams p) {
+__global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backward_kernel(RecurParams p) {
     __shared__ BwdShared sh;
     const int total = kHalves * p.unit_off[p.N];
     const int cg = blockIdx.x % p.groups;
@@ -815,6 +851,10 @@ __global__ __launch_bounds__(kThreads, 2) void recur_backward_kernel(RecurParams
     const int64_t row0 = pl.row0 + t0;
     const bool whole = rows == kBwdTile && c0 + kCh <= p.D;
     BwdTile<BF16, GATE> t;
+    if (threadIdx.x < kChLanes) {
+#pragma unroll
+        for (int j = 0; j < kVC; ++j) sh.par[l.cl * kVC + j] = make_float2(nrate2[j], bias[j]);
+    }
     if (whole) t.template load<true>(p, l, row0, rows, nrate2, bias);
     else if (rows > 0) t.template load<false>(p, l, row0, rows, nrate2, bias);
     if (rows > 0) t.publish(sh, l);
@@ -841,8 +881,8 @@ __global__ __launch_bounds__(kThreads, 2) void recur_backward_kernel(RecurParams
     float sa[kVC], sb[kVC];
 #pragma unroll
     for (int j = 0; j < kVC; ++j) sa[j] = sb[j] = 0.f;
-    if (whole) t.template finish<true>(p, sh, l, row0, rows, tile, nrate2, sa, sb);
-    else if (rows > 0) t.template finish<false>(p, sh, l, row0, rows, tile, nrate2, sa, sb);
+    if (whole) t.template finish<true>(p, sh, l, row0, rows, tile, sa, sb);
+    else if (rows > 0) t.template finish<false>(p, sh, l, row0, rows, tile, sa, sb);
     if (!p.partial) return;
     // the tile's sums over its rows, in a fixed order
 #pragma unroll
@@ -895,7 +935,7 @@ __global__ __launch_bounds__(kSumThreads) void recur_sum_kernel(RecurParams p) {
             t.y += part[s][ch].y;
         }
         if (p.dA_log) p.dA_log[c] = t.x * kLn2;   // g = g2 ln 2
-        if (p.ddt_bias) p.ddt_bias[c] = -t.y * expf(p.A_log[c]);
+        if (p.ddt_bias) p.ddt_bias[c] = t.y;
     }
 }
 
@@ -969,8 +1009,8 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s) {
 
 static hipError_t launch_plan(const RecurParams& p, hipStream_t s) {
     const int64_t nwords = static_cast<int64_t>(p.tiles) * p.groups * kCh;
-    int64_t blocks = 1 + nwords / (kPlanThreads * 4);
-    if (blocks > 1024) blocks = 1024;
+    int64_t blocks = 2 + nwords / (kPlanThreads * 16);
+    if (blocks > 2048) blocks = 2048;
     hipLaunchKernelGGL(recur_plan_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kPlanThreads), 0, s, p);
     return hipGetLastError();
 }
