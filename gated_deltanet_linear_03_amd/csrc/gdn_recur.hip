@@ -277,6 +277,16 @@ __device__ __forceinline__ Place place_of(int lo, int len, int seq, int unit) {
     return pl;
 }
 
+// How much of a tile exists: all of it; all rows but not all channels (the
+// last group: still one load per four channels, from addresses moved back
+// into the row); or fewer rows, with every row's address clamped by itself.
+// 9001 rows of 1023 fp32 channels, rows 1023 apart, take 55 us with kEdge and
+// 66 us with the clamped form for the last group; 1024 channels take 47.
+enum Part { kWhole, kEdge, kSome };
+__device__ __forceinline__ Part part_of(bool rows, int c0, int D) {
+    return !rows || D < kVC ? kSome : c0 + kCh <= D ? kWhole : kEdge;
+}
+
 struct Lane {
     int wave, lane, cl, rg, nv;                   // cl: lane along the channels; rg: row group of the tile
     int c;                                        // first channel
@@ -354,20 +364,23 @@ struct FwdTile {
     Q z[kFwdRows];
     float A[kVC], H[kVC];                         // inclusive over the wave's groups
 
-    // Reads the tile's rows and composes them up to this lane.  WHOLE: every
-    // row and channel of the tile exists.  Otherwise rows past the unit's end
-    // read its last row and act as (A, H) = (1, 0).
-    template <bool WHOLE>
+    // Reads the tile's rows and composes them up to this lane.  Rows past the
+    // unit's end read its last row and act as (A, H) = (1, 0).
+    template <Part PART>
     __device__ __forceinline__ void load(const RecurParams& p, const Place& pl, const Lane& l, const float* nrate2,
                                          const float* bias) {
         const int r0 = l.rg * kFwdRows;
         Q x[kFwdRows], a[kFwdRows], b[kFwdRows];
         auto fetch = [&](Q* to, const void* from, int64_t stride) {
-            if constexpr (WHOLE) {
-                const T* base = static_cast<const T*>(from) + pl.row0 * stride + (l.c - l.cl * kVC);
-                const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + l.cl * kVC) * sizeof(T);
+            if constexpr (PART != kSome) {
+                const T* base = static_cast<const T*>(from) + pl.row0 * stride;
+                const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + (PART == kEdge ? l.lc : l.c)) * sizeof(T);
 #pragma unroll
                 for (int i = 0; i < kFwdRows; ++i) to[i] = Q::template load<!KEEP>(lane_ptr(base + i * stride, off));
+                if constexpr (PART == kEdge) {
+#pragma unroll
+                    for (int i = 0; i < kFwdRows; ++i) to[i] = to[i].dropped(l.drop);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < kFwdRows; ++i) {
@@ -387,7 +400,7 @@ struct FwdTile {
                 const Gate g = gate(a[i].get(j) + bias[j], nrate2[j]);
                 al[i][j] = g.alpha;
                 u[i][j] = __builtin_amdgcn_sqrtf(g.q) * sigmoid_fast(b[i].get(j)) * x[i].get(j);
-                if constexpr (!WHOLE) {
+                if constexpr (PART == kSome) {
                     if (r0 + i >= pl.rows) { al[i][j] = 1.f; u[i][j] = 0.f; }
                 }
                 H[j] = i == 0 ? u[i][j] : fmaf(al[i][j], H[j], u[i][j]);
@@ -405,7 +418,7 @@ struct FwdTile {
     }
 
     // The rows from the state before the tile (sh.start) to the outputs.
-    template <bool WHOLE>
+    template <Part PART>
     __device__ __forceinline__ void finish(const RecurParams& p, const FwdShared& sh, const Place& pl, const Lane& l,
                                            int64_t unit_index) {
         float s[kVC];
@@ -437,8 +450,8 @@ struct FwdTile {
                     o[j] *= zj * sigmoid_fast(zj);
                 }
             }
-            if constexpr (WHOLE) Q::store(lane_ptr(base + i * p.ys, off), o, kVC);
-            else if (r0 + i < pl.rows && l.nv > 0) Q::store(lane_ptr(base + i * p.ys, off), o, l.nv);
+            if constexpr (PART == kWhole) Q::store(lane_ptr(base + i * p.ys, off), o, kVC);
+            else if ((PART == kEdge || r0 + i < pl.rows) && l.nv > 0) Q::store(lane_ptr(base + i * p.ys, off), o, l.nv);
         }
     }
 };
@@ -492,9 +505,10 @@ __global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams 
     if (tile >= total) return;
     const Place pl = unit_place(p, tile);
     FwdTile<BF16, GATE, KEEP> t;
-    const bool whole = pl.rows == kRecurUnit && c0 + kCh <= p.D;
-    if (whole) t.template load<true>(p, pl, l, nrate2, bias);
-    else if (pl.rows > 0) t.template load<false>(p, pl, l, nrate2, bias);
+    const Part part = part_of(pl.rows == kRecurUnit, c0, p.D);
+    if (part == kWhole) t.template load<kWhole>(p, pl, l, nrate2, bias);
+    else if (part == kEdge) t.template load<kEdge>(p, pl, l, nrate2, bias);
+    else if (pl.rows > 0) t.template load<kSome>(p, pl, l, nrate2, bias);
     if (pl.rows > 0) t.publish(sh, l);
     __syncthreads();
     if (l.wave == 0) {
@@ -516,8 +530,8 @@ __global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams 
         sh.start[l.lane] = s;
     }
     __syncthreads();
-    if (whole) t.template finish<true>(p, sh, pl, l, tile);
-    else if (pl.rows > 0) t.template finish<false>(p, sh, pl, l, tile);
+    if (part == kWhole) t.template finish<kWhole>(p, sh, pl, l, tile);
+    else if (pl.rows > 0) t.template finish<kSome>(p, sh, pl, l, tile);
 }
 
 // One work-group per (channel group, sequence) walks the sequence's tiles in
@@ -556,13 +570,13 @@ __global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) 
     const int units = units_of(len);
     for (int k = 0; k < units && len > 0; ++k) {
         const Place pl = place_of(lo, len, seq, k);
-        const bool whole = pl.rows == kRecurUnit && c0 + kCh <= p.D;
-        if (whole) t.template load<true>(p, pl, l, nrate2, bias);
-        else t.template load<false>(p, pl, l, nrate2, bias);
+        const bool whole = part_of(pl.rows == kRecurUnit, c0, p.D) == kWhole;
+        if (whole) t.template load<kWhole>(p, pl, l, nrate2, bias);
+        else t.template load<kSome>(p, pl, l, nrate2, bias);
         t.publish(sh, l);
         __syncthreads();
-        if (whole) t.template finish<true>(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
-        else t.template finish<false>(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
+        if (whole) t.template finish<kWhole>(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
+        else t.template finish<kSome>(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
         float after = 0.f;
         if (l.wave == 0) {
             const float2 e = tile_step(sh.step, l.lane, false);
@@ -674,17 +688,21 @@ struct BwdTile {
         return dy[i].get(j) * (zj * sigmoid_fast(zj));
     }
 
-    template <bool WHOLE>
+    template <Part PART>
     __device__ __forceinline__ void load(const RecurParams& p, const Lane& l, int64_t row0, int rows, const float* nrate2,
                                          const float* bias) {
         const int r0 = l.rg * L;
         Q x[L], b[L];
         auto fetch = [&](Q* to, const void* from, int64_t stride) {
-            if constexpr (WHOLE) {
-                const T* base = static_cast<const T*>(from) + row0 * stride + (l.c - l.cl * kVC);
-                const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + l.cl * kVC) * sizeof(T);
+            if constexpr (PART != kSome) {
+                const T* base = static_cast<const T*>(from) + row0 * stride;
+                const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + (PART == kEdge ? l.lc : l.c)) * sizeof(T);
 #pragma unroll
                 for (int i = 0; i < L; ++i) to[i] = Q::template load<true>(lane_ptr(base + i * stride, off));
+                if constexpr (PART == kEdge) {
+#pragma unroll
+                    for (int i = 0; i < L; ++i) to[i] = to[i].dropped(l.drop);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < L; ++i)
@@ -710,7 +728,7 @@ struct BwdTile {
                 wb[i][j] = __builtin_amdgcn_sqrtf(g.q) * beta;
                 al[i][j] = g.alpha;
                 u[i][j] = wb[i][j] * xj;
-                if constexpr (!WHOLE) {
+                if constexpr (PART == kSome) {
                     if (r0 + i >= rows) { al[i][j] = 1.f; u[i][j] = 0.f; }
                 }
                 H[j] = i == 0 ? u[i][j] : fmaf(al[i][j], H[j], u[i][j]);
@@ -724,7 +742,7 @@ struct BwdTile {
             Hr[j] = 0.f;
 #pragma unroll
             for (int i = L - 1; i >= 0; --i)
-                if (WHOLE || r0 + i < rows) Hr[j] = al[i][j] * (Hr[j] + into_h(i, j));
+                if (PART != kSome || r0 + i < rows) Hr[j] = al[i][j] * (Hr[j] + into_h(i, j));
         }
         wave_compose<false>(l, A, H);
         wave_compose<true>(l, Ar, Hr);
@@ -742,7 +760,7 @@ struct BwdTile {
     }
 
     // sa, sb: sums of dg g2 and of da over the lane's rows
-    template <bool WHOLE>
+    template <Part PART>
     __device__ __forceinline__ void finish(const RecurParams& p, const BwdShared& sh, const Lane& l, int64_t row0, int rows,
                                            int64_t tile, float* sa, float* sb) {
         if constexpr (GATE) {
@@ -779,7 +797,7 @@ struct BwdTile {
         auto put = [&](void* to, int64_t stride, int i, const float* f) {
             T* base = static_cast<T*>(to) + row0 * stride + (l.c - l.cl * kVC);
             const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(stride) + l.cl * kVC) * sizeof(T);
-            if constexpr (WHOLE) Q::store(lane_ptr(base + i * stride, off), f, kVC);
+            if constexpr (PART == kWhole) Q::store(lane_ptr(base + i * stride, off), f, kVC);
             else if (r0 + i < rows && l.nv > 0) Q::store(lane_ptr(base + i * stride, off), f, l.nv);
         };
 #pragma unroll
@@ -802,7 +820,7 @@ struct BwdTile {
             float dx[kVC], da[kVC], db[kVC];
 #pragma unroll
             for (int j = 0; j < kVC; ++j) {
-                const bool on = WHOLE || r0 + i < rows;
+                const bool on = PART == kWhole || r0 + i < rows;
                 const float G = (on ? into_h(i, j) : 0.f) + r[j];
                 const float aG = al[i][j] * G;
                 r[j] = aG;
@@ -849,14 +867,15 @@ __global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backwar
     const int left = pl.rows - t0;
     const int rows = left < 0 ? 0 : (left < kBwdTile ? left : kBwdTile);
     const int64_t row0 = pl.row0 + t0;
-    const bool whole = rows == kBwdTile && c0 + kCh <= p.D;
+    const Part part = part_of(rows == kBwdTile, c0, p.D);
     BwdTile<BF16, GATE> t;
     if (threadIdx.x < kChLanes) {
 #pragma unroll
         for (int j = 0; j < kVC; ++j) sh.par[l.cl * kVC + j] = make_float2(nrate2[j], bias[j]);
     }
-    if (whole) t.template load<true>(p, l, row0, rows, nrate2, bias);
-    else if (rows > 0) t.template load<false>(p, l, row0, rows, nrate2, bias);
+    if (part == kWhole) t.template load<kWhole>(p, l, row0, rows, nrate2, bias);
+    else if (part == kEdge) t.template load<kEdge>(p, l, row0, rows, nrate2, bias);
+    else if (rows > 0) t.template load<kSome>(p, l, row0, rows, nrate2, bias);
     if (rows > 0) t.publish(sh, l);
     __syncthreads();
     if (l.wave == 0) {
@@ -881,8 +900,8 @@ __global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backwar
     float sa[kVC], sb[kVC];
 #pragma unroll
     for (int j = 0; j < kVC; ++j) sa[j] = sb[j] = 0.f;
-    if (whole) t.template finish<true>(p, sh, l, row0, rows, tile, sa, sb);
-    else if (rows > 0) t.template finish<false>(p, sh, l, row0, rows, tile, sa, sb);
+    if (part == kWhole) t.template finish<kWhole>(p, sh, l, row0, rows, tile, sa, sb);
+    else if (rows > 0) t.template finish<kSome>(p, sh, l, row0, rows, tile, sa, sb);
     if (!p.partial) return;
     // the tile's sums over its rows, in a fixed order
 #pragma unroll
