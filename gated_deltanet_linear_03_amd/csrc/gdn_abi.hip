@@ -1059,6 +1059,13 @@ gdn_status recur_workspace(const RecurWs& w, void* ws, size_t ws_bytes, gdn::Rec
     return GDN_OK;
 }
 
+// What a call without sequences has to write
+gdn_status recur_status_clear(const gdn_recur_io* io, void* stream) {
+    hipError_t e = gdn::launch_fill_zero(reinterpret_cast<float*>(io->status), 1, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "fill launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
 }  // namespace
 
 size_t gdn_recur_saved_bytes(const gdn_recur* R, int32_t N, int64_t T) {
@@ -1110,7 +1117,7 @@ gdn_status gdn_recur_forward(const gdn_recur* R, const gdn_recur_io* io, void* w
             return fail(GDN_ERR_INVALID_ARGUMENT, "workspace overlaps an output or a state");
     }
     p.partial = nullptr;
-    if (io->N == 0) return GDN_OK;
+    if (io->N == 0) return recur_status_clear(io, stream);
     hipError_t e = gdn::launch_recur_forward(p, R->act_dtype == GDN_DTYPE_BF16, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(GDN_ERR_HIP, "recurrence launch failed: %s", hipGetErrorString(e));
     return GDN_OK;
@@ -1183,11 +1190,16 @@ gdn_status gdn_recur_backward(const gdn_recur* R, const gdn_recur_io* io, const 
     if (overlaps(gr->d_initial_state, ns, io->saved, nsv) || overlaps(gr->d_initial_state, ns, ws, nw) ||
         overlaps(ws, nw, io->saved, nsv) || overlaps(ws, nw, gr->d_final_state, ns))
         return fail(GDN_ERR_INVALID_ARGUMENT, "workspace, saved and state gradients must not overlap");
+    if (overlaps(gr->dA_log, 4 * D, gr->ddt_bias, 4 * D) || overlaps(gr->dA_log, 4 * D, gr->d_initial_state, ns) ||
+        overlaps(gr->ddt_bias, 4 * D, gr->d_initial_state, ns) || overlaps(gr->dA_log, 4 * D, ws, nw) ||
+        overlaps(gr->ddt_bias, 4 * D, ws, nw))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "dA_log and ddt_bias must not overlap each other or another output");
     if (io->N > 0 && (st = recur_workspace(w, ws, ws_bytes, &p, kHalves * units)) != GDN_OK) return st;
     if (!gr->dA_log && !gr->ddt_bias) p.partial = nullptr;
     if (io->N == 0) {
         // no tokens: the parameters' gradients are zero
         hipStream_t s = static_cast<hipStream_t>(stream);
+        if ((st = recur_status_clear(io, stream)) != GDN_OK) return st;
         hipError_t e = gdn::launch_fill_zero(gr->dA_log, D, s);
         if (e == hipSuccess) e = gdn::launch_fill_zero(gr->ddt_bias, D, s);
         if (e != hipSuccess) return fail(GDN_ERR_HIP, "fill launch failed: %s", hipGetErrorString(e));
@@ -1230,10 +1242,11 @@ gdn_status check_dims(int64_t M, int64_t N, int64_t K) {
                     static_cast<long long>(N), static_cast<long long>(K));
     if (K % 8 || K > kMaxStride)
         return fail(GDN_ERR_INVALID_ARGUMENT, "K (%lld) must be a multiple of 8 up to 2^22", static_cast<long long>(K));
-    // one work-group per 64 x 64 tile of an output at the least
+    // a work-group for each 64 x 64 tile of an output at the most (dp's blocks
+    // of 32 x 256 are fewer)
     const int64_t tiles = lim / 2;
     auto count = [](int64_t r, int64_t c) { return ((r + 63) / 64) * ((c + 63) / 64); };
-    if (count(M, N) >= tiles || count(M, K) + count(N, K) >= tiles || (M / 64 + 1) * (N / 256 + 1) >= tiles)
+    if (count(M, N) >= tiles || count(M, K) + count(N, K) >= tiles)
         return fail(GDN_ERR_INVALID_ARGUMENT, "output too large");
     return GDN_OK;
 }

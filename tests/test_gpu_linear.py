@@ -298,6 +298,46 @@ def test_graph_replays_and_other_stream():
     assert torch.equal(got, want)
 
 
+def test_rows_past_4_gib():
+    """Operands and outputs whose rows lie 131072 elements apart, over 5 GiB:
+    the same bits as dense ones."""
+    M, N, K, ld = 20500, 72, 136, 131072
+    g, x, w = data(M, N, K, 12)
+    dy = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+    y = gdn.linear(x, w, residual=dy)
+    ref = gdn.linear_backward(dy, x, w, want_dbias=True)
+    wide = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    assert wide.numel() * 2 > 5 * 2 ** 30
+    wx, wdy = wide[:, :K], wide[:, 200:200 + N]
+    wx.copy_(x)
+    wdy.copy_(dy)
+    out = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    wy, wdx = out[:, 8:8 + N], out[:, 100:100 + K]
+    assert torch.equal(gdn.linear(wx, w, residual=wdy, out=wy), y)
+    r = gdn.linear_backward(wdy, wx, w, dx=wdx, want_dbias=True)
+    for n in ref:
+        assert torch.equal(r[n], ref[n]), n
+    # few rows of a w with as wide rows
+    ww = wide[:, :K]
+    for m in (3, 40):
+        assert torch.equal(gdn.linear(x[:m], ww), gdn.linear(x[:m], ww.contiguous())), m
+
+
+def test_two_calls_at_once():
+    g, x, w = data(2000, 1032, 2056, 13)
+    dy = torch.randn((2000, 1032), generator=g, device="cuda").to(torch.bfloat16)
+    calls = [lambda **k: [gdn.linear(x, w, **k), gdn.linear(x[:50], w, **k), gdn.linear(x[:9], w, **k)],
+             lambda **k: list(gdn.linear_backward(dy, x, w, want_dbias=True, **k).values())]
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[c(stream=s) for c, s in zip(calls, streams)] for _ in range(6)]
+    torch.cuda.synchronize()
+    for r in got:
+        for a, b in zip(want, r):
+            assert len(a) == len(b) and all(torch.equal(u, v) for u, v in zip(a, b))
+
+
 def test_binding_refusals():
     g, x, w = data(80, 40, 64, 11)
     with pytest.raises(ValueError, match="bfloat16 needed"):

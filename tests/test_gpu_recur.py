@@ -383,6 +383,74 @@ def test_graph_replays_and_other_stream():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("lens", [[1, 0] * 256, [1] * 513, [3, 130, 0] * 100, [2, 0, 257] * 250], ids=["512", "513", "300", "750"])
+def test_many_sequences(lens):
+    """On both sides of the counts at which the layout of the units changes."""
+    c = Case(lens, 20, "bf16", seed=21)
+    f = c.forward(want_saved=True)
+    g = c.backward(f["saved"])
+    val, err = c.reference()
+    check("y", f["out"], val["y"], err["y"], HALF["bf16"])
+    check("final_state", f["final_state"], val["final"], err["final"], HALF["fp32"])
+    for n in ("dx", "da", "db", "dz"):
+        check(n, g[n], val[n], err[n], HALF["bf16"])
+    for n, v in (("d_initial_state", "d_initial"), ("dA_log", "dA_log"), ("ddt_bias", "ddt_bias")):
+        check(n, g[n], val[v], err[v], HALF["fp32"])
+
+
+def test_rows_past_4_gib():
+    """Rows 131072 elements apart, 5 GiB of them: the same bits as dense rows."""
+    T, D, ld = 20500, 70, 131072
+    c = Case([T - 700, 700], D, "bf16", seed=22, packed=False)
+    ref = c.forward(want_saved=True)
+    gref = c.backward(ref["saved"])
+    wide = torch.empty((T, ld), dtype=torch.bfloat16, device="cuda")
+    assert wide.numel() * 2 > 5 * 2 ** 30
+    at = {n: wide[:, 96 * i:96 * i + D] for i, n in enumerate(("x", "a", "b", "z", "y", "dy"))}
+    for n in ("x", "a", "b", "z", "dy"):
+        at[n].copy_(c.t[n])
+    r = gdn.recur_forward(c.rec, *(at[n] for n in "xabz"), c.cu, initial_state=c.dh0, want_saved=True, out=at["y"])
+    assert torch.equal(at["y"], ref["out"]) and torch.equal(r["final_state"], ref["final_state"])
+    grad = torch.empty((T, ld), dtype=torch.bfloat16, device="cuda")
+    out = {n: grad[:, 96 * i:96 * i + D] for i, n in enumerate(("dx", "da", "db", "dz"))}
+    ws = torch.empty(gdn.recur_backward_workspace_bytes(c.rec, c.N, T), dtype=torch.uint8, device="cuda")
+    gdn.recur_backward_raw(c.rec, N=c.N, T_total=T, cu_seqlens=c.cu, dy=at["dy"], saved=r["saved"], workspace=ws,
+                           d_final_state=c.ddhT, **{n: at[n] for n in "xabz"}, **out)
+    for n, v in out.items():
+        assert torch.equal(v, gref[n]), n
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own buffers and workspace, both long enough
+    to share the device: the bits of either alone."""
+    cs = [Case([30000], 512, "bf16", seed=23, packed=False), Case([9000, 0, 11000], 512, "bf16", seed=24, packed=False)]
+    want = [(f := c.forward(want_saved=True)) | c.backward(f["saved"]) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for k, c in enumerate(cs):
+            f = c.forward(want_saved=True, stream=streams[k])
+            got[k].append(f | c.backward(f["saved"], stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for r in got[k]:
+            for n in want[k]:
+                if n != "saved":
+                    assert torch.equal(r[n], want[k][n]), (k, n)
+
+
+def test_no_sequences():
+    c = Case([5], 8, "bf16", seed=25)
+    none = {n: c.t[n][:0] for n in "xabz"}
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    st = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    f = gdn.recur_forward(c.rec, *none.values(), cu, want_saved=True, status=st)
+    assert st.item() == 0 and f["out"].shape == (0, 8)
+    g = gdn.recur_backward(c.rec, *none.values(), c.t["dy"][:0], f["saved"], cu)
+    assert (g["dA_log"] == 0).all() and (g["ddt_bias"] == 0).all()
+
+
 def test_binding_refusals():
     c = Case([20], 16, "bf16", seed=1)
     t = c.t

@@ -127,6 +127,7 @@ def _grad(**kw):
     (dict(d_final_state=FAKE + 15 * FAR + 4), {}, "partially overlaps"),
     ({}, dict(saved=None), "saved"), (dict(dx=FAKE + 16 * FAR), {}, "another buffer"),
     (dict(d_initial_state=WS), {}, "must not overlap"),
+    (dict(dA_log=FAKE + 14 * FAR), {}, "dA_log and ddt_bias"), (dict(ddt_bias=WS), {}, "dA_log and ddt_bias"),
 ])
 def test_backward_refuses(change, io, word):
     io = _io(**dict(dict(saved=FAKE + 16 * FAR), **io))
