@@ -14,6 +14,8 @@
 // Few rows: the product is a stream over w, and bound by HBM.  Up to 16 rows
 // each work-group takes 16 columns with K split over its waves; up to 64 rows
 // K is split over work-groups of 64 columns, whose sums a second kernel adds.
+#include <cmath>
+
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -681,13 +683,22 @@ __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void linear_forward_kerne
     gemm_tile<true, true, false, S>(p, blockIdx.x, shared);
 }
 
-// dx (first `first` work-groups) and dw (the rest) in one launch: each alone
-// often has fewer tiles than the card has compute units.
+// dx and dw in one launch: each alone often has fewer tiles than the card has
+// compute units.  The product with the longer reduction takes the first
+// work-groups, so that its tiles are not the last ones running.
+// tx, tw: tiles (or tiles in parts) of dx and dw.
+__device__ __forceinline__ bool is_dx(int tx, int tw, bool dw_leads, int* tile) {
+    const int b = blockIdx.x, first = dw_leads ? tw : tx;
+    *tile = b < first ? b : b - first;
+    return (b < first) != dw_leads;
+}
+
 template <typename S>
-__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void linear_backward_kernel(GemmProduct dx, GemmProduct dw, int first) {
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void linear_backward_kernel(GemmProduct dx, GemmProduct dw, int tx, int tw) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
-    if (static_cast<int>(blockIdx.x) < first) gemm_tile<true, false, true, S>(dx, blockIdx.x, shared);
-    else gemm_tile<false, false, true, S>(dw, blockIdx.x - first, shared);
+    int tile;
+    if (is_dx(tx, tw, dw.K > dx.K, &tile)) gemm_tile<true, false, true, S>(dx, tile, shared);
+    else gemm_tile<false, false, true, S>(dw, tile, shared);
 }
 
 // ---- the reduction in parts ------------------------------------------------------
@@ -720,12 +731,13 @@ __global__ __launch_bounds__(Small::kThreads, Small::kPerSimd) void linear_part_
     gemm_part<true, true>(p, blockIdx.x, sums, parts, shared);
 }
 
-// dx (the first `first` work-groups) and dw in parts
+// dx and dw in parts
 __global__ __launch_bounds__(Small::kThreads, Small::kPerSimd) void linear_backward_part_kernel(
-        GemmProduct dx, GemmProduct dw, float* sx, float* sw, int px, int pw, int first) {
+        GemmProduct dx, GemmProduct dw, float* sx, float* sw, int px, int pw, int tx, int tw) {
     __shared__ __align__(1024) uint8_t shared[Small::kBytes];
-    if (static_cast<int>(blockIdx.x) < first) gemm_part<true, false>(dx, blockIdx.x, sx, px, shared);
-    else gemm_part<false, false>(dw, blockIdx.x - first, sw, pw, shared);
+    int tile;
+    if (is_dx(tx, tw, part_share(dw.K, pw) > part_share(dx.K, px), &tile)) gemm_part<true, false>(dx, tile, sx, px, shared);
+    else gemm_part<false, false>(dw, tile, sw, pw, shared);
 }
 
 // four columns a thread
@@ -932,7 +944,7 @@ template <typename S>
 hipError_t backward_t(const GemmProduct& dx, const GemmProduct& dw, hipStream_t s) {
     const int64_t t1 = dx.ep.y ? tiles<S>(dx) : 0, t2 = dw.ep.y ? tiles<S>(dw) : 0;
     hipLaunchKernelGGL((linear_backward_kernel<S>), dim3(static_cast<unsigned>(t1 + t2)), dim3(S::kThreads), 0, s, dx, dw,
-                       static_cast<int>(t1));
+                       static_cast<int>(t1), static_cast<int>(t2));
     return hipGetLastError();
 }
 
@@ -951,13 +963,10 @@ struct Choice {
     double us;
 };
 
-static Choice choose(const GemmProduct* a, const GemmProduct* b, int cus) {
+static Choice choose(const GemmProduct& p, int cus) {
     auto us = [&](int64_t n, double each) { return static_cast<double>((n + cus - 1) / cus) * each; };
-    auto count = [&](auto f) { return (a ? f(*a) : 0) + (b ? f(*b) : 0); };
-    const Choice all[4] = {{kLarge, us(count([](const GemmProduct& p) { return tiles<Large>(p); }), 47.0)},
-                           {kWide, us(count([](const GemmProduct& p) { return tiles<Wide>(p); }), 30.0)},
-                           {kMedium, us(count([](const GemmProduct& p) { return tiles<Medium>(p); }), 21.0)},
-                           {kSmall, us(count([](const GemmProduct& p) { return tiles<Small>(p); }), 8.5)}};
+    const Choice all[4] = {{kLarge, us(tiles<Large>(p), 47.0)}, {kWide, us(tiles<Wide>(p), 30.0)},
+                           {kMedium, us(tiles<Medium>(p), 21.0)}, {kSmall, us(tiles<Small>(p), 8.5)}};
     Choice best = all[0];
     for (int i = 1; i < 4; ++i)
         if (all[i].us < best.us) best = all[i];
@@ -986,16 +995,14 @@ static GemmProduct columns(const GemmProduct& p, int64_t n0, int64_t n) {
     return c;
 }
 
-// Parts of a reduction of K for `tiles` tiles of 64 x 64: as many as fill
-// the compute units twice, of 256 at least.
-static int parts_for(int64_t tiles, int64_t K, int cus) {
-    const int64_t want = (2 * cus + tiles - 1) / tiles, most = K / 256;
+// Parts of 17 to 64 rows' reduction: as many as there are compute units for
+// each tile of 64 columns, of 256 at least.  64 x 2048 x 4096: 17.0 us with
+// 16 parts, 13.2 with 8, 14.6 with 4; 64 x 12352 x 2048: 20.3 with 1, 22.6 with 2.
+int linear_parts(int64_t M, int64_t N, int64_t K) {
+    if (M <= kLinearStreamRows || M > kLinearFewRows || N <= 0) return 1;
+    const int64_t want = compute_units() / ((N + 63) / 64), most = K / 256;
     const int64_t n = want < most ? want : most;
     return n < 1 ? 1 : static_cast<int>(n > 64 ? 64 : n);
-}
-
-int linear_parts(int64_t M, int64_t N, int64_t K) {
-    return M > kLinearStreamRows && M <= kLinearFewRows ? parts_for((N + 63) / 64, K, compute_units()) : 1;
 }
 
 static int64_t join_blocks(const GemmProduct& p) { return (p.M * ((p.N + 3) / 4) + kJoinThreads - 1) / kJoinThreads; }
@@ -1023,11 +1030,11 @@ hipError_t launch_linear(const GemmProduct& given, float* sums, hipStream_t s) {
     // instead of three): then the rest goes by itself in smaller tiles.  A
     // column's sum runs in the same order either way.
     const int cus = compute_units();
-    const Choice whole = choose(&p, nullptr, cus);
+    const Choice whole = choose(p, cus);
     const int64_t rest = p.N % 256, main = p.N - rest;
     if (rest > 0 && main > 0) {
         const GemmProduct m = columns(p, 0, main), r = columns(p, main, rest);
-        const Choice cm = choose(&m, nullptr, cus), cr = choose(&r, nullptr, cus);
+        const Choice cm = choose(m, cus), cr = choose(r, cus);
         if (cm.us + cr.us + 3.0 < whole.us) {     // 3: the second launch
             const hipError_t e = forward(m, cm.tiles, s);
             return e != hipSuccess ? e : forward(r, cr.tiles, s);
@@ -1038,16 +1045,57 @@ hipError_t launch_linear(const GemmProduct& given, float* sums, hipStream_t s) {
 
 int64_t linear_dp_blocks(int64_t M) { return (M + kDpRows - 1) / kDpRows; }
 
-// Parts of dx's and dw's reductions
-void linear_backward_parts(int64_t M, int64_t N, int64_t K, int* dx, int* dw) {
+// How the backward products run: dx (reduction N) and dw (reduction M) share
+// a launch, so their tiles' times are weighed by their reductions: the work
+// over the compute units in rounds of the shorter reduction, and no less than
+// one tile of the longer one takes by itself (a 64 x 64 tile alone: 11 us at
+// 2048).  Reductions may be cut into parts, which costs the sums' way through
+// memory and a launch.  Measured, in the order 256 x 256, 256 x 128, 128 x
+// 128, 64 x 64, and the best number of parts' time:
+//    700 x 8192 x  256: 126,  91,  65,  38 us, 24 in parts of 2048
+//   8192 x  512 x  512: 126,  84,  62,  44 us, 33 in parts of 2048
+//   4096 x 1000 x  512:  67,  45,  33,  27 us, 29 in parts of 2048
+//   2048 x 2048 x 2048:  42,  33,  36,  55 us, 77 in parts of 1024
+//   4096 x 4096 x 2048:  96, 124, 131, 224 us, 243 in parts of 2048
+struct BackwardPlan {
+    Tiles tiles;
+    int px, pw;                                   // parts of dx's and dw's reductions (1, 1: no sums)
+};
+
+static BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K) {
     const int cus = compute_units();
-    const int64_t tx = ((M + 63) / 64) * ((K + 63) / 64), tw = ((N + 63) / 64) * ((K + 63) / 64);
-    *dx = *dw = 1;
-    // (from as many small tiles as compute units on, larger tiles take over)
-    if (tx > 0 && tw > 0 && tx + tw < cus) {
-        *dx = parts_for(tx + tw, N, cus);
-        *dw = parts_for(tx + tw, M, cus);
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    auto us = [&](int bm, int bn, double each, double alone, int px, int pw) {
+        const int64_t tx = up(M, bm) * up(K, bn) * px, tw = up(N, bm) * up(K, bn) * pw;
+        const double lx = static_cast<double>(up(N, px)), lw = static_cast<double>(up(M, pw));
+        const double least = lx < lw ? lx : lw, most = lx < lw ? lw : lx;
+        if (least <= 0 || tx + tw > (int64_t(1) << 30)) return px * pw > 1 ? 1e30 : 0.0;
+        const double work = std::ceil((tx * lx + tw * lw) / (cus * least)) * least * each;
+        return (work > most * alone ? work : most * alone) / 2048;
+    };
+    BackwardPlan best{kLarge, 1, 1};
+    double least = us(256, 256, 47, 47, 1, 1);
+    auto offer = [&](double t, BackwardPlan p) {
+        if (t < least) { least = t; best = p; }
+    };
+    offer(us(256, 128, 30, 30, 1, 1), {kWide, 1, 1});
+    offer(us(128, 128, 21, 21, 1, 1), {kMedium, 1, 1});
+    offer(us(64, 64, 8.5, 11, 1, 1), {kSmall, 1, 1});
+    for (int len = 256; len <= (1 << 20); len *= 2) {
+        const int px = N > len ? static_cast<int>(up(N, len)) : 1, pw = M > len ? static_cast<int>(up(M, len)) : 1;
+        if (px == 1 && pw == 1) break;
+        if (px > 64 || pw > 64) continue;         // (the sums are joined one after the other)
+        const double sums = 8.0 * static_cast<double>(K) * (static_cast<double>(px) * M + static_cast<double>(pw) * N);
+        offer(us(64, 64, 8.5, 11, px, pw) + 5 + sums / 3e6, {kSmall, px, pw});
     }
+    return best;
+}
+
+// (the sums' places: no sums where no reduction is cut)
+void linear_backward_parts(int64_t M, int64_t N, int64_t K, int* dx, int* dw) {
+    const BackwardPlan b = backward_plan(M, N, K);
+    *dx = b.px;
+    *dw = b.pw;
 }
 
 hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias, float* sums_dx,
@@ -1067,12 +1115,12 @@ hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, con
         if (e != hipSuccess) return e;
     }
     if (!dx.ep.y && !dw.ep.y) return hipSuccess;
-    int px = 1, pw = 1;
-    linear_backward_parts(dp.M, dp.N, dx.N, &px, &pw);
+    const BackwardPlan plan = backward_plan(dp.M, dp.N, dx.N);
+    const int px = plan.px, pw = plan.pw;
     if (px > 1 || pw > 1) {
         const int64_t t1 = dx.ep.y ? tiles<Small>(dx) * px : 0, t2 = dw.ep.y ? tiles<Small>(dw) * pw : 0;
         hipLaunchKernelGGL(linear_backward_part_kernel, dim3(static_cast<unsigned>(t1 + t2)), dim3(Small::kThreads), 0, s, dx, dw,
-                           sums_dx, sums_dw, px, pw, static_cast<int>(t1));
+                           sums_dx, sums_dw, px, pw, static_cast<int>(t1), static_cast<int>(t2));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int64_t b1 = dx.ep.y ? join_blocks(dx) : 0, b2 = dw.ep.y ? join_blocks(dw) : 0;
@@ -1080,7 +1128,7 @@ hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, con
                            sums_dx, sums_dw, px, pw, static_cast<int>(b1));
         return hipGetLastError();
     }
-    switch (choose(dx.ep.y ? &dx : nullptr, dw.ep.y ? &dw : nullptr, compute_units()).tiles) {
+    switch (plan.tiles) {
         case kLarge: return backward_t<Large>(dx, dw, s);
         case kWide: return backward_t<Wide>(dx, dw, s);
         case kMedium: return backward_t<Medium>(dx, dw, s);

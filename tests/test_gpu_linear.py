@@ -115,7 +115,7 @@ def test_forward_in_large_tiles(M, N, K):
 
 
 GRADS = [(1, 1, 8), (3, 5, 16), (64, 64, 64), (65, 130, 72), (130, 67, 200), (200, 96, 128), (257, 300, 136), (1000, 33, 264), (1030, 70, 72), (90, 1100, 200), (700, 520, 40),
-         (0, 16, 8), (5, 0, 8)]
+         (0, 16, 8), (5, 0, 8), (5000, 72, 136), (70, 5100, 136), (2600, 2700, 40)]
 
 
 @pytest.mark.parametrize("act", list(ACTS))
