@@ -663,6 +663,7 @@ struct BwdShared {
     float2 sums[kWaves][kCh];
     float2 par[kCh];                              // nrate2, bias (kept here, not in registers, while the tile waits)
     float start[kCh];                             // c past the tile's last row
+    float before[kCh];                            // the state before its first row
     int tile;
 };
 
@@ -762,7 +763,7 @@ struct BwdTile {
     // sa, sb: sums of dg g2 and of da over the lane's rows
     template <Part PART>
     __device__ __forceinline__ void finish(const RecurParams& p, const BwdShared& sh, const Lane& l, int64_t row0, int rows,
-                                           int64_t tile, float* sa, float* sb) {
+                                           float* sa, float* sb) {
         if constexpr (GATE) {
 #pragma unroll
             for (int i = 0; i < L; ++i) z[i].forget();
@@ -770,12 +771,11 @@ struct BwdTile {
 #pragma unroll
         for (int i = 0; i < L; ++i) a[i].forget();
         float s[kVC], r[kVC], nrate2[kVC], bias[kVC];
-        const Quad<false> h = Quad<false>::load(p.saved + tile * p.D + l.c, l.nv);
 #pragma unroll
         for (int j = 0; j < kVC; ++j) {
             nrate2[j] = sh.par[l.cl * kVC + j].x;
             bias[j] = sh.par[l.cl * kVC + j].y;
-            s[j] = h.get(j);
+            s[j] = sh.before[l.cl * kVC + j];
             r[j] = sh.start[l.cl * kVC + j];
         }
         for (int w = 0; w < l.wave; ++w)
@@ -895,13 +895,15 @@ __global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backwar
         if (!first) put_word(w, pack_word(kState, after));
         else if (p.dh0 && ch < p.D) p.dh0[static_cast<int64_t>(pl.seq) * p.D + ch] = rows > 0 ? after : s;
         sh.start[l.lane] = s;
+    } else if (l.wave == 1) {
+        sh.before[l.lane] = c0 + l.lane < p.D ? p.saved[static_cast<int64_t>(tile) * p.D + c0 + l.lane] : 0.f;
     }
     __syncthreads();
     float sa[kVC], sb[kVC];
 #pragma unroll
     for (int j = 0; j < kVC; ++j) sa[j] = sb[j] = 0.f;
-    if (part == kWhole) t.template finish<kWhole>(p, sh, l, row0, rows, tile, sa, sb);
-    else if (rows > 0) t.template finish<kSome>(p, sh, l, row0, rows, tile, sa, sb);
+    if (part == kWhole) t.template finish<kWhole>(p, sh, l, row0, rows, sa, sb);
+    else if (rows > 0) t.template finish<kSome>(p, sh, l, row0, rows, sa, sb);
     if (!p.partial) return;
     // the tile's sums over its rows, in a fixed order
 #pragma unroll
@@ -930,15 +932,15 @@ __global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backwar
 }
 
 // dA_log and ddt_bias from the tiles' sums, each channel's tiles in a fixed
-// order.  One work-group per channel group: 16 threads a channel.
-constexpr int kSumThreads = 1024, kSumSlices = kSumThreads / kCh;
+// order.  A work-group for 16 channels, 64 threads a channel.
+constexpr int kSumThreads = 1024, kSumCh = 16, kSumSlices = kSumThreads / kSumCh;
 
 __global__ __launch_bounds__(kSumThreads) void recur_sum_kernel(RecurParams p) {
     const int total = kHalves * p.unit_off[p.N];
     if (total < 0) return;
-    __shared__ float2 part[kSumSlices][kCh];
-    const int ch = threadIdx.x % kCh, sl = threadIdx.x / kCh;
-    const int c = blockIdx.x * kCh + ch;
+    __shared__ float2 part[kSumSlices][kSumCh];
+    const int ch = threadIdx.x % kSumCh, sl = threadIdx.x / kSumCh;
+    const int c = blockIdx.x * kSumCh + ch;
     float2 t = make_float2(0.f, 0.f);
     for (int i = sl; i < total; i += kSumSlices) {
         const float2 e = p.partial[static_cast<int64_t>(i) * p.groups * kCh + c];
@@ -1053,7 +1055,7 @@ hipError_t launch_recur_backward(const RecurParams& p, bool bf16, hipStream_t s)
     GDN_RECUR_CALL(recur_backward_kernel, static_cast<int64_t>(p.groups) * p.tiles, kThreads);
     e = hipGetLastError();
     if (e != hipSuccess || !p.partial) return e;
-    hipLaunchKernelGGL(recur_sum_kernel, dim3(static_cast<unsigned>(p.groups)), dim3(kSumThreads), 0, s, p);
+    hipLaunchKernelGGL(recur_sum_kernel, dim3(static_cast<unsigned>((p.D + kSumCh - 1) / kSumCh)), dim3(kSumThreads), 0, s, p);
     return hipGetLastError();
 }
 
