@@ -256,48 +256,55 @@ __device__ __forceinline__ void load_to_lds(const void* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
 }
 
-// One operand's tile of R output rows x 32 of the reduction, in an LDS stage
-// of R * 32 bf16 that is filled by load_to_lds (a wave's 64 lanes x 16
-// bytes land in a row of 1 KiB; which 16 bytes a lane fetches is free, and
+// One operand's tile of R output rows x TK (32 or 64) of the reduction, in an
+// LDS stage of R * TK bf16 that is filled by load_to_lds (a wave's 64 lanes x
+// 16 bytes land in a row of 1 KiB; which 16 bytes a lane fetches is free, and
 // that is where the bank swizzle is done).
-//   KC (reduction contiguous): rows of 32 = four 16-byte chunks, chunk c of
-//     row r at c ^ f(r), f = bit 2 of r + 2 (bit 1 ^ bit 3): the chunks that
-//     8 or 16 adjacent lanes read lie in different banks.  A fragment is one
-//     ds_read_b128.
-//   else (output rows contiguous): 32 rows of R, each as 32-byte pairs, pair
-//     q of reduction row k at q ^ f(k), f = k % 4 + 4 (k / 8) (as many bits as
-//     there are pairs).  A fragment is two ds_read_b64_tr_b16, whose 16 lanes
-//     read four rows x 32 bytes and get a column each.
+//   KC (reduction contiguous): rows of TK = four or eight 16-byte chunks,
+//     chunk c of row r at c ^ f(r).  TK 32: f = bit 2 of r + 2 (bit 1 ^ bit 3);
+//     TK 64: f = r / 2 % 8; the chunks that 8 or 16 adjacent lanes read lie in
+//     different banks.  A fragment is one ds_read_b128.  With TK 64 a row's
+//     request is a whole 128-byte line: 4096 x 12288 x 2048 in tiles of 256 x
+//     256 takes 177 us with requests of 64 bytes, 155 with these.
+//   else (output rows contiguous): TK rows of R, each as 32-byte pairs, pair
+//     q of reduction row k at q ^ f(k), f = k % 4 + 4 (k % 32 / 8) (as many
+//     bits as there are pairs).  A fragment is two ds_read_b64_tr_b16, whose
+//     16 lanes read four rows x 32 bytes and get a column each.
 // NW: waves of the work-group; WR: rows of a wave.
-template <bool KC, int R, int NW, int WR>
+template <bool KC, int R, int NW, int WR, int TK>
 struct Operand {
-    static constexpr int kLoads = R * kTK * 2 / 1024 / NW;       // per wave and stage
+    static constexpr int kLoads = R * TK * 2 / 1024 / NW;        // per wave and stage
     static constexpr int kPairs = R / 16;
     static_assert(kLoads >= 1, "a stage is at least one load of each wave");
     // A lane's addresses: a wave-uniform one that moves along the reduction,
     // plus 32-bit byte offsets (strides are of 22 bits).
     const uint8_t* base;
-    int64_t step;                             // bytes per slice
+    int64_t step;                             // bytes per stage
     uint32_t off[kLoads];
-    int k[kLoads];                            // first reduction index within a slice
-    // fragment addresses within a stage, elements
-    int at[KC ? 1 : WR / 16];
+    int k[kLoads];                            // first reduction index within a stage
+    // fragment addresses within a stage, elements (KC: of each half of TK 64)
+    int at[KC ? TK / 32 : WR / 16];
 
-    __device__ __forceinline__ static int chunk_swizzle(int r) { return ((r >> 2) & 1) | ((((r >> 1) ^ (r >> 3)) & 1) << 1); }
-    __device__ __forceinline__ static int pair_swizzle(int kr) { return ((kr & 3) | ((kr >> 3) << 2)) & (kPairs - 1); }
+    __device__ __forceinline__ static int chunk_swizzle(int r) {
+        return TK == 64 ? (r >> 1) & 7 : ((r >> 2) & 1) | ((((r >> 1) ^ (r >> 3)) & 1) << 1);
+    }
+    __device__ __forceinline__ static int pair_swizzle(int kr) { return ((kr & 3) | (((kr & 31) >> 3) << 2)) & (kPairs - 1); }
 
     // rows: of the output; row0: the tile's first; w: which of the tile's WR rows are this wave's
     __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int wave, int lane, int w) {
         const int l16 = lane % 16, lq = lane / 16;
-        step = 2 * (KC ? kTK : kTK * ld);
+        step = 2 * (KC ? TK : TK * ld);
+        // rows past the end, up to a whole tile of them, read the last row and are never stored
+        if (row0 >= rows) row0 = KC ? rows - 1 : (rows - 1) / 8 * 8;
         base = reinterpret_cast<const uint8_t*>(KC ? p + row0 * ld : p + row0);
-        const int left = rows - row0 < R ? static_cast<int>(rows - row0) : R;   // rows past the end: never stored
+        const int left = rows - row0 < R ? static_cast<int>(rows - row0) : R;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
             const int j = wave + u * NW;
             if constexpr (KC) {
-                const int r = 16 * j + lane / 4;
-                k[u] = 8 * ((lane & 3) ^ chunk_swizzle(r));
+                constexpr int kChunks = TK / 8;
+                const int r = kWave / kChunks * j + lane / kChunks;
+                k[u] = 8 * ((lane % kChunks) ^ chunk_swizzle(r));
                 off[u] = 2 * (static_cast<uint32_t>(r < left ? r : left - 1) * static_cast<uint32_t>(ld) + k[u]);
             } else {
                 constexpr int kChunks = R / 8;
@@ -307,7 +314,8 @@ struct Operand {
             }
         }
         if constexpr (KC) {
-            at[0] = (w * WR + l16) * kTK + 8 * (lq ^ chunk_swizzle(l16));
+#pragma unroll
+            for (int h = 0; h < TK / 32; ++h) at[h] = (w * WR + l16) * TK + 8 * ((4 * h + lq) ^ chunk_swizzle(l16));
         } else {
             const int kr = 8 * lq + l16 / 4;
 #pragma unroll
@@ -315,8 +323,8 @@ struct Operand {
         }
     }
 
-    // the next slice into a stage; left: how much of the reduction there still
-    // is (FULL: a whole slice at least)
+    // the next TK of the reduction into a stage; left: how much of it there
+    // still is (FULL: all of TK at least)
     template <bool FULL>
     __device__ __forceinline__ void issue(uint16_t* lds, int wave, int64_t left) {
 #pragma unroll
@@ -328,14 +336,15 @@ struct Operand {
         base += step;
     }
 
-    // fragment of the wave's output rows 16 i .. 16 i + 15
-    __device__ __forceinline__ u32x4 frag(const uint16_t* lds, int i) const {
+    // fragment of the wave's output rows 16 i .. 16 i + 15 and the reduction's 32 h .. 32 h + 31
+    __device__ __forceinline__ u32x4 frag(const uint16_t* lds, int i, int h) const {
         if constexpr (KC) {
-            return *reinterpret_cast<const u32x4*>(lds + at[0] + 16 * i * kTK);
+            return *reinterpret_cast<const u32x4*>(lds + at[h] + 16 * i * TK);
         } else {
+            lds += at[i] + 32 * h * R;
             union { s16x4 h[2]; u32x4 v; } f;
-            f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at[i]));
-            f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at[i] + 4 * R));
+            f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lds);
+            f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + 4 * R));
             return f.v;
         }
     }
@@ -386,6 +395,9 @@ struct Shape {
     static constexpr int kWaves = NWM * NWN, kThreads = kWaves * kWave;
     static constexpr int WM = BM / NWM, WN = BN / NWN, TM = WM / 16, TN = WN / 16;
     static constexpr int kA = BM * kTK, kB = BN * kTK;            // elements of a stage
+    // rows of a wave: two runs of WM / 2.  Eight waves: one in each half of
+    // the tile, which are operands of their own; four: one after the other.
+    static constexpr int kHalfRows = WM / 2, kHalfStep = kWaves == 8 ? BM / 2 : kHalfRows, kWaveStep = kWaves == 8 ? kHalfRows : WM;
     // the epilogue's strips: half of each wave's rows, in 32 bits, four columns of padding
     static constexpr int kStripTiles = TM / 2;
     static constexpr int kStripLd = WN + 4, kStrip = 16 * kStripTiles * kStripLd;
@@ -424,8 +436,8 @@ struct Store {
         if (PLAIN || !early) return;
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
-            const int64_t m = m0 + half * kRows + first + u * kRowsAtOnce;
-            if (m < p.M) 
+            const int64_t m = m0 + half * S::kHalfStep + first + u * kRowsAtOnce;
+            if (m < p.M)
                 res[u] = __builtin_nontemporal_load(
                     reinterpret_cast<const Run8*>(static_cast<const uint16_t*>(p.ep.residual) + m * p.ep.ldr + n));
         }
@@ -457,7 +469,7 @@ struct Store {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) { f[u][e] = q0[e] + bias[e]; f[u][4 + e] = q1[e] + bias[4 + e]; }
                 }
-                const int64_t mb = m0 + half * kRows + first + u0 * kRowsAtOnce;
+                const int64_t mb = m0 + half * S::kHalfStep + first + u0 * kRowsAtOnce;
                 if (!PLAIN && p.ep.preact) {
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
@@ -500,89 +512,99 @@ struct Store {
 };
 
 // Large tiles, 256 x 256 for 2 x 4 waves of 128 x 64: one work-group fills a
-// compute unit, with two waves on each SIMD.  A slice of 32 of the reduction
-// is two phases of 16 matrix instructions a wave (its upper and its lower 64
-// rows); before a phase the wave reads the fragments it needs, between two
-// barriers.  The lower four waves run half a phase behind the upper four, so
-// while one wave of a SIMD feeds the matrix core the other one reads and
-// requests.  Slice kt + 3 is requested in the second phase of slice kt, into
-// the stage of slice kt - 1, whose last fragments every wave had in registers
-// before the barrier that this phase began with.
+// compute unit, with two waves on each SIMD.  A stage is 64 of the reduction,
+// so that a row's request is a whole line, in three operands: the weights, and
+// the tile's upper and lower rows (a wave has as many of either).  It is four
+// phases of 16 matrix instructions a wave: the upper rows with the first and
+// the second 32 of the reduction, then the lower rows with both (the weights'
+// fragments stay in registers); before a phase the wave reads the fragments
+// it needs, between two barriers.  The lower four waves run half a phase
+// behind the upper four, so while one wave of a SIMD feeds the matrix core the
+// other one reads and requests.
+// Two stages in LDS: in the fourth phase of stage t the weights and upper rows
+// of t + 2 are requested into their places in it, which were last read in the
+// second phase, and in the second phase the lower rows of t + 1, into those of
+// t - 1, last read in its fourth phase: every wave had those fragments in
+// registers before the barrier that the requesting phase began with.  What is
+// requested has four phases to land.
 template <bool AK, bool BK, bool PLAIN, typename S>
 __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8_t* shared) {
-    using OA = Operand<AK, S::BM, S::kWaves, S::WM>;
-    using OB = Operand<BK, S::BN, S::kWaves, S::WN>;
-    constexpr int TM = S::TM, TN = S::TN, H = TM / 2;
-    constexpr int kPer = OA::kLoads + OB::kLoads, kStages = S::kStages;
-    uint16_t* const as = reinterpret_cast<uint16_t*>(shared);
-    uint16_t* const bs = as + kStages * S::kA;
+    constexpr int K2 = 2 * kTK, TM = S::TM, TN = S::TN, H = TM / 2;
+    using OA = Operand<AK, S::BM / 2, S::kWaves, S::kHalfRows, K2>;
+    using OB = Operand<BK, S::BN, S::kWaves, S::WN, K2>;
+    constexpr int kInFlight = 2 * OA::kLoads + OB::kLoads;
+    static_assert(S::kStages == 4, "two stages of 64");
+    uint16_t* const us = reinterpret_cast<uint16_t*>(shared);
+    uint16_t* const ls = us + 2 * S::kA;
+    uint16_t* const bs = ls + 2 * S::kA;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     const int wm = wave / S::NWN, wn = wave % S::NWN;
     int tm, tn;
     tile_of(tile, static_cast<int>((p.M + S::BM - 1) / S::BM), static_cast<int>((p.N + S::BN - 1) / S::BN), &tm, &tn);
     const int64_t m0 = static_cast<int64_t>(tm) * S::BM, n0 = static_cast<int64_t>(tn) * S::BN;
-    OA a;
+    OA upper, lower;
     OB b;
-    a.init(static_cast<const uint16_t*>(p.A), p.lda, m0, p.M, wave, lane, wm);
+    upper.init(static_cast<const uint16_t*>(p.A), p.lda, m0, p.M, wave, lane, wm);
+    lower.init(static_cast<const uint16_t*>(p.A), p.lda, m0 + S::BM / 2, p.M, wave, lane, wm);
     b.init(static_cast<const uint16_t*>(p.B), p.ldb, n0, p.N, wave, lane, wn);
     f32x4 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // slices in whole rounds of the stages: those past the reduction's end read zeros
-    const int nk = static_cast<int>((p.K + kTK - 1) / kTK + kStages - 1) / kStages * kStages;
-    const int full = static_cast<int>(p.K / kTK);
+    // an even number of stages: past the reduction's end they read zeros
+    const int nk = static_cast<int>((p.K + K2 - 1) / K2 + 1) / 2 * 2;
+    const int full = static_cast<int>(p.K / K2);
     Store<S, PLAIN> out;
-    out.init(p, m0 + wm * S::WM, n0 + wn * S::WN, lane);
-    auto round = [&](auto whole, int kt) {    // slices kt .. kt + 3 (kt a multiple of 4)
+    out.init(p, m0 + wm * S::kWaveStep, n0 + wn * S::WN, lane);
+    auto round = [&](auto whole, int kt) {    // stages kt and kt + 1 (kt even)
         constexpr bool FULL = decltype(whole)::value;
 #pragma unroll
-        for (int st = 0; st < kStages; ++st) {
-            u32x4 fa[H], fb[TN];
+        for (int st = 0; st < 2; ++st) {
+            u32x4 fa[H], fb[2][TN];
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = b.frag(bs + st * S::kB, j);
+            for (int ph = 0; ph < 4; ++ph) {
+                const int h = ph % 2, half = ph / 2;
+                if (half == 0) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) fa[i] = a.frag(as + st * S::kA, i);
-            wave_barrier();
-            __builtin_amdgcn_s_setprio(1);
+                    for (int j = 0; j < TN; ++j) fb[h][j] = b.frag(bs + st * 2 * S::kB, j, h);
+                }
 #pragma unroll
-            for (int i = 0; i < H; ++i)
+                for (int i = 0; i < H; ++i) fa[i] = half == 0 ? upper.frag(us + st * S::kA, i, h) : lower.frag(ls + st * S::kA, i, h);
+                if (ph == 1) {
+                    lower.template issue<FULL>(ls + (st ^ 1) * S::kA, wave, p.K - static_cast<int64_t>(kt + st + 1) * K2);
+                    wait_vm<kInFlight>();     // this stage's lower rows have landed
+                }
+                if (ph == 3) {
+                    const int64_t left = p.K - static_cast<int64_t>(kt + st + 2) * K2;
+                    upper.template issue<FULL>(us + st * S::kA, wave, left);
+                    b.template issue<FULL>(bs + st * 2 * S::kB, wave, left);
+                    wait_vm<kInFlight>();     // the next stage's weights and upper rows have landed
+                }
+                wave_barrier();
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma(fb[j], fa[i], acc[i][j]);
-            __builtin_amdgcn_s_setprio(0);
-            wave_barrier();
-            constexpr int kAhead = kStages - 1;
-            const int64_t left = p.K - static_cast<int64_t>(kt + st + kAhead) * kTK;
+                for (int i = 0; i < H; ++i)
 #pragma unroll
-            for (int i = 0; i < H; ++i) fa[i] = a.frag(as + st * S::kA, H + i);
-            a.template issue<FULL>(as + (st + kAhead) % kStages * S::kA, wave, left);
-            b.template issue<FULL>(bs + (st + kAhead) % kStages * S::kB, wave, left);
-            wait_vm<(kStages - 2) * kPer>();  // slice kt + 1 has landed
-            wave_barrier();
-            __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-            for (int i = 0; i < H; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[H + i][j] = mfma(fb[j], fa[i], acc[H + i][j]);
-            __builtin_amdgcn_s_setprio(0);
-            wave_barrier();
+                    for (int j = 0; j < TN; ++j) acc[half * H + i][j] = mfma(fb[h][j], fa[i], acc[half * H + i][j]);
+                __builtin_amdgcn_s_setprio(0);
+                wave_barrier();
+            }
         }
     };
     if (nk > 0) {
-#pragma unroll
-        for (int st = 0; st < kStages - 1; ++st) {
-            const int64_t left = p.K - st * kTK;
-            a.template issue<false>(as + st * S::kA, wave, left);
-            b.template issue<false>(bs + st * S::kB, wave, left);
-        }
-        wait_vm<(kStages - 2) * kPer>();      // slice 0
+        upper.template issue<false>(us, wave, p.K);
+        b.template issue<false>(bs, wave, p.K);
+        lower.template issue<false>(ls, wave, p.K);
+        upper.template issue<false>(us + S::kA, wave, p.K - K2);
+        b.template issue<false>(bs + 2 * S::kB, wave, p.K - K2);
+        wait_vm<kInFlight>();                 // the first stage's weights and upper rows
         wave_barrier();
         if (wave >= S::kWaves / 2) wave_barrier();   // half a phase behind
         int kt = 0;
-        for (; kt + 2 * kStages - 1 <= full; kt += kStages) round(Bool<true>{}, kt);
+        for (; kt + 4 <= full; kt += 2) round(Bool<true>{}, kt);
         out.fetch(p, 0);
-        for (; kt < nk; kt += kStages) round(Bool<false>{}, kt);
+        for (; kt < nk; kt += 2) round(Bool<false>{}, kt);
         if (wave < S::kWaves / 2) wave_barrier();
         wait_vm<0>();                         // the requests past the end
     }
@@ -598,8 +620,8 @@ __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8
 // read from an iteration ago; one barrier an iteration.
 template <bool AK, bool BK, bool PLAIN, typename S>
 __device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8_t* shared) {
-    using OA = Operand<AK, S::BM, S::kWaves, S::WM>;
-    using OB = Operand<BK, S::BN, S::kWaves, S::WN>;
+    using OA = Operand<AK, S::BM, S::kWaves, S::WM, kTK>;
+    using OB = Operand<BK, S::BN, S::kWaves, S::WN, kTK>;
     constexpr int TM = S::TM, TN = S::TN;
     constexpr int kPer = OA::kLoads + OB::kLoads, kStages = S::kStages;
     uint16_t* const as = reinterpret_cast<uint16_t*>(shared);
@@ -621,13 +643,13 @@ __device__ __forceinline__ void gemm_small(const GemmProduct& p, int tile, uint8
     const int nk = static_cast<int>((p.K + kTK - 1) / kTK + kStages - 1) / kStages * kStages;
     const int full = static_cast<int>(p.K / kTK);
     Store<S, PLAIN> out;
-    out.init(p, m0 + wm * S::WM, n0 + wn * S::WN, lane);
+    out.init(p, m0 + wm * S::kWaveStep, n0 + wn * S::WN, lane);
     u32x4 fa[2][TM], fb[2][TN];
     auto fragments = [&](int stage, int set) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) fb[set][j] = b.frag(bs + stage * S::kB, j);
+        for (int j = 0; j < TN; ++j) fb[set][j] = b.frag(bs + stage * S::kB, j, 0);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fa[set][i] = a.frag(as + stage * S::kA, i);
+        for (int i = 0; i < TM; ++i) fa[set][i] = a.frag(as + stage * S::kA, i, 0);
     };
     auto round = [&](auto whole, int kt) {
         constexpr bool FULL = decltype(whole)::value;
