@@ -63,8 +63,8 @@ __device__ __forceinline__ float half_erfc(float p, float* e) {
 // squares on [0, 14]; relative error of the result below 5e-6 for |p| < 4,
 // 5e-4 where it is below 1e-5, and past the fit the leading term takes it to
 // 0): 15 vector operations a value instead of 24.  For outputs in bf16, whose
-// rounding is 2^-9; at 4096 x 12288 x 2048 gelu's share of the kernel's time
-// falls from 25 to 13 us of 190.
+// rounding is 2^-9.  4096 x 12288 x 2048: 147 us without an activation, 160
+// with this one, 171 with the one above.
 __device__ __forceinline__ float half_erfc_bf16(float p) {
     const float x = fabsf(p);
     float q = -1.40202519e-06f;
@@ -527,6 +527,9 @@ struct Store {
 // t - 1, last read in its fourth phase: every wave had those fragments in
 // registers before the barrier that the requesting phase began with.  What is
 // requested has four phases to land.
+// Bound: the matrix cores at the clock that their power leaves (4096 x 12288 x
+// 2048: 148 us, 1390 TFLOP/s).  The epilogue of a round of tiles does not
+// overlap with the next one's products: with gelu, bias and residual 173 us.
 template <bool AK, bool BK, bool PLAIN, typename S>
 __device__ __forceinline__ void gemm_large(const GemmProduct& p, int tile, uint8_t* shared) {
     constexpr int K2 = 2 * kTK, TM = S::TM, TN = S::TN, H = TM / 2;
@@ -802,8 +805,10 @@ __global__ __launch_bounds__(kJoinThreads) void linear_backward_join_kernel(Gemm
 }
 
 // ---- few rows --------------------------------------------------------------------
-// Up to 16 rows.  (More would read all of x through each compute unit's L1
-// for every 16 columns: 64 x 2048 x 4096 took 23 us so.)  A work-group owns 16 rows of w (16 columns of y) and splits K over its waves;
+// Up to 16 rows; bound by HBM: 1 x 12352 x 2048 takes 12.7 us, 4.0 TB/s of
+// weights.  (More rows would read all of x through each compute unit's L1 for
+// every 16 columns: 64 x 2048 x 4096 took 23 us so, and 13 in parts.)  A
+// work-group owns 16 rows of w (16 columns of y) and splits K over its waves;
 // per 64-wide step of K the lanes of a row read two runs of 64 bytes of their
 // weight row and of their row of x, DEPTH steps ahead.  Steps past a
 // wave's share and k past K read zeros.  The waves' partial tiles are summed
@@ -858,7 +863,7 @@ __global__ __launch_bounds__(kFewWaves * kWave, 2) void linear_few_kernel(GemmPr
 }
 
 // ---- dp = dy act'(p) and its column sums -------------------------------------------
-// Bound: HBM (dy and p in, dp out).  A work-group covers 32 rows x 256
+// Bound: HBM (dy and p in, dp out: 4096 x 4096 in bf16 25 us, 4.0 TB/s).  A work-group covers 32 rows x 256
 // columns: 32 lanes of eight columns, every eighth row, the four rows' loads
 // in flight together; dp is rounded to bf16 (the products' operand type), the
 // sums are of the values before that.
@@ -972,12 +977,15 @@ hipError_t backward_t(const GemmProduct& dx, const GemmProduct& dw, hipStream_t 
 
 }  // namespace
 
-// Which tiles: the time of one tile on a compute unit at K = 2048, in us
-// (measured at 4096 x 4096 for 256 x 256, 4096 x 2048 for 256 x 128, 2048 x
-// 2048 for 128 x 128 and 64 x 64), times the rounds of tiles over the compute
-// units.  At 4096 x 2048 x 4096: 81 us in tiles of 256 x 256, 68 in 256 x
-// 128, 80 in 128 x 128, 126 in 64 x 64; at 2048 x 2048 x 2048: 44, 31, 25, 33;
-// at 1024 x 2048 x 2048: 42, 29, 23, 17; at 1024 x 12352 x 2048: 54, 68, 75, 96.
+// Which tiles: the time of one tile on a compute unit at K = 2048, in us, times
+// the rounds of tiles over the compute units.  Measured, in the order 256 x
+// 256, 256 x 128, 128 x 128, 64 x 64:
+//   4096 x 12288 x 2048: 148, 173, 231, 341 us
+//   4096 x  2048 x 4096:  73,  55,  75, 125 us
+//   2048 x  2048 x 2048:  41,  27,  24,  34 us
+//   1024 x  2048 x 2048:  40,  26,  23,  18 us
+//   1024 x 12352 x 2048:  45,  54,  70,  93 us
+constexpr double kLargeUs = 46.0, kWideUs = 27.0, kMediumUs = 21.0, kSmallUs = 8.5;
 enum Tiles { kLarge, kWide, kMedium, kSmall };
 
 struct Choice {
@@ -987,8 +995,8 @@ struct Choice {
 
 static Choice choose(const GemmProduct& p, int cus) {
     auto us = [&](int64_t n, double each) { return static_cast<double>((n + cus - 1) / cus) * each; };
-    const Choice all[4] = {{kLarge, us(tiles<Large>(p), 47.0)}, {kWide, us(tiles<Wide>(p), 30.0)},
-                           {kMedium, us(tiles<Medium>(p), 21.0)}, {kSmall, us(tiles<Small>(p), 8.5)}};
+    const Choice all[4] = {{kLarge, us(tiles<Large>(p), kLargeUs)}, {kWide, us(tiles<Wide>(p), kWideUs)},
+                           {kMedium, us(tiles<Medium>(p), kMediumUs)}, {kSmall, us(tiles<Small>(p), kSmallUs)}};
     Choice best = all[0];
     for (int i = 1; i < 4; ++i)
         if (all[i].us < best.us) best = all[i];
@@ -1049,8 +1057,9 @@ hipError_t launch_linear(const GemmProduct& given, float* sums, hipStream_t s) {
     if (p.M <= kLinearFewRows) return forward_t<Small>(p, s);
     // A last column of tiles that is nearly empty can cost a whole round of
     // them (12352 = 48 x 256 + 64 columns at 4096 rows: 784 tiles, four rounds
-    // instead of three): then the rest goes by itself in smaller tiles.  A
-    // column's sum runs in the same order either way.
+    // instead of three; with gelu, bias and residual 210 us): then the rest
+    // goes by itself in smaller tiles (184 us).  A column's sum runs in the
+    // same order either way.
     const int cus = compute_units();
     const Choice whole = choose(p, cus);
     const int64_t rest = p.N % 256, main = p.N - rest;
@@ -1070,15 +1079,16 @@ int64_t linear_dp_blocks(int64_t M) { return (M + kDpRows - 1) / kDpRows; }
 // How the backward products run: dx (reduction N) and dw (reduction M) share
 // a launch, so their tiles' times are weighed by their reductions: the work
 // over the compute units in rounds of the shorter reduction, and no less than
-// one tile of the longer one takes by itself (a 64 x 64 tile alone: 11 us at
-// 2048).  Reductions may be cut into parts, which costs the sums' way through
+// one tile of the longer one takes by itself.  Reductions may be cut into parts, which costs the sums' way through
 // memory and a launch.  Measured, in the order 256 x 256, 256 x 128, 128 x
 // 128, 64 x 64, and the best number of parts' time:
 //    700 x 8192 x  256: 126,  91,  65,  38 us, 24 in parts of 2048
 //   8192 x  512 x  512: 126,  84,  62,  44 us, 33 in parts of 2048
 //   4096 x 1000 x  512:  67,  45,  33,  27 us, 29 in parts of 2048
-//   2048 x 2048 x 2048:  42,  33,  36,  55 us, 77 in parts of 1024
-//   4096 x 4096 x 2048:  96, 124, 131, 224 us, 243 in parts of 2048
+//   2048 x 2048 x 2048:  42,  32,  36,  54 us, 77 in parts of 1024
+//   8192 x 2048 x 2048: 146, 118, 131, 227 us, 245 in parts of 2048
+//   4096 x 4096 x 2048:  97, 125, 127, 221 us, 243 in parts of 2048
+constexpr double kSmallAlone = 11.0;              // a 64 x 64 tile with a compute unit to itself
 struct BackwardPlan {
     Tiles tiles;
     int px, pw;                                   // parts of dx's and dw's reductions (1, 1: no sums)
@@ -1096,19 +1106,19 @@ static BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K) {
         return (work > most * alone ? work : most * alone) / 2048;
     };
     BackwardPlan best{kLarge, 1, 1};
-    double least = us(256, 256, 47, 47, 1, 1);
+    double least = us(256, 256, kLargeUs, kLargeUs, 1, 1);
     auto offer = [&](double t, BackwardPlan p) {
         if (t < least) { least = t; best = p; }
     };
-    offer(us(256, 128, 30, 30, 1, 1), {kWide, 1, 1});
-    offer(us(128, 128, 21, 21, 1, 1), {kMedium, 1, 1});
-    offer(us(64, 64, 8.5, 11, 1, 1), {kSmall, 1, 1});
+    offer(us(256, 128, kWideUs, kWideUs, 1, 1), {kWide, 1, 1});
+    offer(us(128, 128, kMediumUs, kMediumUs, 1, 1), {kMedium, 1, 1});
+    offer(us(64, 64, kSmallUs, kSmallAlone, 1, 1), {kSmall, 1, 1});
     for (int len = 256; len <= (1 << 20); len *= 2) {
         const int px = N > len ? static_cast<int>(up(N, len)) : 1, pw = M > len ? static_cast<int>(up(M, len)) : 1;
         if (px == 1 && pw == 1) break;
         if (px > 64 || pw > 64) continue;         // (the sums are joined one after the other)
         const double sums = 8.0 * static_cast<double>(K) * (static_cast<double>(px) * M + static_cast<double>(pw) * N);
-        offer(us(64, 64, 8.5, 11, px, pw) + 5 + sums / 3e6, {kSmall, px, pw});
+        offer(us(64, 64, kSmallUs, kSmallAlone, px, pw) + 5 + sums / 3e6, {kSmall, px, pw});
     }
     return best;
 }
