@@ -821,16 +821,21 @@ def layer_decode_raw(layer: Layer, proj: Proj, *, B, x, y, state_in, state_out, 
 # (One token's call costs more on the host than on the device, so these checks
 # try what is usual first and name what is wrong only when it is not.)
 
+_torch = None       # the module, once a tensor is looked at (an import statement a check costs a call microseconds)
+
+
 def _device():
     """Index of the current device: the library launches there."""
-    import torch
-    return torch.cuda.current_device()
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda.current_device()
 
 
 def _raw_stream(stream, dev):
     """Handle of a stream (None: torch's current one on device `dev`)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _on_device(t, name, dev):
@@ -870,13 +875,13 @@ def _dense(t, name, rows, cols, dev):
     [>= rows])."""
     if t is None:
         return None
-    import torch
+    if t.get_device() != dev:
+        _on_device(t, name, dev)
     shape = t.shape
     ok = len(shape) == 1 if cols is None else (len(shape) == 2 and shape[1] == cols)
-    if (ok and t.get_device() == dev and shape[0] >= rows and t.dtype is torch.float32
+    if (ok and shape[0] >= rows and t.dtype is _torch.float32
             and t.is_contiguous()):
         return t.data_ptr()
-    _on_device(t, name, dev)
     raise ValueError(f"{name}: contiguous float32 [{rows}{'' if cols is None else f', {cols}'}] "
                      f"needed, not {t.dtype} {tuple(shape)}")
 
@@ -885,10 +890,10 @@ def _index(t, name, n, dev):
     """Pointer of an optional contiguous device int32 tensor of >= n entries."""
     if t is None:
         return None
-    import torch
-    if t.dtype is torch.int32 and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+    if t.get_device() != dev:
+        _on_device(t, name, dev)
+    if t.dtype is _torch.int32 and t.numel() >= n and t.is_contiguous():
         return t.data_ptr()
-    _on_device(t, name, dev)
     raise ValueError(f"{name}: a contiguous device int32 tensor of {n} entries is required")
 
 
@@ -929,21 +934,11 @@ class Recur:
         import torch
         return torch.bfloat16 if self.act_dtype == GDN_DTYPE_BF16 else torch.float32
 
-    def c(self) -> CRecur:
-        # the parameters are measured once per set of tensors, device and shape
-        A, d = self.A_log, self.dt_bias
-        key = (A.data_ptr(), d.data_ptr(), A.shape, d.shape, self.D, self.act_dtype)
-        if self.__dict__.get("_key") != key:
-            for t, name in ((A, "A_log"), (d, "dt_bias")):
-                if not t.is_cuda:
-                    raise ValueError(f"{name}: a device tensor is required")
-            self._dev = _device()
-            self._c = CRecur(self.D, self.act_dtype, _dense(A, "A_log", self.D, None, self._dev),
-                             _dense(d, "dt_bias", self.D, None, self._dev))
-            self._key = key
-        elif self._dev != _device():
-            _on_device(A, "A_log", _device())
-        return self._c
+    def c(self, dev=None) -> CRecur:
+        if dev is None:
+            dev = _device() if self.A_log.is_cuda else 0
+        return CRecur(self.D, self.act_dtype, _dense(self.A_log, "A_log", self.D, None, dev),
+                      _dense(self.dt_bias, "dt_bias", self.D, None, dev))
 
 
 def _recur_size(name, rec, N, T):
@@ -1000,7 +995,7 @@ def recur_forward_raw(rec: Recur, *, N, T_total, cu_seqlens, x, a, b, y, z=None,
                    state_slots, int(num_slots), saved, status)
     _recur_saved(rec, saved, N, T, dev)
     ws, nb = _bytes(workspace, "workspace", dev)
-    _check(lib().gdn_recur_forward(ctypes.byref(rec.c()), ctypes.byref(io), ws, nb,
+    _check(lib().gdn_recur_forward(ctypes.byref(rec.c(dev)), ctypes.byref(io), ws, nb,
                                    _raw_stream(stream, dev)))
 
 
@@ -1091,7 +1086,7 @@ def recur_decode_raw(rec: Recur, *, N, x, a, b, y, initial_state, final_state, z
     N, dev = int(N), _device()
     io = _recur_io(rec, dev, N, 0, N, None, x, a, b, z, y, initial_state, final_state, state_slots,
                    int(num_slots), None, status)
-    _check(lib().gdn_recur_decode(ctypes.byref(rec.c()), ctypes.byref(io), _raw_stream(stream, dev)))
+    _check(lib().gdn_recur_decode(ctypes.byref(rec.c(dev)), ctypes.byref(io), _raw_stream(stream, dev)))
 
 
 def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True, out=None,
@@ -1106,7 +1101,7 @@ def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True,
     fs = state if in_place else _new(state, state.shape, state.dtype, stream)
     io = _recur_io(rec, dev, B, 0, B, None, x, a, b, z, out, state, fs, state_slots,
                    0 if state_slots is None else state.shape[0], None, status)
-    _check(lib().gdn_recur_decode(ctypes.byref(rec.c()), ctypes.byref(io), _raw_stream(stream, dev)))
+    _check(lib().gdn_recur_decode(ctypes.byref(rec.c(dev)), ctypes.byref(io), _raw_stream(stream, dev)))
     return {"out": out, "final_state": fs}
 
 
