@@ -964,13 +964,14 @@ def recur_backward_workspace_bytes(rec: Recur, N: int, T_total: int) -> int:
 
 
 def _recur_io(rec, dev, N, T, rows, cu_seqlens, x, a, b, z, y, initial_state, final_state,
-              state_slots, num_slots, saved, status):
+              state_slots, num_slots, saved, status, fresh=False):
+    # fresh: y is the dense tensor that the binding itself has just allocated like x
     D, dt = rec.D, rec.dtype
     px, sx = _matrix(x, "x", rows, D, dt, dev)
     pa, sa = _matrix(a, "a", rows, D, dt, dev)
     pb, sb = _matrix(b, "b", rows, D, dt, dev)
     pz, sz = (None, 0) if z is None else _matrix(z, "z", rows, D, dt, dev)
-    py, sy = (None, 0) if y is None else _matrix(y, "y", rows, D, dt, dev)
+    py, sy = (None, 0) if y is None else (y.data_ptr(), D) if fresh else _matrix(y, "y", rows, D, dt, dev)
     entries = N if state_slots is None else num_slots
     ps = _dense(initial_state, "initial_state", entries, D, dev)
     pf = ps if final_state is initial_state else _dense(final_state, "final_state", entries, D, dev)
@@ -1095,12 +1096,13 @@ def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True,
     (or a pool [slots, D] with state_slots int32 [B]), updated in place by
     default.  Returns a dict with out [B, D] and final_state (in_place=False:
     a new tensor, of which only these sequences' entries are written)."""
-    B, D, dev = x.shape[0], rec.D, _device()
-    if out is None:
-        out = _new(x, (B, D), rec.dtype, stream)
+    B, dev, fresh = x.shape[0], _device(), out is None
+    if fresh:
+        out = (_torch.empty_like(x, memory_format=_torch.contiguous_format) if stream is None
+               else _new(x, x.shape, x.dtype, stream))
     fs = state if in_place else _new(state, state.shape, state.dtype, stream)
     io = _recur_io(rec, dev, B, 0, B, None, x, a, b, z, out, state, fs, state_slots,
-                   0 if state_slots is None else state.shape[0], None, status)
+                   0 if state_slots is None else state.shape[0], None, status, fresh)
     _check(lib().gdn_recur_decode(ctypes.byref(rec.c(dev)), ctypes.byref(io), _raw_stream(stream, dev)))
     return {"out": out, "final_state": fs}
 
