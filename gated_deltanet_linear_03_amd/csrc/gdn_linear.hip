@@ -978,14 +978,16 @@ hipError_t backward_t(const GemmProduct& dx, const GemmProduct& dw, hipStream_t 
 }  // namespace
 
 // Which tiles: the time of one tile on a compute unit at K = 2048, in us, times
-// the rounds of tiles over the compute units.  Measured, in the order 256 x
+// the rounds of tiles over the compute units; tiles that share one take longer
+// where they have it to themselves.  Measured, in the order 256 x
 // 256, 256 x 128, 128 x 128, 64 x 64:
 //   4096 x 12288 x 2048: 148, 173, 231, 341 us
 //   4096 x  2048 x 4096:  73,  55,  75, 125 us
 //   2048 x  2048 x 2048:  41,  27,  24,  34 us
 //   1024 x  2048 x 2048:  40,  26,  23,  18 us
 //   1024 x 12352 x 2048:  45,  54,  70,  93 us
-constexpr double kLargeUs = 46.0, kWideUs = 27.0, kMediumUs = 21.0, kSmallUs = 8.5;
+constexpr double kLargeUs = 46.0, kWideUs = 27.0, kMediumUs = 18.0, kSmallUs = 8.5;
+constexpr double kMediumAlone = 24.0, kSmallAlone = 11.0;
 enum Tiles { kLarge, kWide, kMedium, kSmall };
 
 struct Choice {
@@ -994,9 +996,13 @@ struct Choice {
 };
 
 static Choice choose(const GemmProduct& p, int cus) {
-    auto us = [&](int64_t n, double each) { return static_cast<double>((n + cus - 1) / cus) * each; };
-    const Choice all[4] = {{kLarge, us(tiles<Large>(p), kLargeUs)}, {kWide, us(tiles<Wide>(p), kWideUs)},
-                           {kMedium, us(tiles<Medium>(p), kMediumUs)}, {kSmall, us(tiles<Small>(p), kSmallUs)}};
+    auto us = [&](int64_t n, double each, double alone) {
+        const double t = static_cast<double>((n + cus - 1) / cus) * each;
+        return t > alone ? t : alone;
+    };
+    const Choice all[4] = {{kLarge, us(tiles<Large>(p), kLargeUs, kLargeUs)}, {kWide, us(tiles<Wide>(p), kWideUs, kWideUs)},
+                           {kMedium, us(tiles<Medium>(p), kMediumUs, kMediumAlone)},
+                           {kSmall, us(tiles<Small>(p), kSmallUs, kSmallAlone)}};
     Choice best = all[0];
     for (int i = 1; i < 4; ++i)
         if (all[i].us < best.us) best = all[i];
@@ -1085,10 +1091,10 @@ int64_t linear_dp_blocks(int64_t M) { return (M + kDpRows - 1) / kDpRows; }
 //    700 x 8192 x  256: 126,  91,  65,  38 us, 24 in parts of 2048
 //   8192 x  512 x  512: 126,  84,  62,  44 us, 33 in parts of 2048
 //   4096 x 1000 x  512:  67,  45,  33,  27 us, 29 in parts of 2048
+//   1537 x 1000 x 2048:  39,  26,  24,  29 us, 43 in parts of 1024
 //   2048 x 2048 x 2048:  42,  32,  36,  54 us, 77 in parts of 1024
 //   8192 x 2048 x 2048: 146, 118, 131, 227 us, 245 in parts of 2048
 //   4096 x 4096 x 2048:  97, 125, 127, 221 us, 243 in parts of 2048
-constexpr double kSmallAlone = 11.0;              // a 64 x 64 tile with a compute unit to itself
 struct BackwardPlan {
     Tiles tiles;
     int px, pw;                                   // parts of dx's and dw's reductions (1, 1: no sums)
@@ -1111,7 +1117,7 @@ static BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K) {
         if (t < least) { least = t; best = p; }
     };
     offer(us(256, 128, kWideUs, kWideUs, 1, 1), {kWide, 1, 1});
-    offer(us(128, 128, kMediumUs, kMediumUs, 1, 1), {kMedium, 1, 1});
+    offer(us(128, 128, kMediumUs, kMediumAlone, 1, 1), {kMedium, 1, 1});
     offer(us(64, 64, kSmallUs, kSmallAlone, 1, 1), {kSmall, 1, 1});
     for (int len = 256; len <= (1 << 20); len *= 2) {
         const int px = N > len ? static_cast<int>(up(N, len)) : 1, pw = M > len ? static_cast<int>(up(M, len)) : 1;
