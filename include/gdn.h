@@ -639,8 +639,8 @@ typedef struct {
 } gdn_linear_io;
 
 /* Bytes of device workspace gdn_linear needs; 0 where it needs none (up to 16
- * and from 65 rows on, and with a short K) and on error (gdn_last_error()
- * tells). */
+ * and from 65 rows on, and with a short K or a large N) and on error
+ * (gdn_last_error() tells). */
 size_t gdn_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Enqueue the layer.  Up to 16 rows run on a weight-streaming kernel, up to
