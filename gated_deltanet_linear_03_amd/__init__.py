@@ -1161,7 +1161,7 @@ def linear(x, w, bias=None, act=GDN_ACT_NONE, residual=None, out=None, out_dtype
     ws, nb = None, 0
     if workspace is not None:
         ws, nb = _bytes(workspace, "workspace", dev)
-    elif 16 < M <= 64:
+    elif 16 < M <= 256:
         nb = linear_workspace_bytes(M, N, K)
         if nb:
             workspace = _new(x, (nb,), torch.uint8, stream)

@@ -267,7 +267,8 @@ struct LinearDp {
 };
 
 constexpr int kLinearStreamRows = 16;    // up to this many rows: the weight-streaming kernel
-constexpr int kLinearFewRows = 64;       // up to this many: the reduction in parts, as N and K make it
+constexpr int kLinearFewRows = 64;       // up to this many, and then up to
+constexpr int kLinearSomeRows = 256;     // that many: the reduction in parts, as N and K make it
 
 // Parts of the reduction: 1 or how many [M][N] fp32 sums the call keeps
 int linear_parts(int64_t M, int64_t N, int64_t K);

@@ -12,7 +12,7 @@
 // so nothing is ever transposed in memory.
 //
 // Few rows: the product is a stream over w, and bound by HBM.  Up to 16 rows
-// each work-group takes 16 columns with K split over its waves; up to 64 rows
+// each work-group takes 16 columns with K split over its waves; up to 256 rows
 // K is split over work-groups of 64 columns, whose sums a second kernel adds.
 #include <cmath>
 
@@ -1167,12 +1167,16 @@ static GemmProduct columns(const GemmProduct& p, int64_t n0, int64_t n) {
     return c;
 }
 
-// Parts of 17 to 64 rows' reduction: as many as there are compute units for
-// each tile of 64 columns, of 256 at least.  64 x 2048 x 4096: 17.0 us with
+// Parts of the reduction of 17 to 64 rows: as many as there are compute units
+// for each tile of 64 columns, of 256 at least.  64 x 2048 x 4096: 17.0 us with
 // 16 parts, 13.2 with 8, 14.6 with 4; 64 x 12352 x 2048: 20.3 with 1, 22.6 with 2.
+// Of 65 to 256 rows: the same for four tiles of rows, of 1024 at least (128 x
+// 1024 x 8192: 53 us in one part, 21 in four).  The number is one for all the
+// rows of a range, so that a row's sum does not depend on how many there are.
 int linear_parts(int64_t M, int64_t N, int64_t K) {
-    if (M <= kLinearStreamRows || M > kLinearFewRows || N <= 0) return 1;
-    const int64_t want = compute_units() / ((N + 63) / 64), most = K / 256;
+    if (M <= kLinearStreamRows || M > kLinearSomeRows || N <= 0) return 1;
+    const bool few = M <= kLinearFewRows;
+    const int64_t want = compute_units() / ((few ? 1 : 4) * ((N + 63) / 64)), most = K / (few ? 256 : 1024);
     const int64_t n = want < most ? want : most;
     return n < 1 ? 1 : static_cast<int>(n > 64 ? 64 : n);
 }

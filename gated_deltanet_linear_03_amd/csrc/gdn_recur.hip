@@ -636,11 +636,20 @@ __global__ __launch_bounds__(kPlanThreads) void recur_plan_kernel(RecurParams p)
         total += part[w];
     }
     int at = upto - sum;
-    for (int n = n0; n < n1; ++n) {
-        p.unit_off[n] = at;
-        const int k = units_of(p.cu[n + 1] - p.cu[n]);
-        if (p.N > kPlanThreads)                   // (few sequences: all threads together, below)
-            for (int i = 0; i < k; ++i) p.unit_seq[at + i] = n;
+    for (int r = 0; r < per; ++r) {               // (as many rounds for every thread of a wave)
+        const int n = n0 + r;
+        const int k = n < n1 ? units_of(p.cu[n + 1] - p.cu[n]) : 0;
+        if (n < n1) p.unit_off[n] = at;
+        if (p.N > kPlanThreads) {                 // (few sequences: all threads together, below)
+            // a long sequence's units by the whole wave
+            for (uint64_t wide = __ballot(k > kWave); wide != 0; wide &= wide - 1) {
+                const int from = __ffsll(static_cast<unsigned long long>(wide)) - 1;
+                const int first_of = __shfl(at, from, kWave), units = __shfl(k, from, kWave), seq = __shfl(n, from, kWave);
+                for (int i = tid % kWave; i < units; i += kWave) p.unit_seq[first_of + i] = seq;
+            }
+            if (k <= kWave)
+                for (int i = 0; i < k; ++i) p.unit_seq[at + i] = n;
+        }
         at += k;
     }
     if (tid == 0) p.unit_off[p.N] = total;

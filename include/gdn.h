@@ -639,14 +639,15 @@ typedef struct {
 } gdn_linear_io;
 
 /* Bytes of device workspace gdn_linear needs; 0 where it needs none (up to 16
- * and from 65 rows on, and with a short K or a large N) and on error
+ * and from 257 rows on, and with a short K or a large N) and on error
  * (gdn_last_error() tells). */
 size_t gdn_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Enqueue the layer.  Up to 16 rows run on a weight-streaming kernel, up to
- * 64 with K in parts (one more kernel adds them), more on tiles.  Each sums
- * in an order that does not depend on the other rows, but the orders differ,
- * so a row's bits may change when M crosses 16 or 64.  workspace: device
+ * 64 and up to 256 with K in as many parts as N and K suggest (one more
+ * kernel adds them), more on tiles.  Each sums in an order that does not
+ * depend on the other rows, but the orders differ, so a row's bits may change
+ * when M crosses 16, 64 or 256.  workspace: device
  * memory, 256-byte aligned, not shared with a concurrently running call (its
  * contents need not start at zero). */
 gdn_status gdn_linear(const gdn_linear_io* io, void* workspace,

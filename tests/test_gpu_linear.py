@@ -81,7 +81,8 @@ def reference(x, w, bias, act, res):
 
 
 SHAPES = [(1, 1, 8), (1, 65, 2048), (2, 200, 72), (16, 16, 128), (17, 33, 136), (33, 100, 640), (64, 130, 256),
-          (20, 70, 1000), (33, 200, 2064), (64, 40, 4096), (65, 7, 8), (65, 64, 64), (100, 129, 72), (129, 255, 200), (300, 300, 1000), (64, 50, 0), (70, 50, 0)]
+          (20, 70, 1000), (33, 200, 2064), (64, 40, 4096), (65, 7, 8), (65, 64, 64), (100, 129, 72), (129, 255, 200), (300, 300, 1000), (64, 50, 0), (70, 50, 0),
+          (65, 130, 2048), (200, 70, 4104), (256, 513, 2056)]
 
 
 @pytest.mark.parametrize("act", list(ACTS))
@@ -258,6 +259,10 @@ def test_same_bits_next_to_other_rows_and_again():
     assert torch.equal(gdn.linear(x[100:300], w), y[100:300])
     few, stream = gdn.linear(x[:64], w), gdn.linear(x[:16], w)
     assert torch.equal(gdn.linear(x[5:6], w), stream[5:6]) and torch.equal(gdn.linear(x[30:50], w), few[30:50])
+    g, x2, w2 = data(256, 300, 4104, 9)
+    some = gdn.linear(x2, w2)
+    for r in (slice(0, 65), slice(100, 229), slice(56, 256)):
+        assert torch.equal(gdn.linear(x2[r], w2), some[r]), r
     dy = torch.randn((700, 600), generator=g, device="cuda").to(torch.bfloat16)
     a = gdn.linear_backward(dy, x, w, want_dbias=True)
     for _ in range(3):

@@ -383,7 +383,8 @@ def test_graph_replays_and_other_stream():
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("lens", [[1, 0] * 256, [1] * 513, [3, 130, 0] * 100, [2, 0, 257] * 250], ids=["512", "513", "300", "750"])
+@pytest.mark.parametrize("lens", [[1, 0] * 256, [1] * 513, [3, 130, 0] * 100, [2, 0, 257] * 250, [1] * 200 + [8400, 9000] + [0] * 100 + [70],
+                                  [8200] + [5] * 600], ids=["512", "513", "300", "750", "long", "first"])
 def test_many_sequences(lens):
     """On both sides of the counts at which the layout of the units changes."""
     c = Case(lens, 20, "bf16", seed=21)

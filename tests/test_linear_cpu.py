@@ -45,12 +45,15 @@ def test_empty_outputs_are_no_calls():
 
 
 def test_forward_workspace():
-    """Rows 17 .. 64 keep [parts][M][N] fp32 sums when K is at least 512."""
+    """Rows 17 .. 64 keep [parts][M][N] fp32 sums when K is at least 512, rows
+    65 .. 256 when it is at least 2048 and N is small."""
     L = gdn.lib()
-    for M, N, K in ((16, 2048, 4096), (65, 2048, 4096), (32, 2048, 504), (0, 64, 4096)):
+    for M, N, K in ((16, 2048, 4096), (257, 2048, 4096), (65, 12352, 4096), (256, 2048, 2040), (32, 2048, 504), (0, 64, 4096)):
         assert L.gdn_linear_workspace_bytes(M, N, K) == 0 and L.gdn_last_error() == b""
     need = L.gdn_linear_workspace_bytes(40, 72, 1024)
     assert need > 0 and need % 256 == 0 and need % (4 * 40 * 72) < 256
+    need_some = L.gdn_linear_workspace_bytes(70, 72, 2048)
+    assert need_some > 0 and need_some % (4 * 70 * 72) < 256
     assert L.gdn_linear_workspace_bytes(1, 1, 3) == 0 and L.gdn_last_error()
     for ws, n in ((None, NWS), (WS + 8, NWS), (WS, need - 1)):
         assert L.gdn_linear(ctypes.byref(_io(M=40, K=1024)), ws, n, None) == gdn.GDN_ERR_WORKSPACE
