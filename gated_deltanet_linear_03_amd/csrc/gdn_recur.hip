@@ -348,6 +348,29 @@ __device__ __forceinline__ Q load_edge(const typename Q::T* row, const Lane& l, 
     return q;
 }
 
+// Rows r0 .. r0 + ROWS - 1 of a tile of `rows` rows at `base`; those past the
+// end read the last one.
+// FAST: one address and offsets of 32 bits.  It takes registers from the whole
+// tiles of the kernel that it is compiled into: forward without saved states,
+// 131072 x 2048 in one sequence 646 us (618 without FAST), 60000 x 1024 in 600
+// sequences 205 us (296).
+template <typename Q, int ROWS, bool ONCE, bool FAST>
+__device__ __forceinline__ void load_some(Q* to, const typename Q::T* base, int64_t stride, int r0, int rows, const Lane& l, int D) {
+    const int at = r0 < rows ? r0 : rows - 1, more = rows - 1 - at;
+    if (FAST && D >= kVC) {
+        const uint32_t ld = static_cast<uint32_t>(stride), off = static_cast<uint32_t>(at) * ld + l.lc;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            to[i] = Q::template load<ONCE>(
+                lane_ptr(base, (off + __umul24(i < more ? i : more, ld)) * static_cast<uint32_t>(sizeof(typename Q::T))));
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) to[i] = to[i].dropped(l.drop);
+    } else {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) to[i] = load_edge<Q>(base + (r0 + i < rows ? r0 + i : rows - 1) * stride, l, D);
+    }
+}
+
 // ---- forward ---------------------------------------------------------------
 struct FwdShared {
     float2 step[kWaves][kCh];                  // (A, H) of a wave's rows
@@ -355,8 +378,8 @@ struct FwdShared {
     int tile;
 };
 
-// KEEP: the inputs are read again by a backward pass
-template <bool BF16, bool GATE, bool KEEP>
+// KEEP: the inputs are read again by a backward pass; FAST: see load_some
+template <bool BF16, bool GATE, bool KEEP, bool FAST>
 struct FwdTile {
     using Q = Quad<BF16>;
     using T = typename Q::T;
@@ -382,11 +405,7 @@ struct FwdTile {
                     for (int i = 0; i < kFwdRows; ++i) to[i] = to[i].dropped(l.drop);
                 }
             } else {
-#pragma unroll
-                for (int i = 0; i < kFwdRows; ++i) {
-                    const int r = r0 + i < pl.rows ? r0 + i : pl.rows - 1;
-                    to[i] = load_edge<Q>(static_cast<const T*>(from) + (pl.row0 + r) * stride, l, p.D);
-                }
+                load_some<Q, kFwdRows, !KEEP, FAST>(to, static_cast<const T*>(from) + pl.row0 * stride, stride, r0, pl.rows, l, p.D);
             }
         };
         fetch(a, p.a, p.as);
@@ -492,7 +511,7 @@ __device__ __forceinline__ int draw_ticket(const RecurParams& p, int cg) {
 // 24 us.  (Work-groups that stay and draw
 // tile after tile, with the next ticket drawn early, were slower: they need
 // more registers, so fewer run at once.)
-template <bool BF16, bool GATE, bool KEEP>
+template <bool BF16, bool GATE, bool KEEP, bool FAST>
 __global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams p) {
     __shared__ FwdShared sh;
     const int total = p.unit_off[p.N];            // < 0: the call's indices were rejected
@@ -506,7 +525,7 @@ __global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams 
     const int tile = __builtin_amdgcn_readfirstlane(sh.tile);
     if (tile >= total) return;
     const Place pl = unit_place(p, tile);
-    FwdTile<BF16, GATE, KEEP> t;
+    FwdTile<BF16, GATE, KEEP, FAST> t;
     const Part part = part_of(pl.rows == kRecurUnit, c0, p.D);
     if (part == kWhole) t.template load<kWhole>(p, pl, l, nrate2, bias);
     else if (part == kEdge) t.template load<kEdge>(p, pl, l, nrate2, bias);
@@ -568,7 +587,7 @@ __global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) 
     const int c = c0 + l.lane;
     const int64_t at = static_cast<int64_t>(state_slot(p.slots, seq)) * p.D + c;
     if (l.wave == 0) sh.start[l.lane] = p.h0 && c < p.D ? p.h0[at] : 0.f;
-    FwdTile<BF16, GATE, KEEP> t;
+    FwdTile<BF16, GATE, KEEP, false> t;
     const int units = units_of(len);
     for (int k = 0; k < units && len > 0; ++k) {
         const Place pl = place_of(lo, len, seq, k);
@@ -716,10 +735,7 @@ struct BwdTile {
                     for (int i = 0; i < L; ++i) to[i] = to[i].dropped(l.drop);
                 }
             } else {
-#pragma unroll
-                for (int i = 0; i < L; ++i)
-                    to[i] = load_edge<Q>(static_cast<const T*>(from) + (row0 + (r0 + i < rows ? r0 + i : rows - 1)) * stride, l,
-                                         p.D);
+                load_some<Q, L, true, true>(to, static_cast<const T*>(from) + row0 * stride, stride, r0, rows, l, p.D);
             }
         };
         fetch(a, p.a, p.as);
@@ -857,10 +873,10 @@ struct BwdTile {
 // grid: channel groups x kHalves x the bound on units; the tiles of a sequence
 // are taken from its end.  The rows' h are run again from the state the
 // forward pass saved at the tile's first row.
-// 32768 x 4096 bf16: 693 us, 3.5 TB/s, the vector units 69% busy (127
+// 32768 x 4096 bf16: 665 us, 3.6 TB/s, the vector units 69% busy (127
 // instructions an element).  Three waves a SIMD where the registers allow it:
 // with the gates' values kept (228 registers, two waves) the training step of
-// that size took 1.12 ms, with a's gate computed again 1.07 (1.05 now); fp32
+// that size took 1.12 ms, with a's gate computed again 1.07 (1.00 now); fp32
 // rows with a gate would spill.  Work-groups of 512 threads that keep all of
 // it in 122 registers: 1.18, as only two share a compute unit.
 template <bool BF16, bool GATE>
@@ -1059,8 +1075,12 @@ hipError_t launch_recur_forward(const RecurParams& p, bool bf16, hipStream_t s) 
     hipError_t e = launch_plan(p, s);
     if (e != hipSuccess) return e;
     const int64_t grid = static_cast<int64_t>(p.groups) * p.tiles;
-    if (p.saved) GDN_RECUR_CALL(recur_forward_kernel, grid, kThreads, , true);
-    else GDN_RECUR_CALL(recur_forward_kernel, grid, kThreads, , false);
+    // sequences of fewer than four units on average: a quarter of the tiles or
+    // more is cut (33000 x 1024, 300 tokens each: 114 us with FAST, 118
+    // without; 900 tokens each: 104 and 100)
+    if (p.saved) GDN_RECUR_CALL(recur_forward_kernel, grid, kThreads, , true, true);
+    else if (p.T / p.N < 4 * kRecurUnit) GDN_RECUR_CALL(recur_forward_kernel, grid, kThreads, , false, true);
+    else GDN_RECUR_CALL(recur_forward_kernel, grid, kThreads, , false, false);
     return hipGetLastError();
 }
 
