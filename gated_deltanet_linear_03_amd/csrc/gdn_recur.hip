@@ -327,14 +327,12 @@ __device__ __forceinline__ void wave_compose(const Lane& l, float* A, float* H) 
 
 // This lane's start: `s` through the inclusive (A, H) of the group before
 // it in the wave.
-template <bool REV>
 __device__ __forceinline__ void wave_start(const Lane& l, const float* A, const float* H, float* s) {
-    const int g = l.lane / kChLanes, at = REV ? kGroupsPerWave - 1 - g : g;
-    const int from = (REV ? l.lane + kChLanes : l.lane - kChLanes) & (kWave - 1);
+    const int from = (l.lane - kChLanes) & (kWave - 1);
 #pragma unroll
     for (int j = 0; j < kVC; ++j) {
         const float a = __shfl(A[j], from, kWave), h = __shfl(H[j], from, kWave);
-        if (at > 0) s[j] = fmaf(a, s[j], h);
+        if (l.lane >= kChLanes) s[j] = fmaf(a, s[j], h);
     }
 }
 
@@ -450,7 +448,7 @@ struct FwdTile {
                 s[j] = fmaf(e.x, s[j], e.y);
             }
         }
-        wave_start<false>(l, A, H, s);
+        wave_start(l, A, H, s);
         constexpr int kPer = kGroups / kHalves;   // row groups between saved states
         if (p.saved && l.rg % kPer == 0)
             Quad<false>::store(p.saved + (kHalves * unit_index + l.rg / kPer) * p.D + l.c, s, l.nv);
@@ -484,11 +482,11 @@ __device__ __forceinline__ void load_params(const RecurParams& p, const Lane& l,
 }
 
 // (A, H) of a whole tile, for channel `lane`
-__device__ __forceinline__ float2 tile_step(const float2 (*step)[kCh], int lane, bool rev) {
+__device__ __forceinline__ float2 tile_step(const float2 (*step)[kCh], int lane) {
     float A = 1.f, H = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        const float2 e = step[rev ? kWaves - 1 - w : w][lane];
+        const float2 e = step[w][lane];
         H = fmaf(e.x, H, e.y);
         A *= e.x;
     }
@@ -534,7 +532,7 @@ __global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams 
     __syncthreads();
     if (l.wave == 0) {
         const int c = c0 + l.lane;
-        const float2 e = pl.rows > 0 ? tile_step(sh.step, l.lane, false) : make_float2(1.f, 0.f);
+        const float2 e = pl.rows > 0 ? tile_step(sh.step, l.lane) : make_float2(1.f, 0.f);
         uint64_t* w = p.words + static_cast<int64_t>(tile) * p.groups * kCh + c;
         const bool last = pl.unit + 1 == pl.units;
         float s = 0.f;
@@ -600,7 +598,7 @@ __global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) 
         else t.template finish<kSome>(p, sh, pl, l, static_cast<int64_t>(first_unit) + k);
         float after = 0.f;
         if (l.wave == 0) {
-            const float2 e = tile_step(sh.step, l.lane, false);
+            const float2 e = tile_step(sh.step, l.lane);
             after = fmaf(e.x, sh.start[l.lane], e.y);
         }
         __syncthreads();
@@ -689,7 +687,9 @@ __global__ __launch_bounds__(kPlanThreads) void recur_plan_kernel(RecurParams p)
 
 // ---- backward --------------------------------------------------------------
 struct BwdShared {
-    float2 fwd[kWaves][kCh], rev[kWaves][kCh];
+    // each row group's (A, H), inclusive over its wave (kept here, not in
+    // registers, while the tile waits)
+    float2 fwd[kGroups][kCh], rev[kGroups][kCh];
     float2 sums[kWaves][kCh];
     float2 par[kCh];                              // nrate2, bias (kept here, not in registers, while the tile waits)
     float start[kCh];                             // c past the tile's last row
@@ -710,7 +710,6 @@ struct BwdTile {
     float al[L][kVC], u[L][kVC];                  // alpha; u, later h before the row
     float wb[L][kVC];                             // w beta
     float xn[L][kVC], xk[L][kVC];                 // x (1 - beta), x alpha^2 / w^2 (0 where w is)
-    float A[kVC], H[kVC], Ar[kVC], Hr[kVC];       // inclusive over the wave's groups, both ways
 
     // dy silu(z)
     __device__ __forceinline__ float into_h(int i, int j) const {
@@ -720,9 +719,10 @@ struct BwdTile {
     }
 
     template <Part PART>
-    __device__ __forceinline__ void load(const RecurParams& p, const Lane& l, int64_t row0, int rows, const float* nrate2,
-                                         const float* bias) {
+    __device__ __forceinline__ void load(const RecurParams& p, BwdShared& sh, const Lane& l, int64_t row0, int rows,
+                                         const float* nrate2, const float* bias) {
         const int r0 = l.rg * L;
+        float A[kVC], H[kVC], Ar[kVC], Hr[kVC];
         Q x[L], b[L];
         auto fetch = [&](Q* to, const void* from, int64_t stride) {
             if constexpr (PART != kSome) {
@@ -774,16 +774,10 @@ struct BwdTile {
         }
         wave_compose<false>(l, A, H);
         wave_compose<true>(l, Ar, Hr);
-    }
-
-    __device__ __forceinline__ void publish(BwdShared& sh, const Lane& l) {
-        if (l.lane / kChLanes == kGroupsPerWave - 1) {
 #pragma unroll
-            for (int j = 0; j < kVC; ++j) sh.fwd[l.wave][l.cl * kVC + j] = make_float2(A[j], H[j]);
-        }
-        if (l.lane / kChLanes == 0) {
-#pragma unroll
-            for (int j = 0; j < kVC; ++j) sh.rev[l.wave][l.cl * kVC + j] = make_float2(Ar[j], Hr[j]);
+        for (int j = 0; j < kVC; ++j) {
+            sh.fwd[l.rg][l.cl * kVC + j] = make_float2(A[j], H[j]);
+            sh.rev[l.rg][l.cl * kVC + j] = make_float2(Ar[j], Hr[j]);
         }
     }
 
@@ -805,20 +799,15 @@ struct BwdTile {
             s[j] = sh.before[l.cl * kVC + j];
             r[j] = sh.start[l.cl * kVC + j];
         }
-        for (int w = 0; w < l.wave; ++w)
+        // through the waves before this one, then through its groups before this lane's
+        auto apply = [&](const float2* t, float* v) {
 #pragma unroll
-            for (int j = 0; j < kVC; ++j) {
-                const float2 t = sh.fwd[w][l.cl * kVC + j];
-                s[j] = fmaf(t.x, s[j], t.y);
-            }
-        for (int w = kWaves - 1; w > l.wave; --w)
-#pragma unroll
-            for (int j = 0; j < kVC; ++j) {
-                const float2 t = sh.rev[w][l.cl * kVC + j];
-                r[j] = fmaf(t.x, r[j], t.y);
-            }
-        wave_start<false>(l, A, H, s);
-        wave_start<true>(l, Ar, Hr, r);
+            for (int j = 0; j < kVC; ++j) v[j] = fmaf(t[l.cl * kVC + j].x, v[j], t[l.cl * kVC + j].y);
+        };
+        for (int w = 0; w < l.wave; ++w) apply(sh.fwd[w * kGroupsPerWave + kGroupsPerWave - 1], s);
+        for (int w = kWaves - 1; w > l.wave; --w) apply(sh.rev[w * kGroupsPerWave], r);
+        if (l.rg % kGroupsPerWave > 0) apply(sh.fwd[l.rg - 1], s);
+        if (l.rg % kGroupsPerWave < kGroupsPerWave - 1) apply(sh.rev[l.rg + 1], r);
         const int r0 = l.rg * L;
         // a row's four gradients at (row0 + r0 + i); strides are of 22 bits, so offsets are of 32
         auto put = [&](void* to, int64_t stride, int i, const float* f) {
@@ -903,14 +892,18 @@ __global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backwar
 #pragma unroll
         for (int j = 0; j < kVC; ++j) sh.par[l.cl * kVC + j] = make_float2(nrate2[j], bias[j]);
     }
-    if (part == kWhole) t.template load<kWhole>(p, l, row0, rows, nrate2, bias);
-    else if (part == kEdge) t.template load<kEdge>(p, l, row0, rows, nrate2, bias);
-    else if (rows > 0) t.template load<kSome>(p, l, row0, rows, nrate2, bias);
-    if (rows > 0) t.publish(sh, l);
+    if (part == kWhole) t.template load<kWhole>(p, sh, l, row0, rows, nrate2, bias);
+    else if (part == kEdge) t.template load<kEdge>(p, sh, l, row0, rows, nrate2, bias);
+    else if (rows > 0) t.template load<kSome>(p, sh, l, row0, rows, nrate2, bias);
     __syncthreads();
     if (l.wave == 0) {
         const int ch = c0 + l.lane;
-        const float2 e = rows > 0 ? tile_step(sh.rev, l.lane, true) : make_float2(1.f, 0.f);
+        float2 e = make_float2(1.f, 0.f);         // (A, H) of the whole tile
+        for (int w = kWaves - 1; w >= 0 && rows > 0; --w) {
+            const float2 g = sh.rev[w * kGroupsPerWave][l.lane];
+            e.y = fmaf(g.x, e.y, g.y);
+            e.x *= g.x;
+        }
         uint64_t* w = p.words + static_cast<int64_t>(tile) * p.groups * kCh + ch;
         const bool first = pl.unit == 0 && tile % kHalves == 0;
         const int behind = kHalves * (pl.units - pl.unit) - 1 - tile % kHalves;   // tiles of the sequence after this one
