@@ -76,7 +76,7 @@ __device__ __forceinline__ float apply_word(uint64_t w, float s) {
     return hi == kState ? lo : fmaf(__uint_as_float(hi), s, lo);
 }
 
-constexpr int kWindow = 4;                        // words looked at in one go (4, 8: the same; 16: 1% slower)
+constexpr int kWindow = 4;                        // words looked at in one go (8: 6% slower at 131072 x 2048, whose kernel then takes 136 registers instead of 128)
 
 // The state after the predecessor tile.  Predecessor k (1 = the nearest,
 // `depth` = the first tile of the sequence) has its word at w + k * step.
@@ -862,10 +862,10 @@ struct BwdTile {
 // grid: channel groups x kHalves x the bound on units; the tiles of a sequence
 // are taken from its end.  The rows' h are run again from the state the
 // forward pass saved at the tile's first row.
-// 32768 x 4096 bf16: 665 us, 3.6 TB/s, the vector units 69% busy (127
+// 32768 x 4096 bf16: 656 us, 3.7 TB/s, the vector units 69% busy (127
 // instructions an element).  Three waves a SIMD where the registers allow it:
 // with the gates' values kept (228 registers, two waves) the training step of
-// that size took 1.12 ms, with a's gate computed again 1.07 (1.00 now); fp32
+// that size took 1.12 ms, with a's gate computed again 1.07 (0.98 now); fp32
 // rows with a gate would spill.  Work-groups of 512 threads that keep all of
 // it in 122 registers: 1.18, as only two share a compute unit.
 template <bool BF16, bool GATE>
