@@ -303,6 +303,27 @@ def test_graph_replays_and_other_stream():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("M, N, K", [(40, 24, 64), (300, 200, 264), (1537, 1000, 520), (2048, 2040, 1032), (4096, 4104, 1032),
+                                     (5000, 72, 136)])
+def test_each_gradient_alone(M, N, K):
+    """Tiles, parts and the bias sums are laid out by the sizes alone: an output
+    asked for by itself has the bits that it has among the others."""
+    g, x, w = data(M, N, K, 14)
+    dy = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+    pre = torch.randn((M, N), generator=g, device="cuda").to(torch.bfloat16)
+    kw = dict(preact=pre, act=gdn.GDN_ACT_SILU)
+    every = gdn.linear_backward(dy, x, w, want_dbias=True, **kw)
+    for n in ("dx", "dw", "dbias"):
+        one = gdn.linear_backward(dy, x, w, want_dx=n == "dx", want_dw=n == "dw", want_dbias=n == "dbias", **kw)
+        if n == "dbias":
+            # another order of at most 96 additions a value (4 rows, 8 row groups, M / 32 / 4 blocks, 16 slices), each
+            # to 2^-24 of a partial sum; |silu'| < 1.1
+            lim = 2 * 96 * 2.0 ** -24 * 1.1 * dy.double().abs().sum(0)
+            assert ((one[n].double() - every[n].double()).abs() <= lim).all(), n
+        else:
+            assert torch.equal(one[n], every[n]), n
+
+
 def test_rows_past_4_gib():
     """Operands and outputs whose rows lie 131072 elements apart, over 5 GiB:
     the same bits as dense ones."""

@@ -441,6 +441,30 @@ def test_two_calls_at_once():
                     assert torch.equal(r[n], want[k][n]), (k, n)
 
 
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of different lengths in one workspace, replayed in
+    turn on one stream."""
+    cs = [Case([700, 900], 96, "bf16", seed=26), Case([2500], 96, "bf16", seed=27)]
+    ws = torch.empty(max(gdn.recur_workspace_bytes(c.rec, c.N, c.T) for c in cs), dtype=torch.uint8, device="cuda")
+    want = [c.forward()["out"] for c in cs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in cs:
+            c.forward(workspace=ws)
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in cs], []
+    for c, gr in zip(cs, graphs):
+        with torch.cuda.graph(gr):
+            outs.append(c.forward(workspace=ws)["out"])
+    for k in (0, 1, 1, 0, 1, 0):
+        outs[k].zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[k], want[k]), k
+        assert torch.equal(cs[1 - k].forward()["out"], want[1 - k])
+
+
 def test_no_sequences():
     c = Case([5], 8, "bf16", seed=25)
     none = {n: c.t[n][:0] for n in "xabz"}
