@@ -691,7 +691,8 @@ struct BwdShared {
     // registers, while the tile waits)
     float2 fwd[kGroups][kCh], rev[kGroups][kCh];
     float2 sums[kWaves][kCh];
-    float2 par[kCh];                              // nrate2, bias (kept here, not in registers, while the tile waits)
+    // each lane's own, for the same reason: g log2(e), and da / dg
+    f32x4 g2[kBwdRows][kThreads], sg[kBwdRows][kThreads];
     float start[kCh];                             // c past the tile's last row
     float before[kCh];                            // the state before its first row
     int tile;
@@ -699,14 +700,15 @@ struct BwdShared {
 
 // A lane's rows of a backward tile: what the second half (after the tile's
 // start is known) needs of each element.  Registers decide how many
-// work-groups share a compute unit, so what comes from z and dy, and what a's
-// gate gives beside alpha, is computed again from their packed rows.
+// work-groups share a compute unit, so what comes from z and dy is computed
+// again from their packed rows, and what a's gate gives beside alpha waits in
+// LDS.
 template <bool BF16, bool GATE>
 struct BwdTile {
     using Q = Quad<BF16>;
     using T = typename Q::T;
     static constexpr int L = kBwdRows;
-    Q a[L], dy[L], z[L];
+    Q dy[L], z[L];
     float al[L][kVC], u[L][kVC];                  // alpha; u, later h before the row
     float wb[L][kVC];                             // w beta
     float xn[L][kVC], xk[L][kVC];                 // x (1 - beta), x alpha^2 / w^2 (0 where w is)
@@ -723,7 +725,7 @@ struct BwdTile {
                                          const float* nrate2, const float* bias) {
         const int r0 = l.rg * L;
         float A[kVC], H[kVC], Ar[kVC], Hr[kVC];
-        Q x[L], b[L];
+        Q a[L], x[L], b[L];
         auto fetch = [&](Q* to, const void* from, int64_t stride) {
             if constexpr (PART != kSome) {
                 const T* base = static_cast<const T*>(from) + row0 * stride;
@@ -745,6 +747,7 @@ struct BwdTile {
         if constexpr (GATE) fetch(z, p.z, p.zs);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
+            f32x4 g2, sg;
 #pragma unroll
             for (int j = 0; j < kVC; ++j) {
                 const float v = a[i].get(j) + bias[j], xj = x[i].get(j);
@@ -756,12 +759,17 @@ struct BwdTile {
                 wb[i][j] = __builtin_amdgcn_sqrtf(g.q) * beta;
                 al[i][j] = g.alpha;
                 u[i][j] = wb[i][j] * xj;
+                const float rv = __builtin_amdgcn_rcpf(1.f + g.e);
+                g2[j] = g.g2;
+                sg[j] = (v < 0.f ? g.e * rv : rv) * (nrate2[j] * kLn2);
                 if constexpr (PART == kSome) {
                     if (r0 + i >= rows) { al[i][j] = 1.f; u[i][j] = 0.f; }
                 }
                 H[j] = i == 0 ? u[i][j] : fmaf(al[i][j], H[j], u[i][j]);
                 A[j] = i == 0 ? al[i][j] : A[j] * al[i][j];
             }
+            sh.g2[i][threadIdx.x] = g2;
+            sh.sg[i][threadIdx.x] = sg;
         }
         // c_t = alpha_t (c_{t+1} + e_t); a row past the end hands c on
 #pragma unroll
@@ -789,13 +797,9 @@ struct BwdTile {
 #pragma unroll
             for (int i = 0; i < L; ++i) z[i].forget();
         }
-#pragma unroll
-        for (int i = 0; i < L; ++i) a[i].forget();
-        float s[kVC], r[kVC], nrate2[kVC], bias[kVC];
+        float s[kVC], r[kVC];
 #pragma unroll
         for (int j = 0; j < kVC; ++j) {
-            nrate2[j] = sh.par[l.cl * kVC + j].x;
-            bias[j] = sh.par[l.cl * kVC + j].y;
             s[j] = sh.before[l.cl * kVC + j];
             r[j] = sh.start[l.cl * kVC + j];
         }
@@ -834,6 +838,7 @@ struct BwdTile {
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
             float dx[kVC], da[kVC], db[kVC];
+            const f32x4 g2 = sh.g2[i][threadIdx.x], sg = sh.sg[i][threadIdx.x];
 #pragma unroll
             for (int j = 0; j < kVC; ++j) {
                 const bool on = PART == kWhole || r0 + i < rows;
@@ -843,12 +848,9 @@ struct BwdTile {
                 dx[j] = G * wb[i][j];
                 db[j] = dx[j] * xn[i][j];
                 const float dg = fmaf(aG, u[i][j], -dx[j] * xk[i][j]);
-                const float v = a[i].get(j) + bias[j];
-                const float ev = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v)), rv = __builtin_amdgcn_rcpf(1.f + ev);
-                const float g2 = nrate2[j] * fmaf(log1p_unit_over(ev), ev, fmaxf(v, 0.f));
-                da[j] = dg * ((v < 0.f ? ev * rv : rv) * (nrate2[j] * kLn2));
+                da[j] = dg * sg[j];
                 if (on) {
-                    sa[j] = fmaf(dg, g2, sa[j]);
+                    sa[j] = fmaf(dg, g2[j], sa[j]);
                     sb[j] += da[j];
                 }
             }
@@ -862,14 +864,13 @@ struct BwdTile {
 // grid: channel groups x kHalves x the bound on units; the tiles of a sequence
 // are taken from its end.  The rows' h are run again from the state the
 // forward pass saved at the tile's first row.
-// 32768 x 4096 bf16: 656 us, 3.7 TB/s, the vector units 69% busy (127
-// instructions an element).  Three waves a SIMD where the registers allow it:
-// with the gates' values kept (228 registers, two waves) the training step of
-// that size took 1.12 ms, with a's gate computed again 1.07 (0.98 now); fp32
-// rows with a gate would spill.  Work-groups of 512 threads that keep all of
-// it in 122 registers: 1.18, as only two share a compute unit.
+// 32768 x 4096 bf16: 615 us, 3.9 TB/s.  Three waves a SIMD: with all of the
+// gates' values in registers (228, two waves) the training step of that size
+// took 1.12 ms, with a's gate computed again 1.00, with it in LDS 0.955.
+// Work-groups of 512 threads that keep all of it in 122 registers: 1.18, as
+// only two share a compute unit.
 template <bool BF16, bool GATE>
-__global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backward_kernel(RecurParams p) {
+__global__ __launch_bounds__(kThreads, 3) void recur_backward_kernel(RecurParams p) {
     __shared__ BwdShared sh;
     const int total = kHalves * p.unit_off[p.N];
     const int cg = blockIdx.x % p.groups;
@@ -888,10 +889,6 @@ __global__ __launch_bounds__(kThreads, BF16 || !GATE ? 3 : 2) void recur_backwar
     const int64_t row0 = pl.row0 + t0;
     const Part part = part_of(rows == kBwdTile, c0, p.D);
     BwdTile<BF16, GATE> t;
-    if (threadIdx.x < kChLanes) {
-#pragma unroll
-        for (int j = 0; j < kVC; ++j) sh.par[l.cl * kVC + j] = make_float2(nrate2[j], bias[j]);
-    }
     if (part == kWhole) t.template load<kWhole>(p, sh, l, row0, rows, nrate2, bias);
     else if (part == kEdge) t.template load<kEdge>(p, sh, l, row0, rows, nrate2, bias);
     else if (rows > 0) t.template load<kSome>(p, sh, l, row0, rows, nrate2, bias);
