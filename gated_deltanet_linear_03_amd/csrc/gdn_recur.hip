@@ -864,7 +864,7 @@ struct BwdTile {
 // grid: channel groups x kHalves x the bound on units; the tiles of a sequence
 // are taken from its end.  The rows' h are run again from the state the
 // forward pass saved at the tile's first row.
-// 32768 x 4096 bf16: 615 us, 3.9 TB/s.  Three waves a SIMD: with all of the
+// 32768 x 4096 bf16: 615 to 628 us, 3.9 TB/s.  Three waves a SIMD: with all of the
 // gates' values in registers (228, two waves) the training step of that size
 // took 1.12 ms, with a's gate computed again 1.00, with it in LDS 0.955.
 // Work-groups of 512 threads that keep all of it in 122 registers: 1.18, as
