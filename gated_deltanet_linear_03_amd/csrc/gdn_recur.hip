@@ -9,6 +9,11 @@
 //   G_t = dy_t silu(z_t) + c_{t+1},   c_t = alpha_t c_{t+1} + alpha_t dy_t silu(z_t)
 //   dx = G w beta, db = G w x beta (1 - beta), dz = dy h silu'(z),
 //   dg = alpha G (h_{t-1} - beta x alpha / w), da = -dg exp(A_log) sigmoid(v).
+// 1 / w grows without end as alpha goes to 1, while sigmoid(v) in da, and g in
+// dA_log's dg g, fall with w^2: dg is formed from 1 / w itself, at most 2^63,
+// never from 1 / w^2, and where w^2 is below the smallest normal number both w
+// and 1 / w count as 0 (what they stand for in a gradient is below 2^-63 of
+// its other factors).
 // Both directions are first-order recurrences of the form s <- A s + H, and
 // such steps compose: (A2, H2) after (A1, H1) is (A2 A1, A2 H1 + H2).
 //
@@ -711,7 +716,7 @@ struct BwdTile {
     Q dy[L], z[L];
     float al[L][kVC], u[L][kVC];                  // alpha; u, later h before the row
     float wb[L][kVC];                             // w beta
-    float xn[L][kVC], xk[L][kVC];                 // x (1 - beta), x alpha^2 / w^2 (0 where w is)
+    float xn[L][kVC], xk[L][kVC];                 // x (1 - beta), beta x alpha / w (0 where w is)
 
     // dy silu(z)
     __device__ __forceinline__ float into_h(int i, int j) const {
@@ -752,11 +757,11 @@ struct BwdTile {
             for (int j = 0; j < kVC; ++j) {
                 const float v = a[i].get(j) + bias[j], xj = x[i].get(j);
                 const Gate g = gate(v, nrate2[j]);
-                // g -> 0: alpha^2 / w^2 grows as sigmoid(v), which multiplies it, falls
-                xk[i][j] = g.q > 0.f ? xj * (g.alpha * g.alpha * __builtin_amdgcn_rcpf(g.q)) : 0.f;
                 const float beta = sigmoid_fast(b[i].get(j));
+                const float over = g.q >= 0x1p-126f ? __builtin_amdgcn_rsqf(g.q) : 0.f;   // 1 / w
                 xn[i][j] = xj * (1.f - beta);
-                wb[i][j] = __builtin_amdgcn_sqrtf(g.q) * beta;
+                wb[i][j] = g.q * over * beta;
+                xk[i][j] = xj * beta * g.alpha * over;
                 al[i][j] = g.alpha;
                 u[i][j] = wb[i][j] * xj;
                 const float rv = __builtin_amdgcn_rcpf(1.f + g.e);
@@ -847,7 +852,7 @@ struct BwdTile {
                 r[j] = aG;
                 dx[j] = G * wb[i][j];
                 db[j] = dx[j] * xn[i][j];
-                const float dg = fmaf(aG, u[i][j], -dx[j] * xk[i][j]);
+                const float dg = aG * (u[i][j] - xk[i][j]);
                 da[j] = dg * sg[j];
                 if (on) {
                     sa[j] = fmaf(dg, g2[j], sa[j]);

@@ -589,7 +589,9 @@ size_t gdn_recur_backward_workspace_bytes(const gdn_recur* recur, int32_t N, int
 
 /* Enqueue the backward pass of a gdn_recur_forward call: io as in that call
  * (x, a, b, z, cu_seqlens and the saved states it wrote are read; y, the
- * states and the pool entries are not used). */
+ * states and the pool entries are not used).  The gradients divide by
+ * sqrt(1 - alpha_t^2): where 1 - alpha_t^2 is below 2^-126 that term counts as
+ * 0, as does the root itself. */
 gdn_status gdn_recur_backward(const gdn_recur* recur, const gdn_recur_io* io,
                               const gdn_recur_grad* grad, void* workspace,
                               size_t workspace_bytes, void* stream);
