@@ -57,6 +57,18 @@ constexpr int kBwdRows = kBwdTile / kGroups;      // rows per lane, backward (4)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// A grid dimension holds fewer than 2^32 work-items, and a launch with more runs
+// a part of them without an error: past kGridX work-groups a call goes on in
+// the second dimension (the last row of groups may have some with nothing to do).
+constexpr int kGridX = 1 << 22;
+
+__device__ __forceinline__ uint32_t group_index() { return blockIdx.y * static_cast<uint32_t>(kGridX) + blockIdx.x; }
+
+dim3 grid_of(int64_t groups) {
+    return groups <= kGridX ? dim3(static_cast<unsigned>(groups))
+                            : dim3(kGridX, static_cast<unsigned>((groups + kGridX - 1) / kGridX));
+}
+
 // ---- words: what a tile publishes per channel ----------------------------
 // high half: A (its bits are never negative: A is a product of decays in
 // [0, 1], NaN is stored as the positive quiet NaN), kState for a state, or
@@ -518,7 +530,7 @@ template <bool BF16, bool GATE, bool KEEP, bool FAST>
 __global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams p) {
     __shared__ FwdShared sh;
     const int total = p.unit_off[p.N];            // < 0: the call's indices were rejected
-    const int cg = blockIdx.x % p.groups;
+    const int cg = group_index() % p.groups;
     if (threadIdx.x == 0) sh.tile = draw_ticket(p, cg);
     const int c0 = cg * kCh;
     const Lane l = lane_of(c0, p.D);
@@ -565,10 +577,12 @@ template <bool BF16, bool GATE, bool KEEP>
 __global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) {
     __shared__ FwdShared sh;
     __shared__ int bad, first_unit;
+    const uint32_t id = group_index();
+    const int seq = id / p.groups;
+    if (seq >= p.N) return;
     if (threadIdx.x == 0) { bad = 0; first_unit = 0; }
     __syncthreads();
     // every work-group checks the indices, so nothing is written on a bad one
-    const int seq = blockIdx.x / p.groups;
     int mine = 0, before = 0;
     for (int n = threadIdx.x; n < p.N; n += kThreads) {
         const int lo = p.cu[n], hi = p.cu[n + 1];
@@ -579,9 +593,9 @@ __global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) 
     if (mine) atomicOr(&bad, 1);
     if (p.saved && before) atomicAdd(&first_unit, before);
     __syncthreads();
-    if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = bad ? kStatusBadIndex : 0;
+    if (p.status && id == 0 && threadIdx.x == 0) *p.status = bad ? kStatusBadIndex : 0;
     if (bad) return;
-    const int cg = blockIdx.x % p.groups;
+    const int cg = id % p.groups;
     const int c0 = cg * kCh;
     const Lane l = lane_of(c0, p.D);
     float nrate2[kVC], bias[kVC];
@@ -878,7 +892,7 @@ template <bool BF16, bool GATE>
 __global__ __launch_bounds__(kThreads, 3) void recur_backward_kernel(RecurParams p) {
     __shared__ BwdShared sh;
     const int total = kHalves * p.unit_off[p.N];
-    const int cg = blockIdx.x % p.groups;
+    const int cg = group_index() % p.groups;
     if (threadIdx.x == 0) sh.tile = draw_ticket(p, cg);
     const int c0 = cg * kCh;
     const Lane l = lane_of(c0, p.D);
@@ -994,9 +1008,9 @@ __global__ __launch_bounds__(kDecodeThreads) void recur_decode_kernel(RecurParam
     using Q = Quad<BF16>;
     using T = typename Q::T;
     const int per = (p.D + kVC - 1) / kVC;        // lanes of a row
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kDecodeThreads + threadIdx.x;
+    const int64_t i = static_cast<int64_t>(group_index()) * kDecodeThreads + threadIdx.x;
+    if (i / per >= p.N) return;
     const int n = static_cast<int>(i / per);
-    if (n >= p.N) return;
     const int c = static_cast<int>(i % per) * kVC;
     const int nv = p.D - c < kVC ? p.D - c : kVC;
     const int slot = state_slot(p.slots, n);
@@ -1047,7 +1061,7 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s) {
 // KERNEL<bf16, gate, ...>
 #define GDN_RECUR_CALL(KERNEL, GRID, BLOCK, ...)                                                    \
     do {                                                                                            \
-        const dim3 g_(static_cast<unsigned>(GRID)), b_(BLOCK);                                      \
+        const dim3 g_ = grid_of(GRID), b_(BLOCK);                                                   \
         if (bf16 && p.z) hipLaunchKernelGGL((KERNEL<true, true __VA_ARGS__>), g_, b_, 0, s, p);     \
         else if (bf16) hipLaunchKernelGGL((KERNEL<true, false __VA_ARGS__>), g_, b_, 0, s, p);      \
         else if (p.z) hipLaunchKernelGGL((KERNEL<false, true __VA_ARGS__>), g_, b_, 0, s, p);       \

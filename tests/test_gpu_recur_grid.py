@@ -40,6 +40,22 @@ def test_forward():
         assert torch.equal(f["out"][s], one["out"]) and torch.equal(f["final_state"][s], one["final_state"]), lo
 
 
+def test_short_calls():
+    """300 one-token sequences x 2^22 channels, without a workspace: 19.7 M work-groups."""
+    _room(32)
+    N, D = 300, 1 << 22
+    rec, x, a = _recur(D), _rows(N, D, 7), _rows(N, D, 8)
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda")
+    status = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    f = gdn.recur_forward(rec, x, a, x, None, cu, status=status)
+    assert status.item() == 0
+    for lo in (0, 1 << 21, D - 4096):
+        c = slice(lo, lo + 4096)
+        part = gdn.Recur(D=4096, A_log=rec.A_log[c], dt_bias=rec.dt_bias[c])
+        one = gdn.recur_forward(part, x[:, c], a[:, c], x[:, c], None, cu)
+        assert torch.equal(f["out"][:, c], one["out"]) and torch.equal(f["final_state"][:, c], one["final_state"]), lo
+
+
 def test_backward():
     """131072 one-token sequences x 4096 channels: as many tiles, two for each."""
     _room(64)
