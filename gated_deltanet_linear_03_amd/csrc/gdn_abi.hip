@@ -1242,12 +1242,20 @@ gdn_status check_dims(int64_t M, int64_t N, int64_t K) {
                     static_cast<long long>(N), static_cast<long long>(K));
     if (K % 8 || K > kMaxStride)
         return fail(GDN_ERR_INVALID_ARGUMENT, "K (%lld) must be a multiple of 8 up to 2^22", static_cast<long long>(K));
-    // a work-group for each 64 x 64 tile of an output at the most (dp's blocks
-    // of 32 x 256 are fewer)
-    const int64_t tiles = lim / 2;
-    auto count = [](int64_t r, int64_t c) { return ((r + 63) / 64) * ((c + 63) / 64); };
-    if (count(M, N) >= tiles || count(M, K) + count(N, K) >= tiles)
-        return fail(GDN_ERR_INVALID_ARGUMENT, "output too large");
+    return GDN_OK;
+}
+
+// A launch holds fewer than 2^32 work-items (one with more runs a part of them
+// without an error): 256 for each 64 x 64 tile of an output at the most, larger
+// tiles have no more of them.
+constexpr int64_t kMaxTiles = int64_t(1) << 24;
+
+int64_t tiles_of_64(int64_t r, int64_t c) { return ((r + 63) / 64) * ((c + 63) / 64); }
+
+gdn_status check_forward(int64_t M, int64_t N) {
+    // (up to 16 rows: 512 for each 16 columns)
+    if (tiles_of_64(M, N) >= kMaxTiles || (M <= gdn::kLinearStreamRows && N > (int64_t(1) << 27) - 16))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "output too large (%lld x %lld)", static_cast<long long>(M), static_cast<long long>(N));
     return GDN_OK;
 }
 
@@ -1275,7 +1283,7 @@ bool any_overlap(const Span& a, const Span* b, int n) {
 
 size_t gdn_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     g_err[0] = 0;
-    if (check_dims(M, N, K) != GDN_OK) return 0;
+    if (check_dims(M, N, K) != GDN_OK || check_forward(M, N) != GDN_OK) return 0;
     const int parts = gdn::linear_parts(M, N, K);
     return parts > 1 ? static_cast<size_t>(round_up(4 * parts * M * N, 256)) : 0;
 }
@@ -1285,7 +1293,7 @@ gdn_status gdn_linear(const gdn_linear_io* io, void* ws, size_t ws_bytes, void* 
     if (!io) return fail(GDN_ERR_INVALID_ARGUMENT, "io is NULL");
     const int64_t M = io->M, N = io->N, K = io->K;
     gdn_status st = check_dims(M, N, K);
-    if (st != GDN_OK) return st;
+    if (st != GDN_OK || (st = check_forward(M, N)) != GDN_OK) return st;
     if (io->act < GDN_ACT_NONE || io->act > GDN_ACT_SILU) return fail(GDN_ERR_INVALID_ARGUMENT, "act %d unknown", io->act);
     if (io->y_dtype != GDN_DTYPE_BF16 && io->y_dtype != GDN_DTYPE_FP32)
         return fail(GDN_ERR_INVALID_ARGUMENT, "y_dtype %d unknown", io->y_dtype);
@@ -1355,9 +1363,14 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K) {
     return w;
 }
 
-// dp's rows are an operand too
-gdn_status check_backward(int64_t N) {
+gdn_status check_backward(int64_t M, int64_t N, int64_t K) {
+    // (dp's rows are an operand too)
     if (N > kMaxStride) return fail(GDN_ERR_INVALID_ARGUMENT, "N (%lld) must be at most 2^22", static_cast<long long>(N));
+    // tiles of dx and dw and the bias sums in one launch; dp's blocks of 256 columns
+    if (tiles_of_64(M, K) + tiles_of_64(N, K) + (N + 63) / 64 >= kMaxTiles ||
+        gdn::linear_dp_blocks(M) * ((N + 255) / 256) >= kMaxTiles)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "output too large (%lld, %lld, %lld)", static_cast<long long>(M),
+                    static_cast<long long>(N), static_cast<long long>(K));
     return GDN_OK;
 }
 
@@ -1365,7 +1378,7 @@ gdn_status check_backward(int64_t N) {
 
 size_t gdn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     g_err[0] = 0;
-    if (check_dims(M, N, K) != GDN_OK || check_backward(N) != GDN_OK) return 0;
+    if (check_dims(M, N, K) != GDN_OK || check_backward(M, N, K) != GDN_OK) return 0;
     return static_cast<size_t>(linear_ws(M, N, K).total);
 }
 
@@ -1374,7 +1387,7 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_by
     if (!gr) return fail(GDN_ERR_INVALID_ARGUMENT, "grad is NULL");
     const int64_t M = gr->M, N = gr->N, K = gr->K;
     gdn_status st = check_dims(M, N, K);
-    if (st != GDN_OK || (st = check_backward(N)) != GDN_OK) return st;
+    if (st != GDN_OK || (st = check_backward(M, N, K)) != GDN_OK) return st;
     if (gr->act < GDN_ACT_NONE || gr->act > GDN_ACT_SILU) return fail(GDN_ERR_INVALID_ARGUMENT, "act %d unknown", gr->act);
     if (gr->dy_dtype != GDN_DTYPE_BF16 && gr->dy_dtype != GDN_DTYPE_FP32)
         return fail(GDN_ERR_INVALID_ARGUMENT, "dy_dtype %d unknown", gr->dy_dtype);

@@ -1247,7 +1247,8 @@ static BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K) {
         const int64_t tx = up(M, bm) * up(K, bn) * px, tw = up(N, bm) * up(K, bn) * pw;
         const double lx = static_cast<double>(up(N, px)), lw = static_cast<double>(up(M, pw));
         const double least = lx < lw ? lx : lw, most = lx < lw ? lw : lx;
-        if (least <= 0 || tx + tw > (int64_t(1) << 30)) return px * pw > 1 ? 1e30 : 0.0;
+        // (large outputs have tiles enough; a launch holds 2^32 work-items)
+        if (least <= 0 || (px * pw > 1 && tx + tw > (int64_t(1) << 21))) return px * pw > 1 ? 1e30 : 0.0;
         const double work = std::ceil((tx * lx + tw * lw) / (cus * least)) * least * each;
         return (work > most * alone ? work : most * alone) / 2048;
     };

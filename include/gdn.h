@@ -619,7 +619,10 @@ gdn_status gdn_recur_decode(const gdn_recur* recur, const gdn_recur_io* io, void
 
 /* Row strides in elements, 0 means dense.  x, w: 16-byte aligned, K and
  * their strides multiples of 8 up to 2^22; the others element aligned, M and
- * N free (N up to 2^22 in the backward pass).
+ * N free (N up to 2^22 in the backward pass) as long as the outputs come to
+ * fewer than 2^24 tiles of 64 x 64 (dx and dw together; with up to 16 rows N
+ * is at most 2^27 - 16, and in the backward pass ceil(M / 32) ceil(N / 256)
+ * is below 2^24).
  * residual may be y itself (same address and stride); otherwise the bytes
  * from the first to the last element of y and of preact must not overlap
  * those of another buffer. */

@@ -94,6 +94,34 @@ def test_backward_workspace():
     assert L.gdn_linear_backward(ctypes.byref(_grad(dx=None, dw=None, dbias=None)), None, 0, None) == gdn.GDN_OK
 
 
+@pytest.mark.parametrize("M, N, K, fits", [
+    (16, (1 << 27) - 16, 8, True), (16, (1 << 27) - 15, 8, False), (1, (1 << 31) - 1, 8, False), (17, (1 << 30) - 64, 8, True),
+    (17, (1 << 30) - 63, 8, False), ((1 << 30) - 64, 64, 8, True), ((1 << 30) - 63, 64, 8, False), (1 << 18, 1 << 18, 8, False),
+    (1 << 25, 64, 1 << 22, True),
+])
+def test_forward_fits_one_launch(M, N, K, fits):
+    """A launch of 2^32 work-items or more would run a part of them: refused."""
+    L = gdn.lib()
+    assert L.gdn_linear_workspace_bytes(M, N, K) == 0 and (L.gdn_last_error() == b"") == fits
+    if not fits:
+        io = _io(M=M, N=N, K=K, x_stride=0, residual=None, preact=None)
+        assert L.gdn_linear(ctypes.byref(io), WS, NWS, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+        assert b"too large" in L.gdn_last_error()
+
+
+@pytest.mark.parametrize("M, N, K, fits", [
+    (1 << 29, 8, 8, False), ((1 << 29) - 32, 8, 8, True), (1 << 24, 8, 4096, False), (1 << 23, 1 << 16, 8, False),
+    ((1 << 21) - 32, 1 << 16, 64, True), (1 << 21, 1 << 16, 64, False), (1 << 12, 1 << 22, 1 << 14, False), (4096, 4096, 4096, True),
+])
+def test_backward_fits_one_launch(M, N, K, fits):
+    L = gdn.lib()
+    assert (L.gdn_linear_backward_workspace_bytes(M, N, K) > 0) == fits
+    if not fits:
+        gr = _grad(M=M, N=N, K=K)
+        assert L.gdn_linear_backward(ctypes.byref(gr), WS, 1 << 62, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+        assert b"too large" in L.gdn_last_error()
+
+
 def test_struct_layouts(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
