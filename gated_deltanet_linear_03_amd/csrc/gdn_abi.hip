@@ -947,6 +947,9 @@ RecurWs recur_ws(const gdn_recur* R, int32_t N, int64_t T, bool backward) {
     return w;
 }
 
+// A row stride; one row has none that means anything.
+int64_t row_stride(int64_t s, int64_t dense, int64_t rows) { return rows <= 1 ? dense : stride_or(s, dense); }
+
 // rows [rows][D] with a row stride: bytes from the first element to the last
 size_t row_bytes(int64_t rows, int64_t stride, int64_t D, size_t es) {
     return rows > 0 ? static_cast<size_t>((rows - 1) * stride + D) * es : 0;
@@ -985,10 +988,10 @@ gdn_status recur_params(const gdn_recur* R, const gdn_recur_io* io, int64_t rows
     p->A_log = R->A_log;
     p->dt_bias = R->dt_bias;
     p->x = io->x; p->a = io->a; p->b = io->b; p->z = io->z;
-    p->xs = stride_or(io->x_stride, D);
-    p->as = stride_or(io->a_stride, D);
-    p->bs = stride_or(io->b_stride, D);
-    p->zs = stride_or(io->z_stride, D);
+    p->xs = row_stride(io->x_stride, D, rows);
+    p->as = row_stride(io->a_stride, D, rows);
+    p->bs = row_stride(io->b_stride, D, rows);
+    p->zs = row_stride(io->z_stride, D, rows);
     p->status = io->status;
     if (!R->A_log || !R->dt_bias || !aligned(R->A_log, 4) || !aligned(R->dt_bias, 4))
         return fail(GDN_ERR_INVALID_ARGUMENT, "A_log and dt_bias are required, 4-byte aligned");
@@ -1009,7 +1012,7 @@ gdn_status recur_outputs(const gdn_recur* R, const gdn_recur_io* io, int64_t row
     const size_t es = act_size(R->act_dtype);
     const int64_t D = R->D;
     p->y = io->y;
-    p->ys = stride_or(io->y_stride, D);
+    p->ys = row_stride(io->y_stride, D, rows);
     p->h0 = io->initial_state;
     p->hT = io->final_state;
     p->slots = io->state_slots;
@@ -1141,11 +1144,11 @@ gdn_status gdn_recur_backward(const gdn_recur* R, const gdn_recur_io* io, const 
     p.saved = io->saved;
     p.dy = gr->dy;
     p.dx = gr->dx; p.da = gr->da; p.db = gr->db; p.dz = gr->dz;
-    p.dys = stride_or(gr->dy_stride, D);
-    p.dxs = stride_or(gr->dx_stride, D);
-    p.das = stride_or(gr->da_stride, D);
-    p.dbs = stride_or(gr->db_stride, D);
-    p.dzs = stride_or(gr->dz_stride, D);
+    p.dys = row_stride(gr->dy_stride, D, T);
+    p.dxs = row_stride(gr->dx_stride, D, T);
+    p.das = row_stride(gr->da_stride, D, T);
+    p.dbs = row_stride(gr->db_stride, D, T);
+    p.dzs = row_stride(gr->dz_stride, D, T);
     p.dhT = gr->d_final_state;
     p.dh0 = gr->d_initial_state;
     p.dA_log = gr->dA_log;
@@ -1302,19 +1305,19 @@ gdn_status gdn_linear(const gdn_linear_io* io, void* ws, size_t ws_bytes, void* 
     gdn::GemmProduct p{};
     p.M = M; p.N = N; p.K = K;
     p.A = io->x; p.B = io->w;
-    p.lda = stride_or(io->x_stride, K);
-    p.ldb = stride_or(io->w_stride, K);
+    p.lda = row_stride(io->x_stride, K, M);
+    p.ldb = row_stride(io->w_stride, K, N);
     if (K > 0 && (st = check_operand("x", io->x, p.lda, K)) != GDN_OK) return st;
     if (K > 0 && (st = check_operand("w", io->w, p.ldb, K)) != GDN_OK) return st;
     p.ep.bias = io->bias;
     p.ep.act = io->act;
     p.ep.bf16 = io->y_dtype == GDN_DTYPE_BF16;
     p.ep.y = io->y;
-    p.ep.ldy = stride_or(io->y_stride, N);
+    p.ep.ldy = row_stride(io->y_stride, N, M);
     p.ep.residual = io->residual;
-    p.ep.ldr = stride_or(io->residual_stride, N);
+    p.ep.ldr = row_stride(io->residual_stride, N, M);
     p.ep.preact = static_cast<uint16_t*>(io->preact);
-    p.ep.ldp = stride_or(io->preact_stride, N);
+    p.ep.ldp = row_stride(io->preact_stride, N, M);
     if (!aligned(io->bias, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "bias must be 4-byte aligned");
     if ((st = check_rows("y", io->y, p.ep.ldy, N, es)) != GDN_OK) return st;
     if (io->residual && (st = check_rows("residual", io->residual, p.ep.ldr, N, es)) != GDN_OK) return st;
@@ -1402,11 +1405,11 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_by
     dp.M = M; dp.N = N;
     dp.dy = gr->dy;
     dp.dy_bf16 = gr->dy_dtype == GDN_DTYPE_BF16;
-    dp.ldy = stride_or(gr->dy_stride, N);
+    dp.ldy = row_stride(gr->dy_stride, N, M);
     dp.act = gr->act;
-    dp.ldp = stride_or(gr->preact_stride, N);
-    const int64_t ldx = stride_or(gr->x_stride, K), ldw = stride_or(gr->w_stride, K);
-    const int64_t lddx = stride_or(gr->dx_stride, K), lddw = stride_or(gr->dw_stride, K);
+    dp.ldp = row_stride(gr->preact_stride, N, M);
+    const int64_t ldx = row_stride(gr->x_stride, K, M), ldw = row_stride(gr->w_stride, K, N);
+    const int64_t lddx = row_stride(gr->dx_stride, K, M), lddw = row_stride(gr->dw_stride, K, N);
     if (M > 0 && N > 0) {
         if ((st = check_rows("dy", gr->dy, dp.ldy, N, ds)) != GDN_OK) return st;
         if (gr->act != GDN_ACT_NONE) {

@@ -512,8 +512,8 @@ gdn_status gdn_snapshot_restore(const gdn_layer* layer, const void* host_buf,
  * Forward over packed sequences, its backward pass, and one token for each
  * of a batch of sequences.  A sequence's results are bit-identical whether
  * it runs alone or in a batch, and from call to call.  Rows are [tokens][D]
- * with a row stride in elements (0 means dense), so slices of a packed
- * projection's rows can be given; D and the strides are at most 2^22, and
+ * with a row stride in elements (0 means dense; a single row's is not looked
+ * at), so slices of a packed projection's rows can be given; D and the strides are at most 2^22, and
  * they and the addresses need no more than element alignment. */
 typedef struct {
     int32_t D;                     /* channels, >= 1 */
@@ -617,7 +617,8 @@ gdn_status gdn_recur_decode(const gdn_recur* recur, const gdn_recur_io* io, void
 #define GDN_ACT_GELU_TANH 3        /* p (1 + tanh(sqrt(2/pi) (p + 0.044715 p^3))) / 2 */
 #define GDN_ACT_SILU 4             /* p sigmoid(p) */
 
-/* Row strides in elements, 0 means dense.  x, w: 16-byte aligned, K and
+/* Row strides in elements, 0 means dense; a single row's is not looked at.
+ * x, w: 16-byte aligned, K and
  * their strides multiples of 8 up to 2^22; the others element aligned, M and
  * N free (N up to 2^22 in the backward pass) as long as the outputs come to
  * fewer than 2^24 tiles of 64 x 64 (dx and dw together; with up to 16 rows N

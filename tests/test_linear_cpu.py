@@ -122,6 +122,21 @@ def test_backward_fits_one_launch(M, N, K, fits):
         assert b"too large" in L.gdn_last_error()
 
 
+def test_one_rows_stride_is_not_looked_at():
+    """hidden[:, -1] of a long prompt: one row, with whatever stride.  (The
+    calls are refused for what is checked last.)"""
+    L = gdn.lib()
+    odd = dict(x_stride=(1 << 23) + 4, y_stride=5, residual_stride=3, preact_stride=1)
+    assert L.gdn_linear(ctypes.byref(_io(M=1, preact=FAKE + 5 * FAR, **odd)), WS, NWS, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert b"overlaps" in L.gdn_last_error()
+    assert L.gdn_linear(ctypes.byref(_io(N=1, w_stride=12, preact=FAKE + 5 * FAR)), WS, NWS, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert b"overlaps" in L.gdn_last_error()
+    odd = dict(dy_stride=1, x_stride=(1 << 23) + 4, preact_stride=2, dx_stride=7)
+    for g in (dict(M=1, **odd), dict(N=1, w_stride=12, dw_stride=3)):
+        st = L.gdn_linear_backward(ctypes.byref(_grad(dbias=WS, **g)), WS, NWS, None)
+        assert st == gdn.GDN_ERR_INVALID_ARGUMENT and b"overlaps" in L.gdn_last_error()
+
+
 def test_struct_layouts(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:

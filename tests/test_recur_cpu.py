@@ -153,6 +153,21 @@ def test_decode_refuses():
     assert L.gdn_recur_decode(ctypes.byref(_recur()), ctypes.byref(_io(N=0)), None) == gdn.GDN_OK
 
 
+def test_one_rows_stride_is_not_looked_at():
+    """One token's row, with whatever stride.  (The calls are refused for what
+    is checked last.)"""
+    L = gdn.lib()
+    odd = {k + "_stride": v for k, v in zip("xabzy", ((1 << 22) + 1, 3, 1 << 30, 127, 1))}
+    io = _io(N=1, T_total=1, status=FAKE + 7 * FAR, **odd)
+    for st in (L.gdn_recur_decode(ctypes.byref(_recur()), ctypes.byref(io), None),
+               L.gdn_recur_forward(ctypes.byref(_recur()), ctypes.byref(io), WS, NWS, None)):
+        assert st == gdn.GDN_ERR_INVALID_ARGUMENT and b"status overlaps" in L.gdn_last_error()
+    io = _io(N=1, T_total=1, saved=FAKE + 16 * FAR, **odd)
+    gr = _grad(ddt_bias=WS, **{k + "_stride": v for k, v in zip(("dy", "dx", "da", "db", "dz"), (1, 2, 3, 1 << 23, 5))})
+    assert L.gdn_recur_backward(ctypes.byref(_recur()), ctypes.byref(io), ctypes.byref(gr), WS, NWS, None) == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert b"dA_log and ddt_bias" in L.gdn_last_error()
+
+
 def test_binding_refuses_host_tensors():
     import torch
     r = gdn.Recur(D=4, A_log=torch.zeros(4), dt_bias=torch.zeros(4))
