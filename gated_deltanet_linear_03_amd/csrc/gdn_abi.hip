@@ -51,6 +51,17 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+bool any_overlap(const Span& a, const Span* b, int n) {
+    for (int i = 0; i < n; ++i)
+        if (overlaps(a.p, a.n, b[i].p, b[i].n)) return true;
+    return false;
+}
+
 // An output buffer (out, core_out) that shares bytes with a recurrent or
 // conv state would be overwritten, or overwrite it, while the kernels run.
 bool output_hits_state(const void* o, size_t no, const void* s_in, const void* s_out, size_t ns,
@@ -1007,8 +1018,25 @@ gdn_status recur_params(const gdn_recur* R, const gdn_recur_io* io, int64_t rows
     return GDN_OK;
 }
 
-// The states and y of a forward or one-token call
-gdn_status recur_outputs(const gdn_recur* R, const gdn_recur_io* io, int64_t rows, gdn::RecurParams* p) {
+// What a call of the recurrence reads beside its states: x, a, b, z, then
+// cu_seqlens, the pool entries and the parameters (p: from recur_params, with
+// its cu and slots).
+constexpr int kReads = 8, kRowReads = 4;
+
+void recur_reads(const gdn::RecurParams& p, int64_t rows, size_t es, Span* r) {
+    const size_t params = static_cast<size_t>(p.D) * 4;
+    r[0] = {p.x, row_bytes(rows, p.xs, p.D, es)};
+    r[1] = {p.a, row_bytes(rows, p.as, p.D, es)};
+    r[2] = {p.b, row_bytes(rows, p.bs, p.D, es)};
+    r[3] = {p.z, row_bytes(rows, p.zs, p.D, es)};
+    r[4] = {p.cu, (static_cast<size_t>(p.N) + 1) * 4};
+    r[5] = {p.slots, static_cast<size_t>(p.N) * 4};
+    r[6] = {p.A_log, params};
+    r[7] = {p.dt_bias, params};
+}
+
+// The states and y of a forward or one-token call; reads: what it reads
+gdn_status recur_outputs(const gdn_recur* R, const gdn_recur_io* io, int64_t rows, gdn::RecurParams* p, Span* reads) {
     const size_t es = act_size(R->act_dtype);
     const int64_t D = R->D;
     p->y = io->y;
@@ -1021,6 +1049,7 @@ gdn_status recur_outputs(const gdn_recur* R, const gdn_recur_io* io, int64_t row
         return fail(GDN_ERR_INVALID_ARGUMENT, "num_slots (%d) must be positive and state_slots 4-byte aligned", io->num_slots);
     if (!aligned(io->initial_state, 4) || !aligned(io->final_state, 4))
         return fail(GDN_ERR_INVALID_ARGUMENT, "states must be 4-byte aligned");
+    recur_reads(*p, rows, es, reads);
     const size_t ns = static_cast<size_t>(io->state_slots ? io->num_slots : io->N) * D * 4;
     if (bad_alias(io->initial_state, ns, io->final_state, ns))
         return fail(GDN_ERR_INVALID_ARGUMENT, "final_state partially overlaps initial_state");
@@ -1031,19 +1060,20 @@ gdn_status recur_outputs(const gdn_recur* R, const gdn_recur_io* io, int64_t row
         ny = row_bytes(rows, p->ys, D, es);
         if (overlaps(io->y, ny, io->initial_state, ns) || overlaps(io->y, ny, io->final_state, ns))
             return fail(GDN_ERR_INVALID_ARGUMENT, "y overlaps a state");
-        const void* in[4] = {io->x, io->a, io->b, io->z};
-        const int64_t stride[4] = {p->xs, p->as, p->bs, p->zs};
-        for (int i = 0; i < 4; ++i) {
-            if (!in[i]) continue;
-            if (overlaps(io->final_state, ns, in[i], row_bytes(rows, stride[i], D, es)))
-                return fail(GDN_ERR_INVALID_ARGUMENT, "final_state overlaps an input");
-            if (!(in[i] == io->y && stride[i] == p->ys) && rows_clash(io->y, p->ys, in[i], stride[i], rows, D, es))
+        const int64_t stride[kRowReads] = {p->xs, p->as, p->bs, p->zs};
+        for (int i = 0; i < kRowReads; ++i) {
+            const void* in = reads[i].p;
+            if (in && !(in == io->y && stride[i] == p->ys) && rows_clash(io->y, p->ys, in, stride[i], rows, D, es))
                 return fail(GDN_ERR_INVALID_ARGUMENT, "y overlaps an input's rows");
         }
     }
-    if (io->status && (overlaps(io->status, 4, io->y, ny) || overlaps(io->status, 4, io->initial_state, ns) ||
-                       overlaps(io->status, 4, io->final_state, ns)))
-        return fail(GDN_ERR_INVALID_ARGUMENT, "status overlaps an output or a state");
+    const Span y{io->y, ny}, first{io->initial_state, ns}, last{io->final_state, ns}, status{io->status, 4};
+    if (any_overlap(y, reads + kRowReads, kReads - kRowReads))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "y overlaps an input: indices or a parameter");
+    if (any_overlap(last, reads, kReads)) return fail(GDN_ERR_INVALID_ARGUMENT, "final_state overlaps an input");
+    if (any_overlap(status, &y, 1) || any_overlap(status, &first, 1) || any_overlap(status, &last, 1) ||
+        any_overlap(status, reads, kReads))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "status overlaps an input, an output or a state");
     return GDN_OK;
 }
 
@@ -1099,9 +1129,10 @@ gdn_status gdn_recur_forward(const gdn_recur* R, const gdn_recur_io* io, void* w
         return fail(GDN_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL or misaligned");
     gdn::RecurParams p{};
     if ((st = recur_params(R, io, io->T_total, &p)) != GDN_OK) return st;
-    if ((st = recur_outputs(R, io, io->T_total, &p)) != GDN_OK) return st;
-    if (!aligned(io->saved, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "saved must be 4-byte aligned");
     p.cu = io->cu_seqlens;
+    Span reads[kReads];
+    if ((st = recur_outputs(R, io, io->T_total, &p, reads)) != GDN_OK) return st;
+    if (!aligned(io->saved, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "saved must be 4-byte aligned");
     p.saved = io->saved;
     p.walk = recur_walks(io->N, io->T_total);
     const int64_t units = gdn::recur_units(io->N, io->T_total);
@@ -1109,15 +1140,16 @@ gdn_status gdn_recur_forward(const gdn_recur* R, const gdn_recur_io* io, void* w
     const size_t ns = static_cast<size_t>(io->state_slots ? io->num_slots : io->N) * R->D * 4;
     const size_t ny = row_bytes(io->T_total, p.ys, R->D, act_size(R->act_dtype));
     if (overlaps(io->saved, nsv, io->y, ny) || overlaps(io->saved, nsv, io->initial_state, ns) ||
-        overlaps(io->saved, nsv, io->final_state, ns) || overlaps(io->saved, nsv, io->status, 4))
-        return fail(GDN_ERR_INVALID_ARGUMENT, "saved overlaps y, a state or status");
+        overlaps(io->saved, nsv, io->final_state, ns) || overlaps(io->saved, nsv, io->status, 4) ||
+        any_overlap({io->saved, nsv}, reads, kReads))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "saved overlaps an input, y, a state or status");
     if (!p.walk) {
         const RecurWs w = recur_ws(R, io->N, io->T_total, false);
         if ((st = recur_workspace(w, ws, ws_bytes, &p, units)) != GDN_OK) return st;
         const size_t nw = static_cast<size_t>(w.total);
         if (overlaps(ws, nw, io->y, ny) || overlaps(ws, nw, io->initial_state, ns) || overlaps(ws, nw, io->final_state, ns) ||
-            overlaps(ws, nw, io->saved, nsv) || overlaps(ws, nw, io->status, 4))
-            return fail(GDN_ERR_INVALID_ARGUMENT, "workspace overlaps an output or a state");
+            overlaps(ws, nw, io->saved, nsv) || overlaps(ws, nw, io->status, 4) || any_overlap({ws, nw}, reads, kReads))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "workspace overlaps an input, an output or a state");
     }
     p.partial = nullptr;
     if (io->N == 0) return recur_status_clear(io, stream);
@@ -1197,6 +1229,22 @@ gdn_status gdn_recur_backward(const gdn_recur* R, const gdn_recur_io* io, const 
         overlaps(gr->ddt_bias, 4 * D, gr->d_initial_state, ns) || overlaps(gr->dA_log, 4 * D, ws, nw) ||
         overlaps(gr->ddt_bias, 4 * D, ws, nw))
         return fail(GDN_ERR_INVALID_ARGUMENT, "dA_log and ddt_bias must not overlap each other or another output");
+    Span reads[kReads + 3];
+    recur_reads(p, T, es, reads);
+    reads[kReads] = {gr->dy, row_bytes(T, p.dys, D, es)};
+    reads[kReads + 1] = {io->saved, nsv};
+    reads[kReads + 2] = {gr->d_final_state, ns};
+    const size_t params = static_cast<size_t>(D) * 4;
+    const Span out[8] = {{gr->dx, row_bytes(T, p.dxs, D, es)}, {gr->da, row_bytes(T, p.das, D, es)},
+                         {gr->db, row_bytes(T, p.dbs, D, es)}, {io->z ? gr->dz : nullptr, row_bytes(T, p.dzs, D, es)},
+                         {gr->dA_log, params}, {gr->ddt_bias, params}, {ws, nw}, {gr->d_initial_state, ns}};
+    // (d_initial_state may be d_final_state itself: the last of either list)
+    for (int i = 0; i < 8; ++i)
+        if (any_overlap(out[i], reads, kReads + (i < 7 ? 3 : 2)))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input");
+    const Span status{io->status, 4};
+    if (any_overlap(status, out, 8) || any_overlap(status, reads, kReads + 3))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "status overlaps another buffer");
     if (io->N > 0 && (st = recur_workspace(w, ws, ws_bytes, &p, kHalves * units)) != GDN_OK) return st;
     if (!gr->dA_log && !gr->ddt_bias) p.partial = nullptr;
     if (io->N == 0) {
@@ -1224,7 +1272,8 @@ gdn_status gdn_recur_decode(const gdn_recur* R, const gdn_recur_io* io, void* st
     if (!io->final_state) return fail(GDN_ERR_INVALID_ARGUMENT, "final_state is NULL");
     gdn::RecurParams p{};
     if ((st = recur_params(R, io, io->N, &p)) != GDN_OK) return st;
-    if ((st = recur_outputs(R, io, io->N, &p)) != GDN_OK) return st;
+    Span reads[kReads];
+    if ((st = recur_outputs(R, io, io->N, &p, reads)) != GDN_OK) return st;
     hipError_t e = gdn::launch_recur_decode(p, R->act_dtype == GDN_DTYPE_BF16, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(GDN_ERR_HIP, "recurrence launch failed: %s", hipGetErrorString(e));
     return GDN_OK;
@@ -1269,17 +1318,6 @@ gdn_status check_operand(const char* name, const void* p, int64_t stride, int64_
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned with a stride that is a multiple of 8", name);
     if (stride < cols) return fail(GDN_ERR_INVALID_ARGUMENT, "%s_stride (%lld) is below its row length", name, static_cast<long long>(stride));
     return check_stride(name, stride);
-}
-
-struct Span {
-    const void* p;
-    size_t n;
-};
-
-bool any_overlap(const Span& a, const Span* b, int n) {
-    for (int i = 0; i < n; ++i)
-        if (overlaps(a.p, a.n, b[i].p, b[i].n)) return true;
-    return false;
 }
 
 }  // namespace

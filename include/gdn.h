@@ -526,8 +526,9 @@ typedef struct {
  * (the state passes through).  initial_state NULL means zeros; final_state
  * may equal initial_state (in-place update) but must not partially overlap
  * it; NULL = not written.  Rows of y past T_total are not touched.  y may be
- * x, a, b or z itself (same address and stride), and must otherwise share no
- * bytes with what is read. */
+ * x, a, b or z itself (same address and stride), and what is written must
+ * otherwise share no bytes with what is read, the workspace and the indices
+ * included. */
 typedef struct {
     int32_t N;
     int64_t T_total;               /* == cu_seqlens[N], < 2^31 */
@@ -572,7 +573,8 @@ gdn_status gdn_recur_forward(const gdn_recur* recur, const gdn_recur_io* io,
 
 /* The gradient's buffers.  dx, da, db (and dz where io has z) are written in
  * the act dtype, row strides as above; they may be slices of one packed
- * buffer and must share no bytes with what is read.  d_final_state NULL
+ * buffer; nothing that is written may share bytes with what is read, except
+ * that d_initial_state may be d_final_state itself.  d_final_state NULL
  * means zeros.  dA_log, ddt_bias and d_initial_state are optional. */
 typedef struct {
     const void* dy;

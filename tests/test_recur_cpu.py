@@ -153,6 +153,43 @@ def test_decode_refuses():
     assert L.gdn_recur_decode(ctypes.byref(_recur()), ctypes.byref(_io(N=0)), None) == gdn.GDN_OK
 
 
+# FAKE: cu_seqlens and the parameters; FAKE + i FAR: x, a, b, z
+@pytest.mark.parametrize("change, word", [
+    (dict(saved=FAKE + FAR), "saved overlaps"), (dict(saved=FAKE + 4 * FAR + 1024), "saved overlaps"), (dict(saved=FAKE), "saved overlaps"),
+    (dict(x=WS + 4096), "workspace overlaps"), (dict(z=WS), "workspace overlaps"), (dict(cu_seqlens=WS + 64), "workspace overlaps"),
+    (dict(y=FAKE), "y overlaps an input"), (dict(final_state=FAKE), "final_state overlaps"), (dict(status=FAKE + 4), "status overlaps"),
+    (dict(status=FAKE + 2 * FAR), "status overlaps"),
+    (dict(state_slots=FAKE + 9 * FAR, num_slots=4, final_state=FAKE + 9 * FAR, initial_state=None), "final_state overlaps"),
+])
+def test_forward_refuses_what_shares_bytes_with_its_inputs(change, word):
+    st = gdn.lib().gdn_recur_forward(ctypes.byref(_recur()), ctypes.byref(_io(**change)), WS, NWS, None)
+    assert st == gdn.GDN_ERR_INVALID_ARGUMENT and word in gdn.lib().gdn_last_error().decode()
+
+
+@pytest.mark.parametrize("grad, io, word", [
+    ({}, dict(x=WS + 64), "overlaps an input"), ({}, dict(b=WS), "overlaps an input"), (dict(dy=WS + 4096), {}, "overlaps an input"),
+    ({}, dict(cu_seqlens=WS), "overlaps an input"), (dict(dA_log=FAKE), {}, "overlaps an input"),
+    (dict(dA_log=FAKE + 2 * FAR), {}, "overlaps an input"), (dict(ddt_bias=FAKE + 16 * FAR), {}, "overlaps an input"),
+    (dict(d_initial_state=FAKE + 8 * FAR), {}, "overlaps an input"), (dict(d_initial_state=FAKE), {}, "overlaps an input"),
+    (dict(dx=FAKE), {}, "overlaps an input"), (dict(dA_log=FAKE + 17 * FAR, d_final_state=FAKE + 17 * FAR), {}, "overlaps an input"),
+    ({}, dict(status=FAKE + 9 * FAR), "status overlaps"), ({}, dict(status=WS + 8), "status overlaps"),
+    ({}, dict(status=FAKE + 16 * FAR), "status overlaps"),
+])
+def test_backward_refuses_what_shares_bytes_with_its_inputs(grad, io, word):
+    io = _io(**dict(dict(saved=FAKE + 16 * FAR), **io))
+    st = gdn.lib().gdn_recur_backward(ctypes.byref(_recur()), ctypes.byref(io), ctypes.byref(_grad(**grad)), WS, NWS, None)
+    assert st == gdn.GDN_ERR_INVALID_ARGUMENT and word in gdn.lib().gdn_last_error().decode()
+
+
+def test_decode_refuses_what_shares_bytes_with_its_inputs():
+    L = gdn.lib()
+    for change in (dict(y=FAKE), dict(final_state=FAKE), dict(status=FAKE + 3 * FAR), dict(status=FAKE),
+                   dict(state_slots=FAKE + 5 * FAR, num_slots=2)):
+        io = _io(**dict(dict(cu_seqlens=None), **change))
+        st = L.gdn_recur_decode(ctypes.byref(_recur()), ctypes.byref(io), None)
+        assert st == gdn.GDN_ERR_INVALID_ARGUMENT and b"overlaps an input" in L.gdn_last_error(), change
+
+
 def test_one_rows_stride_is_not_looked_at():
     """One token's row, with whatever stride.  (The calls are refused for what
     is checked last.)"""
