@@ -1161,8 +1161,8 @@ def linear(x, w, bias=None, act=GDN_ACT_NONE, residual=None, out=None, out_dtype
     ws, nb = None, 0
     if workspace is not None:
         ws, nb = _bytes(workspace, "workspace", dev)
-    elif 16 < M <= 256:
-        nb = linear_workspace_bytes(M, N, K)
+    else:
+        nb = lib().gdn_linear_workspace_bytes(M, N, K)      # (0 too where gdn_linear refuses the sizes)
         if nb:
             workspace = _new(x, (nb,), torch.uint8, stream)
             ws = workspace.data_ptr()
