@@ -835,7 +835,11 @@ def _device():
 
 def _raw_stream(stream, dev):
     """Handle of a stream (None: torch's current one on device `dev`)."""
-    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream: on {stream.device}, the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _on_device(t, name, dev):
@@ -912,8 +916,8 @@ def _new(like, shape, dtype, stream):
     one): memory that a call on it uses is not reused under it."""
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
-    import torch
-    with torch.cuda.stream(stream):
+    _raw_stream(stream, _device())
+    with _torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
 
