@@ -50,7 +50,8 @@ EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_prefill_window_slots", "gdn_decode_workspace_bytes", "gdn_gemm_bf16_path",
            "gdn_recur_saved_bytes", "gdn_recur_workspace_bytes", "gdn_recur_forward",
            "gdn_recur_backward_workspace_bytes", "gdn_recur_backward", "gdn_recur_decode",
-           "gdn_linear", "gdn_linear_workspace_bytes", "gdn_linear_backward_workspace_bytes", "gdn_linear_backward")
+           "gdn_linear", "gdn_linear_workspace_bytes", "gdn_linear_backward_workspace_bytes", "gdn_linear_backward",
+           "gdn_linear_tiles")
 NOALLOC_SCRATCH_BYTES = 128 << 20       # GDN_NOALLOC_SCRATCH_BYTES
 SNAPSHOT_MAGIC = 0x50534E47
 SNAPSHOT_VERSION = 1
@@ -288,6 +289,8 @@ def lib():
         L.gdn_linear_workspace_bytes.argtypes = [ctypes.c_int64] * 3
         L.gdn_linear_backward_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_linear_backward_workspace_bytes.argtypes = [ctypes.c_int64] * 3
+        L.gdn_linear_tiles.restype = ctypes.c_int
+        L.gdn_linear_tiles.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int32] + [ctypes.POINTER(ctypes.c_int32)] * 2
         L.gdn_linear_backward.restype = ctypes.c_int
         L.gdn_linear_backward.argtypes = [ctypes.POINTER(CLinearGrad), ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]
@@ -1179,6 +1182,14 @@ def linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
     if n == 0:
         raise GdnError(GDN_ERR_INVALID_ARGUMENT, lib().gdn_last_error().decode())
     return int(n)
+
+
+def linear_tiles(M: int, N: int, K: int, backward=False):
+    """(rows, columns) of the output tiles that ``gdn_linear`` or
+    ``gdn_linear_backward`` runs these sizes with."""
+    r, c = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().gdn_linear_tiles(int(M), int(N), int(K), int(backward), ctypes.byref(r), ctypes.byref(c)))
+    return r.value, c.value
 
 
 def linear_backward(dy, x, w, preact=None, act=GDN_ACT_NONE, want_dx=True, want_dw=True,

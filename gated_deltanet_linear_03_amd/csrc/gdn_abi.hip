@@ -1499,6 +1499,16 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* gr, void* ws, size_t ws_by
     return GDN_OK;
 }
 
+gdn_status gdn_linear_tiles(int64_t M, int64_t N, int64_t K, int32_t backward, int32_t* rows, int32_t* cols) {
+    g_err[0] = 0;
+    if (!rows || !cols) return fail(GDN_ERR_INVALID_ARGUMENT, "NULL pointer");
+    gdn_status st = check_dims(M, N, K);
+    if (st != GDN_OK || (st = backward ? check_backward(M, N, K) : check_forward(M, N)) != GDN_OK) return st;
+    if (backward) gdn::linear_backward_tiles(M, N, K, rows, cols);
+    else gdn::linear_tiles(M, N, K, rows, cols);
+    return GDN_OK;
+}
+
 gdn_status gdn_selftest_mfma(const float* A, const float* B, float* C, void* stream) {
     g_err[0] = 0;
     if (!A || !B || !C) return fail(GDN_ERR_INVALID_ARGUMENT, "NULL pointer");

@@ -274,6 +274,9 @@ constexpr int kLinearSomeRows = 256;     // that many: the reduction in parts, a
 int linear_parts(int64_t M, int64_t N, int64_t K);
 // the same for dx ([M][K]) and dw ([N][K])
 void linear_backward_parts(int64_t M, int64_t N, int64_t K, int* dx, int* dw);
+// rows and columns of the tiles (of the most columns, forward)
+void linear_tiles(int64_t M, int64_t N, int64_t K, int32_t* rows, int32_t* cols);
+void linear_backward_tiles(int64_t M, int64_t N, int64_t K, int32_t* rows, int32_t* cols);
 int64_t linear_dp_blocks(int64_t M);
 hipError_t launch_linear(const GemmProduct& p, float* sums, hipStream_t s);
 // dx or dw with ep.y NULL is left out

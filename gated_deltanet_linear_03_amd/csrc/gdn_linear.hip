@@ -1182,6 +1182,42 @@ int linear_parts(int64_t M, int64_t N, int64_t K) {
     return n < 1 ? 1 : static_cast<int>(n > 64 ? 64 : n);
 }
 
+// Tiles of more than kLinearFewRows rows.  A last column of tiles that is
+// nearly empty can cost a whole round of them (12352 = 48 x 256 + 64 columns
+// at 4096 rows: 784 tiles, four rounds instead of three; with gelu, bias and
+// residual 210 us): then the rest goes by itself in smaller tiles (184 us).  A
+// column's sum runs in the same order either way.
+struct ForwardPlan {
+    int64_t columns;                              // of `tiles`; N or what is left over goes in `rest`
+    Tiles tiles, rest;
+};
+
+static ForwardPlan forward_plan(const GemmProduct& p) {
+    const int cus = compute_units();
+    const Choice whole = choose(p, cus);
+    const int64_t rest = p.N % 256, main = p.N - rest;
+    if (rest > 0 && main > 0) {
+        GemmProduct m = p, r = p;
+        m.N = main;
+        r.N = rest;
+        const Choice cm = choose(m, cus), cr = choose(r, cus);
+        if (cm.us + cr.us + 3.0 < whole.us) return {main, cm.tiles, cr.tiles};   // 3: the second launch
+    }
+    return {p.N, whole.tiles, whole.tiles};
+}
+
+static void tile_size(Tiles t, int32_t* rows, int32_t* cols) {
+    *rows = t == kLarge ? Large::BM : t == kWide ? Wide::BM : t == kMedium ? Medium::BM : Small::BM;
+    *cols = t == kLarge ? Large::BN : t == kWide ? Wide::BN : t == kMedium ? Medium::BN : Small::BN;
+}
+
+void linear_tiles(int64_t M, int64_t N, int64_t K, int32_t* rows, int32_t* cols) {
+    GemmProduct p{};
+    p.M = M; p.N = N; p.K = K;
+    if (M <= kLinearStreamRows) *rows = *cols = 16;
+    else tile_size(linear_parts(M, N, K) > 1 || M <= kLinearFewRows ? kSmall : forward_plan(p).tiles, rows, cols);
+}
+
 static int64_t join_blocks(const GemmProduct& p) { return (p.M * ((p.N + 3) / 4) + kJoinThreads - 1) / kJoinThreads; }
 
 hipError_t launch_linear(const GemmProduct& given, float* sums, hipStream_t s) {
@@ -1202,23 +1238,10 @@ hipError_t launch_linear(const GemmProduct& given, float* sums, hipStream_t s) {
         return hipGetLastError();
     }
     if (p.M <= kLinearFewRows) return forward_t<Small>(p, s);
-    // A last column of tiles that is nearly empty can cost a whole round of
-    // them (12352 = 48 x 256 + 64 columns at 4096 rows: 784 tiles, four rounds
-    // instead of three; with gelu, bias and residual 210 us): then the rest
-    // goes by itself in smaller tiles (184 us).  A column's sum runs in the
-    // same order either way.
-    const int cus = compute_units();
-    const Choice whole = choose(p, cus);
-    const int64_t rest = p.N % 256, main = p.N - rest;
-    if (rest > 0 && main > 0) {
-        const GemmProduct m = columns(p, 0, main), r = columns(p, main, rest);
-        const Choice cm = choose(m, cus), cr = choose(r, cus);
-        if (cm.us + cr.us + 3.0 < whole.us) {     // 3: the second launch
-            const hipError_t e = forward(m, cm.tiles, s);
-            return e != hipSuccess ? e : forward(r, cr.tiles, s);
-        }
-    }
-    return forward(p, whole.tiles, s);
+    const ForwardPlan plan = forward_plan(p);
+    if (plan.columns == p.N) return forward(p, plan.tiles, s);
+    const hipError_t e = forward(columns(p, 0, plan.columns), plan.tiles, s);
+    return e != hipSuccess ? e : forward(columns(p, plan.columns, p.N - plan.columns), plan.rest, s);
 }
 
 int64_t linear_dp_blocks(int64_t M) { return (M + kDpRows - 1) / kDpRows; }
@@ -1276,6 +1299,10 @@ void linear_backward_parts(int64_t M, int64_t N, int64_t K, int* dx, int* dw) {
     const BackwardPlan b = backward_plan(M, N, K);
     *dx = b.px;
     *dw = b.pw;
+}
+
+void linear_backward_tiles(int64_t M, int64_t N, int64_t K, int32_t* rows, int32_t* cols) {
+    tile_size(backward_plan(M, N, K).tiles, rows, cols);
 }
 
 hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias, float* sums_dx,

@@ -695,6 +695,12 @@ size_t gdn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 gdn_status gdn_linear_backward(const gdn_linear_grad* grad, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* Rows and columns of the output tiles that gdn_linear (backward: 0) or
+ * gdn_linear_backward runs these sizes with on the current device; a forward
+ * call may give its last columns to smaller ones. */
+gdn_status gdn_linear_tiles(int64_t M, int64_t N, int64_t K, int32_t backward,
+                            int32_t* rows, int32_t* cols);
+
 /* Static text for a status code. */
 const char* gdn_status_string(gdn_status status);
 

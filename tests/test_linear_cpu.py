@@ -122,6 +122,18 @@ def test_backward_fits_one_launch(M, N, K, fits):
         assert b"too large" in L.gdn_last_error()
 
 
+def test_tiles():
+    assert gdn.linear_tiles(1, 4096, 512) == (16, 16) and gdn.linear_tiles(40, 4096, 2048) == (64, 64)
+    with pytest.raises(gdn.GdnError, match="multiple of 8"):
+        gdn.linear_tiles(64, 64, 60)
+    with pytest.raises(gdn.GdnError, match="too large"):
+        gdn.linear_tiles(1 << 20, 1 << 20, 64)
+    with pytest.raises(gdn.GdnError, match="2\\^22"):
+        gdn.linear_tiles(64, (1 << 22) + 8, 64, backward=True)
+    rows = ctypes.c_int32()
+    assert gdn.lib().gdn_linear_tiles(64, 64, 64, 0, ctypes.byref(rows), None) == gdn.GDN_ERR_INVALID_ARGUMENT
+
+
 def test_one_rows_stride_is_not_looked_at():
     """hidden[:, -1] of a long prompt: one row, with whatever stride.  (The
     calls are refused for what is checked last.)"""
