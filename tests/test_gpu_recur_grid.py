@@ -91,3 +91,18 @@ def test_decode():
     gdn.recur_decode(rec, x, x, x, None, state, out=x)
     for lo in spots:
         assert torch.equal(x[lo:lo + 1024], want["out"]) and torch.equal(state[lo:lo + 1024], want["final_state"]), lo
+
+
+@pytest.mark.parametrize("N", [3, 600])
+def test_only_empty_sequences(N):
+    """Without a token anywhere the states and their gradients pass through."""
+    D = 70
+    rec, none = _recur(D), torch.empty((0, D), dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+    status = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    state, grad = torch.randn((N, D), device="cuda"), torch.randn((N, D), device="cuda")
+    f = gdn.recur_forward(rec, none, none, none, none, cu, initial_state=state, want_saved=True, status=status)
+    assert status.item() == 0 and torch.equal(f["final_state"], state)
+    g = gdn.recur_backward(rec, none, none, none, none, none, f["saved"], cu, d_final_state=grad, want_d_initial=True, status=status)
+    assert status.item() == 0 and torch.equal(g["d_initial_state"], grad)
+    assert (g["dA_log"] == 0).all() and (g["ddt_bias"] == 0).all()
