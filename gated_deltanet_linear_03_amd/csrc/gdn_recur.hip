@@ -366,9 +366,9 @@ __device__ __forceinline__ Q load_edge(const typename Q::T* row, const Lane& l, 
 // Rows r0 .. r0 + ROWS - 1 of a tile of `rows` rows at `base`; those past the
 // end read the last one.
 // FAST: one address and offsets of 32 bits.  It takes registers from the whole
-// tiles of the kernel that it is compiled into: forward without saved states,
-// 131072 x 2048 in one sequence 646 us (618 without FAST), 60000 x 1024 in 600
-// sequences 205 us (296).
+// tiles of the kernel that it is compiled into (166 instead of 128): forward
+// without saved states, 131072 x 2048 in one sequence 646 us (618 without FAST),
+// 60000 x 1024 in 600 sequences 205 us (296).
 template <typename Q, int ROWS, bool ONCE, bool FAST>
 __device__ __forceinline__ void load_some(Q* to, const typename Q::T* base, int64_t stride, int r0, int rows, const Lane& l, int D) {
     const int at = r0 < rows ? r0 : rows - 1, more = rows - 1 - at;
@@ -572,7 +572,9 @@ __global__ __launch_bounds__(kThreads, 3) void recur_forward_kernel(RecurParams 
 
 // One work-group per (channel group, sequence) walks the sequence's tiles in
 // order: no words, no workspace, one launch.  Same bits: the state after a
-// tile is the same fma.
+// tile is the same fma.  Bound by the latency of a tile, one after the other: 8
+// sequences of 64 tokens x 2048 14.4 us (the call's host time), one of 512 22.3,
+// where tiles that run side by side take 18.7 for 513 tokens.
 template <bool BF16, bool GATE, bool KEEP>
 __global__ __launch_bounds__(kThreads, 3) void recur_walk_kernel(RecurParams p) {
     __shared__ FwdShared sh;
@@ -883,11 +885,12 @@ struct BwdTile {
 // grid: channel groups x kHalves x the bound on units; the tiles of a sequence
 // are taken from its end.  The rows' h are run again from the state the
 // forward pass saved at the tile's first row.
-// 32768 x 4096 bf16: 615 to 628 us, 3.9 TB/s.  Three waves a SIMD: with all of the
+// 32768 x 4096 bf16: 604 to 628 us, 3.9 TB/s.  Three waves a SIMD: with all of the
 // gates' values in registers (228, two waves) the training step of that size
-// took 1.12 ms, with a's gate computed again 1.00, with it in LDS 0.955.
+// took 1.12 ms, with a's gate computed again 1.00, with it in LDS 0.95.
 // Work-groups of 512 threads that keep all of it in 122 registers: 1.18, as
-// only two share a compute unit.
+// only two share a compute unit.  (fp32 spills 3 registers, 18 without z: 16384
+// x 2048 247 us, without z 204, 4.9 and 4.6 TB/s.)
 template <bool BF16, bool GATE>
 __global__ __launch_bounds__(kThreads, 3) void recur_backward_kernel(RecurParams p) {
     __shared__ BwdShared sh;
@@ -1000,7 +1003,7 @@ __global__ __launch_bounds__(kSumThreads) void recur_sum_kernel(RecurParams p) {
 }
 
 // ---- one token per sequence ------------------------------------------------
-// (bound by the launch: 64 x 2048 takes 4.5 us)
+// (bound by the launch: 64 x 4096 takes 4.6 us)
 constexpr int kDecodeThreads = 256;
 
 template <bool BF16, bool GATE>
@@ -1084,6 +1087,9 @@ hipError_t launch_recur_forward(const RecurParams& p, bool bf16, hipStream_t s) 
     hipError_t e = launch_plan(p, s);
     if (e != hipSuccess) return e;
     const int64_t grid = static_cast<int64_t>(p.groups) * p.tiles;
+    // Saved states: 132 registers without FAST, so three waves a SIMD either way
+    // (32768 x 4096 in 8 whole sequences 319 us with FAST, 320 without; in 8
+    // ragged ones 329 and 349; 60000 x 1024 in 600 sequences 213 and 359).  Else
     // sequences of fewer than four units on average: a quarter of the tiles or
     // more is cut (33000 x 1024, 300 tokens each: 114 us with FAST, 118
     // without; 900 tokens each: 104 and 100)
