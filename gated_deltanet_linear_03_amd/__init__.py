@@ -840,8 +840,9 @@ def _raw_stream(stream, dev):
     """Handle of a stream (None: torch's current one on device `dev`)."""
     if stream is None:
         return _torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device.index != dev:
-        raise ValueError(f"stream: on {stream.device}, the current device is cuda:{dev}")
+    on = getattr(stream, "device", None)            # (a bare handle's owner does not tell)
+    if on is not None and on.index != dev:
+        raise ValueError(f"stream: on {on}, the current device is cuda:{dev}")
     return stream.cuda_stream
 
 

@@ -36,3 +36,16 @@ def test_a_stream_of_another_device_is_refused(given):
     if given:
         assert (out == 3.0).all()
     assert (state == 0).all()
+
+
+def test_a_bare_handle_is_taken_as_it_is():
+    D = 16
+    t = [torch.randn((3, D), device="cuda").to(torch.bfloat16) for _ in range(4)]
+    rec = gdn.Recur(D=D, A_log=torch.zeros(D, device="cuda"), dt_bias=torch.zeros(D, device="cuda"))
+    side = torch.cuda.Stream()
+    out, a, b = torch.empty_like(t[0]), torch.zeros((3, D), device="cuda"), torch.zeros((3, D), device="cuda")
+    want = gdn.recur_decode(rec, *t, a)["out"]
+    torch.cuda.synchronize()
+    gdn.recur_decode(rec, *t, b, out=out, stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(a, b)

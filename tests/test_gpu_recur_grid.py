@@ -9,6 +9,12 @@ import gated_deltanet_linear_03_amd as gdn
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _give_back():
+    yield
+    torch.cuda.empty_cache()
+
+
 def _rows(T, D, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return torch.randn((T, D), generator=g, device="cuda", dtype=torch.bfloat16)
