@@ -1,0 +1,470 @@
+"""Cases of what a training step needs around the recurrence and the linear layer
+(gdn.norm*, gdn.linear_cross_entropy*, gdn.adamw_step): inputs, plain forms in
+elementary torch operations, the framework's calls, the work each cannot do
+without, and the exact values in 64 bits.
+
+Norm, per row:  xh = (x - mean) rstd (rms: xh = x rstd),  y = xh weight + bias.
+
+Loss, per row, with l = x w^T + bias, lse = log sum exp(l), t the target, e the
+label smoothing and c the weight of the squared normaliser:
+    loss = (1 - e) (lse - l_t) + e (lse - mean(l)) + c lse^2
+
+AdamW, per element at step k:
+    m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2
+    p' = p - lr (m' / (1 - b1^k) / (sqrt(v' / (1 - b2^k)) + eps) + decay p)
+with m and v in 32 bits, or m and r = sqrt(v) in e4m3 times one scale for 256
+elements (the largest magnitude / 448), rounded up or down at random: up with
+the probability that keeps the expected value, by 16 bits of a hash of the
+element's index, the tensor's, the step and a seed.  A positive r is not
+rounded to zero.
+"""
+import math
+
+import numpy as np
+import torch
+
+#: False: run() computes the plain forms; True: it calls the framework.
+own = False
+
+BETA1, BETA2, EPS, DECAY = 0.9, 0.999, 1e-8, 0.1
+LR = 2e-5                       # late in its schedule
+
+
+# ---- the cases ---------------------------------------------------------------
+
+def listed():
+    return [
+        # the normalisation before a block, for the next token of one chat: fp32 stream in, bf16 operand out
+        dict(name="norm token", op="norm", M=1, D=2048, kind="rms", x="fp32", y="bf16", bias=False),
+        # the same for a 4096-token prompt
+        dict(name="norm prompt", op="norm", M=4096, D=2048, kind="layer", x="fp32", y="bf16", bias=True),
+        # a training step on 8 packed sequences of a 4096-wide layer, the skip connection's gradient added
+        dict(name="norm train packed", op="norm_train", M=32768, D=4096, kind="layer", x="bf16", y="bf16", bias=True,
+             skip=True),
+        # a training step on a ragged batch of an odd width in fp32
+        dict(name="norm train ragged", op="norm_train", M=9001, D=1023, kind="rms", x="fp32", y="fp32", bias=False,
+             skip=False),
+        # the log-likelihood of one token over the whole vocabulary
+        dict(name="loss token", op="loss", M=1, V=248320, K=2048, bias=False, smooth=0.0, z=0.0),
+        # scoring a 4096-token prompt
+        dict(name="loss prompt", op="loss", M=4096, V=248320, K=2048, bias=False, smooth=0.0, z=0.0),
+        # a training step's loss and gradients on a 4096-token batch
+        dict(name="loss train", op="loss_train", M=4096, V=248320, K=2048, bias=False, smooth=0.0, z=1e-4),
+        # a ragged batch on a narrower head with a bias and smoothed labels
+        dict(name="loss train ragged", op="loss_train", M=1537, V=50001, K=1000, bias=True, smooth=0.1, z=0.0),
+        # the vectors of 30 layers (norms, biases, decay rates): many small tensors
+        dict(name="adamw vectors", op="adamw", bits=32, sizes="30*2048+30*32+30*32+30*128", grad="fp32", copy=False),
+        # the projections, norms and gates of 8 layers, states in 32 bits
+        dict(name="adamw 8 layers", op="adamw", bits=32, sizes="8*25296896+8*8388608+16*2048+16*32", grad="bf16", copy=True),
+        # the same with states in 8 bits
+        dict(name="adamw 8 layers, 8 bits", op="adamw", bits=8, sizes="8*25296896+8*8388608+16*2048+16*32", grad="bf16",
+             copy=True),
+        # odd sizes in 8 bits, tensors that end inside a block
+        dict(name="adamw ragged, 8 bits", op="adamw", bits=8, sizes="1*1+3*1023+2*300001+1*9173505+5*77", grad="fp32",
+             copy=False),
+    ]
+
+
+def _sizes(text):
+    return [int(n) for part in text.split("+") for c, n in [part.split("*")] for _ in range(int(c))]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "norm_train", "loss", "loss_train", "adamw", "adamw"])
+    if op in ("norm", "norm_train"):
+        D = _log(rng, 64, 16384)
+        D = D if rng.random() < 0.4 else max(64, D // 64 * 64)
+        M = _log(rng, 1, min(32768 * 4096 // D, 131072))
+        case = dict(op=op, M=M, D=D, kind=rng.choice(["layer", "rms"]), x=rng.choice(["bf16", "fp32"]),
+                    y=rng.choice(["bf16", "bf16", "fp32"]), bias=rng.random() < 0.5)
+        if op == "norm_train":
+            case["skip"] = rng.random() < 0.5
+        return case
+    if op in ("loss", "loss_train"):
+        V = _log(rng, 1000, 248320)
+        V = V if rng.random() < 0.5 else max(1024, V // 64 * 64)
+        K = 8 * _log(rng, 32, 512)
+        V = min(V, 248320 * 2048 // K)
+        M = _log(rng, 1, min(8192, 4096 * 248320 * 2048 // (V * K)))
+        return dict(op=op, M=M, V=V, K=K, bias=rng.random() < 0.3, smooth=rng.choice([0.0, 0.0, 0.1]),
+                    z=rng.choice([0.0, 1e-4]))
+    bits = rng.choice([8, 32])
+    total, count = _log(rng, 1000, 200_000_000), rng.choice([1, 2, 5, 20, 100])
+    r = np.random.RandomState(rng.randrange(1 << 20))
+    sizes = [max(1, int(w * total)) for w in r.dirichlet(np.full(count, 0.7))]
+    return dict(op="adamw", bits=bits, sizes="+".join("1*%d" % n for n in sizes), grad=rng.choice(["bf16", "fp32"]),
+                copy=rng.random() < 0.5)
+
+
+# ---- the inputs --------------------------------------------------------------
+
+_TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, scale=1.0, dtype=torch.float32):
+        return (torch.randn(shape, generator=gen, device="cuda") * scale).to(dtype)
+
+    s = dict(case)
+    if case["op"] in ("norm", "norm_train"):
+        M, D = case["M"], case["D"]
+        x, y = _TYPES[case["x"]], _TYPES[case["y"]]
+        # rows of different sizes, channels with offsets
+        s["h"] = ((normal(M, D) + 0.5 * normal(D)) * torch.exp(normal(M, 1))).to(x)
+        s["weight"] = 1 + 0.2 * normal(D)
+        s["b"] = 0.2 * normal(D) if case["bias"] else None
+        if case["op"] == "norm_train":
+            s["dy"] = normal(M, D, dtype=y)
+            s["d_skip"] = normal(M, D, dtype=x) if case["skip"] else None
+        return s
+    if case["op"] in ("loss", "loss_train"):
+        M, V, K = case["M"], case["V"], case["K"]
+        s["h"] = normal(M, K, dtype=torch.bfloat16)
+        s["w"] = normal(V, K, scale=2 * K ** -0.5, dtype=torch.bfloat16)
+        s["b"] = normal(V) if case["bias"] else None
+        s["targets"] = torch.randint(0, V, (M,), generator=gen, device="cuda")
+        if M > 1:                                   # prompts and padding carry no target
+            s["targets"][torch.rand(M, generator=gen, device="cuda") < 0.1] = -100
+        if case["op"] == "loss_train":              # the mean over the rows that count, as the user's program forms it
+            s["dloss"] = 1 / (s["targets"] >= 0).sum().clamp(min=1).float().reshape(1)
+        return s
+    # One buffer for each kind of tensor, the tensors views of it that begin at whole lines.
+    sizes = _sizes(case["sizes"])
+    at = [0]
+    for n in sizes:
+        at.append(at[-1] + -(-n // 256) * 256)
+    total = at[-1]
+
+    def views(flat, per=1):
+        return [flat[a // per:a // per + -(-n // per)] for a, n in zip(at, sizes)]
+
+    s["step"] = 1000 + seed % 1000
+    s["seed"] = seed % (1 << 31)
+    s["p"] = normal(total, scale=0.02)
+    g = normal(total, scale=1e-3)
+    v = (normal(total) * 0.3).exp_().mul_(1e-3).square_()               # of about the gradient's square
+    m = normal(total, scale=3e-4)
+    s["decay"] = [0.0 if n < 65536 else DECAY for n in sizes]           # matrices decay, vectors do not
+    s["params"] = views(s["p"])
+    s["grads"] = views(g.to(_TYPES[case["grad"]]))
+    s["copy_of"] = torch.zeros(total, dtype=torch.bfloat16, device="cuda") if case["copy"] else None
+    s["copies"] = views(s["copy_of"]) if case["copy"] else None
+    if case["bits"] == 32:
+        s["m"], s["v"] = m, v
+    else:
+        # (a tensor's last block is filled up with zeros)
+        inside = torch.zeros(total, device="cuda")
+        for a, n in zip(at, sizes):
+            inside[a:a + n] = 1
+        for name, value in (("m", m * inside), ("v", v.sqrt_() * inside)):
+            blocks = value.view(-1, 256)
+            s[name + "_scale"] = blocks.abs().amax(1) / 448
+            q = (blocks / s[name + "_scale"].clamp(min=1e-30)[:, None]).clamp_(-448, 448)
+            if name == "v":
+                q = torch.where(blocks > 0, q.clamp(min=2.0 ** -9), q)
+            s[name] = q.to(torch.float8_e4m3fn).view(-1)
+            s[name + "_scales"] = views(s[name + "_scale"], 256)
+    s["ms"], s["vs"] = views(s["m"]), views(s["v"])
+    return s
+
+
+# ---- one pass ----------------------------------------------------------------
+
+def run(s):
+    if own:
+        return _call(s)
+    op = s["op"]
+    if op in ("norm", "norm_train"):
+        return _plain_norm(s)
+    return _plain_loss(s) if op in ("loss", "loss_train") else _plain_adamw(s)
+
+
+def _call(s):
+    """The framework's calls, as a user's program makes them."""
+    import gated_deltanet_linear_03_amd as gdn
+    op = s["op"]
+    if op in ("norm", "norm_train"):
+        kind = gdn.GDN_NORM_LAYER if s["kind"] == "layer" else gdn.GDN_NORM_RMS
+        out_dtype = _TYPES[s["y"]]
+        if op == "norm":
+            return {"y": gdn.norm(s["h"], s["weight"], s["b"], kind=kind, out_dtype=out_dtype)}
+        stats = torch.empty((2, s["M"]), device="cuda")
+        y = gdn.norm(s["h"], s["weight"], s["b"], kind=kind, out_dtype=out_dtype, stats=stats)
+        g = gdn.norm_backward(s["dy"], s["h"], s["weight"], stats, kind=kind, d_residual=s["d_skip"],
+                              want_dbias=s["bias"])
+        return {"y": y, "rstd": stats[1], **g}
+    if op in ("loss", "loss_train"):
+        how = dict(bias=s["b"], label_smoothing=s["smooth"], z_loss=s["z"])
+        out = gdn.linear_cross_entropy(s["h"], s["w"], s["targets"], **how)
+        if op == "loss_train":
+            out.update(gdn.linear_cross_entropy_backward(s["dloss"], s["h"], s["w"], s["targets"], out["lse"], **how))
+        return out
+    if "opt" not in s:
+        scales = {k: s[k + "s"] for k in ("m_scale", "v_scale") if s["bits"] == 8}
+        s["opt"] = gdn.AdamW(s["params"], s["ms"], s["vs"], **scales, copies=s["copies"], beta1=BETA1, beta2=BETA2,
+                             eps=EPS, weight_decay=s["decay"], seed=s["seed"])
+    gdn.adamw_step(s["opt"], s["grads"], lr=LR, step=s["step"])
+    return _updated(s)
+
+
+def _updated(s):
+    names = ["p", "copy_of", "m", "v"] + (["m_scale", "v_scale"] if s["bits"] == 8 else [])
+    return {k: s[k] for k in names if s[k] is not None}
+
+
+def _plain_norm(s):
+    x = s["h"].float()
+    centred = x - x.mean(1, keepdim=True) if s["kind"] == "layer" else x
+    rstd = 1 / torch.sqrt((centred * centred).mean(1, keepdim=True) + 1e-5)
+    xh = centred * rstd
+    y = xh * s["weight"]
+    if s["b"] is not None:
+        y = y + s["b"]
+    out = {"y": y.to(_TYPES[s["y"]])}
+    if s["op"] == "norm":
+        return out
+    dy = s["dy"].float()
+    q = dy * s["weight"]
+    dx = q - xh * (q * xh).mean(1, keepdim=True)
+    if s["kind"] == "layer":
+        dx = dx - q.mean(1, keepdim=True)
+    dx = dx * rstd
+    if s["d_skip"] is not None:
+        dx = dx + s["d_skip"].float()
+    out.update(rstd=rstd[:, 0], dx=dx.to(_TYPES[s["x"]]), dweight=(dy * xh).double().sum(0).float())
+    if s["bias"]:
+        out["dbias"] = dy.double().sum(0).float()
+    return out
+
+
+def _plain_loss(s):
+    x, w, t, e = s["h"].float(), s["w"].float(), s["targets"], s["smooth"]
+    V = s["V"]
+    l = x @ w.t()
+    if s["b"] is not None:
+        l = l + s["b"]
+    top = l.amax(1, keepdim=True)
+    lse = (top + torch.log(torch.exp(l - top).sum(1, keepdim=True)))[:, 0]
+    counts = t >= 0
+    at = t.clamp(min=0)[:, None]
+    loss = (1 - e) * (lse - l.gather(1, at)[:, 0]) + s["z"] * lse * lse
+    if e:
+        loss = loss + e * (lse - l.mean(1))
+    out = {"loss": torch.where(counts, loss, torch.zeros_like(loss)), "lse": lse}
+    if s["op"] == "loss":
+        return out
+    g = torch.where(counts, s["dloss"].expand_as(lse), torch.zeros_like(lse))
+    dl = torch.exp(l - lse[:, None]) * (1 + 2 * s["z"] * lse)[:, None]
+    dl -= e / V
+    dl.scatter_add_(1, at, torch.full_like(at, -(1 - e), dtype=torch.float32))
+    dl *= g[:, None]
+    out["dx"], out["dw"] = (dl @ w).to(torch.bfloat16), (dl.t() @ x).to(torch.bfloat16)
+    if s["bias"]:
+        out["dbias"] = dl.double().sum(0).float()
+    return out
+
+
+def _mix(h):
+    """The 32-bit finaliser of MurmurHash3 (Appleby), in the low half of 64 bits."""
+    h = h & 0xFFFFFFFF
+    h = ((h ^ (h >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
+    h = ((h ^ (h >> 13)) * 0xC2B2AE35) & 0xFFFFFFFF
+    return h ^ (h >> 16)
+
+
+def _round_up_or_down(value, scale, chance):
+    """e4m3 of value / scale: up where the fraction of a step is more than 1 - chance / 65536 (in 64 bits: next to a border)."""
+    y = (value.double() / scale.double().clamp(min=1e-300)).clamp(-448, 448)
+    low = torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6)))        # exponents of the format: -6 .. 8
+    unit = torch.exp2(low - 3)
+    steps = torch.floor(y.abs() / unit + chance / 65536.0)
+    return torch.where(y < 0, -1, 1) * (steps * unit).clamp(max=448)
+
+
+def _plain_adamw(s):
+    b1, b2, k = BETA1, BETA2, s["step"]
+    c1, c2 = 1 - b1 ** k, 1 - b2 ** k
+    for i, (p, g, m, v) in enumerate(zip(s["params"], s["grads"], s["ms"], s["vs"])):
+        n = p.numel()
+        g = g.float()
+        if s["bits"] == 8:
+            block = torch.arange(n, device=p.device) // 256
+            ms, vs = s["m_scales"][i], s["v_scales"][i]
+            m0, v0 = m.float() * ms[block], (v.float() * vs[block]).square()
+        else:
+            m0, v0 = m, v
+        m1 = b1 * m0 + (1 - b1) * g
+        v1 = b2 * v0 + (1 - b2) * g * g
+        p -= LR * (m1 / c1 / (torch.sqrt(v1 / c2) + EPS) + s["decay"][i] * p)
+        if s["copies"] is not None:
+            s["copies"][i].copy_(p)
+        if s["bits"] == 32:
+            m.copy_(m1)
+            v.copy_(v1)
+            continue
+        at = torch.arange(n, device=p.device)
+        word = _mix(_mix(s["seed"] + k * 0x9E3779B1) + i * 0x9E3779B1)
+        h = _mix(word + (at & 0xFFFFFFFF) * 0x9E3779B1)
+        # in 64 bits, so that no border is missed
+        g = g.double()
+        m1 = b1 * m0.double() + (1 - b1) * g
+        r1 = torch.sqrt(b2 * v0.double() + (1 - b2) * g * g)
+        for value, q, scale, chance in ((m1, m, ms, h & 0xFFFF), (r1, v, vs, h >> 16)):
+            full = torch.zeros(scale.numel() * 256, dtype=torch.float64, device=p.device)
+            full[:n] = value.abs()
+            scale.copy_(full.view(-1, 256).amax(1) / 448)
+            new = _round_up_or_down(value, scale[block], chance)
+            if q is v:
+                new = torch.where((value > 0) & (new == 0), 2.0 ** -9, new)
+            q.copy_(new.to(torch.float32).to(torch.float8_e4m3fn))
+    return _updated(s)
+
+
+# ---- what a pass cannot do without -------------------------------------------
+
+def work(case):
+    op = case["op"]
+    size = {"bf16": 2, "fp32": 4}
+    if op in ("norm", "norm_train"):
+        M, D, x, y = case["M"], case["D"], size[case["x"]], size[case["y"]]
+        params = 4 * D * (2 if case["bias"] else 1)
+        nbytes, flops = M * D * (x + y) + params, 8 * M * D
+        if op == "norm_train":
+            # then x and dy in, dx out, the gradients of the parameters, a number a row in between
+            nbytes += M * D * (2 * x + y + (x if case["skip"] else 0)) + 2 * params + 4 * M
+            flops += 14 * M * D
+        return {"bytes": nbytes, "flops": flops}
+    if op in ("loss", "loss_train"):
+        M, V, K = case["M"], case["V"], case["K"]
+        nbytes, flops = 2 * (M + V) * K + 16 * M + (4 * V if case["bias"] else 0), 2 * M * V * K
+        if op == "loss_train":
+            nbytes, flops = 2 * nbytes + 2 * (M + V) * K, 3 * flops
+        return {"bytes": nbytes, "flops": flops}
+    n = sum(_sizes(case["sizes"]))
+    state = 16 if case["bits"] == 32 else 4 + 16 / 256
+    return {"bytes": int(n * (8 + size[case["grad"]] + (2 if case["copy"] else 0) + state)), "flops": 16 * n}
+
+
+# ---- the exact values --------------------------------------------------------
+
+def exact(case, seed):
+    """From the definitions, in 64 bits."""
+    s = prepare(case, seed)
+    if case["op"] in ("norm", "norm_train"):
+        return _exact_norm(s)
+    return _exact_loss(s) if case["op"] in ("loss", "loss_train") else _exact_adamw(s)
+
+
+def _exact_norm(s):
+    x, D, scale = s["h"].double(), s["D"], s["weight"].double()
+    if s["kind"] == "layer":
+        x = x - x.sum(1, keepdim=True) / D
+    deviation = torch.sqrt(x.square().sum(1, keepdim=True) / D + 1e-5)
+    unit = x / deviation
+    y = unit * scale if s["b"] is None else torch.addcmul(s["b"].double(), unit, scale)
+    if s["op"] == "norm":
+        return {"y": y}
+    dy = s["dy"].double()
+    d_unit = dy * scale
+    # through deviation, which every element of the row has a part in, then through the mean
+    d_dev = -(d_unit * x).sum(1, keepdim=True) / deviation ** 2
+    dx = d_unit / deviation + d_dev * x / (D * deviation)
+    if s["kind"] == "layer":
+        dx = dx - dx.sum(1, keepdim=True) / D
+    if s["d_skip"] is not None:
+        dx = dx + s["d_skip"].double()
+    out = {"y": y, "rstd": 1 / deviation[:, 0], "dx": dx, "dweight": torch.einsum("md,md->d", dy, unit)}
+    if s["bias"]:
+        out["dbias"] = torch.einsum("md->d", dy)
+    return out
+
+
+def _exact_loss(s):
+    x, w = s["h"].double(), s["w"].double()
+    M, V, e, z = s["M"], s["V"], s["smooth"], s["z"]
+    logits = torch.mm(x, w.t())
+    if s["b"] is not None:
+        logits += s["b"].double()
+    lse = torch.logsumexp(logits, 1)
+    rows = (s["targets"] >= 0).nonzero()[:, 0]
+    cols = s["targets"][rows]
+    loss = torch.zeros(M, dtype=torch.float64, device=x.device)
+    # cross entropy with the smoothed distribution, which adds up to one
+    mixed = (1 - e) * logits[rows, cols] + (e / V) * logits[rows].sum(1) if e else logits[rows, cols]
+    loss[rows] = lse[rows] - mixed + z * lse[rows] ** 2
+    out = {"loss": loss, "lse": lse}
+    if s["op"] == "loss":
+        return out
+    d = logits.sub_(lse[:, None]).exp_()
+    d *= (1 + 2 * z * lse)[:, None]
+    d -= e / V
+    d[rows, cols] -= 1 - e
+    g = torch.zeros_like(loss)
+    g[rows] = s["dloss"].double()
+    d *= g[:, None]
+    out["dx"], out["dw"] = torch.mm(d, w), torch.mm(d.t(), x)
+    if s["bias"]:
+        out["dbias"] = d.sum(0)
+    return out
+
+
+def _exact_adamw(s):
+    k, eight = s["step"], s["bits"] == 8
+    out = {n: t.double() for n, t in _updated(s).items()}
+    at = 0
+    for i, p in enumerate(s["params"]):
+        n = p.numel()
+        blocks = -(-n // 256)
+        part, lines = slice(at, at + n), slice(at // 256, at // 256 + blocks)
+        at += blocks * 256
+        grad = s["grads"][i].double()
+        m, v = out["m"][part], out["v"][part]
+        if eight:
+            m = m * out["m_scale"][lines].repeat_interleave(256)[:n]
+            v = (v * out["v_scale"][lines].repeat_interleave(256)[:n]) ** 2
+        m = torch.lerp(grad, m, BETA1)
+        v = torch.lerp(grad * grad, v, BETA2)
+        rate = (m / (1 - BETA1 ** k)) / ((v / (1 - BETA2 ** k)) ** 0.5 + EPS)
+        out["p"][part] = p.double() * (1 - LR * s["decay"][i]) - LR * rate
+        if "copy_of" in out:
+            out["copy_of"][part] = out["p"][part]
+        if not eight:
+            out["m"][part], out["v"][part] = m, v
+            continue
+        # the hash in 32-bit words of numpy's kind of arithmetic: products wrap
+        def mixed(u):
+            u = u ^ (u >> np.uint32(16))
+            u = u * np.uint32(0x85EBCA6B)
+            u = u ^ (u >> np.uint32(13))
+            u = u * np.uint32(0xC2B2AE35)
+            return u ^ (u >> np.uint32(16))
+
+        golden = np.uint32(0x9E3779B1)
+        with np.errstate(over="ignore"):
+            key = mixed(np.array([s["seed"]], dtype=np.uint32) + np.uint32(k) * golden)
+            key = mixed(key + np.uint32(i) * golden)
+            bits = mixed(np.arange(n, dtype=np.uint32) * golden + key[0])
+        half = torch.from_numpy((bits & np.uint32(0xFFFF)).astype(np.int32)).to(p.device).double()
+        rest = torch.from_numpy((bits >> np.uint32(16)).astype(np.int32)).to(p.device).double()
+        for name, value, up in (("m", m, half), ("v", v ** 0.5, rest)):
+            pad = torch.zeros(blocks * 256, dtype=torch.float64, device=p.device)
+            pad[:n] = value
+            scale = pad.view(blocks, 256).abs().max(1).values / 448
+            # what the state stands for is relative to the scale as it is kept, in 32 bits
+            scale = scale.float().double()
+            ratio = (pad.view(blocks, 256) / torch.where(scale > 0, scale, 1.0)[:, None]).view(-1)[:n].clamp(-448, 448)
+            mantissa, exponent = torch.frexp(ratio.abs().clamp(min=2.0 ** -6))
+            step = torch.ldexp(torch.ones_like(ratio), exponent - 4)
+            near = torch.floor(ratio.abs() / step + up / 65536) * step
+            near = torch.minimum(near, torch.full_like(near, 448.0)) * torch.sign(ratio)
+            if name == "v":
+                near = torch.where((value > 0) & (near == 0), torch.full_like(near, 2.0 ** -9), near)
+            out[name][part] = near
+            out[name + "_scale"][lines] = scale
+    return out
