@@ -40,6 +40,9 @@ GDN_ACT_RELU = 1
 GDN_ACT_GELU = 2
 GDN_ACT_GELU_TANH = 3
 GDN_ACT_SILU = 4
+GDN_NORM_LAYER = 0
+GDN_NORM_RMS = 1
+GDN_ADAMW_BLOCK = 256
 
 EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_prefill_timed", "gdn_prefill_launches", "gdn_decode", "gdn_decode_multi",
@@ -51,7 +54,8 @@ EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_recur_saved_bytes", "gdn_recur_workspace_bytes", "gdn_recur_forward",
            "gdn_recur_backward_workspace_bytes", "gdn_recur_backward", "gdn_recur_decode",
            "gdn_linear", "gdn_linear_workspace_bytes", "gdn_linear_backward_workspace_bytes", "gdn_linear_backward",
-           "gdn_linear_tiles")
+           "gdn_linear_tiles", "gdn_norm", "gdn_norm_backward_workspace_bytes", "gdn_norm_backward",
+           "gdn_adamw_step")
 NOALLOC_SCRATCH_BYTES = 128 << 20       # GDN_NOALLOC_SCRATCH_BYTES
 SNAPSHOT_MAGIC = 0x50534E47
 SNAPSHOT_VERSION = 1
@@ -182,6 +186,38 @@ class CLinearGrad(ctypes.Structure):
                 ("dbias", ctypes.c_void_p)]
 
 
+class CNormIO(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("x_dtype", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int32), ("y_stride", ctypes.c_int64),
+                ("stats", ctypes.c_void_p)]
+
+
+class CNormGrad(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("kind", ctypes.c_int32),
+                ("dy", ctypes.c_void_p), ("dy_dtype", ctypes.c_int32), ("dy_stride", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("stats", ctypes.c_void_p),
+                ("d_residual", ctypes.c_void_p), ("d_residual_stride", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p)]
+
+
+class CAdamWTensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("grad_dtype", ctypes.c_int32), ("copy", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("weight_decay", ctypes.c_float)]
+
+
+class CAdamW(ctypes.Structure):
+    _fields_ = [("state_bits", ctypes.c_int32), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("lr", ctypes.c_float), ("eps", ctypes.c_float), ("step", ctypes.c_int32),
+                ("seed", ctypes.c_uint32), ("lr_ptr", ctypes.c_void_p), ("step_ptr", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -294,6 +330,16 @@ def lib():
         L.gdn_linear_backward.restype = ctypes.c_int
         L.gdn_linear_backward.argtypes = [ctypes.POINTER(CLinearGrad), ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]
+        L.gdn_norm.restype = ctypes.c_int
+        L.gdn_norm.argtypes = [ctypes.POINTER(CNormIO), ctypes.c_void_p]
+        L.gdn_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_norm_backward_workspace_bytes.argtypes = [ctypes.c_int64] * 2
+        L.gdn_norm_backward.restype = ctypes.c_int
+        L.gdn_norm_backward.argtypes = [ctypes.POINTER(CNormGrad), ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p]
+        L.gdn_adamw_step.restype = ctypes.c_int
+        L.gdn_adamw_step.argtypes = [ctypes.POINTER(CAdamW), ctypes.POINTER(CAdamWTensor), ctypes.c_int32,
+                                     ctypes.c_void_p]
         _lib = L
     return _lib
 
@@ -1230,6 +1276,197 @@ def linear_backward(dy, x, w, preact=None, act=GDN_ACT_NONE, want_dx=True, want_
     ws, nb = _bytes(workspace, "workspace", dev)
     _check(lib().gdn_linear_backward(ctypes.byref(gr), ws, nb, _raw_stream(stream, dev)))
     return res
+
+
+# ---- norms over rows ------------------------------------------------------------
+
+def norm(x, weight=None, bias=None, kind=GDN_NORM_LAYER, eps=1e-5, out=None, out_dtype=None, stats=None,
+         stream=None):
+    """Layer norm (or, with GDN_NORM_RMS, RMS norm) of the rows of x [M, D]
+    (bf16 or fp32, rows may be strided), times weight [D] plus bias [D] (fp32,
+    optional).  out: the tensor to write, else one of out_dtype (default: x's
+    type).  stats: a [2, M] fp32 tensor that receives each row's mean (RMS: 0)
+    and 1 / deviation for norm_backward.  Returns the output."""
+    if x.dim() != 2:
+        raise ValueError(f"x: a matrix needed, shape is {tuple(x.shape)}")
+    dev = _device()
+    M, D = x.shape
+    xc = _float_code(x.dtype, "x")
+    px, sx = _matrix(x, "x", M, D, x.dtype, dev)
+    if out is None:
+        dt = x.dtype if out_dtype is None else out_dtype
+        yc = _float_code(dt, "out_dtype")
+        out = _new(x, (M, D), dt, stream)
+        py, sy = out.data_ptr(), D
+    else:
+        if out_dtype is not None and out_dtype != out.dtype:
+            raise ValueError(f"out: {out_dtype} needed, not {out.dtype}")
+        yc = _float_code(out.dtype, "out")
+        py, sy = _matrix(out, "out", M, D, out.dtype, dev)
+    io = CNormIO(M, D, kind, eps, px, xc, sx, _dense(weight, "weight", D, None, dev),
+                 _dense(bias, "bias", D, None, dev), py, yc, sy, _stats(stats, M, dev))
+    _check(lib().gdn_norm(ctypes.byref(io), _raw_stream(stream, dev)))
+    return out
+
+
+def _stats(stats, M, dev):
+    """Pointer of optional norm statistics: contiguous fp32 [2, M]."""
+    if stats is None:
+        return None
+    _on_device(stats, "stats", dev)
+    if stats.shape != (2, M) or stats.dtype is not _torch.float32 or not stats.is_contiguous():
+        raise ValueError(f"stats: contiguous float32 [2, {M}] needed, not {stats.dtype} {tuple(stats.shape)}")
+    return stats.data_ptr()
+
+
+def norm_backward_workspace_bytes(M: int, D: int) -> int:
+    """Bytes of workspace of ``gdn_norm_backward``."""
+    n = lib().gdn_norm_backward_workspace_bytes(int(M), int(D))
+    if n == 0:
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, lib().gdn_last_error().decode())
+    return int(n)
+
+
+def norm_backward(dy, x, weight, stats, kind=GDN_NORM_LAYER, d_residual=None, want_dx=True, want_dweight=True,
+                  want_dbias=False, dx=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """Gradients of norm() from dy [M, D] (the output's type): a dict with dx
+    [M, D] (x's type), dweight [D] and, if asked, dbias [D] (fp32).  weight and
+    stats: as given to norm() and as it wrote them.  d_residual [M, D] (x's
+    type): added to dx, the gradient that reaches x beside the norm; may be dx
+    itself.  dx, dweight, dbias: tensors to write instead of new ones."""
+    import torch
+    if dy.dim() != 2 or x.dim() != 2:
+        raise ValueError("dy and x: matrices needed")
+    if stats is None:
+        raise ValueError("stats: needed, as norm() wrote them")
+    dev = _device()
+    M, D = x.shape
+    xc, yc = _float_code(x.dtype, "x"), _float_code(dy.dtype, "dy")
+    px, sx = _matrix(x, "x", M, D, x.dtype, dev)
+    py, sy = _matrix(dy, "dy", M, D, dy.dtype, dev)
+    pr, sr = (None, 0) if d_residual is None else _matrix(d_residual, "d_residual", M, D, x.dtype, dev)
+    res = {}
+    if want_dx or dx is not None:
+        res["dx"] = dx if dx is not None else _new(x, (M, D), x.dtype, stream)
+    if want_dweight or dweight is not None:
+        res["dweight"] = dweight if dweight is not None else _new(x, (D,), torch.float32, stream)
+    if want_dbias or dbias is not None:
+        res["dbias"] = dbias if dbias is not None else _new(x, (D,), torch.float32, stream)
+    pdx, sdx = _matrix(res["dx"], "dx", M, D, x.dtype, dev) if "dx" in res else (None, 0)
+    if workspace is None and ("dweight" in res or "dbias" in res):
+        workspace = _new(x, (norm_backward_workspace_bytes(M, D),), torch.uint8, stream)
+    gr = CNormGrad(M, D, kind, py, yc, sy, px, xc, sx, _dense(weight, "weight", D, None, dev),
+                   _stats(stats, M, dev), pr, sr, pdx, sdx, _dense(res.get("dweight"), "dweight", D, None, dev),
+                   _dense(res.get("dbias"), "dbias", D, None, dev))
+    ws, nb = _bytes(workspace, "workspace", dev)
+    _check(lib().gdn_norm_backward(ctypes.byref(gr), ws, nb, _raw_stream(stream, dev)))
+    return res
+
+
+# ---- the update of the weights ----------------------------------------------------
+
+class AdamW:
+    """The tensors that adamw_step updates and the numbers they share: params
+    (fp32, contiguous, any shapes) and for each of them its states.  States in
+    32 bits: m and v, fp32 of the parameter's size.  States in 8 bits (with
+    m_scale and v_scale): m and v hold m and sqrt(v) as float8_e4m3fn (or
+    uint8), in units of m_scale and v_scale, fp32 of one entry for 256
+    elements.  copies: bf16 tensors of the parameters' sizes (or None, alone
+    or in the list) that receive the new values.  weight_decay: a number, or
+    one for each tensor.  seed: of the random rounding of 8-bit states.
+    adamw_states() makes the states."""
+
+    def __init__(self, params, m, v, m_scale=None, v_scale=None, copies=None, beta1=0.9, beta2=0.999,
+                 eps=1e-8, weight_decay=0.0, seed=0):
+        n = len(params)
+        self.bits = 32 if m_scale is None and v_scale is None else 8
+        if self.bits == 8 and (m_scale is None or v_scale is None):
+            raise ValueError("m_scale and v_scale: both are needed for states in 8 bits")
+        scales = [None] * n
+        decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+        lists = dict(params=params, m=m, v=v, m_scale=scales if m_scale is None else m_scale,
+                     v_scale=scales if v_scale is None else v_scale,
+                     copies=scales if copies is None else copies, weight_decay=decay)
+        for name, x in lists.items():
+            if len(x) != n:
+                raise ValueError(f"{name}: {n} entries needed, not {len(x)}")
+        for name in lists:
+            setattr(self, name, list(lists[name]))
+        self.beta1, self.beta2, self.eps, self.seed = float(beta1), float(beta2), float(eps), int(seed) & 0xFFFFFFFF
+        dev = self.device = _device()
+        import torch
+        floats, codes = (torch.float32,), (torch.float8_e4m3fn, torch.uint8)
+        state = floats if self.bits == 32 else codes
+        self._c = (CAdamWTensor * n)()
+        for i, p in enumerate(self.params):
+            size = p.numel()
+            blocks = -(-size // GDN_ADAMW_BLOCK)
+            c = self._c[i]
+            c.n, c.param = size, _flat(p, f"params[{i}]", size, floats, dev)
+            c.m, c.v = (_flat(t[i], f"{k}[{i}]", size, state, dev) for k, t in (("m", self.m), ("v", self.v)))
+            if self.bits == 8:
+                c.m_scale, c.v_scale = (_flat(t[i], f"{k}[{i}]", blocks, floats, dev)
+                                        for k, t in (("m_scale", self.m_scale), ("v_scale", self.v_scale)))
+            if self.copies[i] is not None:
+                c.copy = _flat(self.copies[i], f"copies[{i}]", size, (torch.bfloat16,), dev)
+            c.weight_decay = self.weight_decay[i]
+
+
+def _flat(t, name, n, dtypes, dev):
+    """Pointer of a contiguous tensor of n elements of one of `dtypes`."""
+    if t.dtype in dtypes and t.get_device() == dev and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    _on_device(t, name, dev)
+    raise ValueError(f"{name}: {n} contiguous elements of {' or '.join(str(d) for d in dtypes)} needed, "
+                     f"not {t.dtype} {tuple(t.shape)}")
+
+
+def adamw_states(params, bits=32):
+    """Zero states for params, as keyword arguments of AdamW: m and v, with
+    bits=8 in e4m3 and with m_scale and v_scale."""
+    import torch
+    if bits not in (8, 32):
+        raise ValueError(f"bits: 8 or 32 needed, not {bits}")
+    dt = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    states = {k: [torch.zeros(p.shape, dtype=dt, device=p.device) for p in params] for k in ("m", "v")}
+    if bits == 8:
+        for k in ("m_scale", "v_scale"):
+            states[k] = [p.new_zeros(-(-p.numel() // GDN_ADAMW_BLOCK), dtype=torch.float32) for p in params]
+    return states
+
+
+def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
+    """One AdamW step of all of opt's tensors: grads, bf16 or fp32 of the
+    parameters' sizes, contiguous.  lr: a number, or a one-element fp32 device
+    tensor; step: the step's number, from 1 on, or a one-element int32 device
+    tensor: a captured step reads those at every replay.  grad_scale: a
+    one-element fp32 device tensor, a factor of every gradient; when it is not
+    finite nothing is written."""
+    import torch
+    n, dev = len(opt.params), _device()
+    if dev != opt.device:
+        raise ValueError(f"opt: made on cuda:{opt.device}, the current device is cuda:{dev}")
+    if len(grads) != n:
+        raise ValueError(f"grads: {n} entries needed, not {len(grads)}")
+    a = CAdamW(opt.bits, opt.beta1, opt.beta2, 0.0, opt.eps, 0, opt.seed, None, None, None)
+    if isinstance(lr, torch.Tensor):
+        a.lr_ptr = _flat(lr, "lr", 1, (torch.float32,), dev)
+    else:
+        a.lr = lr
+    if isinstance(step, torch.Tensor):
+        a.step_ptr = _flat(step, "step", 1, (torch.int32,), dev)
+    else:
+        a.step = step
+    if grad_scale is not None:
+        a.grad_scale = _flat(grad_scale, "grad_scale", 1, (torch.float32,), dev)
+    # the call's own table: two threads may step the same tensors' gradients one after the other
+    c = (CAdamWTensor * n)()
+    ctypes.memmove(c, opt._c, ctypes.sizeof(c))
+    kinds = (torch.bfloat16, torch.float32)
+    for t, g in zip(c, grads):
+        t.grad = _flat(g, "grads", t.n, kinds, dev)
+        t.grad_dtype = GDN_DTYPE_BF16 if g.dtype is torch.bfloat16 else GDN_DTYPE_FP32
+    _check(lib().gdn_adamw_step(ctypes.byref(a), c, n, _raw_stream(stream, dev)))
 
 
 def snapshot_bytes(layer: Layer) -> int:

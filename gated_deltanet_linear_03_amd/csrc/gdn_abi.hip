@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "../../include/gdn.h"
@@ -1506,6 +1507,188 @@ gdn_status gdn_linear_tiles(int64_t M, int64_t N, int64_t K, int32_t backward, i
     if (st != GDN_OK || (st = backward ? check_backward(M, N, K) : check_forward(M, N)) != GDN_OK) return st;
     if (backward) gdn::linear_backward_tiles(M, N, K, rows, cols);
     else gdn::linear_tiles(M, N, K, rows, cols);
+    return GDN_OK;
+}
+
+// ---- norms over rows ----------------------------------------------------------------
+
+namespace {
+
+gdn_status check_dtype(const char* name, int32_t dt) {
+    if (dt != GDN_DTYPE_BF16 && dt != GDN_DTYPE_FP32) return fail(GDN_ERR_INVALID_ARGUMENT, "%s %d unknown", name, dt);
+    return GDN_OK;
+}
+
+gdn_status check_norm(int64_t M, int64_t D, int32_t kind) {
+    if (M < 0 || M >= (int64_t(1) << 31) || D < 1 || D > kMaxStride)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "M (%lld) must be in [0, 2^31), D (%lld) in [1, 2^22]", static_cast<long long>(M),
+                    static_cast<long long>(D));
+    if (kind != GDN_NORM_LAYER && kind != GDN_NORM_RMS) return fail(GDN_ERR_INVALID_ARGUMENT, "kind %d unknown", kind);
+    return GDN_OK;
+}
+
+// an optional fp32 buffer
+gdn_status check_floats(const char* name, const void* p) {
+    if (!aligned(p, 4)) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 4-byte aligned", name);
+    return GDN_OK;
+}
+
+}  // namespace
+
+gdn_status gdn_norm(const gdn_norm_io* io, void* stream) {
+    g_err[0] = 0;
+    if (!io) return fail(GDN_ERR_INVALID_ARGUMENT, "io is NULL");
+    const int64_t M = io->M, D = io->D;
+    gdn_status st = check_norm(M, D, io->kind);
+    if (st != GDN_OK || (st = check_dtype("x_dtype", io->x_dtype)) != GDN_OK || (st = check_dtype("y_dtype", io->y_dtype)) != GDN_OK)
+        return st;
+    if (!(io->eps >= 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+    if (M == 0) return GDN_OK;
+    gdn::NormParams p{};
+    p.M = M; p.D = D;
+    p.center = io->kind == GDN_NORM_LAYER;
+    p.eps = io->eps;
+    p.x = io->x; p.y = io->y;
+    p.weight = io->weight; p.bias = io->bias;
+    p.stats = io->stats;
+    p.xs = row_stride(io->x_stride, D, M);
+    p.ys = row_stride(io->y_stride, D, M);
+    const size_t xe = act_size(io->x_dtype), ye = act_size(io->y_dtype);
+    if ((st = check_rows("x", io->x, p.xs, D, xe)) != GDN_OK || (st = check_rows("y", io->y, p.ys, D, ye)) != GDN_OK) return st;
+    if ((st = check_floats("weight", io->weight)) != GDN_OK || (st = check_floats("bias", io->bias)) != GDN_OK ||
+        (st = check_floats("stats", io->stats)) != GDN_OK)
+        return st;
+    const size_t params = static_cast<size_t>(D) * 4;
+    const Span in[3] = {{io->x, row_bytes(M, p.xs, D, xe)}, {io->weight, params}, {io->bias, params}};
+    const Span y{io->y, row_bytes(M, p.ys, D, ye)}, stats{io->stats, static_cast<size_t>(M) * 8};
+    if (any_overlap(y, in, 3) || any_overlap(stats, in, 3) || any_overlap(y, &stats, 1))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "y or stats overlaps an input or each other");
+    hipError_t e = gdn::launch_norm(p, io->x_dtype == GDN_DTYPE_BF16, io->y_dtype == GDN_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "norm launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
+size_t gdn_norm_backward_workspace_bytes(int64_t M, int64_t D) {
+    g_err[0] = 0;
+    if (check_norm(M, D, GDN_NORM_LAYER) != GDN_OK) return 0;
+    const int64_t n = round_up(8 * gdn::norm_parts(M, D) * D, 256);
+    return static_cast<size_t>(n < 256 ? 256 : n);
+}
+
+gdn_status gdn_norm_backward(const gdn_norm_grad* gr, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = 0;
+    if (!gr) return fail(GDN_ERR_INVALID_ARGUMENT, "grad is NULL");
+    const int64_t M = gr->M, D = gr->D;
+    gdn_status st = check_norm(M, D, gr->kind);
+    if (st != GDN_OK || (st = check_dtype("x_dtype", gr->x_dtype)) != GDN_OK ||
+        (st = check_dtype("dy_dtype", gr->dy_dtype)) != GDN_OK)
+        return st;
+    gdn::NormParams p{};
+    p.M = M; p.D = D;
+    p.center = gr->kind == GDN_NORM_LAYER;
+    p.x = gr->x; p.dy = gr->dy;
+    p.weight = gr->weight;
+    p.stats_in = gr->stats;
+    p.dx = M > 0 ? gr->dx : nullptr;
+    p.d_residual = p.dx ? gr->d_residual : nullptr;
+    p.dweight = gr->dweight; p.dbias = gr->dbias;
+    const bool params = p.dweight || p.dbias;
+    if (!p.dx && !params) return GDN_OK;
+    p.xs = row_stride(gr->x_stride, D, M);
+    p.dys = row_stride(gr->dy_stride, D, M);
+    p.drs = row_stride(gr->d_residual_stride, D, M);
+    p.dxs = row_stride(gr->dx_stride, D, M);
+    const size_t xe = act_size(gr->x_dtype), ye = act_size(gr->dy_dtype), D4 = static_cast<size_t>(D) * 4;
+    if (M > 0) {
+        if ((st = check_rows("x", gr->x, p.xs, D, xe)) != GDN_OK || (st = check_rows("dy", gr->dy, p.dys, D, ye)) != GDN_OK) return st;
+        if (!gr->stats) return fail(GDN_ERR_INVALID_ARGUMENT, "stats is NULL");
+    }
+    if (p.dx && (st = check_rows("dx", p.dx, p.dxs, D, xe)) != GDN_OK) return st;
+    if (p.d_residual && (st = check_rows("d_residual", p.d_residual, p.drs, D, xe)) != GDN_OK) return st;
+    if ((st = check_floats("weight", gr->weight)) != GDN_OK || (st = check_floats("stats", gr->stats)) != GDN_OK ||
+        (st = check_floats("dweight", gr->dweight)) != GDN_OK || (st = check_floats("dbias", gr->dbias)) != GDN_OK)
+        return st;
+    const size_t need = gdn_norm_backward_workspace_bytes(M, D);
+    if (params && M > 0) {
+        if (!ws) return fail(GDN_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+        if (!aligned(ws, 256)) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        if (ws_bytes < need) return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, need %zu", ws_bytes, need);
+        p.part = static_cast<float*>(ws);
+    }
+    const Span in[4] = {{gr->x, row_bytes(M, p.xs, D, xe)}, {gr->dy, row_bytes(M, p.dys, D, ye)}, {gr->weight, D4},
+                        {gr->stats, static_cast<size_t>(M) * 8}};
+    const Span res{p.d_residual, row_bytes(M, p.drs, D, xe)};
+    const Span out[4] = {{p.dx, row_bytes(M, p.dxs, D, xe)}, {p.dweight, D4}, {p.dbias, D4}, {p.part, p.part ? need : 0}};
+    const bool in_place = p.d_residual == p.dx && p.drs == p.dxs;
+    for (int i = 0; i < 4; ++i)
+        if (any_overlap(out[i], in, 4) || any_overlap(out[i], out, i) || (!(in_place && i == 0) && any_overlap(out[i], &res, 1)))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input or another output");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (M > 0) {
+        e = gdn::launch_norm_backward(p, gr->x_dtype == GDN_DTYPE_BF16, gr->dy_dtype == GDN_DTYPE_BF16, s);
+    } else {
+        e = gdn::launch_fill_zero(p.dweight, D, s);
+        if (e == hipSuccess) e = gdn::launch_fill_zero(p.dbias, D, s);
+    }
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "norm backward launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
+// ---- the update of the weights ------------------------------------------------------
+
+static_assert(GDN_ADAMW_BLOCK == gdn::kAdamwBlock, "block of the 8-bit states");
+
+gdn_status gdn_adamw_step(const gdn_adamw* a, const gdn_adamw_tensor* tensors, int32_t count, void* stream) {
+    g_err[0] = 0;
+    if (!a) return fail(GDN_ERR_INVALID_ARGUMENT, "adamw is NULL");
+    if (a->state_bits != 8 && a->state_bits != 32)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "state_bits must be 8 or 32, not %d", a->state_bits);
+    if (!(a->beta1 >= 0 && a->beta1 < 1 && a->beta2 >= 0 && a->beta2 < 1))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "beta1 and beta2 must be in [0, 1)");
+    if (!(a->eps >= 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+    if (!a->lr_ptr && !std::isfinite(a->lr)) return fail(GDN_ERR_INVALID_ARGUMENT, "lr must be finite");
+    if (!a->step_ptr && a->step < 1) return fail(GDN_ERR_INVALID_ARGUMENT, "step (%d) must be at least 1", a->step);
+    if (!aligned(a->lr_ptr, 4) || !aligned(a->step_ptr, 4) || !aligned(a->grad_scale, 4))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "lr_ptr, step_ptr and grad_scale must be 4-byte aligned");
+    if (count < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "count (%d) is negative", count);
+    if (count > 0 && !tensors) return fail(GDN_ERR_INVALID_ARGUMENT, "tensors is NULL");
+    const bool eight = a->state_bits == 8;
+    const size_t se = eight ? 1 : 4;
+    for (int32_t i = 0; i < count; ++i) {
+        const gdn_adamw_tensor& t = tensors[i];
+        if (t.n < 0 || t.n > (int64_t(1) << 40) || gdn::adamw_chunks(t.n) > gdn::kAdamwMostChunks)
+            return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: n (%lld) is negative or too large", i, static_cast<long long>(t.n));
+        if (t.n == 0) continue;
+        if (t.grad_dtype != GDN_DTYPE_BF16 && t.grad_dtype != GDN_DTYPE_FP32)
+            return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: grad_dtype %d unknown", i, t.grad_dtype);
+        const size_t ge = act_size(t.grad_dtype), n = static_cast<size_t>(t.n);
+        if (!t.param || !t.grad || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale)))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: param, grad, m, v or a scale is NULL", i);
+        if (!aligned(t.param, 4) || !aligned(t.grad, ge) || !aligned(t.copy, 2) || !aligned(t.m, se) || !aligned(t.v, se) ||
+            (eight && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: not element aligned", i);
+        if (!(t.weight_decay >= 0.f) || std::isinf(t.weight_decay))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: weight_decay must be >= 0 and finite", i);
+        const size_t blocks = eight ? (n + GDN_ADAMW_BLOCK - 1) / GDN_ADAMW_BLOCK * 4 : 0;
+        const Span out[9] = {{t.param, 4 * n}, {t.copy, 2 * n}, {t.m, se * n}, {t.v, se * n}, {eight ? t.m_scale : nullptr, blocks},
+                             {eight ? t.v_scale : nullptr, blocks}, {a->lr_ptr, 4}, {a->step_ptr, 4}, {a->grad_scale, 4}};
+        const Span in{t.grad, ge * n};
+        for (int k = 0; k < 9; ++k)
+            if ((k < 6 && any_overlap(out[k], &in, 1)) || any_overlap(out[k], out, k < 6 ? k : 6))
+                return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: two of its buffers overlap", i);
+    }
+    gdn::AdamwParams p{};
+    p.lr = a->lr; p.eps = a->eps;
+    p.beta1 = static_cast<float>(a->beta1); p.rest1 = static_cast<float>(1 - a->beta1);
+    p.beta2 = static_cast<float>(a->beta2); p.rest2 = static_cast<float>(1 - a->beta2);
+    p.log_beta1 = static_cast<float>(std::log(a->beta1));
+    p.log_beta2 = static_cast<float>(std::log(a->beta2));
+    p.step = a->step;
+    p.seed = a->seed;
+    p.lr_ptr = a->lr_ptr; p.step_ptr = a->step_ptr; p.grad_scale = a->grad_scale;
+    hipError_t e = gdn::launch_adamw(p, tensors, count, eight, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "adamw launch failed: %s", hipGetErrorString(e));
     return GDN_OK;
 }
 

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/gdn.h"
+
 namespace gdn {
 
 struct DecodeParams {
@@ -282,5 +284,49 @@ hipError_t launch_linear(const GemmProduct& p, float* sums, hipStream_t s);
 // dx or dw with ep.y NULL is left out
 hipError_t launch_linear_backward(const LinearDp& dp, const GemmProduct& dx, const GemmProduct& dw, float* dbias, float* sums_dx,
                                   float* sums_dw, hipStream_t s);
+
+// ---- norms over rows (gdn_norm.hip) -----------------------------------------
+struct NormParams {
+    int64_t M, D;
+    int center;                          // 0: RMS, the mean counts as 0
+    float eps;
+    const void* x;
+    const float *weight, *bias;          // [D] or NULL
+    void* y;
+    int64_t xs, ys;                      // row strides, elements
+    float* stats;                        // [2][M] mean and 1 / deviation, or NULL
+    // backward
+    const float* stats_in;
+    const void *dy, *d_residual;
+    void* dx;
+    int64_t dys, drs, dxs;
+    float *dweight, *dbias;
+    float* part;                         // [norm_parts(M, D)][2][D], or NULL: neither dweight nor dbias
+};
+
+int norm_parts(int64_t M, int64_t D);
+// M, D > 0; d_residual and dx have x's type, dy has y's
+hipError_t launch_norm(const NormParams& p, bool x_bf16, bool y_bf16, hipStream_t s);
+hipError_t launch_norm_backward(const NormParams& p, bool x_bf16, bool y_bf16, hipStream_t s);
+
+// ---- AdamW over many tensors (gdn_adamw.hip) ----------------------------------
+constexpr int kAdamwBlock = 256;         // elements that share a scale of the 8-bit states
+constexpr int kAdamwTensors = 32;        // tensors of a launch (its arguments hold them)
+constexpr int64_t kAdamwMostChunks = (int64_t(1) << 24) - 1;   // work-groups of a launch: fewer than 2^32 work-items
+
+struct AdamwParams {
+    float lr, eps;
+    float beta1, beta2, rest1, rest2;    // beta and 1 - beta
+    float log_beta1, log_beta2;
+    int32_t step;
+    uint32_t seed;
+    const float* lr_ptr;                 // device values instead of lr and step, or NULL
+    const int32_t* step_ptr;
+    const float* grad_scale;             // device factor of the gradients (not finite: no step), or NULL
+};
+
+// work-groups of a tensor of n elements
+int64_t adamw_chunks(int64_t n);
+hipError_t launch_adamw(const AdamwParams& p, const gdn_adamw_tensor* tensors, int count, bool eight, hipStream_t s);
 
 }  // namespace gdn

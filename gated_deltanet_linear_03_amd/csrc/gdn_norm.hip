@@ -1,0 +1,496 @@
+// gdn_norm.hip -- layer norm and RMS norm over rows, forward and backward.
+//
+// Forward, per row of D values: xh = (x - mean) rstd with rstd = 1 /
+// sqrt(var + eps) (RMS: mean = 0, rstd = 1 / sqrt(mean(x^2) + eps)), y = xh
+// weight + bias.  The row stays in registers, so the variance is summed from
+// the differences to the mean, and x is read once.
+// Backward, with q = dy weight: dx = rstd (q - mean(q) - xh mean(q xh)) (RMS:
+// without mean(q)) + d_residual, dweight = sum over rows of dy xh, dbias = sum
+// of dy.  A work-group keeps its columns' sums of all its rows in registers
+// and leaves them once; a second kernel adds the work-groups' sums in order.
+// Everything is in 32 bits between the loads and the stores.
+#include "gdn_device.hpp"
+#include "gdn_kernels.hpp"
+
+namespace gdn {
+
+namespace {
+
+// W adjacent elements as they lie in memory, element aligned
+template <bool BF16, int W>
+struct Run {
+    static constexpr int kWords = BF16 ? W / 2 : W;
+    typedef uint32_t V __attribute__((ext_vector_type(kWords), aligned(BF16 ? 2 : 4)));
+    V v;
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        v = *reinterpret_cast<const V*>(static_cast<const uint8_t*>(p) + at * (BF16 ? 2 : 4));
+    }
+    __device__ __forceinline__ void load_once(const void* p, int64_t at) {
+        v = __builtin_nontemporal_load(reinterpret_cast<const V*>(static_cast<const uint8_t*>(p) + at * (BF16 ? 2 : 4)));
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (BF16) return __uint_as_float(e % 2 ? v[e / 2] & 0xFFFF0000u : v[e / 2] << 16);
+        else return __uint_as_float(v[e]);
+    }
+    __device__ __forceinline__ static void store(void* p, int64_t at, const float* f) {
+        V o;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (BF16) {
+                const f32x2 t = {f[2 * i], f[2 * i + 1]};
+                o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(t, bf16x2));
+            } else {
+                o[i] = __float_as_uint(f[i]);
+            }
+        }
+        __builtin_nontemporal_store(o, reinterpret_cast<V*>(static_cast<uint8_t*>(p) + at * (BF16 ? 2 : 4)));
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float load_one(const void* p, int64_t at) {
+    if constexpr (BF16) return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[at]);
+    else return static_cast<const float*>(p)[at];
+}
+template <bool BF16>
+__device__ __forceinline__ void store_one(void* p, int64_t at, float f) {
+    if constexpr (BF16) static_cast<uint16_t*>(p)[at] = f32_to_bf16_bits(f);
+    else static_cast<float*>(p)[at] = f;
+}
+
+// Columns of a thread: NV runs of W, T threads to a row.  Run j begins at
+// column W (t + T j), but never past D - W: the last runs of a row whose D is
+// no multiple of their columns begin earlier and repeat columns that another
+// thread (or run) has too.  Those count once: fresh() tells.  So no load has a
+// condition.  (D >= W.)
+template <int W, int T, int NV>
+struct Columns {
+    int at[NV], from[NV];                     // first column; the first that counts here (at + W: none)
+    __device__ __forceinline__ void init(int t, int64_t D) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = static_cast<int64_t>(W) * (t + T * j);
+            at[j] = static_cast<int>(c + W <= D ? c : D - W);
+            from[j] = static_cast<int>(c < D ? c : D);
+        }
+    }
+    __device__ __forceinline__ bool fresh(int j, int e) const { return at[j] + e >= from[j]; }
+};
+
+// Sums of N values over the T threads of a row, in every one of them.  red:
+// one of two places in LDS, in turn (a wave that is a sum ahead writes the
+// other one).
+template <int T, int N>
+__device__ __forceinline__ void row_sums(float* s, float* red, int t) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = T == 16 ? group_sum<16>(s[i]) : wave_sum(s[i]);
+    if constexpr (T > kWave) {
+        constexpr int kW = T / kWave;
+        if (t % kWave == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[i * kW + t / kWave] = s[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            s[i] = red[i * kW];
+#pragma unroll
+            for (int w = 1; w < kW; ++w) s[i] += red[i * kW + w];
+        }
+    }
+}
+
+constexpr int rows_of(int T) { return T < 256 ? 256 / T : 1; }   // rows that a work-group holds at a time
+
+// One block of rows a work-group, and more only where the grid would be past
+// what a launch holds.  MASK: D is not W T NV.
+template <bool XB, bool YB, bool MASK, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormParams p) {
+    constexpr int W = XB && YB ? 8 : 4, R = rows_of(T);
+    __shared__ float red[2][T > kWave ? T / kWave : 1];
+    const int t = threadIdx.x % T;
+    Columns<W, T, NV> cols;
+    cols.init(t, p.D);
+    const float per = 1.f / static_cast<float>(p.D);
+    int turn = 0;
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * R; m0 < p.M; m0 += static_cast<int64_t>(gridDim.x) * R) {
+        int64_t m = m0 + threadIdx.x / T;
+        const bool real = R == 1 || m < p.M;
+        if (!real) m = p.M - 1;
+        Run<XB, W> x[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j].load_once(p.x, m * p.xs + cols.at[j]);
+        float s[1] = {0.f}, mean = 0.f;
+        if (p.center) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < W; ++e) s[0] += !MASK || cols.fresh(j, e) ? x[j].get(e) : 0.f;
+            row_sums<T, 1>(s, red[turn], t);
+            turn ^= 1;
+            mean = s[0] / static_cast<float>(p.D);   // (a constant row has differences of 0)
+            s[0] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float d = !MASK || cols.fresh(j, e) ? x[j].get(e) - mean : 0.f;
+                s[0] = fmaf(d, d, s[0]);
+            }
+        row_sums<T, 1>(s, red[turn], t);
+        turn ^= 1;
+        const float rstd = 1.f / sqrtf(fmaf(s[0], per, p.eps));
+        if (!real) continue;
+        if (t == 0 && p.stats) {
+            p.stats[m] = mean;
+            p.stats[p.M + m] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (MASK && cols.from[j] >= p.D) continue;
+            float f[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) f[e] = (x[j].get(e) - mean) * rstd;
+#pragma unroll
+            for (int g = 0; g < W / 4; ++g) {
+                if (p.weight) {
+                    Run<false, 4> w;
+                    w.load(p.weight, cols.at[j] + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[4 * g + e] *= w.get(e);
+                }
+                if (p.bias) {
+                    Run<false, 4> b;
+                    b.load(p.bias, cols.at[j] + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[4 * g + e] += b.get(e);
+                }
+            }
+            Run<YB, W>::store(p.y, m * p.ys + cols.at[j], f);
+        }
+    }
+}
+
+// Rows that no work-group can hold, and rows of fewer than eight values: read
+// again for each step (from the L2).
+constexpr int kLongThreads = 512;
+
+template <bool XB, bool YB>
+__global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormParams p) {
+    __shared__ float red[2][kLongThreads / kWave];
+    const int t = threadIdx.x;
+    const float per = 1.f / static_cast<float>(p.D);
+    int turn = 0;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        float s[1] = {0.f}, mean = 0.f;
+        if (p.center) {
+            for (int64_t c = t; c < p.D; c += kLongThreads) s[0] += load_one<XB>(p.x, m * p.xs + c);
+            row_sums<kLongThreads, 1>(s, red[turn], t);
+            turn ^= 1;
+            mean = s[0] / static_cast<float>(p.D);   // (a constant row has differences of 0)
+            s[0] = 0.f;
+        }
+        for (int64_t c = t; c < p.D; c += kLongThreads) {
+            const float d = load_one<XB>(p.x, m * p.xs + c) - mean;
+            s[0] = fmaf(d, d, s[0]);
+        }
+        row_sums<kLongThreads, 1>(s, red[turn], t);
+        turn ^= 1;
+        const float rstd = 1.f / sqrtf(fmaf(s[0], per, p.eps));
+        if (t == 0 && p.stats) {
+            p.stats[m] = mean;
+            p.stats[p.M + m] = rstd;
+        }
+        for (int64_t c = t; c < p.D; c += kLongThreads) {
+            float f = (load_one<XB>(p.x, m * p.xs + c) - mean) * rstd;
+            if (p.weight) f *= p.weight[c];
+            if (p.bias) f += p.bias[c];
+            store_one<YB>(p.y, m * p.ys + c, f);
+        }
+    }
+}
+
+// ---- backward ------------------------------------------------------------------
+// A work-group takes every gridDim-th block of rows.  part: [work-group][2][D]
+// sums of dy xh and of dy.
+template <bool XB, bool YB, bool MASK, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormParams p) {
+    constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
+    constexpr int kW = T > kWave ? T / kWave : 1;
+    __shared__ float red[2][R][2 * kW];
+    const int t = threadIdx.x % T, r = threadIdx.x / T;
+    Columns<W, T, NV> cols;
+    cols.init(t, p.D);
+    float w[C], dw[C], db[C];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            w[W * j + e] = p.weight ? p.weight[cols.at[j] + e] : 1.f;
+            dw[W * j + e] = db[W * j + e] = 0.f;
+        }
+    const float per = 1.f / static_cast<float>(p.D);
+    const bool params = p.part != nullptr;
+    int turn = 0;
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * R; m0 < p.M; m0 += static_cast<int64_t>(gridDim.x) * R) {
+        int64_t m = m0 + r;
+        const bool real = R == 1 || m < p.M;
+        if (!real) m = p.M - 1;
+        Run<XB, W> x[NV], skip[NV];
+        Run<YB, W> dy[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            x[j].load_once(p.x, m * p.xs + cols.at[j]);
+            dy[j].load_once(p.dy, m * p.dys + cols.at[j]);
+        }
+        if (p.d_residual) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) skip[j].load_once(p.d_residual, m * p.drs + cols.at[j]);
+        }
+        const float mean = p.center ? p.stats_in[m] : 0.f, rstd = p.stats_in[p.M + m];
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const bool count = !MASK || cols.fresh(j, e);
+                const float d = count ? dy[j].get(e) : 0.f, xh = (x[j].get(e) - mean) * rstd, q = d * w[W * j + e];
+                s[0] += q;
+                s[1] = fmaf(q, count ? xh : 0.f, s[1]);
+                if (params && real) {
+                    dw[W * j + e] = fmaf(d, count ? xh : 0.f, dw[W * j + e]);
+                    db[W * j + e] += d;
+                }
+            }
+        if (!p.dx) continue;
+        row_sums<T, 2>(s, red[turn][r], t);
+        turn ^= 1;
+        if (!real) continue;
+        const float a = p.center ? s[0] * per : 0.f, b = s[1] * per;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (MASK && cols.from[j] >= p.D) continue;
+            float f[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float xh = (x[j].get(e) - mean) * rstd;
+                f[e] = rstd * (dy[j].get(e) * w[W * j + e] - a - xh * b);
+                if (p.d_residual) f[e] += skip[j].get(e);
+            }
+            Run<XB, W>::store(p.dx, m * p.dxs + cols.at[j], f);
+        }
+    }
+    if (!params) return;
+    float* const out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+    if constexpr (R == 1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (!MASK || cols.fresh(j, e)) {
+                    out[cols.at[j] + e] = dw[W * j + e];
+                    out[p.D + cols.at[j] + e] = db[W * j + e];
+                }
+    } else {                                  // the rows' sums, added in order
+        __shared__ float all[R - 1][2 * C][T];
+        if (r > 0) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                all[r - 1][i][t] = dw[i];
+                all[r - 1][C + i][t] = db[i];
+            }
+        }
+        __syncthreads();
+        if (r > 0) return;
+#pragma unroll 1
+        for (int k = 0; k < R - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                dw[i] += all[k][i][t];
+                db[i] += all[k][C + i][t];
+            }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (!MASK || cols.fresh(j, e)) {
+                    out[cols.at[j] + e] = dw[W * j + e];
+                    out[p.D + cols.at[j] + e] = db[W * j + e];
+                }
+    }
+}
+
+template <bool XB, bool YB>
+__global__ __launch_bounds__(kLongThreads) void norm_backward_long_kernel(NormParams p) {
+    __shared__ float red[2][2 * kLongThreads / kWave];
+    const int t = threadIdx.x;
+    const float per = 1.f / static_cast<float>(p.D);
+    int turn = 0;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        const float mean = p.center ? p.stats_in[m] : 0.f, rstd = p.stats_in[p.M + m];
+        float s[2] = {0.f, 0.f};
+        for (int64_t c = t; c < p.D; c += kLongThreads) {
+            const float q = load_one<YB>(p.dy, m * p.dys + c) * (p.weight ? p.weight[c] : 1.f);
+            s[0] += q;
+            s[1] = fmaf(q, (load_one<XB>(p.x, m * p.xs + c) - mean) * rstd, s[1]);
+        }
+        row_sums<kLongThreads, 2>(s, red[turn], t);
+        turn ^= 1;
+        const float a = p.center ? s[0] * per : 0.f, b = s[1] * per;
+        for (int64_t c = t; c < p.D; c += kLongThreads) {
+            const float q = load_one<YB>(p.dy, m * p.dys + c) * (p.weight ? p.weight[c] : 1.f);
+            const float xh = (load_one<XB>(p.x, m * p.xs + c) - mean) * rstd;
+            float f = rstd * (q - a - xh * b);
+            if (p.d_residual) f += load_one<XB>(p.d_residual, m * p.drs + c);
+            store_one<XB>(p.dx, m * p.dxs + c, f);
+        }
+    }
+}
+
+// The parameters' sums of the same rows: a column a thread, blockIdx.y taking
+// every gridDim.y-th row.
+template <bool XB, bool YB>
+__global__ __launch_bounds__(256) void norm_params_long_kernel(NormParams p) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (c >= p.D) return;
+    float dw = 0.f, db = 0.f;
+    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
+        const float mean = p.center ? p.stats_in[m] : 0.f, rstd = p.stats_in[p.M + m];
+        const float d = load_one<YB>(p.dy, m * p.dys + c);
+        dw = fmaf(d, (load_one<XB>(p.x, m * p.xs + c) - mean) * rstd, dw);
+        db += d;
+    }
+    float* const out = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.D;
+    out[c] = dw;
+    out[p.D + c] = db;
+}
+
+// dweight and dbias from the work-groups' sums, in their order: 32 columns a
+// work-group, each by 32 threads.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormParams p, int blocks) {
+    __shared__ float t[32][33];
+    const int col = threadIdx.x % 32, sl = threadIdx.x / 32;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col;
+    float s = 0.f;
+    if (c < 2 * p.D) {
+#pragma unroll 8
+        for (int64_t i = sl; i < blocks; i += 32) s += p.part[i * 2 * p.D + c];
+    }
+    t[sl][col] = s;
+    __syncthreads();
+    if (sl == 0 && c < 2 * p.D) {
+#pragma unroll
+        for (int k = 1; k < 32; ++k) s += t[k][col];
+        if (c < p.D) {
+            if (p.dweight) p.dweight[c] = s;
+        } else if (p.dbias) {
+            p.dbias[c - p.D] = s;
+        }
+    }
+}
+
+// (a launch of 2^32 work-items or more runs a part of them without an error)
+dim3 grid_of_rows(int64_t n) { return dim3(static_cast<unsigned>(n < (1 << 21) ? n : 1 << 21)); }
+
+// Threads of a row and runs of a thread.  Forward: a wave to a row as long as
+// its registers hold it (eight runs), then work-groups.  Backward: 16 columns
+// a thread at the most, whose sums, weights and inputs take about 100
+// registers.
+template <bool XB, bool YB, bool MASK, int T, int NV>
+hipError_t forward_t(const NormParams& p, hipStream_t s) {
+    constexpr int R = rows_of(T);
+    hipLaunchKernelGGL((norm_forward_kernel<XB, YB, MASK, T, NV>), grid_of_rows((p.M + R - 1) / R),
+                       dim3(T < 256 ? 256 : T), 0, s, p);
+    return hipGetLastError();
+}
+
+template <bool XB, bool YB, int T, int NV>
+hipError_t forward_m(const NormParams& p, hipStream_t s) {
+    constexpr int W = XB && YB ? 8 : 4;
+    return p.D == W * T * NV ? forward_t<XB, YB, false, T, NV>(p, s) : forward_t<XB, YB, true, T, NV>(p, s);
+}
+
+template <bool XB, bool YB>
+hipError_t forward(const NormParams& p, hipStream_t s) {
+    constexpr int W = XB && YB ? 8 : 4;
+    const int64_t runs = (p.D + W - 1) / W;
+    if (p.D < W || runs > 4096) {
+        hipLaunchKernelGGL((norm_forward_long_kernel<XB, YB>), grid_of_rows(p.M), dim3(kLongThreads), 0, s, p);
+        return hipGetLastError();
+    }
+    if (runs <= 16) return forward_m<XB, YB, 16, 1>(p, s);
+    if (runs <= 64) return forward_m<XB, YB, 64, 1>(p, s);
+    if (runs <= 128) return forward_m<XB, YB, 64, 2>(p, s);
+    if (runs <= 256) return forward_m<XB, YB, 64, 4>(p, s);
+    if (runs <= 512) return forward_m<XB, YB, 64, 8>(p, s);
+    if (runs <= 1024) return forward_m<XB, YB, 256, 4>(p, s);
+    if (runs <= 2048) return forward_m<XB, YB, 256, 8>(p, s);
+    return forward_m<XB, YB, 1024, 4>(p, s);
+}
+
+template <bool XB, bool YB, bool MASK, int T, int NV>
+hipError_t backward_t(const NormParams& p, hipStream_t s) {
+    hipLaunchKernelGGL((norm_backward_kernel<XB, YB, MASK, T, NV>), dim3(static_cast<unsigned>(norm_parts(p.M, p.D))),
+                       dim3(T < 256 ? 256 : T), 0, s, p);
+    return hipGetLastError();
+}
+
+template <bool XB, bool YB, int T, int NV>
+hipError_t backward_m(const NormParams& p, hipStream_t s) {
+    constexpr int W = XB && YB ? 8 : 4;
+    return p.D == W * T * NV ? backward_t<XB, YB, false, T, NV>(p, s) : backward_t<XB, YB, true, T, NV>(p, s);
+}
+
+constexpr int64_t kLongRow = 16384;
+
+template <bool XB, bool YB>
+hipError_t backward(const NormParams& p, hipStream_t s) {
+    constexpr int W = XB && YB ? 8 : 4, NV = 16 / W;
+    if (p.D < 8 || p.D > kLongRow) {
+        if (p.dx) {
+            hipLaunchKernelGGL((norm_backward_long_kernel<XB, YB>), grid_of_rows(p.M), dim3(kLongThreads), 0, s, p);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess || !p.part) return e;
+        }
+        hipLaunchKernelGGL((norm_params_long_kernel<XB, YB>),
+                           dim3(static_cast<unsigned>((p.D + 255) / 256), static_cast<unsigned>(norm_parts(p.M, p.D))), dim3(256), 0, s, p);
+        return hipGetLastError();
+    }
+    if (p.D <= 16 * W) return backward_m<XB, YB, 16, 1>(p, s);
+    if (p.D <= 64 * W) return backward_m<XB, YB, 64, 1>(p, s);
+    if (p.D <= 1024) return backward_m<XB, YB, 64, NV>(p, s);
+    if (p.D <= 2048) return backward_m<XB, YB, 128, NV>(p, s);
+    if (p.D <= 4096) return backward_m<XB, YB, 256, NV>(p, s);
+    if (p.D <= 8192) return backward_m<XB, YB, 512, NV>(p, s);
+    return backward_m<XB, YB, 1024, NV>(p, s);
+}
+
+}  // namespace
+
+// Work-groups of the backward pass, each of which leaves a sum for each
+// column: as many as fill the card (less than a work-group of 256 threads four
+// times a compute unit leaves loads waiting), no more than there are rows.
+int norm_parts(int64_t M, int64_t D) {
+    const int64_t rows = D <= 128 ? 16 : D <= 1024 ? 4 : D <= 2048 ? 2 : 1;
+    const int64_t fill = D > kLongRow || D < 8 ? 64 : compute_units() * (D <= 4096 ? 4 : D <= 8192 ? 2 : 1);
+    const int64_t n = (M + rows - 1) / rows;
+    return static_cast<int>(n < fill ? n : fill);
+}
+
+hipError_t launch_norm(const NormParams& p, bool x_bf16, bool y_bf16, hipStream_t s) {
+    if (x_bf16) return y_bf16 ? forward<true, true>(p, s) : forward<true, false>(p, s);
+    return y_bf16 ? forward<false, true>(p, s) : forward<false, false>(p, s);
+}
+
+hipError_t launch_norm_backward(const NormParams& p, bool x_bf16, bool y_bf16, hipStream_t s) {
+    hipError_t e;
+    if (x_bf16) e = y_bf16 ? backward<true, true>(p, s) : backward<true, false>(p, s);
+    else e = y_bf16 ? backward<false, true>(p, s) : backward<false, false>(p, s);
+    if (e != hipSuccess || !p.part) return e;
+    hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<unsigned>((2 * p.D + 31) / 32)), dim3(1024), 0, s, p,
+                       norm_parts(p.M, p.D));
+    return hipGetLastError();
+}
+
+}  // namespace gdn

@@ -703,6 +703,128 @@ gdn_status gdn_linear_backward(const gdn_linear_grad* grad, void* workspace,
 gdn_status gdn_linear_tiles(int64_t M, int64_t N, int64_t K, int32_t backward,
                             int32_t* rows, int32_t* cols);
 
+/* ---- norms over rows ------------------------------------------------------
+ * What stands before a block, and its backward pass.  Per row of D values:
+ *
+ *   xh = (x - mean) rstd,  rstd = 1 / sqrt(var + eps)     (GDN_NORM_LAYER)
+ *   xh = x rstd,           rstd = 1 / sqrt(mean(x^2) + eps) (GDN_NORM_RMS)
+ *   y = xh weight + bias
+ *
+ * in fp32 between x and y, each of which is bf16 or fp32; the variance is the
+ * mean square of the differences to the mean.  A row's bits do not depend on
+ * the other rows.  Row strides in elements, 0 means dense, a single row's is
+ * not looked at; they and the addresses need no more than element alignment. */
+#define GDN_NORM_LAYER 0
+#define GDN_NORM_RMS 1
+
+/* The bytes from the first to the last element of y and the stats must not
+ * overlap those of another buffer. */
+typedef struct {
+    int64_t M, D;                  /* M >= 0, 1 <= D <= 2^22 */
+    int32_t kind;                  /* GDN_NORM_* */
+    float eps;                     /* >= 0 */
+    const void* x;                 /* [M][D] */
+    int32_t x_dtype;
+    int64_t x_stride;
+    const float* weight;           /* [D], NULL: ones */
+    const float* bias;             /* [D], NULL: zeros */
+    void* y;                       /* [M][D] */
+    int32_t y_dtype;
+    int64_t y_stride;
+    float* stats;                  /* optional [2][M]: mean (RMS: 0) and rstd, for gdn_norm_backward */
+} gdn_norm_io;
+
+gdn_status gdn_norm(const gdn_norm_io* io, void* stream);
+
+/* Gradients of gdn_norm: with q = dy weight,
+ *   dx = rstd (q - mean(q) - xh mean(q xh)) + d_residual  (RMS: without mean(q)),
+ *   dweight = sum over the rows of dy xh, dbias = sum of dy.
+ * d_residual: what reaches x beside the norm (the skip connection's gradient).
+ * Each of dx, dweight, dbias may be NULL.  d_residual may be dx itself (same
+ * address and stride); otherwise the bytes from the first to the last element
+ * of an output must not overlap those of another buffer.  The sums' order is
+ * fixed by M, D and the device: the same bits from call to call. */
+typedef struct {
+    int64_t M, D;
+    int32_t kind;
+    const void* dy;                /* [M][D] */
+    int32_t dy_dtype;
+    int64_t dy_stride;
+    const void* x;                 /* [M][D], as given to gdn_norm */
+    int32_t x_dtype;
+    int64_t x_stride;
+    const float* weight;           /* as given to gdn_norm */
+    const float* stats;            /* [2][M], as gdn_norm wrote it */
+    const void* d_residual;        /* optional [M][D] in x_dtype */
+    int64_t d_residual_stride;
+    void* dx;                      /* [M][D] in x_dtype */
+    int64_t dx_stride;
+    float* dweight;                /* [D] */
+    float* dbias;                  /* [D] */
+} gdn_norm_grad;
+
+/* Bytes of device workspace gdn_norm_backward needs; 0 on error.  (Without
+ * dweight and dbias it needs none and looks at none.) */
+size_t gdn_norm_backward_workspace_bytes(int64_t M, int64_t D);
+
+/* Enqueue the backward pass.  workspace: device memory, 256-byte aligned, not
+ * shared with a concurrently running call. */
+gdn_status gdn_norm_backward(const gdn_norm_grad* grad, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* ---- the update of the weights ----------------------------------------------
+ * One AdamW step over many tensors.  Per element at step k:
+ *
+ *   m' = beta1 m + (1 - beta1) g,  v' = beta2 v + (1 - beta2) g^2
+ *   p' = p - lr (m' / (1 - beta1^k) / (sqrt(v' / (1 - beta2^k)) + eps)
+ *                + weight_decay p)
+ *
+ * in fp32.  States in 32 bits: m and v.  States in 8 bits: m and r = sqrt(v) in
+ * e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest 448) times an fp32 scale
+ * for GDN_ADAMW_BLOCK consecutive elements, which is the largest magnitude of
+ * the new values / 448 (0 where that is below 2^-100).  A value / scale is
+ * rounded up or down at random, up when its fraction of a step of the format
+ * plus u / 65536 reaches 1, so that its expected value is kept; a positive r is
+ * not rounded to 0.  u: for m the low and for r the high 16 bits of
+ *   mix(key + mix(i >> 32) + i * 0x9E3779B1),
+ *   key = mix(mix(seed + k * 0x9E3779B1) + t * 0x9E3779B1)
+ * of element i of tensor t, in 32 bits, mix the finaliser of MurmurHash3.  The
+ * parameter is updated from the unrounded m' and v'. */
+#define GDN_ADAMW_BLOCK 256
+
+typedef struct {
+    int64_t n;                     /* elements; 0: nothing to do */
+    float* param;                  /* updated in place */
+    const void* grad;
+    int32_t grad_dtype;            /* gdn_dtype */
+    void* copy;                    /* optional: receives the new values in bf16 */
+    void *m, *v;                   /* fp32, or bytes (m and r in e4m3); zeros before the first step */
+    float *m_scale, *v_scale;      /* 8 bits: [ceil(n / GDN_ADAMW_BLOCK)] each */
+    float weight_decay;
+} gdn_adamw_tensor;
+
+typedef struct {
+    int32_t state_bits;            /* 8 or 32 */
+    double beta1, beta2;           /* in [0, 1) (1 - beta is formed from the 64 bits) */
+    float lr, eps;                 /* eps >= 0 */
+    int32_t step;                  /* k, from 1 on */
+    uint32_t seed;
+    /* optional device values instead of lr and step, read by the kernel (a
+     * captured call follows them) */
+    const float* lr_ptr;
+    const int32_t* step_ptr;       /* a value below 1 counts as 1 */
+    /* optional device factor of every gradient (clipping, loss scaling); when
+     * it is not finite nothing is written */
+    const float* grad_scale;
+} gdn_adamw;
+
+/* Enqueue the step.  tensors: host memory, read before the call returns.
+ * Addresses need element alignment only.  No two written ranges of the call's
+ * tensors may overlap, nor one and a gradient: within a tensor this is
+ * checked, between tensors it is the caller's contract. */
+gdn_status gdn_adamw_step(const gdn_adamw* adamw, const gdn_adamw_tensor* tensors,
+                          int32_t count, void* stream);
+
 /* Static text for a status code. */
 const char* gdn_status_string(gdn_status status);
 
