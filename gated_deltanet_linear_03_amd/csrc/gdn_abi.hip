@@ -1680,8 +1680,8 @@ gdn_status gdn_adamw_step(const gdn_adamw* a, const gdn_adamw_tensor* tensors, i
     }
     gdn::AdamwParams p{};
     p.lr = a->lr; p.eps = a->eps;
-    p.beta1 = static_cast<float>(a->beta1); p.rest1 = static_cast<float>(1 - a->beta1);
-    p.beta2 = static_cast<float>(a->beta2); p.rest2 = static_cast<float>(1 - a->beta2);
+    p.beta1 = a->beta1; p.rest1 = 1 - a->beta1;
+    p.beta2 = a->beta2; p.rest2 = 1 - a->beta2;
     p.log_beta1 = static_cast<float>(std::log(a->beta1));
     p.log_beta2 = static_cast<float>(std::log(a->beta2));
     p.step = a->step;

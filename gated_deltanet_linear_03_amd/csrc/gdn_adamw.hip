@@ -11,8 +11,15 @@
 // expected value: a step changes v by a thousandth of itself and e4m3 has
 // steps of an eighth to a sixteenth, so rounding to the nearest would leave v
 // where it was for ever.  A positive r is never rounded to zero (the next step
-// would divide by eps alone).  Everything between the loads and the stores is
-// in 32 bits.
+// would divide by eps alone).
+// Everything between the loads and the stores is in 32 bits, but for what
+// decides an 8-bit code: where a value lies between two codes is compared with
+// the random bits, and 32 bits would decide a millionth of the elements
+// otherwise than the formula does, each of them by a whole step.  So the
+// scales come from the largest value in 64 bits, and a block with a value that
+// lies nearer to its border than 32 bits can tell (one or two in a hundred)
+// takes its codes from 64 bits.  (All of them in 64 bits: the vector units
+// bind, 235 M elements take 948 us.)
 //
 // Bound: HBM.  Each element is read and written once: 28 bytes with 32-bit
 // states, a bf16 gradient and a bf16 copy, 16 with 8-bit states.  A wave's 64
@@ -55,37 +62,109 @@ __device__ __forceinline__ uint32_t mix(uint32_t h) {
 // Code of y (|y| <= 448 but for a rounding) in e4m3, up or down by 16 random
 // bits: they are added below the last of the three mantissa bits that stay.
 // Below 2^-6 the format's steps are 2^-9 throughout, which are those of the
-// mantissa of y + 2^-6.
-__device__ __forceinline__ uint32_t e4m3(float y, uint32_t random16) {
-    const uint32_t bits = __float_as_uint(y), sign = bits >> 31 << 7;
+// mantissa of y + 2^-6.  near: y is within kNear of its last bits of the
+// border.  (In those bits m' y is off by up to 5: m' by 1, the scale's
+// reciprocal and the product by up to 2 and 1 at the upper end of a binade, y +
+// 2^-6 by 1/2; r's y by up to 8: its square by 2.5 halves, the root by 2, and
+// the same.)
+constexpr uint32_t kNear = 8;
+__device__ __forceinline__ uint32_t e4m3(float y, uint32_t random16, bool* near) {
     const float a = fabsf(y);
     const bool small = a < 0.015625f;
     const uint32_t t = __float_as_uint(small ? a + 0.015625f : a) + (random16 << 4);
+    *near = ((t + kNear) & 0xFFFFFu) < 2 * kNear;
     // exponent -6 has the codes 8 .. 15
     uint32_t code = (t >> 20) - ((127 - 6) << 3) + (small ? 0 : 8);
     code = code < 0x7E ? code : 0x7E;
-    return sign | (y != y ? 0x7F : code);
+    return __float_as_uint(y) >> 31 << 7 | (y != y ? 0x7F : code);
+}
+// the same in 64 bits, of whose upper word all that counts is part
+__device__ __forceinline__ uint32_t upper_word(double y) {
+    return static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(y)) >> 32);
+}
+__device__ __forceinline__ uint32_t e4m3(double y, uint32_t random16) {
+    const double a = fabs(y);
+    const bool small = a < 0.015625;
+    const uint32_t t = upper_word(small ? a + 0.015625 : a) + (random16 << 1);
+    uint32_t code = (t >> 17) - ((1023 - 6) << 3) + (small ? 0 : 8);
+    code = code < 0x7E ? code : 0x7E;
+    return upper_word(y) >> 31 << 7 | (y != y ? 0x7F : code);
 }
 
-__device__ __forceinline__ float wave_max(float x) {
-    x = fmaxf(x, dpp_f32<0xB1>(x));
-    x = fmaxf(x, dpp_f32<0x4E>(x));
-    x = fmaxf(x, dpp_f32<0x141>(x));
-    x = fmaxf(x, dpp_f32<0x140>(x));
-    x = fmaxf(x, __shfl_xor(x, 16, kWave));
-    return fmaxf(x, __shfl_xor(x, 32, kWave));
+// The largest x >= 0 of a wave, in a scalar register: within rows of 16 lanes,
+// from row to row, to lane 63 (non-negative floats are ordered like their
+// bits; lanes without a neighbour get 0).
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
+    const uint32_t y = __builtin_amdgcn_update_dpp(0, x, CTRL, 0xF, 0xF, true);
+    return x > y ? x : y;
+}
+__device__ __forceinline__ float wave_max(float v) {
+    uint32_t x = __float_as_uint(v);
+    x = max_dpp<0x111>(x);                                  // row_shr 1, 2, 4, 8
+    x = max_dpp<0x112>(x);
+    x = max_dpp<0x114>(x);
+    x = max_dpp<0x118>(x);
+    x = max_dpp<0x142>(x);                                  // row_bcast 15, 31
+    x = max_dpp<0x143>(x);
+    return __uint_as_float(__builtin_amdgcn_readlane(x, 63));
+}
+
+// The largest of the lanes' x / 448 (x >= 0, NaN does not count), rounded once:
+// of those that are the largest in 32 bits the largest in 64.
+__device__ __forceinline__ float block_scale(double x) {
+    const float f = fmaxf(static_cast<float>(x), 0.f), top = wave_max(f);
+    if (!(top < __builtin_inff())) return top;
+    // (next to nothing counts as nothing: the ratios stay finite)
+    if (top < 0x1p-100f) return 0.f;
+    uint64_t who = __ballot(f == top);
+    double most = 0.0;
+    while (who) {                                           // (one round but for ties)
+        const int lane = __builtin_ctzll(who);
+        who &= who - 1;
+        const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(x));
+        const uint64_t b = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits >> 32), lane))) << 32 |
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits), lane));
+        most = fmax(most, __longlong_as_double(static_cast<long long>(b)));
+    }
+    return static_cast<float>(most * (1.0 / 448));
+}
+
+// 1 / s to 2^-45 (0 for 0)
+__device__ __forceinline__ double inverse(float s) {
+    const double x = __builtin_amdgcn_rcpf(s);
+    return s > 0.f ? x * fma(-static_cast<double>(s), x, 2.0) : 0.0;
 }
 
 // what a step's elements have in common
 struct Step {
-    float lr, b1, b2, rest1, rest2, eps, decay, c1, c2;     // c1 = lr / (1 - b1^k), c2 = 1 / sqrt(1 - b2^k)
+    double b1, b2, rest1, rest2;                            // beta and 1 - beta
+    float f_b1, f_b2, f_rest1, f_rest2, low_b1, low_rest1;  // in 32 bits, and what is left
+    float lr, eps, decay, c1, c2;                           // c1 = lr / (1 - b1^k), c2 = 1 / sqrt(1 - b2^k)
     float grad_scale;
     uint32_t key;                                           // of the random bits
 };
 
+// m' and r = sqrt(v') to 2^-45 of themselves (r: one of Newton's steps from the
+// root in 32 bits)
+__device__ __forceinline__ double new_m(const Step& s, float m0, float g) {
+    return fma(s.b1, static_cast<double>(m0), s.rest1 * g);
+}
+__device__ __forceinline__ double new_r(const Step& s, float v0, float g) {
+    const double v1 = fma(s.b2, static_cast<double>(v0), s.rest2 * g * g);
+    const float r = __builtin_amdgcn_sqrtf(static_cast<float>(v1));
+    const double r0 = r;
+    return r > 0.f && r < __builtin_inff() ? fma(fma(-r0, r0, v1), 0.5 * static_cast<double>(__builtin_amdgcn_rcpf(r)), r0) : r0;
+}
+
 template <bool EIGHT, bool GB, bool FULL>
 struct Elements {
     float p[kLane], g[kLane], m[kLane], v[kLane];
+    float m0[EIGHT ? kLane : 1], v0[EIGHT ? kLane : 1];     // 8 bits: what the states stand for; v: r
+    // 8 bits: codes and scales before the step and after it (the scales are the wave's)
+    uint32_t qm, qv, new_qm, new_qv;
+    float sm, sv;
+    uint32_t border;                                        // bits 0 .. 3: m's elements next to their borders, 4 .. 7: r's
     float ms, vs;
 
     // (FULL: all four elements exist)
@@ -104,9 +183,8 @@ struct Elements {
                 for (int e = 0; e < kLane; ++e) g[e] = __uint_as_float(b[e]);
             }
             if constexpr (EIGHT) {
-                const uint32_t qm = __builtin_nontemporal_load(reinterpret_cast<const U1*>(static_cast<const uint8_t*>(t.m) + at));
-                const uint32_t qv = __builtin_nontemporal_load(reinterpret_cast<const U1*>(static_cast<const uint8_t*>(t.v) + at));
-                decode(qm, qv);
+                qm = __builtin_nontemporal_load(reinterpret_cast<const U1*>(static_cast<const uint8_t*>(t.m) + at));
+                qv = __builtin_nontemporal_load(reinterpret_cast<const U1*>(static_cast<const uint8_t*>(t.v) + at));
             } else {
                 const U4 b = __builtin_nontemporal_load(reinterpret_cast<const U4*>(static_cast<const float*>(t.m) + at));
                 const U4 c = __builtin_nontemporal_load(reinterpret_cast<const U4*>(static_cast<const float*>(t.v) + at));
@@ -114,7 +192,7 @@ struct Elements {
                 for (int e = 0; e < kLane; ++e) { m[e] = __uint_as_float(b[e]); v[e] = __uint_as_float(c[e]); }
             }
         } else {
-            uint32_t qm = 0, qv = 0;
+            qm = qv = 0;
 #pragma unroll
             for (int e = 0; e < kLane; ++e) {
                 p[e] = g[e] = m[e] = v[e] = 0.f;
@@ -130,16 +208,15 @@ struct Elements {
                     }
                 }
             }
-            if constexpr (EIGHT) decode(qm, qv);
         }
         if constexpr (EIGHT) {
-            const int64_t block = at / kAdamwBlock;
-            ms = nv > 0 ? t.m_scale[block] : 0.f;
-            vs = nv > 0 ? t.v_scale[block] : 0.f;
+            const int64_t block = __builtin_amdgcn_readfirstlane(static_cast<int>(at / kAdamwBlock));   // (fewer than 2^31: n is below 2^36)
+            ms = t.m_scale[block];
+            vs = t.v_scale[block];
         }
     }
 
-    __device__ __forceinline__ void decode(uint32_t qm, uint32_t qv) {
+    __device__ __forceinline__ void decode() {
         const f32x2 m0 = __builtin_amdgcn_cvt_pk_f32_fp8(qm, false), m1 = __builtin_amdgcn_cvt_pk_f32_fp8(qm, true);
         const f32x2 v0 = __builtin_amdgcn_cvt_pk_f32_fp8(qv, false), v1 = __builtin_amdgcn_cvt_pk_f32_fp8(qv, true);
         m[0] = m0[0]; m[1] = m0[1]; m[2] = m1[0]; m[3] = m1[1];
@@ -148,47 +225,90 @@ struct Elements {
 
     // p, and m and v (8 bits: r in v) after the step
     __device__ __forceinline__ void update(const Step& s) {
+        if constexpr (EIGHT) decode();
 #pragma unroll
         for (int e = 0; e < kLane; ++e) {
-            float m0 = m[e], v0 = v[e];
+            g[e] *= s.grad_scale;
+            float r;
             if constexpr (EIGHT) {
-                m0 *= ms;
-                v0 *= vs;
-                v0 *= v0;
+                m0[e] = m[e] * ms;
+                v0[e] = v[e] * vs;
+                v0[e] *= v0[e];
+                // to its last bit also where its terms cancel: with what the
+                // product and the factors have lost
+                const float gg = s.f_rest1 * g[e], q = fmaf(s.f_b1, m0[e], gg);
+                m[e] = q + fmaf(s.low_b1, m0[e], fmaf(s.low_rest1, g[e], fmaf(s.f_rest1, g[e], -gg)));
+                r = __builtin_amdgcn_sqrtf(fmaf(s.f_b2, v0[e], s.f_rest2 * g[e] * g[e]));
+                v[e] = r;
+            } else {
+                m[e] = fmaf(s.f_b1, m[e], s.f_rest1 * g[e]);
+                v[e] = fmaf(s.f_b2, v[e], s.f_rest2 * g[e] * g[e]);
+                r = __builtin_amdgcn_sqrtf(v[e]);
             }
-            const float grad = g[e] * s.grad_scale;
-            m[e] = fmaf(s.b1, m0, s.rest1 * grad);
-            const float v1 = fmaf(s.b2, v0, s.rest2 * grad * grad);
-            const float r = __builtin_amdgcn_sqrtf(v1);
-            v[e] = EIGHT ? r : v1;
             const float step = m[e] * s.c1 * __builtin_amdgcn_rcpf(fmaf(r, s.c2, s.eps));
             p[e] -= fmaf(s.lr * s.decay, p[e], step);
         }
     }
 
-    // all of a wave's lanes, nv of the elements of each
-    __device__ __forceinline__ void store(const gdn_adamw_tensor& t, const Step& s, int64_t at, int nv, int lane) {
-        uint32_t qm = 0, qv = 0;
-        if constexpr (EIGHT) {
-            float tm = 0.f, tv = 0.f;
+    __device__ __forceinline__ static uint32_t random(const Step& s, int64_t at) {
+        const uint32_t high = mix(static_cast<uint32_t>(static_cast<uint64_t>(at) >> 32));   // (0 for 0)
+        return mix(s.key + high + static_cast<uint32_t>(at) * 0x9E3779B1u);
+    }
+
+    // the codes of the new states, and their scales
+    __device__ __forceinline__ void encode(const Step& s, int64_t at) {
+        // (elements past the end are zeros)
+        float m1 = m0[0], gm = g[0], tm = fabsf(m[0]), v1 = v0[0], gv = g[0], tv = v[0];
 #pragma unroll
-            for (int e = 0; e < kLane; ++e)
-                if (FULL || e < nv) { tm = fmaxf(tm, fabsf(m[e])); tv = fmaxf(tv, v[e]); }
-            tm = wave_max(tm);
-            tv = wave_max(tv);
-            // (next to nothing counts as nothing: 448 / 2^-100 is finite)
-            const float um = tm < 0x1p-100f ? 0.f : 448.f / tm, uv = tv < 0x1p-100f ? 0.f : 448.f / tv;
-            if (lane == 0) {
-                t.m_scale[at / kAdamwBlock] = um > 0.f ? tm * (1.f / 448.f) : 0.f;
-                t.v_scale[at / kAdamwBlock] = uv > 0.f ? tv * (1.f / 448.f) : 0.f;
+        for (int e = 1; e < kLane; ++e) {
+            if (fabsf(m[e]) > tm || tm != tm) { m1 = m0[e]; gm = g[e]; tm = fabsf(m[e]); }
+            if (v[e] > tv || tv != tv) { v1 = v0[e]; gv = g[e]; tv = v[e]; }
+        }
+        sm = uniform_f32(block_scale(fabs(new_m(s, m1, gm))));
+        sv = uniform_f32(block_scale(new_r(s, v1, gv)));
+        const float um = sm > 0.f ? __builtin_amdgcn_rcpf(sm) : 0.f, uv = sv > 0.f ? __builtin_amdgcn_rcpf(sv) : 0.f;
+        new_qm = new_qv = border = 0;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            const uint32_t h = random(s, at + e);
+            bool near_m, near_r;
+            new_qm |= e4m3(m[e] * um, h & 0xFFFFu, &near_m) << (8 * e);
+            const uint32_t r = e4m3(v[e] * uv, h >> 16, &near_r);
+            new_qv |= (r == 0 && v[e] > 0.f && sv > 0.f ? 1u : r) << (8 * e);
+            border |= (near_m ? 1u << e : 0u) | (near_r ? 16u << e : 0u);
+        }
+    }
+
+    // Codes next to a border once more, from 64 bits, over those that store()
+    // has written (a lane's stores to an address stay in order).  One or two
+    // blocks in a hundred have any.
+    __device__ __forceinline__ void settle(const gdn_adamw_tensor& t, const Step& s, int64_t at) {
+        while (border) {
+            const int b = __builtin_ctz(border), e = b % kLane;
+            border &= border - 1;
+            const bool of_m = b < kLane;
+            const float grad = s.grad_scale * (GB ? bf16_bits_to_f32(static_cast<const uint16_t*>(t.grad)[at + e])
+                                                  : static_cast<const float*>(t.grad)[at + e]);
+            const uint32_t h = random(s, at + e);
+            const float old = __builtin_amdgcn_cvt_f32_fp8((of_m ? qm : qv) >> (8 * e), 0) * (of_m ? ms : vs);
+            uint32_t code;
+            if (of_m) {
+                code = e4m3(new_m(s, old, grad) * inverse(sm), h & 0xFFFFu);
+            } else {
+                const double r = new_r(s, old * old, grad);
+                code = e4m3(r * inverse(sv), h >> 16);
+                if (code == 0 && r > 0.0 && sv > 0.f) code = 1;
             }
-            const uint32_t high = mix(static_cast<uint32_t>(static_cast<uint64_t>(at) >> 32));   // (0 for 0)
-#pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-                const uint32_t h = mix(s.key + high + static_cast<uint32_t>(at + e) * 0x9E3779B1u);
-                qm |= e4m3(m[e] * um, h & 0xFFFFu) << (8 * e);
-                const uint32_t r = e4m3(v[e] * uv, h >> 16);
-                qv |= (r == 0 && v[e] > 0.f && uv > 0.f ? 1u : r) << (8 * e);
+            static_cast<uint8_t*>(of_m ? t.m : t.v)[at + e] = static_cast<uint8_t>(code);
+        }
+    }
+
+    // all of a wave's lanes, nv of the elements of each
+    __device__ __forceinline__ void store(const gdn_adamw_tensor& t, int64_t at, int nv, int lane) {
+        if constexpr (EIGHT) {
+            if (lane == 0) {
+                t.m_scale[at / kAdamwBlock] = sm;
+                t.v_scale[at / kAdamwBlock] = sv;
             }
         }
         if constexpr (FULL) {
@@ -201,8 +321,8 @@ struct Elements {
                 __builtin_nontemporal_store(c, reinterpret_cast<U2*>(static_cast<uint16_t*>(t.copy) + at));
             }
             if constexpr (EIGHT) {
-                __builtin_nontemporal_store(qm, reinterpret_cast<U1*>(static_cast<uint8_t*>(t.m) + at));
-                __builtin_nontemporal_store(qv, reinterpret_cast<U1*>(static_cast<uint8_t*>(t.v) + at));
+                __builtin_nontemporal_store(new_qm, reinterpret_cast<U1*>(static_cast<uint8_t*>(t.m) + at));
+                __builtin_nontemporal_store(new_qv, reinterpret_cast<U1*>(static_cast<uint8_t*>(t.v) + at));
             } else {
                 const U4 b = {__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])};
                 const U4 c = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
@@ -216,8 +336,8 @@ struct Elements {
                 t.param[at + e] = p[e];
                 if (t.copy) static_cast<uint16_t*>(t.copy)[at + e] = f32_to_bf16_bits(p[e]);
                 if constexpr (EIGHT) {
-                    static_cast<uint8_t*>(t.m)[at + e] = static_cast<uint8_t>(qm >> (8 * e));
-                    static_cast<uint8_t*>(t.v)[at + e] = static_cast<uint8_t>(qv >> (8 * e));
+                    static_cast<uint8_t*>(t.m)[at + e] = static_cast<uint8_t>(new_qm >> (8 * e));
+                    static_cast<uint8_t*>(t.v)[at + e] = static_cast<uint8_t>(new_qv >> (8 * e));
                 } else {
                     static_cast<float*>(t.m)[at + e] = m[e];
                     static_cast<float*>(t.v)[at + e] = v[e];
@@ -239,7 +359,12 @@ __device__ __forceinline__ void chunk(const gdn_adamw_tensor& t, const Step& s, 
 #pragma unroll
         for (int i = 0; i < kRounds; ++i) {
             x[i].update(s);
-            x[i].store(t, s, at0 + i * kAdamwBlock, kLane, lane);
+            if constexpr (EIGHT) x[i].encode(s, at0 + i * kAdamwBlock);
+            x[i].store(t, at0 + i * kAdamwBlock, kLane, lane);
+        }
+        if constexpr (EIGHT) {
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) x[i].settle(t, s, at0 + i * kAdamwBlock);
         }
         return;
     }
@@ -250,12 +375,17 @@ __device__ __forceinline__ void chunk(const gdn_adamw_tensor& t, const Step& s, 
         Elements<EIGHT, GB, false> x;
         x.load(t, at, nv);
         x.update(s);
-        x.store(t, s, at, nv, lane);
+        if constexpr (EIGHT) x.encode(s, at);
+        x.store(t, at, nv, lane);
+        if constexpr (EIGHT) {
+            x.border &= ((1u << nv) - 1) * 0x11u;           // (none of elements past the end)
+            x.settle(t, s, at);
+        }
     }
 }
 
 template <bool EIGHT>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(Launch a) {
+__global__ __launch_bounds__(kThreads, 5) void adamw_kernel(Launch a) {
     const AdamwParams& p = a.p;
     // the gradients' factor decides whether there is a step at all
     const float gs = p.grad_scale ? *p.grad_scale : 1.f;
@@ -273,6 +403,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Launch a) {
     s.b2 = p.beta2;
     s.rest1 = p.rest1;
     s.rest2 = p.rest2;
+    s.f_b1 = static_cast<float>(p.beta1);
+    s.f_b2 = static_cast<float>(p.beta2);
+    s.f_rest1 = static_cast<float>(p.rest1);
+    s.f_rest2 = static_cast<float>(p.rest2);
+    s.low_b1 = static_cast<float>(p.beta1 - s.f_b1);
+    s.low_rest1 = static_cast<float>(p.rest1 - s.f_rest1);
     s.eps = p.eps;
     s.decay = t.weight_decay;
     s.grad_scale = gs;

@@ -315,8 +315,8 @@ constexpr int kAdamwTensors = 32;        // tensors of a launch (its arguments h
 constexpr int64_t kAdamwMostChunks = (int64_t(1) << 24) - 1;   // work-groups of a launch: fewer than 2^32 work-items
 
 struct AdamwParams {
+    double beta1, beta2, rest1, rest2;   // beta and 1 - beta
     float lr, eps;
-    float beta1, beta2, rest1, rest2;    // beta and 1 - beta
     float log_beta1, log_beta2;
     int32_t step;
     uint32_t seed;
