@@ -55,7 +55,8 @@ EXPORTS = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill",
            "gdn_recur_backward_workspace_bytes", "gdn_recur_backward", "gdn_recur_decode",
            "gdn_linear", "gdn_linear_workspace_bytes", "gdn_linear_backward_workspace_bytes", "gdn_linear_backward",
            "gdn_linear_tiles", "gdn_norm", "gdn_norm_backward_workspace_bytes", "gdn_norm_backward",
-           "gdn_adamw_step")
+           "gdn_adamw_step", "gdn_linear_cross_entropy_workspace_bytes", "gdn_linear_cross_entropy",
+           "gdn_linear_cross_entropy_backward_workspace_bytes", "gdn_linear_cross_entropy_backward")
 NOALLOC_SCRATCH_BYTES = 128 << 20       # GDN_NOALLOC_SCRATCH_BYTES
 SNAPSHOT_MAGIC = 0x50534E47
 SNAPSHOT_VERSION = 1
@@ -204,6 +205,21 @@ class CNormGrad(ctypes.Structure):
                 ("dbias", ctypes.c_void_p)]
 
 
+class CLossIO(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("V", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("w_stride", ctypes.c_int64), ("bias", ctypes.c_void_p), ("targets", ctypes.c_void_p),
+                ("target_bytes", ctypes.c_int32), ("ignore_index", ctypes.c_int64),
+                ("label_smoothing", ctypes.c_float), ("z_loss", ctypes.c_float), ("loss", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class CLossGrad(ctypes.Structure):
+    _fields_ = [("dloss", ctypes.c_void_p), ("dloss_one", ctypes.c_int32), ("dx", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64), ("dw", ctypes.c_void_p), ("dw_stride", ctypes.c_int64),
+                ("dbias", ctypes.c_void_p)]
+
+
 class CAdamWTensor(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
                 ("grad_dtype", ctypes.c_int32), ("copy", ctypes.c_void_p), ("m", ctypes.c_void_p),
@@ -337,6 +353,17 @@ def lib():
         L.gdn_norm_backward.restype = ctypes.c_int
         L.gdn_norm_backward.argtypes = [ctypes.POINTER(CNormGrad), ctypes.c_void_p, ctypes.c_size_t,
                                         ctypes.c_void_p]
+        for name in ("gdn_linear_cross_entropy_workspace_bytes",
+                     "gdn_linear_cross_entropy_backward_workspace_bytes"):
+            f = getattr(L, name)
+            f.restype = ctypes.c_size_t
+            f.argtypes = [ctypes.c_int64] * 3
+        L.gdn_linear_cross_entropy.restype = ctypes.c_int
+        L.gdn_linear_cross_entropy.argtypes = [ctypes.POINTER(CLossIO), ctypes.c_void_p, ctypes.c_size_t,
+                                               ctypes.c_void_p]
+        L.gdn_linear_cross_entropy_backward.restype = ctypes.c_int
+        L.gdn_linear_cross_entropy_backward.argtypes = [ctypes.POINTER(CLossIO), ctypes.POINTER(CLossGrad),
+                                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
         L.gdn_adamw_step.restype = ctypes.c_int
         L.gdn_adamw_step.argtypes = [ctypes.POINTER(CAdamW), ctypes.POINTER(CAdamWTensor), ctypes.c_int32,
                                      ctypes.c_void_p]
@@ -1360,6 +1387,95 @@ def norm_backward(dy, x, weight, stats, kind=GDN_NORM_LAYER, d_residual=None, wa
                    _dense(res.get("dbias"), "dbias", D, None, dev))
     ws, nb = _bytes(workspace, "workspace", dev)
     _check(lib().gdn_norm_backward(ctypes.byref(gr), ws, nb, _raw_stream(stream, dev)))
+    return res
+
+
+# ---- the cross entropy of a linear layer's outputs --------------------------------
+
+def _loss_size(name, M, V, K):
+    n = getattr(lib(), name)(int(M), int(V), int(K))
+    if n == 0:
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, lib().gdn_last_error().decode())
+    return int(n)
+
+
+def linear_cross_entropy_workspace_bytes(M: int, V: int, K: int) -> int:
+    """Bytes of workspace of ``gdn_linear_cross_entropy``."""
+    return _loss_size("gdn_linear_cross_entropy_workspace_bytes", M, V, K)
+
+
+def linear_cross_entropy_backward_workspace_bytes(M: int, V: int, K: int) -> int:
+    """Bytes of workspace of ``gdn_linear_cross_entropy_backward``."""
+    return _loss_size("gdn_linear_cross_entropy_backward_workspace_bytes", M, V, K)
+
+
+def _loss_io(x, w, targets, bias, label_smoothing, z_loss, ignore_index, loss, lse, status, dev):
+    import torch
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"x and w: matrices needed, shapes are {tuple(x.shape)} and {tuple(w.shape)}")
+    M, K = x.shape
+    V = w.shape[0]
+    px, sx = _matrix(x, "x", M, K, torch.bfloat16, dev)
+    pw, sw = _matrix(w, "w", V, K, torch.bfloat16, dev)
+    pt = _flat(targets, "targets", M, (torch.int64, torch.int32), dev)
+    return CLossIO(M, V, K, px, sx, pw, sw, _dense(bias, "bias", V, None, dev), pt, targets.element_size(),
+                   int(ignore_index), label_smoothing, z_loss, loss, lse, _index(status, "status", 1, dev))
+
+
+def linear_cross_entropy(x, w, targets, bias=None, label_smoothing=0.0, z_loss=0.0, ignore_index=-100,
+                         workspace=None, stream=None, status=None):
+    """Softmax cross entropy of the logits x w^T + bias, without keeping them:
+    x [M, K], w [V, K] bf16 (rows may be strided, in multiples of 8 elements),
+    bias [V] fp32, targets [M] int64 or int32.  A dict with loss [M] (0 where
+    the target is ignore_index) and lse [M], the logarithm of the sum of the
+    logits' exponentials, both fp32.  label_smoothing: the share of the target
+    distribution that is spread over the vocabulary; z_loss: the weight of
+    lse^2.  status: optional int32 device word; GDN_STATUS_BAD_INDEX is ORed in
+    when another target is not in [0, V) (its loss is NaN)."""
+    import torch
+    dev = _device()
+    M = x.shape[0]
+    res = {"loss": _new(x, (M,), torch.float32, stream), "lse": _new(x, (M,), torch.float32, stream)}
+    io = _loss_io(x, w, targets, bias, label_smoothing, z_loss, ignore_index, res["loss"].data_ptr(),
+                  res["lse"].data_ptr(), status, dev)
+    if workspace is None:
+        workspace = _new(x, (linear_cross_entropy_workspace_bytes(io.M, io.V, io.K),), torch.uint8, stream)
+    ws, nb = _bytes(workspace, "workspace", dev)
+    _check(lib().gdn_linear_cross_entropy(ctypes.byref(io), ws, nb, _raw_stream(stream, dev)))
+    return res
+
+
+def linear_cross_entropy_backward(dloss, x, w, targets, lse, bias=None, label_smoothing=0.0, z_loss=0.0,
+                                  ignore_index=-100, want_dx=True, want_dw=True, want_dbias=None, dx=None,
+                                  dw=None, dbias=None, workspace=None, stream=None):
+    """Gradients of linear_cross_entropy() from dloss, fp32 [M] or of one
+    element for all rows (for a mean: 1 / the rows that count): a dict with dx
+    [M, K] and dw [V, K] (bf16) and dbias [V] (fp32; by default with a bias).
+    lse: as the forward call gave it, the other arguments as it was given
+    them.  dx, dw, dbias: tensors to write instead of new ones."""
+    import torch
+    dev = _device()
+    M, K = x.shape
+    V = w.shape[0]
+    io = _loss_io(x, w, targets, bias, label_smoothing, z_loss, ignore_index, None,
+                  _flat(lse, "lse", M, (torch.float32,), dev), None, dev)
+    one = dloss.numel() == 1
+    pg = _flat(dloss, "dloss", 1 if one else M, (torch.float32,), dev)
+    res = {}
+    if want_dx or dx is not None:
+        res["dx"] = dx if dx is not None else _new(x, (M, K), torch.bfloat16, stream)
+    if want_dw or dw is not None:
+        res["dw"] = dw if dw is not None else _new(x, (V, K), torch.bfloat16, stream)
+    if (bias is not None if want_dbias is None else want_dbias) or dbias is not None:
+        res["dbias"] = dbias if dbias is not None else _new(x, (V,), torch.float32, stream)
+    pdx, sdx = _matrix(res["dx"], "dx", M, K, torch.bfloat16, dev) if "dx" in res else (None, 0)
+    pdw, sdw = _matrix(res["dw"], "dw", V, K, torch.bfloat16, dev) if "dw" in res else (None, 0)
+    if workspace is None:
+        workspace = _new(x, (linear_cross_entropy_backward_workspace_bytes(M, V, K),), torch.uint8, stream)
+    gr = CLossGrad(pg, one, pdx, sdx, pdw, sdw, _dense(res.get("dbias"), "dbias", V, None, dev))
+    ws, nb = _bytes(workspace, "workspace", dev)
+    _check(lib().gdn_linear_cross_entropy_backward(ctypes.byref(io), ctypes.byref(gr), ws, nb,
+                                                   _raw_stream(stream, dev)))
     return res
 
 

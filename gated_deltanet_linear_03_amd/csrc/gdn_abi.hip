@@ -1635,6 +1635,137 @@ gdn_status gdn_norm_backward(const gdn_norm_grad* gr, void* ws, size_t ws_bytes,
     return GDN_OK;
 }
 
+// ---- the cross entropy of a linear layer's outputs ----------------------------------
+
+namespace {
+
+gdn_status check_loss(int64_t M, int64_t V, int64_t K, bool backward) {
+    gdn_status st = check_dims(M, V, K);
+    if (st != GDN_OK) return st;
+    if (V < 1 || K < 8) return fail(GDN_ERR_INVALID_ARGUMENT, "V (%lld) must be at least 1, K (%lld) at least 8", static_cast<long long>(V),
+                                    static_cast<long long>(K));
+    if (M > (int64_t(1) << 25) || M * K > (int64_t(1) << 33) || tiles_of_64(M, V) >= kMaxTiles || (V + 255) / 256 >= kMaxTiles / 2 ||
+        (backward && tiles_of_64(M, K) + tiles_of_64(V, K) >= kMaxTiles))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "sizes too large (%lld, %lld, %lld)", static_cast<long long>(M), static_cast<long long>(V),
+                    static_cast<long long>(K));
+    return GDN_OK;
+}
+
+// what both passes read, into c and the spans (x, w, bias, targets)
+gdn_status loss_call(const gdn_loss_io* io, gdn::LossCall* c, Span* in) {
+    const int64_t M = io->M, V = io->V, K = io->K;
+    gdn_status st;
+    if (io->target_bytes != 4 && io->target_bytes != 8)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "target_bytes must be 4 or 8, not %d", io->target_bytes);
+    if (!(io->label_smoothing >= 0.f && io->label_smoothing < 1.f))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "label_smoothing must be in [0, 1)");
+    if (!(io->z_loss >= 0.f) || std::isinf(io->z_loss)) return fail(GDN_ERR_INVALID_ARGUMENT, "z_loss must be >= 0 and finite");
+    c->M = M; c->V = V; c->K = K;
+    c->x = io->x; c->w = io->w;
+    c->ldx = row_stride(io->x_stride, K, M);
+    c->ldw = row_stride(io->w_stride, K, V);
+    c->bias = io->bias;
+    c->rows.V = V;
+    c->rows.targets = io->targets;
+    c->rows.targets64 = io->target_bytes == 8;
+    c->rows.ignore = io->ignore_index;
+    c->rows.smooth = io->label_smoothing;
+    c->rows.z = io->z_loss;
+    c->rows.status = io->status;
+    if (M > 0) {
+        if ((st = check_operand("x", io->x, c->ldx, K)) != GDN_OK || (st = check_operand("w", io->w, c->ldw, K)) != GDN_OK) return st;
+        if (!io->targets) return fail(GDN_ERR_INVALID_ARGUMENT, "targets is NULL");
+        if (!aligned(io->targets, io->target_bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "targets is not element aligned");
+    }
+    if ((st = check_floats("bias", io->bias)) != GDN_OK || (st = check_floats("loss", io->loss)) != GDN_OK ||
+        (st = check_floats("lse", io->lse)) != GDN_OK || (st = check_floats("status", io->status)) != GDN_OK)
+        return st;
+    in[0] = {io->x, row_bytes(M, c->ldx, K, 2)};
+    in[1] = {io->w, row_bytes(V, c->ldw, K, 2)};
+    in[2] = {io->bias, static_cast<size_t>(V) * 4};
+    in[3] = {io->targets, static_cast<size_t>(M) * io->target_bytes};
+    return GDN_OK;
+}
+
+gdn_status check_workspace(const void* ws, size_t bytes, size_t need) {
+    if (!ws) return fail(GDN_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+    if (!aligned(ws, 256)) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (bytes < need) return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, need %zu", bytes, need);
+    return GDN_OK;
+}
+
+}  // namespace
+
+size_t gdn_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    g_err[0] = 0;
+    if (check_loss(M, V, K, false) != GDN_OK) return 0;
+    return M > 0 ? static_cast<size_t>(gdn::loss_workspace(M, V, K)) : 256;
+}
+
+gdn_status gdn_linear_cross_entropy(const gdn_loss_io* io, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = 0;
+    if (!io) return fail(GDN_ERR_INVALID_ARGUMENT, "io is NULL");
+    gdn_status st = check_loss(io->M, io->V, io->K, false);
+    if (st != GDN_OK) return st;
+    gdn::LossCall c{};
+    Span in[4];
+    if ((st = loss_call(io, &c, in)) != GDN_OK) return st;
+    c.loss = io->loss;
+    c.lse = io->lse;
+    if (io->M == 0 || (!io->loss && !io->lse)) return GDN_OK;
+    const size_t need = gdn_linear_cross_entropy_workspace_bytes(io->M, io->V, io->K), rows = static_cast<size_t>(io->M) * 4;
+    if ((st = check_workspace(ws, ws_bytes, need)) != GDN_OK) return st;
+    const Span out[4] = {{io->loss, rows}, {io->lse, rows}, {io->status, 4}, {ws, need}};
+    for (int i = 0; i < 4; ++i)
+        if (any_overlap(out[i], in, 4) || any_overlap(out[i], out, i))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input or another output");
+    hipError_t e = gdn::launch_loss(c, ws, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "cross entropy launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
+size_t gdn_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    g_err[0] = 0;
+    if (check_loss(M, V, K, true) != GDN_OK) return 0;
+    return M > 0 ? static_cast<size_t>(gdn::loss_backward_workspace(M, V, K)) : 256;
+}
+
+gdn_status gdn_linear_cross_entropy_backward(const gdn_loss_io* io, const gdn_loss_grad* gr, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = 0;
+    if (!io || !gr) return fail(GDN_ERR_INVALID_ARGUMENT, "io or grad is NULL");
+    const int64_t M = io->M, V = io->V, K = io->K;
+    gdn_status st = check_loss(M, V, K, true);
+    if (st != GDN_OK) return st;
+    gdn::LossCall c{};
+    Span in[6];
+    if ((st = loss_call(io, &c, in)) != GDN_OK) return st;
+    c.rows.lse = io->lse;
+    c.rows.dloss = gr->dloss;
+    c.rows.dloss_one = gr->dloss_one != 0;
+    c.rows.status = nullptr;
+    c.dx = M > 0 ? gr->dx : nullptr;
+    c.dw = gr->dw;
+    c.dbias = gr->dbias;
+    c.lddx = row_stride(gr->dx_stride, K, M);
+    c.lddw = row_stride(gr->dw_stride, K, V);
+    if (!c.dx && !c.dw && !c.dbias) return GDN_OK;
+    if (M > 0 && (!io->lse || !gr->dloss)) return fail(GDN_ERR_INVALID_ARGUMENT, "lse or dloss is NULL");
+    if ((st = check_floats("dloss", gr->dloss)) != GDN_OK || (st = check_floats("dbias", gr->dbias)) != GDN_OK) return st;
+    if (c.dx && (st = check_rows("dx", c.dx, c.lddx, K, 2)) != GDN_OK) return st;
+    if (c.dw && (st = check_rows("dw", c.dw, c.lddw, K, 2)) != GDN_OK) return st;
+    const size_t need = gdn_linear_cross_entropy_backward_workspace_bytes(M, V, K);
+    if ((st = check_workspace(ws, ws_bytes, need)) != GDN_OK) return st;
+    in[4] = {io->lse, static_cast<size_t>(M) * 4};
+    in[5] = {gr->dloss, c.rows.dloss_one ? 4 : static_cast<size_t>(M) * 4};
+    const Span out[4] = {{c.dx, row_bytes(M, c.lddx, K, 2)}, {c.dw, row_bytes(V, c.lddw, K, 2)}, {c.dbias, static_cast<size_t>(V) * 4}, {ws, need}};
+    for (int i = 0; i < 4; ++i)
+        if (any_overlap(out[i], in, 6) || any_overlap(out[i], out, i))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input or another output");
+    hipError_t e = gdn::launch_loss_backward(c, ws, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(GDN_ERR_HIP, "cross entropy backward launch failed: %s", hipGetErrorString(e));
+    return GDN_OK;
+}
+
 // ---- the update of the weights ------------------------------------------------------
 
 static_assert(GDN_ADAMW_BLOCK == gdn::kAdamwBlock, "block of the 8-bit states");

@@ -329,4 +329,37 @@ struct AdamwParams {
 int64_t adamw_chunks(int64_t n);
 hipError_t launch_adamw(const AdamwParams& p, const gdn_adamw_tensor* tensors, int count, bool eight, hipStream_t s);
 
+// ---- the cross entropy of a linear layer's outputs (gdn_loss.hip) --------------
+// what belongs to a row
+struct LossRows {
+    int64_t V;
+    const void* targets;                 // int32, or int64 where targets64
+    int targets64;
+    int64_t ignore;
+    float smooth, z;
+    int32_t* status;
+    // backward
+    const float *lse, *dloss;
+    int dloss_one;                       // one value for all rows
+};
+
+struct LossCall {
+    int64_t M, V, K;
+    const void *x, *w;
+    int64_t ldx, ldw;
+    const float* bias;
+    LossRows rows;
+    float *loss, *lse;
+    // backward; each may be NULL
+    void *dx, *dw;
+    int64_t lddx, lddw;
+    float* dbias;
+};
+
+// bytes (M, V, K > 0)
+int64_t loss_workspace(int64_t M, int64_t V, int64_t K);
+int64_t loss_backward_workspace(int64_t M, int64_t V, int64_t K);
+hipError_t launch_loss(const LossCall& c, void* ws, hipStream_t s);
+hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s);
+
 }  // namespace gdn

@@ -316,9 +316,6 @@ __global__ __launch_bounds__(1024) void linear_sum_kernel(ColumnSums c) {
 }
 
 template <typename S>
-int64_t tiles(const GemmProduct& p) { return ((p.M + S::BM - 1) / S::BM) * ((p.N + S::BN - 1) / S::BN); }
-
-template <typename S>
 hipError_t forward_t(const GemmProduct& p, hipStream_t s) {
     hipLaunchKernelGGL((linear_forward_kernel<S>), dim3(static_cast<unsigned>(tiles<S>(p))), dim3(S::kThreads), 0, s, p);
     return hipGetLastError();
@@ -333,38 +330,6 @@ hipError_t backward_t(const GemmProduct& dx, const GemmProduct& dw, const Column
 }
 
 }  // namespace
-
-// Which tiles: the time of one tile on a compute unit at K = 2048, in us, times
-// the rounds of tiles over the compute units; tiles that share one take longer
-// where they have it to themselves.  Measured, in the order 256 x
-// 256, 256 x 128, 128 x 128, 64 x 64:
-//   4096 x 12288 x 2048: 148, 173, 231, 341 us
-//   4096 x  2048 x 4096:  73,  55,  75, 125 us
-//   2048 x  2048 x 2048:  41,  27,  24,  34 us
-//   1024 x  2048 x 2048:  40,  26,  23,  18 us
-//   1024 x 12352 x 2048:  45,  54,  70,  93 us
-constexpr double kLargeUs = 46.0, kWideUs = 27.0, kMediumUs = 18.0, kSmallUs = 8.5;
-constexpr double kMediumAlone = 24.0, kSmallAlone = 11.0;
-enum Tiles { kLarge, kWide, kMedium, kSmall };
-
-struct Choice {
-    Tiles tiles;
-    double us;
-};
-
-static Choice choose(const GemmProduct& p, int cus) {
-    auto us = [&](int64_t n, double each, double alone) {
-        const double t = static_cast<double>((n + cus - 1) / cus) * each;
-        return t > alone ? t : alone;
-    };
-    const Choice all[4] = {{kLarge, us(tiles<Large>(p), kLargeUs, kLargeUs)}, {kWide, us(tiles<Wide>(p), kWideUs, kWideUs)},
-                           {kMedium, us(tiles<Medium>(p), kMediumUs, kMediumAlone)},
-                           {kSmall, us(tiles<Small>(p), kSmallUs, kSmallAlone)}};
-    Choice best = all[0];
-    for (int i = 1; i < 4; ++i)
-        if (all[i].us < best.us) best = all[i];
-    return best;
-}
 
 static hipError_t forward(const GemmProduct& p, Tiles t, hipStream_t s) {
     switch (t) {

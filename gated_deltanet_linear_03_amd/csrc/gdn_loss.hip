@@ -1,0 +1,635 @@
+// gdn_loss.hip -- the softmax cross entropy of a linear layer's outputs over a
+// vocabulary, and its gradients, without keeping the logits.
+//
+// With l = x w^T + bias, lse = log sum_v exp(l_v), e the label smoothing and c
+// the weight of the squared normaliser, per row with target t:
+//   loss = (1 - e) (lse - l_t) + e (lse - mean_v l_v) + c lse^2
+//   dl_v = g ((1 + 2 c lse) exp(l_v - lse) - (1 - e) [v = t] - e / V)
+//   dx = dl w,  dw = dl^T x,  dbias = sum over the rows of dl
+//
+// Forward: the tiles of the product x w^T leave, for each of their rows, the
+// largest of their logits and the sum of the exponentials of the others' (all)
+// distances to it; a second kernel joins a row's tiles.  Nothing of the size
+// rows x vocabulary is written.  Up to 16 rows it is a stream over w, bound by
+// HBM.
+// Backward: for a piece of the vocabulary at a time the tiles of the product
+// are computed once more and leave dl in bf16, the operand type of the two
+// products that follow: dx, in 32 bits from piece to piece, and the piece's
+// rows of dw.  (dl is rounded to bf16 once, as dp is in the linear layer's
+// backward pass; dbias sums it in 32 bits before that.)
+// Statistics are in base two: 2^(l log2 e - top), one multiply-add and one
+// v_exp_f32 a logit.
+#include "gdn_tiles.hpp"
+
+namespace gdn {
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int64_t target_of(const LossRows& r, int64_t m) {
+    return r.targets64 ? static_cast<const int64_t*>(r.targets)[m] : static_cast<const int32_t*>(r.targets)[m];
+}
+
+// over the four lanes that share a row of a tile's 16 x 16 accumulators
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16, kWave));
+    return fmaxf(x, __shfl_xor(x, 32, kWave));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor(x, 16, kWave);
+    return x + __shfl_xor(x, 32, kWave);
+}
+
+// A set of logits: the largest times log2 e, and the sum of 2^(l log2 e - top).
+// None: top = -inf, sum = 0.
+struct Part {
+    float top, sum;
+};
+__device__ __forceinline__ Part join(Part a, Part b) {
+    const float top = fmaxf(a.top, b.top);
+    // (an empty part's -inf less -inf counts as nothing; NaN stays NaN through the sums)
+    const float ea = a.top == top ? 1.f : __builtin_amdgcn_exp2f(a.top - top);
+    const float eb = b.top == top ? 1.f : __builtin_amdgcn_exp2f(b.top - top);
+    return Part{top, fmaf(a.sum, ea, b.sum * eb)};
+}
+
+// the piece of the product that a launch covers
+struct LossProduct : GemmProduct {
+    LossRows rows;
+    int64_t v0;                               // the vocabulary's index of column 0
+    const float* bias;                        // of column 0, or NULL
+    // forward
+    Part* part;                               // [column tiles][M]
+    float* totals;                            // [column tiles][M] sums of the logits, or NULL
+    float* logit;                             // [M] the target's
+    // backward
+    GemmProduct out;                          // dl: rows, columns (padded with zeros), address and stride
+    float* columns;                           // [row tiles][V] sums of dl, or NULL
+    int64_t columns_ld;
+};
+
+// row of a wave's accumulators acc[i][.] in lane l16
+template <typename S>
+__device__ __forceinline__ int64_t row_of(int64_t m0, int wave, int i, int l16) {
+    return m0 + wave / S::NWN * S::kWaveStep + i / S::kStripTiles * S::kHalfStep + 16 * (i % S::kStripTiles) + l16;
+}
+
+// acc += bias, and -inf for columns past the vocabulary (they hold the last column's product again)
+template <typename S>
+__device__ __forceinline__ void finish_logits(const LossProduct& p, f32x4 (&acc)[S::TM][S::TN], int64_t n0, int wave, int lane) {
+    const bool cut = n0 + S::BN > p.N;
+    if (!p.bias && !cut) return;
+    const int64_t first = n0 + wave % S::NWN * S::WN + 4 * (lane / 16);
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t n = first + 16 * j + e;
+            const float b = p.bias && n < p.N ? p.bias[n] : 0.f;
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i) acc[i][j][e] = n < p.N ? acc[i][j][e] + b : -__builtin_inff();
+        }
+}
+
+// ---- forward -------------------------------------------------------------------
+// A tile's rows to their parts: each lane its 4 TN logits of a row, the four
+// lanes that share the row, then the waves that do, through LDS.
+template <typename S>
+struct RowParts {
+    int64_t m0, n0;
+    __device__ __forceinline__ void init(const LossProduct&, int64_t m, int64_t n, int, int) { m0 = m; n0 = n; }
+    __device__ __forceinline__ void fetch(const LossProduct&, int) {}
+    __device__ __forceinline__ void run(const LossProduct& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
+        Part* const red = reinterpret_cast<Part*>(shared);                         // [NWN][BM]
+        float* const tot = reinterpret_cast<float*>(shared + S::NWN * S::BM * sizeof(Part));
+        const int l16 = lane % 16, lq = lane / 16, wn = wave % S::NWN;
+        const int64_t first = n0 + wn * S::WN + 4 * lq;
+        finish_logits<S>(p, acc, n0, wave, lane);
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            const int64_t m = row_of<S>(m0, wave, i, l16);
+            float top = acc[i][0][0];
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, acc[i][j][e]);
+            top = quad_max(top) * kLog2e;
+            const float base = top == -__builtin_inff() ? 0.f : top;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLog2e, -base));
+            sum = quad_sum(sum);
+            const int r = static_cast<int>(m - m0);
+            if (lq == 0) red[wn * S::BM + r] = Part{top, sum};
+            if (p.totals) {
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s += first + 16 * j + e < p.N ? acc[i][j][e] : 0.f;
+                s = quad_sum(s);
+                if (lq == 0) tot[wn * S::BM + r] = s;
+            }
+            // the target's logit, where this lane has it
+            const int64_t t = m < p.M ? target_of(p.rows, m) - p.v0 - first : -1;
+            if (t >= 0 && t < S::WN) {
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (t == 16 * j + e && first + t < p.N) p.logit[m] = acc[i][j][e];
+            }
+        }
+        __syncthreads();
+        for (int r = threadIdx.x; r < S::BM; r += S::kThreads) {
+            if (m0 + r >= p.M) continue;
+            Part a = red[r];
+#pragma unroll
+            for (int w = 1; w < S::NWN; ++w) a = join(a, red[w * S::BM + r]);
+            const int64_t at = n0 / S::BN * p.M + m0 + r;
+            p.part[at] = a;
+            if (p.totals) {
+                float s = tot[r];
+#pragma unroll
+                for (int w = 1; w < S::NWN; ++w) s += tot[w * S::BM + r];
+                p.totals[at] = s;
+            }
+        }
+    }
+};
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_forward_kernel(LossProduct p) {
+    __shared__ __align__(1024) uint8_t shared[S::kBytes];
+    gemm_tile<true, true, RowParts<S>, S>(p, blockIdx.x, shared);
+}
+
+// Up to 16 rows: a wave takes 16 columns at a time, over the whole of K, and
+// keeps its rows' parts from one to the next.  Per 64-wide step of K the lanes
+// of a row read two runs of 64 bytes of their weight row and of their row of x,
+// DEPTH steps ahead.
+constexpr int kFewWaves = 4, kFewDepth = 4;
+
+__global__ __launch_bounds__(kFewWaves * kWave, 4) void loss_few_kernel(LossProduct p) {
+    __shared__ Part red[kFewWaves][16];
+    __shared__ float tot[kFewWaves][16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const int l16 = lane % 16, lq = lane / 16;
+    const int64_t groups = (p.N + 15) / 16, all = static_cast<int64_t>(gridDim.x) * kFewWaves;
+    const int64_t m = l16 < p.M ? l16 : p.M - 1;                                   // (rows past the end are never stored)
+    const uint16_t* const arow = static_cast<const uint16_t*>(p.A) + m * p.lda;
+    const int64_t target = target_of(p.rows, m);
+    const int steps = static_cast<int>((p.K + 63) / 64);
+    Part mine{-__builtin_inff(), 0.f};
+    float total = 0.f;
+    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kFewWaves + wave; g < groups; g += all) {
+        const int64_t n0 = 16 * g;
+        const uint16_t* const brow = static_cast<const uint16_t*>(p.B) + (n0 + l16 < p.N ? n0 + l16 : p.N - 1) * p.ldb;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        u32x4 bf[kFewDepth][2], af[kFewDepth][2];
+        auto load = [&](int st, int slot) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t k = 64 * static_cast<int64_t>(st) + 32 * h + 8 * lq;
+                bf[slot][h] = *reinterpret_cast<const u32x4*>(k < p.K ? brow + k : zero_chunk);
+                af[slot][h] = *reinterpret_cast<const u32x4*>(k < p.K ? arow + k : zero_chunk);
+            }
+        };
+#pragma unroll
+        for (int d = 0; d < kFewDepth; ++d) load(d, d);
+        for (int st = 0; st < steps; st += kFewDepth) {
+#pragma unroll
+            for (int d = 0; d < kFewDepth; ++d) {
+                acc = mfma(bf[d][0], af[d][0], acc);
+                acc = mfma(bf[d][1], af[d][1], acc);
+                if (st + kFewDepth < steps) load(st + kFewDepth + d, d);
+            }
+        }
+        // this lane: row l16, columns n0 + 4 lq ..
+        Part a{-__builtin_inff(), 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t n = n0 + 4 * lq + e;
+            if (n >= p.N) { acc[e] = -__builtin_inff(); continue; }
+            if (p.bias) acc[e] += p.bias[n];
+            total += acc[e];
+            if (n + p.v0 == target && l16 < p.M) p.logit[l16] = acc[e];
+        }
+        a.top = fmaxf(fmaxf(acc[0], acc[1]), fmaxf(acc[2], acc[3])) * kLog2e;
+        const float base = a.top == -__builtin_inff() ? 0.f : a.top;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a.sum += __builtin_amdgcn_exp2f(fmaf(acc[e], kLog2e, -base));
+        mine = join(mine, a);
+    }
+#pragma unroll
+    for (int x = 16; x < kWave; x *= 2) {
+        const Part o{__shfl_xor(mine.top, x, kWave), __shfl_xor(mine.sum, x, kWave)};
+        mine = join(mine, o);
+        total += __shfl_xor(total, x, kWave);
+    }
+    if (lane < 16) {
+        red[wave][lane] = mine;
+        tot[wave][lane] = total;
+    }
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r >= p.M) return;
+    Part a = red[0][r];
+    float s = tot[0][r];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) {
+        a = join(a, red[w][r]);
+        s += tot[w][r];
+    }
+    p.part[blockIdx.x * p.M + r] = a;
+    if (p.totals) p.totals[blockIdx.x * p.M + r] = s;
+}
+
+// A row's parts to its lse and loss: 16 rows a work-group, 64 threads each,
+// whose parts are joined in their order.
+constexpr int kJoinRows = 16, kJoinSlices = 64;
+
+__global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(LossProduct p, int64_t tiles, float* loss, float* lse) {
+    __shared__ Part red[kJoinSlices][kJoinRows];
+    __shared__ float tot[kJoinSlices][kJoinRows];
+    const int r = threadIdx.x % kJoinRows, sl = threadIdx.x / kJoinRows;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
+    Part a{-__builtin_inff(), 0.f};
+    float total = 0.f;
+    if (m < p.M) {
+#pragma unroll 4
+        for (int64_t t = sl; t < tiles; t += kJoinSlices) a = join(a, p.part[t * p.M + m]);
+        if (p.totals) {
+#pragma unroll 4
+            for (int64_t t = sl; t < tiles; t += kJoinSlices) total += p.totals[t * p.M + m];
+        }
+    }
+    red[sl][r] = a;
+    tot[sl][r] = total;
+    for (int half = kJoinSlices / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (sl < half) {
+            red[sl][r] = join(red[sl][r], red[sl + half][r]);
+            tot[sl][r] += tot[sl + half][r];
+        }
+    }
+    if (sl > 0 || m >= p.M) return;
+    a = red[0][r];
+    const float l = (a.top + __builtin_amdgcn_logf(a.sum)) * kLn2;                  // (v_log_f32: base two)
+    if (lse) lse[m] = l;
+    if (!loss) return;
+    const int64_t t = target_of(p.rows, m);
+    float out = 0.f;
+    if (t != p.rows.ignore) {
+        if (t < 0 || t >= p.rows.V) {
+            out = __builtin_nanf("");
+            if (p.rows.status) __hip_atomic_fetch_or(p.rows.status, GDN_STATUS_BAD_INDEX, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        } else {
+            const float e = p.rows.smooth;
+            out = (1.f - e) * (l - p.logit[m]) + p.rows.z * l * l;
+            if (e > 0.f) out += e * (l - tot[0][r] / static_cast<float>(p.rows.V));
+        }
+    }
+    loss[m] = out;
+}
+
+// ---- backward ------------------------------------------------------------------
+// A tile's logits to dl, in place, and on as the linear layer's outputs go: as
+// bf16 through LDS in whole rows.
+template <typename S>
+struct Gradient {
+    int64_t m0, n0;
+    Store<S, true, true> store;
+    __device__ __forceinline__ void init(const LossProduct& p, int64_t m, int64_t n, int wave, int lane) {
+        m0 = m;
+        n0 = n;
+        store.init(p.out, m, n, wave, lane);
+    }
+    __device__ __forceinline__ void fetch(const LossProduct&, int) {}
+    __device__ __forceinline__ void run(const LossProduct& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
+        const int l16 = lane % 16, lq = lane / 16, wn = wave % S::NWN;
+        const int64_t first = n0 + wn * S::WN + 4 * lq;
+        finish_logits<S>(p, acc, n0, wave, lane);
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            const int64_t m = row_of<S>(m0, wave, i, l16);
+            int64_t t = -1;
+            if (m < p.M) t = target_of(p.rows, m);
+            const bool counts = m < p.M && t != p.rows.ignore && t >= 0 && t < p.rows.V;
+            float g = 0.f, l = 0.f;
+            if (counts) {
+                g = p.rows.dloss[p.rows.dloss_one ? 0 : m];
+                l = p.rows.lse[m];
+            }
+            const float c = g * fmaf(2.f * p.rows.z, l, 1.f), base = l * kLog2e, rest = g * p.rows.smooth / static_cast<float>(p.rows.V);
+            const float hot = g * (1.f - p.rows.smooth);
+            const int64_t at = t - p.v0 - first;
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float d = c * __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLog2e, -base)) - rest;
+                    if (at == 16 * j + e) d -= hot;
+                    acc[i][j][e] = counts && first + 16 * j + e < p.N ? d : 0.f;
+                }
+        }
+        if (p.columns) {
+            float* const red = reinterpret_cast<float*>(shared);                   // [NWM][BN]
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float s = acc[0][j][e];
+#pragma unroll
+                    for (int i = 1; i < S::TM; ++i) s += acc[i][j][e];
+                    s = group_sum<16>(s);
+                    if (l16 == 0) red[wave / S::NWN * S::BN + wn * S::WN + 16 * j + 4 * lq + e] = s;
+                }
+            __syncthreads();
+            for (int n = threadIdx.x; n < S::BN; n += S::kThreads) {
+                float s = red[n];
+#pragma unroll
+                for (int w = 1; w < S::NWM; ++w) s += red[w * S::BN + n];
+                if (n0 + n < p.N) p.columns[m0 / S::BM * p.columns_ld + p.v0 + n0 + n] = s;
+            }
+            __syncthreads();
+        }
+        store.run(p.out, acc, shared, wave, lane);
+    }
+};
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_gradient_kernel(LossProduct p) {
+    __shared__ __align__(1024) uint8_t shared[S::kBytes];
+    gemm_tile<true, true, Gradient<S>, S>(p, blockIdx.x, shared);
+}
+
+// dx and dw of a piece in one launch.  dx: its reduction, the piece's columns,
+// is cut into `parts`, each with sums of its own ([parts][M][K] in 32 bits),
+// to which a piece adds.  The tiles with the longer reductions come first.
+__host__ __device__ inline int64_t loss_share(int64_t n, int parts) {
+    return ((n + 127) / 128 + parts - 1) / parts * 128;
+}
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel(GemmProduct dx, GemmProduct dw, int parts, int tx, int tw) {
+    __shared__ __align__(1024) uint8_t shared[S::kBytes];
+    const int64_t share = loss_share(dx.K, parts);
+    const bool dw_leads = dw.K > share;
+    const int b = blockIdx.x, first = dw_leads ? tw : tx;
+    const int tile = b < first ? b : b - first;
+    if ((b < first) == dw_leads) {
+        gemm_tile<false, false, Store<S, true>, S>(dw, tile, shared);
+        return;
+    }
+    const int per = tx / parts, part = tile / per;
+    const int64_t k0 = share * part;
+    GemmProduct p = dx;
+    p.K = dx.K - k0 < share ? (dx.K > k0 ? dx.K - k0 : 0) : share;
+    if (p.K > 0) {
+        p.A = static_cast<const uint16_t*>(dx.A) + k0;
+        p.B = static_cast<const uint16_t*>(dx.B) + k0 * dx.ldb;
+    }
+    float* const sums = static_cast<float*>(dx.ep.y) + part * dx.M * dx.N;
+    p.ep.y = sums;
+    if (p.ep.residual) p.ep.residual = sums;
+    gemm_tile<true, false, Store<S, false>, S>(p, tile % per, shared);
+}
+
+// dx from its parts' sums, four columns a thread, and dbias from the row
+// tiles' sums, a column a thread.
+__global__ __launch_bounds__(256) void loss_finish_kernel(const float* sums, int parts, int64_t M, int64_t K, uint16_t* dx, int64_t lddx,
+                                                          int64_t dx_blocks, const float* columns, int64_t rows, int64_t V, float* dbias) {
+    if (static_cast<int64_t>(blockIdx.x) < dx_blocks) {
+        const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, per = K / 4, m = i / per, k = i % per * 4;
+        if (m >= M) return;
+        f32x4 s = *reinterpret_cast<const f32x4*>(sums + m * K + k);
+        for (int a = 1; a < parts; ++a) s += *reinterpret_cast<const f32x4*>(sums + (a * M + m) * K + k);
+        const float f[4] = {s[0], s[1], s[2], s[3]};
+        store_n<4>(dx, true, m * lddx + k, 4, f);
+        return;
+    }
+    const int64_t v = (blockIdx.x - dx_blocks) * 256 + threadIdx.x;
+    if (v >= V) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int64_t r = 0; r < rows; ++r) s += columns[r * V + v];
+    dbias[v] = s;
+}
+
+template <typename S>
+hipError_t forward_t(const LossProduct& p, hipStream_t s) {
+    hipLaunchKernelGGL((loss_forward_kernel<S>), dim3(static_cast<unsigned>(tiles<S>(p))), dim3(S::kThreads), 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename S>
+hipError_t gradient_t(const LossProduct& p, hipStream_t s) {
+    hipLaunchKernelGGL((loss_gradient_kernel<S>), dim3(static_cast<unsigned>(tiles<S>(p))), dim3(S::kThreads), 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename S>
+hipError_t products_t(const GemmProduct& dx, const GemmProduct& dw, int parts, hipStream_t s) {
+    const int64_t tx = dx.ep.y ? tiles<S>(dx) * parts : 0, tw = dw.ep.y ? tiles<S>(dw) : 0;
+    hipLaunchKernelGGL((loss_products_kernel<S>), dim3(static_cast<unsigned>(tx + tw)), dim3(S::kThreads), 0, s, dx, dw, parts,
+                       static_cast<int>(tx), static_cast<int>(tw));
+    return hipGetLastError();
+}
+
+#define GDN_LOSS_TILES(T, CALL)        \
+    switch (T) {                       \
+        case kLarge: return CALL(Large);   \
+        case kWide: return CALL(Wide);     \
+        case kMedium: return CALL(Medium); \
+        default: return CALL(Small);       \
+    }
+
+hipError_t forward(const LossProduct& p, Tiles t, hipStream_t s) {
+#define GDN_CALL(S) forward_t<S>(p, s)
+    GDN_LOSS_TILES(t, GDN_CALL)
+#undef GDN_CALL
+}
+hipError_t gradient(const LossProduct& p, Tiles t, hipStream_t s) {
+#define GDN_CALL(S) gradient_t<S>(p, s)
+    GDN_LOSS_TILES(t, GDN_CALL)
+#undef GDN_CALL
+}
+hipError_t products(const GemmProduct& dx, const GemmProduct& dw, Tiles t, int parts, hipStream_t s) {
+#define GDN_CALL(S) products_t<S>(dx, dw, parts, s)
+    GDN_LOSS_TILES(t, GDN_CALL)
+#undef GDN_CALL
+}
+
+int tile_rows(Tiles t) { return t == kLarge || t == kWide ? 256 : t == kMedium ? 128 : 64; }
+int tile_cols(Tiles t) { return t == kLarge ? 256 : t == kWide || t == kMedium ? 128 : 64; }
+
+Tiles tiles_for(int64_t M, int64_t N, int64_t K) {
+    GemmProduct p{};
+    p.M = M; p.N = N; p.K = K;
+    return choose(p, compute_units()).tiles;
+}
+
+// work-groups of the kernel for few rows: four of them fill a compute unit
+int64_t few_groups(int64_t V) {
+    const int64_t n = ((V + 15) / 16 + kFewWaves - 1) / kFewWaves, most = 4 * compute_units();
+    return n < most ? n : most;
+}
+
+// How the backward pass runs.
+struct Plan {
+    int64_t piece;                            // columns of the vocabulary at a time
+    Tiles gradient, products;
+    int parts;                                // of dx's reduction
+};
+
+// A piece's dl is written by one launch and read by the next, and stays in the
+// 256 MiB of the last-level cache.
+constexpr int64_t kPieceBytes = int64_t(128) << 20, kLeastPiece = 2048;
+
+Plan plan_of(int64_t M, int64_t V, int64_t K) {
+    Plan b{};
+    const int cus = compute_units();
+    int64_t most = kPieceBytes / (2 * (M > 0 ? M : 1)) / 1024 * 1024;
+    if (most < kLeastPiece) most = kLeastPiece;
+    const int64_t pieces = (V + most - 1) / most;
+    b.piece = ((V + pieces - 1) / pieces + 1023) / 1024 * 1024;
+    if (b.piece > V) b.piece = V;
+    b.gradient = tiles_for(M, b.piece, K);
+    // the products' tiles and dx's parts: as in the linear layer's backward
+    // pass, the work over the compute units in rounds of the shorter reduction
+    auto up = [](int64_t a, int64_t c) { return (a + c - 1) / c; };
+    double least = 1e30;
+    auto offer = [&](Tiles t, double each, double alone, int parts) {
+        const int64_t tx = up(M, tile_rows(t)) * up(K, tile_cols(t)) * parts, tw = up(b.piece, tile_rows(t)) * up(K, tile_cols(t));
+        const double lx = static_cast<double>(up(b.piece, parts)), lw = static_cast<double>(M);
+        const double shorter = lx < lw ? lx : lw, longer = lx < lw ? lw : lx;
+        const double work = up(static_cast<int64_t>(tx * lx + tw * lw), static_cast<int64_t>(cus * shorter)) * shorter * each;
+        const double us = (work > longer * alone ? work : longer * alone) / 2048 + 8.0 * M * K * parts / 4e6;
+        if (us < least) { least = us; b.products = t; b.parts = parts; }
+    };
+    for (int parts = 1; parts <= 32 && (parts == 1 || (b.piece / parts >= 256 && up(M, 64) * up(K, 64) <= 4096)); parts *= 2) {
+        offer(kLarge, kLargeUs, kLargeUs, parts);
+        offer(kWide, kWideUs, kWideUs, parts);
+        offer(kMedium, kMediumUs, kMediumAlone, parts);
+        offer(kSmall, kSmallUs, kSmallAlone, parts);
+    }
+    return b;
+}
+
+}  // namespace
+
+// Parts of the forward pass: tiles (or work-groups) across the vocabulary
+static int64_t forward_parts(int64_t M, int64_t V, int64_t K, Tiles* t) {
+    if (M <= kLinearStreamRows) return few_groups(V);
+    *t = tiles_for(M, V, K);
+    return (V + tile_cols(*t) - 1) / tile_cols(*t);
+}
+
+static int64_t round_256(int64_t n) { return (n + 255) / 256 * 256; }
+
+int64_t loss_workspace(int64_t M, int64_t V, int64_t K) {
+    Tiles t;
+    return round_256(8 * forward_parts(M, V, K, &t) * M) + round_256(4 * forward_parts(M, V, K, &t) * M) + round_256(4 * M);
+}
+
+hipError_t launch_loss(const LossCall& c, void* ws, hipStream_t s) {
+    Tiles t = kLarge;
+    const int64_t parts = forward_parts(c.M, c.V, c.K, &t);
+    LossProduct p{};
+    p.A = c.x; p.B = c.w;
+    p.lda = c.ldx; p.ldb = c.ldw;
+    p.M = c.M; p.N = c.V; p.K = c.K;
+    p.rows = c.rows;
+    p.bias = c.bias;
+    uint8_t* const base = static_cast<uint8_t*>(ws);
+    p.part = reinterpret_cast<Part*>(base);
+    if (c.rows.smooth > 0.f) p.totals = reinterpret_cast<float*>(base + round_256(8 * parts * c.M));
+    p.logit = reinterpret_cast<float*>(base + round_256(8 * parts * c.M) + round_256(4 * parts * c.M));
+    hipError_t e;
+    if (c.M <= kLinearStreamRows) {
+        hipLaunchKernelGGL(loss_few_kernel, dim3(static_cast<unsigned>(parts)), dim3(kFewWaves * kWave), 0, s, p);
+        e = hipGetLastError();
+    } else {
+        e = forward(p, t, s);
+    }
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<unsigned>((c.M + kJoinRows - 1) / kJoinRows)), dim3(kJoinRows * kJoinSlices), 0, s,
+                       p, parts, c.loss, c.lse);
+    return hipGetLastError();
+}
+
+struct BackwardWs {
+    int64_t ld, off_sums, off_columns, total;
+};
+
+// dl of a piece, dx's sums, and the row tiles' sums for dbias
+static BackwardWs backward_ws(int64_t M, int64_t V, int64_t K, const Plan& b) {
+    BackwardWs w;
+    w.ld = (b.piece + 63) / 64 * 64;
+    w.off_sums = round_256(2 * M * w.ld);
+    w.off_columns = w.off_sums + round_256(4 * b.parts * M * K);
+    w.total = w.off_columns + round_256(4 * ((M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient)) * V);
+    return w;
+}
+
+int64_t loss_backward_workspace(int64_t M, int64_t V, int64_t K) { return backward_ws(M, V, K, plan_of(M, V, K)).total; }
+
+hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
+    if (c.M == 0) {                           // sums over no rows
+        GemmProduct none{}, pw{};
+        pw.B = c.x; pw.lda = pw.ldb = 8;
+        pw.M = c.V; pw.N = c.K;
+        pw.ep.bf16 = 1;
+        pw.ep.y = c.dw; pw.ep.ldy = c.lddw;
+        const hipError_t e = c.dw ? products(none, pw, kSmall, 1, s) : hipSuccess;
+        return e != hipSuccess ? e : launch_fill_zero(c.dbias, c.V, s);
+    }
+    const Plan b = plan_of(c.M, c.V, c.K);
+    const BackwardWs w = backward_ws(c.M, c.V, c.K, b);
+    uint8_t* const base = static_cast<uint8_t*>(ws);
+    uint16_t* const dl = reinterpret_cast<uint16_t*>(base);
+    float* const sums = reinterpret_cast<float*>(base + w.off_sums);
+    float* const columns = reinterpret_cast<float*>(base + w.off_columns);
+    for (int64_t v0 = 0; v0 < c.V; v0 += b.piece) {
+        const int64_t n = c.V - v0 < b.piece ? c.V - v0 : b.piece;
+        LossProduct p{};
+        p.A = c.x; p.lda = c.ldx;
+        p.B = static_cast<const uint16_t*>(c.w) + v0 * c.ldw; p.ldb = c.ldw;
+        p.M = c.M; p.N = n; p.K = c.K;
+        p.rows = c.rows;
+        p.v0 = v0;
+        p.bias = c.bias ? c.bias + v0 : nullptr;
+        p.out.M = c.M; p.out.N = (n + 7) / 8 * 8;
+        p.out.ep.y = dl; p.out.ep.ldy = w.ld; p.out.ep.bf16 = 1;
+        p.columns = c.dbias ? columns : nullptr;
+        p.columns_ld = c.V;
+        hipError_t e = gradient(p, b.gradient, s);
+        if (e != hipSuccess) return e;
+        if (!c.dx && !c.dw) continue;
+        GemmProduct px{}, pw{};
+        px.A = dl; px.lda = w.ld;
+        px.B = p.B; px.ldb = c.ldw;
+        px.M = c.M; px.N = c.K; px.K = n;
+        px.ep.y = c.dx ? sums : nullptr; px.ep.ldy = c.K;
+        px.ep.residual = v0 > 0 ? sums : nullptr; px.ep.ldr = c.K;
+        pw.A = dl; pw.lda = w.ld;
+        pw.B = c.x; pw.ldb = c.ldx;
+        pw.M = n; pw.N = c.K; pw.K = c.M;
+        pw.ep.bf16 = 1;
+        pw.ep.y = c.dw ? static_cast<uint16_t*>(c.dw) + v0 * c.lddw : nullptr; pw.ep.ldy = c.lddw;
+        e = products(px, pw, b.products, b.parts, s);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t dx_blocks = c.dx ? (c.M * (c.K / 4) + 255) / 256 : 0, bias_blocks = c.dbias ? (c.V + 255) / 256 : 0;
+    if (dx_blocks + bias_blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(loss_finish_kernel, dim3(static_cast<unsigned>(dx_blocks + bias_blocks)), dim3(256), 0, s, sums, b.parts, c.M, c.K,
+                       static_cast<uint16_t*>(c.dx), c.lddx, dx_blocks, columns,
+                       (c.M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient), c.V, c.dbias);
+    return hipGetLastError();
+}
+
+}  // namespace gdn

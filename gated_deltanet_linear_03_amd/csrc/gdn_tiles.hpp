@@ -163,7 +163,8 @@ __device__ __forceinline__ void load_n(const void* p, bool bf16, int64_t at, int
     }
 }
 
-template <int W>
+// KEEP: eight bf16 go the ordinary way, for a kernel that reads them next
+template <int W, bool KEEP = false>
 __device__ __forceinline__ void store_n(void* p, bool bf16, int64_t at, int nv, const float* f) {
     if (bf16) {
         uint16_t* q = static_cast<uint16_t*>(p) + at;
@@ -171,7 +172,8 @@ __device__ __forceinline__ void store_n(void* p, bool bf16, int64_t at, int nv, 
             if constexpr (W == 8) {
                 // (non-temporal: the tiles' outputs and residuals pass the L2 by, which holds operands)
                 const Run8 h = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
-                __builtin_nontemporal_store(h, reinterpret_cast<Run8*>(q));
+                if constexpr (KEEP) *reinterpret_cast<Run8*>(q) = h;
+                else __builtin_nontemporal_store(h, reinterpret_cast<Run8*>(q));
             } else {
                 *reinterpret_cast<Half4*>(q) = Half4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
             }
@@ -409,8 +411,8 @@ struct Shape {
 // is finished and stored as one run, eight columns a lane.  The residual's
 // rows of the first half are requested before the last slices are multiplied,
 // those of the second half before the first one is finished.
-// PLAIN: nothing but y.
-template <typename S, bool PLAIN>
+// PLAIN: nothing but y.  KEEP: as in store_n.
+template <typename S, bool PLAIN, bool KEEP = false>
 struct Store {
     static constexpr int kRun = S::WN / 8;    // lanes of a row
     static constexpr int kRowsAtOnce = kWave / kRun;
@@ -500,7 +502,7 @@ struct Store {
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     const int64_t m = mb + u * kRowsAtOnce;
-                    if (m < p.M && nv > 0) store_n<8>(p.ep.y, p.ep.bf16, m * p.ep.ldy + n, nv, f[u]);
+                    if (m < p.M && nv > 0) store_n<8, KEEP>(p.ep.y, p.ep.bf16, m * p.ep.ldy + n, nv, f[u]);
                 }
             }
             if (half == 0) fetch(p, 1);
@@ -800,6 +802,41 @@ __device__ __forceinline__ void gemm_tile(const P& p, int tile, uint8_t* shared)
     if constexpr (S::BM == 256) gemm_large<AK, BK, Out, S>(p, tile, shared);
     else if constexpr (S::BM == 128) gemm_medium<AK, BK, Out, S>(p, tile, shared);
     else gemm_small<AK, BK, Out, S>(p, tile, shared);
+}
+
+template <typename S>
+int64_t tiles(const GemmProduct& p) { return ((p.M + S::BM - 1) / S::BM) * ((p.N + S::BN - 1) / S::BN); }
+
+// Which tiles: the time of one tile on a compute unit at K = 2048, in us, times
+// the rounds of tiles over the compute units; tiles that share one take longer
+// where they have it to themselves.  Measured, in the order 256 x
+// 256, 256 x 128, 128 x 128, 64 x 64:
+//   4096 x 12288 x 2048: 148, 173, 231, 341 us
+//   4096 x  2048 x 4096:  73,  55,  75, 125 us
+//   2048 x  2048 x 2048:  41,  27,  24,  34 us
+//   1024 x  2048 x 2048:  40,  26,  23,  18 us
+//   1024 x 12352 x 2048:  45,  54,  70,  93 us
+constexpr double kLargeUs = 46.0, kWideUs = 27.0, kMediumUs = 18.0, kSmallUs = 8.5;
+constexpr double kMediumAlone = 24.0, kSmallAlone = 11.0;
+enum Tiles { kLarge, kWide, kMedium, kSmall };
+
+struct Choice {
+    Tiles tiles;
+    double us;
+};
+
+inline Choice choose(const GemmProduct& p, int cus) {
+    auto us = [&](int64_t n, double each, double alone) {
+        const double t = static_cast<double>((n + cus - 1) / cus) * each;
+        return t > alone ? t : alone;
+    };
+    const Choice all[4] = {{kLarge, us(tiles<Large>(p), kLargeUs, kLargeUs)}, {kWide, us(tiles<Wide>(p), kWideUs, kWideUs)},
+                           {kMedium, us(tiles<Medium>(p), kMediumUs, kMediumAlone)},
+                           {kSmall, us(tiles<Small>(p), kSmallUs, kSmallAlone)}};
+    Choice best = all[0];
+    for (int i = 1; i < 4; ++i)
+        if (all[i].us < best.us) best = all[i];
+    return best;
 }
 
 }  // namespace

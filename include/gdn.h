@@ -772,6 +772,72 @@ size_t gdn_norm_backward_workspace_bytes(int64_t M, int64_t D);
 gdn_status gdn_norm_backward(const gdn_norm_grad* grad, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* ---- the cross entropy of a linear layer's outputs ---------------------------
+ * The softmax cross entropy of the logits l = x w^T + bias over a vocabulary of
+ * V, and its gradients, without keeping the logits.  Per row with target t,
+ * lse = log sum_v exp(l_v), e = label_smoothing, c = z_loss:
+ *
+ *   loss = (1 - e) (lse - l_t) + e (lse - mean_v l_v) + c lse^2
+ *   dl_v = dloss ((1 + 2 c lse) exp(l_v - lse) - (1 - e) [v = t] - e / V)
+ *   dx = dl w,  dw = dl^T x,  dbias = column sums of dl
+ *
+ * x and w in bf16, products accumulated and everything of a row in fp32.  A row
+ * whose target is ignore_index has loss 0 and adds nothing to the gradients,
+ * whatever its logits are (its lse is given all the same).  A row whose target
+ * is neither that nor in [0, V) has loss NaN, adds nothing to the gradients,
+ * and GDN_STATUS_BAD_INDEX is ORed into status (never cleared).  This library's own kernels
+ * at every size; the same bits from call to call.
+ * Row strides in elements, 0 means dense; a single row's is not looked at.
+ * x, w: 16-byte aligned, K and their strides multiples of 8 up to 2^22; the
+ * others element aligned. */
+typedef struct {
+    int64_t M, V, K;               /* M >= 0, V >= 1, K >= 8; fewer than 2^24 tiles of 64 x 64 in M x V (and in the
+                                    * backward pass in dx and dw together), M up to 2^25 and M K up to 2^33 */
+    const void* x;                 /* [M][K] bf16 */
+    int64_t x_stride;
+    const void* w;                 /* [V][K] bf16 */
+    int64_t w_stride;
+    const float* bias;             /* optional [V] */
+    const void* targets;           /* [M] int32, or int64 with target_bytes 8 */
+    int32_t target_bytes;          /* 4 or 8 */
+    int64_t ignore_index;
+    float label_smoothing;         /* in [0, 1) */
+    float z_loss;                  /* >= 0 */
+    float* loss;                   /* optional [M] */
+    float* lse;                    /* optional [M], for the backward pass */
+    int32_t* status;               /* optional */
+} gdn_loss_io;
+
+/* Bytes of device workspace; 0 on error.  Forward about 8 bytes for each row
+ * and 256 columns of the vocabulary; backward about 128 MiB beyond dx in fp32. */
+size_t gdn_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K);
+size_t gdn_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
+
+/* Enqueue the forward pass.  workspace: device memory, 256-byte aligned, not
+ * shared with a concurrently running call.  loss and lse must not share bytes
+ * with another buffer. */
+gdn_status gdn_linear_cross_entropy(const gdn_loss_io* io, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* The gradients' buffers; each of dx, dw, dbias may be NULL.  dl is rounded to
+ * bf16 for the two products; dbias sums it in fp32.  The bytes from the first
+ * to the last element of an output must not overlap those of another buffer. */
+typedef struct {
+    const float* dloss;            /* [M], or one value for all rows */
+    int32_t dloss_one;             /* nonzero: one value (for a mean, 1 / rows that count) */
+    void* dx;                      /* [M][K] bf16 */
+    int64_t dx_stride;
+    void* dw;                      /* [V][K] bf16 */
+    int64_t dw_stride;
+    float* dbias;                  /* [V] */
+} gdn_loss_grad;
+
+/* Enqueue the backward pass: io as in the forward call, lse as it wrote it
+ * (loss and status are not used). */
+gdn_status gdn_linear_cross_entropy_backward(const gdn_loss_io* io, const gdn_loss_grad* grad,
+                                             void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
 /* ---- the update of the weights ----------------------------------------------
  * One AdamW step over many tensors.  Per element at step k:
  *

@@ -121,3 +121,57 @@ def adamw64(p, g, m, v, lr, b1, b2, eps, decay, k):
     # c1: 6 U, the root 6 U, c2 6 U, the reciprocal 2 U, products
     e_p = lr * (e_m / c1 / den + 24 * U * np.abs(step)) + 2 * U * np.abs(p) + 4 * U * lr * decay * np.abs(p)
     return (p - lr * (step + decay * p), m1, v1), (e_p + 1e-37, e_m + 1e-37, e_v + 1e-37)
+
+
+# ---- the cross entropy of a linear layer's outputs --------------------------------
+
+def loss64(x, w, bias, targets, smooth, z, ignore=-100):
+    """loss, lse and bounds on 32 bits' errors, and the logits with theirs.  A
+    logit is a sum of K products of bf16 values (exact in 32 bits each), rounded
+    at most K times in any order."""
+    x, w = x.double(), w.double()
+    K, V = x.shape[1], w.shape[0]
+    l = x @ w.t().contiguous()
+    e_l = (x.abs() @ w.abs().t().contiguous()) * (K * U)
+    if bias is not None:
+        l = l + bias.double()
+        e_l = e_l + U * l.abs()
+    lse = torch.logsumexp(l, 1)
+    # off by no more than the logits are; then 2^(l log2 e - top): the product
+    # and the difference to 2 U of l each, v_exp_f32 to 2 U; all terms are
+    # positive, each through at most `steps` additions and joins (of 6 U)
+    steps = 200 + V / 512
+    e_lse = e_l.amax(1) + U * (6 * l.abs().amax(1) + 6 * lse.abs() + steps)
+    counts = (targets != ignore) & (targets >= 0) & (targets < V)
+    rows = torch.arange(x.shape[0], device=x.device)
+    at = targets.long().clamp(0, V - 1)
+    lt, e_lt = l[rows, at], e_l[rows, at]
+    mean = l.mean(1)
+    loss = (1 - smooth) * (lse - lt) + smooth * (lse - mean) + z * lse * lse
+    e_mean = e_l.mean(1) + steps * U * l.abs().mean(1)
+    e = (1 - smooth) * (e_lse + e_lt) + smooth * (e_lse + e_mean) + z * (2 * lse.abs() + e_lse) * e_lse
+    e = e + 6 * U * (lse.abs() + lt.abs() + mean.abs() + z * lse * lse)
+    bad = ~counts & (targets != ignore)
+    loss = torch.where(counts, loss, torch.where(bad, float("nan"), 0.0))
+    return loss, lse, e, e_lse, l, e_l, counts
+
+
+def loss_backward64(dloss, x, w, bias, targets, lse, smooth, z, ignore=-100):
+    """dx, dw, dbias from the lse given, and bounds that count dl's rounding to bf16."""
+    _, _, _, _, l, e_l, counts = loss64(x, w, bias, targets, smooth, z, ignore)
+    x, w, lse = x.double(), w.double(), lse.double()
+    M, V = l.shape
+    g = torch.where(counts, dloss.double().expand(M), 0.0)[:, None]
+    c = 1 + 2 * z * lse[:, None]
+    p = torch.exp(l - lse[:, None])
+    rel = e_l + U * (6 * l.abs() + 6 * lse.abs()[:, None] + 6)
+    hot = torch.zeros_like(p)
+    hot[torch.arange(M, device=x.device), targets.long().clamp(0, V - 1)] = 1 - smooth
+    dl = g * (c * p - hot - smooth / V)
+    e = g.abs() * (c.abs() * p * (rel + rel * rel) + 4 * U * (c.abs() * p + hot + smooth / V)) + 1e-37
+    r = e + HALF[torch.bfloat16] * (dl.abs() + e)                # of dl as the products see it
+    d = dl.abs() + r
+    dx, dw = dl @ w, dl.t().contiguous() @ x
+    e_dx = r @ w.abs() + (V + 64) * U * (d @ w.abs())
+    e_dw = r.t().contiguous() @ x.abs() + (M + 64) * U * (d.t().contiguous() @ x.abs())
+    return (dx, dw, dl.sum(0)), (e_dx + 1e-37, e_dw + 1e-37, e.sum(0) + (M + 64) * U * dl.abs().sum(0))
