@@ -341,6 +341,7 @@ struct LossRows {
     // backward
     const float *lse, *dloss;
     int dloss_one;                       // one value for all rows
+    const float* scale;                  // dl stands over this times 1 - smooth (set by the launcher)
 };
 
 struct LossCall {

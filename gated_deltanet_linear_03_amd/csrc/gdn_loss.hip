@@ -15,8 +15,14 @@
 // Backward: for a piece of the vocabulary at a time the tiles of the product
 // are computed once more and leave dl in bf16, the operand type of the two
 // products that follow: dx, in 32 bits from piece to piece, and the piece's
-// rows of dw.  (dl is rounded to bf16 once, as dp is in the linear layer's
-// backward pass; dbias sums it in 32 bits before that.)
+// rows of dw.  dl is rounded to bf16 once, as dp is in the linear layer's
+// backward pass (dbias sums it in 32 bits before that), and not by itself but
+// over (1 - e) times the largest |g|, by which the outputs are multiplied in 32
+// bits: with one g for all rows the target's entry is then next to -1 and
+// rounds as any other value.  (Times g it would be next to -g in every row,
+// all of them off by the same up to 2^-8 of themselves: 4096 x 248320 x 2048
+// with g = 1/3686: dw 3.4e-3 off in its norm, of which 1.7e-3 are its own
+// rounding.)
 // Statistics are in base two: 2^(l log2 e - top), one multiply-add and one
 // v_exp_f32 a logit.
 #include "gdn_tiles.hpp"
@@ -321,20 +327,36 @@ struct Gradient {
             const bool counts = m < p.M && t != p.rows.ignore && t >= 0 && t < p.rows.V;
             float g = 0.f, l = 0.f;
             if (counts) {
-                g = p.rows.dloss[p.rows.dloss_one ? 0 : m];
+                g = p.rows.dloss_one ? 1.f : p.rows.dloss[m] / *p.rows.scale;
                 l = p.rows.lse[m];
             }
-            const float c = g * fmaf(2.f * p.rows.z, l, 1.f), base = l * kLog2e, rest = g * p.rows.smooth / static_cast<float>(p.rows.V);
-            const float hot = g * (1.f - p.rows.smooth);
-            const int64_t at = t - p.v0 - first;
+            const float g1 = g / (1.f - p.rows.smooth);
+            const float c = g1 * fmaf(2.f * p.rows.z, l, 1.f), base = l * kLog2e, rest = g1 * p.rows.smooth / static_cast<float>(p.rows.V);
 #pragma unroll
             for (int j = 0; j < S::TN; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float d = c * __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLog2e, -base)) - rest;
-                    if (at == 16 * j + e) d -= hot;
-                    acc[i][j][e] = counts && first + 16 * j + e < p.N ? d : 0.f;
+                    const float d = fmaf(c, __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLog2e, -base)), -rest);
+                    acc[i][j][e] = counts ? d : 0.f;
                 }
+            const int64_t at = t - p.v0 - first;
+            if (counts && at >= 0 && at < S::WN) {   // (few lanes: the target is one of V)
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (at == 16 * j + e) acc[i][j][e] -= g;
+            }
+        }
+        if (n0 + S::BN > p.N) {                      // columns past the end
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (first + 16 * j + e >= p.N) {
+#pragma unroll
+                        for (int i = 0; i < S::TM; ++i) acc[i][j][e] = 0.f;
+                    }
         }
         if (p.columns) {
             float* const red = reinterpret_cast<float*>(shared);                   // [NWM][BN]
@@ -367,6 +389,25 @@ __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_gradient_kernel
     gemm_tile<true, true, Gradient<S>, S>(p, blockIdx.x, shared);
 }
 
+// The largest finite |g| of the rows that count (0: none).
+__global__ __launch_bounds__(1024) void loss_scale_kernel(LossRows r, int64_t M, float* out) {
+    __shared__ float red[1024 / kWave];
+    float top = 0.f;
+    for (int64_t m = threadIdx.x; m < M; m += 1024) {
+        const int64_t t = target_of(r, m);
+        const float g = fabsf(r.dloss[m]);
+        if (t != r.ignore && t >= 0 && t < r.V && g < __builtin_inff()) top = fmaxf(top, g);
+    }
+#pragma unroll
+    for (int x = 1; x < kWave; x *= 2) top = fmaxf(top, __shfl_xor(top, x, kWave));
+    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = top;
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+#pragma unroll
+    for (int w = 1; w < 1024 / kWave; ++w) top = fmaxf(top, red[w]);
+    *out = top > 0.f ? top : 1.f;
+}
+
 // dx and dw of a piece in one launch.  dx: its reduction, the piece's columns,
 // is cut into `parts`, each with sums of its own ([parts][M][K] in 32 bits),
 // to which a piece adds.  The tiles with the longer reductions come first.
@@ -375,14 +416,14 @@ __host__ __device__ inline int64_t loss_share(int64_t n, int parts) {
 }
 
 template <typename S>
-__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel(GemmProduct dx, GemmProduct dw, int parts, int tx, int tw) {
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel(GemmProduct dx, ScaledProduct dw, int parts, int tx, int tw) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
     const int64_t share = loss_share(dx.K, parts);
     const bool dw_leads = dw.K > share;
     const int b = blockIdx.x, first = dw_leads ? tw : tx;
     const int tile = b < first ? b : b - first;
     if ((b < first) == dw_leads) {
-        gemm_tile<false, false, Store<S, true>, S>(dw, tile, shared);
+        gemm_tile<false, false, Store<S, true, false, ScaledProduct>, S>(dw, tile, shared);
         return;
     }
     const int per = tx / parts, part = tile / per;
@@ -402,13 +443,15 @@ __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel
 // dx from its parts' sums, four columns a thread, and dbias from the row
 // tiles' sums, a column a thread.
 __global__ __launch_bounds__(256) void loss_finish_kernel(const float* sums, int parts, int64_t M, int64_t K, uint16_t* dx, int64_t lddx,
-                                                          int64_t dx_blocks, const float* columns, int64_t rows, int64_t V, float* dbias) {
+                                                          int64_t dx_blocks, const float* columns, int64_t rows, int64_t V, float* dbias,
+                                                          const float* scale, float factor) {
+    const float by = *scale * factor;
     if (static_cast<int64_t>(blockIdx.x) < dx_blocks) {
         const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, per = K / 4, m = i / per, k = i % per * 4;
         if (m >= M) return;
         f32x4 s = *reinterpret_cast<const f32x4*>(sums + m * K + k);
         for (int a = 1; a < parts; ++a) s += *reinterpret_cast<const f32x4*>(sums + (a * M + m) * K + k);
-        const float f[4] = {s[0], s[1], s[2], s[3]};
+        const float f[4] = {s[0] * by, s[1] * by, s[2] * by, s[3] * by};
         store_n<4>(dx, true, m * lddx + k, 4, f);
         return;
     }
@@ -417,7 +460,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const float* sums, int
     float s = 0.f;
 #pragma unroll 8
     for (int64_t r = 0; r < rows; ++r) s += columns[r * V + v];
-    dbias[v] = s;
+    dbias[v] = s * by;
 }
 
 template <typename S>
@@ -433,7 +476,7 @@ hipError_t gradient_t(const LossProduct& p, hipStream_t s) {
 }
 
 template <typename S>
-hipError_t products_t(const GemmProduct& dx, const GemmProduct& dw, int parts, hipStream_t s) {
+hipError_t products_t(const GemmProduct& dx, const ScaledProduct& dw, int parts, hipStream_t s) {
     const int64_t tx = dx.ep.y ? tiles<S>(dx) * parts : 0, tw = dw.ep.y ? tiles<S>(dw) : 0;
     hipLaunchKernelGGL((loss_products_kernel<S>), dim3(static_cast<unsigned>(tx + tw)), dim3(S::kThreads), 0, s, dx, dw, parts,
                        static_cast<int>(tx), static_cast<int>(tw));
@@ -458,7 +501,7 @@ hipError_t gradient(const LossProduct& p, Tiles t, hipStream_t s) {
     GDN_LOSS_TILES(t, GDN_CALL)
 #undef GDN_CALL
 }
-hipError_t products(const GemmProduct& dx, const GemmProduct& dw, Tiles t, int parts, hipStream_t s) {
+hipError_t products(const GemmProduct& dx, const ScaledProduct& dw, Tiles t, int parts, hipStream_t s) {
 #define GDN_CALL(S) products_t<S>(dx, dw, parts, s)
     GDN_LOSS_TILES(t, GDN_CALL)
 #undef GDN_CALL
@@ -563,7 +606,7 @@ hipError_t launch_loss(const LossCall& c, void* ws, hipStream_t s) {
 }
 
 struct BackwardWs {
-    int64_t ld, off_sums, off_columns, total;
+    int64_t ld, off_sums, off_columns, off_scale, total;
 };
 
 // dl of a piece, dx's sums, and the row tiles' sums for dbias
@@ -572,7 +615,8 @@ static BackwardWs backward_ws(int64_t M, int64_t V, int64_t K, const Plan& b) {
     w.ld = (b.piece + 63) / 64 * 64;
     w.off_sums = round_256(2 * M * w.ld);
     w.off_columns = w.off_sums + round_256(4 * b.parts * M * K);
-    w.total = w.off_columns + round_256(4 * ((M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient)) * V);
+    w.off_scale = w.off_columns + round_256(4 * ((M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient)) * V);
+    w.total = w.off_scale + 256;
     return w;
 }
 
@@ -580,7 +624,8 @@ int64_t loss_backward_workspace(int64_t M, int64_t V, int64_t K) { return backwa
 
 hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
     if (c.M == 0) {                           // sums over no rows
-        GemmProduct none{}, pw{};
+        GemmProduct none{};
+        ScaledProduct pw{};
         pw.B = c.x; pw.lda = pw.ldb = 8;
         pw.M = c.V; pw.N = c.K;
         pw.ep.bf16 = 1;
@@ -594,13 +639,23 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
     uint16_t* const dl = reinterpret_cast<uint16_t*>(base);
     float* const sums = reinterpret_cast<float*>(base + w.off_sums);
     float* const columns = reinterpret_cast<float*>(base + w.off_columns);
+    LossRows rows = c.rows;
+    const float* scale = rows.dloss;
+    if (!rows.dloss_one) {
+        float* const top = reinterpret_cast<float*>(base + w.off_scale);
+        hipLaunchKernelGGL(loss_scale_kernel, dim3(1), dim3(1024), 0, s, rows, c.M, top);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        scale = top;
+    }
+    rows.scale = scale;
     for (int64_t v0 = 0; v0 < c.V; v0 += b.piece) {
         const int64_t n = c.V - v0 < b.piece ? c.V - v0 : b.piece;
         LossProduct p{};
         p.A = c.x; p.lda = c.ldx;
         p.B = static_cast<const uint16_t*>(c.w) + v0 * c.ldw; p.ldb = c.ldw;
         p.M = c.M; p.N = n; p.K = c.K;
-        p.rows = c.rows;
+        p.rows = rows;
         p.v0 = v0;
         p.bias = c.bias ? c.bias + v0 : nullptr;
         p.out.M = c.M; p.out.N = (n + 7) / 8 * 8;
@@ -610,7 +665,10 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
         hipError_t e = gradient(p, b.gradient, s);
         if (e != hipSuccess) return e;
         if (!c.dx && !c.dw) continue;
-        GemmProduct px{}, pw{};
+        GemmProduct px{};
+        ScaledProduct pw{};
+        pw.scale = scale;
+        pw.factor = 1.f - c.rows.smooth;
         px.A = dl; px.lda = w.ld;
         px.B = p.B; px.ldb = c.ldw;
         px.M = c.M; px.N = c.K; px.K = n;
@@ -628,7 +686,7 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
     if (dx_blocks + bias_blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(loss_finish_kernel, dim3(static_cast<unsigned>(dx_blocks + bias_blocks)), dim3(256), 0, s, sums, b.parts, c.M, c.K,
                        static_cast<uint16_t*>(c.dx), c.lddx, dx_blocks, columns,
-                       (c.M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient), c.V, c.dbias);
+                       (c.M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient), c.V, c.dbias, scale, 1.f - c.rows.smooth);
     return hipGetLastError();
 }
 

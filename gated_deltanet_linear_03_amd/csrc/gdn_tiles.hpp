@@ -11,6 +11,8 @@
 //   run(p, acc, shared, wave, lane)   all waves, after the last product; the
 //                                 stages' LDS is the epilogue's
 #pragma once
+#include <type_traits>
+
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -411,8 +413,14 @@ struct Shape {
 // is finished and stored as one run, eight columns a lane.  The residual's
 // rows of the first half are requested before the last slices are multiplied,
 // those of the second half before the first one is finished.
-// PLAIN: nothing but y.  KEEP: as in store_n.
-template <typename S, bool PLAIN, bool KEEP = false>
+// PLAIN: nothing but y.  KEEP: as in store_n.  P: GemmProduct, or one with a
+// factor of its own for the sums (PLAIN).
+struct ScaledProduct : GemmProduct {
+    const float* scale;                       // device; NULL: 1
+    float factor;
+};
+
+template <typename S, bool PLAIN, bool KEEP = false, typename P = GemmProduct>
 struct Store {
     static constexpr int kRun = S::WN / 8;    // lanes of a row
     static constexpr int kRowsAtOnce = kWave / kRun;
@@ -423,7 +431,7 @@ struct Store {
     bool early;                               // the residual can be fetched as bf16 runs
     Run8 res[kMine];
 
-    __device__ __forceinline__ void init(const GemmProduct& p, int64_t tile_m, int64_t tile_n, int wave, int lane) {
+    __device__ __forceinline__ void init(const P& p, int64_t tile_m, int64_t tile_n, int wave, int lane) {
         m0 = tile_m + wave / S::NWN * S::kWaveStep;
         first = lane / kRun;
         n = tile_n + wave % S::NWN * S::WN + 8 * (lane % kRun);
@@ -431,7 +439,7 @@ struct Store {
         early = !PLAIN && p.ep.residual && p.ep.bf16 && nv == 8;
     }
 
-    __device__ __forceinline__ void fetch(const GemmProduct& p, int half) {
+    __device__ __forceinline__ void fetch(const P& p, int half) {
         if (PLAIN || !early) return;
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
@@ -442,13 +450,16 @@ struct Store {
         }
     }
 
-    __device__ __forceinline__ void run(const GemmProduct& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
+    __device__ __forceinline__ void run(const P& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
         float* const strip = reinterpret_cast<float*>(shared) + wave * S::kStrip;
         const int l16 = lane % 16, lq = lane / 16;
         float bias[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) bias[e] = 0.f;
         if (!PLAIN && p.ep.bias && nv > 0) load_n<8>(p.ep.bias, false, n, nv, bias);
+        constexpr bool kScaled = !std::is_same<P, GemmProduct>::value;
+        float scale = 1.f;
+        if constexpr (kScaled) scale = p.scale ? *p.scale * p.factor : 1.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -467,7 +478,10 @@ struct Store {
                                                                     8 * (lane % kRun));
                     const f32x4 q0 = q[0], q1 = q[1];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) { f[u][e] = q0[e] + bias[e]; f[u][4 + e] = q1[e] + bias[4 + e]; }
+                    for (int e = 0; e < 4; ++e) {
+                        f[u][e] = kScaled ? q0[e] * scale : q0[e] + bias[e];
+                        f[u][4 + e] = kScaled ? q1[e] * scale : q1[e] + bias[4 + e];
+                    }
                 }
                 const int64_t mb = m0 + half * S::kHalfStep + first + u0 * kRowsAtOnce;
                 if (!PLAIN && p.ep.preact) {

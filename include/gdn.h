@@ -783,7 +783,8 @@ gdn_status gdn_norm_backward(const gdn_norm_grad* grad, void* workspace,
  *
  * x and w in bf16, products accumulated and everything of a row in fp32.  A row
  * whose target is ignore_index has loss 0 and adds nothing to the gradients,
- * whatever its logits are (its lse is given all the same).  A row whose target
+ * whatever its logits are (its lse is given all the same; an infinity or NaN in
+ * its row of x does reach dw, as 0 times that).  A row whose target
  * is neither that nor in [0, V) has loss NaN, adds nothing to the gradients,
  * and GDN_STATUS_BAD_INDEX is ORed into status (never cleared).  This library's own kernels
  * at every size; the same bits from call to call.
