@@ -25,6 +25,8 @@
 // rounding.)
 // Statistics are in base two: 2^(l log2 e - top), one multiply-add and one
 // v_exp_f32 a logit.
+#include <cmath>
+
 #include "gdn_tiles.hpp"
 
 namespace gdn {
@@ -510,10 +512,41 @@ hipError_t products(const GemmProduct& dx, const ScaledProduct& dw, Tiles t, int
 int tile_rows(Tiles t) { return t == kLarge || t == kWide ? 256 : t == kMedium ? 128 : 64; }
 int tile_cols(Tiles t) { return t == kLarge ? 256 : t == kWide || t == kMedium ? 128 : 64; }
 
-Tiles tiles_for(int64_t M, int64_t N, int64_t K) {
-    GemmProduct p{};
-    p.M = M; p.N = N; p.K = K;
-    return choose(p, compute_units()).tiles;
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Times of tiles in us, by which tiles, parts and pieces are chosen: a tile of
+// reduction 2048 when the card is full of them (`full`: tiles that share a
+// compute unit divided by how many do) and when it has a compute unit to itself
+// (`alone`; faster for the large ones, which do not meet the card's power then),
+// and what a tile takes beside its reduction, with each epilogue.  Fitted to, in the order 256 x
+// 256, 256 x 128, 128 x 128, 64 x 64 (rows x vocabulary x K):
+//   forward   4096 x 248320 x 2048: 2965, 3612, 3691, 8226 us;  1537 x 50001 x 1000: 173, 190, 184, 399;
+//             200 x 5000 x 4096: 76, 48, 37, 34;  8192 x 20000 x 512: 164, 199, 191, 292
+//   dl alone  the same: 3451, 4195, 4284, 8871;  204, 243, 228, 412;  79, 49, 38, 34;  252, 274, 241, 342
+//   backward with the best parts: 9262, 10457, 10640, 19558;  504, 579, 575, 840;  71, 67, 63, 70;  700, 552, 559, 857
+struct TileTimes {
+    double full, alone, forward, gradient, product;
+};
+constexpr TileTimes kTimes[4] = {{42, 35, 7, 10, 6}, {25, 22, 5, 6.5, 6}, {13, 17, 2.5, 3, 3}, {7.5, 15, 1.5, 1.5, 1.5}};
+constexpr double kBytesPerUs = 4.5e6;
+
+// n tiles of one kind: the large ones have a compute unit each and go in rounds
+double tiles_us(Tiles t, int64_t n, double reduction, double other) {
+    const int cus = compute_units();
+    const double r = reduction / 2048, rounds = t == kLarge || t == kWide ? static_cast<double>(up(n, cus)) : static_cast<double>(n) / cus;
+    const double full = rounds * (r * kTimes[t].full + other), alone = r * kTimes[t].alone + other;
+    return full > alone ? full : alone;
+}
+
+// tiles of x w^T
+Tiles tiles_for(int64_t M, int64_t N, int64_t K, double TileTimes::*other, double* us) {
+    Tiles best = kLarge;
+    *us = 1e30;
+    for (Tiles t : {kLarge, kWide, kMedium, kSmall}) {
+        const double e = tiles_us(t, up(M, tile_rows(t)) * up(N, tile_cols(t)), static_cast<double>(K), kTimes[t].*other);
+        if (e < *us) { *us = e; best = t; }
+    }
+    return best;
 }
 
 // work-groups of the kernel for few rows: four of them fill a compute unit
@@ -529,38 +562,77 @@ struct Plan {
     int parts;                                // of dx's reduction
 };
 
-// A piece's dl is written by one launch and read by the next, and stays in the
-// 256 MiB of the last-level cache.
-constexpr int64_t kPieceBytes = int64_t(128) << 20, kLeastPiece = 2048;
+// When the last of a launch's tiles ends: n0 of t0 us first, then n1 of t1, each
+// taken by the next free of `units`.
+double makespan(int64_t n0, double t0, int64_t n1, double t1, int64_t units) {
+    const int64_t q = n0 / units, r = n0 % units;             // r units have one more of the first kind
+    const double early = static_cast<double>(q) * t0, late = early + (r > 0 ? t0 : 0.0);
+    if (n1 == 0) return late;
+    const double even = (static_cast<double>(n0) * t0 + static_cast<double>(n1) * t1) / static_cast<double>(units);
+    const double least = even > late ? even : late;
+    double end = 1e30;
+    for (double from : {early, late}) {
+        int64_t i = static_cast<int64_t>(std::ceil((least - from) / t1 - 1e-9));
+        for (;; ++i) {                                        // (two steps at the most: a unit idles for less than t1)
+            const double t = from + static_cast<double>(i) * t1;
+            if ((units - r) * static_cast<int64_t>((t - early) / t1 + 1e-9) + r * static_cast<int64_t>((t - late) / t1 + 1e-9) >= n1) {
+                if (t < end) end = t;
+                break;
+            }
+        }
+    }
+    return end;
+}
+
+// The best tiles, and parts of dx's reduction, for the products of a piece.  A
+// launch has dx's and dw's tiles, the ones of the longer reduction first.
+double plan_products(int64_t M, int64_t piece, int64_t K, Plan* b) {
+    const int cus = compute_units();
+    double least = 1e30;
+    // w in, dw out
+    const double memory = 4.0 * static_cast<double>(piece) * K / kBytesPerUs;
+    for (int parts = 1; parts <= 32 && (parts == 1 || (piece / parts >= 256 && up(M, 64) * up(K, 64) <= 4096)); parts *= 2) {
+        // the parts' sums: out, and in again
+        const double sums = 8.0 * M * K * parts / kBytesPerUs;
+        for (Tiles t : {kLarge, kWide, kMedium, kSmall}) {
+            const TileTimes& c = kTimes[t];
+            const int64_t tx = up(M, tile_rows(t)) * up(K, tile_cols(t)) * parts, tw = up(piece, tile_rows(t)) * up(K, tile_cols(t));
+            const double lx = static_cast<double>(up(piece, parts)) / 2048, lw = static_cast<double>(M) / 2048;
+            const double x = lx * c.full + c.product, w = lw * c.full + c.product;
+            double us = (lx > lw ? lx : lw) * c.alone + c.product;
+            const double full = t == kMedium || t == kSmall ? (static_cast<double>(tx) * x + static_cast<double>(tw) * w) / cus
+                                : lx >= lw ? makespan(tx, x, tw, w, cus) : makespan(tw, w, tx, x, cus);
+            us = us > full ? us : full;
+            us = (us > memory ? us : memory) + sums;
+            if (us < least) { least = us; b->products = t; b->parts = parts; }
+        }
+    }
+    return least;
+}
+
+// Pieces of up to 256 MiB of dl (no less than 4096 columns).  Smaller ones stay
+// in the last-level cache, which changes little (4096 x 248320 x 2048: 9.45 ms
+// with 64 MiB, 9.6 with 512); how the tiles of a piece fill the card does.
+constexpr int64_t kPieceBytes = int64_t(256) << 20, kLeastPiece = 4096;
 
 Plan plan_of(int64_t M, int64_t V, int64_t K) {
-    Plan b{};
-    const int cus = compute_units();
-    int64_t most = kPieceBytes / (2 * (M > 0 ? M : 1)) / 1024 * 1024;
-    if (most < kLeastPiece) most = kLeastPiece;
-    const int64_t pieces = (V + most - 1) / most;
-    b.piece = ((V + pieces - 1) / pieces + 1023) / 1024 * 1024;
-    if (b.piece > V) b.piece = V;
-    b.gradient = tiles_for(M, b.piece, K);
-    // the products' tiles and dx's parts: as in the linear layer's backward
-    // pass, the work over the compute units in rounds of the shorter reduction
-    auto up = [](int64_t a, int64_t c) { return (a + c - 1) / c; };
+    Plan best{};
     double least = 1e30;
-    auto offer = [&](Tiles t, double each, double alone, int parts) {
-        const int64_t tx = up(M, tile_rows(t)) * up(K, tile_cols(t)) * parts, tw = up(b.piece, tile_rows(t)) * up(K, tile_cols(t));
-        const double lx = static_cast<double>(up(b.piece, parts)), lw = static_cast<double>(M);
-        const double shorter = lx < lw ? lx : lw, longer = lx < lw ? lw : lx;
-        const double work = up(static_cast<int64_t>(tx * lx + tw * lw), static_cast<int64_t>(cus * shorter)) * shorter * each;
-        const double us = (work > longer * alone ? work : longer * alone) / 2048 + 8.0 * M * K * parts / 4e6;
-        if (us < least) { least = us; b.products = t; b.parts = parts; }
-    };
-    for (int parts = 1; parts <= 32 && (parts == 1 || (b.piece / parts >= 256 && up(M, 64) * up(K, 64) <= 4096)); parts *= 2) {
-        offer(kLarge, kLargeUs, kLargeUs, parts);
-        offer(kWide, kWideUs, kWideUs, parts);
-        offer(kMedium, kMediumUs, kMediumAlone, parts);
-        offer(kSmall, kSmallUs, kSmallAlone, parts);
+    int64_t most = kPieceBytes / (2 * (M > 0 ? M : 1)) / 256 * 256;
+    if (most < kLeastPiece) most = kLeastPiece;
+    int64_t before = 0;
+    for (int64_t pieces = up(V, most), tried = 0; tried < 5; pieces += 1 + pieces / 4, ++tried) {
+        Plan b{};
+        b.piece = up(up(V, pieces), 256) * 256;
+        if (b.piece > V) b.piece = V;
+        if (b.piece == before || (tried > 0 && b.piece < kLeastPiece)) break;
+        before = b.piece;
+        double dl;
+        b.gradient = tiles_for(M, b.piece, K, &TileTimes::gradient, &dl);
+        const double us = (dl + plan_products(M, b.piece, K, &b) + 8) * static_cast<double>(V) / static_cast<double>(b.piece);   // 8: two launches
+        if (us < least) { least = us; best = b; }
     }
-    return b;
+    return best;
 }
 
 }  // namespace
@@ -568,7 +640,8 @@ Plan plan_of(int64_t M, int64_t V, int64_t K) {
 // Parts of the forward pass: tiles (or work-groups) across the vocabulary
 static int64_t forward_parts(int64_t M, int64_t V, int64_t K, Tiles* t) {
     if (M <= kLinearStreamRows) return few_groups(V);
-    *t = tiles_for(M, V, K);
+    double us;
+    *t = tiles_for(M, V, K, &TileTimes::forward, &us);
     return (V + tile_cols(*t) - 1) / tile_cols(*t);
 }
 

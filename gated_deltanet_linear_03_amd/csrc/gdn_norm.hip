@@ -102,10 +102,11 @@ __device__ __forceinline__ void row_sums(float* s, float* red, int t) {
 
 constexpr int rows_of(int T) { return T < 256 ? 256 / T : 1; }   // rows that a work-group holds at a time
 
-// One block of rows a work-group, and more only where the grid would be past
-// what a launch holds.  MASK: D is not W T NV.
+// The rows all at once: one block of them a work-group (more only where the
+// grid would be past what a launch holds).  4096 x 2048 in fp32 to bf16: 9.4
+// us, 12.3 with work-groups that stay.  MASK: D is not W T NV.
 template <bool XB, bool YB, bool MASK, int T, int NV>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormParams p) {
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_row_kernel(NormParams p) {
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T);
     __shared__ float red[2][T > kWave ? T / kWave : 1];
     const int t = threadIdx.x % T;
@@ -172,6 +173,78 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormPar
     }
 }
 
+// Many long rows: a work-group takes every gridDim-th block of them and keeps
+// its columns' weights in registers (read again for each row they are several
+// times the row's own bytes), the next row on its way while one is summed.
+// 32768 x 4096 in bf16: 97 us, 131 with a wave a row.
+template <bool XB, bool YB, bool MASK, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormParams p) {
+    constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
+    __shared__ float red[2][R][T > kWave ? T / kWave : 1];
+    const int t = threadIdx.x % T, r = threadIdx.x / T;
+    Columns<W, T, NV> cols;
+    cols.init(t, p.D);
+    float w[C], b[C];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            w[W * j + e] = p.weight ? p.weight[cols.at[j] + e] : 1.f;
+            b[W * j + e] = p.bias ? p.bias[cols.at[j] + e] : 0.f;
+        }
+    const float per = 1.f / static_cast<float>(p.D);
+    int turn = 0;
+    // (rows past the end read the last one)
+    auto row_at = [&](int64_t m0) { return m0 + r < p.M ? m0 + r : p.M - 1; };
+    Run<XB, W> x[NV], next[NV];
+    int64_t m0 = static_cast<int64_t>(blockIdx.x) * R;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) next[j].load_once(p.x, row_at(m0) * p.xs + cols.at[j]);
+    for (; m0 < p.M; m0 += static_cast<int64_t>(gridDim.x) * R) {
+        const int64_t m = row_at(m0), m1 = row_at(m0 + static_cast<int64_t>(gridDim.x) * R);
+        const bool real = R == 1 || m0 + r < p.M;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            x[j] = next[j];
+            next[j].load_once(p.x, m1 * p.xs + cols.at[j]);
+        }
+        float s[1] = {0.f}, mean = 0.f;
+        if (p.center) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < W; ++e) s[0] += !MASK || cols.fresh(j, e) ? x[j].get(e) : 0.f;
+            row_sums<T, 1>(s, red[turn][r], t);
+            turn ^= 1;
+            mean = s[0] / static_cast<float>(p.D);   // (a constant row has differences of 0)
+            s[0] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float d = !MASK || cols.fresh(j, e) ? x[j].get(e) - mean : 0.f;
+                s[0] = fmaf(d, d, s[0]);
+            }
+        row_sums<T, 1>(s, red[turn][r], t);
+        turn ^= 1;
+        const float rstd = 1.f / sqrtf(fmaf(s[0], per, p.eps));
+        if (!real) continue;
+        if (t == 0 && p.stats) {
+            p.stats[m] = mean;
+            p.stats[p.M + m] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (MASK && cols.from[j] >= p.D) continue;
+            float f[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) f[e] = fmaf((x[j].get(e) - mean) * rstd, w[W * j + e], b[W * j + e]);
+            Run<YB, W>::store(p.y, m * p.ys + cols.at[j], f);
+        }
+    }
+}
+
 // Rows that no work-group can hold, and rows of fewer than eight values: read
 // again for each step (from the L2).
 constexpr int kLongThreads = 512;
@@ -212,8 +285,10 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormPar
 }
 
 // ---- backward ------------------------------------------------------------------
-// A work-group takes every gridDim-th block of rows.  part: [work-group][2][D]
-// sums of dy xh and of dy.
+// A work-group takes every gridDim-th block of rows, the next one on its way
+// while one is summed.  part: [work-group][2][D] sums of dy xh and of dy.
+// Bound: HBM (32768 x 4096 in bf16 without d_residual 154 us, 5.2 TB/s; in
+// fp32 to bf16 223 us, 6.0 TB/s).
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormParams p) {
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
@@ -233,22 +308,37 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
     const float per = 1.f / static_cast<float>(p.D);
     const bool params = p.part != nullptr;
     int turn = 0;
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * R; m0 < p.M; m0 += static_cast<int64_t>(gridDim.x) * R) {
-        int64_t m = m0 + r;
-        const bool real = R == 1 || m < p.M;
-        if (!real) m = p.M - 1;
-        Run<XB, W> x[NV], skip[NV];
-        Run<YB, W> dy[NV];
+    // (rows past the end read the last one)
+    auto row_at = [&](int64_t m0) { return m0 + r < p.M ? m0 + r : p.M - 1; };
+    Run<XB, W> x[NV], skip[NV], next_x[NV], next_skip[NV];
+    Run<YB, W> dy[NV], next_dy[NV];
+    float next_mean = 0.f, next_rstd;
+    auto fetch = [&](int64_t m) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            x[j].load_once(p.x, m * p.xs + cols.at[j]);
-            dy[j].load_once(p.dy, m * p.dys + cols.at[j]);
+            next_x[j].load_once(p.x, m * p.xs + cols.at[j]);
+            next_dy[j].load_once(p.dy, m * p.dys + cols.at[j]);
         }
         if (p.d_residual) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) skip[j].load_once(p.d_residual, m * p.drs + cols.at[j]);
+            for (int j = 0; j < NV; ++j) next_skip[j].load_once(p.d_residual, m * p.drs + cols.at[j]);
         }
-        const float mean = p.center ? p.stats_in[m] : 0.f, rstd = p.stats_in[p.M + m];
+        if (p.center) next_mean = p.stats_in[m];
+        next_rstd = p.stats_in[p.M + m];
+    };
+    int64_t m0 = static_cast<int64_t>(blockIdx.x) * R;
+    fetch(row_at(m0));
+    for (; m0 < p.M; m0 += static_cast<int64_t>(gridDim.x) * R) {
+        const int64_t m = row_at(m0);
+        const bool real = R == 1 || m0 + r < p.M;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            x[j] = next_x[j];
+            dy[j] = next_dy[j];
+            skip[j] = next_skip[j];
+        }
+        const float mean = next_mean, rstd = next_rstd;
+        fetch(row_at(m0 + static_cast<int64_t>(gridDim.x) * R));
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -393,45 +483,75 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormParams p, int blocks
 // (a launch of 2^32 work-items or more runs a part of them without an error)
 dim3 grid_of_rows(int64_t n) { return dim3(static_cast<unsigned>(n < (1 << 21) ? n : 1 << 21)); }
 
-// Threads of a row and runs of a thread.  Forward: a wave to a row as long as
-// its registers hold it (eight runs), then work-groups.  Backward: 16 columns
-// a thread at the most, whose sums, weights and inputs take about 100
-// registers.
-template <bool XB, bool YB, bool MASK, int T, int NV>
-hipError_t forward_t(const NormParams& p, hipStream_t s) {
-    constexpr int R = rows_of(T);
-    hipLaunchKernelGGL((norm_forward_kernel<XB, YB, MASK, T, NV>), grid_of_rows((p.M + R - 1) / R),
-                       dim3(T < 256 ? 256 : T), 0, s, p);
+constexpr int64_t kLongRow = 16384;
+
+template <bool XB, bool YB, int T, int NV>
+hipError_t rows_t(const NormParams& p, hipStream_t s) {
+    constexpr int W = XB && YB ? 8 : 4, R = rows_of(T);
+    if (p.D == W * T * NV)
+        hipLaunchKernelGGL((norm_row_kernel<XB, YB, false, T, NV>), grid_of_rows((p.M + R - 1) / R), dim3(T < 256 ? 256 : T), 0, s, p);
+    else
+        hipLaunchKernelGGL((norm_row_kernel<XB, YB, true, T, NV>), grid_of_rows((p.M + R - 1) / R), dim3(T < 256 ? 256 : T), 0, s, p);
     return hipGetLastError();
 }
 
 template <bool XB, bool YB, int T, int NV>
-hipError_t forward_m(const NormParams& p, hipStream_t s) {
-    constexpr int W = XB && YB ? 8 : 4;
-    return p.D == W * T * NV ? forward_t<XB, YB, false, T, NV>(p, s) : forward_t<XB, YB, true, T, NV>(p, s);
+hipError_t forward_t(const NormParams& p, hipStream_t s) {
+    constexpr int W = XB && YB ? 8 : 4, R = rows_of(T);
+    const int64_t blocks = (p.M + R - 1) / R, fill = 2 * compute_units();
+    const dim3 grid(static_cast<unsigned>(blocks < fill ? blocks : fill));
+    if (p.D == W * T * NV) hipLaunchKernelGGL((norm_forward_kernel<XB, YB, false, T, NV>), grid, dim3(T < 256 ? 256 : T), 0, s, p);
+    else hipLaunchKernelGGL((norm_forward_kernel<XB, YB, true, T, NV>), grid, dim3(T < 256 ? 256 : T), 0, s, p);
+    return hipGetLastError();
 }
 
+// Threads of a row and runs of a thread: a wave to a row as long as its
+// registers hold it (eight runs), then work-groups.  Work-groups that stay,
+// with 16 columns a thread, from 2^25 values in rows of more than 1024 on
+// (8192 x 2048 in bf16: 20 us, all rows at once 17; 8192 x 4096: 31 and 36;
+// 32768 x 512: 22 and 17).
 template <bool XB, bool YB>
 hipError_t forward(const NormParams& p, hipStream_t s) {
-    constexpr int W = XB && YB ? 8 : 4;
-    const int64_t runs = (p.D + W - 1) / W;
-    if (p.D < W || runs > 4096) {
+    constexpr int W = XB && YB ? 8 : 4, NV = 16 / W;
+    if (p.D < 8 || p.D > kLongRow) {
         hipLaunchKernelGGL((norm_forward_long_kernel<XB, YB>), grid_of_rows(p.M), dim3(kLongThreads), 0, s, p);
         return hipGetLastError();
     }
-    if (runs <= 16) return forward_m<XB, YB, 16, 1>(p, s);
-    if (runs <= 64) return forward_m<XB, YB, 64, 1>(p, s);
-    if (runs <= 128) return forward_m<XB, YB, 64, 2>(p, s);
-    if (runs <= 256) return forward_m<XB, YB, 64, 4>(p, s);
-    if (runs <= 512) return forward_m<XB, YB, 64, 8>(p, s);
-    if (runs <= 1024) return forward_m<XB, YB, 256, 4>(p, s);
-    if (runs <= 2048) return forward_m<XB, YB, 256, 8>(p, s);
-    return forward_m<XB, YB, 1024, 4>(p, s);
+    if (p.D > 1024 && p.M * p.D >= (int64_t(1) << 25)) {
+        if (p.D <= 2048) return forward_t<XB, YB, 128, NV>(p, s);
+        if (p.D <= 4096) return forward_t<XB, YB, 256, NV>(p, s);
+        if (p.D <= 8192) return forward_t<XB, YB, 512, NV>(p, s);
+        return forward_t<XB, YB, 1024, NV>(p, s);
+    }
+    const int64_t runs = (p.D + W - 1) / W;
+    if (runs <= 16) return rows_t<XB, YB, 16, 1>(p, s);
+    if (runs <= 64) return rows_t<XB, YB, 64, 1>(p, s);
+    if (runs <= 128) return rows_t<XB, YB, 64, 2>(p, s);
+    if (runs <= 256) return rows_t<XB, YB, 64, 4>(p, s);
+    if (runs <= 512) return rows_t<XB, YB, 64, 8>(p, s);
+    if (runs <= 1024) return rows_t<XB, YB, 256, 4>(p, s);
+    if (runs <= 2048) return rows_t<XB, YB, 256, 8>(p, s);
+    return rows_t<XB, YB, 1024, 4>(p, s);
+}
+
+// Work-groups of the backward pass, each of which leaves a sum for each column:
+// one a compute unit with two blocks of rows at least (256 x 8192: 18 us, 20
+// with one block each), and two where the rows come to 2^24 values and fit, in
+// bf16 or up to 1024 columns (8192 x 4096 in bf16: 58 and 62 us, 4096 x 4096:
+// 42 and 39; 32768 x 4096 in fp32: 243 and 223).  Rows that are read in steps:
+// up to 64, for the parameters' sums.
+int64_t norm_parts_of(int64_t M, int64_t D, bool both_bf16) {
+    const bool in_steps = D < 8 || D > kLongRow;
+    const int64_t rows = D > 2048 || D < 8 ? 1 : D > 1024 ? 2 : D > 128 ? 4 : 16;
+    const bool two = M * D >= (int64_t(1) << 24) && (D <= 1024 || (both_bf16 && D <= 4096));
+    const int64_t most = in_steps ? 64 : (two ? 2 : 1) * compute_units();
+    const int64_t n = (M + 2 * rows - 1) / (2 * rows);
+    return n < most ? n : most;
 }
 
 template <bool XB, bool YB, bool MASK, int T, int NV>
 hipError_t backward_t(const NormParams& p, hipStream_t s) {
-    hipLaunchKernelGGL((norm_backward_kernel<XB, YB, MASK, T, NV>), dim3(static_cast<unsigned>(norm_parts(p.M, p.D))),
+    hipLaunchKernelGGL((norm_backward_kernel<XB, YB, MASK, T, NV>), dim3(static_cast<unsigned>(norm_parts_of(p.M, p.D, XB && YB))),
                        dim3(T < 256 ? 256 : T), 0, s, p);
     return hipGetLastError();
 }
@@ -441,8 +561,6 @@ hipError_t backward_m(const NormParams& p, hipStream_t s) {
     constexpr int W = XB && YB ? 8 : 4;
     return p.D == W * T * NV ? backward_t<XB, YB, false, T, NV>(p, s) : backward_t<XB, YB, true, T, NV>(p, s);
 }
-
-constexpr int64_t kLongRow = 16384;
 
 template <bool XB, bool YB>
 hipError_t backward(const NormParams& p, hipStream_t s) {
@@ -454,7 +572,7 @@ hipError_t backward(const NormParams& p, hipStream_t s) {
             if (e != hipSuccess || !p.part) return e;
         }
         hipLaunchKernelGGL((norm_params_long_kernel<XB, YB>),
-                           dim3(static_cast<unsigned>((p.D + 255) / 256), static_cast<unsigned>(norm_parts(p.M, p.D))), dim3(256), 0, s, p);
+                           dim3(static_cast<unsigned>((p.D + 255) / 256), static_cast<unsigned>(norm_parts_of(p.M, p.D, XB && YB))), dim3(256), 0, s, p);
         return hipGetLastError();
     }
     if (p.D <= 16 * W) return backward_m<XB, YB, 16, 1>(p, s);
@@ -468,14 +586,9 @@ hipError_t backward(const NormParams& p, hipStream_t s) {
 
 }  // namespace
 
-// Work-groups of the backward pass, each of which leaves a sum for each
-// column: as many as fill the card (less than a work-group of 256 threads four
-// times a compute unit leaves loads waiting), no more than there are rows.
 int norm_parts(int64_t M, int64_t D) {
-    const int64_t rows = D <= 128 ? 16 : D <= 1024 ? 4 : D <= 2048 ? 2 : 1;
-    const int64_t fill = D > kLongRow || D < 8 ? 64 : compute_units() * (D <= 4096 ? 4 : D <= 8192 ? 2 : 1);
-    const int64_t n = (M + rows - 1) / rows;
-    return static_cast<int>(n < fill ? n : fill);
+    const int64_t a = norm_parts_of(M, D, false), b = norm_parts_of(M, D, true);
+    return static_cast<int>(a > b ? a : b);
 }
 
 hipError_t launch_norm(const NormParams& p, bool x_bf16, bool y_bf16, hipStream_t s) {
@@ -489,7 +602,7 @@ hipError_t launch_norm_backward(const NormParams& p, bool x_bf16, bool y_bf16, h
     else e = y_bf16 ? backward<false, true>(p, s) : backward<false, false>(p, s);
     if (e != hipSuccess || !p.part) return e;
     hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<unsigned>((2 * p.D + 31) / 32)), dim3(1024), 0, s, p,
-                       norm_parts(p.M, p.D));
+                       static_cast<int>(norm_parts_of(p.M, p.D, x_bf16 && y_bf16)));
     return hipGetLastError();
 }
 
