@@ -1481,6 +1481,9 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, bias=None, label_sm
 
 # ---- the update of the weights ----------------------------------------------------
 
+_np = _ADAMW_TABLE = None      # numpy and the columns of CAdamWTensor that a step sets
+
+
 class AdamW:
     """The tensors that adamw_step updates and the numbers they share: params
     (fp32, contiguous, any shapes) and for each of them its states.  States in
@@ -1513,6 +1516,15 @@ class AdamW:
         import torch
         floats, codes = (torch.float32,), (torch.float8_e4m3fn, torch.uint8)
         state = floats if self.bits == 32 else codes
+        global _np, _ADAMW_TABLE
+        if _np is None:
+            import numpy
+            _np = numpy
+            _ADAMW_TABLE = numpy.dtype({
+                "names": ["grad", "grad_dtype"], "formats": ["u8", "i4"],
+                "offsets": [CAdamWTensor.grad.offset, CAdamWTensor.grad_dtype.offset],
+                "itemsize": ctypes.sizeof(CAdamWTensor)})
+        self._sizes = [p.numel() for p in self.params]
         self._c = (CAdamWTensor * n)()
         for i, p in enumerate(self.params):
             size = p.numel()
@@ -1575,13 +1587,20 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
         a.step = step
     if grad_scale is not None:
         a.grad_scale = _flat(grad_scale, "grad_scale", 1, (torch.float32,), dev)
-    # the call's own table: two threads may step the same tensors' gradients one after the other
+    # The call's own table.  (Whole columns of it at a time: a tensor's fields one
+    # by one cost half a microsecond each.)
     c = (CAdamWTensor * n)()
     ctypes.memmove(c, opt._c, ctypes.sizeof(c))
-    kinds = (torch.bfloat16, torch.float32)
-    for t, g in zip(c, grads):
-        t.grad = _flat(g, "grads", t.n, kinds, dev)
-        t.grad_dtype = GDN_DTYPE_BF16 if g.dtype is torch.bfloat16 else GDN_DTYPE_FP32
+    bf16, fp32 = torch.bfloat16, torch.float32
+    kinds = [g.dtype for g in grads]
+    if not ([g.numel() for g in grads] == opt._sizes and {bf16, fp32}.issuperset(kinds)
+            and all(g.is_contiguous() and g.get_device() == dev for g in grads)):
+        for i, g in enumerate(grads):
+            _flat(g, f"grads[{i}]", opt._sizes[i], (bf16, fp32), dev)
+    if n:
+        table = _np.frombuffer(c, dtype=_ADAMW_TABLE)
+        table["grad"] = [g.data_ptr() for g in grads]
+        table["grad_dtype"] = [k is bf16 for k in kinds]
     _check(lib().gdn_adamw_step(ctypes.byref(a), c, n, _raw_stream(stream, dev)))
 
 

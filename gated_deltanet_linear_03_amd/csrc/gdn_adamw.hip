@@ -37,6 +37,7 @@ constexpr int kLane = 4;                                    // adjacent elements
 static_assert(kAdamwBlock == kLane * kWave, "a wave is a block of the 8-bit states");
 constexpr int kRounds = 4;                                  // blocks that a wave has in flight
 constexpr int kChunk = kThreads * kLane * kRounds;          // elements of a work-group
+static_assert((kChunk & (kChunk - 1)) == 0, "a chunk does not cross a multiple of 2^32");
 
 struct Launch {
     AdamwParams p;
@@ -142,7 +143,7 @@ struct Step {
     float f_b1, f_b2, f_rest1, f_rest2, low_b1, low_rest1;  // in 32 bits, and what is left
     float lr, eps, decay, c1, c2;                           // c1 = lr / (1 - b1^k), c2 = 1 / sqrt(1 - b2^k)
     float grad_scale;
-    uint32_t key;                                           // of the random bits
+    uint32_t key;                                           // of the random bits, with the index's upper word
 };
 
 // m' and r = sqrt(v') to 2^-45 of themselves (r: one of Newton's steps from the
@@ -251,8 +252,7 @@ struct Elements {
     }
 
     __device__ __forceinline__ static uint32_t random(const Step& s, int64_t at) {
-        const uint32_t high = mix(static_cast<uint32_t>(static_cast<uint64_t>(at) >> 32));   // (0 for 0)
-        return mix(s.key + high + static_cast<uint32_t>(at) * 0x9E3779B1u);
+        return mix(s.key + static_cast<uint32_t>(at) * 0x9E3779B1u);
     }
 
     // the codes of the new states, and their scales
@@ -417,6 +417,7 @@ __global__ __launch_bounds__(kThreads, 5) void adamw_kernel(Launch a) {
     s.c2 = 1.f / sqrtf(-expm1f(static_cast<float>(k) * p.log_beta2));
     s.key = mix(mix(p.seed + static_cast<uint32_t>(k) * 0x9E3779B1u) + static_cast<uint32_t>(a.index[i]) * 0x9E3779B1u);
     const int64_t base = (b - a.first[i]) * kChunk;
+    s.key += mix(static_cast<uint32_t>(static_cast<uint64_t>(base) >> 32));   // (one for all of the chunk)
     if (t.grad_dtype == GDN_DTYPE_BF16) chunk<EIGHT, true>(t, s, base);
     else chunk<EIGHT, false>(t, s, base);
 }
