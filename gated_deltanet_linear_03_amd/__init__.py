@@ -1190,12 +1190,17 @@ def recur_decode(rec: Recur, x, a, b, z, state, state_slots=None, in_place=True,
 
 # ---- the linear layer with its epilogue ---------------------------------------
 
+_CODES = {}         # torch's dtypes to GDN_DTYPE_*, once the module is loaded
+
+
 def _float_code(dtype, name):
+    code = _CODES.get(dtype)
+    if code is not None:
+        return code
     import torch
-    if dtype == torch.bfloat16:
-        return GDN_DTYPE_BF16
-    if dtype == torch.float32:
-        return GDN_DTYPE_FP32
+    _CODES.update({torch.bfloat16: GDN_DTYPE_BF16, torch.float32: GDN_DTYPE_FP32})
+    if dtype in _CODES:
+        return _CODES[dtype]
     raise ValueError(f"{name}: bfloat16 or float32 needed, not {dtype}")
 
 
@@ -1538,6 +1543,13 @@ class AdamW:
             if self.copies[i] is not None:
                 c.copy = _flat(self.copies[i], f"copies[{i}]", size, (torch.bfloat16,), dev)
             c.weight_decay = self.weight_decay[i]
+        # what a step writes, each byte once
+        spans = sorted((t.data_ptr(), t.numel() * t.element_size(), f"{k}[{i}]")
+                       for k in ("params", "copies", "m", "v", "m_scale", "v_scale")
+                       for i, t in enumerate(getattr(self, k)) if t is not None and t.numel())
+        for (a, na, x), (b, _, y) in zip(spans, spans[1:]):
+            if a + na > b:
+                raise ValueError(f"{x} and {y}: share memory")
 
 
 def _flat(t, name, n, dtypes, dev):
@@ -1564,8 +1576,8 @@ def adamw_states(params, bits=32):
 
 
 def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
-    """One AdamW step of all of opt's tensors: grads, bf16 or fp32 of the
-    parameters' sizes, contiguous.  lr: a number, or a one-element fp32 device
+    """One AdamW step of opt's tensors: grads, bf16 or fp32 of the parameters'
+    sizes, contiguous (None: that tensor is left as it is).  lr: a number, or a one-element fp32 device
     tensor; step: the step's number, from 1 on, or a one-element int32 device
     tensor: a captured step reads those at every replay.  grad_scale: a
     one-element fp32 device tensor, a factor of every gradient; when it is not
@@ -1592,6 +1604,9 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
     c = (CAdamWTensor * n)()
     ctypes.memmove(c, opt._c, ctypes.sizeof(c))
     bf16, fp32 = torch.bfloat16, torch.float32
+    none = [i for i, g in enumerate(grads) if g is None]
+    if none:
+        grads = [opt.params[i] if g is None else g for i, g in enumerate(grads)]     # (whose n is 0)
     kinds = [g.dtype for g in grads]
     if not ([g.numel() for g in grads] == opt._sizes and {bf16, fp32}.issuperset(kinds)
             and all(g.is_contiguous() and g.get_device() == dev for g in grads)):
@@ -1601,6 +1616,8 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
         table = _np.frombuffer(c, dtype=_ADAMW_TABLE)
         table["grad"] = [g.data_ptr() for g in grads]
         table["grad_dtype"] = [k is bf16 for k in kinds]
+        for i in none:
+            c[i].n = 0
     _check(lib().gdn_adamw_step(ctypes.byref(a), c, n, _raw_stream(stream, dev)))
 
 

@@ -18,8 +18,8 @@
 // otherwise than the formula does, each of them by a whole step.  So the
 // scales come from the largest value in 64 bits, and a block with a value that
 // lies nearer to its border than 32 bits can tell (one or two in a hundred)
-// takes its codes from 64 bits.  (All of them in 64 bits: the vector units
-// bind, 235 M elements take 948 us.)
+// takes them from 64 bits: 269 M elements take 830 us, 948 with all of them in
+// 64 bits and 745 with none.
 //
 // Bound: HBM.  Each element is read and written once: 28 bytes with 32-bit
 // states, a bf16 gradient and a bf16 copy, 16 with 8-bit states.  A wave's 64
@@ -111,32 +111,6 @@ __device__ __forceinline__ float wave_max(float v) {
     return __uint_as_float(__builtin_amdgcn_readlane(x, 63));
 }
 
-// The largest of the lanes' x / 448 (x >= 0, NaN does not count), rounded once:
-// of those that are the largest in 32 bits the largest in 64.
-__device__ __forceinline__ float block_scale(double x) {
-    const float f = fmaxf(static_cast<float>(x), 0.f), top = wave_max(f);
-    if (!(top < __builtin_inff())) return top;
-    // (next to nothing counts as nothing: the ratios stay finite)
-    if (top < 0x1p-100f) return 0.f;
-    uint64_t who = __ballot(f == top);
-    double most = 0.0;
-    while (who) {                                           // (one round but for ties)
-        const int lane = __builtin_ctzll(who);
-        who &= who - 1;
-        const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(x));
-        const uint64_t b = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits >> 32), lane))) << 32 |
-                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits), lane));
-        most = fmax(most, __longlong_as_double(static_cast<long long>(b)));
-    }
-    return static_cast<float>(most * (1.0 / 448));
-}
-
-// 1 / s to 2^-45 (0 for 0)
-__device__ __forceinline__ double inverse(float s) {
-    const double x = __builtin_amdgcn_rcpf(s);
-    return s > 0.f ? x * fma(-static_cast<double>(s), x, 2.0) : 0.0;
-}
-
 // what a step's elements have in common
 struct Step {
     double b1, b2, rest1, rest2;                            // beta and 1 - beta
@@ -146,16 +120,66 @@ struct Step {
     uint32_t key;                                           // of the random bits, with the index's upper word
 };
 
-// m' and r = sqrt(v') to 2^-45 of themselves (r: one of Newton's steps from the
-// root in 32 bits)
+// m' and v' in 64 bits, each operation rounded by itself: beta1 = 0.9 makes m' =
+// (9 m + g) / 10, which is a short number every fifth time, and then the ratio
+// to the scale can lie on a border to the bit.
 __device__ __forceinline__ double new_m(const Step& s, float m0, float g) {
-    return fma(s.b1, static_cast<double>(m0), s.rest1 * g);
+#pragma clang fp contract(off)
+    const double a = s.b1 * static_cast<double>(m0), b = s.rest1 * static_cast<double>(g);
+    return a + b;
 }
+__device__ __forceinline__ double new_v(const Step& s, float v0, float g) {
+#pragma clang fp contract(off)
+    const double a = s.b2 * static_cast<double>(v0), b = s.rest2 * static_cast<double>(g) * static_cast<double>(g);
+    return a + b;
+}
+// sqrt(v') to its last bit or next to it: two of Newton's steps from the root in 32 bits
 __device__ __forceinline__ double new_r(const Step& s, float v0, float g) {
-    const double v1 = fma(s.b2, static_cast<double>(v0), s.rest2 * g * g);
+    const double v1 = new_v(s, v0, g);
     const float r = __builtin_amdgcn_sqrtf(static_cast<float>(v1));
-    const double r0 = r;
-    return r > 0.f && r < __builtin_inff() ? fma(fma(-r0, r0, v1), 0.5 * static_cast<double>(__builtin_amdgcn_rcpf(r)), r0) : r0;
+    if (!(r > 0.f && r < __builtin_inff())) return r;
+    const double half = 0.5 * static_cast<double>(__builtin_amdgcn_rcpf(r)), r0 = r;
+    const double r1 = fma(fma(-r0, r0, v1), half, r0);
+    return fma(fma(-r1, r1, v1), half, r1);
+}
+
+// The largest of a wave's values / 448, rounded once.  size: the lane's
+// magnitudes in 32 bits (NaN does not count); old, g: what they come from.
+// Those within 2^-20 of the largest are looked at in 64 bits: one as a rule.
+template <bool R>
+__device__ __forceinline__ float block_scale(const Step& s, const float (&size)[kLane], const float (&old)[kLane], const float (&g)[kLane]) {
+    static_assert(kLane == 4, "four values");
+    const float t = fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], fmaxf(size[3], 0.f))), top = wave_max(t);
+    if (!(top < __builtin_inff())) return top;
+    // (next to nothing counts as nothing: the ratios stay finite)
+    if (top < 0x1p-100f) return 0.f;
+    const float least = top * (1.f - 0x1p-20f);
+    uint64_t who = __ballot(t >= least);
+    double most = 0.0;
+    uint32_t left = 0;
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) left |= size[e] >= least ? 1u << e : 0u;
+    while (left) {
+        const int e = __builtin_ctz(left);
+        left &= left - 1;
+        float o = old[0], q = g[0];
+#pragma unroll
+        for (int k = 1; k < kLane; ++k) {
+            o = e == k ? old[k] : o;
+            q = e == k ? g[k] : q;
+        }
+        most = fmax(most, R ? new_r(s, o, q) : fabs(new_m(s, o, q)));
+    }
+    double all = 0.0;
+    while (who) {
+        const int lane = __builtin_ctzll(who);
+        who &= who - 1;
+        const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(most));
+        const uint64_t b = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits >> 32), lane))) << 32 |
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits), lane));
+        all = fmax(all, __longlong_as_double(static_cast<long long>(b)));
+    }
+    return static_cast<float>(all * (1.0 / 448));
 }
 
 template <bool EIGHT, bool GB, bool FULL>
@@ -236,7 +260,7 @@ struct Elements {
                 v0[e] = v[e] * vs;
                 v0[e] *= v0[e];
                 // to its last bit also where its terms cancel: with what the
-                // product and the factors have lost
+                // product and the factors have lost (a multiply-add rounds the other)
                 const float gg = s.f_rest1 * g[e], q = fmaf(s.f_b1, m0[e], gg);
                 m[e] = q + fmaf(s.low_b1, m0[e], fmaf(s.low_rest1, g[e], fmaf(s.f_rest1, g[e], -gg)));
                 r = __builtin_amdgcn_sqrtf(fmaf(s.f_b2, v0[e], s.f_rest2 * g[e] * g[e]));
@@ -258,14 +282,11 @@ struct Elements {
     // the codes of the new states, and their scales
     __device__ __forceinline__ void encode(const Step& s, int64_t at) {
         // (elements past the end are zeros)
-        float m1 = m0[0], gm = g[0], tm = fabsf(m[0]), v1 = v0[0], gv = g[0], tv = v[0];
+        float size[kLane];
 #pragma unroll
-        for (int e = 1; e < kLane; ++e) {
-            if (fabsf(m[e]) > tm || tm != tm) { m1 = m0[e]; gm = g[e]; tm = fabsf(m[e]); }
-            if (v[e] > tv || tv != tv) { v1 = v0[e]; gv = g[e]; tv = v[e]; }
-        }
-        sm = uniform_f32(block_scale(fabs(new_m(s, m1, gm))));
-        sv = uniform_f32(block_scale(new_r(s, v1, gv)));
+        for (int e = 0; e < kLane; ++e) size[e] = fabsf(m[e]);
+        sm = uniform_f32(block_scale<false>(s, size, m0, g));
+        sv = uniform_f32(block_scale<true>(s, v, v0, g));
         const float um = sm > 0.f ? __builtin_amdgcn_rcpf(sm) : 0.f, uv = sv > 0.f ? __builtin_amdgcn_rcpf(sv) : 0.f;
         new_qm = new_qv = border = 0;
 #pragma unroll
@@ -293,10 +314,10 @@ struct Elements {
             const float old = __builtin_amdgcn_cvt_f32_fp8((of_m ? qm : qv) >> (8 * e), 0) * (of_m ? ms : vs);
             uint32_t code;
             if (of_m) {
-                code = e4m3(new_m(s, old, grad) * inverse(sm), h & 0xFFFFu);
+                code = e4m3(sm > 0.f ? new_m(s, old, grad) / static_cast<double>(sm) : 0.0, h & 0xFFFFu);
             } else {
-                const double r = new_r(s, old * old, grad);
-                code = e4m3(r * inverse(sv), h >> 16);
+                const double r = sqrt(new_v(s, old * old, grad));
+                code = e4m3(sv > 0.f ? r / static_cast<double>(sv) : 0.0, h >> 16);
                 if (code == 0 && r > 0.0 && sv > 0.f) code = 1;
             }
             static_cast<uint8_t*>(of_m ? t.m : t.v)[at + e] = static_cast<uint8_t>(code);

@@ -852,7 +852,8 @@ gdn_status gdn_linear_cross_entropy_backward(const gdn_loss_io* io, const gdn_lo
  * the new values / 448 (0 where that is below 2^-100).  A value / scale is
  * rounded up or down at random, up when its fraction of a step of the format
  * plus u / 65536 reaches 1, so that its expected value is kept; a positive r is
- * not rounded to 0.  u: for m the low and for r the high 16 bits of
+ * not rounded to 0.  (m', r, and their quotients by the scales decide that in 64
+ * bits, from m and v in 32.)  u: for m the low and for r the high 16 bits of
  *   mix(key + mix(i >> 32) + i * 0x9E3779B1),
  *   key = mix(mix(seed + k * 0x9E3779B1) + t * 0x9E3779B1)
  * of element i of tensor t, in 32 bits, mix the finaliser of MurmurHash3.  The

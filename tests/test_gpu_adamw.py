@@ -251,6 +251,35 @@ def test_nothing_outside():
             assert float(sm[0]) == float(sm[5]) == float(sv[0]) == float(sv[5]) == 0.5
 
 
+def test_tensors_without_a_gradient():
+    """They are left as they are, and the others' random bits do not move."""
+    sizes = [300, 5, 1000]
+    p, grads, states = tensors(sizes, 51, 8, FP32, True)
+    opt = gdn.AdamW(p, **states, weight_decay=0.1, seed=6)
+    before = copy_of(p, states)
+    gdn.adamw_step(opt, [grads[0], None, grads[2]], lr=1e-3, step=4)
+    assert torch.equal(p[1], before[0][1]) and all(torch.equal(states[k][1].float(), before[1][k][1].float()) for k in before[1])
+    q, _, other = tensors(sizes, 51, 8, FP32, True)
+    full = gdn.AdamW(q, **other, weight_decay=0.1, seed=6)
+    gdn.adamw_step(full, grads, lr=1e-3, step=4)
+    for i in (0, 2):
+        assert torch.equal(p[i], q[i]) and all(torch.equal(states[k][i].float(), other[k][i].float()) for k in before[1])
+
+
+def test_shared_memory_is_refused():
+    """The same tensor twice, and a state inside another's."""
+    a, b = torch.zeros(100, device="cuda"), torch.zeros(100, device="cuda")
+    st = gdn.adamw_states([a, b])
+    with pytest.raises(ValueError, match="share memory"):
+        gdn.AdamW([a, a], **st)
+    with pytest.raises(ValueError, match="share memory"):
+        gdn.AdamW([a, b], m=[st["m"][0], st["m"][0]], v=st["v"])
+    flat = torch.zeros(150, device="cuda")
+    with pytest.raises(ValueError, match="share memory"):
+        gdn.AdamW([flat[:100], flat[50:]], **st)
+    gdn.AdamW([flat[:100], flat[100:]], **gdn.adamw_states([flat[:100], flat[100:]]))
+
+
 def test_binding_refuses():
     p = [torch.zeros(10, device="cuda")]
     st = gdn.adamw_states(p)
