@@ -18,7 +18,7 @@
 // otherwise than the formula does, each of them by a whole step.  So the
 // scales come from the largest value in 64 bits, and a block with a value that
 // lies nearer to its border than 32 bits can tell (one or two in a hundred)
-// takes them from 64 bits: 269 M elements take 830 us, 948 with all of them in
+// takes them from 64 bits: 269 M elements take 783 us, 948 with all of them in
 // 64 bits and 745 with none.
 //
 // Bound: HBM.  Each element is read and written once: 28 bytes with 32-bit
@@ -143,43 +143,66 @@ __device__ __forceinline__ double new_r(const Step& s, float v0, float g) {
     return fma(fma(-r1, r1, v1), half, r1);
 }
 
-// The largest of a wave's values / 448, rounded once.  size: the lane's
-// magnitudes in 32 bits (NaN does not count); old, g: what they come from.
-// Those within 2^-20 of the largest are looked at in 64 bits: one as a rule.
-template <bool R>
-__device__ __forceinline__ float block_scale(const Step& s, const float (&size)[kLane], const float (&old)[kLane], const float (&g)[kLane]) {
-    static_assert(kLane == 4, "four values");
-    const float t = fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], fmaxf(size[3], 0.f))), top = wave_max(t);
-    if (!(top < __builtin_inff())) return top;
-    // (next to nothing counts as nothing: the ratios stay finite)
-    if (top < 0x1p-100f) return 0.f;
-    const float least = top * (1.f - 0x1p-20f);
-    uint64_t who = __ballot(t >= least);
-    double most = 0.0;
-    uint32_t left = 0;
-#pragma unroll
-    for (int e = 0; e < kLane; ++e) left |= size[e] >= least ? 1u << e : 0u;
-    while (left) {
-        const int e = __builtin_ctz(left);
-        left &= left - 1;
-        float o = old[0], q = g[0];
-#pragma unroll
-        for (int k = 1; k < kLane; ++k) {
-            o = e == k ? old[k] : o;
-            q = e == k ? g[k] : q;
+// What a wave's blocks' scales come from, in the lanes 2 i (m) and 2 i + 1 (r)
+// of block i: the largest magnitude in 32 bits, and the state's value and the
+// gradient behind it.  The scales' 64 bits are then computed once for all of
+// them (block by block 269 M elements take 830 us).
+struct Largest {
+    float top, old, grad;
+
+    __device__ __forceinline__ static float of(const float (&x)[kLane], int e, int lane) {
+        const float a = x[0], b = x[1], c = x[2], d = x[3];
+        const float lo = e & 1 ? b : a, hi = e & 1 ? d : c, v = e & 2 ? hi : lo;
+        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+    }
+    __device__ __forceinline__ static float put(float v, int lane, float to) {
+        return static_cast<int>(__lane_id()) == lane ? v : to;
+    }
+
+    // size: the lane's magnitudes (NaN does not count); x, g: what they come from
+    template <bool R>
+    __device__ __forceinline__ void offer(const Step& s, int at, const float (&size)[kLane], const float (&x)[kLane], const float (&g)[kLane]) {
+        static_assert(kLane == 4, "four values");
+        const float t = fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], fmaxf(size[3], 0.f))), most = wave_max(t);
+        // those that 32 bits do not tell from the largest: one as a rule
+        const float least = most * (1.f - 0x1p-20f);
+        const uint32_t mine = (size[0] >= least ? 1u : 0u) | (size[1] >= least ? 2u : 0u) | (size[2] >= least ? 4u : 0u) | (size[3] >= least ? 8u : 0u);
+        uint64_t who = __ballot(t >= least);
+        int lane = __builtin_ctzll(who | 1ull << 63);
+        uint32_t bits = __builtin_amdgcn_readlane(mine, lane);
+        int e = __builtin_ctz(bits | 16u) % kLane;
+        float x1 = of(x, e, lane), g1 = of(g, e, lane);
+        if ((who & (who - 1)) != 0 || (bits & (bits - 1)) != 0) {
+            double best = -1.0;
+            while (who != 0 && most > 0.f) {
+                lane = __builtin_ctzll(who);
+                who &= who - 1;
+                bits = __builtin_amdgcn_readlane(mine, lane);
+                while (bits) {
+                    e = __builtin_ctz(bits);
+                    bits &= bits - 1;
+                    const float x2 = of(x, e, lane), g2 = of(g, e, lane);
+                    const double v = R ? new_r(s, x2, g2) : fabs(new_m(s, x2, g2));
+                    if (v > best) { best = v; x1 = x2; g1 = g2; }
+                }
+            }
         }
-        most = fmax(most, R ? new_r(s, o, q) : fabs(new_m(s, o, q)));
+        top = put(most, at, top);
+        old = put(x1, at, old);
+        grad = put(g1, at, grad);
     }
-    double all = 0.0;
-    while (who) {
-        const int lane = __builtin_ctzll(who);
-        who &= who - 1;
-        const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(most));
-        const uint64_t b = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits >> 32), lane))) << 32 |
-                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(bits), lane));
-        all = fmax(all, __longlong_as_double(static_cast<long long>(b)));
+
+    // the scale of this lane's block and kind
+    __device__ __forceinline__ float scale(const Step& s, int lane) const {
+        const double m = fabs(new_m(s, old, grad)), r = new_r(s, old, grad);
+        const float v = static_cast<float>((lane % 2 ? r : m) * (1.0 / 448));
+        // (next to nothing counts as nothing: the ratios stay finite)
+        return !(top < __builtin_inff()) ? top : top < 0x1p-100f ? 0.f : v;
     }
-    return static_cast<float>(all * (1.0 / 448));
+};
+
+__device__ __forceinline__ float from_lane(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 
 template <bool EIGHT, bool GB, bool FULL>
@@ -279,14 +302,19 @@ struct Elements {
         return mix(s.key + static_cast<uint32_t>(at) * 0x9E3779B1u);
     }
 
-    // the codes of the new states, and their scales
-    __device__ __forceinline__ void encode(const Step& s, int64_t at) {
+    __device__ __forceinline__ void offer(const Step& s, int block, Largest* l) const {
         // (elements past the end are zeros)
         float size[kLane];
 #pragma unroll
         for (int e = 0; e < kLane; ++e) size[e] = fabsf(m[e]);
-        sm = uniform_f32(block_scale<false>(s, size, m0, g));
-        sv = uniform_f32(block_scale<true>(s, v, v0, g));
+        l->offer<false>(s, 2 * block, size, m0, g);
+        l->offer<true>(s, 2 * block + 1, v, v0, g);
+    }
+
+    // the codes of the new states
+    __device__ __forceinline__ void encode(const Step& s, int64_t at, float new_sm, float new_sv) {
+        sm = new_sm;
+        sv = new_sv;
         const float um = sm > 0.f ? __builtin_amdgcn_rcpf(sm) : 0.f, uv = sv > 0.f ? __builtin_amdgcn_rcpf(sv) : 0.f;
         new_qm = new_qv = border = 0;
 #pragma unroll
@@ -324,14 +352,8 @@ struct Elements {
         }
     }
 
-    // all of a wave's lanes, nv of the elements of each
-    __device__ __forceinline__ void store(const gdn_adamw_tensor& t, int64_t at, int nv, int lane) {
-        if constexpr (EIGHT) {
-            if (lane == 0) {
-                t.m_scale[at / kAdamwBlock] = sm;
-                t.v_scale[at / kAdamwBlock] = sv;
-            }
-        }
+    // nv of the elements of each lane
+    __device__ __forceinline__ void store_param(const gdn_adamw_tensor& t, int64_t at, int nv) const {
         if constexpr (FULL) {
             const U4 a = {__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]), __float_as_uint(p[3])};
             __builtin_nontemporal_store(a, reinterpret_cast<U4*>(t.param + at));
@@ -341,6 +363,24 @@ struct Elements {
                               __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2))};
                 __builtin_nontemporal_store(c, reinterpret_cast<U2*>(static_cast<uint16_t*>(t.copy) + at));
             }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) {
+                if (e >= nv) continue;
+                t.param[at + e] = p[e];
+                if (t.copy) static_cast<uint16_t*>(t.copy)[at + e] = f32_to_bf16_bits(p[e]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store_state(const gdn_adamw_tensor& t, int64_t at, int nv, int lane) const {
+        if constexpr (EIGHT) {
+            if (lane == 0) {
+                t.m_scale[at / kAdamwBlock] = sm;
+                t.v_scale[at / kAdamwBlock] = sv;
+            }
+        }
+        if constexpr (FULL) {
             if constexpr (EIGHT) {
                 __builtin_nontemporal_store(new_qm, reinterpret_cast<U1*>(static_cast<uint8_t*>(t.m) + at));
                 __builtin_nontemporal_store(new_qv, reinterpret_cast<U1*>(static_cast<uint8_t*>(t.v) + at));
@@ -354,8 +394,6 @@ struct Elements {
 #pragma unroll
             for (int e = 0; e < kLane; ++e) {
                 if (e >= nv) continue;
-                t.param[at + e] = p[e];
-                if (t.copy) static_cast<uint16_t*>(t.copy)[at + e] = f32_to_bf16_bits(p[e]);
                 if constexpr (EIGHT) {
                     static_cast<uint8_t*>(t.m)[at + e] = static_cast<uint8_t>(new_qm >> (8 * e));
                     static_cast<uint8_t*>(t.v)[at + e] = static_cast<uint8_t>(new_qv >> (8 * e));
@@ -368,24 +406,36 @@ struct Elements {
     }
 };
 
+template <int I>
+struct Int { static constexpr int value = I; };
+
 template <bool EIGHT, bool GB>
 __device__ __forceinline__ void chunk(const gdn_adamw_tensor& t, const Step& s, int64_t base) {
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     // a wave's blocks follow one another
     const int64_t at0 = base + static_cast<int64_t>(wave) * kRounds * kAdamwBlock + kLane * lane;
     if (base + kChunk <= t.n) {
+        // (indices known to the compiler from the start: the blocks stay in registers)
+        static_assert(kRounds == 4, "four blocks");
+        auto each = [](auto f) __attribute__((always_inline)) { f(Int<0>{}); f(Int<1>{}); f(Int<2>{}); f(Int<3>{}); };
         Elements<EIGHT, GB, true> x[kRounds];
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) x[i].load(t, at0 + i * kAdamwBlock, kLane);
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-            x[i].update(s);
-            if constexpr (EIGHT) x[i].encode(s, at0 + i * kAdamwBlock);
-            x[i].store(t, at0 + i * kAdamwBlock, kLane, lane);
-        }
+        Largest l{0.f, 0.f, 0.f};
+        each([&](auto i) __attribute__((always_inline)) { x[i.value].load(t, at0 + i.value * kAdamwBlock, kLane); });
+        each([&](auto i) __attribute__((always_inline)) {
+            auto& b = x[i.value];
+            b.update(s);
+            b.store_param(t, at0 + i.value * kAdamwBlock, kLane);
+            if constexpr (EIGHT) b.offer(s, i.value, &l);
+            else b.store_state(t, at0 + i.value * kAdamwBlock, kLane, lane);
+        });
         if constexpr (EIGHT) {
-#pragma unroll
-            for (int i = 0; i < kRounds; ++i) x[i].settle(t, s, at0 + i * kAdamwBlock);
+            const float scale = l.scale(s, lane);
+            each([&](auto i) __attribute__((always_inline)) {
+                auto& b = x[i.value];
+                b.encode(s, at0 + i.value * kAdamwBlock, from_lane(scale, 2 * i.value), from_lane(scale, 2 * i.value + 1));
+                b.store_state(t, at0 + i.value * kAdamwBlock, kLane, lane);
+            });
+            each([&](auto i) __attribute__((always_inline)) { x[i.value].settle(t, s, at0 + i.value * kAdamwBlock); });
         }
         return;
     }
@@ -396,8 +446,14 @@ __device__ __forceinline__ void chunk(const gdn_adamw_tensor& t, const Step& s, 
         Elements<EIGHT, GB, false> x;
         x.load(t, at, nv);
         x.update(s);
-        if constexpr (EIGHT) x.encode(s, at);
-        x.store(t, at, nv, lane);
+        x.store_param(t, at, nv);
+        if constexpr (EIGHT) {
+            Largest l{0.f, 0.f, 0.f};
+            x.offer(s, 0, &l);
+            const float scale = l.scale(s, lane);
+            x.encode(s, at, from_lane(scale, 0), from_lane(scale, 1));
+        }
+        x.store_state(t, at, nv, lane);
         if constexpr (EIGHT) {
             x.border &= ((1u << nv) - 1) * 0x11u;           // (none of elements past the end)
             x.settle(t, s, at);
@@ -406,7 +462,7 @@ __device__ __forceinline__ void chunk(const gdn_adamw_tensor& t, const Step& s, 
 }
 
 template <bool EIGHT>
-__global__ __launch_bounds__(kThreads, 5) void adamw_kernel(Launch a) {
+__global__ __launch_bounds__(kThreads, EIGHT ? 4 : 5) void adamw_kernel(Launch a) {
     const AdamwParams& p = a.p;
     // the gradients' factor decides whether there is a step at all
     const float gs = p.grad_scale ? *p.grad_scale : 1.f;
