@@ -70,7 +70,6 @@ struct LossProduct : GemmProduct {
     // forward
     Part* part;                               // [column tiles][M]
     float* totals;                            // [column tiles][M] sums of the logits, or NULL
-    float* logit;                             // [M] the target's
     // backward
     GemmProduct out;                          // dl: rows, columns (padded with zeros), address and stride
     float* columns;                           // [row tiles][V] sums of dl, or NULL
@@ -100,13 +99,27 @@ __device__ __forceinline__ void finish_logits(const LossProduct& p, f32x4 (&acc)
         }
 }
 
+// Which of a lane's columns first + 16 j + e (0 .. WN - 1) is row m's target; -1: none
+template <typename S>
+__device__ __forceinline__ int column_of(const LossProduct& p, int64_t target, int64_t first) {
+    const int64_t at = target - p.v0 - first;
+    return at >= 0 && at < S::WN && at % 16 < 4 ? static_cast<int>(at) : -1;
+}
+
+// What an epilogue reads of its rows is requested before the last slices are
+// multiplied, all rows at once (1537 x 50001 x 1000, forward and backward: 751
+// us row by row, 745 so).
+
 // ---- forward -------------------------------------------------------------------
 // A tile's rows to their parts: each lane its 4 TN logits of a row, the four
 // lanes that share the row, then the waves that do, through LDS.
 template <typename S>
 struct RowParts {
     int64_t m0, n0;
-    __device__ __forceinline__ void init(const LossProduct&, int64_t m, int64_t n, int, int) { m0 = m; n0 = n; }
+    __device__ __forceinline__ void init(const LossProduct&, int64_t m, int64_t n, int, int) {
+        m0 = m;
+        n0 = n;
+    }
     __device__ __forceinline__ void fetch(const LossProduct&, int) {}
     __device__ __forceinline__ void run(const LossProduct& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
         Part* const red = reinterpret_cast<Part*>(shared);                         // [NWN][BM]
@@ -140,15 +153,6 @@ struct RowParts {
                     for (int e = 0; e < 4; ++e) s += first + 16 * j + e < p.N ? acc[i][j][e] : 0.f;
                 s = quad_sum(s);
                 if (lq == 0) tot[wn * S::BM + r] = s;
-            }
-            // the target's logit, where this lane has it
-            const int64_t t = m < p.M ? target_of(p.rows, m) - p.v0 - first : -1;
-            if (t >= 0 && t < S::WN) {
-#pragma unroll
-                for (int j = 0; j < S::TN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (t == 16 * j + e && first + t < p.N) p.logit[m] = acc[i][j][e];
             }
         }
         __syncthreads();
@@ -189,7 +193,6 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void loss_few_kernel(LossProd
     const int64_t groups = (p.N + 15) / 16, all = static_cast<int64_t>(gridDim.x) * kFewWaves;
     const int64_t m = l16 < p.M ? l16 : p.M - 1;                                   // (rows past the end are never stored)
     const uint16_t* const arow = static_cast<const uint16_t*>(p.A) + m * p.lda;
-    const int64_t target = target_of(p.rows, m);
     const int steps = static_cast<int>((p.K + 63) / 64);
     Part mine{-__builtin_inff(), 0.f};
     float total = 0.f;
@@ -224,7 +227,6 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void loss_few_kernel(LossProd
             if (n >= p.N) { acc[e] = -__builtin_inff(); continue; }
             if (p.bias) acc[e] += p.bias[n];
             total += acc[e];
-            if (n + p.v0 == target && l16 < p.M) p.logit[l16] = acc[e];
         }
         a.top = fmaxf(fmaxf(acc[0], acc[1]), fmaxf(acc[2], acc[3])) * kLog2e;
         const float base = a.top == -__builtin_inff() ? 0.f : a.top;
@@ -257,12 +259,14 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void loss_few_kernel(LossProd
 }
 
 // A row's parts to its lse and loss: 16 rows a work-group, 64 threads each,
-// whose parts are joined in their order.
+// whose parts are joined in their order.  The target's logit is computed here,
+// from its row of w (looked for among a tile's logits it takes 1 us of a tile:
+// 4096 x 65536 x 64 148 instead of 124 us).
 constexpr int kJoinRows = 16, kJoinSlices = 64;
 
 __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(LossProduct p, int64_t tiles, float* loss, float* lse) {
     __shared__ Part red[kJoinSlices][kJoinRows];
-    __shared__ float tot[kJoinSlices][kJoinRows];
+    __shared__ float tot[kJoinSlices][kJoinRows], dot[kJoinSlices][kJoinRows];
     const int r = threadIdx.x % kJoinRows, sl = threadIdx.x / kJoinRows;
     const int64_t m = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
     Part a{-__builtin_inff(), 0.f};
@@ -275,13 +279,36 @@ __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(Loss
             for (int64_t t = sl; t < tiles; t += kJoinSlices) total += p.totals[t * p.M + m];
         }
     }
+    float hot = 0.f;
+    int64_t t = -1;
+    bool there = false;
+    if (m < p.M) {
+        t = target_of(p.rows, m);
+        there = loss && t != p.rows.ignore && t >= 0 && t < p.rows.V;
+    }
+    if (there) {
+        const uint16_t* const x = static_cast<const uint16_t*>(p.A) + m * p.lda;
+        const uint16_t* const w = static_cast<const uint16_t*>(p.B) + t * p.ldb;
+#pragma unroll 4
+        for (int64_t k = 8 * sl; k < p.K; k += 8 * kJoinSlices) {
+            const u32x4 q = *reinterpret_cast<const u32x4*>(x + k), v = *reinterpret_cast<const u32x4*>(w + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                hot = fmaf(__uint_as_float(q[e] << 16), __uint_as_float(v[e] << 16), hot);
+                hot = fmaf(__uint_as_float(q[e] & 0xFFFF0000u), __uint_as_float(v[e] & 0xFFFF0000u), hot);
+            }
+        }
+        if (sl == 0 && p.bias) hot += p.bias[t];
+    }
     red[sl][r] = a;
     tot[sl][r] = total;
+    dot[sl][r] = hot;
     for (int half = kJoinSlices / 2; half > 0; half /= 2) {
         __syncthreads();
         if (sl < half) {
             red[sl][r] = join(red[sl][r], red[sl + half][r]);
             tot[sl][r] += tot[sl + half][r];
+            dot[sl][r] += dot[sl + half][r];
         }
     }
     if (sl > 0 || m >= p.M) return;
@@ -289,17 +316,14 @@ __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(Loss
     const float l = (a.top + __builtin_amdgcn_logf(a.sum)) * kLn2;                  // (v_log_f32: base two)
     if (lse) lse[m] = l;
     if (!loss) return;
-    const int64_t t = target_of(p.rows, m);
     float out = 0.f;
-    if (t != p.rows.ignore) {
-        if (t < 0 || t >= p.rows.V) {
-            out = __builtin_nanf("");
-            if (p.rows.status) __hip_atomic_fetch_or(p.rows.status, GDN_STATUS_BAD_INDEX, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        } else {
-            const float e = p.rows.smooth;
-            out = (1.f - e) * (l - p.logit[m]) + p.rows.z * l * l;
-            if (e > 0.f) out += e * (l - tot[0][r] / static_cast<float>(p.rows.V));
-        }
+    if (there) {
+        const float e = p.rows.smooth;
+        out = (1.f - e) * (l - dot[0][r]) + p.rows.z * l * l;
+        if (e > 0.f) out += e * (l - tot[0][r] / static_cast<float>(p.rows.V));
+    } else if (t != p.rows.ignore) {
+        out = __builtin_nanf("");
+        if (p.rows.status) __hip_atomic_fetch_or(p.rows.status, GDN_STATUS_BAD_INDEX, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     loss[m] = out;
 }
@@ -309,45 +333,58 @@ __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(Loss
 // bf16 through LDS in whole rows.
 template <typename S>
 struct Gradient {
-    int64_t m0, n0;
+    int64_t m0, n0, first;
+    int wave, l16, at[S::TM];
+    float g[S::TM], lse[S::TM];
+    uint32_t counts = 0;                      // a bit for each row
     Store<S, true, true> store;
-    __device__ __forceinline__ void init(const LossProduct& p, int64_t m, int64_t n, int wave, int lane) {
+    __device__ __forceinline__ void init(const LossProduct& p, int64_t m, int64_t n, int w, int lane) {
         m0 = m;
         n0 = n;
+        wave = w;
+        l16 = lane % 16;
+        first = n0 + wave % S::NWN * S::WN + 4 * (lane / 16);
         store.init(p.out, m, n, wave, lane);
     }
-    __device__ __forceinline__ void fetch(const LossProduct&, int) {}
-    __device__ __forceinline__ void run(const LossProduct& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
-        const int l16 = lane % 16, lq = lane / 16, wn = wave % S::NWN;
-        const int64_t first = n0 + wn * S::WN + 4 * lq;
-        finish_logits<S>(p, acc, n0, wave, lane);
+    __device__ __forceinline__ void fetch(const LossProduct& p, int) {
+        int64_t t[S::TM];
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) {
-            const int64_t m = row_of<S>(m0, wave, i, l16);
-            int64_t t = -1;
-            if (m < p.M) t = target_of(p.rows, m);
-            const bool counts = m < p.M && t != p.rows.ignore && t >= 0 && t < p.rows.V;
-            float g = 0.f, l = 0.f;
-            if (counts) {
-                g = p.rows.dloss_one ? 1.f : p.rows.dloss[m] / *p.rows.scale;
-                l = p.rows.lse[m];
-            }
-            const float g1 = g / (1.f - p.rows.smooth);
-            const float c = g1 * fmaf(2.f * p.rows.z, l, 1.f), base = l * kLog2e, rest = g1 * p.rows.smooth / static_cast<float>(p.rows.V);
+            int64_t m = row_of<S>(m0, wave, i, l16);
+            m = m < p.M ? m : p.M - 1;
+            t[i] = target_of(p.rows, m);
+            lse[i] = p.rows.lse[m];
+            g[i] = p.rows.dloss[p.rows.dloss_one ? 0 : m];
+        }
+        const float scale = p.rows.dloss_one ? 1.f : *p.rows.scale;
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            counts |= row_of<S>(m0, wave, i, l16) < p.M && t[i] != p.rows.ignore && t[i] >= 0 && t[i] < p.rows.V ? 1u << i : 0u;
+            at[i] = column_of<S>(p, t[i], first);
+            g[i] = p.rows.dloss_one ? 1.f : g[i] / scale;
+        }
+    }
+    __device__ __forceinline__ void run(const LossProduct& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
+        const int lq = lane / 16, wn = wave % S::NWN;
+        finish_logits<S>(p, acc, n0, wave, lane);
+        const float smooth = p.rows.smooth, over = 1.f / (1.f - smooth), even = smooth / static_cast<float>(p.rows.V);
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+            const bool real = (counts >> i & 1u) != 0;
+            const float g1 = g[i] * over, c = g1 * fmaf(2.f * p.rows.z, lse[i], 1.f), base = lse[i] * kLog2e, rest = g1 * even;
 #pragma unroll
             for (int j = 0; j < S::TN; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float d = fmaf(c, __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLog2e, -base)), -rest);
-                    acc[i][j][e] = counts ? d : 0.f;
+                    acc[i][j][e] = real ? d : 0.f;
                 }
-            const int64_t at = t - p.v0 - first;
-            if (counts && at >= 0 && at < S::WN) {   // (few lanes: the target is one of V)
+            if (real && at[i] >= 0) {                // (few lanes: the target is one of V)
 #pragma unroll
                 for (int j = 0; j < S::TN; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (at == 16 * j + e) acc[i][j][e] -= g;
+                        if (at[i] == 16 * j + e) acc[i][j][e] -= g[i];
             }
         }
         if (n0 + S::BN > p.N) {                      // columns past the end
@@ -621,7 +658,9 @@ Plan plan_of(int64_t M, int64_t V, int64_t K) {
     int64_t most = kPieceBytes / (2 * (M > 0 ? M : 1)) / 256 * 256;
     if (most < kLeastPiece) most = kLeastPiece;
     int64_t before = 0;
-    for (int64_t pieces = up(V, most), tried = 0; tried < 5; pieces += 1 + pieces / 4, ++tried) {
+    // (one piece of at most 32 MiB: it is launched fewer times than any other)
+    const int tries = 2 * M * V <= (int64_t(32) << 20) ? 1 : 5;
+    for (int64_t pieces = up(V, most), tried = 0; tried < tries; pieces += 1 + pieces / 4, ++tried) {
         Plan b{};
         b.piece = up(up(V, pieces), 256) * 256;
         if (b.piece > V) b.piece = V;
@@ -649,7 +688,7 @@ static int64_t round_256(int64_t n) { return (n + 255) / 256 * 256; }
 
 int64_t loss_workspace(int64_t M, int64_t V, int64_t K) {
     Tiles t;
-    return round_256(8 * forward_parts(M, V, K, &t) * M) + round_256(4 * forward_parts(M, V, K, &t) * M) + round_256(4 * M);
+    return round_256(8 * forward_parts(M, V, K, &t) * M) + round_256(4 * forward_parts(M, V, K, &t) * M);
 }
 
 hipError_t launch_loss(const LossCall& c, void* ws, hipStream_t s) {
@@ -664,7 +703,6 @@ hipError_t launch_loss(const LossCall& c, void* ws, hipStream_t s) {
     uint8_t* const base = static_cast<uint8_t*>(ws);
     p.part = reinterpret_cast<Part*>(base);
     if (c.rows.smooth > 0.f) p.totals = reinterpret_cast<float*>(base + round_256(8 * parts * c.M));
-    p.logit = reinterpret_cast<float*>(base + round_256(8 * parts * c.M) + round_256(4 * parts * c.M));
     hipError_t e;
     if (c.M <= kLinearStreamRows) {
         hipLaunchKernelGGL(loss_few_kernel, dim3(static_cast<unsigned>(parts)), dim3(kFewWaves * kWave), 0, s, p);

@@ -62,7 +62,8 @@ __device__ __forceinline__ void store_one(void* p, int64_t at, float f) {
 // column W (t + T j), but never past D - W: the last runs of a row whose D is
 // no multiple of their columns begin earlier and repeat columns that another
 // thread (or run) has too.  Those count once: fresh() tells.  So no load has a
-// condition.  (D >= W.)
+// condition.  (D >= W; where NV > 1 more than half of a row's runs are needed,
+// so the first half of a thread's are whole.)
 template <int W, int T, int NV>
 struct Columns {
     int at[NV], from[NV];                     // first column; the first that counts here (at + W: none)
@@ -74,7 +75,8 @@ struct Columns {
             from[j] = static_cast<int>(c < D ? c : D);
         }
     }
-    __device__ __forceinline__ bool fresh(int j, int e) const { return at[j] + e >= from[j]; }
+    __device__ __forceinline__ bool fresh(int j, int e) const { return (NV > 1 && j < NV / 2) || at[j] + e >= from[j]; }
+    __device__ __forceinline__ bool any(int j, int64_t D) const { return (NV > 1 && j < NV / 2) || from[j] < D; }
 };
 
 // Sums of N values over the T threads of a row, in every one of them.  red:
@@ -83,7 +85,16 @@ struct Columns {
 template <int T, int N>
 __device__ __forceinline__ void row_sums(float* s, float* red, int t) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = T == 16 ? group_sum<16>(s[i]) : wave_sum(s[i]);
+    for (int i = 0; i < N; ++i) {
+        if constexpr (T <= 16) {
+            s[i] = group_sum<T>(s[i]);
+        } else if constexpr (T == 32) {
+            s[i] = group_sum<16>(s[i]);
+            s[i] += __shfl_xor(s[i], 16, kWave);
+        } else {
+            s[i] = wave_sum(s[i]);
+        }
+    }
     if constexpr (T > kWave) {
         constexpr int kW = T / kWave;
         if (t % kWave == 0) {
@@ -149,7 +160,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_row_kernel(NormParams 
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (MASK && cols.from[j] >= p.D) continue;
+            if (MASK && !cols.any(j, p.D)) continue;
             float f[W];
 #pragma unroll
             for (int e = 0; e < W; ++e) f[e] = (x[j].get(e) - mean) * rstd;
@@ -236,7 +247,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormPar
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (MASK && cols.from[j] >= p.D) continue;
+            if (MASK && !cols.any(j, p.D)) continue;
             float f[W];
 #pragma unroll
             for (int e = 0; e < W; ++e) f[e] = fmaf((x[j].get(e) - mean) * rstd, w[W * j + e], b[W * j + e]);
@@ -326,11 +337,13 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
         if (p.center) next_mean = p.stats_in[m];
         next_rstd = p.stats_in[p.M + m];
     };
+    constexpr bool kAhead = T <= 512;         // (1024 threads have no registers for the next row)
     int64_t m0 = static_cast<int64_t>(blockIdx.x) * R;
-    fetch(row_at(m0));
+    if constexpr (kAhead) fetch(row_at(m0));
     for (; m0 < p.M; m0 += static_cast<int64_t>(gridDim.x) * R) {
         const int64_t m = row_at(m0);
         const bool real = R == 1 || m0 + r < p.M;
+        if constexpr (!kAhead) fetch(m);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             x[j] = next_x[j];
@@ -338,7 +351,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
             skip[j] = next_skip[j];
         }
         const float mean = next_mean, rstd = next_rstd;
-        fetch(row_at(m0 + static_cast<int64_t>(gridDim.x) * R));
+        if constexpr (kAhead) fetch(row_at(m0 + static_cast<int64_t>(gridDim.x) * R));
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -358,9 +371,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
         turn ^= 1;
         if (!real) continue;
         const float a = p.center ? s[0] * per : 0.f, b = s[1] * per;
+        if constexpr (!kAhead) {
+            // (the inputs are unpacked again, not kept as floats meanwhile)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) asm volatile("" : "+v"(x[j].v), "+v"(dy[j].v));
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (MASK && cols.from[j] >= p.D) continue;
+            if (MASK && !cols.any(j, p.D)) continue;
             float f[W];
 #pragma unroll
             for (int e = 0; e < W; ++e) {
@@ -524,7 +542,9 @@ hipError_t forward(const NormParams& p, hipStream_t s) {
         return forward_t<XB, YB, 1024, NV>(p, s);
     }
     const int64_t runs = (p.D + W - 1) / W;
+    if (runs <= 8) return rows_t<XB, YB, 8, 1>(p, s);
     if (runs <= 16) return rows_t<XB, YB, 16, 1>(p, s);
+    if (runs <= 32) return rows_t<XB, YB, 32, 1>(p, s);
     if (runs <= 64) return rows_t<XB, YB, 64, 1>(p, s);
     if (runs <= 128) return rows_t<XB, YB, 64, 2>(p, s);
     if (runs <= 256) return rows_t<XB, YB, 64, 4>(p, s);
@@ -542,7 +562,7 @@ hipError_t forward(const NormParams& p, hipStream_t s) {
 // up to 64, for the parameters' sums.
 int64_t norm_parts_of(int64_t M, int64_t D, bool both_bf16) {
     const bool in_steps = D < 8 || D > kLongRow;
-    const int64_t rows = D > 2048 || D < 8 ? 1 : D > 1024 ? 2 : D > 128 ? 4 : 16;
+    const int64_t rows = D > 2048 || D < 8 ? 1 : D > 1024 ? 2 : D > 256 ? 4 : D > 64 ? 8 : 16;
     const bool two = M * D >= (int64_t(1) << 24) && (D <= 1024 || (both_bf16 && D <= 4096));
     const int64_t most = in_steps ? 64 : (two ? 2 : 1) * compute_units();
     const int64_t n = (M + 2 * rows - 1) / (2 * rows);
@@ -575,8 +595,11 @@ hipError_t backward(const NormParams& p, hipStream_t s) {
                            dim3(static_cast<unsigned>((p.D + 255) / 256), static_cast<unsigned>(norm_parts_of(p.M, p.D, XB && YB))), dim3(256), 0, s, p);
         return hipGetLastError();
     }
+    if (p.D <= 8 * W) return backward_m<XB, YB, 8, 1>(p, s);
     if (p.D <= 16 * W) return backward_m<XB, YB, 16, 1>(p, s);
+    if (p.D <= 32 * W) return backward_m<XB, YB, 32, 1>(p, s);
     if (p.D <= 64 * W) return backward_m<XB, YB, 64, 1>(p, s);
+    if (W == 4 && p.D <= 512) return backward_m<XB, YB, 64, 2>(p, s);
     if (p.D <= 1024) return backward_m<XB, YB, 64, NV>(p, s);
     if (p.D <= 2048) return backward_m<XB, YB, 128, NV>(p, s);
     if (p.D <= 4096) return backward_m<XB, YB, 256, NV>(p, s);
