@@ -1366,12 +1366,11 @@ def norm_backward(dy, x, weight, stats, kind=GDN_NORM_LAYER, d_residual=None, wa
     stats: as given to norm() and as it wrote them.  d_residual [M, D] (x's
     type): added to dx, the gradient that reaches x beside the norm; may be dx
     itself.  dx, dweight, dbias: tensors to write instead of new ones."""
-    import torch
     if dy.dim() != 2 or x.dim() != 2:
         raise ValueError("dy and x: matrices needed")
     if stats is None:
         raise ValueError("stats: needed, as norm() wrote them")
-    dev = _device()
+    dev, torch = _device(), _torch
     M, D = x.shape
     xc, yc = _float_code(x.dtype, "x"), _float_code(dy.dtype, "dy")
     px, sx = _matrix(x, "x", M, D, x.dtype, dev)
@@ -1415,7 +1414,7 @@ def linear_cross_entropy_backward_workspace_bytes(M: int, V: int, K: int) -> int
 
 
 def _loss_io(x, w, targets, bias, label_smoothing, z_loss, ignore_index, loss, lse, status, dev):
-    import torch
+    torch = _torch
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError(f"x and w: matrices needed, shapes are {tuple(x.shape)} and {tuple(w.shape)}")
     M, K = x.shape
@@ -1437,8 +1436,7 @@ def linear_cross_entropy(x, w, targets, bias=None, label_smoothing=0.0, z_loss=0
     distribution that is spread over the vocabulary; z_loss: the weight of
     lse^2.  status: optional int32 device word; GDN_STATUS_BAD_INDEX is ORed in
     when another target is not in [0, V) (its loss is NaN)."""
-    import torch
-    dev = _device()
+    dev, torch = _device(), _torch
     M = x.shape[0]
     res = {"loss": _new(x, (M,), torch.float32, stream), "lse": _new(x, (M,), torch.float32, stream)}
     io = _loss_io(x, w, targets, bias, label_smoothing, z_loss, ignore_index, res["loss"].data_ptr(),
@@ -1458,8 +1456,7 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, bias=None, label_sm
     [M, K] and dw [V, K] (bf16) and dbias [V] (fp32; by default with a bias).
     lse: as the forward call gave it, the other arguments as it was given
     them.  dx, dw, dbias: tensors to write instead of new ones."""
-    import torch
-    dev = _device()
+    dev, torch = _device(), _torch
     M, K = x.shape
     V = w.shape[0]
     io = _loss_io(x, w, targets, bias, label_smoothing, z_loss, ignore_index, None,
@@ -1582,8 +1579,7 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
     tensor: a captured step reads those at every replay.  grad_scale: a
     one-element fp32 device tensor, a factor of every gradient; when it is not
     finite nothing is written."""
-    import torch
-    n, dev = len(opt.params), _device()
+    n, dev, torch = len(opt.params), _device(), _torch
     if dev != opt.device:
         raise ValueError(f"opt: made on cuda:{opt.device}, the current device is cuda:{dev}")
     if len(grads) != n:

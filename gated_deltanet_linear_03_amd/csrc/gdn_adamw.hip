@@ -1,5 +1,5 @@
-// gdn_adamw.hip -- one AdamW step over many tensors in one launch for every
-// kAdamwTensors of them.
+// gdn_adamw.hip -- one AdamW step over many tensors, 48 (states in 8 bits)
+// or 64 of them a launch.
 //
 //   m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2
 //   p' = p - lr (m' / (1 - b1^k) / (sqrt(v' / (1 - b2^k)) + eps) + decay p)
@@ -25,6 +25,8 @@
 // states, a bf16 gradient and a bf16 copy, 16 with 8-bit states.  A wave's 64
 // lanes take four adjacent elements each, which is a block of the 8-bit
 // states, so a block's largest magnitude is one reduction over a wave.
+#include <type_traits>
+
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -39,14 +41,33 @@ constexpr int kRounds = 4;                                  // blocks that a wav
 constexpr int kChunk = kThreads * kLane * kRounds;          // elements of a work-group
 static_assert((kChunk & (kChunk - 1)) == 0, "a chunk does not cross a multiple of 2^32");
 
+// A tensor as the kernel sees it.  A launch's arguments hold as many as 4 KiB do.
+struct Tensor {
+    int64_t n;
+    float* param;
+    const void* grad;
+    void* copy;
+    void *m, *v;
+    float weight_decay;
+    uint32_t index;                                         // its place in the call, and (top bit) a bf16 gradient
+};
+struct Scales {
+    float *m_scale, *v_scale;
+};
+struct NoScales {};
+
+template <bool EIGHT>
 struct Launch {
+    static constexpr int kTensors = EIGHT ? 48 : 64;
     AdamwParams p;
-    gdn_adamw_tensor t[kAdamwTensors];
-    int64_t first[kAdamwTensors + 1];                       // work-groups before each tensor's
-    int32_t index[kAdamwTensors];                           // a tensor's place in the whole call
+    Tensor t[kTensors];
+    typename std::conditional<EIGHT, Scales, NoScales>::type scales[EIGHT ? kTensors : 1];
+    uint32_t first[kTensors + 1];                           // work-groups before each tensor's
     int count;
 };
-static_assert(sizeof(Launch) <= 4096, "kernel arguments");
+static_assert(sizeof(Launch<true>) <= 4096 && sizeof(Launch<false>) <= 4096, "kernel arguments");
+
+struct Target : Tensor, Scales {};
 
 typedef uint32_t U4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t U2 __attribute__((ext_vector_type(2), aligned(2)));
@@ -216,7 +237,7 @@ struct Elements {
     float ms, vs;
 
     // (FULL: all four elements exist)
-    __device__ __forceinline__ void load(const gdn_adamw_tensor& t, int64_t at, int nv) {
+    __device__ __forceinline__ void load(const Target& t, int64_t at, int nv) {
         if constexpr (FULL) {
             const U4 a = __builtin_nontemporal_load(reinterpret_cast<const U4*>(t.param + at));
 #pragma unroll
@@ -331,7 +352,7 @@ struct Elements {
     // Codes next to a border once more, from 64 bits, over those that store()
     // has written (a lane's stores to an address stay in order).  One or two
     // blocks in a hundred have any.
-    __device__ __forceinline__ void settle(const gdn_adamw_tensor& t, const Step& s, int64_t at) {
+    __device__ __forceinline__ void settle(const Target& t, const Step& s, int64_t at) {
         while (border) {
             const int b = __builtin_ctz(border), e = b % kLane;
             border &= border - 1;
@@ -353,7 +374,7 @@ struct Elements {
     }
 
     // nv of the elements of each lane
-    __device__ __forceinline__ void store_param(const gdn_adamw_tensor& t, int64_t at, int nv) const {
+    __device__ __forceinline__ void store_param(const Target& t, int64_t at, int nv) const {
         if constexpr (FULL) {
             const U4 a = {__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]), __float_as_uint(p[3])};
             __builtin_nontemporal_store(a, reinterpret_cast<U4*>(t.param + at));
@@ -373,7 +394,7 @@ struct Elements {
         }
     }
 
-    __device__ __forceinline__ void store_state(const gdn_adamw_tensor& t, int64_t at, int nv, int lane) const {
+    __device__ __forceinline__ void store_state(const Target& t, int64_t at, int nv, int lane) const {
         if constexpr (EIGHT) {
             if (lane == 0) {
                 t.m_scale[at / kAdamwBlock] = sm;
@@ -410,7 +431,7 @@ template <int I>
 struct Int { static constexpr int value = I; };
 
 template <bool EIGHT, bool GB>
-__device__ __forceinline__ void chunk(const gdn_adamw_tensor& t, const Step& s, int64_t base) {
+__device__ __forceinline__ void chunk(const Target& t, const Step& s, int64_t base) {
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     // a wave's blocks follow one another
     const int64_t at0 = base + static_cast<int64_t>(wave) * kRounds * kAdamwBlock + kLane * lane;
@@ -462,16 +483,18 @@ __device__ __forceinline__ void chunk(const gdn_adamw_tensor& t, const Step& s, 
 }
 
 template <bool EIGHT>
-__global__ __launch_bounds__(kThreads, EIGHT ? 4 : 5) void adamw_kernel(Launch a) {
+__global__ __launch_bounds__(kThreads, EIGHT ? 4 : 5) void adamw_kernel(Launch<EIGHT> a) {
     const AdamwParams& p = a.p;
     // the gradients' factor decides whether there is a step at all
     const float gs = p.grad_scale ? *p.grad_scale : 1.f;
     if (!(fabsf(gs) <= 3.402823466e38f)) return;
-    const int64_t b = blockIdx.x;
+    const uint32_t b = blockIdx.x;
     int i = 0;
-    for (int step = kAdamwTensors / 2; step > 0; step /= 2)
+    for (int step = 32; step > 0; step /= 2)
         if (i + step < a.count && b >= a.first[i + step]) i += step;
-    const gdn_adamw_tensor t = a.t[i];
+    Target t;
+    static_cast<Tensor&>(t) = a.t[i];
+    if constexpr (EIGHT) static_cast<Scales&>(t) = a.scales[i];
     Step s;
     int32_t k = p.step_ptr ? *p.step_ptr : p.step;
     k = k < 1 ? 1 : k;
@@ -492,10 +515,10 @@ __global__ __launch_bounds__(kThreads, EIGHT ? 4 : 5) void adamw_kernel(Launch a
     // 1 - b^k = -expm1(k ln b): no cancellation where b^k is next to one
     s.c1 = s.lr / -expm1f(static_cast<float>(k) * p.log_beta1);
     s.c2 = 1.f / sqrtf(-expm1f(static_cast<float>(k) * p.log_beta2));
-    s.key = mix(mix(p.seed + static_cast<uint32_t>(k) * 0x9E3779B1u) + static_cast<uint32_t>(a.index[i]) * 0x9E3779B1u);
-    const int64_t base = (b - a.first[i]) * kChunk;
+    s.key = mix(mix(p.seed + static_cast<uint32_t>(k) * 0x9E3779B1u) + (t.index & 0x7FFFFFFFu) * 0x9E3779B1u);
+    const int64_t base = static_cast<int64_t>(b - a.first[i]) * kChunk;
     s.key += mix(static_cast<uint32_t>(static_cast<uint64_t>(base) >> 32));   // (one for all of the chunk)
-    if (t.grad_dtype == GDN_DTYPE_BF16) chunk<EIGHT, true>(t, s, base);
+    if (t.index >> 31) chunk<EIGHT, true>(t, s, base);
     else chunk<EIGHT, false>(t, s, base);
 }
 
@@ -503,29 +526,37 @@ __global__ __launch_bounds__(kThreads, EIGHT ? 4 : 5) void adamw_kernel(Launch a
 
 int64_t adamw_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 
-hipError_t launch_adamw(const AdamwParams& p, const gdn_adamw_tensor* tensors, int count, bool eight, hipStream_t s) {
+namespace {
+
+template <bool EIGHT>
+hipError_t launch(const AdamwParams& p, const gdn_adamw_tensor* tensors, int count, hipStream_t s) {
     for (int i = 0; i < count;) {
-        Launch a;
+        Launch<EIGHT> a;
         a.p = p;
         a.count = 0;
         a.first[0] = 0;
-        for (; i < count && a.count < kAdamwTensors; ++i) {
-            if (tensors[i].n <= 0) continue;
-            const int64_t chunks = adamw_chunks(tensors[i].n);
-            if (a.count > 0 && a.first[a.count] + chunks > kAdamwMostChunks) break;
-            a.t[a.count] = tensors[i];
-            a.index[a.count] = i;
-            a.first[a.count + 1] = a.first[a.count] + chunks;
-            ++a.count;
+        for (; i < count && a.count < Launch<EIGHT>::kTensors; ++i) {
+            const gdn_adamw_tensor& t = tensors[i];
+            if (t.n <= 0) continue;
+            const int64_t end = a.first[a.count] + adamw_chunks(t.n);
+            if (a.count > 0 && end > kAdamwMostChunks) break;
+            a.t[a.count] = {t.n, t.param, t.grad, t.copy, t.m, t.v, t.weight_decay,
+                            static_cast<uint32_t>(i) | (t.grad_dtype == GDN_DTYPE_BF16 ? 1u << 31 : 0u)};
+            if constexpr (EIGHT) a.scales[a.count] = {t.m_scale, t.v_scale};
+            a.first[++a.count] = static_cast<uint32_t>(end);
         }
         if (a.count == 0) break;
-        const dim3 grid(static_cast<unsigned>(a.first[a.count]));
-        if (eight) hipLaunchKernelGGL(adamw_kernel<true>, grid, dim3(kThreads), 0, s, a);
-        else hipLaunchKernelGGL(adamw_kernel<false>, grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL(adamw_kernel<EIGHT>, dim3(a.first[a.count]), dim3(kThreads), 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwParams& p, const gdn_adamw_tensor* tensors, int count, bool eight, hipStream_t s) {
+    return eight ? launch<true>(p, tensors, count, s) : launch<false>(p, tensors, count, s);
 }
 
 }  // namespace gdn

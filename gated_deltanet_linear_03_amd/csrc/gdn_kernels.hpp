@@ -311,7 +311,6 @@ hipError_t launch_norm_backward(const NormParams& p, bool x_bf16, bool y_bf16, h
 
 // ---- AdamW over many tensors (gdn_adamw.hip) ----------------------------------
 constexpr int kAdamwBlock = 256;         // elements that share a scale of the 8-bit states
-constexpr int kAdamwTensors = 32;        // tensors of a launch (its arguments hold them)
 constexpr int64_t kAdamwMostChunks = (int64_t(1) << 24) - 1;   // work-groups of a launch: fewer than 2^32 work-items
 
 struct AdamwParams {

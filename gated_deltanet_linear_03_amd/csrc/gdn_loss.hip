@@ -450,11 +450,12 @@ __global__ __launch_bounds__(1024) void loss_scale_kernel(LossRows r, int64_t M,
 // dx and dw of a piece in one launch.  dx: its reduction, the piece's columns,
 // is cut into `parts`, each with sums of its own ([parts][M][K] in 32 bits),
 // to which a piece adds.  The tiles with the longer reductions come first.
+// DIRECT: one piece, one part: dx is what the product gives.
 __host__ __device__ inline int64_t loss_share(int64_t n, int parts) {
     return ((n + 127) / 128 + parts - 1) / parts * 128;
 }
 
-template <typename S>
+template <typename S, bool DIRECT>
 __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel(GemmProduct dx, ScaledProduct dw, int parts, int tx, int tw) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
     const int64_t share = loss_share(dx.K, parts);
@@ -463,6 +464,14 @@ __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel
     const int tile = b < first ? b : b - first;
     if ((b < first) == dw_leads) {
         gemm_tile<false, false, Store<S, true, false, ScaledProduct>, S>(dw, tile, shared);
+        return;
+    }
+    if constexpr (DIRECT) {
+        ScaledProduct p;
+        static_cast<GemmProduct&>(p) = dx;
+        p.scale = dw.scale;
+        p.factor = dw.factor;
+        gemm_tile<true, false, Store<S, true, false, ScaledProduct>, S>(p, tile, shared);
         return;
     }
     const int per = tx / parts, part = tile / per;
@@ -515,10 +524,12 @@ hipError_t gradient_t(const LossProduct& p, hipStream_t s) {
 }
 
 template <typename S>
-hipError_t products_t(const GemmProduct& dx, const ScaledProduct& dw, int parts, hipStream_t s) {
+hipError_t products_t(const GemmProduct& dx, const ScaledProduct& dw, int parts, bool direct, hipStream_t s) {
     const int64_t tx = dx.ep.y ? tiles<S>(dx) * parts : 0, tw = dw.ep.y ? tiles<S>(dw) : 0;
-    hipLaunchKernelGGL((loss_products_kernel<S>), dim3(static_cast<unsigned>(tx + tw)), dim3(S::kThreads), 0, s, dx, dw, parts,
-                       static_cast<int>(tx), static_cast<int>(tw));
+    const dim3 grid(static_cast<unsigned>(tx + tw)), block(S::kThreads);
+    const int nx = static_cast<int>(tx), nw = static_cast<int>(tw);
+    if (direct) hipLaunchKernelGGL((loss_products_kernel<S, true>), grid, block, 0, s, dx, dw, parts, nx, nw);
+    else hipLaunchKernelGGL((loss_products_kernel<S, false>), grid, block, 0, s, dx, dw, parts, nx, nw);
     return hipGetLastError();
 }
 
@@ -540,8 +551,8 @@ hipError_t gradient(const LossProduct& p, Tiles t, hipStream_t s) {
     GDN_LOSS_TILES(t, GDN_CALL)
 #undef GDN_CALL
 }
-hipError_t products(const GemmProduct& dx, const ScaledProduct& dw, Tiles t, int parts, hipStream_t s) {
-#define GDN_CALL(S) products_t<S>(dx, dw, parts, s)
+hipError_t products(const GemmProduct& dx, const ScaledProduct& dw, Tiles t, int parts, bool direct, hipStream_t s) {
+#define GDN_CALL(S) products_t<S>(dx, dw, parts, direct, s)
     GDN_LOSS_TILES(t, GDN_CALL)
 #undef GDN_CALL
 }
@@ -623,14 +634,14 @@ double makespan(int64_t n0, double t0, int64_t n1, double t1, int64_t units) {
 
 // The best tiles, and parts of dx's reduction, for the products of a piece.  A
 // launch has dx's and dw's tiles, the ones of the longer reduction first.
-double plan_products(int64_t M, int64_t piece, int64_t K, Plan* b) {
+double plan_products(int64_t M, int64_t piece, int64_t K, bool one, Plan* b) {
     const int cus = compute_units();
     double least = 1e30;
     // w in, dw out
     const double memory = 4.0 * static_cast<double>(piece) * K / kBytesPerUs;
     for (int parts = 1; parts <= 32 && (parts == 1 || (piece / parts >= 256 && up(M, 64) * up(K, 64) <= 4096)); parts *= 2) {
-        // the parts' sums: out, and in again
-        const double sums = 8.0 * M * K * parts / kBytesPerUs;
+        // the parts' sums: out, and in again; one piece without parts has none, and no kernel that adds them
+        const double sums = one && parts == 1 ? 0.0 : 8.0 * M * K * parts / kBytesPerUs + (one ? 4.0 : 0.0);
         for (Tiles t : {kLarge, kWide, kMedium, kSmall}) {
             const TileTimes& c = kTimes[t];
             const int64_t tx = up(M, tile_rows(t)) * up(K, tile_cols(t)) * parts, tw = up(piece, tile_rows(t)) * up(K, tile_cols(t));
@@ -668,7 +679,7 @@ Plan plan_of(int64_t M, int64_t V, int64_t K) {
         before = b.piece;
         double dl;
         b.gradient = tiles_for(M, b.piece, K, &TileTimes::gradient, &dl);
-        const double us = (dl + plan_products(M, b.piece, K, &b) + 8) * static_cast<double>(V) / static_cast<double>(b.piece);   // 8: two launches
+        const double us = (dl + plan_products(M, b.piece, K, b.piece == V, &b) + 8) * static_cast<double>(V) / static_cast<double>(b.piece);   // 8: two launches
         if (us < least) { least = us; best = b; }
     }
     return best;
@@ -721,11 +732,13 @@ struct BackwardWs {
 };
 
 // dl of a piece, dx's sums, and the row tiles' sums for dbias
+static bool is_direct(int64_t V, const Plan& b) { return b.piece >= V && b.parts == 1; }
+
 static BackwardWs backward_ws(int64_t M, int64_t V, int64_t K, const Plan& b) {
     BackwardWs w;
     w.ld = (b.piece + 63) / 64 * 64;
     w.off_sums = round_256(2 * M * w.ld);
-    w.off_columns = w.off_sums + round_256(4 * b.parts * M * K);
+    w.off_columns = w.off_sums + (is_direct(V, b) ? 0 : round_256(4 * b.parts * M * K));
     w.off_scale = w.off_columns + round_256(4 * ((M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient)) * V);
     w.total = w.off_scale + 256;
     return w;
@@ -741,7 +754,7 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
         pw.M = c.V; pw.N = c.K;
         pw.ep.bf16 = 1;
         pw.ep.y = c.dw; pw.ep.ldy = c.lddw;
-        const hipError_t e = c.dw ? products(none, pw, kSmall, 1, s) : hipSuccess;
+        const hipError_t e = c.dw ? products(none, pw, kSmall, 1, false, s) : hipSuccess;
         return e != hipSuccess ? e : launch_fill_zero(c.dbias, c.V, s);
     }
     const Plan b = plan_of(c.M, c.V, c.K);
@@ -750,6 +763,7 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
     uint16_t* const dl = reinterpret_cast<uint16_t*>(base);
     float* const sums = reinterpret_cast<float*>(base + w.off_sums);
     float* const columns = reinterpret_cast<float*>(base + w.off_columns);
+    const bool direct = is_direct(c.V, b);
     LossRows rows = c.rows;
     const float* scale = rows.dloss;
     if (!rows.dloss_one) {
@@ -783,17 +797,21 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
         px.A = dl; px.lda = w.ld;
         px.B = p.B; px.ldb = c.ldw;
         px.M = c.M; px.N = c.K; px.K = n;
-        px.ep.y = c.dx ? sums : nullptr; px.ep.ldy = c.K;
-        px.ep.residual = v0 > 0 ? sums : nullptr; px.ep.ldr = c.K;
+        if (direct) {
+            px.ep.y = c.dx; px.ep.ldy = c.lddx; px.ep.bf16 = 1;
+        } else {
+            px.ep.y = c.dx ? sums : nullptr; px.ep.ldy = c.K;
+            px.ep.residual = v0 > 0 ? sums : nullptr; px.ep.ldr = c.K;
+        }
         pw.A = dl; pw.lda = w.ld;
         pw.B = c.x; pw.ldb = c.ldx;
         pw.M = n; pw.N = c.K; pw.K = c.M;
         pw.ep.bf16 = 1;
         pw.ep.y = c.dw ? static_cast<uint16_t*>(c.dw) + v0 * c.lddw : nullptr; pw.ep.ldy = c.lddw;
-        e = products(px, pw, b.products, b.parts, s);
+        e = products(px, pw, b.products, b.parts, direct, s);
         if (e != hipSuccess) return e;
     }
-    const int64_t dx_blocks = c.dx ? (c.M * (c.K / 4) + 255) / 256 : 0, bias_blocks = c.dbias ? (c.V + 255) / 256 : 0;
+    const int64_t dx_blocks = c.dx && !direct ? (c.M * (c.K / 4) + 255) / 256 : 0, bias_blocks = c.dbias ? (c.V + 255) / 256 : 0;
     if (dx_blocks + bias_blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(loss_finish_kernel, dim3(static_cast<unsigned>(dx_blocks + bias_blocks)), dim3(256), 0, s, sums, b.parts, c.M, c.K,
                        static_cast<uint16_t*>(c.dx), c.lddx, dx_blocks, columns,

@@ -390,15 +390,18 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
         }
     }
     if (!params) return;
-    float* const out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+    // one work-group's sums are the gradients themselves
+    const bool only = gridDim.x == 1;
+    float* const ow = only ? p.dweight : p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+    float* const ob = only ? p.dbias : ow + p.D;
     if constexpr (R == 1) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < W; ++e)
                 if (!MASK || cols.fresh(j, e)) {
-                    out[cols.at[j] + e] = dw[W * j + e];
-                    out[p.D + cols.at[j] + e] = db[W * j + e];
+                    if (ow) ow[cols.at[j] + e] = dw[W * j + e];
+                    if (ob) ob[cols.at[j] + e] = db[W * j + e];
                 }
     } else {                                  // the rows' sums, added in order
         __shared__ float all[R - 1][2 * C][T];
@@ -423,8 +426,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
 #pragma unroll
             for (int e = 0; e < W; ++e)
                 if (!MASK || cols.fresh(j, e)) {
-                    out[cols.at[j] + e] = dw[W * j + e];
-                    out[p.D + cols.at[j] + e] = db[W * j + e];
+                    if (ow) ow[cols.at[j] + e] = dw[W * j + e];
+                    if (ob) ob[cols.at[j] + e] = db[W * j + e];
                 }
     }
 }
@@ -469,9 +472,11 @@ __global__ __launch_bounds__(256) void norm_params_long_kernel(NormParams p) {
         dw = fmaf(d, (load_one<XB>(p.x, m * p.xs + c) - mean) * rstd, dw);
         db += d;
     }
-    float* const out = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.D;
-    out[c] = dw;
-    out[p.D + c] = db;
+    const bool only = gridDim.y == 1;
+    float* const ow = only ? p.dweight : p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.D;
+    float* const ob = only ? p.dbias : ow + p.D;
+    if (ow) ow[c] = dw;
+    if (ob) ob[c] = db;
 }
 
 // dweight and dbias from the work-groups' sums, in their order: 32 columns a
@@ -559,12 +564,14 @@ hipError_t forward(const NormParams& p, hipStream_t s) {
 // with one block each), and two where the rows come to 2^24 values and fit, in
 // bf16 or up to 1024 columns (8192 x 4096 in bf16: 58 and 62 us, 4096 x 4096:
 // 42 and 39; 32768 x 4096 in fp32: 243 and 223).  Rows that are read in steps:
-// up to 64, for the parameters' sums.
+// up to 64, for the parameters' sums.  A few blocks of rows go to one
+// work-group, whose sums no second kernel has to add.
 int64_t norm_parts_of(int64_t M, int64_t D, bool both_bf16) {
     const bool in_steps = D < 8 || D > kLongRow;
     const int64_t rows = D > 2048 || D < 8 ? 1 : D > 1024 ? 2 : D > 256 ? 4 : D > 64 ? 8 : 16;
     const bool two = M * D >= (int64_t(1) << 24) && (D <= 1024 || (both_bf16 && D <= 4096));
     const int64_t most = in_steps ? 64 : (two ? 2 : 1) * compute_units();
+    if (M <= 4 * rows) return 1;
     const int64_t n = (M + 2 * rows - 1) / (2 * rows);
     return n < most ? n : most;
 }
@@ -623,7 +630,7 @@ hipError_t launch_norm_backward(const NormParams& p, bool x_bf16, bool y_bf16, h
     hipError_t e;
     if (x_bf16) e = y_bf16 ? backward<true, true>(p, s) : backward<true, false>(p, s);
     else e = y_bf16 ? backward<false, true>(p, s) : backward<false, false>(p, s);
-    if (e != hipSuccess || !p.part) return e;
+    if (e != hipSuccess || !p.part || norm_parts_of(p.M, p.D, x_bf16 && y_bf16) == 1) return e;
     hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<unsigned>((2 * p.D + 31) / 32)), dim3(1024), 0, s, p,
                        static_cast<int>(norm_parts_of(p.M, p.D, x_bf16 && y_bf16)));
     return hipGetLastError();
