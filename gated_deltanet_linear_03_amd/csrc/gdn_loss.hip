@@ -15,7 +15,9 @@
 // Backward: for a piece of the vocabulary at a time the tiles of the product
 // are computed once more and leave dl in bf16, the operand type of the two
 // products that follow: dx, in 32 bits from piece to piece, and the piece's
-// rows of dw.  dl is rounded to bf16 once, as dp is in the linear layer's
+// rows of dw.  Rows without a target add nothing: a large call first brings the
+// others together, and all that follows is as long as there are of those (the
+// host does not know how many: tiles past them end at once).  dl is rounded to bf16 once, as dp is in the linear layer's
 // backward pass (dbias sums it in 32 bits before that), and not by itself but
 // over (1 - e) times the largest |g|, by which the outputs are multiplied in 32
 // bits: with one g for all rows the target's entry is then next to -1 and
@@ -74,6 +76,7 @@ struct LossProduct : GemmProduct {
     GemmProduct out;                          // dl: rows, columns (padded with zeros), address and stride
     float* columns;                           // [row tiles][V] sums of dl, or NULL
     int64_t columns_ld;
+    const int32_t* count;                     // device: how many of the M rows there are; NULL: all
 };
 
 // row of a wave's accumulators acc[i][.] in lane l16
@@ -425,7 +428,74 @@ struct Gradient {
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_gradient_kernel(LossProduct p) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
+    if (p.count) {
+        p.M = p.out.M = *p.count;
+        if (blockIdx.x >= ((p.M + S::BM - 1) / S::BM) * ((p.N + S::BN - 1) / S::BN)) return;
+    }
     gemm_tile<true, true, Gradient<S>, S>(p, blockIdx.x, shared);
+}
+
+// The rows that count, in their order: place[m] among them or -1, and how many.
+constexpr int kListThreads = 1024, kListEach = 8;
+
+__global__ __launch_bounds__(kListThreads) void loss_list_kernel(LossRows r, int64_t M, int32_t* place, int32_t* count) {
+    __shared__ int32_t waves[kListThreads / kWave];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    int32_t before = 0;
+    for (int64_t m0 = 0; m0 < M; m0 += kListThreads * kListEach) {
+        const int64_t first = m0 + static_cast<int64_t>(threadIdx.x) * kListEach;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < kListEach; ++e) {
+            const int64_t m = first + e, t = target_of(r, m < M ? m : M - 1);
+            mine |= m < M && t != r.ignore && t >= 0 && t < r.V ? 1u << e : 0u;
+        }
+        const int32_t own = __builtin_popcount(mine);
+        int32_t upto = own;                                   // of the wave's lanes up to this one
+#pragma unroll
+        for (int x = 1; x < kWave; x *= 2) {
+            const int32_t v = __shfl_up(upto, x, kWave);
+            upto += lane >= x ? v : 0;
+        }
+        if (lane == kWave - 1) waves[wave] = upto;
+        __syncthreads();
+        int32_t at = before + upto - own;
+#pragma unroll
+        for (int w = 0; w < kListThreads / kWave; ++w) {
+            at += w < wave ? waves[w] : 0;
+            before += waves[w];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kListEach; ++e) {
+            if (first + e < M) place[first + e] = mine >> e & 1u ? at : -1;
+            at += static_cast<int32_t>(mine >> e & 1u);
+        }
+    }
+    if (threadIdx.x == 0) *count = before;
+}
+
+// What the backward pass reads of those rows, together; a wave a row.
+struct LossList {
+    const int32_t* place;                     // [M]
+    uint16_t* x;                              // [count][K]
+    int32_t* targets;
+    float *lse, *dloss;                       // dloss: not written where there is one for all
+};
+
+__global__ __launch_bounds__(256) void loss_gather_kernel(LossRows r, LossList l, const uint16_t* x, int64_t ldx, int64_t M, int64_t K) {
+    const int lane = threadIdx.x % kWave;
+    for (int64_t m = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave; m < M; m += static_cast<int64_t>(gridDim.x) * 4) {
+        const int64_t at = l.place[m];
+        if (at < 0) continue;
+        for (int64_t k = 8 * lane; k < K; k += 8 * kWave)
+            *reinterpret_cast<u32x4*>(l.x + at * K + k) = *reinterpret_cast<const u32x4*>(x + m * ldx + k);
+        if (lane == 0) {
+            l.targets[at] = static_cast<int32_t>(target_of(r, m));
+            l.lse[at] = r.lse[m];
+            if (!r.dloss_one) l.dloss[at] = r.dloss[m];
+        }
+    }
 }
 
 // The largest finite |g| of the rows that count (0: none).
@@ -456,8 +526,14 @@ __host__ __device__ inline int64_t loss_share(int64_t n, int parts) {
 }
 
 template <typename S, bool DIRECT>
-__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel(GemmProduct dx, ScaledProduct dw, int parts, int tx, int tw) {
+__global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel(GemmProduct dx, ScaledProduct dw, int parts, int tx, int tw,
+                                                                                        const int32_t* count) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
+    if (count) {
+        dx.M = dw.K = *count;
+        if (tx > 0) tx = static_cast<int>((dx.M + S::BM - 1) / S::BM * ((dx.N + S::BN - 1) / S::BN)) * parts;
+        if (static_cast<int>(blockIdx.x) >= tx + tw) return;
+    }
     const int64_t share = loss_share(dx.K, parts);
     const bool dw_leads = dw.K > share;
     const int b = blockIdx.x, first = dw_leads ? tw : tx;
@@ -490,25 +566,43 @@ __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_products_kernel
 
 // dx from its parts' sums, four columns a thread, and dbias from the row
 // tiles' sums, a column a thread.
-__global__ __launch_bounds__(256) void loss_finish_kernel(const float* sums, int parts, int64_t M, int64_t K, uint16_t* dx, int64_t lddx,
-                                                          int64_t dx_blocks, const float* columns, int64_t rows, int64_t V, float* dbias,
-                                                          const float* scale, float factor) {
-    const float by = *scale * factor;
-    if (static_cast<int64_t>(blockIdx.x) < dx_blocks) {
-        const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, per = K / 4, m = i / per, k = i % per * 4;
-        if (m >= M) return;
-        f32x4 s = *reinterpret_cast<const f32x4*>(sums + m * K + k);
-        for (int a = 1; a < parts; ++a) s += *reinterpret_cast<const f32x4*>(sums + (a * M + m) * K + k);
-        const float f[4] = {s[0] * by, s[1] * by, s[2] * by, s[3] * by};
-        store_n<4>(dx, true, m * lddx + k, 4, f);
+struct LossFinish {
+    const float* sums;                        // [parts][rows][K]
+    int parts;
+    int64_t M, K, V;
+    const int32_t *place, *count;             // NULL: the rows are all M
+    uint16_t* dx;
+    int64_t lddx, dx_blocks;
+    const float* columns;                     // [row tiles][V]
+    int tile_rows;
+    float* dbias;
+    const float* scale;
+    float factor;
+};
+
+__global__ __launch_bounds__(256) void loss_finish_kernel(LossFinish f) {
+    const float by = *f.scale * f.factor;
+    const int64_t rows = f.count ? *f.count : f.M;
+    if (static_cast<int64_t>(blockIdx.x) < f.dx_blocks) {
+        const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, per = f.K / 4, m = i / per, k = i % per * 4;
+        if (m >= f.M) return;
+        const int64_t at = f.place ? f.place[m] : m;
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        if (at >= 0) {
+            s = *reinterpret_cast<const f32x4*>(f.sums + at * f.K + k);
+            for (int a = 1; a < f.parts; ++a) s += *reinterpret_cast<const f32x4*>(f.sums + (a * rows + at) * f.K + k);
+            s *= by;
+        }
+        const float v[4] = {s[0], s[1], s[2], s[3]};
+        store_n<4>(f.dx, true, m * f.lddx + k, 4, v);
         return;
     }
-    const int64_t v = (blockIdx.x - dx_blocks) * 256 + threadIdx.x;
-    if (v >= V) return;
+    const int64_t v = (blockIdx.x - f.dx_blocks) * 256 + threadIdx.x, tiles = (rows + f.tile_rows - 1) / f.tile_rows;
+    if (v >= f.V) return;
     float s = 0.f;
 #pragma unroll 8
-    for (int64_t r = 0; r < rows; ++r) s += columns[r * V + v];
-    dbias[v] = s * by;
+    for (int64_t r = 0; r < tiles; ++r) s += f.columns[r * f.V + v];
+    f.dbias[v] = s * by;
 }
 
 template <typename S>
@@ -524,12 +618,12 @@ hipError_t gradient_t(const LossProduct& p, hipStream_t s) {
 }
 
 template <typename S>
-hipError_t products_t(const GemmProduct& dx, const ScaledProduct& dw, int parts, bool direct, hipStream_t s) {
+hipError_t products_t(const GemmProduct& dx, const ScaledProduct& dw, int parts, bool direct, const int32_t* count, hipStream_t s) {
     const int64_t tx = dx.ep.y ? tiles<S>(dx) * parts : 0, tw = dw.ep.y ? tiles<S>(dw) : 0;
     const dim3 grid(static_cast<unsigned>(tx + tw)), block(S::kThreads);
     const int nx = static_cast<int>(tx), nw = static_cast<int>(tw);
-    if (direct) hipLaunchKernelGGL((loss_products_kernel<S, true>), grid, block, 0, s, dx, dw, parts, nx, nw);
-    else hipLaunchKernelGGL((loss_products_kernel<S, false>), grid, block, 0, s, dx, dw, parts, nx, nw);
+    if (direct) hipLaunchKernelGGL((loss_products_kernel<S, true>), grid, block, 0, s, dx, dw, parts, nx, nw, count);
+    else hipLaunchKernelGGL((loss_products_kernel<S, false>), grid, block, 0, s, dx, dw, parts, nx, nw, count);
     return hipGetLastError();
 }
 
@@ -551,8 +645,8 @@ hipError_t gradient(const LossProduct& p, Tiles t, hipStream_t s) {
     GDN_LOSS_TILES(t, GDN_CALL)
 #undef GDN_CALL
 }
-hipError_t products(const GemmProduct& dx, const ScaledProduct& dw, Tiles t, int parts, bool direct, hipStream_t s) {
-#define GDN_CALL(S) products_t<S>(dx, dw, parts, direct, s)
+hipError_t products(const GemmProduct& dx, const ScaledProduct& dw, Tiles t, int parts, bool direct, const int32_t* count, hipStream_t s) {
+#define GDN_CALL(S) products_t<S>(dx, dw, parts, direct, count, s)
     GDN_LOSS_TILES(t, GDN_CALL)
 #undef GDN_CALL
 }
@@ -608,6 +702,7 @@ struct Plan {
     int64_t piece;                            // columns of the vocabulary at a time
     Tiles gradient, products;
     int parts;                                // of dx's reduction
+    bool gather;                              // the rows that count are brought together first
 };
 
 // When the last of a launch's tiles ends: n0 of t0 us first, then n1 of t1, each
@@ -682,6 +777,8 @@ Plan plan_of(int64_t M, int64_t V, int64_t K) {
         const double us = (dl + plan_products(M, b.piece, K, b.piece == V, &b) + 8) * static_cast<double>(V) / static_cast<double>(b.piece);   // 8: two launches
         if (us < least) { least = us; best = b; }
     }
+    // (two more launches, 15 us: of a call that takes 20 times that)
+    best.gather = least >= 300 && M >= 512;
     return best;
 }
 
@@ -728,11 +825,11 @@ hipError_t launch_loss(const LossCall& c, void* ws, hipStream_t s) {
 }
 
 struct BackwardWs {
-    int64_t ld, off_sums, off_columns, off_scale, total;
+    int64_t ld, off_sums, off_columns, off_scale, off_place, off_rows, off_x, total;
 };
 
 // dl of a piece, dx's sums, and the row tiles' sums for dbias
-static bool is_direct(int64_t V, const Plan& b) { return b.piece >= V && b.parts == 1; }
+static bool is_direct(int64_t V, const Plan& b) { return b.piece >= V && b.parts == 1 && !b.gather; }
 
 static BackwardWs backward_ws(int64_t M, int64_t V, int64_t K, const Plan& b) {
     BackwardWs w;
@@ -740,7 +837,10 @@ static BackwardWs backward_ws(int64_t M, int64_t V, int64_t K, const Plan& b) {
     w.off_sums = round_256(2 * M * w.ld);
     w.off_columns = w.off_sums + (is_direct(V, b) ? 0 : round_256(4 * b.parts * M * K));
     w.off_scale = w.off_columns + round_256(4 * ((M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient)) * V);
-    w.total = w.off_scale + 256;
+    w.off_place = w.off_scale + 256;          // the rows that count: their places, and their number before them
+    w.off_rows = w.off_place + (b.gather ? round_256(4 * M) : 0);
+    w.off_x = w.off_rows + (b.gather ? 3 * round_256(4 * M) : 0);
+    w.total = w.off_x + (b.gather ? round_256(2 * M * K) : 0);
     return w;
 }
 
@@ -754,7 +854,7 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
         pw.M = c.V; pw.N = c.K;
         pw.ep.bf16 = 1;
         pw.ep.y = c.dw; pw.ep.ldy = c.lddw;
-        const hipError_t e = c.dw ? products(none, pw, kSmall, 1, false, s) : hipSuccess;
+        const hipError_t e = c.dw ? products(none, pw, kSmall, 1, false, nullptr, s) : hipSuccess;
         return e != hipSuccess ? e : launch_fill_zero(c.dbias, c.V, s);
     }
     const Plan b = plan_of(c.M, c.V, c.K);
@@ -774,10 +874,39 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
         scale = top;
     }
     rows.scale = scale;
+    const void* x = c.x;
+    int64_t ldx = c.ldx;
+    const int32_t *place = nullptr, *count = nullptr;
+    if (b.gather) {
+        int32_t* const list = reinterpret_cast<int32_t*>(base + w.off_place);
+        int32_t* const n = reinterpret_cast<int32_t*>(base + w.off_scale + 128);
+        uint8_t* const kept = base + w.off_rows;
+        const int64_t each = round_256(4 * c.M);
+        LossList l{list, reinterpret_cast<uint16_t*>(base + w.off_x), reinterpret_cast<int32_t*>(kept),
+                   reinterpret_cast<float*>(kept + each), reinterpret_cast<float*>(kept + 2 * each)};
+        hipLaunchKernelGGL(loss_list_kernel, dim3(1), dim3(kListThreads), 0, s, rows, c.M, list, n);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const int64_t groups = (c.M + 3) / 4;
+        hipLaunchKernelGGL(loss_gather_kernel, dim3(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20)), dim3(256), 0, s, rows, l,
+                           static_cast<const uint16_t*>(c.x), c.ldx, c.M, c.K);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        place = list;
+        count = n;
+        x = l.x;
+        ldx = c.K;
+        rows.targets = l.targets;
+        rows.targets64 = 0;
+        rows.ignore = -1;
+        rows.lse = l.lse;
+        if (!rows.dloss_one) rows.dloss = l.dloss;
+    }
     for (int64_t v0 = 0; v0 < c.V; v0 += b.piece) {
         const int64_t n = c.V - v0 < b.piece ? c.V - v0 : b.piece;
         LossProduct p{};
-        p.A = c.x; p.lda = c.ldx;
+        p.A = x; p.lda = ldx;
+        p.count = count;
         p.B = static_cast<const uint16_t*>(c.w) + v0 * c.ldw; p.ldb = c.ldw;
         p.M = c.M; p.N = n; p.K = c.K;
         p.rows = rows;
@@ -804,18 +933,18 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
             px.ep.residual = v0 > 0 ? sums : nullptr; px.ep.ldr = c.K;
         }
         pw.A = dl; pw.lda = w.ld;
-        pw.B = c.x; pw.ldb = c.ldx;
+        pw.B = x; pw.ldb = ldx;
         pw.M = n; pw.N = c.K; pw.K = c.M;
         pw.ep.bf16 = 1;
         pw.ep.y = c.dw ? static_cast<uint16_t*>(c.dw) + v0 * c.lddw : nullptr; pw.ep.ldy = c.lddw;
-        e = products(px, pw, b.products, b.parts, direct, s);
+        e = products(px, pw, b.products, b.parts, direct, p.count, s);
         if (e != hipSuccess) return e;
     }
     const int64_t dx_blocks = c.dx && !direct ? (c.M * (c.K / 4) + 255) / 256 : 0, bias_blocks = c.dbias ? (c.V + 255) / 256 : 0;
     if (dx_blocks + bias_blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(loss_finish_kernel, dim3(static_cast<unsigned>(dx_blocks + bias_blocks)), dim3(256), 0, s, sums, b.parts, c.M, c.K,
-                       static_cast<uint16_t*>(c.dx), c.lddx, dx_blocks, columns,
-                       (c.M + tile_rows(b.gradient) - 1) / tile_rows(b.gradient), c.V, c.dbias, scale, 1.f - c.rows.smooth);
+    const LossFinish f{sums, b.parts, c.M, c.K, c.V, place, count, static_cast<uint16_t*>(c.dx), c.lddx, dx_blocks, columns,
+                       tile_rows(b.gradient), c.dbias, scale, 1.f - c.rows.smooth};
+    hipLaunchKernelGGL(loss_finish_kernel, dim3(static_cast<unsigned>(dx_blocks + bias_blocks)), dim3(256), 0, s, f);
     return hipGetLastError();
 }
 

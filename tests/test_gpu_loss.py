@@ -109,6 +109,32 @@ def test_targets(M):
     assert all(bool((b5[n] == 0).all()) for n in b5)
 
 
+@pytest.mark.parametrize("share", [0.0, 0.03, 0.5, 0.97, 1.0])
+@pytest.mark.parametrize("one", [True, False])
+def test_rows_brought_together(share, one):
+    """Calls large enough to bring the rows that count together: none of them,
+    a few at odd places, half, nearly all and all; a bad target among the rest."""
+    M, V, K = 2055, 60001, 1032
+    g, x, w, t = data(M, V, K, 67, ignored=False)
+    if share < 1:
+        t[torch.rand(M, generator=g, device="cuda") >= share] = -100
+    if share == 0.5:
+        t[17], t[2054] = V, 5
+    bias = torch.randn(V, generator=g, device="cuda")
+    r = gdn.linear_cross_entropy(x, w, t, bias=bias, label_smoothing=0.05)
+    dloss = torch.randn(1 if one else M, generator=g, device="cuda")
+    b = gdn.linear_cross_entropy_backward(dloss, x, w, t, r["lse"], bias=bias, label_smoothing=0.05)
+    want, lim = loss_backward64(dloss, x, w, bias, t, r["lse"], 0.05, 0.0)
+    for name, v, l in zip(("dx", "dw", "dbias"), want, lim):
+        close(name, b[name], v.cpu(), (l + (v.abs() + l) * HALF[b[name].dtype]).cpu())
+    if share == 0.0:
+        assert all(bool((b[n] == 0).all()) for n in b)
+    for name in b:
+        only = gdn.linear_cross_entropy_backward(dloss, x, w, t, r["lse"], bias=bias, label_smoothing=0.05,
+                                                 **{"want_" + n: n == name for n in ("dx", "dw", "dbias")})
+        assert torch.equal(only[name], b[name]), name
+
+
 @pytest.mark.parametrize("M", [5, 70])
 def test_masked_vocabulary(M):
     """A bias of -inf takes an entry out of the softmax; a bias of the type's
