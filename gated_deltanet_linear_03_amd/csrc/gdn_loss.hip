@@ -17,14 +17,16 @@
 // products that follow: dx, in 32 bits from piece to piece, and the piece's
 // rows of dw.  Rows without a target add nothing: a large call first brings the
 // others together, and all that follows is as long as there are of those (the
-// host does not know how many: tiles past them end at once).  dl is rounded to bf16 once, as dp is in the linear layer's
-// backward pass (dbias sums it in 32 bits before that), and not by itself but
-// over (1 - e) times the largest |g|, by which the outputs are multiplied in 32
-// bits: with one g for all rows the target's entry is then next to -1 and
-// rounds as any other value.  (Times g it would be next to -g in every row,
-// all of them off by the same up to 2^-8 of themselves: 4096 x 248320 x 2048
-// with g = 1/3686: dw 3.4e-3 off in its norm, of which 1.7e-3 are its own
-// rounding.)
+// host does not know how many: tiles past them end at once); in a small one dw
+// is formed from a copy of x in which they are zero, so that an infinity or NaN
+// in them does not reach it as 0 times that.
+// dl is rounded to bf16 once, as dp is in the linear layer's backward pass
+// (dbias sums it in 32 bits before that), and not by itself but over (1 - e)
+// times the largest |g|, by which the outputs are multiplied in 32 bits: with
+// one g for all rows the target's entry is then next to -1 and rounds as any
+// other value.  (Times g it would be next to -g in every row, all of them off
+// by the same up to 2^-8 of themselves: 4096 x 248320 x 2048 with g = 1/3686:
+// dw 3.4e-3 off in its norm, of which 1.7e-3 are its own rounding.)
 // Statistics are in base two: 2^(l log2 e - top), one multiply-add and one
 // v_exp_f32 a logit.
 #include <cmath>
@@ -77,6 +79,7 @@ struct LossProduct : GemmProduct {
     float* columns;                           // [row tiles][V] sums of dl, or NULL
     int64_t columns_ld;
     const int32_t* count;                     // device: how many of the M rows there are; NULL: all
+    uint16_t* clean;                          // [M][K]: receives x, zeros where a row has no target, or NULL
 };
 
 // row of a wave's accumulators acc[i][.] in lane l16
@@ -425,12 +428,39 @@ struct Gradient {
     }
 };
 
+// The work-groups after the tiles' write p.clean: up to kCleanGroups, a thread 8
+// values kCleanEach times at once (4096 x 2000 x 2048, forward and backward: 141
+// us without, 152 us with 1024 work-groups and once, 146 us so).
+constexpr int kCleanGroups = 256, kCleanEach = 8;
+
+__host__ __device__ inline int clean_groups(int64_t M, int64_t K, int threads) {
+    const int64_t n = (M * (K / 8) + threads - 1) / threads;
+    return static_cast<int>(n < kCleanGroups ? n : kCleanGroups);
+}
+
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, S::kPerSimd) void loss_gradient_kernel(LossProduct p) {
     __shared__ __align__(1024) uint8_t shared[S::kBytes];
-    if (p.count) {
-        p.M = p.out.M = *p.count;
-        if (blockIdx.x >= ((p.M + S::BM - 1) / S::BM) * ((p.N + S::BN - 1) / S::BN)) return;
+    if (p.count) p.M = p.out.M = *p.count;
+    const int64_t past = static_cast<int64_t>(blockIdx.x) - ((p.M + S::BM - 1) / S::BM) * ((p.N + S::BN - 1) / S::BN);
+    if (past >= 0) {
+        if (!p.clean) return;
+        const uint32_t per = static_cast<uint32_t>(p.K / 8), all = static_cast<uint32_t>(p.M) * per;
+        const uint32_t step = clean_groups(p.M, p.K, S::kThreads) * S::kThreads;
+        for (uint32_t i = static_cast<uint32_t>(past) * S::kThreads + threadIdx.x; i < all; i += kCleanEach * step) {
+            u32x4 q[kCleanEach];
+#pragma unroll
+            for (int u = 0; u < kCleanEach; ++u) {
+                const uint32_t at = i + u * step < all ? i + u * step : i, m = at / per, k = at % per * 8;
+                const int64_t t = target_of(p.rows, m);
+                const bool real = t != p.rows.ignore && t >= 0 && t < p.rows.V;
+                q[u] = *reinterpret_cast<const u32x4*>(real ? static_cast<const uint16_t*>(p.A) + m * p.lda + k : zero_chunk);
+            }
+#pragma unroll
+            for (int u = 0; u < kCleanEach; ++u)
+                if (i + u * step < all) *reinterpret_cast<u32x4*>(p.clean + 8 * static_cast<int64_t>(i + u * step)) = q[u];
+        }
+        return;
     }
     gemm_tile<true, true, Gradient<S>, S>(p, blockIdx.x, shared);
 }
@@ -613,7 +643,8 @@ hipError_t forward_t(const LossProduct& p, hipStream_t s) {
 
 template <typename S>
 hipError_t gradient_t(const LossProduct& p, hipStream_t s) {
-    hipLaunchKernelGGL((loss_gradient_kernel<S>), dim3(static_cast<unsigned>(tiles<S>(p))), dim3(S::kThreads), 0, s, p);
+    const int64_t n = tiles<S>(p) + (p.clean ? clean_groups(p.M, p.K, S::kThreads) : 0);
+    hipLaunchKernelGGL((loss_gradient_kernel<S>), dim3(static_cast<unsigned>(n)), dim3(S::kThreads), 0, s, p);
     return hipGetLastError();
 }
 
@@ -840,7 +871,7 @@ static BackwardWs backward_ws(int64_t M, int64_t V, int64_t K, const Plan& b) {
     w.off_place = w.off_scale + 256;          // the rows that count: their places, and their number before them
     w.off_rows = w.off_place + (b.gather ? round_256(4 * M) : 0);
     w.off_x = w.off_rows + (b.gather ? 3 * round_256(4 * M) : 0);
-    w.total = w.off_x + (b.gather ? round_256(2 * M * K) : 0);
+    w.total = w.off_x + round_256(2 * M * K);
     return w;
 }
 
@@ -902,6 +933,7 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
         rows.lse = l.lse;
         if (!rows.dloss_one) rows.dloss = l.dloss;
     }
+    uint16_t* const clean = c.dw && !b.gather ? reinterpret_cast<uint16_t*>(base + w.off_x) : nullptr;
     for (int64_t v0 = 0; v0 < c.V; v0 += b.piece) {
         const int64_t n = c.V - v0 < b.piece ? c.V - v0 : b.piece;
         LossProduct p{};
@@ -916,6 +948,7 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
         p.out.ep.y = dl; p.out.ep.ldy = w.ld; p.out.ep.bf16 = 1;
         p.columns = c.dbias ? columns : nullptr;
         p.columns_ld = c.V;
+        p.clean = v0 == 0 ? clean : nullptr;
         hipError_t e = gradient(p, b.gradient, s);
         if (e != hipSuccess) return e;
         if (!c.dx && !c.dw) continue;
@@ -933,7 +966,7 @@ hipError_t launch_loss_backward(const LossCall& c, void* ws, hipStream_t s) {
             px.ep.residual = v0 > 0 ? sums : nullptr; px.ep.ldr = c.K;
         }
         pw.A = dl; pw.lda = w.ld;
-        pw.B = x; pw.ldb = ldx;
+        pw.B = clean ? clean : x; pw.ldb = clean ? c.K : ldx;
         pw.M = n; pw.N = c.K; pw.K = c.M;
         pw.ep.bf16 = 1;
         pw.ep.y = c.dw ? static_cast<uint16_t*>(c.dw) + v0 * c.lddw : nullptr; pw.ep.ldy = c.lddw;

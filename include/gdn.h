@@ -783,11 +783,10 @@ gdn_status gdn_norm_backward(const gdn_norm_grad* grad, void* workspace,
  *
  * x and w in bf16, products accumulated and everything of a row in fp32.  A row
  * whose target is ignore_index has loss 0 and adds nothing to the gradients,
- * whatever its logits are (its lse is given all the same; an infinity or NaN in
- * its row of x may reach dw, as 0 times that).  A row whose target
- * is neither that nor in [0, V) has loss NaN, adds nothing to the gradients,
- * and GDN_STATUS_BAD_INDEX is ORed into status (never cleared).  This library's own kernels
- * at every size; the same bits from call to call.
+ * whatever its row of x holds (its lse is given all the same).  A row whose
+ * target is neither that nor in [0, V) has loss NaN, adds nothing to the
+ * gradients, and GDN_STATUS_BAD_INDEX is ORed into status (never cleared).
+ * This library's own kernels at every size; the same bits from call to call.
  * Row strides in elements, 0 means dense; a single row's is not looked at.
  * x, w: 16-byte aligned, K and their strides multiples of 8 up to 2^22; the
  * others element aligned. */
@@ -812,7 +811,7 @@ typedef struct {
 /* Bytes of device workspace; 0 on error.  Forward about 12 bytes for each row
  * and 64 to 256 columns of the vocabulary; backward dl in bf16 for as many
  * columns as 256 MiB hold (4096 at the least), dx once or a few times in fp32,
- * and in large calls a copy of x. */
+ * and a copy of x. */
 size_t gdn_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K);
 size_t gdn_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
 

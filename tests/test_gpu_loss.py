@@ -179,6 +179,36 @@ def test_infinite_rows():
         assert bool(b["dx"][7].isnan().any()) and torch.equal(b["dx"][others], want["dx"][others])
 
 
+@pytest.mark.parametrize("M,V,K,stride", [(5, 300, 64, 64), (130, 700, 72, 72), (130, 700, 72, 80), (700, 1000, 1032, 1032), (600, 50001, 1000, 1008)])
+def test_unset_rows(M, V, K, stride):
+    """Rows without a target hold anything (the padding of a batch that nobody
+    wrote): no gradient sees it, in small calls and in large ones, nor with one
+    target of the vocabulary's end."""
+    g, x, w, t = data(M, V, K, 68, ignored=False)
+    t[1::3] = -100
+    t[0] = V - 1
+    t[M - 1] = V                                # not an index: its loss is NaN, and it adds nothing either
+    out = t == -100
+    out[M - 1] = True
+    held = torch.zeros(M, stride, dtype=x.dtype, device="cuda")[:, :K]
+    held.copy_(x)
+    held[out] = 0
+    any_ = held.clone() if stride == K else torch.zeros(M, stride, dtype=x.dtype, device="cuda")[:, :K].copy_(held)
+    rows = out.nonzero()[:, 0]
+    for i, v in enumerate((float("nan"), float("inf"), -float("inf"), 3e38)):
+        any_[rows[i::4]] = v
+    lse = gdn.linear_cross_entropy(held, w, t)["lse"]
+    r = gdn.linear_cross_entropy(any_, w, t)
+    assert torch.equal(r["lse"][~out], lse[~out])
+    for dloss in (torch.full((1,), 0.5, device="cuda"), torch.randn(M, generator=g, device="cuda")):
+        want = gdn.linear_cross_entropy_backward(dloss, held, w, t, lse, want_dbias=True)
+        b = gdn.linear_cross_entropy_backward(dloss, any_, w, t, r["lse"], want_dbias=True)
+        assert all(torch.equal(b[n], want[n]) and bool(b[n].isfinite().all()) for n in want)
+        assert bool((b["dx"][out] == 0).all())
+        only = gdn.linear_cross_entropy_backward(dloss, any_, w, t, r["lse"], want_dx=False)
+        assert torch.equal(only["dw"], want["dw"])
+
+
 def test_nothing_outside():
     """Guards around every written buffer, and around the workspaces."""
     for M, V, K in ((3, 77, 40), (67, 301, 72)):
