@@ -1495,7 +1495,9 @@ class AdamW:
     elements.  copies: bf16 tensors of the parameters' sizes (or None, alone
     or in the list) that receive the new values.  weight_decay: a number, or
     one for each tensor.  seed: of the random rounding of 8-bit states.
-    adamw_states() makes the states."""
+    adamw_states() makes the states.  The lists are read here, once: a step
+    updates the memory that their tensors have now, and refuses a parameter
+    that has been given other memory since."""
 
     def __init__(self, params, m, v, m_scale=None, v_scale=None, copies=None, beta1=0.9, beta2=0.999,
                  eps=1e-8, weight_decay=0.0, seed=0):
@@ -1513,6 +1515,9 @@ class AdamW:
                 raise ValueError(f"{name}: {n} entries needed, not {len(x)}")
         for name in lists:
             setattr(self, name, list(lists[name]))
+        # (aliases: the memory lives as long as this does, whatever the caller's tensors become)
+        self._held = [t.detach() for k in ("params", "m", "v", "m_scale", "v_scale", "copies")
+                      for t in getattr(self, k) if t is not None]
         self.beta1, self.beta2, self.eps, self.seed = float(beta1), float(beta2), float(eps), int(seed) & 0xFFFFFFFF
         dev = self.device = _device()
         import torch
@@ -1527,6 +1532,7 @@ class AdamW:
                 "offsets": [CAdamWTensor.grad.offset, CAdamWTensor.grad_dtype.offset],
                 "itemsize": ctypes.sizeof(CAdamWTensor)})
         self._sizes = [p.numel() for p in self.params]
+        self._at = [p.data_ptr() for p in self.params]
         self._c = (CAdamWTensor * n)()
         for i, p in enumerate(self.params):
             size = p.numel()
@@ -1574,16 +1580,18 @@ def adamw_states(params, bits=32):
 
 def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
     """One AdamW step of opt's tensors: grads, bf16 or fp32 of the parameters'
-    sizes, contiguous (None: that tensor is left as it is).  lr: a number, or a one-element fp32 device
-    tensor; step: the step's number, from 1 on, or a one-element int32 device
-    tensor: a captured step reads those at every replay.  grad_scale: a
-    one-element fp32 device tensor, a factor of every gradient; when it is not
-    finite nothing is written."""
+    sizes, contiguous (None: that tensor is left as it is).  lr: a number, or a
+    one-element fp32 device tensor; step: the step's number, from 1 on, or a
+    one-element int32 device tensor: a captured step reads those at every
+    replay.  grad_scale: a one-element fp32 device tensor, a factor of every
+    gradient; when it is not finite nothing is written."""
     n, dev, torch = len(opt.params), _device(), _torch
     if dev != opt.device:
         raise ValueError(f"opt: made on cuda:{opt.device}, the current device is cuda:{dev}")
     if len(grads) != n:
         raise ValueError(f"grads: {n} entries needed, not {len(grads)}")
+    if [p.data_ptr() for p in opt.params] != opt._at:
+        raise ValueError("opt: a parameter's memory is not the one that it was made with")
     a = CAdamW(opt.bits, opt.beta1, opt.beta2, 0.0, opt.eps, 0, opt.seed, None, None, None)
     if isinstance(lr, torch.Tensor):
         a.lr_ptr = _flat(lr, "lr", 1, (torch.float32,), dev)

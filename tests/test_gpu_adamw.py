@@ -299,3 +299,23 @@ def test_binding_refuses():
     with pytest.raises(gdn.GdnError):
         gdn.adamw_step(opt, g, lr=1e-3, step=0)
     assert float(p[0].abs().max()) == 0
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_moved_memory(bits):
+    """A parameter with other memory than at the start is refused; states that
+    the caller lets go of stay alive."""
+    p = [torch.ones(300, device="cuda"), torch.ones(70, device="cuda")]
+    st = gdn.adamw_states(p, bits)
+    opt = gdn.AdamW(p, **st)
+    was = opt._held[0]
+    p[0].data = torch.full((300,), 2.0, device="cuda")
+    g = [torch.ones_like(x) for x in p]
+    with pytest.raises(ValueError, match="memory"):
+        gdn.adamw_step(opt, g, lr=1e-2, step=1)
+    assert float((was - 1).abs().max()) == 0 and float((p[0] - 2).abs().max()) == 0 and float((p[1] - 1).abs().max()) == 0
+    opt = gdn.AdamW(p, **st)
+    for t in st["m"] + st["v"]:
+        t.data = torch.empty(0, dtype=t.dtype, device="cuda")
+    gdn.adamw_step(opt, g, lr=1e-2, step=1)
+    assert float((p[0] - 1.99).abs().max()) < 1e-5 and float((p[1] - 0.99).abs().max()) < 1e-5
