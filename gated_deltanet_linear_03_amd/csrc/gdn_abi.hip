@@ -1571,7 +1571,7 @@ gdn_status gdn_norm(const gdn_norm_io* io, void* stream) {
 size_t gdn_norm_backward_workspace_bytes(int64_t M, int64_t D) {
     g_err[0] = 0;
     if (check_norm(M, D, GDN_NORM_LAYER) != GDN_OK) return 0;
-    const int64_t n = round_up(8 * gdn::norm_parts(M, D) * D, 256);
+    const int64_t n = M > 0 ? round_up(8 * gdn::norm_parts(M, D) * D, 256) : 0;
     return static_cast<size_t>(n < 256 ? 256 : n);
 }
 
