@@ -784,15 +784,22 @@ double plan_products(int64_t M, int64_t piece, int64_t K, bool one, Plan* b) {
     return least;
 }
 
-// Pieces of up to 256 MiB of dl (no less than 4096 columns).  Smaller ones stay
-// in the last-level cache, which changes little (4096 x 248320 x 2048: 9.45 ms
-// with 64 MiB, 9.6 with 512); how the tiles of a piece fill the card does.
-constexpr int64_t kPieceBytes = int64_t(256) << 20, kLeastPiece = 4096;
+// Pieces of up to 160 MiB of dl, which stay in the last-level cache from the
+// launch that writes them to the one that reads them twice (2048 x 128000 x
+// 1024, forward and backward: 1.93 ms in pieces of 125 MiB, 1.98 in ones of
+// 250; 4096 x 248320 x 2048: 12.6 to 13.3 ms at 8 to 24 pieces, in no order).
+// Of up to 8192 columns they hold 256 MiB, as dx's sums go out and in with each
+// piece (16384 x 128000 x 1024: 13.8 ms, 15.0 in pieces of 4096 columns), and
+// they have no fewer than 4096.
+constexpr int64_t kPieceBytes = int64_t(160) << 20, kWidePieceBytes = int64_t(256) << 20, kWidePiece = 8192, kLeastPiece = 4096;
 
 Plan plan_of(int64_t M, int64_t V, int64_t K) {
     Plan best{};
     double least = 1e30;
-    int64_t most = kPieceBytes / (2 * (M > 0 ? M : 1)) / 256 * 256;
+    const int64_t rows = 2 * (M > 0 ? M : 1);
+    int64_t most = kWidePieceBytes / rows / 256 * 256;
+    if (most > kWidePiece) most = kWidePiece;
+    if (most < kPieceBytes / rows / 256 * 256) most = kPieceBytes / rows / 256 * 256;
     if (most < kLeastPiece) most = kLeastPiece;
     int64_t before = 0;
     // (one piece of at most 32 MiB: it is launched fewer times than any other)

@@ -810,8 +810,8 @@ typedef struct {
 
 /* Bytes of device workspace; 0 on error.  Forward about 12 bytes for each row
  * and 64 to 256 columns of the vocabulary; backward dl in bf16 for as many
- * columns as 256 MiB hold (4096 at the least), dx once or a few times in fp32,
- * and a copy of x. */
+ * columns as 160 MiB hold (256 MiB up to 8192 columns; 4096 at the least), dx
+ * once or a few times in fp32, and a copy of x. */
 size_t gdn_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K);
 size_t gdn_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
 
