@@ -9,6 +9,7 @@
 // of dy.  A work-group keeps its columns' sums of all its rows in registers
 // and leaves them once; a second kernel adds the work-groups' sums in order.
 // Everything is in 32 bits between the loads and the stores.
+// Bound: HBM, and the launch where there are few rows (1 x 2048: 3.1 us).
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -114,8 +115,9 @@ __device__ __forceinline__ void row_sums(float* s, float* red, int t) {
 constexpr int rows_of(int T) { return T < 256 ? 256 / T : 1; }   // rows that a work-group holds at a time
 
 // The rows all at once: one block of them a work-group (more only where the
-// grid would be past what a launch holds).  4096 x 2048 in fp32 to bf16: 9.4
-// us, 12.3 with work-groups that stay.  MASK: D is not W T NV.
+// grid would be past what a launch holds).  4096 x 2048 in fp32 to bf16: 9.4 us
+// with the call (the kernel 8.4, 6.0 TB/s), 12.3 with work-groups that stay.
+// MASK: D is not W T NV.
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_row_kernel(NormParams p) {
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T);
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_row_kernel(NormParams 
 // Many long rows: a work-group takes every gridDim-th block of them and keeps
 // its columns' weights in registers (read again for each row they are several
 // times the row's own bytes), the next row on its way while one is summed.
-// 32768 x 4096 in bf16: 97 us, 131 with a wave a row.
+// 32768 x 4096 in bf16: 97 to 125 us (4.3 to 5.5 TB/s), 131 with a wave a row.
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormParams p) {
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
@@ -298,8 +300,8 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormPar
 // ---- backward ------------------------------------------------------------------
 // A work-group takes every gridDim-th block of rows, the next one on its way
 // while one is summed.  part: [work-group][2][D] sums of dy xh and of dy.
-// Bound: HBM (32768 x 4096 in bf16 without d_residual 154 us, 5.2 TB/s; in
-// fp32 to bf16 223 us, 6.0 TB/s).
+// Bound: HBM (32768 x 4096 in bf16 with d_residual 186 us, 5.8 TB/s, without 154,
+// 5.2; in fp32 to bf16 223 us, 6.0 TB/s).
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormParams p) {
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
