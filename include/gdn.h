@@ -712,8 +712,10 @@ gdn_status gdn_linear_tiles(int64_t M, int64_t N, int64_t K, int32_t backward,
  *
  * in fp32 between x and y, each of which is bf16 or fp32; the variance is the
  * mean square of the differences to the mean.  A row's bits do not depend on
- * the other rows.  Row strides in elements, 0 means dense, a single row's is
- * not looked at; they and the addresses need no more than element alignment. */
+ * the other rows, and on how many there are only in that rows of more than 1024
+ * are summed in another order from M D = 2^25 on.  Row strides in elements, 0
+ * means dense, a single row's is not looked at; they and the addresses need no
+ * more than element alignment. */
 #define GDN_NORM_LAYER 0
 #define GDN_NORM_RMS 1
 

@@ -179,7 +179,7 @@ def test_infinite_rows():
         assert bool(b["dx"][7].isnan().any()) and torch.equal(b["dx"][others], want["dx"][others])
 
 
-@pytest.mark.parametrize("M,V,K,stride", [(5, 300, 64, 64), (130, 700, 72, 72), (130, 700, 72, 80), (700, 1000, 1032, 1032), (600, 50001, 1000, 1008)])
+@pytest.mark.parametrize("M,V,K,stride", [(5, 300, 64, 64), (130, 700, 72, 72), (130, 700, 72, 80), (700, 1000, 1032, 1032), (600, 50001, 1000, 1008), (1300, 60001, 1032, 1032)])
 def test_unset_rows(M, V, K, stride):
     """Rows without a target hold anything (the padding of a batch that nobody
     wrote): no gradient sees it, in small calls and in large ones, nor with one
@@ -301,3 +301,29 @@ def test_stream_and_graph(M):
         eb = gdn.linear_cross_entropy_backward(dloss, x, w, t, eager["lse"], z_loss=1e-4, want_dbias=True)
         assert all(torch.equal(eb[n], b[n]) for n in b)
     del gs
+
+
+@pytest.mark.parametrize("one", [True, False])
+def test_graph_of_a_large_call(one):
+    """Captured with all rows counting, replayed with half of them, none, one
+    and all: the tiles follow the targets that a replay finds."""
+    M, V, K = 1300, 60001, 1032
+    g, x, w, t = data(M, V, K, 69, ignored=False)
+    t0 = t.clone()
+    dloss = torch.randn(1 if one else M, generator=g, device="cuda")
+    lse = gdn.linear_cross_entropy(x, w, t)["lse"]
+    warm = gdn.linear_cross_entropy_backward(dloss, x, w, t, lse, want_dbias=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b = gdn.linear_cross_entropy_backward(dloss, x, w, t, lse, want_dbias=True)
+    for share in (0.5, 0.0, 1.0, 0.9):
+        t.copy_(torch.where(torch.rand(M, generator=g, device="cuda") < share, t0, -100))
+        if share == 0.0:
+            t[M - 1] = 3
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = gdn.linear_cross_entropy_backward(dloss, x, w, t, lse, want_dbias=True)
+        assert all(torch.equal(eager[n], b[n]) for n in b), share
+        if share == 1.0:
+            assert all(torch.equal(warm[n], b[n]) for n in b)

@@ -146,6 +146,18 @@ def test_rows_are_their_own():
     assert torch.equal(gdn.norm(x[2:3], w, None), plain[2:3])
 
 
+@pytest.mark.parametrize("M,D", [(8191, 4096), (4097, 8190), (40000, 1024), (3, 2050)])
+def test_bits_of_some_rows(M, D):
+    """A row alone, among a few and among many (fewer than 2^25 values in all,
+    or rows of up to 1024): the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(M, D, generator=g, device="cuda").to(BF16)
+    w = torch.randn(D, generator=g, device="cuda")
+    y = gdn.norm(x, w, w)
+    for a, b in ((0, 1), (M - 1, M), (M // 2, M // 2 + 2), (1, min(M, 700))):
+        assert torch.equal(gdn.norm(x[a:b], w, w), y[a:b])
+
+
 def test_no_rows():
     x = torch.empty((0, 16), device="cuda")
     assert gdn.norm(x).shape == (0, 16)
