@@ -1590,7 +1590,9 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
         raise ValueError(f"opt: made on cuda:{opt.device}, the current device is cuda:{dev}")
     if len(grads) != n:
         raise ValueError(f"grads: {n} entries needed, not {len(grads)}")
-    if [p.data_ptr() for p in opt.params] != opt._at:
+    # (methods mapped over the lists: a tenth less time than a comprehension's calls)
+    of = torch.Tensor
+    if list(map(of.data_ptr, opt.params)) != opt._at:
         raise ValueError("opt: a parameter's memory is not the one that it was made with")
     a = CAdamW(opt.bits, opt.beta1, opt.beta2, 0.0, opt.eps, 0, opt.seed, None, None, None)
     if isinstance(lr, torch.Tensor):
@@ -1611,15 +1613,16 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
     none = [i for i, g in enumerate(grads) if g is None]
     if none:
         grads = [opt.params[i] if g is None else g for i, g in enumerate(grads)]     # (whose n is 0)
-    kinds = [g.dtype for g in grads]
-    if not ([g.numel() for g in grads] == opt._sizes and {bf16, fp32}.issuperset(kinds)
-            and all(g.is_contiguous() and g.get_device() == dev for g in grads)):
+    kinds = list(map(of.dtype.__get__, grads))
+    if not (list(map(of.numel, grads)) == opt._sizes and {bf16, fp32}.issuperset(kinds)
+            and all(map(of.is_contiguous, grads)) and {dev}.issuperset(map(of.get_device, grads))):
         for i, g in enumerate(grads):
             _flat(g, f"grads[{i}]", opt._sizes[i], (bf16, fp32), dev)
     if n:
         table = _np.frombuffer(c, dtype=_ADAMW_TABLE)
-        table["grad"] = [g.data_ptr() for g in grads]
-        table["grad_dtype"] = [k is bf16 for k in kinds]
+        table["grad"] = list(map(of.data_ptr, grads))
+        halves = kinds.count(bf16)
+        table["grad_dtype"] = [k is bf16 for k in kinds] if 0 < halves < n else halves > 0
         for i in none:
             c[i].n = 0
     _check(lib().gdn_adamw_step(ctypes.byref(a), c, n, _raw_stream(stream, dev)))
