@@ -78,6 +78,36 @@ struct Columns {
     }
     __device__ __forceinline__ bool fresh(int j, int e) const { return (NV > 1 && j < NV / 2) || at[j] + e >= from[j]; }
     __device__ __forceinline__ bool any(int j, int64_t D) const { return (NV > 1 && j < NV / 2) || from[j] < D; }
+
+    // A value of p for each column (NULL: `none`), and one to each that counts
+    // here, four at a time (16 x 8192 in bf16, backward: one by one 17 us, so 8;
+    // 32768 x 4096, forward and backward: 279 and 265).
+    __device__ __forceinline__ void load(const float* p, float none, float* v) const {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int g = 0; g < W / 4; ++g) {
+                Run<false, 4> q;
+                if (p) q.load(p, at[j] + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[W * j + 4 * g + e] = p ? q.get(e) : none;
+            }
+    }
+    __device__ __forceinline__ void store(float* p, const float* v) const {
+        typedef float V __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if ((NV > 1 && j < NV / 2) || from[j] == at[j]) {
+#pragma unroll
+                for (int g = 0; g < W / 4; ++g)
+                    *reinterpret_cast<V*>(p + at[j] + 4 * g) = V{v[W * j + 4 * g], v[W * j + 4 * g + 1], v[W * j + 4 * g + 2], v[W * j + 4 * g + 3]};
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (fresh(j, e)) p[at[j] + e] = v[W * j + e];
+            }
+        }
+    }
 };
 
 // Sums of N values over the T threads of a row, in every one of them.  red:
@@ -198,13 +228,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormPar
     Columns<W, T, NV> cols;
     cols.init(t, p.D);
     float w[C], b[C];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            w[W * j + e] = p.weight ? p.weight[cols.at[j] + e] : 1.f;
-            b[W * j + e] = p.bias ? p.bias[cols.at[j] + e] : 0.f;
-        }
+    cols.load(p.weight, 1.f, w);
+    cols.load(p.bias, 0.f, b);
     const float per = 1.f / static_cast<float>(p.D);
     int turn = 0;
     // (rows past the end read the last one)
@@ -311,13 +336,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
     Columns<W, T, NV> cols;
     cols.init(t, p.D);
     float w[C], dw[C], db[C];
+    cols.load(p.weight, 1.f, w);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            w[W * j + e] = p.weight ? p.weight[cols.at[j] + e] : 1.f;
-            dw[W * j + e] = db[W * j + e] = 0.f;
-        }
+    for (int i = 0; i < C; ++i) dw[i] = db[i] = 0.f;
     const float per = 1.f / static_cast<float>(p.D);
     const bool params = p.part != nullptr;
     int turn = 0;
@@ -396,16 +417,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
     const bool only = gridDim.x == 1;
     float* const ow = only ? p.dweight : p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
     float* const ob = only ? p.dbias : ow + p.D;
-    if constexpr (R == 1) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (!MASK || cols.fresh(j, e)) {
-                    if (ow) ow[cols.at[j] + e] = dw[W * j + e];
-                    if (ob) ob[cols.at[j] + e] = db[W * j + e];
-                }
-    } else {                                  // the rows' sums, added in order
+    if constexpr (R > 1) {                    // the rows' sums, added in order
         __shared__ float all[R - 1][2 * C][T];
         if (r > 0) {
 #pragma unroll
@@ -423,15 +435,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
                 dw[i] += all[k][i][t];
                 db[i] += all[k][C + i][t];
             }
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (!MASK || cols.fresh(j, e)) {
-                    if (ow) ow[cols.at[j] + e] = dw[W * j + e];
-                    if (ob) ob[cols.at[j] + e] = db[W * j + e];
-                }
     }
+    if (ow) cols.store(ow, dw);
+    if (ob) cols.store(ob, db);
 }
 
 template <bool XB, bool YB>
@@ -562,19 +568,22 @@ hipError_t forward(const NormParams& p, hipStream_t s) {
 }
 
 // Work-groups of the backward pass, each of which leaves a sum for each column:
-// one a compute unit with two blocks of rows at least (256 x 8192: 18 us, 20
-// with one block each), and two where the rows come to 2^24 values and fit, in
-// bf16 or up to 1024 columns (8192 x 4096 in bf16: 58 and 62 us, 4096 x 4096:
-// 42 and 39; 32768 x 4096 in fp32: 243 and 223).  Rows that are read in steps:
-// up to 64, for the parameters' sums.  A few blocks of rows go to one
-// work-group, whose sums no second kernel has to add.
+// one for each block of rows up to 64 (100 x 2048 in bf16: 6.6 us from a graph,
+// 7.3 with two blocks each), then with two blocks at least (100 x 8192 in fp32:
+// 9.5, 10.3 with one each) up to one a compute unit, and two where the rows come
+// to 2^24 values and fit, in bf16 or up to 1024 columns (8192 x 4096 in bf16: 58
+// and 62 us, 4096 x 4096: 42 and 39; 32768 x 4096 in fp32: 243 and 223).  Rows
+// that are read in steps: up to 64, for the parameters' sums.  A few blocks of
+// rows go to one work-group, whose sums no second kernel has to add: a launch
+// less, 3 us of the host's, for about 1 us more on the device (4 x 8192 in bf16:
+// 7.7 and 6.6 us; 100 x 64: 6.4 and 7.0; 4 x 16000: 14.6 and 10.6, so two there).
 int64_t norm_parts_of(int64_t M, int64_t D, bool both_bf16) {
     const bool in_steps = D < 8 || D > kLongRow;
     const int64_t rows = D > 2048 || D < 8 ? 1 : D > 1024 ? 2 : D > 256 ? 4 : D > 64 ? 8 : 16;
     const bool two = M * D >= (int64_t(1) << 24) && (D <= 1024 || (both_bf16 && D <= 4096));
     const int64_t most = in_steps ? 64 : (two ? 2 : 1) * compute_units();
-    if (M <= 4 * rows) return 1;
-    const int64_t n = (M + 2 * rows - 1) / (2 * rows);
+    if (M <= (D > 8192 ? 2 : D > 256 ? 4 : 8) * rows) return 1;
+    const int64_t each = (M + rows - 1) / rows, n = each <= 64 ? each : (M + 2 * rows - 1) / (2 * rows);
     return n < most ? n : most;
 }
 
