@@ -570,18 +570,21 @@ hipError_t forward(const NormParams& p, hipStream_t s) {
 // Work-groups of the backward pass, each of which leaves a sum for each column:
 // one for each block of rows up to 64 (100 x 2048 in bf16: 6.6 us from a graph,
 // 7.3 with two blocks each), then with two blocks at least (100 x 8192 in fp32:
-// 9.5, 10.3 with one each) up to one a compute unit, and two where the rows come
-// to 2^24 values and fit, in bf16 or up to 1024 columns (8192 x 4096 in bf16: 58
-// and 62 us, 4096 x 4096: 42 and 39; 32768 x 4096 in fp32: 243 and 223).  Rows
-// that are read in steps: up to 64, for the parameters' sums.  A few blocks of
-// rows go to one work-group, whose sums no second kernel has to add: a launch
-// less, 3 us of the host's, for about 1 us more on the device (4 x 8192 in bf16:
-// 7.7 and 6.6 us; 100 x 64: 6.4 and 7.0; 4 x 16000: 14.6 and 10.6, so two there).
+// 9.5, 10.3 with one each) up to as many a compute unit as are fastest: four up
+// to 512 columns (2^25 values in rows of 256 in bf16: 84, 57, 46, 42 and 49 us
+// with 1, 2, 3, 4 and 6; of 300 in fp32 156, 102, 87, 87, 91), two up to 1536
+// (of 768 in bf16 71, 48, 60, 53, 58) and where 2^24 values fit, up to 2048
+// columns or 4096 in bf16 (8192 x 4096 in bf16: 58 and 50, 4096 x 4096: 34 and
+// 33; 32768 x 4096 in fp32: 221 and 244).  Rows that are read in steps: up to
+// 64, for the parameters' sums.  A few blocks of rows go to one work-group,
+// whose sums no second kernel has to add: a launch less, 3 us of the host's, for
+// about 1 us more on the device (4 x 8192 in bf16: 7.7 and 6.6 us; 100 x 64: 6.4
+// and 7.0; 4 x 16000: 14.6 and 10.6, so two there).
 int64_t norm_parts_of(int64_t M, int64_t D, bool both_bf16) {
     const bool in_steps = D < 8 || D > kLongRow;
     const int64_t rows = D > 2048 || D < 8 ? 1 : D > 1024 ? 2 : D > 256 ? 4 : D > 64 ? 8 : 16;
-    const bool two = M * D >= (int64_t(1) << 24) && (D <= 1024 || (both_bf16 && D <= 4096));
-    const int64_t most = in_steps ? 64 : (two ? 2 : 1) * compute_units();
+    const bool two = D <= 1536 || (M * D >= (int64_t(1) << 24) && (D <= 2048 || (both_bf16 && D <= 4096)));
+    const int64_t most = in_steps ? 64 : (D <= 512 ? 4 : two ? 2 : 1) * compute_units();
     if (M <= (D > 8192 ? 2 : D > 256 ? 4 : 8) * rows) return 1;
     const int64_t each = (M + rows - 1) / rows, n = each <= 64 ? each : (M + 2 * rows - 1) / (2 * rows);
     return n < most ? n : most;
