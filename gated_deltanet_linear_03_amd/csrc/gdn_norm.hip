@@ -219,7 +219,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_row_kernel(NormParams 
 // Many long rows: a work-group takes every gridDim-th block of them and keeps
 // its columns' weights in registers (read again for each row they are several
 // times the row's own bytes), the next row on its way while one is summed.
-// 32768 x 4096 in bf16: 97 to 125 us (4.3 to 5.5 TB/s), 131 with a wave a row.
+// 32768 x 4096 in bf16: 89 to 123 us (4.4 to 6.0 TB/s), 131 with a wave a row.
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormParams p) {
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
@@ -325,8 +325,8 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormPar
 // ---- backward ------------------------------------------------------------------
 // A work-group takes every gridDim-th block of rows, the next one on its way
 // while one is summed.  part: [work-group][2][D] sums of dy xh and of dy.
-// Bound: HBM (32768 x 4096 in bf16 with d_residual 186 us, 5.8 TB/s, without 154,
-// 5.2; in fp32 to bf16 223 us, 6.0 TB/s).
+// Bound: HBM (32768 x 4096 in bf16 with d_residual 170 to 180 us, 6.0 to 6.3 TB/s;
+// in fp32 to bf16 222 us, 6.0 TB/s).
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormParams p) {
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
