@@ -218,7 +218,7 @@ struct Largest {
     // the scale of this lane's block and kind
     __device__ __forceinline__ float scale(const Step& s, int lane) const {
         const double m = fabs(new_m(s, old, grad)), r = new_r(s, old, grad);
-        const float v = static_cast<float>((lane % 2 ? r : m) * (1.0 / 448));
+        const float v = static_cast<float>((lane % 2 ? r : m) / 448.0);   // (not times 1 / 448: ties)
         // (next to nothing counts as nothing: the ratios stay finite)
         return !(top < __builtin_inff()) ? top : top < 0x1p-100f ? 0.f : v;
     }

@@ -319,3 +319,30 @@ def test_moved_memory(bits):
         t.data = torch.empty(0, dtype=t.dtype, device="cuda")
     gdn.adamw_step(opt, g, lr=1e-2, step=1)
     assert float((p[0] - 1.99).abs().max()) < 1e-5 and float((p[1] - 0.99).abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("grad", [BF16, FP32])
+def test_codes_to_the_last(grad):
+    """Scales and codes of 8-bit states are the formula's, none but by a border:
+    in 64 bits from the states as they stand in 32, over scales in 32."""
+    rng = np.random.RandomState(19)
+    sizes = [int(n) for n in rng.randint(1, 700, 200)] + [70001]
+    p, grads, states = tensors(sizes, 91, 8, grad, False, first=1)
+    opt = gdn.AdamW(p, **states, beta1=0.9, beta2=0.95, seed=4)
+    old = {k: [f64(t) for t in states[k]] for k in ("m", "v", "m_scale", "v_scale")}
+    gdn.adamw_step(opt, grads, lr=1e-3, step=33)
+    for i, n in enumerate(sizes):
+        block = np.arange(n) // 256
+        m, r = ((old[k][i] * old[k + "_scale"][i][block]).astype(np.float32) for k in ("m", "v"))
+        g, v = f64(grads[i]), (r * r).astype(np.float64)
+        lo, hi = random_halves(4, 33, i, n)
+        for name, value, u in (("m", opt.beta1 * m.astype(np.float64) + (1 - opt.beta1) * g, lo),
+                               ("v", np.sqrt(opt.beta2 * v + (1 - opt.beta2) * g * g), hi)):
+            full = np.zeros(-(-n // 256) * 256)
+            full[:n] = np.abs(value)
+            scale = f64(getattr(opt, name + "_scale")[i])
+            assert (scale == (full.reshape(-1, 256).max(1) / 448).astype(np.float32)).all(), (name, i)
+            want = up_or_down(np.clip(value / scale[block], -448, 448), u)[0]
+            if name == "v":
+                want = np.where((want == 0) & (value > 0), 2.0 ** -9, want)
+            assert (f64(getattr(opt, name)[i]) == want).all(), (name, i)
