@@ -18,7 +18,7 @@
 // otherwise than the formula does, each of them by a whole step.  So the
 // scales come from the largest value in 64 bits, and a block with a value that
 // lies nearer to its border than 32 bits can tell (one or two in a hundred)
-// takes them from 64 bits: 269.5 M elements take 783 us, 948 with all of them in
+// takes them from 64 bits: 269.5 M elements take 783 to 802 us, 948 with all of them in
 // 64 bits and 745 with none.
 //
 // Bound: HBM.  Each element is read and written once: 28 bytes with 32-bit
