@@ -57,10 +57,10 @@ def listed():
         # the projections, norms and gates of 8 layers, states in 32 bits
         dict(name="adamw 8 layers", op="adamw", bits=32, sizes="8*25296896+8*8388608+16*2048+16*32", grad="bf16", copy=True),
         # the same with states in 8 bits
-        dict(name="adamw 8 layers in 8 bits", op="adamw", bits=8, sizes="8*25296896+8*8388608+16*2048+16*32", grad="bf16",
+        dict(name="adamw 8 layers, 8 bits", op="adamw", bits=8, sizes="8*25296896+8*8388608+16*2048+16*32", grad="bf16",
              copy=True),
         # odd sizes in 8 bits, tensors that end inside a block
-        dict(name="adamw ragged in 8 bits", op="adamw", bits=8, sizes="1*1+3*1023+2*300001+1*9173505+5*77", grad="fp32",
+        dict(name="adamw ragged, 8 bits", op="adamw", bits=8, sizes="1*1+3*1023+2*300001+1*9173505+5*77", grad="fp32",
              copy=False),
     ]
 
