@@ -1452,8 +1452,9 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, bias=None, label_sm
                                   ignore_index=-100, want_dx=True, want_dw=True, want_dbias=None, dx=None,
                                   dw=None, dbias=None, workspace=None, stream=None):
     """Gradients of linear_cross_entropy() from dloss, fp32 [M] or of one
-    element for all rows (for a mean: 1 / the rows that count): a dict with dx
-    [M, K] and dw [V, K] (bf16) and dbias [V] (fp32; by default with a bias).
+    element for all rows (for a mean: 1 / the rows that count; with none of
+    them the gradients are zero, whatever dloss is): a dict with dx [M, K] and
+    dw [V, K] (bf16) and dbias [V] (fp32; by default with a bias).
     lse: as the forward call gave it, the other arguments as it was given
     them.  dx, dw, dbias: tensors to write instead of new ones."""
     dev, torch = _device(), _torch

@@ -26,7 +26,9 @@
 // one g for all rows the target's entry is then next to -1 and rounds as any
 // other value.  (Times g it would be next to -g in every row, all of them off
 // by the same up to 2^-8 of themselves: 4096 x 248320 x 2048 with g = 1/3686:
-// dw 3.4e-3 off in its norm, of which 1.7e-3 are its own rounding.)
+// dw 3.4e-3 off in its norm, of which 1.7e-3 are its own rounding.)  A g that
+// is not finite is no factor of the outputs, whose zeros it would make NaN, but
+// of its own rows of dl: rows without a target stay zero.
 // Statistics are in base two: 2^(l log2 e - top), one multiply-add and one
 // v_exp_f32 a logit.
 #include <cmath>
@@ -351,7 +353,7 @@ struct Gradient {
     int64_t m0, n0, first;
     int wave, l16, at[S::TM];
     float g[S::TM], lse[S::TM];
-    uint32_t counts = 0;                      // a bit for each row
+    uint32_t counts = 0, odd = 0;             // a bit for each row; of those: dloss is not finite (g: 1)
     Store<S, true, true> store;
     __device__ __forceinline__ void init(const LossProduct& p, int64_t m, int64_t n, int w, int lane) {
         m0 = m;
@@ -376,7 +378,8 @@ struct Gradient {
         for (int i = 0; i < S::TM; ++i) {
             counts |= row_of<S>(m0, wave, i, l16) < p.M && t[i] != p.rows.ignore && t[i] >= 0 && t[i] < p.rows.V ? 1u << i : 0u;
             at[i] = column_of<S>(p, t[i], first);
-            g[i] = p.rows.dloss_one ? 1.f : g[i] / scale;
+            odd |= is_finite(g[i]) ? 0u : counts & 1u << i;
+            g[i] = p.rows.dloss_one || !is_finite(g[i]) ? 1.f : g[i] / scale;
         }
     }
     __device__ __forceinline__ void run(const LossProduct& p, f32x4 (&acc)[S::TM][S::TN], uint8_t* shared, int wave, int lane) {
@@ -400,6 +403,13 @@ struct Gradient {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (at[i] == 16 * j + e) acc[i][j][e] -= g[i];
+            }
+            if (odd >> i & 1u) {
+                const float d = p.rows.dloss[p.rows.dloss_one ? 0 : row_of<S>(m0, wave, i, l16)];
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] *= d;
             }
         }
         if (n0 + S::BN > p.N) {                      // columns past the end
@@ -620,7 +630,7 @@ struct LossFinish {
 };
 
 __global__ __launch_bounds__(256) void loss_finish_kernel(LossFinish f) {
-    const float by = *f.scale * f.factor;
+    const float by = finite_or_one(*f.scale) * f.factor;
     const int64_t rows = f.count ? *f.count : f.M;
     if (static_cast<int64_t>(blockIdx.x) < f.dx_blocks) {
         const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, per = f.K / 4, m = i / per, k = i % per * 4;

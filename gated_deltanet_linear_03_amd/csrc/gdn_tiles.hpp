@@ -416,9 +416,12 @@ struct Shape {
 // PLAIN: nothing but y.  KEEP: as in store_n.  P: GemmProduct, or one with a
 // factor of its own for the sums (PLAIN).
 struct ScaledProduct : GemmProduct {
-    const float* scale;                       // device; NULL: 1
+    const float* scale;                       // device; NULL, or not finite: 1
     float factor;
 };
+
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+__device__ __forceinline__ float finite_or_one(float x) { return is_finite(x) ? x : 1.f; }
 
 template <typename S, bool PLAIN, bool KEEP = false, typename P = GemmProduct>
 struct Store {
@@ -459,7 +462,7 @@ struct Store {
         if (!PLAIN && p.ep.bias && nv > 0) load_n<8>(p.ep.bias, false, n, nv, bias);
         constexpr bool kScaled = !std::is_same<P, GemmProduct>::value;
         float scale = 1.f;
-        if constexpr (kScaled) scale = p.scale ? *p.scale * p.factor : 1.f;
+        if constexpr (kScaled) scale = p.scale ? finite_or_one(*p.scale) * p.factor : 1.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll

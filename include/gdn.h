@@ -824,7 +824,9 @@ gdn_status gdn_linear_cross_entropy(const gdn_loss_io* io, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
 /* The gradients' buffers; each of dx, dw, dbias may be NULL.  dl is rounded to
- * bf16 for the two products; dbias sums it in fp32.  The bytes from the first
+ * bf16 for the two products; dbias sums it in fp32.  A dloss that is not finite
+ * (a mean over no rows) reaches the rows that count and nothing else: with none
+ * of them the gradients are zero.  The bytes from the first
  * to the last element of an output must not overlap those of another buffer. */
 typedef struct {
     const float* dloss;            /* [M], or one value for all rows */

@@ -327,3 +327,59 @@ def test_graph_of_a_large_call(one):
         assert all(torch.equal(eager[n], b[n]) for n in b), share
         if share == 1.0:
             assert all(torch.equal(warm[n], b[n]) for n in b)
+
+
+@pytest.mark.parametrize("M, V, K", [(12, 400, 64), (130, 700, 72), (700, 3000, 1032), (500, 200000, 8), (1300, 60001, 1032)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_dloss_not_finite(M, V, K, value):
+    """The mean over no rows is 1 / 0 of nothing: a dloss that is not finite
+    reaches the rows that count and no others, in calls of one piece, of several,
+    with dx in parts, and in those that bring rows together."""
+    g, x, w, t0 = data(M, V, K, 80, ignored=False)
+    none, row = torch.full_like(t0, -100), M // 2
+    for smooth in (0.0, 0.1):
+        # no row counts: every gradient is zero
+        lse = gdn.linear_cross_entropy(x, w, none, label_smoothing=smooth)["lse"]
+        for dloss in (torch.full((1,), value, device="cuda"), torch.full((M,), value, device="cuda")):
+            b = gdn.linear_cross_entropy_backward(dloss, x, w, none, lse, label_smoothing=smooth, want_dbias=True)
+            assert all(bool((b[n] == 0).all()) for n in b)
+        # one row: dl is `value` times what it is otherwise, column by column
+        t = none.clone()
+        t[row] = t0[row]
+        lse = gdn.linear_cross_entropy(x, w, t, label_smoothing=smooth)["lse"]
+        l = x[row:row + 1].double() @ w.double().t().contiguous()
+        p = torch.exp(l - lse[row].double())[0]
+        p[t[row]] -= 1 - smooth
+        sure = (p - smooth / V).abs() > 1e-3 * smooth / V + 1e-30          # (its sign is known in 32 bits)
+        dl = (p - smooth / V) * value
+        dw = dl[:, None] * x[row].double()
+        for dloss in (torch.full((1,), value, device="cuda"), torch.full((M,), value, device="cuda")):
+            b = gdn.linear_cross_entropy_backward(dloss, x, w, t, lse, label_smoothing=smooth, want_dbias=True)
+            assert int(sure.sum()) > V // 2
+            assert bool(torch.isclose(b["dbias"].double()[sure], dl[sure], equal_nan=True).all())
+            some = sure.nonzero()[:, 0]
+            some = torch.cat([some[:500], t[row:row + 1]])
+            assert bool(torch.isclose(b["dw"][some].double(), dw[some], equal_nan=True).all())
+            others = torch.arange(M, device="cuda") != row
+            assert bool((b["dx"][others] == 0).all()) and bool(b["dx"][row].isnan().all())
+
+
+@pytest.mark.parametrize("M, V, K", [(12, 400, 64), (700, 3000, 1032), (1300, 60001, 1032)])
+def test_dloss_of_one_row_not_finite(M, V, K):
+    """The other rows' dx keep their bits, an ignored row's dloss is not looked at."""
+    g, x, w, t = data(M, V, K, 81, ignored=False)
+    t[3], t[M - 1] = -100, -100
+    lse = gdn.linear_cross_entropy(x, w, t)["lse"]
+    dloss = torch.randn(M, generator=g, device="cuda").clamp(-1, 1)
+    dloss[0], dloss[5] = 1.0, 0.5
+    want = gdn.linear_cross_entropy_backward(dloss, x, w, t, lse, want_dbias=True)
+    dloss[3], dloss[M - 1] = float("nan"), float("inf")
+    b = gdn.linear_cross_entropy_backward(dloss, x, w, t, lse, want_dbias=True)
+    assert all(torch.equal(b[n], want[n]) for n in b)
+    dloss[5] = float("inf")
+    b = gdn.linear_cross_entropy_backward(dloss, x, w, t, lse, want_dbias=True)
+    others = torch.arange(M, device="cuda") != 5
+    assert torch.equal(b["dx"][others], want["dx"][others]) and bool(b["dx"][5].isnan().all())
+    p = torch.exp(x[5:6].double() @ w.double().t().contiguous() - lse[5].double())[0]
+    p[t[5]] -= 1
+    assert bool(torch.isclose(b["dbias"].double(), p * float("inf")).all())
