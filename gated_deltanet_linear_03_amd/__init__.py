@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from itertools import chain
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -1496,9 +1497,10 @@ class AdamW:
     elements.  copies: bf16 tensors of the parameters' sizes (or None, alone
     or in the list) that receive the new values.  weight_decay: a number, or
     one for each tensor.  seed: of the random rounding of 8-bit states.
-    adamw_states() makes the states.  The lists are read here, once: a step
-    updates the memory that their tensors have now, and refuses a parameter
-    that has been given other memory since."""
+    adamw_states() makes the states.  A step updates the memory that the lists'
+    tensors have now: one that has been given other memory since is refused.
+    (The states and copies may be let go, to tensors of no elements: this keeps
+    their memory.)"""
 
     def __init__(self, params, m, v, m_scale=None, v_scale=None, copies=None, beta1=0.9, beta2=0.999,
                  eps=1e-8, weight_decay=0.0, seed=0):
@@ -1533,7 +1535,6 @@ class AdamW:
                 "offsets": [CAdamWTensor.grad.offset, CAdamWTensor.grad_dtype.offset],
                 "itemsize": ctypes.sizeof(CAdamWTensor)})
         self._sizes = [p.numel() for p in self.params]
-        self._at = [p.data_ptr() for p in self.params]
         self._c = (CAdamWTensor * n)()
         for i, p in enumerate(self.params):
             size = p.numel()
@@ -1547,6 +1548,10 @@ class AdamW:
             if self.copies[i] is not None:
                 c.copy = _flat(self.copies[i], f"copies[{i}]", size, (torch.bfloat16,), dev)
             c.weight_decay = self.weight_decay[i]
+        self._copied = any(t is not None for t in self.copies)
+        self._at = self._addresses()
+        self._was = {k: [0 if t is None else t.data_ptr() for t in getattr(self, k)]
+                     for k in ("params", "m", "v", "m_scale", "v_scale", "copies")}
         # what a step writes, each byte once
         spans = sorted((t.data_ptr(), t.numel() * t.element_size(), f"{k}[{i}]")
                        for k in ("params", "copies", "m", "v", "m_scale", "v_scale")
@@ -1554,6 +1559,31 @@ class AdamW:
         for (a, na, x), (b, _, y) in zip(spans, spans[1:]):
             if a + na > b:
                 raise ValueError(f"{x} and {y}: share memory")
+
+
+    def _lists(self):
+        names = ["params", "m", "v"] + ["m_scale", "v_scale"] * (self.bits == 8)
+        # (a list of None is counted without looking into a tensor)
+        return names + ["copies"] * (self._copied or self.copies.count(None) != len(self.copies))
+
+    def _addresses(self):
+        # (one method mapped over the lists: a tenth less time than a comprehension's calls)
+        lists = [getattr(self, k) for k in self._lists()]
+        try:
+            return list(map(_torch.Tensor.data_ptr, chain.from_iterable(lists)))
+        except TypeError:                                 # (some without a copy)
+            return [0 if t is None else t.data_ptr() for t in chain.from_iterable(lists)]
+
+    def _check_memory(self):
+        if self._addresses() == self._at:
+            return
+        for name, old in self._was.items():
+            now = [0 if t is None else t.data_ptr() for t in getattr(self, name)]
+            if len(now) != len(old):
+                raise ValueError(f"opt.{name}: {len(old)} entries needed, not {len(now)}")
+            for i, (a, b) in enumerate(zip(now, old)):
+                if a != b and (a or name == "params"):
+                    raise ValueError(f"opt.{name}[{i}]: its memory is not the one that opt was made with")
 
 
 def _flat(t, name, n, dtypes, dev):
@@ -1591,10 +1621,8 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
         raise ValueError(f"opt: made on cuda:{opt.device}, the current device is cuda:{dev}")
     if len(grads) != n:
         raise ValueError(f"grads: {n} entries needed, not {len(grads)}")
-    # (methods mapped over the lists: a tenth less time than a comprehension's calls)
     of = torch.Tensor
-    if list(map(of.data_ptr, opt.params)) != opt._at:
-        raise ValueError("opt: a parameter's memory is not the one that it was made with")
+    opt._check_memory()
     a = CAdamW(opt.bits, opt.beta1, opt.beta2, 0.0, opt.eps, 0, opt.seed, None, None, None)
     if isinstance(lr, torch.Tensor):
         a.lr_ptr = _flat(lr, "lr", 1, (torch.float32,), dev)
@@ -1611,19 +1639,22 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
     c = (CAdamWTensor * n)()
     ctypes.memmove(c, opt._c, ctypes.sizeof(c))
     bf16, fp32 = torch.bfloat16, torch.float32
-    none = [i for i, g in enumerate(grads) if g is None]
-    if none:
+    none = ()
+    try:
+        kinds = list(map(of.dtype.__get__, grads))
+    except TypeError:
+        none = [i for i, g in enumerate(grads) if g is None]
         grads = [opt.params[i] if g is None else g for i, g in enumerate(grads)]     # (whose n is 0)
-    kinds = list(map(of.dtype.__get__, grads))
-    if not (list(map(of.numel, grads)) == opt._sizes and {bf16, fp32}.issuperset(kinds)
+        kinds = list(map(of.dtype.__get__, grads))
+    kind = set(kinds)
+    if not (list(map(of.numel, grads)) == opt._sizes and {bf16, fp32}.issuperset(kind)
             and all(map(of.is_contiguous, grads)) and {dev}.issuperset(map(of.get_device, grads))):
         for i, g in enumerate(grads):
             _flat(g, f"grads[{i}]", opt._sizes[i], (bf16, fp32), dev)
     if n:
         table = _np.frombuffer(c, dtype=_ADAMW_TABLE)
         table["grad"] = list(map(of.data_ptr, grads))
-        halves = kinds.count(bf16)
-        table["grad_dtype"] = [k is bf16 for k in kinds] if 0 < halves < n else halves > 0
+        table["grad_dtype"] = [k is bf16 for k in kinds] if len(kind) > 1 else bf16 in kind
         for i in none:
             c[i].n = 0
     _check(lib().gdn_adamw_step(ctypes.byref(a), c, n, _raw_stream(stream, dev)))

@@ -1802,12 +1802,22 @@ gdn_status gdn_adamw_step(const gdn_adamw* a, const gdn_adamw_tensor* tensors, i
         if (!(t.weight_decay >= 0.f) || std::isinf(t.weight_decay))
             return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: weight_decay must be >= 0 and finite", i);
         const size_t blocks = eight ? (n + GDN_ADAMW_BLOCK - 1) / GDN_ADAMW_BLOCK * 4 : 0;
-        const Span out[9] = {{t.param, 4 * n}, {t.copy, 2 * n}, {t.m, se * n}, {t.v, se * n}, {eight ? t.m_scale : nullptr, blocks},
-                             {eight ? t.v_scale : nullptr, blocks}, {a->lr_ptr, 4}, {a->step_ptr, 4}, {a->grad_scale, 4}};
-        const Span in{t.grad, ge * n};
-        for (int k = 0; k < 9; ++k)
-            if ((k < 6 && any_overlap(out[k], &in, 1)) || any_overlap(out[k], out, k < 6 ? k : 6))
-                return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: two of its buffers overlap", i);
+        // (those that there are, and no function for a pair: 120 tensors' checks take a third of the time)
+        uintptr_t from[10], to[10];
+        int written = 0, all = 0;
+        const auto add = [&](const void* q, size_t bytes) {
+            from[all] = reinterpret_cast<uintptr_t>(q);
+            to[all] = from[all] + bytes;
+            all += q ? 1 : 0;
+        };
+        add(t.param, 4 * n); add(t.copy, 2 * n); add(t.m, se * n); add(t.v, se * n);
+        if (eight) { add(t.m_scale, blocks); add(t.v_scale, blocks); }
+        written = all;
+        add(t.grad, ge * n); add(a->lr_ptr, 4); add(a->step_ptr, 4); add(a->grad_scale, 4);
+        bool shared = false;
+        for (int k = 0; k < written; ++k)
+            for (int j = k + 1; j < all; ++j) shared |= from[k] < to[j] && from[j] < to[k];
+        if (shared) return fail(GDN_ERR_INVALID_ARGUMENT, "tensor %d: two of its buffers overlap", i);
     }
     gdn::AdamwParams p{};
     p.lr = a->lr; p.eps = a->eps;

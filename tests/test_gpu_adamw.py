@@ -346,3 +346,50 @@ def test_codes_to_the_last(grad):
             if name == "v":
                 want = np.where((want == 0) & (value > 0), 2.0 ** -9, want)
             assert (f64(getattr(opt, name)[i]) == want).all(), (name, i)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("how", ["data", "entry"])
+def test_moved_states_and_copies(bits, how):
+    """A bf16 copy or a state with other memory than at the start, by its data
+    or as another tensor in its list, is refused and nothing is written; the
+    step goes on once it is back, and where copies were let go."""
+    p = [torch.ones(n, device="cuda") for n in (300, 70, 0)]
+    g = [torch.ones_like(x) for x in p]
+    st = gdn.adamw_states(p, bits)
+    copies = [torch.ones(300, device="cuda", dtype=BF16), None, torch.ones(0, device="cuda", dtype=BF16)]
+    opt = gdn.AdamW(p, **st, copies=copies)
+    for name in ["m", "v", "copies"] + ["m_scale", "v_scale"] * (bits == 8):
+        t = getattr(opt, name)[0]
+        other, was = t.clone(), t.data
+        if how == "data":
+            t.data = other
+        else:
+            getattr(opt, name)[0] = other
+        with pytest.raises(ValueError, match=rf"opt\.{name}\[0\].*memory"):
+            gdn.adamw_step(opt, g, lr=1e-2, step=1)
+        assert all(float((x - 1).abs().sum()) == 0 for x in p) and float((was.float() - other.float()).abs().max()) == 0
+        if how == "data":
+            t.data = was
+        else:
+            getattr(opt, name)[0] = t
+    opt.copies[1] = torch.ones(70, device="cuda", dtype=BF16)
+    with pytest.raises(ValueError, match=r"opt\.copies\[1\]"):
+        gdn.adamw_step(opt, g, lr=1e-2, step=1)
+    opt.copies[1] = None
+    opt.m.append(opt.m[0])
+    with pytest.raises(ValueError, match=r"opt\.m: 3 entries"):
+        gdn.adamw_step(opt, g, lr=1e-2, step=1)
+    opt.m.pop()
+    gdn.adamw_step(opt, g, lr=1e-2, step=1)
+    assert float((copies[0].float() - 0.99).abs().max()) < 2.0 ** -8 and float((p[0] - 0.99).abs().max()) < 1e-5
+    copies[0].data = torch.empty(0, device="cuda", dtype=BF16)
+    gdn.adamw_step(opt, g, lr=1e-2, step=2)
+    opt.copies = [None] * 3
+    gdn.adamw_step(opt, g, lr=1e-2, step=3)
+    assert float((p[0] - 0.97).abs().max()) < 1e-5
+    # a list that had none
+    bare = gdn.AdamW([torch.ones(5, device="cuda")], **gdn.adamw_states([torch.ones(5, device="cuda")], bits))
+    bare.copies = [torch.ones(5, device="cuda", dtype=BF16)]
+    with pytest.raises(ValueError, match=r"opt\.copies\[0\]"):
+        gdn.adamw_step(bare, [torch.ones(5, device="cuda")], lr=1e-2, step=1)
