@@ -1496,7 +1496,8 @@ class AdamW:
     uint8), in units of m_scale and v_scale, fp32 of one entry for 256
     elements.  copies: bf16 tensors of the parameters' sizes (or None, alone
     or in the list) that receive the new values.  weight_decay: a number, or
-    one for each tensor.  seed: of the random rounding of 8-bit states.
+    one for each tensor.  seed: of the random rounding of 8-bit states.  These
+    numbers may be changed between steps (a captured step keeps its own).
     adamw_states() makes the states.  A step updates the memory that the lists'
     tensors have now: one that has been given other memory since is refused.
     (The states and copies may be let go, to tensors of no elements: this keeps
@@ -1509,7 +1510,7 @@ class AdamW:
         if self.bits == 8 and (m_scale is None or v_scale is None):
             raise ValueError("m_scale and v_scale: both are needed for states in 8 bits")
         scales = [None] * n
-        decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+        decay = self._each(weight_decay, n)
         lists = dict(params=params, m=m, v=v, m_scale=scales if m_scale is None else m_scale,
                      v_scale=scales if v_scale is None else v_scale,
                      copies=scales if copies is None else copies, weight_decay=decay)
@@ -1548,6 +1549,7 @@ class AdamW:
             if self.copies[i] is not None:
                 c.copy = _flat(self.copies[i], f"copies[{i}]", size, (torch.bfloat16,), dev)
             c.weight_decay = self.weight_decay[i]
+        self._decay = list(self.weight_decay)             # as self._c has it
         self._copied = any(t is not None for t in self.copies)
         self._at = self._addresses()
         self._was = {k: [0 if t is None else t.data_ptr() for t in getattr(self, k)]
@@ -1560,6 +1562,17 @@ class AdamW:
             if a + na > b:
                 raise ValueError(f"{x} and {y}: share memory")
 
+    @staticmethod
+    def _each(x, n):
+        return list(x) if hasattr(x, "__len__") else [x] * n
+
+    def _read_decay(self):
+        decay = self._each(self.weight_decay, len(self._c))
+        if len(decay) != len(self._c):
+            raise ValueError(f"opt.weight_decay: {len(self._c)} entries needed, not {len(decay)}")
+        for c, x in zip(self._c, decay):
+            c.weight_decay = x
+        self._decay = decay
 
     def _lists(self):
         names = ["params", "m", "v"] + ["m_scale", "v_scale"] * (self.bits == 8)
@@ -1623,6 +1636,8 @@ def adamw_step(opt: AdamW, grads, lr, step, grad_scale=None, stream=None):
         raise ValueError(f"grads: {n} entries needed, not {len(grads)}")
     of = torch.Tensor
     opt._check_memory()
+    if opt.weight_decay != opt._decay:
+        opt._read_decay()
     a = CAdamW(opt.bits, opt.beta1, opt.beta2, 0.0, opt.eps, 0, opt.seed, None, None, None)
     if isinstance(lr, torch.Tensor):
         a.lr_ptr = _flat(lr, "lr", 1, (torch.float32,), dev)

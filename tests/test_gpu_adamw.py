@@ -393,3 +393,33 @@ def test_moved_states_and_copies(bits, how):
     bare.copies = [torch.ones(5, device="cuda", dtype=BF16)]
     with pytest.raises(ValueError, match=r"opt\.copies\[0\]"):
         gdn.adamw_step(bare, [torch.ones(5, device="cuda")], lr=1e-2, step=1)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_changed_weight_decay(bits):
+    """A weight decay that was changed since, one of the list or all of them,
+    holds from the next step on, as the other numbers of the object do."""
+    p = [torch.ones(300, device="cuda"), torch.ones(70, device="cuda")]
+    g = [torch.zeros_like(x) for x in p]
+    opt = gdn.AdamW(p, **gdn.adamw_states(p, bits), weight_decay=0.0)
+    want = [1.0, 1.0]
+    for new in (0.0, [0.5, 0.0], 0.25, "entry", (0.0, 0.125)):
+        if new == "entry":
+            opt.weight_decay = [0.25, 0.25]
+            gdn.adamw_step(opt, g, lr=0.0, step=1)
+            opt.weight_decay[1] = 0.5
+        else:
+            opt.weight_decay = new
+        gdn.adamw_step(opt, g, lr=0.5, step=1)
+        each = [0.25, 0.5] if new == "entry" else list(new) if isinstance(new, (list, tuple)) else [new] * 2
+        want = [w * (1 - 0.5 * d) for w, d in zip(want, each)]            # (exact: few bits)
+        assert [float(x.min()) for x in p] == [float(x.max()) for x in p] == want
+    opt.weight_decay = [0.1]
+    with pytest.raises(ValueError, match="weight_decay: 2 entries"):
+        gdn.adamw_step(opt, g, lr=0.5, step=1)
+    opt.weight_decay = -1.0
+    with pytest.raises(gdn.GdnError, match="weight_decay"):
+        gdn.adamw_step(opt, g, lr=0.5, step=1)
+    opt.weight_decay = 0.0
+    gdn.adamw_step(opt, g, lr=0.5, step=1)
+    assert [float(x.max()) for x in p] == want
