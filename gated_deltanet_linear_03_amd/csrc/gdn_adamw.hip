@@ -196,18 +196,26 @@ struct Largest {
         int e = __builtin_ctz(bits | 16u) % kLane;
         float x1 = of(x, e, lane), g1 = of(g, e, lane);
         if ((who & (who - 1)) != 0 || (bits & (bits - 1)) != 0) {
+            // One after the other, all that come from the same pair (or, as
+            // magnitudes go, from its negative) at once: gradients of one size
+            // make ties of whole blocks (2^26 elements of one gradient: value by
+            // value 6.78 ms, so 0.23; of random ones 0.21 either way).
             double best = -1.0;
+            uint32_t left = mine;
             while (who != 0 && most > 0.f) {
                 lane = __builtin_ctzll(who);
-                who &= who - 1;
-                bits = __builtin_amdgcn_readlane(mine, lane);
-                while (bits) {
-                    e = __builtin_ctz(bits);
-                    bits &= bits - 1;
-                    const float x2 = of(x, e, lane), g2 = of(g, e, lane);
-                    const double v = R ? new_r(s, x2, g2) : fabs(new_m(s, x2, g2));
-                    if (v > best) { best = v; x1 = x2; g1 = g2; }
+                e = __builtin_ctz(__builtin_amdgcn_readlane(left, lane) | 16u) % kLane;
+                const float x2 = of(x, e, lane), g2 = of(g, e, lane);
+                const double v = R ? new_r(s, x2, g2) : fabs(new_m(s, x2, g2));
+                if (v > best) { best = v; x1 = x2; g1 = g2; }
+#pragma unroll
+                for (int k = 0; k < kLane; ++k) {
+                    const bool same = (x[k] == x2 && (R ? fabsf(g[k]) == fabsf(g2) : g[k] == g2)) || (!R && x[k] == -x2 && g[k] == -g2);
+                    left &= same ? ~(1u << k) : ~0u;
                 }
+                // (the one itself in any case: the loop ends after 256 of them at the most)
+                left &= static_cast<int>(__lane_id()) == lane ? ~(1u << e) : ~0u;
+                who = __ballot(left != 0);
             }
         }
         top = put(most, at, top);

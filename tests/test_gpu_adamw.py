@@ -423,3 +423,52 @@ def test_changed_weight_decay(bits):
     opt.weight_decay = 0.0
     gdn.adamw_step(opt, g, lr=0.5, step=1)
     assert [float(x.max()) for x in p] == want
+
+
+@pytest.mark.parametrize("grad", [BF16, FP32])
+def test_ties(grad):
+    """Blocks with many largest values: all of one size, of both signs, from two
+    pairs of a state and a gradient that differ by less than 32 bits tell, and of
+    one value among zeros: scales and codes to the last, as of any other block."""
+    rng = np.random.RandomState(23)
+    n = 256 * 12 + 100
+    p, grads, states = tensors([n], 92, 8, grad, False)
+    m, v, g = (np.zeros(n, dtype=np.float32) for _ in range(3))
+    block = np.arange(n) // 256
+    sign = np.where(rng.rand(n) < 0.5, -1, 1)
+    half = rng.rand(n) < 0.5
+    ulp = np.float32(2.0 ** -24)
+    g[block < 4] = 1e-3                                     # one value
+    g[(block >= 2) & (block < 4)] *= sign[(block >= 2) & (block < 4)]
+    m[block == 3] = 448 * sign[block == 3]                  # a state of the same or the other sign
+    for b in (4, 5, 6, 7):                                  # m' = 0.9 m + 0.1 g: 0.9 * 448 s or 0.1 g, nearly as large
+        here = block == b
+        m[here & half] = 448
+        g[here & ~half] = np.float32(0.9 * 448 / 0.1 * 2.0 ** -12) * (1 + (b - 5) * ulp * 2)
+        v[here & half] = 448
+    g[256 * 8 + 77] = -1e-3
+    m[256 * 9] = v[256 * 9 + 255] = 448
+    m[block == 10], v[block == 10] = 416 * sign[block == 10], 3.5
+    g[block == 12] = rng.choice([1e-3, -1e-3, 0.0], 100)
+    scale = np.float32(2.0 ** -12)
+    states["m"][0].copy_(torch.from_numpy(m)), states["v"][0].copy_(torch.from_numpy(v))
+    for k in ("m_scale", "v_scale"):
+        states[k][0].fill_(float(scale))
+    grads[0].copy_(torch.from_numpy(g))
+    opt = gdn.AdamW(p, **states, beta1=0.9, beta2=0.95, seed=6)
+    g64 = f64(grads[0])
+    gdn.adamw_step(opt, grads, lr=1e-3, step=3)
+    lo, hi = random_halves(6, 3, 0, n)
+    r = (v * scale).astype(np.float32)
+    for name, value, u in (("m", 0.9 * (m * scale).astype(np.float64) + (1 - 0.9) * g64, lo),
+                           ("v", np.sqrt(0.95 * (r * r).astype(np.float64) + (1 - 0.95) * g64 * g64), hi)):
+        full = np.zeros(-(-n // 256) * 256)
+        full[:n] = np.abs(value)
+        got = f64(getattr(opt, name + "_scale")[0])
+        assert (got == (full.reshape(-1, 256).max(1) / 448).astype(np.float32)).all(), name
+        with np.errstate(invalid="ignore", divide="ignore"):
+            ratio = np.where(got[block] > 0, value / got[block], 0.0)
+        want = up_or_down(np.clip(ratio, -448, 448), u)[0]
+        if name == "v":
+            want = np.where((want == 0) & (value > 0), 2.0 ** -9, want)
+        assert (f64(getattr(opt, name)[0]) == want).all(), name
