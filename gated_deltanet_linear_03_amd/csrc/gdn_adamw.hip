@@ -143,6 +143,11 @@ struct Step {
     uint32_t key;                                           // of the random bits, with the index's upper word
 };
 
+// Squares below this may lose bits in 32 (gradients below 1e-13 or so): there the
+// r of 8-bit states comes from 64 (2^26 elements: 202 us, 197 to 199 without;
+// zeros 196 and 184, all of them small 252 and 187).
+constexpr float kSmallSquare = 0x1p-96f;
+
 // m' and v' in 64 bits, each operation rounded by itself: beta1 = 0.9 makes m' =
 // (9 m + g) / 10, which is a short number every fifth time, and then the ratio
 // to the scale can lie on a border to the bit.
@@ -151,19 +156,34 @@ __device__ __forceinline__ double new_m(const Step& s, float m0, float g) {
     const double a = s.b1 * static_cast<double>(m0), b = s.rest1 * static_cast<double>(g);
     return a + b;
 }
-__device__ __forceinline__ double new_v(const Step& s, float v0, float g) {
+// (r0: the old v's root; its square counts in 32 bits where those hold it)
+__device__ __forceinline__ double new_v(const Step& s, float r0, float g) {
 #pragma clang fp contract(off)
-    const double a = s.b2 * static_cast<double>(v0), b = s.rest2 * static_cast<double>(g) * static_cast<double>(g);
+    const float q = r0 * r0;
+    const double v0 = q < kSmallSquare ? static_cast<double>(r0) * static_cast<double>(r0) : static_cast<double>(q);
+    const double a = s.b2 * v0, b = s.rest2 * static_cast<double>(g) * static_cast<double>(g);
     return a + b;
 }
 // sqrt(v') to its last bit or next to it: two of Newton's steps from the root in 32 bits
-__device__ __forceinline__ double new_r(const Step& s, float v0, float g) {
-    const double v1 = new_v(s, v0, g);
+__device__ __forceinline__ double new_r(const Step& s, float r0, float g) {
+    const double v1 = new_v(s, r0, g);
+    if (v1 < kSmallSquare && v1 > 0.0) return sqrt(v1);
     const float r = __builtin_amdgcn_sqrtf(static_cast<float>(v1));
     if (!(r > 0.f && r < __builtin_inff())) return r;
-    const double half = 0.5 * static_cast<double>(__builtin_amdgcn_rcpf(r)), r0 = r;
-    const double r1 = fma(fma(-r0, r0, v1), half, r0);
-    return fma(fma(-r1, r1, v1), half, r1);
+    const double half = 0.5 * static_cast<double>(__builtin_amdgcn_rcpf(r)), a = r;
+    const double b = fma(fma(-a, a, v1), half, a);
+    return fma(fma(-b, b, v1), half, b);
+}
+// the same in 32 bits where v' is below kSmallSquare; zero only for zero
+__device__ __forceinline__ float small_r(const Step& s, float r0, float g) {
+    const double r = sqrt(new_v(s, r0, g));
+    const float f = static_cast<float>(r);
+    return r > 0.0 && f == 0.f ? 0x1p-149f : f;
+}
+// v_sqrt_f32 takes a subnormal number for zero
+__device__ __forceinline__ float root(float v) {
+    const bool small = v < kSmallSquare;
+    return __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v) * (small ? 0x1p-32f : 1.f);
 }
 
 // What a wave's blocks' scales come from, in the lanes 2 i (m) and 2 i + 1 (r)
@@ -239,7 +259,7 @@ __device__ __forceinline__ float from_lane(float v, int lane) {
 template <bool EIGHT, bool GB, bool FULL>
 struct Elements {
     float p[kLane], g[kLane], m[kLane], v[kLane];
-    float m0[EIGHT ? kLane : 1], v0[EIGHT ? kLane : 1];     // 8 bits: what the states stand for; v: r
+    float m0[EIGHT ? kLane : 1], r0[EIGHT ? kLane : 1];     // 8 bits: what the states stand for (v: r)
     // 8 bits: codes and scales before the step and after it (the scales are the wave's)
     uint32_t qm, qv, new_qm, new_qv;
     float sm, sv;
@@ -305,26 +325,44 @@ struct Elements {
     // p, and m and v (8 bits: r in v) after the step
     __device__ __forceinline__ void update(const Step& s) {
         if constexpr (EIGHT) decode();
+        float r[kLane];
 #pragma unroll
         for (int e = 0; e < kLane; ++e) {
             g[e] *= s.grad_scale;
-            float r;
             if constexpr (EIGHT) {
                 m0[e] = m[e] * ms;
-                v0[e] = v[e] * vs;
-                v0[e] *= v0[e];
+                r0[e] = v[e] * vs;
                 // to its last bit also where its terms cancel: with what the
                 // product and the factors have lost (a multiply-add rounds the other)
                 const float gg = s.f_rest1 * g[e], q = fmaf(s.f_b1, m0[e], gg);
                 m[e] = q + fmaf(s.low_b1, m0[e], fmaf(s.low_rest1, g[e], fmaf(s.f_rest1, g[e], -gg)));
-                r = __builtin_amdgcn_sqrtf(fmaf(s.f_b2, v0[e], s.f_rest2 * g[e] * g[e]));
-                v[e] = r;
+                v[e] = fmaf(s.f_b2, r0[e] * r0[e], s.f_rest2 * g[e] * g[e]);
+                r[e] = __builtin_amdgcn_sqrtf(v[e]);
             } else {
                 m[e] = fmaf(s.f_b1, m[e], s.f_rest1 * g[e]);
                 v[e] = fmaf(s.f_b2, v[e], s.f_rest2 * g[e] * g[e]);
-                r = __builtin_amdgcn_sqrtf(v[e]);
+                r[e] = root(v[e]);
             }
-            const float step = m[e] * s.c1 * __builtin_amdgcn_rcpf(fmaf(r, s.c2, s.eps));
+        }
+        if constexpr (EIGHT) {
+            static_assert(kLane == 4, "four values");
+            if (__any(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])) < kSmallSquare)) {
+                uint32_t small = 0;                         // (zeros of zeros are as they are)
+#pragma unroll
+                for (int e = 0; e < kLane; ++e)
+                    small |= v[e] < kSmallSquare && (__float_as_uint(r0[e]) | __float_as_uint(g[e])) << 1 != 0 ? 1u << e : 0u;
+                if (__any(small != 0)) {
+#pragma unroll
+                    for (int e = 0; e < kLane; ++e)
+                        if (small >> e & 1u) r[e] = small_r(s, r0[e], g[e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) v[e] = r[e];
+        }
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            const float step = m[e] * s.c1 * __builtin_amdgcn_rcpf(fmaf(r[e], s.c2, s.eps));
             p[e] -= fmaf(s.lr * s.decay, p[e], step);
         }
     }
@@ -339,7 +377,7 @@ struct Elements {
 #pragma unroll
         for (int e = 0; e < kLane; ++e) size[e] = fabsf(m[e]);
         l->offer<false>(s, 2 * block, size, m0, g);
-        l->offer<true>(s, 2 * block + 1, v, v0, g);
+        l->offer<true>(s, 2 * block + 1, v, r0, g);
     }
 
     // the codes of the new states
@@ -375,7 +413,7 @@ struct Elements {
             if (of_m) {
                 code = e4m3(sm > 0.f ? new_m(s, old, grad) / static_cast<double>(sm) : 0.0, h & 0xFFFFu);
             } else {
-                const double r = sqrt(new_v(s, old * old, grad));
+                const double r = sqrt(new_v(s, old, grad));
                 code = e4m3(sv > 0.f ? r / static_cast<double>(sv) : 0.0, h >> 16);
                 if (code == 0 && r > 0.0 && sv > 0.f) code = 1;
             }

@@ -854,11 +854,14 @@ gdn_status gdn_linear_cross_entropy_backward(const gdn_loss_io* io, const gdn_lo
  * in fp32.  States in 32 bits: m and v.  States in 8 bits: m and r = sqrt(v) in
  * e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest 448) times an fp32 scale
  * for GDN_ADAMW_BLOCK consecutive elements, which is the largest magnitude of
- * the new values / 448 (0 where that is below 2^-100).  A value / scale is
+ * the new values / 448 (0 where that magnitude is below 2^-100; NaN does not
+ * count, and an infinite one, from an infinite gradient, makes the scale
+ * infinite: the block's other values are lost, where states in 32 bits lose that
+ * element alone).  A value / scale is
  * rounded up or down at random, up when its fraction of a step of the format
  * plus u / 65536 reaches 1, so that its expected value is kept; a positive r is
  * not rounded to 0.  (m', r, and their quotients by the scales decide that in 64
- * bits, from m and v in 32.)  u: for m the low and for r the high 16 bits of
+ * bits, from m and v = r^2 in 32; squares below 2^-96 are not rounded.)  u: for m the low and for r the high 16 bits of
  *   mix(key + mix(i >> 32) + i * 0x9E3779B1),
  *   key = mix(mix(seed + k * 0x9E3779B1) + t * 0x9E3779B1)
  * of element i of tensor t, in 32 bits, mix the finaliser of MurmurHash3.  The

@@ -472,3 +472,64 @@ def test_ties(grad):
         if name == "v":
             want = np.where((want == 0) & (value > 0), 2.0 ** -9, want)
         assert (f64(getattr(opt, name)[0]) == want).all(), name
+
+
+@pytest.mark.parametrize("first", [False, True])
+def test_small_gradients(first):
+    """8-bit states where v' leaves the range of 32 bits: gradients of 1e-17 to
+    1e-28, alone in their blocks and beside ordinary ones, from zero states and
+    from states as small: codes and scales to the last (a scale is 0 where the
+    largest magnitude is below 2^-100, and no positive r is rounded to 0)."""
+    rng = np.random.RandomState(29)
+    sizes = [10 ** -k for k in range(17, 29)]
+    n = 256 * 2 * len(sizes) + 50
+    g = np.zeros(n, dtype=np.float32)
+    for k, size in enumerate(sizes):
+        g[512 * k:512 * k + 512] = rng.randn(512) * size
+        g[512 * k + 256 + 5 * k] = 1e-3                     # the second block of each: beside this one
+    g[-50:] = 1e-24
+    g[::7] = 0
+    p = [torch.zeros(n, device="cuda")]
+    st = gdn.adamw_states(p, 8)
+    if not first:                                           # the states that a few steps of other gradients leave
+        opt = gdn.AdamW(p, **st, beta1=0.9, beta2=0.95, seed=8)
+        for k in range(1, 4):
+            gdn.adamw_step(opt, [torch.from_numpy(np.roll(g, k)).cuda()], lr=0.0, step=k)
+    old = {k: f64(st[k][0]) for k in st}
+    opt = gdn.AdamW(p, **st, beta1=0.9, beta2=0.95, seed=9, eps=1e-8)
+    gdn.adamw_step(opt, [torch.from_numpy(g).cuda()], lr=1e-3, step=4)
+    block = np.arange(n) // 256
+    m, r = ((old[k] * old[k + "_scale"][block]).astype(np.float32) for k in ("m", "v"))
+    g64, square = g.astype(np.float64), (r * r).astype(np.float64)
+    v = np.where(square < 2.0 ** -96, r.astype(np.float64) ** 2, square)
+    lo, hi = random_halves(9, 4, 0, n)
+    for name, value, u in (("m", 0.9 * m.astype(np.float64) + (1 - 0.9) * g64, lo),
+                           ("v", np.sqrt(0.95 * v + (1 - 0.95) * g64 * g64), hi)):
+        full = np.zeros(-(-n // 256) * 256)
+        full[:n] = np.abs(value)
+        top = full.reshape(-1, 256).max(1)
+        got = f64(getattr(opt, name + "_scale")[0])
+        assert (got == np.where(top < 2.0 ** -100, 0.0, top / 448).astype(np.float32)).all(), name
+        assert first is False or name == "m" or int((got > 0).sum()) >= 2 * len(sizes)       # 1e-28 has an r above 2^-100
+        with np.errstate(invalid="ignore", divide="ignore"):
+            ratio = np.where(got[block] > 0, value / got[block], 0.0)
+        want = up_or_down(np.clip(ratio, -448, 448), u)[0]
+        if name == "v":
+            want = np.where((want == 0) & (value > 0) & (got[block] > 0), 2.0 ** -9, want)
+        assert (f64(getattr(opt, name)[0]) == want).all(), name
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_no_eps(bits):
+    """A first step without eps is lr long whatever the gradient's size, as long
+    as 32 bits hold v' (8 bits: r): in 32 bits below 2^-126 with what they lose
+    of it, half of 2^-149."""
+    size = torch.tensor([10.0 ** -k for k in range(0, 21)], dtype=torch.float64)
+    g = size.float().repeat(20).cuda()
+    p = [torch.zeros(g.numel(), device="cuda")]
+    opt = gdn.AdamW(p, **gdn.adamw_states(p, bits), eps=0.0)
+    gdn.adamw_step(opt, [g], lr=1.0, step=1)
+    v = (1 - 0.999) * g.double().cpu() ** 2
+    # v' and its root, c1 and c2, the reciprocal: adamw64's count; v' may lose two halves of its least bit (product, sum)
+    lost = 2 * 2.0 ** -150 / v if bits == 32 else torch.zeros_like(v)
+    close("p", p[0], -torch.ones_like(v), 30 * U + lost)
