@@ -330,9 +330,12 @@ __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(Loss
     if (!loss) return;
     float out = 0.f;
     if (there) {
+        // No logit and no mean of logits is above lse, but its own sum's rounding
+        // may put it there (a row that is sure of its target).
+        const auto above = [](float a, float b) { const float d = a - b; return d < 0.f ? 0.f : d; };
         const float e = p.rows.smooth;
-        out = (1.f - e) * (l - dot[0][r]) + p.rows.z * l * l;
-        if (e > 0.f) out += e * (l - tot[0][r] / static_cast<float>(p.rows.V));
+        out = (1.f - e) * above(l, dot[0][r]) + p.rows.z * l * l;
+        if (e > 0.f) out += e * above(l, tot[0][r] / static_cast<float>(p.rows.V));
     } else if (t != p.rows.ignore) {
         out = __builtin_nanf("");
         if (p.rows.status) __hip_atomic_fetch_or(p.rows.status, GDN_STATUS_BAD_INDEX, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -383,3 +383,23 @@ def test_dloss_of_one_row_not_finite(M, V, K):
     p = torch.exp(x[5:6].double() @ w.double().t().contiguous() - lse[5].double())[0]
     p[t[5]] -= 1
     assert bool(torch.isclose(b["dbias"].double(), p * float("inf")).all())
+
+
+@pytest.mark.parametrize("M", [16, 200, 1300])
+@pytest.mark.parametrize("smooth", [0.0, 0.1])
+def test_no_loss_below_zero(M, smooth):
+    """Rows that are sure of their target, and a vocabulary of one entry: the
+    loss may round to zero and not below; a NaN stays one."""
+    V, K = 900, 1032
+    g, x, w, t = data(M, V, K, 82, scale=1.0, ignored=False)
+    x = (w[t].float() * 60).to(BF16)
+    r = gdn.linear_cross_entropy(x, w, t, label_smoothing=smooth)
+    loss, lse, e, e_lse = loss64(x.cpu(), w.cpu(), None, t.cpu(), smooth, 0.0)[:4]
+    close("loss", r["loss"], loss, e)
+    assert bool((r["loss"] >= 0).all())
+    one = gdn.linear_cross_entropy(x, w[:1].contiguous(), torch.zeros_like(t), label_smoothing=smooth)
+    loss, _, e = loss64(x.cpu(), w[:1].cpu(), None, torch.zeros(M, dtype=torch.int64), smooth, 0.0)[:3]
+    close("loss of one entry", one["loss"], loss, e)
+    assert bool((one["loss"] >= 0).all())
+    x[3, 5] = float("nan")
+    assert bool(gdn.linear_cross_entropy(x, w, t, label_smoothing=smooth)["loss"][3].isnan())
