@@ -296,9 +296,9 @@ __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(Loss
     bool there = false;
     if (m < p.M) {
         t = target_of(p.rows, m);
-        there = loss && t != p.rows.ignore && t >= 0 && t < p.rows.V;
+        there = t != p.rows.ignore && t >= 0 && t < p.rows.V;
     }
-    if (there) {
+    if (there && loss) {
         const uint16_t* const x = static_cast<const uint16_t*>(p.A) + m * p.lda;
         const uint16_t* const w = static_cast<const uint16_t*>(p.B) + t * p.ldb;
 #pragma unroll 4
@@ -327,7 +327,6 @@ __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(Loss
     a = red[0][r];
     const float l = (a.top + __builtin_amdgcn_logf(a.sum)) * kLn2;                  // (v_log_f32: base two)
     if (lse) lse[m] = l;
-    if (!loss) return;
     float out = 0.f;
     if (there) {
         // No logit and no mean of logits is above lse, but its own sum's rounding
@@ -340,7 +339,7 @@ __global__ __launch_bounds__(kJoinRows * kJoinSlices) void loss_join_kernel(Loss
         out = __builtin_nanf("");
         if (p.rows.status) __hip_atomic_fetch_or(p.rows.status, GDN_STATUS_BAD_INDEX, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    loss[m] = out;
+    if (loss) loss[m] = out;
 }
 
 // ---- backward ------------------------------------------------------------------

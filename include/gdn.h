@@ -806,7 +806,7 @@ typedef struct {
     float label_smoothing;         /* in [0, 1) */
     float z_loss;                  /* >= 0 */
     float* loss;                   /* optional [M] */
-    float* lse;                    /* optional [M], for the backward pass */
+    float* lse;                    /* optional [M], for the backward pass (without either output nothing is done) */
     int32_t* status;               /* optional */
 } gdn_loss_io;
 

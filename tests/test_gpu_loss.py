@@ -2,6 +2,8 @@
 definition in 64 bits, forward and backward: single rows, vocabularies that end
 inside a tile and of one entry, several pieces, ignored and bad targets, masked
 vocabulary entries; nothing written outside; the same bits from call to call."""
+import ctypes
+
 import pytest
 import torch
 
@@ -403,3 +405,23 @@ def test_no_loss_below_zero(M, smooth):
     assert bool((one["loss"] >= 0).all())
     x[3, 5] = float("nan")
     assert bool(gdn.linear_cross_entropy(x, w, t, label_smoothing=smooth)["loss"][3].isnan())
+
+
+@pytest.mark.parametrize("M", [9, 200])
+def test_status_without_loss(M):
+    """A call for lse alone reports a target outside the vocabulary too, and its
+    lse has the bits of a call for both."""
+    V, K = 300, 64
+    g, x, w, t = data(M, V, K, 83, ignored=False)
+    t[4] = -100
+    want = gdn.linear_cross_entropy(x, w, t)["lse"]
+    ws = torch.empty(gdn.linear_cross_entropy_workspace_bytes(M, V, K), dtype=torch.uint8, device="cuda")
+    for bad in (None, V, -7):
+        if bad is not None:
+            t[5] = bad
+        lse, status = torch.zeros(M, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        io = gdn.CLossIO(M, V, K, x.data_ptr(), K, w.data_ptr(), K, None, t.data_ptr(), 8, -100, 0.0, 0.0, None, lse.data_ptr(),
+                         status.data_ptr())
+        assert gdn.lib().gdn_linear_cross_entropy(ctypes.byref(io), ws.data_ptr(), ws.numel(),
+                                                  torch.cuda.current_stream().cuda_stream) == gdn.GDN_OK
+        assert int(status) == (0 if bad is None else gdn.GDN_STATUS_BAD_INDEX) and torch.equal(lse, want)
