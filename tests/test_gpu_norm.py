@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_03_amd as gdn
-from train_helpers import HALF, close, norm64, norm_backward64, norm_bounds
+from train_helpers import HALF, U, close, norm64, norm_backward64, norm_bounds
 
 pytestmark = pytest.mark.gpu
 
@@ -205,3 +205,52 @@ def test_stream_and_graph():
         assert torch.equal(gdn.norm(x, w, None, stats=st), y) and torch.equal(st, stats)
         eager = gdn.norm_backward(dy, x, w, st, want_dbias=True)
         assert all(torch.equal(eager[n], r[n]) for n in r)
+
+
+@pytest.mark.parametrize("D", [1, 2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("M", [255, 2049, 20000, 100003])
+def test_many_narrow_rows(M, D):
+    """Rows of fewer than eight values, in one and in many work-groups, each of
+    which goes round several times; strided, and dx over d_residual."""
+    k = D + M
+    xt, yt = (BF16, FP32)[k % 2], (BF16, FP32)[k // 2 % 2]
+    layer = D % 2 == 0 or M == 2049
+    g = torch.Generator(device="cuda").manual_seed(k)
+    x, dy, skip = rows(g, M, D, xt, k % 3, k % 2, scale=2, offset=1), rows(g, M, D, yt, (k + 1) % 3, 1), rows(g, M, D, xt, 1, 0)
+    w, b = torch.randn(D, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda") if M % 2 else None
+    stats, out = torch.empty((2, M), device="cuda"), rows(g, M, D, yt, k % 2, 1)
+    y = gdn.norm(x, w, b, kind=KIND[layer], out=out, stats=stats)
+    cpu = [None if t is None else t.cpu() for t in (x, w, b)]
+    want, mean, rstd = norm64(*cpu, layer, 1e-5)
+    e, e_mean, e_rstd = norm_bounds(*cpu, layer, 1e-5)
+    close("y", y, want, e + (want.abs() + e) * HALF[yt])
+    close("mean", stats[0], mean, e_mean)
+    close("rstd", stats[1], rstd, e_rstd)
+    assert torch.equal(gdn.norm(x[:100], w, b, kind=KIND[layer], out_dtype=yt), y[:100])
+    r = gdn.norm_backward(dy, x, w, stats, kind=KIND[layer], d_residual=skip, want_dbias=True)
+    ref, lim = norm_backward64(dy.cpu(), x.cpu(), w.cpu(), stats[0].cpu(), stats[1].cpu(), layer, skip.cpu())
+    for name, a, l in zip(("dx", "dweight", "dbias"), ref, lim):
+        close(name, r[name], a, l + (a.abs() + l) * HALF[r[name].dtype])
+    only = gdn.norm_backward(dy, x, w, stats, kind=KIND[layer], want_dx=False, want_dweight=False, want_dbias=True)
+    assert list(only) == ["dbias"] and torch.equal(only["dbias"], r["dbias"])
+    gdn.norm_backward(dy, x, w, stats, kind=KIND[layer], d_residual=skip, dx=skip, want_dweight=False)
+    assert torch.equal(skip, r["dx"])
+
+
+@pytest.mark.parametrize("D", [1, 4, 7, 8, 300])
+def test_sums_over_many_rows(D):
+    """The parameters' gradients of rows whose terms all have one sign: a value
+    goes through at most 2^21 / 2^18 additions of its thread (rows of up to seven;
+    the others' work-groups hold fewer rows: 2^21 / (4 x 1024)), 10 of the
+    work-group's and 64 of the work-groups'."""
+    M = (1 << 21) if D < 8 else (1 << 23) // D
+    x = torch.zeros((M, D), device="cuda")
+    x[:, 0] = 1.0
+    stats = torch.zeros((2, M), device="cuda")
+    stats[1] = 0.3
+    dy = torch.full((M, D), 0.1, device="cuda")
+    r = gdn.norm_backward(dy, x, None, stats, kind=gdn.GDN_NORM_RMS, want_dbias=True)
+    steps = 10 + 64 + (8 if D < 8 else M // 4096 + 1)
+    one, hat = float(dy[0, 0]), float(dy[0, 0]) * float(stats[1, 0])
+    assert float((r["dbias"].double() / (M * one) - 1).abs().max()) <= steps * U
+    assert abs(float(r["dweight"][0]) / (M * hat) - 1) <= (steps + 2) * U and bool((r["dweight"][1:] == 0).all())
