@@ -63,7 +63,10 @@ __device__ __forceinline__ void store_one(void* p, int64_t at, float f) {
 // column W (t + T j), but never past D - W: the last runs of a row whose D is
 // no multiple of their columns begin earlier and repeat columns that another
 // thread (or run) has too.  Those count once: fresh() tells.  So no load has a
-// condition.  (D >= W; where NV > 1 more than half of a row's runs are needed,
+// condition, and both threads store them, with the same bits: in these kernels no
+// product is joined with a sum but by fmaf (left to the compiler that differs
+// from run to run, and the bits with it; stored by one thread only, 300000 x 100
+// in bf16 backward takes 48 us instead of 44).  (D >= W; where NV > 1 more than half of a row's runs are needed,
 // so the first half of a thread's are whole.)
 template <int W, int T, int NV>
 struct Columns {
@@ -150,6 +153,7 @@ constexpr int rows_of(int T) { return T < 256 ? 256 / T : 1; }   // rows that a 
 // MASK: D is not W T NV.
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_row_kernel(NormParams p) {
+#pragma clang fp contract(off)
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T);
     __shared__ float red[2][T > kWave ? T / kWave : 1];
     const int t = threadIdx.x % T;
@@ -222,6 +226,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_row_kernel(NormParams 
 // 32768 x 4096 in bf16: 89 to 123 us (4.4 to 6.0 TB/s), 131 with a wave a row.
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormParams p) {
+#pragma clang fp contract(off)
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
     __shared__ float red[2][R][T > kWave ? T / kWave : 1];
     const int t = threadIdx.x % T, r = threadIdx.x / T;
@@ -374,6 +379,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormPar
 // in fp32 to bf16 222 us, 6.0 TB/s).
 template <bool XB, bool YB, bool MASK, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormParams p) {
+#pragma clang fp contract(off)
     constexpr int W = XB && YB ? 8 : 4, R = rows_of(T), C = W * NV;
     constexpr int kW = T > kWave ? T / kWave : 1;
     __shared__ float red[2][R][2 * kW];
@@ -450,9 +456,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
             float f[W];
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float xh = (x[j].get(e) - mean) * rstd;
-                f[e] = rstd * (dy[j].get(e) * w[W * j + e] - a - xh * b);
-                if (p.d_residual) f[e] += skip[j].get(e);
+                const float xh = (x[j].get(e) - mean) * rstd, q = dy[j].get(e) * w[W * j + e];
+                const float t = fmaf(-xh, b, q - a);
+                f[e] = p.d_residual ? fmaf(rstd, t, skip[j].get(e)) : rstd * t;
             }
             Run<XB, W>::store(p.dx, m * p.dxs + cols.at[j], f);
         }

@@ -254,3 +254,38 @@ def test_sums_over_many_rows(D):
     one, hat = float(dy[0, 0]), float(dy[0, 0]) * float(stats[1, 0])
     assert float((r["dbias"].double() / (M * one) - 1).abs().max()) <= steps * U
     assert abs(float(r["dweight"][0]) / (M * hat) - 1) <= (steps + 2) * U and bool((r["dweight"][1:] == 0).all())
+
+
+MANY = [(1 << 25) // D + 1 for D in (1025, 2048, 2052, 4096, 4099, 8192, 8193, 12345, 16384)] + [150, 70]
+WIDTHS = [1025, 2048, 2052, 4096, 4099, 8192, 8193, 12345, 16384, 16385, 40001]
+
+
+@pytest.mark.parametrize("i", range(len(WIDTHS)), ids=[str(d) for d in WIDTHS])
+@pytest.mark.parametrize("types", [(BF16, BF16), (BF16, FP32), (FP32, BF16), (FP32, FP32)])
+@pytest.mark.parametrize("layer", [True, False])
+def test_many_long_rows(i, types, layer):
+    """From 2^25 values on rows of more than 1024 go to work-groups that stay, of
+    128 to 1024 threads; in the backward pass each has several rows at every width,
+    and in rows of more than 16384 the parameters' threads have.  The reference on
+    the device in 64 bits."""
+    M, D = MANY[i], WIDTHS[i]
+    xt, yt = types
+    k = i + layer
+    g = torch.Generator(device="cuda").manual_seed(3000 + 8 * i + 2 * layer)
+    x, dy = rows(g, M, D, xt, k % 3, k % 2, scale=2, offset=1), rows(g, M, D, yt, (k + 1) % 3, 0)
+    skip = rows(g, M, D, xt, 0, 0) if k % 2 else None
+    w, b = torch.randn(D, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda") if k % 3 else None
+    stats = torch.empty((2, M), device="cuda")
+    y = gdn.norm(x, w, b, kind=KIND[layer], out_dtype=yt, stats=stats)
+    with torch.device("cuda"):
+        want, mean, rstd = norm64(x, w, b, layer, 1e-5)
+        e, e_mean, e_rstd = norm_bounds(x, w, b, layer, 1e-5)
+    assert bool(((y.double() - want).abs() <= e + (want.abs() + e) * HALF[yt]).all())
+    assert bool(((stats[0].double() - mean).abs() <= e_mean).all()) and bool(((stats[1].double() - rstd).abs() <= e_rstd).all())
+    del want, e
+    r = gdn.norm_backward(dy, x, w, stats, kind=KIND[layer], d_residual=skip, want_dbias=True)
+    ref, lim = norm_backward64(dy, x, w, stats[0], stats[1], layer, skip)
+    for name, a, l in zip(("dx", "dweight", "dbias"), ref, lim):
+        assert bool(((r[name].double() - a).abs() <= l + (a.abs() + l) * HALF[r[name].dtype]).all()), name
+    again = gdn.norm_backward(dy, x, w, stats, kind=KIND[layer], d_residual=skip, want_dbias=True)
+    assert all(torch.equal(again[n], r[n]) for n in r)
