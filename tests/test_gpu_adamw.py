@@ -533,3 +533,33 @@ def test_no_eps(bits):
     # v' and its root, c1 and c2, the reciprocal: adamw64's count; v' may lose two halves of its least bit (product, sum)
     lost = 2 * 2.0 ** -150 / v if bits == 32 else torch.zeros_like(v)
     close("p", p[0], -torch.ones_like(v), 30 * U + lost)
+
+
+@pytest.mark.parametrize("grad", [BF16, FP32])
+def test_every_code_is_a_neighbour(grad):
+    """Every element's new code, those next to a border and those whose m' is a
+    difference too, is one of the two values of the format around its ratio to
+    the scale (in 64 bits, over the scale in 32): within a step of it, and on its
+    side of zero."""
+    rng = np.random.RandomState(31)
+    sizes = [int(n) for n in rng.randint(1, 900, 100)] + [200003]
+    p, grads, states = tensors(sizes, 93, 8, grad, False)
+    for i in range(0, len(sizes), 2):                       # m' next to nothing of either term
+        m = states["m"][i].float() * states["m_scale"][i].repeat_interleave(256)[:sizes[i]]
+        grads[i].copy_(-9 * m * (1 + 1e-6 * torch.randn(sizes[i], device="cuda", generator=torch.Generator(device="cuda").manual_seed(i))))
+    opt = gdn.AdamW(p, **states, beta1=0.9, beta2=0.999, seed=5)
+    for k in (1, 2):
+        old = {n: [f64(t) for t in getattr(opt, n)] for n in ("m", "v", "m_scale", "v_scale")}
+        gdn.adamw_step(opt, grads, lr=1e-3, step=k)
+        for i, n in enumerate(sizes):
+            block = np.arange(n) // 256
+            m, r = ((old[q][i] * old[q + "_scale"][i][block]).astype(np.float32) for q in ("m", "v"))
+            g = f64(grads[i])
+            for name, value in (("m", 0.9 * m.astype(np.float64) + (1 - 0.9) * g),
+                                ("v", np.sqrt(0.999 * (r * r).astype(np.float64) + (1 - 0.999) * g * g))):
+                scale = f64(getattr(opt, name + "_scale")[i])[block]
+                ratio = np.where(scale > 0, value / np.where(scale > 0, scale, 1), 0.0)
+                got = f64(getattr(opt, name)[i])
+                unit = np.exp2(np.floor(np.log2(np.maximum(np.abs(ratio), 2.0 ** -6))) - 3)
+                # (64 bits are exact to 2^-50 of the terms, which are at most 10 times the block's largest where m' cancels)
+                assert bool((np.abs(got - ratio) <= unit * (1 + 1e-9)).all()) and bool((got * ratio >= 0).all()), (name, i, k)

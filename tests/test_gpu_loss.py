@@ -425,3 +425,25 @@ def test_status_without_loss(M):
         assert gdn.lib().gdn_linear_cross_entropy(ctypes.byref(io), ws.data_ptr(), ws.numel(),
                                                   torch.cuda.current_stream().cuda_stream) == gdn.GDN_OK
         assert int(status) == (0 if bad is None else gdn.GDN_STATUS_BAD_INDEX) and torch.equal(lse, want)
+
+
+@pytest.mark.parametrize("M, V, K", [(451, 16323, 1120), (1183, 6517, 1256), (1921, 3970, 1232), (1267, 6485, 752), (1983, 8167, 400),
+                                     (660, 13763, 568), (1922, 16144, 168)])
+def test_wide_tiles(M, V, K):
+    """Sizes that go to tiles of 256 x 128 on 256 compute units: the first four in
+    the forward pass, the first three for dl, the last three for the products (in
+    parts); the reference on the device in 64 bits."""
+    g, x, w, t = data(M, V, K, M + 1)
+    bias = torch.randn(V, generator=g, device="cuda")
+    how = dict(bias=bias, label_smoothing=0.05, z_loss=1e-4)
+    r = gdn.linear_cross_entropy(x, w, t, **how)
+    loss, lse, e, e_lse = loss64(x, w, bias, t, 0.05, 1e-4)[:4]
+    close("loss", r["loss"], loss.cpu(), e.cpu())
+    close("lse", r["lse"], lse.cpu(), e_lse.cpu())
+    for dloss in (torch.randn(M, generator=g, device="cuda"), torch.full((1,), 1 / M, device="cuda")):
+        b = gdn.linear_cross_entropy_backward(dloss, x, w, t, r["lse"], **how)
+        want, lim = loss_backward64(dloss, x, w, bias, t, r["lse"], 0.05, 1e-4)
+        for name, v, l in zip(("dx", "dw", "dbias"), want, lim):
+            close(name, b[name], v.cpu(), (l + (v.abs() + l) * HALF[b[name].dtype]).cpu())
+        only = gdn.linear_cross_entropy_backward(dloss, x, w, t, r["lse"], want_dx=False, want_dbias=False, **how)
+        assert torch.equal(only["dw"], b["dw"])
