@@ -673,8 +673,10 @@ hipError_t forward(const NormParams& p, hipStream_t s) {
     if (runs <= 256) return rows_t<XB, YB, 64, 4>(p, s);
     if (runs <= 512) return rows_t<XB, YB, 64, 8>(p, s);
     if (runs <= 1024) return rows_t<XB, YB, 256, 4>(p, s);
-    if (runs <= 2048) return rows_t<XB, YB, 256, 8>(p, s);
-    return rows_t<XB, YB, 1024, 4>(p, s);
+    if constexpr (W == 4) {
+        if (runs > 2048) return rows_t<XB, YB, 1024, 4>(p, s);
+    }
+    return rows_t<XB, YB, 256, 8>(p, s);
 }
 
 // Work-groups of the backward pass, each of which leaves a sum for each column:

@@ -447,3 +447,22 @@ def test_wide_tiles(M, V, K):
             close(name, b[name], v.cpu(), (l + (v.abs() + l) * HALF[b[name].dtype]).cpu())
         only = gdn.linear_cross_entropy_backward(dloss, x, w, t, r["lse"], want_dx=False, want_dbias=False, **how)
         assert torch.equal(only["dw"], b["dw"])
+
+
+@pytest.mark.parametrize("M, V, K", [(199, 179, 23184), (1090, 5, 25200), (131, 1412, 14376), (4304, 197, 9456)])
+def test_direct_products(M, V, K):
+    """One piece without parts, whose dx its product writes: on tiles of 256 x 256
+    (the first two) and of 256 x 128."""
+    g, x, w, t = data(M, V, K, M + 2)
+    r = gdn.linear_cross_entropy(x, w, t)
+    loss, lse, e, e_lse = loss64(x, w, None, t, 0.0, 0.0)[:4]
+    close("loss", r["loss"], loss.cpu(), e.cpu())
+    close("lse", r["lse"], lse.cpu(), e_lse.cpu())
+    for dloss in (torch.randn(M, generator=g, device="cuda"), torch.full((1,), 1 / M, device="cuda")):
+        b = gdn.linear_cross_entropy_backward(dloss, x, w, t, r["lse"])
+        want, lim = loss_backward64(dloss, x, w, None, t, r["lse"], 0.0, 0.0)
+        for name, v, l in zip(("dx", "dw"), want, lim):
+            close(name, b[name], v.cpu(), (l + (v.abs() + l) * HALF[BF16]).cpu())
+        for name in b:
+            only = gdn.linear_cross_entropy_backward(dloss, x, w, t, r["lse"], **{"want_" + n: n == name for n in b})
+            assert torch.equal(only[name], b[name]), name

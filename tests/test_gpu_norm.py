@@ -289,3 +289,23 @@ def test_many_long_rows(i, types, layer):
         assert bool(((r[name].double() - a).abs() <= l + (a.abs() + l) * HALF[r[name].dtype]).all()), name
     again = gdn.norm_backward(dy, x, w, stats, kind=KIND[layer], d_residual=skip, want_dbias=True)
     assert all(torch.equal(again[n], r[n]) for n in r)
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (BF16, FP32), (FP32, BF16), (FP32, FP32)])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_whole_narrow_rows(types, D):
+    """Rows that fill eight, sixteen or thirty-two threads to the last column."""
+    xt, yt = types
+    for M, layer in ((5, True), (3001, False)):
+        g = torch.Generator(device="cuda").manual_seed(D + M)
+        x, dy = rows(g, M, D, xt, 0, 0, scale=2, offset=1), rows(g, M, D, yt, 0, 0)
+        w, b, stats = torch.randn(D, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda"), torch.empty((2, M), device="cuda")
+        y = gdn.norm(x, w, b, kind=KIND[layer], out_dtype=yt, stats=stats)
+        cpu = [t.cpu() for t in (x, w, b)]
+        want = norm64(*cpu, layer, 1e-5)[0]
+        e = norm_bounds(*cpu, layer, 1e-5)[0]
+        close("y", y, want, e + (want.abs() + e) * HALF[yt])
+        r = gdn.norm_backward(dy, x, w, stats, kind=KIND[layer], want_dbias=True)
+        ref, lim = norm_backward64(dy.cpu(), x.cpu(), w.cpu(), stats[0].cpu(), stats[1].cpu(), layer, None)
+        for name, a, l in zip(("dx", "dweight", "dbias"), ref, lim):
+            close(name, r[name], a, l + (a.abs() + l) * HALF[r[name].dtype])
