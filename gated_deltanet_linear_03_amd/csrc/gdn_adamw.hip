@@ -18,12 +18,12 @@
 // otherwise than the formula does, each of them by a whole step.  So the
 // scales come from the largest value in 64 bits, and a block with a value that
 // lies nearer to its border than 32 bits can tell (one or two in a hundred)
-// takes them from 64 bits: 269.5 M elements take 783 to 802 us, 948 with all of them in
+// takes them from 64 bits: 269.5 M elements take 776 to 818 us, 948 with all of them in
 // 64 bits and 745 with none.
 //
 // Bound: HBM.  Each element is read and written once: 28 bytes with 32-bit
 // states, a bf16 gradient and a bf16 copy, 16 with 8-bit states (269.5 M elements:
-// 1.30 ms, 5.8 TB/s, and 0.78 to 0.81 ms, 5.4, with the vector units busy
+// 1.27 to 1.30 ms, 5.8 TB/s, and 0.78 to 0.82 ms, 5.4, with the vector units busy
 // throughout).  A wave's 64
 // lanes take four adjacent elements each, which is a block of the 8-bit
 // states, so a block's largest magnitude is one reduction over a wave.

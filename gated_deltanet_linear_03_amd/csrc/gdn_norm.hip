@@ -411,7 +411,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormPa
         if (p.center) next_mean = p.stats_in[m];
         next_rstd = p.stats_in[p.M + m];
     };
-    constexpr bool kAhead = T <= 512;         // (1024 threads have no registers for the next row)
+    constexpr bool kAhead = T <= 512;         // (1024 threads' registers are full without the next row)
     int64_t m0 = static_cast<int64_t>(blockIdx.x) * R;
     if constexpr (kAhead) fetch(row_at(m0));
     for (; m0 < p.M; m0 += static_cast<int64_t>(gridDim.x) * R) {
