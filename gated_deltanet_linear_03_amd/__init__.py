@@ -1520,8 +1520,9 @@ class AdamW:
         for name in lists:
             setattr(self, name, list(lists[name]))
         # (aliases: the memory lives as long as this does, whatever the caller's tensors become)
-        self._held = [t.detach() for k in ("params", "m", "v", "m_scale", "v_scale", "copies")
-                      for t in getattr(self, k) if t is not None]
+        self._alias = {k: [None if t is None else t.detach() for t in getattr(self, k)]
+                       for k in ("params", "m", "v", "m_scale", "v_scale", "copies")}
+        self._held = [t for x in self._alias.values() for t in x if t is not None]
         self.beta1, self.beta2, self.eps, self.seed = float(beta1), float(beta2), float(eps), int(seed) & 0xFFFFFFFF
         dev = self.device = _device()
         import torch
@@ -1552,8 +1553,7 @@ class AdamW:
         self._decay = list(self.weight_decay)             # as self._c has it
         self._copied = any(t is not None for t in self.copies)
         self._at = self._addresses()
-        self._was = {k: [0 if t is None else t.data_ptr() for t in getattr(self, k)]
-                     for k in ("params", "m", "v", "m_scale", "v_scale", "copies")}
+        self._was = {k: [0 if t is None else t.data_ptr() for t in x] for k, x in self._alias.items()}
         # what a step writes, each byte once
         spans = sorted((t.data_ptr(), t.numel() * t.element_size(), f"{k}[{i}]")
                        for k in ("params", "copies", "m", "v", "m_scale", "v_scale")
@@ -1574,28 +1574,31 @@ class AdamW:
             c.weight_decay = x
         self._decay = decay
 
-    def _lists(self):
-        names = ["params", "m", "v"] + ["m_scale", "v_scale"] * (self.bits == 8)
-        # (a list of None is counted without looking into a tensor)
-        return names + ["copies"] * (self._copied or self.copies.count(None) != len(self.copies))
-
     def _addresses(self):
         # (one method mapped over the lists: a tenth less time than a comprehension's calls)
-        lists = [getattr(self, k) for k in self._lists()]
-        try:
-            return list(map(_torch.Tensor.data_ptr, chain.from_iterable(lists)))
-        except TypeError:                                 # (some without a copy)
-            return [0 if t is None else t.data_ptr() for t in chain.from_iterable(lists)]
+        of = _torch.Tensor.data_ptr
+        scales = (self.m_scale, self.v_scale) if self.bits == 8 else ()
+        at = list(map(of, chain(self.params, self.m or (), self.v or (), *(x or () for x in scales))))
+        # (a list of None is counted without looking into a tensor; a comparison with a tensor takes microseconds)
+        if self._copied or (self.copies is not None and self.copies.count(None) != len(self.copies)):
+            try:
+                at += list(map(of, self.copies or ()))
+            except TypeError:                             # (some without a copy)
+                at += [0 if t is None else of(t) for t in self.copies]
+        return at
 
     def _check_memory(self):
         if self._addresses() == self._at:
             return
         for name, old in self._was.items():
-            now = [0 if t is None else t.data_ptr() for t in getattr(self, name)]
+            now = getattr(self, name)
+            now = [None] * len(old) if now is None else now
             if len(now) != len(old):
                 raise ValueError(f"opt.{name}: {len(old)} entries needed, not {len(now)}")
-            for i, (a, b) in enumerate(zip(now, old)):
-                if a != b and (a or name == "params"):
+            for i, (t, b, alias) in enumerate(zip(now, old, self._alias[name])):
+                a = 0 if t is None else t.data_ptr()
+                # (let go: the memory is there as long as the alias has it)
+                if a != b and (a or name == "params" or alias.data_ptr() != b):
                     raise ValueError(f"opt.{name}[{i}]: its memory is not the one that opt was made with")
 
 

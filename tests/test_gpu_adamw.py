@@ -563,3 +563,21 @@ def test_every_code_is_a_neighbour(grad):
                 unit = np.exp2(np.floor(np.log2(np.maximum(np.abs(ratio), 2.0 ** -6))) - 3)
                 # (64 bits are exact to 2^-50 of the terms, which are at most 10 times the block's largest where m' cancels)
                 assert bool((np.abs(got - ratio) <= unit * (1 + 1e-9)).all()) and bool((got * ratio >= 0).all()), (name, i, k)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_freed_memory(bits):
+    """A state or a copy whose storage itself was resized to nothing is refused
+    (its memory is gone); copies that the object's list no longer has are not."""
+    p = [torch.ones(300, device="cuda")]
+    g = [torch.ones(300, device="cuda")]
+    for name in ["m", "v", "copies"] + ["m_scale", "v_scale"] * (bits == 8):
+        opt = gdn.AdamW(p, **gdn.adamw_states(p, bits), copies=[torch.ones(300, device="cuda", dtype=BF16)])
+        getattr(opt, name)[0].untyped_storage().resize_(0)
+        with pytest.raises(ValueError, match=rf"opt\.{name}\[0\].*memory"):
+            gdn.adamw_step(opt, g, lr=1e-2, step=1)
+        assert float((p[0] - 1).abs().max()) == 0
+    opt = gdn.AdamW(p, **gdn.adamw_states(p, bits), copies=[torch.ones(300, device="cuda", dtype=BF16)])
+    opt.copies = None
+    gdn.adamw_step(opt, g, lr=1e-2, step=1)
+    assert float((p[0] - 0.99).abs().max()) < 1e-5
