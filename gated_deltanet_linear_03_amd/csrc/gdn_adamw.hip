@@ -219,7 +219,7 @@ struct Largest {
             // One after the other, all that come from the same pair (or, as
             // magnitudes go, from its negative) at once: gradients of one size
             // make ties of whole blocks (2^26 elements of one gradient: value by
-            // value 6.78 ms, so 0.23; of random ones 0.21 either way).
+            // value 6.78 ms, so 0.24; of random ones 0.20 to 0.21 either way).
             double best = -1.0;
             uint32_t left = mine;
             while (who != 0 && most > 0.f) {
